@@ -260,6 +260,161 @@ int csr_spmm_row_softmax(int M, int K, int N, int nnz,
                          usm_dtype dtype, void *stream);
 
 /*
+ * Query blocks, heads and positions, as the sparse-attention calls below read
+ * them.  The rows of the mask are query rows: block b = r / seg_rows holds
+ * seg_rows of them (seg_rows <= 0 or > M: one block of M rows), and belongs to
+ * head b % num_heads (blocks are batch-major, heads fastest).  Row r stands at
+ * query position r % seg_rows + q_offset[b].  The columns are key rows: blocks
+ * of seg_cols of them (seg_cols <= 0: one block), and a row's columns lie in
+ * one block, the one of its first column; column c stands at key position
+ * c - seg_cols·floor(first column / seg_cols).  Several query blocks may list
+ * the columns of one key block (heads that share keys).
+ *
+ * usm_rel_bias — a learned bias by relative position (key position minus query
+ * position), shared by buckets of positions.  A host struct: the calls read it
+ * before they return and keep no pointer to it.
+ */
+typedef struct usm_rel_bias {
+    const void *table;     /* device, num_heads×num_buckets row-major, table_dtype */
+    usm_dtype table_dtype;
+    int num_heads;         /* > 0 */
+    int num_buckets;       /* 1..USM_REL_BIAS_MAX_BUCKETS */
+    const int *bucket_map; /* device int32[2·max_distance + 1]: entry max_distance + d is the
+                              bucket of relative position d; values are clamped into
+                              [0, num_buckets) when read */
+    int max_distance;      /* 1..USM_REL_BIAS_MAX_DISTANCE; positions beyond ±max_distance
+                              take the bucket of ±max_distance */
+    int seg_cols;          /* key rows per block */
+    const int *q_offset;   /* device int32[number of query blocks], or NULL for zeros */
+} usm_rel_bias;
+
+#define USM_REL_BIAS_MAX_BUCKETS 512
+#define USM_REL_BIAS_MAX_DISTANCE 8192
+
+/*
+ * rel_bucket_build — the bucket map of logarithmic position buckets.
+ *
+ * bucket_map : device int32[2·max_distance + 1], written.  With causal = 1 a
+ *   key at distance n = max(-d, 0) behind the query takes one of b =
+ *   num_buckets buckets (keys ahead share bucket 0); with causal = 0 n = |d|,
+ *   b = num_buckets / 2 and keys ahead of the query (d > 0) use the upper b
+ *   buckets.  With e = b / 2 (integer division): n < e takes bucket n, larger n
+ *   bucket min(b - 1, e + floor(ln(n/e) / ln(max_distance/e) · (b - e))).
+ *   The logarithms are 64-bit; a quotient within 1e-9 below a whole number
+ *   counts as that number, so distances on a boundary always take the upper
+ *   bucket.
+ * Limits: num_buckets ≥ 2 (causal) or an even number ≥ 4, max_distance > e,
+ * both within the limits above.
+ */
+int rel_bucket_build(int num_buckets, int max_distance, int causal, int *bucket_map, void *stream);
+
+/*
+ * csr_rel_bias — out[p] = scores[p] + table[h][bucket(p)] on the mask's
+ * nonzeros: h the head of p's row, bucket(p) = bucket_map[max_distance +
+ * clamp(d, ±max_distance)], d the relative position of p's column and row.
+ * The step between the SDDMM's scores and the row softmax.
+ *   scores, out : fp32 [nnz] in CSR order; out may be scores (in place).
+ *   One fp32 addition; a bf16 table is widened first.
+ * M = 0 or nnz = 0 is a no-op.
+ */
+int csr_rel_bias(int M, int K, int nnz, const int *row_offsets, const int *col_indices, const float *scores,
+                 int seg_rows, const usm_rel_bias *bias, float *out, void *stream);
+
+/*
+ * csr_rel_bias_grad — the gradient of the table:
+ *   dtable[h][k] = Σ dscores[p] over the nonzeros p of head h's rows with
+ *   bucket(p) = k (every block of the head); OVERWRITTEN, zero where none is.
+ *   dscores : [nnz], fp32 or bf16.  dtable : fp32, num_heads×num_buckets.
+ *   bias    : as csr_rel_bias; table and table_dtype are not read.
+ *   workspace : csr_rel_bias_grad_workspace_bytes(...) bytes of device
+ *           scratch, 16-byte aligned, contents ignored.
+ * Sums are fp32 in a fixed order (no atomics): the same call gives the same
+ * bits.  The scores' own gradient is dscores unchanged.
+ */
+size_t csr_rel_bias_grad_workspace_bytes(int M, int nnz, int seg_rows, int num_heads, int num_buckets);
+
+int csr_rel_bias_grad(int M, int K, int nnz, const int *row_offsets, const int *col_indices, const void *dscores,
+                      usm_dtype dscores_dtype, int seg_rows, const usm_rel_bias *bias, float *dtable,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * csr_diff_softmax — the map of differential attention, the difference of two
+ * row softmaxes with a learned weight per head:
+ *   out[p] = P1[p] - lambda[h]·P2[p],
+ *   Pk[p] = exp(sk[p] - mk) / Σ_{q in row} exp(sk[q] - mk),  mk = max over the row of sk.
+ * Its output is the value array of csr_spmm with V (and, transposed, of the
+ * gradient of V).
+ *   scores1, scores2 : fp32 [nnz].  lambda : device fp32 [num_heads].
+ *   out : [nnz], fp32 or bf16 (one rounding to nearest even, at the end).
+ * Masked entries: a score of -inf has probability 0 in its map; a row whose
+ * scores are all -inf has a zero map, and an empty row writes nothing.  NaN or
+ * +inf scores make their row's outputs NaN.
+ * Maxima, sums and the difference are fp32; exponentials are CUDA's __expf.
+ */
+int csr_diff_softmax(int M, int nnz, const int *row_offsets, const float *scores1, const float *scores2,
+                     const float *lambda, int num_heads, int seg_rows, void *out, usm_dtype out_dtype,
+                     void *stream);
+
+/*
+ * csr_diff_softmax_grad — gradients of csr_diff_softmax.  With dA = dout and
+ * ck = Σ_{q in row} Pk[q]·dA[q]:
+ *   dscores1[p] = P1[p]·(dA[p] - c1),
+ *   dscores2[p] = -lambda[h]·P2[p]·(dA[p] - c2),
+ *   dlambda[h]  = -Σ c2 over the rows of head h (all its blocks), OVERWRITTEN.
+ * The probabilities are formed again from the scores, so the forward pass
+ * keeps nothing.
+ *   dout : [nnz], fp32 or bf16.  dscores1, dscores2 : [nnz], `out_dtype`; each
+ *   may be its scores array when out_dtype is USM_F32 (in place).
+ *   dlambda : fp32 [num_heads], or NULL (then no workspace is needed).
+ *   workspace : csr_diff_softmax_grad_workspace_bytes(M) bytes, 16-byte
+ *           aligned, contents ignored.
+ * A masked entry (score -inf in map k) gives 0 in dscoresk and adds nothing
+ * to ck, whatever dout holds there.  Sums are fp32 in a fixed order.
+ */
+size_t csr_diff_softmax_grad_workspace_bytes(int M);
+
+int csr_diff_softmax_grad(int M, int nnz, const int *row_offsets, const float *scores1, const float *scores2,
+                          const float *lambda, int num_heads, int seg_rows, const void *dout, usm_dtype dout_dtype,
+                          void *dscores1, void *dscores2, usm_dtype out_dtype, float *dlambda,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * csr_row_softmax_grad — the gradient of csr_row_softmax:
+ *   dscores[p] = P[p]·(dout[p] - Σ_{q in row} P[q]·dout[q]),
+ * P formed again from the fp32 scores.  Types, masked entries and in-place use
+ * as csr_diff_softmax_grad.
+ */
+int csr_row_softmax_grad(int M, int nnz, const int *row_offsets, const float *scores, const void *dout,
+                         usm_dtype dout_dtype, void *dscores, usm_dtype out_dtype, void *stream);
+
+/*
+ * csr_attention — sparse attention of few query rows in one pass, the form for
+ * single tokens over a cache of keys and values:
+ *   s1[p] = scale·(Q[r]·Km[c_p]) + bias(p),     s2[p] = scale·(Q2[r]·K2[c_p]) + bias(p),
+ *   C[r][j] = Σ_{p in row r} (P1[p] - lambda[h]·P2[p])·V[c_p][j],
+ * Pk the row softmax of sk; with Q2 = K2 = lambda = NULL there is one map and
+ * C = Σ P1·V.  Nothing is written but C: scores and probabilities stay in
+ * registers in fp32.  It reads the listed rows of Km, K2 and V where they lie,
+ * so many rows that list the same keys read them again each (from L2);
+ * prompts take csr_sddmm, csr_rel_bias, csr_diff_softmax and csr_spmm, which
+ * stage the keys once for many rows.
+ *
+ *   Q, Q2 : M×D, Km, K2 : K×D, V : K×N dense, row-major, `dtype` (rows by
+ *           ldq, ldq2, ldk, ldk2, ldv).
+ *   bias  : usm_rel_bias, or NULL for none; added to both maps' scores.
+ *   C     : M×N fp32, ldc ≥ N, overwritten; a row with no entry, or whose
+ *           scores are all -inf in both maps, is zero.  Rows of V under an
+ *           entry that is -inf in every map are not used, whatever they hold.
+ * Limits: D, N ≤ 256 (fp32) or 512 (bf16).  Alignment as csr_spmm.
+ * Deterministic (no atomics).  Empty cases: M = 0 or N = 0 is a no-op;
+ * nnz = 0 zero-fills C; D = 0 reads no Q or K and has zero products (weights by the bias alone).
+ */
+int csr_attention(int M, int K, int D, int N, int nnz, const int *row_offsets, const int *col_indices,
+                  const void *Q, int ldq, const void *Km, int ldk, const void *Q2, int ldq2, const void *K2, int ldk2,
+                  const void *V, int ldv, float scale, const float *lambda, int num_heads, int seg_rows,
+                  const usm_rel_bias *bias, float *C, int ldc, usm_dtype dtype, void *stream);
+
+/*
  * csr_transpose — Aᵀ in CSR, for the sparse layer's input gradient.
  *
  * Source: "Sparse GPU Kernels for Deep Learning", summary card, "Summary"

@@ -301,6 +301,174 @@ int csr_row_softmax(int M, int nnz, const int* row_offsets, const float* scores,
     return launch_row_softmax(M, nnz, row_offsets, scores, out, out_dtype == USM_BF16, as_stream(stream));
 }
 
+namespace {
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool dtype_ok(usm_dtype d) { return d == USM_F32 || d == USM_BF16; }
+size_t dtype_size(usm_dtype d) { return d == USM_BF16 ? 2 : 4; }
+
+// Checks of a usm_rel_bias; `table`: whether its table is read.
+int check_bias(const usm_rel_bias* b, bool table) {
+    if (!b || b->num_heads <= 0 || b->num_buckets <= 0 || b->max_distance <= 0 || !b->bucket_map)
+        return USM_ERR_INVALID_ARG;
+    if (table && (!b->table || !dtype_ok(b->table_dtype))) return USM_ERR_INVALID_ARG;
+    if (b->num_buckets > USM_REL_BIAS_MAX_BUCKETS || b->max_distance > USM_REL_BIAS_MAX_DISTANCE)
+        return USM_ERR_UNSUPPORTED;
+    if (!aligned_to(b->bucket_map, 4) || !aligned_to(b->q_offset, 4) ||
+        (table && !aligned_to(b->table, dtype_size(b->table_dtype))))
+        return USM_ERR_ALIGNMENT;
+    return USM_OK;
+}
+
+RelArgs rel_args(const usm_rel_bias* b, int M, int seg_rows) {
+    return {b->table,    b->table_dtype == USM_BF16, b->num_heads, b->num_buckets, b->bucket_map, b->max_distance,
+            b->seg_cols, b->q_offset,                effective_seg(M, seg_rows)};
+}
+}  // namespace
+
+int rel_bucket_build(int num_buckets, int max_distance, int causal, int* bucket_map, void* stream) {
+    if (causal != 0 && causal != 1) return USM_ERR_INVALID_ARG;
+    if (causal ? num_buckets < 2 : (num_buckets < 4 || num_buckets % 2 != 0)) return USM_ERR_INVALID_ARG;
+    if (max_distance <= (causal ? num_buckets : num_buckets / 2) / 2) return USM_ERR_INVALID_ARG;
+    if (num_buckets > USM_REL_BIAS_MAX_BUCKETS || max_distance > USM_REL_BIAS_MAX_DISTANCE)
+        return USM_ERR_UNSUPPORTED;
+    if (!bucket_map) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(bucket_map, 4)) return USM_ERR_ALIGNMENT;
+    return launch_rel_bucket_build(num_buckets, max_distance, causal == 1, bucket_map, as_stream(stream));
+}
+
+int csr_rel_bias(int M, int K, int nnz, const int* row_offsets, const int* col_indices, const float* scores,
+                 int seg_rows, const usm_rel_bias* bias, float* out, void* stream) {
+    if (M < 0 || K < 0 || nnz < 0) return USM_ERR_INVALID_ARG;
+    const int c = check_bias(bias, true);
+    if (c != USM_OK) return c;
+    if (M == 0 || nnz == 0) return USM_OK;
+    if (K == 0 || !row_offsets || !col_indices || !scores || !out) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(scores, 4) || !aligned_to(out, 4) || !aligned_to(col_indices, 4)) return USM_ERR_ALIGNMENT;
+    return launch_rel_bias(M, nnz, row_offsets, col_indices, scores, rel_args(bias, M, seg_rows), out,
+                           as_stream(stream));
+}
+
+size_t csr_rel_bias_grad_workspace_bytes(int M, int nnz, int seg_rows, int num_heads, int num_buckets) {
+    if (M <= 0 || nnz <= 0 || num_heads <= 0 || num_buckets <= 0 || num_buckets > USM_REL_BIAS_MAX_BUCKETS) return 0;
+    return rel_bias_grad_workspace_bytes(M, nnz, effective_seg(M, seg_rows), num_heads, num_buckets);
+}
+
+int csr_rel_bias_grad(int M, int K, int nnz, const int* row_offsets, const int* col_indices, const void* dscores,
+                      usm_dtype dscores_dtype, int seg_rows, const usm_rel_bias* bias, float* dtable,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || K < 0 || nnz < 0 || !dtype_ok(dscores_dtype)) return USM_ERR_INVALID_ARG;
+    const int c = check_bias(bias, false);
+    if (c != USM_OK) return c;
+    if (!dtable) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(dtable, 4)) return USM_ERR_ALIGNMENT;
+    if (M == 0 || nnz == 0)
+        return launch_fill_out(dtable, (long long)bias->num_heads * bias->num_buckets, false, as_stream(stream));
+    if (K == 0 || !row_offsets || !col_indices || !dscores) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(dscores, dtype_size(dscores_dtype)) || !aligned_to(col_indices, 4)) return USM_ERR_ALIGNMENT;
+    const size_t need = csr_rel_bias_grad_workspace_bytes(M, nnz, seg_rows, bias->num_heads, bias->num_buckets);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return USM_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return USM_ERR_ALIGNMENT;
+    return launch_rel_bias_grad(M, nnz, row_offsets, col_indices, dscores, dscores_dtype == USM_BF16,
+                                rel_args(bias, M, seg_rows), dtable, workspace, as_stream(stream));
+}
+
+int csr_diff_softmax(int M, int nnz, const int* row_offsets, const float* scores1, const float* scores2,
+                     const float* lambda, int num_heads, int seg_rows, void* out, usm_dtype out_dtype, void* stream) {
+    if (M < 0 || nnz < 0 || num_heads <= 0 || !dtype_ok(out_dtype)) return USM_ERR_INVALID_ARG;
+    if (M == 0 || nnz == 0) return USM_OK;
+    if (!row_offsets || !scores1 || !scores2 || !lambda || !out) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(scores1, 4) || !aligned_to(scores2, 4) || !aligned_to(lambda, 4) ||
+        !aligned_to(out, dtype_size(out_dtype)))
+        return USM_ERR_ALIGNMENT;
+    const MapArgs a{M,       nnz, row_offsets, scores1, scores2, lambda, num_heads, effective_seg(M, seg_rows),
+                    nullptr, 0,   out,         nullptr, out_dtype == USM_BF16, nullptr};
+    return launch_diff_softmax(a, as_stream(stream));
+}
+
+size_t csr_diff_softmax_grad_workspace_bytes(int M) { return M > 0 ? (size_t)M * 4 : 0; }
+
+int csr_diff_softmax_grad(int M, int nnz, const int* row_offsets, const float* scores1, const float* scores2,
+                          const float* lambda, int num_heads, int seg_rows, const void* dout, usm_dtype dout_dtype,
+                          void* dscores1, void* dscores2, usm_dtype out_dtype, float* dlambda,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || nnz < 0 || num_heads <= 0 || !dtype_ok(dout_dtype) || !dtype_ok(out_dtype))
+        return USM_ERR_INVALID_ARG;
+    if (!aligned_to(dlambda, 4)) return USM_ERR_ALIGNMENT;
+    if (M == 0 || nnz == 0)
+        return dlambda ? launch_fill_out(dlambda, num_heads, false, as_stream(stream)) : (int)USM_OK;
+    if (!row_offsets || !scores1 || !scores2 || !lambda || !dout || !dscores1 || !dscores2)
+        return USM_ERR_INVALID_ARG;
+    if (!aligned_to(scores1, 4) || !aligned_to(scores2, 4) || !aligned_to(lambda, 4) ||
+        !aligned_to(dout, dtype_size(dout_dtype)) || !aligned_to(dscores1, dtype_size(out_dtype)) ||
+        !aligned_to(dscores2, dtype_size(out_dtype)))
+        return USM_ERR_ALIGNMENT;
+    if (dlambda) {
+        if (!workspace || workspace_bytes < csr_diff_softmax_grad_workspace_bytes(M)) return USM_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return USM_ERR_ALIGNMENT;
+    }
+    const MapArgs a{M,
+                    nnz,
+                    row_offsets,
+                    scores1,
+                    scores2,
+                    lambda,
+                    num_heads,
+                    effective_seg(M, seg_rows),
+                    dout,
+                    dout_dtype == USM_BF16,
+                    dscores1,
+                    dscores2,
+                    out_dtype == USM_BF16,
+                    dlambda ? static_cast<float*>(workspace) : nullptr};
+    return launch_diff_softmax_grad(a, dlambda, as_stream(stream));
+}
+
+int csr_row_softmax_grad(int M, int nnz, const int* row_offsets, const float* scores, const void* dout,
+                         usm_dtype dout_dtype, void* dscores, usm_dtype out_dtype, void* stream) {
+    if (M < 0 || nnz < 0 || !dtype_ok(dout_dtype) || !dtype_ok(out_dtype)) return USM_ERR_INVALID_ARG;
+    if (M == 0 || nnz == 0) return USM_OK;
+    if (!row_offsets || !scores || !dout || !dscores) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(scores, 4) || !aligned_to(dout, dtype_size(dout_dtype)) ||
+        !aligned_to(dscores, dtype_size(out_dtype)))
+        return USM_ERR_ALIGNMENT;
+    const MapArgs a{M,    nnz, row_offsets, scores,  nullptr, nullptr, 1, M, dout, dout_dtype == USM_BF16,
+                    dscores, nullptr, out_dtype == USM_BF16, nullptr};
+    return launch_row_softmax_grad(a, as_stream(stream));
+}
+
+int csr_attention(int M, int K, int D, int N, int nnz, const int* row_offsets, const int* col_indices,
+                  const void* Q, int ldq, const void* Km, int ldk, const void* Q2, int ldq2, const void* K2, int ldk2,
+                  const void* V, int ldv, float scale, const float* lambda, int num_heads, int seg_rows,
+                  const usm_rel_bias* bias, float* C, int ldc, usm_dtype dtype, void* stream) {
+    if (M < 0 || K < 0 || D < 0 || N < 0 || nnz < 0 || num_heads <= 0 || !dtype_ok(dtype))
+        return USM_ERR_INVALID_ARG;
+    if (bias) {
+        const int c = check_bias(bias, true);
+        if (c != USM_OK) return c;
+        if (bias->num_heads != num_heads) return USM_ERR_INVALID_ARG;
+    }
+    if (M == 0 || N == 0) return USM_OK;
+    const bool two = lambda != nullptr;
+    if (D > 0 && (two != (Q2 != nullptr) || two != (K2 != nullptr))) return USM_ERR_INVALID_ARG;
+    if (!C || !row_offsets || ldc < N) return USM_ERR_INVALID_ARG;
+    if (!aligned16(C) || ldc % 4 != 0) return USM_ERR_ALIGNMENT;
+    if (nnz == 0) return launch_fill_f32(C, M, N, ldc, as_stream(stream));
+    if (K == 0 || !col_indices || !V || ldv < N) return USM_ERR_INVALID_ARG;
+    if (D > 0 && (!Q || !Km || ldq < D || ldk < D || (two && (ldq2 < D || ldk2 < D)))) return USM_ERR_INVALID_ARG;
+    const long long es = (long long)dtype_size(dtype);
+    const int most = dtype == USM_BF16 ? 512 : 256;
+    if (D > most || N > most) return USM_ERR_UNSUPPORTED;
+    if (!aligned16(V) || ldv * es % 16 != 0 || !aligned_to(lambda, 4)) return USM_ERR_ALIGNMENT;
+    if (D > 0 && (!aligned16(Q) || !aligned16(Km) || ldq * es % 16 != 0 || ldk * es % 16 != 0)) return USM_ERR_ALIGNMENT;
+    if (D > 0 && two && (!aligned16(Q2) || !aligned16(K2) || ldq2 * es % 16 != 0 || ldk2 * es % 16 != 0))
+        return USM_ERR_ALIGNMENT;
+    AttnArgs a{M,    K,   D,   N,    nnz,  row_offsets, col_indices, Q,      Km,        Q2, K2, V,
+               ldq,  ldk, ldq2, ldk2, ldv, scale,       lambda,      num_heads, effective_seg(M, seg_rows),
+               RelArgs{}, C,   ldc};
+    if (bias) a.bias = rel_args(bias, M, seg_rows);
+    return launch_attention(a, dtype == USM_BF16, as_stream(stream));
+}
+
 size_t csr_transpose_workspace_bytes(int M, int K, int nnz) {
     if (M < 0 || K < 0 || nnz <= 0) return 0;
     return transpose_workspace_bytes(M, K, nnz);

@@ -37,4 +37,46 @@ struct SddmmArgs {
     int tiles_per_block = 0;  // row tiles per diagonal block (set by the launcher)
 };
 
+// A relative position bias (usm_rel_bias) and the query blocks it applies to.
+struct RelArgs {
+    const void* table;  // null: no bias
+    int table_bf16;
+    int heads, buckets;
+    const int* map;
+    int reach;            // max_distance
+    int seg_cols;         // <= 0: one key block
+    const int* q_offset;  // may be null
+    int seg_rows;         // > 0
+};
+
+// Softmax maps over CSR rows and their gradients.  s2, lambda: null with one map.
+struct MapArgs {
+    int M, nnz;
+    const int* row_offsets;
+    const float* s1;
+    const float* s2;
+    const float* lambda;
+    int heads, seg_rows;  // > 0
+    const void* dout;     // gradients only
+    int dout_bf16;
+    void* out1;           // the map, or the gradient of s1
+    void* out2;           // the gradient of s2
+    int out_bf16;
+    float* row_c2;        // gradients with two maps: c2 of each row, or null
+};
+
+struct AttnArgs {
+    int M, K, D, N, nnz;
+    const int* row_offsets;
+    const int* col_indices;
+    const void *Q, *Km, *Q2, *K2, *V;  // Q2, K2: null with one map
+    long long ldq, ldk, ldq2, ldk2, ldv;
+    float scale;
+    const float* lambda;
+    int heads, seg_rows;
+    RelArgs bias;
+    float* C;
+    long long ldc;
+};
+
 }  // namespace usm

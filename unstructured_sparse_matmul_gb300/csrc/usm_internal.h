@@ -68,6 +68,19 @@ int launch_dense_transpose(const void* src, long long lds, int rows, int cols, b
                            long long ldd, cudaStream_t stream);
 int launch_row_softmax(int M, int nnz, const int* row_offsets, const float* scores, void* out, bool out_bf16,
                        cudaStream_t stream);
+
+// Number of query blocks of seg rows in M rows (seg in [1, M]).
+inline int query_blocks(int M, int seg) { return (int)(((long long)M + seg - 1) / seg); }
+int launch_rel_bucket_build(int num_buckets, int max_distance, bool causal, int* bucket_map, cudaStream_t stream);
+int launch_rel_bias(int M, int nnz, const int* row_offsets, const int* col_indices, const float* scores,
+                    const RelArgs& bias, float* out, cudaStream_t stream);
+size_t rel_bias_grad_workspace_bytes(int M, int nnz, int seg_rows, int num_heads, int num_buckets);
+int launch_rel_bias_grad(int M, int nnz, const int* row_offsets, const int* col_indices, const void* dscores,
+                         bool bf16, const RelArgs& bias, float* dtable, void* workspace, cudaStream_t stream);
+int launch_diff_softmax(const MapArgs& a, cudaStream_t stream);
+int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stream);
+int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream);
+int launch_attention(const AttnArgs& a, bool bf16, cudaStream_t stream);
 int launch_csr_validate(int M, int K, int nnz, const int* row_offsets, const int* col_indices, int* result,
                         cudaStream_t stream);
 
