@@ -12,6 +12,7 @@ I3 for the SDDMM form, I4 for the row swizzle, I5 for plain CSR).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -91,6 +92,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libusm.so (building it first if needed) and bind its symbols."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -328,29 +331,51 @@ def row_softmax(row_offsets, scores, out=None, out_dtype=None, stream=None):
     return out
 
 
+# ---------------------------------------------------------------------------
 # Sparse attention: position bias, differential map, softmax gradients, and
 # attention of few rows.  Every tensor of a call lies on one device, which need
-# not be the current one; 1-D arrays are contiguous.
-class _Call:
-    """One call: the checks of its tensors, its device and its stream.  With a
-    stream of the caller's, the call's copies, outputs and scratch belong to
-    that stream too (as under torch.cuda.stream), so none of them races the
-    current stream's work."""
+# not be the current one; 1-D arrays are contiguous.  Single tokens spend most
+# of such a call on the host, so a check that passes costs one expression and
+# only a failing one looks for the reason.
+# ---------------------------------------------------------------------------
+def _on_stream(fn):
+    """Gives an operation its `stream` keyword.  With a stream of the caller's,
+    copies, outputs and scratch belong to that stream too (as under
+    torch.cuda.stream), so none of them races the current stream's work."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        torch = _torch()
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
 
-    def __init__(self, stream):
-        self.torch, self.stream, self.device = _torch(), stream, None
+    return call
 
-    def __enter__(self):
-        if self.stream is not None:
-            self.context = self.torch.cuda.stream(self.stream)
-            self.context.__enter__()
-        return self
 
-    def __exit__(self, *error):
-        if self.stream is not None:
-            self.context.__exit__(*error)
+class _Types:
+    """Element types the operations take (filled in once torch is there)."""
+    torch = i32 = f32 = real = empty = raw_stream = None
 
-    def tensor(self, t, name, dtypes, dims=1):
+
+def _types():
+    if _Types.torch is None:
+        torch = _torch()
+        _Types.i32, _Types.f32, _Types.real = (torch.int32,), (torch.float32,), (torch.float32, torch.bfloat16)
+        _Types.empty = staticmethod(torch.empty)
+        # The current stream's handle; the public way builds a Stream object for it.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _Types.raw_stream = staticmethod(raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+        _Types.torch = torch
+    return _Types
+
+
+def _tensor(t, name, index, dtypes, dims):
+    """A tensor of the call: its type, number of dimensions and device."""
+    if t is None or t.dtype not in dtypes or t.dim() != dims or t.get_device() != index or index < 0:
         if t is None:
             raise ValueError(f"{name} is required")
         if not t.is_cuda:
@@ -359,63 +384,38 @@ class _Call:
             raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
         if t.dim() != dims:
             raise ValueError(f"{name} must have {dims} dimension(s), has {t.dim()}")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
-        return t
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
+    return t
 
-    def array(self, t, name, dtypes, n=None):
-        self.tensor(t, name, dtypes)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-        return t
 
-    def csr(self, row_offsets, col_indices):
-        i32 = (self.torch.int32,)
-        self.array(row_offsets, "row_offsets", i32)
-        if row_offsets.numel() < 1:
-            raise ValueError("row_offsets needs at least one element")
-        self.array(col_indices, "col_indices", i32)
-        _int32(rows=row_offsets.numel(), nonzeros=col_indices.numel())
-        return row_offsets.numel() - 1, col_indices.numel()
+def _array(t, name, index, dtypes, n=None):
+    """A contiguous 1-D tensor, of n elements unless None."""
+    _tensor(t, name, index, dtypes, 1)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return t
 
-    def out(self, out, n, dtype, name="out"):
-        """A given 1-D output, checked, or a new one."""
-        if out is None:
-            return self.torch.empty(n, dtype=dtype if dtype is not None else self.torch.float32, device=self.device)
-        f = (self.torch.float32, self.torch.bfloat16)
-        self.array(out, name, f if dtype is None else (dtype,), n)
-        return out
 
-    def bias(self, bucket_map, num_heads, num_buckets, seg_cols, q_offset, blocks, table=None):
-        """The usm_rel_bias struct (and nothing that outlives the call)."""
-        i32 = (self.torch.int32,)
-        _int32(seg_cols=seg_cols, num_heads=num_heads, num_buckets=num_buckets)
-        self.array(bucket_map, "bucket_map", i32)
-        n = bucket_map.numel()
-        if n < 3 or n % 2 == 0:
-            raise ValueError("bucket_map has 2*max_distance + 1 entries")
-        if q_offset is not None:
-            self.array(q_offset, "q_offset", i32, blocks)
-        if table is not None and not table.is_contiguous():
-            raise ValueError("table must be contiguous")
-        return RelBias(_ptr(table), USM_F32 if table is None else _dtype_code(table), num_heads, num_buckets,
-                       bucket_map.data_ptr(), (n - 1) // 2, seg_cols, _ptr(q_offset))
+def _device_of(t, name) -> int:
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t.get_device()
 
-    def run(self, name, fn, *args):
-        """Call the library on the tensors' device."""
-        cuda, device = self.torch.cuda, self.device
-        if self.stream is not None and self.stream.device != device:
-            raise ValueError(f"stream is on {self.stream.device}, tensors on {device}")
-        stream = cuda.current_stream(device).cuda_stream
-        if device.index == cuda.current_device():
-            _check(name, fn(*args, stream))
-        else:
-            with cuda.device(device):
-                _check(name, fn(*args, stream))
+
+def _rows(row_offsets, index, T) -> int:
+    _array(row_offsets, "row_offsets", index, T.i32)
+    M = row_offsets.numel() - 1
+    if not 0 <= M < 2**31:
+        raise ValueError(f"row_offsets has {M + 1} elements: from 1 to 2**31 are expected")
+    return M
+
+
+def _entries(n: int) -> int:
+    if n >= 2**31:
+        raise ValueError(f"{n} entries do not fit 32 bits")
+    return n
 
 
 def _int32(**values):
@@ -424,188 +424,249 @@ def _int32(**values):
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 
-def _blocks(M: int, seg_rows: int) -> int:
-    _int32(seg_rows=seg_rows)
-    return 1 if seg_rows <= 0 or seg_rows > M else -(-M // seg_rows)
+def _out(out, like, n, dtype, index, T, name="out"):
+    """A given 1-D output, checked, or a new one beside `like`."""
+    if out is None:
+        return T.empty(n, dtype=T.f32[0] if dtype is None else dtype, device=like.device)
+    return _array(out, name, index, T.real if dtype is None else (dtype,), n)
 
 
-def rel_bucket_map(num_buckets: int, max_distance: int, causal: bool = False, device=None, stream=None):
-    """int32[2*max_distance + 1]: the bucket of each relative position
-    -max_distance..max_distance, logarithmic past num_buckets/2 (causal) or
-    num_buckets/4; see rel_bucket_build."""
-    torch = _torch()
-    _int32(num_buckets=num_buckets, max_distance=max_distance)
-    with _Call(stream) as c:
-        device = torch.device("cuda" if device is None else device)
-        out = torch.empty(max(2 * max_distance + 1, 1), dtype=torch.int32, device=device)
-        c.tensor(out, "bucket_map", (torch.int32,))
-        c.run("rel_bucket_build", load().rel_bucket_build, num_buckets, max_distance, int(bool(causal)), out.data_ptr())
-        return out
-
-
-def rel_bias(row_offsets, col_indices, scores, table, bucket_map, seg_rows: int = 0, seg_cols: int = 0, q_offset=None,
-             out=None, K: int | None = None, stream=None):
-    """out[p] = scores[p] + table[head][bucket of p's relative position]; out
-    may be scores.  table: num_heads x num_buckets, fp32 or bf16; see
-    csr_rel_bias."""
-    with _Call(stream) as c:
-        torch = c.torch
-        M, nnz = c.csr(row_offsets, col_indices)
-        c.array(scores, "scores", (torch.float32,), nnz)
-        c.tensor(table, "table", (torch.float32, torch.bfloat16), 2)
-        b = c.bias(bucket_map, table.shape[0], table.shape[1], seg_cols, q_offset, _blocks(M, seg_rows), table)
-        out = c.out(out, nnz, torch.float32)
-        c.run("csr_rel_bias", load().csr_rel_bias, M, _K_ANY if K is None else K, nnz, row_offsets.data_ptr(),
-              col_indices.data_ptr(), scores.data_ptr(), seg_rows, ctypes.addressof(b), out.data_ptr())
-        return out
-
-
-def rel_bias_grad(row_offsets, col_indices, dscores, num_heads: int, num_buckets: int, bucket_map, seg_rows: int = 0,
-                  seg_cols: int = 0, q_offset=None, out=None, workspace=None, K: int | None = None, stream=None):
-    """The gradient of rel_bias's table (num_heads x num_buckets fp32) from the
-    scores' gradient (fp32 or bf16); see csr_rel_bias_grad."""
-    with _Call(stream) as c:
-        torch = c.torch
-        lib = load()
-        M, nnz = c.csr(row_offsets, col_indices)
-        c.array(dscores, "dscores", (torch.float32, torch.bfloat16), nnz)
-        b = c.bias(bucket_map, num_heads, num_buckets, seg_cols, q_offset, _blocks(M, seg_rows))
-        if out is None:
-            out = torch.empty((max(num_heads, 0), max(num_buckets, 0)), dtype=torch.float32, device=c.device)
-        else:
-            c.tensor(out, "out", (torch.float32,), 2)
-            if not out.is_contiguous() or tuple(out.shape) != (num_heads, num_buckets):
-                raise ValueError("out must be a contiguous num_heads x num_buckets tensor")
-        need = lib.csr_rel_bias_grad_workspace_bytes(M, nnz, seg_rows, num_heads, num_buckets)
-        ws = _workspace(c, workspace, need)
-        c.run("csr_rel_bias_grad", lib.csr_rel_bias_grad, M, _K_ANY if K is None else K, nnz, row_offsets.data_ptr(),
-              col_indices.data_ptr(), dscores.data_ptr(), _dtype_code(dscores), seg_rows, ctypes.addressof(b),
-              out.data_ptr(), _ptr(ws), need)
-        return out
-
-
-_K_ANY = 2**31 - 1  # these calls address nothing by column: K only says whether there may be columns
-
-
-def _workspace(c, workspace, need: int):
+def _workspace(workspace, need: int, like, T):
     """The caller's workspace, if it holds `need` bytes, or a new one."""
     if need == 0:
         return None
     if workspace is not None:
-        if not workspace.is_cuda or workspace.device != c.device or not workspace.is_contiguous():
+        if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the device of the others")
         if workspace.numel() * workspace.element_size() >= need:
             return workspace
-    return c.torch.empty(need, dtype=c.torch.uint8, device=c.device)
+    return T.empty(need, dtype=T.torch.uint8, device=like.device)
 
 
-def diff_softmax(row_offsets, scores1, scores2, lam, seg_rows: int = 0, out=None, out_dtype=None, stream=None):
+def _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, index, T, table=None):
+    """The usm_rel_bias struct (and nothing that outlives the call)."""
+    _int32(seg_rows=seg_rows, seg_cols=seg_cols, num_heads=num_heads, num_buckets=num_buckets)
+    _array(bucket_map, "bucket_map", index, T.i32)
+    n = bucket_map.numel()
+    if n < 3 or n % 2 == 0:
+        raise ValueError("bucket_map has 2*max_distance + 1 entries")
+    if q_offset is not None:
+        blocks = 1 if seg_rows <= 0 or seg_rows > M else -(-M // seg_rows)
+        _array(q_offset, "q_offset", index, T.i32, blocks)
+    if table is not None and not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    return RelBias(None if table is None else table.data_ptr(), USM_F32 if table is None else _code(table, T), num_heads,
+                   num_buckets, bucket_map.data_ptr(), n // 2, seg_cols, _ptr(q_offset))
+
+
+def _code(t, T) -> int:
+    """Type code of a tensor that holds fp32 or bf16."""
+    d = t.dtype
+    if d not in T.real:
+        raise TypeError(f"unsupported element type {d} (fp32 or bf16)")
+    return USM_F32 if d is T.f32[0] else USM_BF16
+
+
+def _run(name, fn, index, T, *args):
+    """Call the library on device `index`, on its current stream."""
+    cuda = T.torch.cuda
+    if index == cuda.current_device():
+        code = fn(*args, T.raw_stream(index))
+    else:
+        with cuda.device(index):
+            code = fn(*args, T.raw_stream(index))
+    if code != 0:
+        raise USMError(name, code)
+
+
+@_on_stream
+def rel_bucket_map(num_buckets: int, max_distance: int, causal: bool = False, device=None):
+    """int32[2*max_distance + 1]: the bucket of each relative position
+    -max_distance..max_distance, logarithmic past num_buckets/2 (causal) or
+    num_buckets/4; see rel_bucket_build."""
+    T, lib = _types(), load()
+    _int32(num_buckets=num_buckets, max_distance=max_distance)
+    out = T.torch.empty(max(2 * max_distance + 1, 1), dtype=T.i32[0], device="cuda" if device is None else device)
+    index = out.get_device()
+    _array(out, "bucket_map", index, T.i32)
+    _run("rel_bucket_build", lib.rel_bucket_build, index, T, num_buckets, max_distance, int(bool(causal)),
+         out.data_ptr())
+    return out
+
+
+@_on_stream
+def rel_bias(row_offsets, col_indices, scores, table, bucket_map, seg_rows: int = 0, seg_cols: int = 0, q_offset=None,
+             out=None):
+    """out[p] = scores[p] + table[head][bucket of p's relative position]; out
+    may be scores.  table: num_heads x num_buckets, fp32 or bf16; see
+    csr_rel_bias."""
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(scores, "scores", index, T.f32)
+    nnz = _entries(scores.numel())
+    _array(col_indices, "col_indices", index, T.i32, nnz)
+    _tensor(table, "table", index, T.real, 2)
+    heads, buckets = table.shape
+    b = _bias(bucket_map, heads, buckets, seg_rows, seg_cols, q_offset, M, index, T, table)
+    out = _out(out, scores, nnz, T.f32[0], index, T)
+    _run("csr_rel_bias", lib.csr_rel_bias, index, T, M, _ANY_COLUMN, nnz, row_offsets.data_ptr(),
+         col_indices.data_ptr(), scores.data_ptr(), seg_rows, ctypes.addressof(b), out.data_ptr())
+    return out
+
+
+_ANY_COLUMN = 2**31 - 1  # K of calls that address nothing by column: it only says that there are columns
+
+
+@_on_stream
+def rel_bias_grad(row_offsets, col_indices, dscores, num_heads: int, num_buckets: int, bucket_map, seg_rows: int = 0,
+                  seg_cols: int = 0, q_offset=None, out=None, workspace=None):
+    """The gradient of rel_bias's table (num_heads x num_buckets fp32) from the
+    scores' gradient (fp32 or bf16); see csr_rel_bias_grad."""
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(dscores, "dscores", index, T.real)
+    nnz = _entries(dscores.numel())
+    _array(col_indices, "col_indices", index, T.i32, nnz)
+    b = _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, index, T)
+    if out is None:
+        out = T.empty((max(num_heads, 0), max(num_buckets, 0)), dtype=T.f32[0], device=dscores.device)
+    else:
+        _tensor(out, "out", index, T.f32, 2)
+        if not out.is_contiguous() or tuple(out.shape) != (num_heads, num_buckets):
+            raise ValueError("out must be a contiguous num_heads x num_buckets tensor")
+    need = lib.csr_rel_bias_grad_workspace_bytes(M, nnz, seg_rows, num_heads, num_buckets)
+    ws = _workspace(workspace, need, dscores, T)
+    _run("csr_rel_bias_grad", lib.csr_rel_bias_grad, index, T, M, _ANY_COLUMN, nnz, row_offsets.data_ptr(),
+         col_indices.data_ptr(), dscores.data_ptr(), _code(dscores, T), seg_rows, ctypes.addressof(b), out.data_ptr(),
+         _ptr(ws), need)
+    return out
+
+
+@_on_stream
+def diff_softmax(row_offsets, scores1, scores2, lam, seg_rows: int = 0, out=None, out_dtype=None):
     """softmax_rows(scores1) - lam[head]*softmax_rows(scores2) on the stored
     entries: the value array of spmm with V; see csr_diff_softmax."""
-    with _Call(stream) as c:
-        torch = c.torch
-        c.array(row_offsets, "row_offsets", (torch.int32,))
-        c.array(scores1, "scores1", (torch.float32,))
-        nnz = scores1.numel()
-        c.array(scores2, "scores2", (torch.float32,), nnz)
-        c.array(lam, "lam", (torch.float32,))
-        out = c.out(out, nnz, out_dtype)
-        c.run("csr_diff_softmax", load().csr_diff_softmax, row_offsets.numel() - 1, nnz, row_offsets.data_ptr(),
-              scores1.data_ptr(), scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, out.data_ptr(),
-              _dtype_code(out))
-        return out
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(scores1, "scores1", index, T.f32)
+    nnz = _entries(scores1.numel())
+    _array(scores2, "scores2", index, T.f32, nnz)
+    _array(lam, "lam", index, T.f32)
+    _int32(seg_rows=seg_rows)
+    out = _out(out, scores1, nnz, out_dtype, index, T)
+    _run("csr_diff_softmax", lib.csr_diff_softmax, index, T, M, nnz, row_offsets.data_ptr(), scores1.data_ptr(),
+         scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, out.data_ptr(), _code(out, T))
+    return out
 
 
+@_on_stream
 def diff_softmax_grad(row_offsets, scores1, scores2, lam, dout, seg_rows: int = 0, out1=None, out2=None,
-                      out_dtype=None, dlam=None, workspace=None, stream=None):
+                      out_dtype=None, dlam=None, workspace=None):
     """Gradients of diff_softmax: (dscores1, dscores2, dlam) from the map's
     gradient dout (fp32 or bf16); see csr_diff_softmax_grad."""
-    with _Call(stream) as c:
-        torch = c.torch
-        lib = load()
-        c.array(row_offsets, "row_offsets", (torch.int32,))
-        c.array(scores1, "scores1", (torch.float32,))
-        nnz, M = scores1.numel(), row_offsets.numel() - 1
-        c.array(scores2, "scores2", (torch.float32,), nnz)
-        c.array(lam, "lam", (torch.float32,))
-        c.array(dout, "dout", (torch.float32, torch.bfloat16), nnz)
-        if out_dtype is None:
-            given = out1 if out1 is not None else out2
-            out_dtype = given.dtype if given is not None else torch.float32
-        out1, out2 = c.out(out1, nnz, out_dtype, "out1"), c.out(out2, nnz, out_dtype, "out2")
-        dlam = c.out(dlam, lam.numel(), torch.float32, "dlam")
-        need = lib.csr_diff_softmax_grad_workspace_bytes(M)
-        ws = _workspace(c, workspace, need)
-        c.run("csr_diff_softmax_grad", lib.csr_diff_softmax_grad, M, nnz, row_offsets.data_ptr(), scores1.data_ptr(),
-              scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, dout.data_ptr(), _dtype_code(dout),
-              out1.data_ptr(), out2.data_ptr(), _dtype_code(out1), dlam.data_ptr(), _ptr(ws), need)
-        return out1, out2, dlam
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(scores1, "scores1", index, T.f32)
+    nnz = _entries(scores1.numel())
+    _array(scores2, "scores2", index, T.f32, nnz)
+    _array(lam, "lam", index, T.f32)
+    _array(dout, "dout", index, T.real, nnz)
+    _int32(seg_rows=seg_rows)
+    if out_dtype is None:
+        given = out1 if out1 is not None else out2
+        out_dtype = T.f32[0] if given is None else given.dtype
+    out1 = _out(out1, scores1, nnz, out_dtype, index, T, "out1")
+    out2 = _out(out2, scores1, nnz, out_dtype, index, T, "out2")
+    dlam = _out(dlam, scores1, lam.numel(), T.f32[0], index, T, "dlam")
+    need = lib.csr_diff_softmax_grad_workspace_bytes(M)
+    ws = _workspace(workspace, need, scores1, T)
+    _run("csr_diff_softmax_grad", lib.csr_diff_softmax_grad, index, T, M, nnz, row_offsets.data_ptr(),
+         scores1.data_ptr(), scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, dout.data_ptr(),
+         _code(dout, T), out1.data_ptr(), out2.data_ptr(), _code(out1, T), dlam.data_ptr(), _ptr(ws), need)
+    return out1, out2, dlam
 
 
-def row_softmax_grad(row_offsets, scores, dout, out=None, out_dtype=None, stream=None):
+@_on_stream
+def row_softmax_grad(row_offsets, scores, dout, out=None, out_dtype=None):
     """The gradient of row_softmax's scores from the probabilities' gradient
     dout (fp32 or bf16); see csr_row_softmax_grad."""
-    with _Call(stream) as c:
-        torch = c.torch
-        c.array(row_offsets, "row_offsets", (torch.int32,))
-        c.array(scores, "scores", (torch.float32,))
-        nnz = scores.numel()
-        c.array(dout, "dout", (torch.float32, torch.bfloat16), nnz)
-        out = c.out(out, nnz, out_dtype)
-        c.run("csr_row_softmax_grad", load().csr_row_softmax_grad, row_offsets.numel() - 1, nnz, row_offsets.data_ptr(),
-              scores.data_ptr(), dout.data_ptr(), _dtype_code(dout), out.data_ptr(), _dtype_code(out))
-        return out
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(scores, "scores", index, T.f32)
+    nnz = _entries(scores.numel())
+    _array(dout, "dout", index, T.real, nnz)
+    out = _out(out, scores, nnz, out_dtype, index, T)
+    _run("csr_row_softmax_grad", lib.csr_row_softmax_grad, index, T, M, nnz, row_offsets.data_ptr(), scores.data_ptr(),
+         dout.data_ptr(), _code(dout, T), out.data_ptr(), _code(out, T))
+    return out
 
 
+def _operand(t, name, index, dtypes, rows, cols):
+    """A dense operand of the given shape as the library reads it, and its
+    leading dimension (a copy only where rows are not 16-byte aligned)."""
+    _tensor(t, name, index, dtypes, 2)
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
+    t = _tma_ready(t)
+    return t, t.stride(0)
+
+
+@_on_stream
 def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K2=None, lam=None, seg_rows: int = 0,
-              table=None, bucket_map=None, seg_cols: int = 0, q_offset=None, out=None, stream=None):
+              table=None, bucket_map=None, seg_cols: int = 0, q_offset=None, out=None):
     """Sparse attention of few query rows in one pass (fp32 out): softmax of
     scale*(Q[r].Km[col]) + bias over each row's entries, times V; with Q2, K2
     and lam the differential map, with table and bucket_map the relative
     position bias; see csr_attention."""
-    with _Call(stream) as c:
-        torch = c.torch
-        M, nnz = c.csr(row_offsets, col_indices)
-        c.tensor(Q, "Q", (torch.float32, torch.bfloat16), 2)
-        dt = (Q.dtype,)
-        c.tensor(Km, "Km", dt, 2)
-        c.tensor(V, "V", dt, 2)
-        K, D, N = Km.shape[0], Q.shape[1], V.shape[1]
-        two = lam is not None
-        if two != (Q2 is not None) or two != (K2 is not None):
+    T, lib = _types(), load()
+    index = _device_of(row_offsets, "row_offsets")
+    M = _rows(row_offsets, index, T)
+    _array(col_indices, "col_indices", index, T.i32)
+    nnz = _entries(col_indices.numel())
+    _tensor(Km, "Km", index, T.real, 2)
+    _tensor(V, "V", index, T.real, 2)
+    K, D = Km.shape
+    N = V.shape[1]
+    dt = (Km.dtype,)
+    Q, ldq = _operand(Q, "Q", index, dt, M, D)
+    Km, ldk = _operand(Km, "Km", index, dt, K, D)
+    V, ldv = _operand(V, "V", index, dt, K, N)
+    _int32(seg_rows=seg_rows)
+    heads, ldq2, ldk2, b = 1, 0, 0, None
+    if lam is None:
+        if Q2 is not None or K2 is not None:
             raise ValueError("Q2, K2 and lam come together")
-        if Q.shape[0] != M or Km.shape[1] != D or V.shape[0] != K:
-            raise ValueError("Q is M x D, Km is K x D and V is K x N")
-        heads = 1
-        if two:
-            c.tensor(Q2, "Q2", dt, 2)
-            c.tensor(K2, "K2", dt, 2)
-            c.array(lam, "lam", (torch.float32,))
-            heads = lam.numel()
-            if Q2.shape != Q.shape or K2.shape != Km.shape:
-                raise ValueError("Q2 and K2 have the shapes of Q and Km")
-            Q2, K2 = _tma_ready(Q2), _tma_ready(K2)
-        b = None
-        if table is not None:
-            c.tensor(table, "table", (torch.float32, torch.bfloat16), 2)
-            if two and table.shape[0] != heads:
-                raise ValueError("table and lam disagree on the number of heads")
-            heads = table.shape[0]
-            b = c.bias(bucket_map, heads, table.shape[1], seg_cols, q_offset, _blocks(M, seg_rows), table)
-        elif bucket_map is not None or q_offset is not None:
-            raise ValueError("bucket_map and q_offset need a table")
-        Q, Km, V = _tma_ready(Q), _tma_ready(Km), _tma_ready(V)
-        if out is None:
-            out = _new_dense_out(M, N, c.device)
-        else:
-            c.tensor(out, "out", (torch.float32,), 2)
-            if tuple(out.shape) != (M, N):
-                raise ValueError("out must be M x N")
-        c.run("csr_attention", load().csr_attention, M, K, D, N, nnz, row_offsets.data_ptr(), col_indices.data_ptr(),
-              Q.data_ptr(), _ld(Q), Km.data_ptr(), _ld(Km), _ptr(Q2), 0 if Q2 is None else _ld(Q2), _ptr(K2),
-              0 if K2 is None else _ld(K2), V.data_ptr(), _ld(V), scale, _ptr(lam), heads, seg_rows,
-              None if b is None else ctypes.addressof(b), out.data_ptr(), _ld(out), _dtype_code(Q))
-        return out
+    else:
+        if Q2 is None or K2 is None:
+            raise ValueError("Q2, K2 and lam come together")
+        Q2, ldq2 = _operand(Q2, "Q2", index, dt, M, D)
+        K2, ldk2 = _operand(K2, "K2", index, dt, K, D)
+        heads = _array(lam, "lam", index, T.f32).numel()
+    if table is not None:
+        _tensor(table, "table", index, T.real, 2)
+        if lam is not None and table.shape[0] != heads:
+            raise ValueError("table and lam disagree on the number of heads")
+        heads, buckets = table.shape
+        b = _bias(bucket_map, heads, buckets, seg_rows, seg_cols, q_offset, M, index, T, table)
+    elif bucket_map is not None or q_offset is not None:
+        raise ValueError("bucket_map and q_offset need a table")
+    if out is None:
+        out = _new_dense_out(M, N, Km.device)
+        ldc = out.stride(0)
+    else:
+        _tensor(out, "out", index, T.f32, 2)
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be M x N")
+        ldc = _ld(out)
+    _run("csr_attention", lib.csr_attention, index, T, M, K, D, N, nnz, row_offsets.data_ptr(), col_indices.data_ptr(),
+         Q.data_ptr(), ldq, Km.data_ptr(), ldk, _ptr(Q2), ldq2, _ptr(K2), ldk2, V.data_ptr(), ldv, scale, _ptr(lam),
+         heads, seg_rows, None if b is None else ctypes.addressof(b), out.data_ptr(), ldc, _code(Km, T))
+    return out
 
 
 def csr_validate(row_offsets, col_indices, K: int, stream=None):

@@ -18,6 +18,7 @@
 // memory: no workspace, no atomics.
 #include <cmath>
 
+#include "usm_cluster.cuh"
 #include "usm_internal.h"
 #include "usm_rel.cuh"
 
@@ -25,28 +26,6 @@ namespace usm {
 namespace {
 
 constexpr int kWarps = 4;
-
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t n;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
-    return n;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t n;
-    asm volatile("mov.u32 %0, %%cluster_ctaid.x;" : "=r"(n));
-    return n;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The float at this CTA's shared address `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 
 // 16 bytes of a row, `left` of its elements still inside the row's width
 // (RAGGED: fewer than a whole piece at the end are read one by one).
@@ -127,8 +106,8 @@ __global__ void __launch_bounds__(kWarps * 32, TWO || CH > 1 ? 3 : 4) attention_
             for (int j = threadIdx.x; j < a.N; j += kWarps * 32) a.C[(long long)r * a.ldc + j] = 0.f;
         return;
     }
-    long long shift = 0;
-    if (a.bias.table) shift = rel_shift(a.bias, block, r - block * a.seg_rows, __ldg(a.col_indices + p0));
+    const int start =
+        a.bias.table ? rel_start(a.bias, block, r - block * a.seg_rows, __ldg(a.col_indices + p0)) : 0;
 
     uint4 q1[CH], q2[CH];
     int left_d[CH], left_n[CH];  // elements of the lane's pieces inside D and N
@@ -192,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32, TWO || CH > 1 ? 3 : 4) attention_
             const int c0 = __shfl_sync(kFullMask, col, j & 31);
             float bias = 0.f;
             if (a.bias.table)
-                bias = rel_table(a.bias, block % a.heads, rel_bucket(a.bias, rel_entry(c0, shift, a.bias.reach)));
+                bias = rel_table(a.bias, block % a.heads, rel_bucket(a.bias, rel_entry(c0, start, a.bias.reach)));
             float e[MAPS];
             bool used = false;
 #pragma unroll

@@ -7,20 +7,20 @@
 
 namespace usm {
 
-// What a column of row r is measured from: d = column - shift is its relative
-// position.  64 bits: the block's first column and the query position (both up
-// to 2^31, q_offset any int) add up.
-__device__ __forceinline__ long long rel_shift(const RelArgs& b, int block, int row_in_block, int first_col) {
-    long long shift = row_in_block;
-    if (b.q_offset) shift += __ldg(b.q_offset + block);
-    if (b.seg_cols > 0) shift += (long long)(first_col / b.seg_cols) * b.seg_cols;
-    return shift;
+// The column at which row r's part of the bucket map starts: column col reads
+// entry clamp(col - start, 0, 2·reach), since its relative position is col less
+// the row's key block's first column and its query position.  Those can add up
+// past 32 bits (and q_offset may be negative); a start outside [-2^30, 2^31)
+// gives every column the same entry as the nearest start inside does.
+__device__ __forceinline__ int rel_start(const RelArgs& b, int block, int row_in_block, int first_col) {
+    long long start = (long long)row_in_block - b.reach;
+    if (b.q_offset) start += __ldg(b.q_offset + block);
+    if (b.seg_cols > 0) start += (long long)(first_col / b.seg_cols) * b.seg_cols;
+    return (int)min(max(start, -(1LL << 30)), 0x7fffffffLL);
 }
 
-// Entry of the bucket map (and of tables laid out like it) for column col.
-__device__ __forceinline__ int rel_entry(int col, long long shift, int reach) {
-    const long long d = col - shift;
-    return (int)min(max(d, -(long long)reach), (long long)reach) + reach;
+__device__ __forceinline__ int rel_entry(int col, int start, int reach) {
+    return col < start ? 0 : (int)min((unsigned)col - (unsigned)start, 2u * (unsigned)reach);
 }
 
 __device__ __forceinline__ int rel_bucket(const RelArgs& b, int entry) {

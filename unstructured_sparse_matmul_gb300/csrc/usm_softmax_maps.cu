@@ -2,25 +2,33 @@
 //     differential map   A = P1 - λ P2,
 //     its gradient       dS1 = P1 (dA - c1), dS2 = -λ P2 (dA - c2), dλ = -Σ_rows c2, ck = Σ_row Pk dA,
 //     softmax gradient   dS = P (dP - Σ_row P dP),
-// Pk = exp(sk - mk) / Σ exp(sk - mk) over the row's stored entries.
+// Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
+// stored entries.
+//
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  A row is
+// read once into registers (four quads a lane: 512 entries a warp, 4096 a CTA),
+// its maximum and then its sums are reduced over the lanes, and the results are
+// written from the registers.  Entries past those are summed as they are read,
+// with a running maximum, and read a second time (from L2) for the output.
+// A warp takes a row; rows over kLong entries wait until the warps of the CTA
+// are done and are then taken by the whole CTA, so a long row among short ones
+// costs an eighth of its time.  Where rows are long throughout, or few, a CTA
+// or a cluster of up to 8 takes each row (launch_map), the CTAs joining their
+// maxima and sums through distributed shared memory.
 #include <cmath>
+#include <type_traits>
 
+#include "usm_cluster.cuh"
 #include "usm_internal.h"
+#include "usm_quads.cuh"
 #include "usm_rel.cuh"
 
 namespace usm {
 namespace {
 
-__device__ __forceinline__ float load_elem(const void* p, int bf16, long long i) {
-    return bf16 ? __uint_as_float((uint32_t) static_cast<const unsigned short*>(p)[i] << 16)
-                : static_cast<const float*>(p)[i];
-}
-__device__ __forceinline__ void store_elem(void* p, int bf16, long long i, float v) {
-    if (bf16)
-        static_cast<uint16_t*>(p)[i] = f32_to_bf16_rne(v);
-    else
-        static_cast<float*>(p)[i] = v;
-}
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kQuads = 4;             // quads a lane keeps in registers
+constexpr unsigned kLong = 2048;      // entries above which a CTA takes the row
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -33,95 +41,319 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// What exponents are measured from: the row's maximum, or 0 where it is -inf
-// (every entry masked), so that exp(-inf - 0) = 0 and the row's map is zero.
+// What exponents are measured from: the maximum, or 0 where it is -inf (every
+// entry masked), so that exp(-inf - 0) = 0 and the row's map is zero.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 // 1/z, or 0 for a row without weight; NaN stays NaN.
 __device__ __forceinline__ float inverse(float z) { return z == 0.f ? 0.f : 1.f / z; }
-// e·d, 0 where the entry is masked (whatever d is there).
-__device__ __forceinline__ float masked_mul(float s, float e, float d) { return s == -INFINITY ? 0.f : e * d; }
+// w·d, or 0 under a weight of 0 (a masked entry) whatever d is there.
+__device__ __forceinline__ float weighted(float w, float d) { return w == 0.f ? 0.f : w * d; }
 
-// A warp per row; TWO maps or one, GRAD or the map itself.
-template <bool TWO, bool GRAD>
-__global__ void softmax_map_kernel(const MapArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long warps = ((long long)gridDim.x * blockDim.x) >> 5;
-    for (long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < a.M; r += warps) {
-        int p0, p1;
-        row_range(a.row_offsets, (int)r, a.nnz, p0, p1);
-        if (p0 == p1) {
-            if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
-            continue;
-        }
-        const float lam = TWO ? __ldg(a.lambda + (int)r / a.seg_rows % a.heads) : 0.f;
-        float m1 = -INFINITY, m2 = -INFINITY;
-        for (int p = p0 + lane; p < p1; p += 32) {
-            m1 = fmaxf(m1, a.s1[p]);
-            if (TWO) m2 = fmaxf(m2, a.s2[p]);
-        }
-        m1 = base_of(warp_max(m1));
-        if (TWO) m2 = base_of(warp_max(m2));
-        float z1 = 0.f, z2 = 0.f, c1 = 0.f, c2 = 0.f;
-        for (int p = p0 + lane; p < p1; p += 32) {
-            const float x1 = a.s1[p], e1 = __expf(x1 - m1);
-            const float d = GRAD ? load_elem(a.dout, a.dout_bf16, p) : 0.f;
-            z1 += e1;
-            if (GRAD) c1 += masked_mul(x1, e1, d);
-            if (TWO) {
-                const float x2 = a.s2[p], e2 = __expf(x2 - m2);
-                z2 += e2;
-                if (GRAD) c2 += masked_mul(x2, e2, d);
+// Sums of one map over (part of) a row: the maximum m, z = Σ exp(s - m) and
+// c = Σ exp(s - m)·d.
+struct Stat {
+    float m, z, c;
+};
+
+// Shared memory of a CTA that takes a row: one slot a warp, and the CTA's.
+struct BlockStats {
+    float top[2][kWarps];
+    float sum[2][2][kWarps];
+    float whole[2][3];
+};
+
+// One row [p0, p1).  BLOCK: by the CTA (or its cluster's), else by the warp.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC, bool BLOCK>
+__device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, unsigned p1, BlockStats& sh, int ctas,
+                                        int rank) {
+    constexpr int MAPS = TWO ? 2 : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned nnz = a.nnz;
+    // Thread t of T reads quads t, t + T, ... of the row.
+    const unsigned T = BLOCK ? kThreads * ctas : 32, t = BLOCK ? rank * kThreads + threadIdx.x : lane;
+    const unsigned q0 = (p0 & ~3u) + 4 * t, step = 4 * T;
+    const float* s[2] = {a.s1, a.s2};
+
+    auto load_scores = [&](int k, unsigned q, float (&x)[4]) {
+        load_quad<false, VEC>(s[k], q, nnz, x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (q + u < p0 || q + u >= p1) x[u] = -INFINITY;
+    };
+
+    float x[MAPS][kQuads][4], d[GRAD ? kQuads : 1][4];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+        const unsigned q = q0 + i * step;
+        if (q < p1) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) load_scores(k, q, x[k][i]);
+            if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, d[i]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int k = 0; k < MAPS; ++k) x[k][i][u] = -INFINITY;
+                if constexpr (GRAD) d[i][u] = 0.f;
             }
         }
-        const float r1 = inverse(warp_sum(z1)), r2 = TWO ? inverse(warp_sum(z2)) : 0.f;
-        if (GRAD) {
-            c1 = warp_sum(c1) * r1;
-            if (TWO) c2 = warp_sum(c2) * r2;
-            if (TWO && a.row_c2 && lane == 0) a.row_c2[r] = c2;
-        }
-        for (int p = p0 + lane; p < p1; p += 32) {
-            const float x1 = a.s1[p], e1 = __expf(x1 - m1) * r1;
-            const float x2 = TWO ? a.s2[p] : 0.f, e2 = TWO ? __expf(x2 - m2) * r2 : 0.f;
-            if (GRAD) {
-                const float d = load_elem(a.dout, a.dout_bf16, p);
-                store_elem(a.out1, a.out_bf16, p, masked_mul(x1, e1, d - c1));
-                if (TWO) store_elem(a.out2, a.out_bf16, p, -lam * masked_mul(x2, e2, d - c2));
-            } else {
-                store_elem(a.out1, a.out_bf16, p, e1 - lam * e2);
+    }
+    // Quads past the registers: a running maximum and sums.
+    const unsigned tail = q0 + kQuads * step;
+    Stat run[MAPS];
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
+#pragma unroll 1
+    for (unsigned q = tail; q < p1; q += step) {
+        float y[4], dy[4];
+        if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            load_scores(k, q, y);
+            const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), run[k].m);
+            const float base = base_of(top), f = __expf(run[k].m - base);
+            run[k].z *= f;
+            run[k].c *= f;
+            run[k].m = top;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float e = __expf(y[u] - base);
+                run[k].z += e;
+                if constexpr (GRAD) run[k].c += weighted(e, dy[u]);
             }
         }
+    }
+
+    // Maximum over the warp or CTA.
+    float m[MAPS];
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        float top = run[k].m;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+            top = fmaxf(top, fmaxf(fmaxf(x[k][i][0], x[k][i][1]), fmaxf(x[k][i][2], x[k][i][3])));
+        m[k] = warp_max(top);
+        if (BLOCK && lane == 0) sh.top[k][warp] = m[k];
+    }
+    if constexpr (BLOCK) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
+    }
+    // Weights (in the scores' registers) and their sums.
+    float z[MAPS], c[MAPS], inv[MAPS];
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        const float base = base_of(m[k]), f = __expf(run[k].m - base);
+        z[k] = run[k].z * f;
+        c[k] = run[k].c * f;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[k][i][u] = __expf(x[k][i][u] - base);
+                z[k] += x[k][i][u];
+                if constexpr (GRAD) c[k] += weighted(x[k][i][u], d[i][u]);
+            }
+        z[k] = warp_sum(z[k]);
+        if constexpr (GRAD) c[k] = warp_sum(c[k]);
+        if (BLOCK && lane == 0) {
+            sh.sum[k][0][warp] = z[k];
+            if constexpr (GRAD) sh.sum[k][1][warp] = c[k];
+        }
+    }
+    if constexpr (BLOCK) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            z[k] = c[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                z[k] += sh.sum[k][0][w];
+                if constexpr (GRAD) c[k] += sh.sum[k][1][w];
+            }
+        }
+    }
+    float own[MAPS];  // what this CTA's weights are multiplied by to be the row's
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) own[k] = 1.f;
+    if (BLOCK && ctas > 1) {
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                sh.whole[k][0] = m[k];
+                sh.whole[k][1] = z[k];
+                sh.whole[k][2] = c[k];
+            }
+        }
+        cluster_sync();
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            float top = -INFINITY;
+            for (int i = 0; i < ctas; ++i) top = fmaxf(top, load_cluster(smem_addr(&sh.whole[k][0]), i));
+            const float base = base_of(top);
+            z[k] = c[k] = 0.f;
+            for (int i = 0; i < ctas; ++i) {
+                const float f = __expf(load_cluster(smem_addr(&sh.whole[k][0]), i) - base);
+                z[k] += f * load_cluster(smem_addr(&sh.whole[k][1]), i);
+                if constexpr (GRAD) c[k] += weighted(f, load_cluster(smem_addr(&sh.whole[k][2]), i));
+            }
+            own[k] = __expf(m[k] - base);
+        }
+        cluster_sync();  // no CTA goes on to overwrite, or leave, what another reads
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        inv[k] = inverse(z[k]);
+        if constexpr (GRAD) c[k] *= inv[k];
+        inv[k] *= own[k];
+    }
+    const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
+    if (GRAD && TWO && a.row_c2 && (BLOCK ? rank == 0 && threadIdx.x == 0 : lane == 0)) a.row_c2[r] = c[MAPS - 1];
+
+    // The results of one quad from its weights (and dout).
+    auto finish = [&](unsigned q, const float (&w1)[4], const float (&w2)[4], const float (&dy)[4]) {
+        float y[4];
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = weighted(w1[u] * inv[0], dy[u] - c[0]);
+            store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
+            if constexpr (TWO) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) y[u] = -lam * weighted(w2[u] * inv[1], dy[u] - c[1]);
+                store_quad<OUT, VEC>(a.out2, q, p0, p1, y);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = fmaf(-lam, w2[u] * inv[MAPS - 1], w1[u] * inv[0]);
+            store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+        const unsigned q = q0 + i * step;
+        if (q < p1) finish(q, x[0][i], x[MAPS - 1][i], d[GRAD ? i : 0]);
+    }
+#pragma unroll 1
+    for (unsigned q = tail; q < p1; q += step) {
+        float y[MAPS][4], dy[4];
+        if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            load_scores(k, q, y[k]);
+            const float base = base_of(m[k]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[k][u] = __expf(y[k][u] - base);
+        }
+        finish(q, y[0], y[MAPS - 1], dy);
     }
 }
 
+// A warp per row; long rows by the CTA.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
+__global__ void __launch_bounds__(kThreads) warp_rows_kernel(const MapArgs a) {
+    __shared__ BlockStats sh;
+    __shared__ int waits[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long first = (long long)blockIdx.x * kWarps;
+    int p0 = 0, p1 = 0;
+    const int r = (int)min(first + warp, (long long)a.M - 1);
+    const bool live = first + warp < a.M;
+    if (live) row_range(a.row_offsets, r, a.nnz, p0, p1);
+    const bool is_long = (unsigned)(p1 - p0) > kLong;
+    if (lane == 0) waits[warp] = is_long;
+    if (live && !is_long) {
+        if (p0 < p1)
+            map_row<TWO, GRAD, DIN, OUT, VEC, false>(a, r, p0, p1, sh, 1, 0);
+        else if (GRAD && TWO && a.row_c2 && lane == 0)
+            a.row_c2[r] = 0.f;
+    }
+    if (!__syncthreads_or(is_long)) return;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+        if (!waits[w]) continue;
+        row_range(a.row_offsets, (int)first + w, a.nnz, p0, p1);
+        map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, (int)first + w, p0, p1, sh, 1, 0);
+    }
+}
+
+// A CTA, or a cluster, per row.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
+__global__ void __launch_bounds__(kThreads) block_rows_kernel(const MapArgs a) {
+    __shared__ BlockStats sh;
+    const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
+    const int r = blockIdx.x / ctas;
+    int p0, p1;
+    row_range(a.row_offsets, r, a.nnz, p0, p1);
+    if (p0 == p1) {
+        if (GRAD && TWO && a.row_c2 && rank == 0 && threadIdx.x == 0) a.row_c2[r] = 0.f;
+        return;
+    }
+    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, r, p0, p1, sh, ctas, rank);
+}
+
 // dλ[h] = -Σ c2 over head h's rows: a CTA per head, a fixed order.
-__global__ void lambda_grad_kernel(int M, int heads, int seg_rows, const float* __restrict__ row_c2,
-                                   float* __restrict__ dlambda) {
-    __shared__ float warp_part[8];
-    const int head = blockIdx.x, t = threadIdx.x;
-    const int blocks = (M + seg_rows - 1) / seg_rows;
-    const long long rows = head < blocks ? (long long)((blocks - 1 - head) / heads + 1) * seg_rows : 0;
+__global__ void __launch_bounds__(1024) lambda_grad_kernel(int M, int blocks, int heads, int seg_rows,
+                                                           const float* __restrict__ row_c2,
+                                                           float* __restrict__ dlambda) {
+    __shared__ float warp_part[32];
+    const int head = blockIdx.x, t = threadIdx.x, lane = t & 31;
     float x = 0.f;
-    for (long long i = t; i < rows; i += blockDim.x) {
-        const long long r = (head + i / seg_rows * heads) * seg_rows + i % seg_rows;
-        if (r < M) x += row_c2[r];
+    for (long long b = head; b < blocks; b += heads) {
+        const long long r0 = b * seg_rows;
+        const int n = (int)min((long long)seg_rows, M - r0);
+        for (int i = t; i < n; i += 1024) x += row_c2[r0 + i];
     }
     x = warp_sum(x);
-    if ((t & 31) == 0) warp_part[t >> 5] = x;
+    if (lane == 0) warp_part[t >> 5] = x;
     __syncthreads();
-    if (t == 0) {
-        float y = 0.f;
-        for (int w = 0; w < 8; ++w) y += warp_part[w];
-        dlambda[head] = -y;
+    if (t < 32) {
+        x = warp_sum(warp_part[lane]);
+        if (lane == 0) dlambda[head] = -x;
     }
+}
+
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
+int launch_rows(const MapArgs& a, cudaStream_t stream) {
+    const int sms = sm_count_current_device();
+    const int mean = a.nnz / a.M;
+    // A CTA a row where most rows are long, or where rows are too few to fill
+    // the SMs with a warp each; a cluster where they are too few for CTAs.
+    if (mean > (int)kLong || (mean > 128 * kQuads && a.M < kWarps * sms)) {
+        int ctas = 1;
+        while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kThreads * 4 * kQuads / 2) ctas *= 2;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = ctas;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((long long)a.M * ctas));
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, block_rows_kernel<TWO, GRAD, DIN, OUT, VEC>, a) == cudaSuccess ? USM_OK
+                                                                                                      : USM_ERR_CUDA;
+    }
+    warp_rows_kernel<TWO, GRAD, DIN, OUT, VEC><<<(unsigned)(((long long)a.M + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
 template <bool TWO, bool GRAD>
 int launch_map(const MapArgs& a, cudaStream_t stream) {
-    long long blocks = ((long long)a.M * 32 + 255) / 256;
-    const long long cap = 16LL * sm_count_current_device();
-    if (blocks > cap) blocks = cap;
-    softmax_map_kernel<TWO, GRAD><<<(int)blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    const bool vec = quad_aligned(a.s1, false) && (!TWO || quad_aligned(a.s2, false)) &&
+                     (!GRAD || quad_aligned(a.dout, a.dout_bf16)) && quad_aligned(a.out1, a.out_bf16) &&
+                     (!(GRAD && TWO) || quad_aligned(a.out2, a.out_bf16));
+    auto pick = [&](auto din, auto out) {
+        constexpr bool D = decltype(din)::value, O = decltype(out)::value;
+        return vec ? launch_rows<TWO, GRAD, D, O, true>(a, stream) : launch_rows<TWO, GRAD, D, O, false>(a, stream);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (GRAD && a.dout_bf16) return a.out_bf16 ? pick(std::bool_constant<GRAD>{}, Yes{}) : pick(std::bool_constant<GRAD>{}, No{});
+    return a.out_bf16 ? pick(No{}, Yes{}) : pick(No{}, No{});
 }
 
 }  // namespace
@@ -133,7 +365,8 @@ int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream) { return laun
 int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stream) {
     const int r = launch_map<true, true>(a, stream);
     if (r != USM_OK || !dlambda) return r;
-    lambda_grad_kernel<<<a.heads, 256, 0, stream>>>(a.M, a.heads, a.seg_rows, a.row_c2, dlambda);
+    lambda_grad_kernel<<<a.heads, 1024, 0, stream>>>(a.M, query_blocks(a.M, a.seg_rows), a.heads, a.seg_rows,
+                                                       a.row_c2, dlambda);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
