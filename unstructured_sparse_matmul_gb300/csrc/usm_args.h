@@ -77,6 +77,7 @@ struct AttnArgs {
     RelArgs bias;
     float* C;
     long long ldc;
+    int* status;
 };
 
 }  // namespace usm

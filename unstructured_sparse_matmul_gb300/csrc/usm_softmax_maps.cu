@@ -69,33 +69,39 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
     constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned nnz = a.nnz;
-    // Thread t of T reads quads t, t + T, ... of the row.
+    // Thread t of T takes quads t, t + T, ... of the row.
     const unsigned T = BLOCK ? kThreads * ctas : 32, t = BLOCK ? rank * kThreads + threadIdx.x : lane;
     const unsigned q0 = (p0 & ~3u) + 4 * t, step = 4 * T;
     const float* s[2] = {a.s1, a.s2};
 
-    auto load_scores = [&](int k, unsigned q, float (&x)[4]) {
-        load_quad<false, VEC>(s[k], q, nnz, x);
+    // Scores of quad q; entries of neighbouring rows become -inf.  Only the
+    // row's first quad (thread 0's) can hold entries before it.
+    auto load_scores = [&](unsigned q, bool first, float (&x)[MAPS][4]) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (q + u < p0 || q + u >= p1) x[u] = -INFINITY;
+        for (int k = 0; k < MAPS; ++k) load_quad<false, VEC>(s[k], q, nnz, x[k]);
+        const int left = (int)(p1 - q);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool out = u >= left || (first && q + u < p0);
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k)
+                if (out) x[k][u] = -INFINITY;
+        }
     };
 
-    float x[MAPS][kQuads][4], d[GRAD ? kQuads : 1][4];
+    float x[kQuads][MAPS][4], d[GRAD ? kQuads : 1][4];
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
         const unsigned q = q0 + i * step;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) x[i][k][u] = -INFINITY;
+            if constexpr (GRAD) d[i][u] = 0.f;
+        }
         if (q < p1) {
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) load_scores(k, q, x[k][i]);
+            load_scores(q, i == 0, x[i]);
             if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, d[i]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k) x[k][i][u] = -INFINITY;
-                if constexpr (GRAD) d[i][u] = 0.f;
-            }
         }
     }
     // Quads past the registers: a running maximum and sums.
@@ -105,19 +111,19 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
     for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
 #pragma unroll 1
     for (unsigned q = tail; q < p1; q += step) {
-        float y[4], dy[4];
+        float y[MAPS][4], dy[4];
+        load_scores(q, false, y);
         if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-            load_scores(k, q, y);
-            const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), run[k].m);
-            const float base = base_of(top), f = __expf(run[k].m - base);
+            const float top = fmaxf(fmaxf(fmaxf(y[k][0], y[k][1]), fmaxf(y[k][2], y[k][3])), run[k].m);
+            const float base = base_of(top), f = exp_flush(run[k].m - base);
             run[k].z *= f;
             run[k].c *= f;
             run[k].m = top;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float e = __expf(y[u] - base);
+                const float e = exp_flush(y[k][u] - base);
                 run[k].z += e;
                 if constexpr (GRAD) run[k].c += weighted(e, dy[u]);
             }
@@ -131,7 +137,7 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
         float top = run[k].m;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
-            top = fmaxf(top, fmaxf(fmaxf(x[k][i][0], x[k][i][1]), fmaxf(x[k][i][2], x[k][i][3])));
+            top = fmaxf(top, fmaxf(fmaxf(x[i][k][0], x[i][k][1]), fmaxf(x[i][k][2], x[i][k][3])));
         m[k] = warp_max(top);
         if (BLOCK && lane == 0) sh.top[k][warp] = m[k];
     }
@@ -144,24 +150,46 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
     }
     // Weights (in the scores' registers) and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
+    auto dot = [&](int k, bool guarded) {
+        float sum = 0.f;
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    sum = guarded && x[i][k][u] == 0.f ? sum : fmaf(x[i][k][u], d[i][u], sum);
+        }
+        return sum;
+    };
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        const float base = base_of(m[k]), f = __expf(run[k].m - base);
+        const float base = base_of(m[k]), f = exp_flush(run[k].m - base);
         z[k] = run[k].z * f;
-        c[k] = run[k].c * f;
+        run[k].c *= f;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                x[k][i][u] = __expf(x[k][i][u] - base);
-                z[k] += x[k][i][u];
-                if constexpr (GRAD) c[k] += weighted(x[k][i][u], d[i][u]);
+                x[i][k][u] = exp_flush(x[i][k][u] - base);
+                z[k] += x[i][k][u];
             }
         z[k] = warp_sum(z[k]);
-        if constexpr (GRAD) c[k] = warp_sum(c[k]);
+        c[k] = 0.f;
+        if constexpr (GRAD) c[k] = warp_sum(run[k].c + dot(k, BLOCK));
         if (BLOCK && lane == 0) {
             sh.sum[k][0][warp] = z[k];
-            if constexpr (GRAD) sh.sum[k][1][warp] = c[k];
+            sh.sum[k][1][warp] = c[k];
+        }
+    }
+    // A dout that is not finite makes c so too, even under weights of 0: such a
+    // row (and every row of a CTA) guards each product.
+    bool guarded = BLOCK;
+    if constexpr (GRAD && !BLOCK) {
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) guarded = guarded || !(fabsf(c[k]) < INFINITY);
+        if (guarded) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) c[k] = warp_sum(run[k].c + dot(k, true));
         }
     }
     if constexpr (BLOCK) {
@@ -196,11 +224,11 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
             const float base = base_of(top);
             z[k] = c[k] = 0.f;
             for (int i = 0; i < ctas; ++i) {
-                const float f = __expf(load_cluster(smem_addr(&sh.whole[k][0]), i) - base);
+                const float f = exp_flush(load_cluster(smem_addr(&sh.whole[k][0]), i) - base);
                 z[k] += f * load_cluster(smem_addr(&sh.whole[k][1]), i);
                 if constexpr (GRAD) c[k] += weighted(f, load_cluster(smem_addr(&sh.whole[k][2]), i));
             }
-            own[k] = __expf(m[k] - base);
+            own[k] = exp_flush(m[k] - base);
         }
         cluster_sync();  // no CTA goes on to overwrite, or leave, what another reads
     }
@@ -210,50 +238,53 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
         if constexpr (GRAD) c[k] *= inv[k];
         inv[k] *= own[k];
     }
-    const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
     if (GRAD && TWO && a.row_c2 && (BLOCK ? rank == 0 && threadIdx.x == 0 : lane == 0)) a.row_c2[r] = c[MAPS - 1];
+    if constexpr (TWO) inv[1] *= -__ldg(a.lambda + r / a.seg_rows % a.heads);
 
-    // The results of one quad from its weights (and dout).
-    auto finish = [&](unsigned q, const float (&w1)[4], const float (&w2)[4], const float (&dy)[4]) {
+    // The results of one quad from its weights (and dout).  Gradients are
+    // w·(inv·d - inv·c).
+    auto finish = [&](unsigned q, const float (&w)[MAPS][4], const float (&dy)[4]) {
         float y[4];
         if constexpr (GRAD) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = weighted(w1[u] * inv[0], dy[u] - c[0]);
-            store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
-            if constexpr (TWO) {
+            for (int k = 0; k < MAPS; ++k) {
+                const float ic = -inv[k] * c[k];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) y[u] = -lam * weighted(w2[u] * inv[1], dy[u] - c[1]);
-                store_quad<OUT, VEC>(a.out2, q, p0, p1, y);
+                for (int u = 0; u < 4; ++u) {
+                    const float g = fmaf(inv[k], dy[u], ic);
+                    y[u] = guarded ? weighted(w[k][u], g) : w[k][u] * g;
+                }
+                store_quad<OUT, VEC>(k == 0 ? a.out1 : a.out2, q, p0, p1, y);
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = fmaf(-lam, w2[u] * inv[MAPS - 1], w1[u] * inv[0]);
+            for (int u = 0; u < 4; ++u) y[u] = fmaf(w[0][u], inv[0], w[MAPS - 1][u] * inv[MAPS - 1]);
             store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
         }
     };
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
         const unsigned q = q0 + i * step;
-        if (q < p1) finish(q, x[0][i], x[MAPS - 1][i], d[GRAD ? i : 0]);
+        if (q < p1) finish(q, x[i], d[GRAD ? i : 0]);
     }
 #pragma unroll 1
     for (unsigned q = tail; q < p1; q += step) {
         float y[MAPS][4], dy[4];
+        load_scores(q, false, y);
         if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-            load_scores(k, q, y[k]);
             const float base = base_of(m[k]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[k][u] = __expf(y[k][u] - base);
+            for (int u = 0; u < 4; ++u) y[k][u] = exp_flush(y[k][u] - base);
         }
-        finish(q, y[0], y[MAPS - 1], dy);
+        finish(q, y, dy);
     }
 }
 
 // A warp per row; long rows by the CTA.
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads) warp_rows_kernel(const MapArgs a) {
+__global__ void __launch_bounds__(kThreads, TWO && GRAD ? 3 : 4) warp_rows_kernel(const MapArgs a) {
     __shared__ BlockStats sh;
     __shared__ int waits[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
