@@ -97,9 +97,8 @@ int sm_count_current_device() {
     return n;
 }
 
-namespace {
-bool encode_map(CUtensorMap* map, const void* base, bool bf16, long long rows, long long cols, long long ld_elems,
-                int box_cols, int box_rows, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
+                          long long cols, long long ld_elems, int box_cols, int box_rows) {
     std::call_once(g_encode_once, [] {
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_entry("cuTensorMapEncodeTiled", 12000));
     });
@@ -110,22 +109,10 @@ bool encode_map(CUtensorMap* map, const void* base, bool bf16, long long rows, l
     cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                          promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
-}
-}  // namespace
-
-bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
-                          long long cols, long long ld_elems, int box_cols, int box_rows) {
-    return encode_map(map, base, bf16, rows, cols, ld_elems, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-}
-
-bool encode_gather_map(CUtensorMap* map, const void* base, bool bf16, long long rows, long long cols,
-                       long long ld_elems) {
-    return encode_map(map, base, bf16, rows, cols, ld_elems, bf16 ? 64 : 32, 1, CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 int launch_wait_timeout_selftest(long long limit_ns, int* status, cudaStream_t stream) {
@@ -475,11 +462,9 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int* row_offsets, c
     if (D > 0 && (!aligned16(Q) || !aligned16(Km) || ldq * es % 16 != 0 || ldk * es % 16 != 0)) return USM_ERR_ALIGNMENT;
     if (D > 0 && two && (!aligned16(Q2) || !aligned16(K2) || ldq2 * es % 16 != 0 || ldk2 * es % 16 != 0))
         return USM_ERR_ALIGNMENT;
-    int* status = status_word_for_current_device();
-    if (!status) return USM_ERR_CUDA;
     AttnArgs a{M,    K,   D,   N,    nnz,  row_offsets, col_indices, Q,      Km,        Q2, K2, V,
                ldq,  ldk, ldq2, ldk2, ldv, scale,       lambda,      num_heads, effective_seg(M, seg_rows),
-               RelArgs{}, C,   ldc,  status};
+               RelArgs{}, C,   ldc};
     if (bias) a.bias = rel_args(bias, M, seg_rows);
     return launch_attention(a, dtype == USM_BF16, as_stream(stream));
 }

@@ -77,7 +77,6 @@ struct AttnArgs {
     RelArgs bias;
     float* C;
     long long ldc;
-    int* status;
 };
 
 }  // namespace usm

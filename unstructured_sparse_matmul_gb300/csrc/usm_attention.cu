@@ -10,10 +10,13 @@
 // copies must be in flight all the time, whatever the arithmetic does.  A
 // cluster of 1, 2, 4 or 8 CTAs works on one row; its warps take windows of 16
 // entries in turn, each warp with a ring of stages of its own in shared memory
-// that TMA fills with the windows' rows of K1, K2 and V (four listed rows an
-// instruction, in slabs of 128 bytes a row, 16-byte pieces swizzled by the row
-// so that reading one piece of different rows meets no bank conflict).  No
-// barrier but the stage's own, in the warp that owns it.
+// that asynchronous 16-byte copies fill with the windows' rows of K1, K2 and V:
+// no barrier, and a warp's copies run ahead of its arithmetic by the ring.  A
+// stage holds slabs of 128 bytes of each row, the 16-byte pieces of row i moved
+// by i mod 8, so that reading one piece of eight rows meets no bank conflict.
+// (TMA's gather of four rows an instruction was slower, 163 us against the
+// figures below: each such instruction costs the warp about 14 issue slots,
+// eight asynchronous copies that move as much about 16 for a whole window.)
 //
 // Products.  bf16: matrix instructions (16 x 8 x 16), which take the operands
 // as they lie and leave the issue slots to the copies: on CUDA cores a window
@@ -30,62 +33,84 @@
 namespace usm {
 namespace {
 
-constexpr int kMaxWarps = 4, kMaxStages = 4, kWindow = 16;
+constexpr int kMaxStages = 4, kWindow = 16;
 
-// A warp's ring of stages, and how a window's rows lie in a stage: slab i of a
-// row of K1, then K2, then V (128 bytes of each of the 16 rows).
-struct Stages {
-    int warps;    // warps a CTA
-    int count;    // stages a warp
-    int slabs_d;  // slabs of a row of K1 or K2, and of V
-    int slabs_n;
-};
+// A stage holds, slab after slab (128 bytes of each of the 16 rows), SD slabs of
+// K1, SD of K2 with two maps, and SN of V.
 constexpr int kSlab = kWindow * 128;
+template <bool TWO, int SD, int SN>
+constexpr int kStageBytes = ((TWO ? 2 : 1) * SD + SN) * kSlab;
 
-struct GatherMaps {
-    CUtensorMap k1, k2, v;
-};
+// Warps a CTA: four while two stages each fit in 96 KB (two CTAs an SM), else
+// two; as many stages as fit there, 2 to kMaxStages.
+constexpr int ring_warps(int stage_bytes) { return stage_bytes <= 12 * 1024 ? 4 : 2; }
+constexpr int ring_stages(int stage_bytes) {
+    const int n = 96 * 1024 / (ring_warps(stage_bytes) * stage_bytes);
+    return n < 2 ? 2 : n > kMaxStages ? kMaxStages : n;
+}
 
 // Sums of a CTA's warps: o by column, the maximum and the sum of weights.
-template <int MAPS, int NC>
+template <int MAPS, int NC, int WARPS>
 struct Joined {
-    float part[MAPS][kMaxWarps][NC];
-    float stat[MAPS][kMaxWarps][2];
+    float part[MAPS][WARPS][NC];
+    float stat[MAPS][WARPS][2];
     float whole[MAPS][NC + 2];
 };
 
-// One warp's windows of its row and the ring their rows are copied into.
-struct Ring {
-    uint32_t base, stage_bytes, bars;  // shared addresses; bytes a stage
-    int (*cols)[kWindow];              // columns of each stage's entries
-    int p0, p1, lane, count, slabs_d, slabs, maps;
-    long long windows, first, stride;  // the warp's windows: first, first + stride, ...
+__device__ __forceinline__ void copy_piece(uint32_t dst, const unsigned char* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most LEFT of the thread's groups are in flight.
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
-    __device__ __forceinline__ int size(long long w) const {
-        return (int)min((long long)kWindow, p1 - p0 - w * kWindow);
-    }
+// One warp's windows of its row, and the ring their rows are copied into.  A
+// lane copies one 16-byte piece (lane mod 8) of a row (lane / 8, of four at
+// once) in every slab.
+template <bool TWO, int SD, int SN, int ES>
+struct Ring {
+    static constexpr int kBytes = kStageBytes<TWO, SD, SN>, kWarps = ring_warps(kBytes), kCount = ring_stages(kBytes);
+    uint32_t base;                      // shared address
+    int (*cols)[kWindow];               // columns of each stage's entries
+    int p0, p1, lane;
+    int windows, first, stride;         // the warp's windows: first, first + stride, ... < windows
+    int bytes_d[SD], bytes_n[SN];       // bytes of the lane's piece inside D and N: the rest become zeros, unread
+    const unsigned char *k1, *k2, *v;   // the operands, at the lane's piece
+
+    __device__ __forceinline__ int size(int w) const { return min(kWindow, p1 - (p0 + w * kWindow)); }
     // Column of entry `lane` of window w (the last entry's past the row's end).
-    __device__ __forceinline__ int load_col(const int* __restrict__ ci, long long w) const {
-        return w < windows && lane < kWindow ? __ldg(ci + min(p0 + w * kWindow + lane, (long long)p1 - 1)) : 0;
+    __device__ __forceinline__ int load_col(const int* __restrict__ ci, int w) const {
+        return w < windows && lane < kWindow ? __ldg(ci + p0 + w * kWindow + min(lane, size(w) - 1)) : 0;
     }
-    // Copies window w's rows into stage s: lane = quad of entries + 4·slab.
-    __device__ __forceinline__ void issue(const GatherMaps& m, long long w, int s, int col, int K, int slab_cols) const {
-        const int quads = (size(w) + 3) / 4, quad = lane & 3;
-        if (lane < kWindow) cols[s][lane] = col;
-        col = min(max(col, 0), K - 1);
-        const int y0 = __shfl_sync(kFullMask, col, 4 * quad), y1 = __shfl_sync(kFullMask, col, 4 * quad + 1);
-        const int y2 = __shfl_sync(kFullMask, col, 4 * quad + 2), y3 = __shfl_sync(kFullMask, col, 4 * quad + 3);
-        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * s, quads * 512 * slabs);
-        __syncwarp();
-        if (quad < quads) {
-            for (int i = lane >> 2; i < slabs; i += 8) {
-                const int k2 = i - slabs_d, v = i - maps * slabs_d;
-                const CUtensorMap* map = v >= 0 ? &m.v : k2 >= 0 ? &m.k2 : &m.k1;
-                const int x = v >= 0 ? v : k2 >= 0 ? k2 : i;
-                tma_gather_rows4(base + s * stage_bytes + i * kSlab + quad * 512, map, x * slab_cols, y0, y1, y2, y3,
-                                 bars + 8 * s);
+    // Copies window w's rows into stage s (one group, empty past the last window).
+    __device__ __forceinline__ void issue(const AttnArgs& a, int w, int s, int col) const {
+        if (w < windows) {
+            if (lane < kWindow) cols[s][lane] = col;
+            col = min(max(col, 0), a.K - 1);
+            const int n = size(w);
+            const uint32_t dst = base + s * kBytes + (lane >> 3) * 128;
+#pragma unroll
+            for (int i = 0; i < kWindow / 4; ++i) {
+                const int row = i * 4 + (lane >> 3);
+                const long long c = (long long)__shfl_sync(kFullMask, col, row) * ES;
+                if (i * 4 >= n) break;
+                const uint32_t at = dst + i * 512 + (((lane ^ row) & 7) << 4);
+                const unsigned char *r1 = k1 + c * a.ldk, *rv = v + c * a.ldv;
+#pragma unroll
+                for (int j = 0; j < SD; ++j) copy_piece(at + j * kSlab, r1 + j * 128, bytes_d[j]);
+                if constexpr (TWO) {
+                    const unsigned char* r2 = k2 + c * a.ldk2;
+#pragma unroll
+                    for (int j = 0; j < SD; ++j) copy_piece(at + (SD + j) * kSlab, r2 + j * 128, bytes_d[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < SN; ++j) copy_piece(at + ((TWO ? 2 : 1) * SD + j) * kSlab, rv + j * 128, bytes_n[j]);
             }
         }
+        copies_commit();
     }
 };
 
@@ -93,19 +118,18 @@ struct Ring {
 __device__ __forceinline__ float join_weight(float m_i, float top) { return m_i == -INFINITY ? 0.f : __expf(m_i - top); }
 
 // The CTA's warps (in `sh`), then the cluster's CTAs, and the row of C.
-template <int MAPS, int NC>
-__device__ __forceinline__ void join(Joined<MAPS, NC>& sh, const AttnArgs& a, int r, int head, int warps, int ctas,
-                                     int rank) {
+template <int MAPS, int NC, int WARPS>
+__device__ __forceinline__ void join(Joined<MAPS, NC, WARPS>& sh, const AttnArgs& a, int r, int head, int ctas, int rank) {
     __syncthreads();
-    const int threads = warps * 32;
+    constexpr int threads = WARPS * 32;
     const float lam = MAPS > 1 ? __ldg(a.lambda + head) : 0.f;
     for (int j = threadIdx.x; j < a.N; j += threads) {
         float res = 0.f;
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             float top = -INFINITY, x = 0.f, sum = 0.f;
-            for (int i = 0; i < warps; ++i) top = fmaxf(top, sh.stat[k][i][0]);
-            for (int i = 0; i < warps; ++i) {
+            for (int i = 0; i < WARPS; ++i) top = fmaxf(top, sh.stat[k][i][0]);
+            for (int i = 0; i < WARPS; ++i) {
                 const float f = join_weight(sh.stat[k][i][0], top);
                 x += f * sh.part[k][i][j];
                 sum += f * sh.stat[k][i][1];
@@ -154,14 +178,16 @@ __device__ __forceinline__ void load_matrix4_trans(uint32_t at, uint32_t (&x)[4]
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                  : "r"(at));
 }
-// Rows 0-7 of D = A·B + C (16 x 8 x 16, bf16 in, fp32 sums); rows 8-15 of A are
-// zero, so are theirs.
-__device__ __forceinline__ void mma_upper(float& c0, float& c1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-    [[maybe_unused]] float z2, z3;
+// Rows 0-7 of A·B + (c0, c1) (16 x 8 x 16, bf16 in, fp32 sums); rows 8-15 of A
+// are zero, and theirs are dropped.
+__device__ __forceinline__ float2 mma_upper(float2 c, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+    float2 d;
+    [[maybe_unused]] float d2, d3;
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%9,%9};"
-        : "+f"(c0), "+f"(c1), "=f"(z2), "=f"(z3)
-        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%9,%10,%11,%11};"
+        : "=f"(d.x), "=f"(d.y), "=f"(d2), "=f"(d3)
+        : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(0.f));
+    return d;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t w;
@@ -171,59 +197,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // Everything both kernels do before their first window; false for a row
 // without entries (its output is written).
-template <int MAPS>
-__device__ __forceinline__ bool start_row(const GatherMaps& maps, const AttnArgs& a, const Stages& st, Ring& ring,
-                                          unsigned char* smem, uint64_t* bars, int (*cols)[kWindow], int r, int ctas,
-                                          int rank, int slab_cols) {
+template <bool TWO, int SD, int SN, int ES>
+__device__ __forceinline__ bool start_row(const AttnArgs& a, Ring<TWO, SD, SN, ES>& ring, unsigned char* smem,
+                                          int (*cols)[Ring<TWO, SD, SN, ES>::kCount][kWindow], int r, int ctas, int rank) {
+    using R = Ring<TWO, SD, SN, ES>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     row_range(a.row_offsets, r, a.nnz, ring.p0, ring.p1);
     if (ring.p0 == ring.p1) {  // the same in every CTA of the cluster
         if (rank == 0)
-            for (int j = threadIdx.x; j < a.N; j += st.warps * 32) a.C[(long long)r * a.ldc + j] = 0.f;
+            for (int j = threadIdx.x; j < a.N; j += R::kWarps * 32) a.C[(long long)r * a.ldc + j] = 0.f;
         return false;
     }
     ring.lane = lane;
-    ring.maps = MAPS;
-    ring.count = st.count;
-    ring.slabs_d = st.slabs_d;
-    ring.slabs = MAPS * st.slabs_d + st.slabs_n;
-    ring.stage_bytes = ring.slabs * kSlab;
-    ring.base = smem_addr(smem) + warp * st.count * ring.stage_bytes;
-    ring.bars = smem_addr(bars);
-    ring.cols = cols;
-    ring.windows = ((long long)(ring.p1 - ring.p0) + kWindow - 1) / kWindow;
-    ring.first = rank * st.warps + warp;
-    ring.stride = (long long)ctas * st.warps;
-    int ahead[kMaxStages];
+    ring.base = smem_addr(smem) + warp * R::kCount * R::kBytes;
+    ring.cols = cols[warp];
+    ring.windows = (ring.p1 - ring.p0 - 1) / kWindow + 1;
+    ring.first = rank * R::kWarps + warp;
+    ring.stride = ctas * R::kWarps;
+    const int piece = (lane & 7) * 16;
 #pragma unroll
-    for (int s = 0; s < kMaxStages; ++s)
-        ahead[s] = s < st.count ? ring.load_col(a.col_indices, ring.first + s * ring.stride) : 0;
-    if (lane < st.count) mbar_init(ring.bars + 8 * lane, 1);
-    if (threadIdx.x == 0) {
-        prefetch_tensor_map(&maps.v);
-        if (a.D > 0) prefetch_tensor_map(&maps.k1);
-        if (MAPS > 1 && a.D > 0) prefetch_tensor_map(&maps.k2);
+    for (int j = 0; j < SD; ++j) ring.bytes_d[j] = min(max(a.D * ES - j * 128 - piece, 0), 16);
+#pragma unroll
+    for (int j = 0; j < SN; ++j) ring.bytes_n[j] = min(max(a.N * ES - j * 128 - piece, 0), 16);
+    ring.k1 = static_cast<const unsigned char*>(a.Km) + piece;
+    ring.k2 = static_cast<const unsigned char*>(a.K2) + piece;
+    ring.v = static_cast<const unsigned char*>(a.V) + piece;
+    int ahead[R::kCount];
+#pragma unroll
+    for (int s = 0; s < R::kCount; ++s) ahead[s] = ring.load_col(a.col_indices, ring.first + s * ring.stride);
+#pragma unroll 1
+    for (int s = 0; s < R::kCount; ++s) {
+        int col = ahead[0];
+#pragma unroll
+        for (int i = 1; i < R::kCount; ++i) col = s == i ? ahead[i] : col;
+        ring.issue(a, ring.first + s * ring.stride, s, col);
     }
-    fence_barrier_init();
-    __syncwarp();
-#pragma unroll
-    for (int s = 0; s < kMaxStages; ++s)
-        if (s < st.count && ring.first + s * ring.stride < ring.windows)
-            ring.issue(maps, ring.first + s * ring.stride, s, ahead[s], a.K, slab_cols);
     return true;
-}
-
-// A copy never landed: say so, and wait (bounded) for those in flight, so that
-// none lands after the CTA has gone.  The row is incomplete.
-__device__ __forceinline__ void give_up(const AttnArgs& a, const Ring& ring) {
-    if (ring.lane == 0) {
-        record_status(a.status, USM_ERR_TIMEOUT);
-        for (int i = 0; i < ring.count; ++i) {
-            mbar_wait_bounded(ring.bars + 8 * i, 0, 1000000ull);
-            mbar_wait_bounded(ring.bars + 8 * i, 1, 1000000ull);
-        }
-    }
-    __syncwarp();
 }
 
 // bf16.  With lane = 4·row + t, a matrix instruction gives the lane elements
@@ -237,31 +246,27 @@ __device__ __forceinline__ void give_up(const AttnArgs& a, const Ring& ring) {
 // part of its row alone, and nothing is exchanged but two shuffles for the
 // maximum.  Each window's products with V start from zero and are added to the
 // running sums in fp32: matrix instructions do not round their sums to nearest.
-// NT: tiles of 8 columns of V.
-template <bool TWO, int NT>
-__global__ void __launch_bounds__(kMaxWarps * 32)
-    attention_bf16_kernel(const __grid_constant__ GatherMaps maps, const AttnArgs a, const Stages st) {
-    constexpr int MAPS = TWO ? 2 : 1, NC = NT * 8;
-    extern __shared__ unsigned char smem_base[];
-    __shared__ Joined<MAPS, NC> sh;
-    __shared__ int cols[kMaxWarps][kMaxStages][kWindow];
-    __shared__ uint64_t bars[kMaxWarps][kMaxStages];
-    // Slabs start on 1024 bytes (the swizzle's period).
-    unsigned char* smem = smem_base + ((1024 - (smem_addr(smem_base) & 1023)) & 1023);
+template <bool TWO, int SD, int SN>
+__global__ void __launch_bounds__(ring_warps(kStageBytes<TWO, SD, SN>) * 32) attention_bf16_kernel(const AttnArgs a) {
+    constexpr int MAPS = TWO ? 2 : 1, NT = SN * 8, NC = NT * 8;  // tiles of 8 columns of V
+    constexpr int kSteps = SD * 4;                               // steps of 16 dimensions
+    using R = Ring<TWO, SD, SN, 2>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Joined<MAPS, NC, R::kWarps> sh;
+    __shared__ int cols[R::kWarps][R::kCount][kWindow];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
-    Ring ring;
-    if (!start_row<MAPS>(maps, a, st, ring, smem, bars[warp], cols[warp], r, ctas, rank, 64)) return;
+    R ring;
+    if (!start_row(a, ring, smem, cols, r, ctas, rank)) return;
     const int block = r / a.seg_rows, head = block % a.heads;
     const int start =
         a.bias.table ? rel_start(a.bias, block, r - block * a.seg_rows, __ldg(a.col_indices + ring.p0)) : 0;
 
-    // q, in steps of 16 dimensions: for each t the two words the lane passes.
-    const int ksteps = (a.D + 15) / 16;
-    uint32_t* qs = reinterpret_cast<uint32_t*>(smem + st.warps * st.count * ring.stage_bytes);
-    for (int i = threadIdx.x; i < MAPS * ksteps * 8; i += st.warps * 32) {
-        const int k = i / (ksteps * 8), w = i - k * ksteps * 8;
+    // q in steps of 16 dimensions (zeros past D): for each t the two words the lane passes.
+    uint32_t* qs = reinterpret_cast<uint32_t*>(smem + R::kWarps * R::kCount * R::kBytes);
+    for (int i = threadIdx.x; i < MAPS * kSteps * 8; i += R::kWarps * 32) {
+        const int k = i / (kSteps * 8), w = i % (kSteps * 8);
         const int d = w / 8 * 16 + (w & 7) / 2 * 2 + (w & 1) * 8;
         const uint16_t* q = static_cast<const uint16_t*>(k ? a.Q2 : a.Q) + (long long)r * (k ? a.ldq2 : a.ldq);
         const uint32_t lo = d < a.D ? __ldg(q + d) : 0, hi = d + 1 < a.D ? __ldg(q + d + 1) : 0;
@@ -279,32 +284,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     const uint32_t q_addr = smem_addr(qs) + t * 8;
 
     float m = -INFINITY, z = 0.f;  // the lane's map's
-    float o[NT][2];
+    float2 o[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = 0.f;
-    bool alive = true;
-    int s = 0, phase = 0;
-    for (long long w = ring.first; w < ring.windows; w += ring.stride) {
-        const int next = ring.load_col(a.col_indices, w + ring.count * ring.stride);
-        const uint32_t stage = ring.base + s * ring.stage_bytes;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(ring.bars + 8 * s, phase, kWaitLimitNs))) {
-            alive = false;
-            break;
-        }
+    for (int i = 0; i < NT; ++i) o[i] = make_float2(0.f, 0.f);
+    int s = 0;
+#pragma unroll 1
+    for (int w = ring.first; w < ring.windows; w += ring.stride) {
+        const int next = ring.load_col(a.col_indices, w + R::kCount * ring.stride);
+        const uint32_t stage = ring.base + s * R::kBytes;
+        copies_wait<R::kCount - 1>();
+        __syncwarp();  // every lane's copies have landed
         // Dot products: 4 of each map in every lane.
-        float x[MAPS][4];
+        float2 x[MAPS][2];
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[k][u] = 0.f;
-            const uint32_t at = stage + k * st.slabs_d * kSlab + k_row, q = q_addr + k * ksteps * 32;
+            x[k][0] = x[k][1] = make_float2(0.f, 0.f);
 #pragma unroll 4
-            for (int c = 0; c < ksteps; ++c) {
+            for (int c = 0; c < kSteps; ++c) {
                 uint32_t b[4];
-                load_matrix4(at + (c >> 2) * kSlab + ((((c & 3) * 2 + k_piece) ^ tile_row) << 4), b);
-                const uint2 qw = lds64(q + c * 32);
-                mma_upper(x[k][0], x[k][1], qw.x, qw.y, b[0], b[1]);
-                mma_upper(x[k][2], x[k][3], qw.x, qw.y, b[2], b[3]);
+                load_matrix4(stage + k_row + (k * SD + c / 4) * kSlab + (((c % 4 * 2 + k_piece) ^ tile_row) << 4), b);
+                const uint2 qw = lds64(q_addr + (k * kSteps + c) * 32);
+                x[k][0] = mma_upper(x[k][0], qw.x, qw.y, b[0], b[1]);
+                x[k][1] = mma_upper(x[k][1], qw.x, qw.y, b[2], b[3]);
             }
         }
         // Scores of the lane's map; entries that no map uses.
@@ -321,7 +322,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
             bool none = true;
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
-                y[k] = en < n ? fmaf(x[k][u], a.scale, bias) : -INFINITY;
+                const float dot = u & 1 ? x[k][u >> 1].y : x[k][u >> 1].x;
+                y[k] = en < n ? fmaf(dot, a.scale, bias) : -INFINITY;
                 none = none && y[k] == -INFINITY;
             }
             sc[u] = mine ? y[MAPS - 1] : y[0];
@@ -334,10 +336,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
             const float f = __expf(m - top);
             z *= f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                o[i][0] *= f;
-                o[i][1] *= f;
-            }
+            for (int i = 0; i < NT; ++i) o[i] = __fmul2_rn(o[i], make_float2(f, f));
             m = top;
         }
         const float base = m == -INFINITY ? 0.f : m;
@@ -367,38 +366,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
             unused |= __shfl_xor_sync(kFullMask, unused, 1);
             unused |= __shfl_xor_sync(kFullMask, unused, 2);
             for (; unused; unused &= unused - 1) {
-                const uint32_t at = stage + MAPS * st.slabs_d * kSlab + (__ffs(unused) - 1) * 128;
-                for (int i = lane; i < st.slabs_n * 8; i += 32)
+                const uint32_t at = stage + MAPS * SD * kSlab + (__ffs(unused) - 1) * 128;
+                for (int i = lane; i < SN * 8; i += 32)
                     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + (i >> 3) * kSlab + (i & 7) * 16), "r"(0)
                                  : "memory");
             }
             __syncwarp();
         }
-        const uint32_t v_at = stage + MAPS * st.slabs_d * kSlab + v_row;
+        const uint32_t v_at = stage + MAPS * SD * kSlab + v_row;
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
-            if (i * 16 >= a.N) break;
             uint32_t b[4];
-            load_matrix4_trans(v_at + (i >> 2) * kSlab + ((((i & 3) * 2 + v_piece) ^ tile_row) << 4), b);
+            load_matrix4_trans(v_at + i / 4 * kSlab + (((i % 4 * 2 + v_piece) ^ tile_row) << 4), b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float c0 = 0.f, c1 = 0.f;
-                mma_upper(c0, c1, w0, w1, b[2 * h], b[2 * h + 1]);
-                o[2 * i + h][0] += c0;
-                o[2 * i + h][1] += c1;
-            }
+            for (int h = 0; h < 2; ++h)
+                o[2 * i + h] = __fadd2_rn(o[2 * i + h],
+                                          mma_upper(make_float2(0.f, 0.f), w0, w1, b[2 * h], b[2 * h + 1]));
         }
         __syncwarp();  // every lane is done with the stage
-        if (w + ring.count * ring.stride < ring.windows) {
-            fence_proxy_async_smem();
-            ring.issue(maps, w + ring.count * ring.stride, s, next, a.K, 64);
-        }
-        if (++s == ring.count) {
-            s = 0;
-            phase ^= 1;
-        }
+        ring.issue(a, w + R::kCount * ring.stride, s, next);
+        s = s + 1 == R::kCount ? 0 : s + 1;
     }
-    if (!alive) give_up(a, ring);
 
     z += __shfl_xor_sync(kFullMask, z, 1);
     z += __shfl_xor_sync(kFullMask, z, 2);
@@ -411,45 +399,44 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float mid = __shfl_down_sync(kFullMask, o[i][u], 4), low = __shfl_down_sync(kFullMask, o[i][u], 8);
-            if (writes) sh.part[mine][warp][i * 8 + 2 * t + u] = o[i][u] + (mid + low);
+            const float high = u ? o[i].y : o[i].x;
+            const float mid = __shfl_down_sync(kFullMask, high, 4), low = __shfl_down_sync(kFullMask, high, 8);
+            if (writes) sh.part[mine][warp][i * 8 + 2 * t + u] = high + (mid + low);
         }
-    join(sh, a, r, head, st.warps, ctas, rank);
+    join(sh, a, r, head, ctas, rank);
 }
 
 // fp32 on CUDA cores.  Scores: two lanes to an entry, each summing every other
 // piece of 16 bytes.  Output: LV lanes to a row of V, four columns a lane (NP
 // times), 32 / LV entries at once, weights broadcast by shuffles.
-template <bool TWO, int LV, int NP>
-__global__ void __launch_bounds__(kMaxWarps * 32)
-    attention_f32_kernel(const __grid_constant__ GatherMaps maps, const AttnArgs a, const Stages st) {
-    constexpr int G = 32 / LV;       // rows of V a step
-    constexpr int NC = LV * NP * 4;  // columns a row of V can have
+template <bool TWO, int SD, int SN>
+__global__ void __launch_bounds__(ring_warps(kStageBytes<TWO, SD, SN>) * 32) attention_f32_kernel(const AttnArgs a) {
     constexpr int MAPS = TWO ? 2 : 1;
-    extern __shared__ unsigned char smem_base[];
-    __shared__ Joined<MAPS, NC> sh;
-    __shared__ int cols[kMaxWarps][kMaxStages][kWindow];
-    __shared__ uint64_t bars[kMaxWarps][kMaxStages];
-    unsigned char* smem = smem_base + ((1024 - (smem_addr(smem_base) & 1023)) & 1023);
+    constexpr int LV = SN >= 4 ? 32 : SN * 8, NP = SN * 8 / LV;
+    constexpr int G = 32 / LV;       // rows of V a step
+    constexpr int NC = LV * NP * 4;  // columns of the slabs
+    using R = Ring<TWO, SD, SN, 4>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Joined<MAPS, NC, R::kWarps> sh;
+    __shared__ int cols[R::kWarps][R::kCount][kWindow];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
-    Ring ring;
-    if (!start_row<MAPS>(maps, a, st, ring, smem, bars[warp], cols[warp], r, ctas, rank, 32)) return;
+    R ring;
+    if (!start_row(a, ring, smem, cols, r, ctas, rank)) return;
     const int block = r / a.seg_rows, head = block % a.heads;
     const int start =
         a.bias.table ? rel_start(a.bias, block, r - block * a.seg_rows, __ldg(a.col_indices + ring.p0)) : 0;
     // Q1 and Q2 in whole slabs, zeros past D.
-    float* qs = reinterpret_cast<float*>(smem + st.warps * st.count * ring.stage_bytes);
-    for (int i = threadIdx.x; i < MAPS * st.slabs_d * 32; i += st.warps * 32) {
-        const int per = st.slabs_d * 32, k = i / per, d = i - k * per;
+    float* qs = reinterpret_cast<float*>(smem + R::kWarps * R::kCount * R::kBytes);
+    for (int i = threadIdx.x; i < MAPS * SD * 32; i += R::kWarps * 32) {
+        const int k = i / (SD * 32), d = i % (SD * 32);
         const float* q = static_cast<const float*>(k ? a.Q2 : a.Q) + (long long)r * (k ? a.ldq2 : a.ldq);
         qs[i] = d < a.D ? __ldg(q + d) : 0.f;
     }
     __syncthreads();
 
     const int entry = lane & (kWindow - 1), share = lane / kWindow;
-    const int pieces = (a.D + 3) / 4;
     const int g = lane / LV, l = lane % LV;
     float m[MAPS], z[MAPS];
     float2 o[MAPS][NP][2];
@@ -465,18 +452,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int byte = (i * LV + l) * 16;
-        v_slab[i] = (MAPS * st.slabs_d + min(byte / 128, st.slabs_n - 1)) * kSlab;
+        v_slab[i] = (MAPS * SD + byte / 128) * kSlab;
         v_byte[i] = byte % 128;
     }
-    bool alive = true;
-    int s = 0, phase = 0;
-    for (long long w = ring.first; w < ring.windows; w += ring.stride) {
-        const int next = ring.load_col(a.col_indices, w + ring.count * ring.stride);
-        const uint32_t stage = ring.base + s * ring.stage_bytes;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(ring.bars + 8 * s, phase, kWaitLimitNs))) {
-            alive = false;
-            break;
-        }
+    int s = 0;
+#pragma unroll 1
+    for (int w = ring.first; w < ring.windows; w += ring.stride) {
+        const int next = ring.load_col(a.col_indices, w + R::kCount * ring.stride);
+        const uint32_t stage = ring.base + s * R::kBytes;
+        copies_wait<R::kCount - 1>();
+        __syncwarp();  // every lane's copies have landed
         const int n = ring.size(w);
         const bool in = entry < n;
         float bias = 0.f;
@@ -487,10 +472,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             float2 x = make_float2(0.f, 0.f), y = x;
-            const uint32_t at = stage + k * st.slabs_d * kSlab + entry * 128, q = smem_addr(qs) + k * st.slabs_d * 128;
-#pragma unroll 4
-            for (int c = share; c < pieces; c += 2) {
-                const uint4 kw = lds128(at + (c >> 3) * kSlab + (((c ^ entry) & 7) << 4)), qw = lds128(q + c * 16);
+            const uint32_t at = stage + k * SD * kSlab + entry * 128, q = smem_addr(qs) + k * SD * 128 + share * 16;
+            const int flip = (entry ^ share) & 7;
+#pragma unroll 8
+            for (int c = 0; c < SD * 8; c += 2) {
+                const uint4 kw = lds128(at + (c >> 3) * kSlab + (((c & 7) ^ flip) << 4)), qw = lds128(q + c * 16);
                 x = __ffma2_rn(make_float2(__uint_as_float(kw.x), __uint_as_float(kw.y)),
                                make_float2(__uint_as_float(qw.x), __uint_as_float(qw.y)), x);
                 y = __ffma2_rn(make_float2(__uint_as_float(kw.z), __uint_as_float(kw.w)),
@@ -543,16 +529,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
             }
         }
         __syncwarp();  // every lane is done with the stage
-        if (w + ring.count * ring.stride < ring.windows) {
-            fence_proxy_async_smem();
-            ring.issue(maps, w + ring.count * ring.stride, s, next, a.K, 32);
-        }
-        if (++s == ring.count) {
-            s = 0;
-            phase ^= 1;
-        }
+        ring.issue(a, w + R::kCount * ring.stride, s, next);
+        s = s + 1 == R::kCount ? 0 : s + 1;
     }
-    if (!alive) give_up(a, ring);
 
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
@@ -573,36 +552,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
             }
         }
     }
-    join(sh, a, r, head, st.warps, ctas, rank);
+    join(sh, a, r, head, ctas, rank);
 }
 
-template <bool BF, bool TWO, class Kernel>
-int launch_kernel(Kernel kernel, const AttnArgs& a, cudaStream_t stream) {
-    constexpr int ES = BF ? 2 : 4, MAPS = TWO ? 2 : 1;
-    Stages st;
-    st.slabs_d = (a.D * ES + 127) / 128;
-    st.slabs_n = (a.N * ES + 127) / 128;
-    // A stage is 0.25 to 48 KB.  Four warps a CTA while two stages each fit in
-    // about 96 KB (so that two CTAs fit an SM), else two; as many stages as fit.
-    const int stage_bytes = (MAPS * st.slabs_d + st.slabs_n) * kSlab;
-    st.warps = stage_bytes <= 12 * 1024 ? 4 : 2;
-    st.count = 96 * 1024 / (st.warps * stage_bytes);
-    st.count = st.count < 2 ? 2 : st.count > kMaxStages ? kMaxStages : st.count;
-    const int smem = 1024 + st.warps * st.count * stage_bytes + MAPS * st.slabs_d * 128;
-
-    GatherMaps maps;
-    if (!encode_gather_map(&maps.v, a.V, BF, a.K, a.N, a.ldv)) return USM_ERR_CUDA;
-    maps.k1 = maps.k2 = maps.v;
-    if (a.D > 0 && !encode_gather_map(&maps.k1, a.Km, BF, a.K, a.D, a.ldk)) return USM_ERR_CUDA;
-    if (TWO && a.D > 0 && !encode_gather_map(&maps.k2, a.K2, BF, a.K, a.D, a.ldk2)) return USM_ERR_CUDA;
-
+template <bool BF, bool TWO, int SD, int SN>
+int launch_slabs(const AttnArgs& a, cudaStream_t stream) {
+    using R = Ring<TWO, SD, SN, BF ? 2 : 4>;
+    constexpr int smem = R::kWarps * R::kCount * R::kBytes + (TWO ? 2 : 1) * SD * 128;
+    constexpr auto kernel = [] {
+        if constexpr (BF)
+            return attention_bf16_kernel<TWO, SD, SN>;
+        else
+            return attention_f32_kernel<TWO, SD, SN>;
+    }();
     // CTAs a row: more until the rows fill the SMs or a row's windows (on
     // average) no longer give every warp one.
     const int sms = sm_count_current_device();
     const long long windows = a.nnz / a.M / kWindow + 1;
     int ctas = 1;
-    while (ctas < 8 && (long long)a.M * ctas < 4LL * sms && (long long)ctas * st.warps < windows) ctas *= 2;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    while (ctas < 8 && (long long)a.M * ctas < 4LL * sms && (long long)ctas * R::kWarps < windows) ctas *= 2;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return USM_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -610,36 +580,34 @@ int launch_kernel(Kernel kernel, const AttnArgs& a, cudaStream_t stream) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.M * ctas));
-    cfg.blockDim = dim3(st.warps * 32);
+    cfg.blockDim = dim3(R::kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, a, st) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
-template <bool TWO>
-int launch_bf16(const AttnArgs& a, cudaStream_t stream) {
-    if (a.N <= 64) return launch_kernel<true, TWO>(attention_bf16_kernel<TWO, 8>, a, stream);
-    if (a.N <= 128) return launch_kernel<true, TWO>(attention_bf16_kernel<TWO, 16>, a, stream);
-    if (a.N <= 256) return launch_kernel<true, TWO>(attention_bf16_kernel<TWO, 32>, a, stream);
-    return launch_kernel<true, TWO>(attention_bf16_kernel<TWO, 64>, a, stream);
-}
-
-template <bool TWO>
-int launch_f32(const AttnArgs& a, cudaStream_t stream) {
-    if (a.N <= 32) return launch_kernel<false, TWO>(attention_f32_kernel<TWO, 8, 1>, a, stream);
-    if (a.N <= 64) return launch_kernel<false, TWO>(attention_f32_kernel<TWO, 16, 1>, a, stream);
-    if (a.N <= 128) return launch_kernel<false, TWO>(attention_f32_kernel<TWO, 32, 1>, a, stream);
-    return launch_kernel<false, TWO>(attention_f32_kernel<TWO, 32, 2>, a, stream);
+// Slabs: 1, 2, 4 or 8 of K, and as many or twice as many of V.
+template <bool BF, bool TWO>
+int launch_type(const AttnArgs& a, cudaStream_t stream) {
+    constexpr int per = BF ? 64 : 32;
+    const int d = (a.D + per - 1) / per, n = (a.N + per - 1) / per;
+    if (d <= 1 && n <= 1) return launch_slabs<BF, TWO, 1, 1>(a, stream);
+    if (d <= 1 && n <= 2) return launch_slabs<BF, TWO, 1, 2>(a, stream);
+    if (d <= 2 && n <= 2) return launch_slabs<BF, TWO, 2, 2>(a, stream);
+    if (d <= 2 && n <= 4) return launch_slabs<BF, TWO, 2, 4>(a, stream);
+    if (d <= 4 && n <= 4) return launch_slabs<BF, TWO, 4, 4>(a, stream);
+    if (d <= 4 && n <= 8) return launch_slabs<BF, TWO, 4, 8>(a, stream);
+    return launch_slabs<BF, TWO, 8, 8>(a, stream);
 }
 
 }  // namespace
 
 int launch_attention(const AttnArgs& a, bool bf16, cudaStream_t stream) {
     const bool two = a.lambda != nullptr;
-    if (bf16) return two ? launch_bf16<true>(a, stream) : launch_bf16<false>(a, stream);
-    return two ? launch_f32<true>(a, stream) : launch_f32<false>(a, stream);
+    if (bf16) return two ? launch_type<true, true>(a, stream) : launch_type<true, false>(a, stream);
+    return two ? launch_type<false, true>(a, stream) : launch_type<false, false>(a, stream);
 }
 
 }  // namespace usm

@@ -52,10 +52,6 @@ inline bool taller_chunk_pays(int K, int kc, int kc_tall) {
 bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
                           long long cols, long long ld_elems, int box_cols, int box_rows);
 
-// The same for gathered rows: a box one row high and 128 bytes wide, its
-// 16-byte pieces swizzled by the row (128-byte pattern).
-bool encode_gather_map(CUtensorMap* map, const void* base, bool bf16, long long rows, long long cols, long long ld_elems);
-
 // softmax: a.values are fp32 scores and each row's values are their softmax
 // probabilities, rounded to B's element type (csr_spmm_row_softmax).
 int launch_spmm(const SpmmArgs& a, const void* B, int ldb, bool bf16, cudaStream_t stream, bool softmax = false);
