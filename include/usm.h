@@ -405,14 +405,20 @@ int csr_row_softmax_grad(int M, int nnz, const int *row_offsets, const float *sc
  *   C     : M×N fp32, ldc ≥ N, overwritten; a row with no entry, or whose
  *           scores are all -inf in both maps, is zero.  Rows of V under an
  *           entry that is -inf in every map are not used, whatever they hold.
+ *   workspace : csr_attention_workspace_bytes(M, K, D, N, nnz, two_maps, dtype)
+ *           bytes of device scratch (two_maps: lambda is given), 16-byte
+ *           aligned, contents ignored; 0 bytes for small problems.
  * Limits: D, N ≤ 256 (fp32) or 512 (bf16).  Alignment as csr_spmm.
  * Deterministic (no atomics).  Empty cases: M = 0 or N = 0 is a no-op;
  * nnz = 0 zero-fills C; D = 0 reads no Q or K and has zero products (weights by the bias alone).
  */
+size_t csr_attention_workspace_bytes(int M, int K, int D, int N, int nnz, int two_maps, usm_dtype dtype);
+
 int csr_attention(int M, int K, int D, int N, int nnz, const int *row_offsets, const int *col_indices,
                   const void *Q, int ldq, const void *Km, int ldk, const void *Q2, int ldq2, const void *K2, int ldk2,
                   const void *V, int ldv, float scale, const float *lambda, int num_heads, int seg_rows,
-                  const usm_rel_bias *bias, float *C, int ldc, usm_dtype dtype, void *stream);
+                  const usm_rel_bias *bias, float *C, int ldc, usm_dtype dtype,
+                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * csr_transpose — Aᵀ in CSR, for the sparse layer's input gradient.

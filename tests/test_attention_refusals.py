@@ -42,7 +42,7 @@ def rel_bias_grad(lib, M=4, K=4, nnz=4, ro=A16, ci=A16, ds=A16, dt=0, seg=2, out
 def attention(lib, b=None, **kw):
     v = dict(M=4, K=4, D=8, N=8, nnz=4, ro=A16, ci=A16, Q=A16, ldq=8, Km=A16, ldk=8, Q2=None, ldq2=0, K2=None, ldk2=0,
              V=A16, ldv=8, scale=1.0, lam=None, heads=2, seg=2, bias=ctypes.addressof(b) if b else None, C=A16, ldc=8,
-             dtype=0)
+             dtype=0, ws=None, wsb=0)
     v.update(kw)
     return lib.csr_attention(*v.values(), None)
 
@@ -145,6 +145,12 @@ def test_attention_refuses(lib):
     assert attention(lib, N=260, ldv=260, ldc=260) == UNSUPPORTED
     assert attention(lib, D=513, ldq=520, ldk=520, dtype=1) == UNSUPPORTED
     assert attention(lib, bias(num_heads=3)) == INVALID  # heads disagree
+    big = dict(M=64, nnz=1 << 20, K=1 << 20)
+    need = lib.csr_attention_workspace_bytes(64, 1 << 20, 8, 8, 1 << 20, 0, 0)
+    assert need > 0 and lib.csr_attention_workspace_bytes(4, 4, 8, 8, 4, 0, 0) == 0
+    assert attention(lib, **big) == WORKSPACE
+    assert attention(lib, **big, ws=A16, wsb=need - 1) == WORKSPACE
+    assert attention(lib, **big, ws=ODD4, wsb=need) == ALIGN
     assert attention(lib, M=0, ro=None, C=None) == 0
     assert attention(lib, N=0, C=None) == 0
 

@@ -657,3 +657,27 @@ def test_graph_replay(usm):
     torch.cuda.synchronize()
     for k, v in eager.items():
         assert torch.equal(v, captured[k]), k
+
+
+@pytest.mark.parametrize("maps,dtype,D,N,biased", [(1, "bf16", 64, 64, True), (2, "bf16", 64, 128, False),
+                                                   (2, "bf16", 72, 200, True), (1, "f32", 64, 64, False),
+                                                   (2, "f32", 33, 100, True)])
+@pytest.mark.parametrize("kind", ["even", "long", "skewed", "short"])
+def test_attention_equal_shares(usm, kind, maps, dtype, D, N, biased):
+    """Problems large enough to be dealt out in equal shares of the entries:
+    rows inside a share, cut by one, and over many; empty rows everywhere."""
+    rng = np.random.default_rng([17, sorted(["even", "long", "skewed", "short"]).index(kind)])
+    cols = 30000 if kind == "long" else 4000
+    lengths = {"even": rng.integers(300, 500, 260), "long": np.array([0, 29000, 30000, 17, 30000, 0]),
+               "skewed": np.concatenate([rng.integers(0, 12, 3000), [4000] * 20, rng.integers(0, 12, 2000)]),
+               "short": rng.integers(0, 12, 20000)}[kind]
+    lengths[:: 5 if kind != "long" else 100] = 0
+    seg = 1 if kind in ("even", "long") else 0
+    base = np.arange(lengths.size) % 3 * cols if seg else None
+    ro, ci = W.csr_from_lengths(rng, lengths.astype(np.int64), cols, base)
+    p = dict(rng=rng, ro=ro, ci=ci, M=lengths.size, K=3 * cols if seg else cols, cols=cols, seg=seg,
+             blocks=lengths.size if seg else 1, nnz=ci.size, heads=R.head_of_rows(lengths.size, seg, HEADS),
+             longest=int(lengths.max()))
+    need = usm.load().csr_attention_workspace_bytes(p["M"], p["K"], D, N, p["nnz"], int(maps == 2), int(dtype == "bf16"))
+    assert need > 0
+    run_attention(usm, p, D, N, maps, dtype, biased, pad=True)

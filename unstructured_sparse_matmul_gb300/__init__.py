@@ -60,7 +60,8 @@ SIGNATURES.update({
     "csr_diff_softmax_grad": (_i, [_i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
     "csr_row_softmax_grad": (_i, [_i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp]),
     "csr_attention": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i,
-                           ctypes.c_float, _vp, _i, _i, _vp, _vp, _i, _i, _vp]),
+                           ctypes.c_float, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+    "csr_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
 })
 
 
@@ -618,7 +619,7 @@ def _operand(t, name, index, dtypes, rows, cols):
 
 @_on_stream
 def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K2=None, lam=None, seg_rows: int = 0,
-              table=None, bucket_map=None, seg_cols: int = 0, q_offset=None, out=None):
+              table=None, bucket_map=None, seg_cols: int = 0, q_offset=None, out=None, workspace=None):
     """Sparse attention of few query rows in one pass (fp32 out): softmax of
     scale*(Q[r].Km[col]) + bias over each row's entries, times V; with Q2, K2
     and lam the differential map, with table and bucket_map the relative
@@ -663,9 +664,12 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
         if tuple(out.shape) != (M, N):
             raise ValueError("out must be M x N")
         ldc = _ld(out)
+    code = _code(Km, T)
+    need = lib.csr_attention_workspace_bytes(M, K, D, N, nnz, int(lam is not None), code)
+    ws = _workspace(workspace, need, Km, T)
     _run("csr_attention", lib.csr_attention, index, T, M, K, D, N, nnz, row_offsets.data_ptr(), col_indices.data_ptr(),
          Q.data_ptr(), ldq, Km.data_ptr(), ldk, _ptr(Q2), ldq2, _ptr(K2), ldk2, V.data_ptr(), ldv, scale, _ptr(lam),
-         heads, seg_rows, None if b is None else ctypes.addressof(b), out.data_ptr(), ldc, _code(Km, T))
+         heads, seg_rows, None if b is None else ctypes.addressof(b), out.data_ptr(), ldc, code, _ptr(ws), need)
     return out
 
 

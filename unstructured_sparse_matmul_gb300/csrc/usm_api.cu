@@ -436,10 +436,25 @@ int csr_row_softmax_grad(int M, int nnz, const int* row_offsets, const float* sc
     return launch_row_softmax_grad(a, as_stream(stream));
 }
 
+size_t csr_attention_workspace_bytes(int M, int K, int D, int N, int nnz, int two_maps, usm_dtype dtype) {
+    const int most = dtype == USM_BF16 ? 512 : 256;
+    if (M <= 0 || K <= 0 || D < 0 || D > most || N <= 0 || N > most || nnz <= 0) return 0;
+    AttnArgs a{};
+    a.M = M;
+    a.K = K;
+    a.D = D;
+    a.N = N;
+    a.nnz = nnz;
+    static const float one = 1.f;
+    a.lambda = two_maps ? &one : nullptr;  // only whether there is one
+    return attention_workspace_bytes(a, dtype == USM_BF16);
+}
+
 int csr_attention(int M, int K, int D, int N, int nnz, const int* row_offsets, const int* col_indices,
                   const void* Q, int ldq, const void* Km, int ldk, const void* Q2, int ldq2, const void* K2, int ldk2,
                   const void* V, int ldv, float scale, const float* lambda, int num_heads, int seg_rows,
-                  const usm_rel_bias* bias, float* C, int ldc, usm_dtype dtype, void* stream) {
+                  const usm_rel_bias* bias, float* C, int ldc, usm_dtype dtype, void* workspace,
+                  size_t workspace_bytes, void* stream) {
     if (M < 0 || K < 0 || D < 0 || N < 0 || nnz < 0 || num_heads <= 0 || !dtype_ok(dtype))
         return USM_ERR_INVALID_ARG;
     if (bias) {
@@ -466,7 +481,10 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int* row_offsets, c
                ldq,  ldk, ldq2, ldk2, ldv, scale,       lambda,      num_heads, effective_seg(M, seg_rows),
                RelArgs{}, C,   ldc};
     if (bias) a.bias = rel_args(bias, M, seg_rows);
-    return launch_attention(a, dtype == USM_BF16, as_stream(stream));
+    const size_t need = attention_workspace_bytes(a, dtype == USM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return USM_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return USM_ERR_ALIGNMENT;
+    return launch_attention(a, dtype == USM_BF16, workspace, as_stream(stream));
 }
 
 size_t csr_transpose_workspace_bytes(int M, int K, int nnz) {

@@ -80,7 +80,8 @@ int launch_rel_bias_grad(int M, int nnz, const int* row_offsets, const int* col_
 int launch_diff_softmax(const MapArgs& a, cudaStream_t stream);
 int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stream);
 int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream);
-int launch_attention(const AttnArgs& a, bool bf16, cudaStream_t stream);
+size_t attention_workspace_bytes(const AttnArgs& a, bool bf16);
+int launch_attention(const AttnArgs& a, bool bf16, void* workspace, cudaStream_t stream);
 int launch_csr_validate(int M, int K, int nnz, const int* row_offsets, const int* col_indices, int* result,
                         cudaStream_t stream);
 
