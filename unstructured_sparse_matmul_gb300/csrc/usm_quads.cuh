@@ -66,15 +66,6 @@ __device__ __forceinline__ void store_quad(void* p, unsigned q, unsigned p0, uns
     }
 }
 
-// exp(x) for x <= 0 (or NaN) with results below 2^-126 flushed to 0: one
-// product and the hardware's exponential, without the scaling that keeps such
-// results as denormals.  Error as CUDA's __expf: 2 + 1.17·|x| steps.
-__device__ __forceinline__ float exp_flush(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-    return y;
-}
-
 // Whether an array can be read and written in quads.
 inline bool quad_aligned(const void* p, bool bf16) { return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 7u : 15u)) == 0; }
 

@@ -27,10 +27,14 @@ __device__ __forceinline__ int rel_bucket(const RelArgs& b, int entry) {
     return min(max(__ldg(b.map + entry), 0), b.buckets - 1);
 }
 
+template <bool BF>
 __device__ __forceinline__ float rel_table(const RelArgs& b, int head, int bucket) {
     const long long i = (long long)head * b.buckets + bucket;
-    if (b.table_bf16) return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(b.table) + i) << 16);
+    if constexpr (BF) return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(b.table) + i) << 16);
     return __ldg(static_cast<const float*>(b.table) + i);
+}
+__device__ __forceinline__ float rel_table(const RelArgs& b, int head, int bucket) {
+    return b.table_bf16 ? rel_table<true>(b, head, bucket) : rel_table<false>(b, head, bucket);
 }
 
 // Entries [s, e) of row r, clamped into [0, nnz) whatever row_offsets holds.

@@ -6,6 +6,7 @@
 #include "usm_internal.h"
 #include "usm_quads.cuh"
 #include "usm_rel.cuh"
+#include "usm_rows.cuh"
 
 namespace usm {
 namespace {
@@ -26,18 +27,8 @@ __global__ void rel_bucket_kernel(int num_buckets, int reach, int causal, int* _
 }
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr unsigned kLong = 2048;  // entries above which a CTA takes a row (or a piece of one)
-
-// Rows are cut into `pieces` equal runs of quads where there are few long ones.
-__device__ __forceinline__ void piece_range(unsigned p0, unsigned p1, int piece, int pieces, unsigned& b0, unsigned& b1) {
-    b0 = p0;
-    b1 = p1;
-    if (pieces > 1) {
-        const unsigned f = p0 & ~3u, quads = (p1 - f + 3) / 4;
-        b0 = max(p0, f + 4 * (unsigned)((unsigned long long)quads * piece / pieces));
-        b1 = min(p1, f + 4 * (unsigned)((unsigned long long)quads * (piece + 1) / pieces));
-    }
-}
+constexpr int kQuads = 4;         // quads a lane has in flight
+constexpr unsigned kLong = 2048;  // entries above which a CTA takes a row
 
 // Columns of quad q (those past the array's end read as 0).
 template <bool VEC>
@@ -54,55 +45,99 @@ __device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigne
     }
 }
 
-// Bound by memory: 8 bytes a nonzero in, 4 out.  A warp per row (or piece),
-// four entries a lane with 16-byte accesses, two quads in flight; long ones by
-// the CTA after its warps are done.  The map and the head's row of the table
-// are a few hundred bytes that stay in L1.
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) rel_bias_kernel(int M, int nnz, const int* __restrict__ ro,
-                                                            const int* __restrict__ ci, const float* s, const RelArgs b,
-                                                            int pieces, float* out) {
-    __shared__ int waits[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long items = (long long)M * pieces, first = (long long)blockIdx.x * kWarps;
-    // Entries of item i by the T threads t = 0..T-1.
-    auto item = [&](long long i, unsigned t, unsigned T, bool long_ones) {
-        const int r = (int)(i / pieces);
-        int p0, p1;
-        row_range(ro, r, nnz, p0, p1);
-        unsigned b0, b1;
-        piece_range(p0, p1, (int)(i - (long long)r * pieces), pieces, b0, b1);
-        if (b0 >= b1) return false;
-        if (!long_ones && b1 - b0 > kLong) return true;
-        const int block = r / b.seg_rows;
-        const int start = rel_start(b, block, r - block * b.seg_rows, __ldg(ci + p0));
-        const int head = block % b.heads;
-        auto quad = [&](unsigned q) {
-            int c[4];
-            float x[4];
-            load_columns<VEC>(ci, q, nnz, c);
-            load_quad<false, VEC>(s, q, nnz, x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] += rel_table(b, head, rel_bucket(b, rel_entry(c[u], start, b.reach)));
-            store_quad<false, VEC>(out, q, b0, b1, x);
-        };
-#pragma unroll 2
-        for (unsigned q = (b0 & ~3u) + 4 * t; q < b1; q += 4 * T) quad(q);
-        return false;
-    };
-    bool is_long = false;
-    if (first + warp < items) is_long = item(first + warp, lane, 32, false);
-    if (lane == 0) waits[warp] = is_long;
-    if (!__syncthreads_or(is_long)) return;
+// Adds the bias to entries [p0, p1) of one row (head and start: the row's), by
+// threads t = 0..T-1.
+template <bool VEC, bool BT>
+__device__ __forceinline__ void bias_entries(const int* __restrict__ ci, unsigned nnz, const float* s, const RelArgs& b,
+                                             float* out, int head, int start, unsigned p0, unsigned p1, unsigned t,
+                                             unsigned T) {
+    const unsigned step = 4 * T;
 #pragma unroll 1
-    for (int w = 0; w < kWarps; ++w)
-        if (waits[w]) item(first + w, threadIdx.x, kThreads, true);
+    for (unsigned q0 = (p0 & ~3u) + 4 * t; q0 < p1; q0 += kQuads * step) {
+        int c[kQuads][4];
+        float x[kQuads][4];
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+            const unsigned q = q0 + i * step;
+            if (q < p1) {
+                load_columns<VEC>(ci, q, nnz, c[i]);
+                load_quad<false, VEC>(s, q, nnz, x[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+            const unsigned q = q0 + i * step;
+            if (q < p1) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    x[i][u] += rel_table<BT>(b, head, rel_bucket(b, rel_entry(c[i][u], start, b.reach)));
+                store_quad<false, VEC>(out, q, p0, p1, x[i]);
+            }
+        }
+    }
 }
 
-// CTA (h, j) takes part j of J of head h's rows (or pieces).  Every thread sums
-// its entries into its own column of a histogram in shared memory ([bucket]
-// [thread]: no bank conflicts, no atomics), and the columns are added in a
-// fixed order.  A thread holds the sum of its latest bucket in a register and
+// Bound by memory: 8 bytes a nonzero in, 4 out.  Quads of entries with 16-byte
+// accesses, four in flight a lane; the map and the head's row of the table are a
+// few hundred bytes that stay in L1.  CTA b of B takes rows [M·b / B, M·(b+1) / B),
+// 64 at a time: long ones by the whole CTA, then each warp fetches row after row.
+template <bool VEC, bool BT>
+__global__ void __launch_bounds__(kThreads) rel_bias_kernel(int M, int nnz, const int* __restrict__ ro,
+                                                            const int* __restrict__ ci, const float* s, const RelArgs b,
+                                                            float* out) {
+    __shared__ RowRun run;
+    __shared__ int heads[kRun], starts[kRun];
+    const int lane = threadIdx.x & 31;
+    const long long r0 = (long long)M * blockIdx.x / gridDim.x, r1 = (long long)M * (blockIdx.x + 1) / gridDim.x;
+    for (long long r = r0; r < r1; r += kRun) {
+        const int n = (int)min((long long)kRun, r1 - r);
+        const bool any_long = run.load(ro, nnz, n, kLong, [&](int i) { return (int)r + i; },
+                                       [&](int i, int row) {
+                                           const int block = row / b.seg_rows;
+                                           heads[i] = block % b.heads;
+                                           if (run.begin[i] < run.end[i])
+                                               starts[i] = rel_start(b, block, row - block * b.seg_rows, __ldg(ci + run.begin[i]));
+                                       });
+        if (any_long) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i)
+                if ((unsigned)(run.end[i] - run.begin[i]) > kLong)
+                    bias_entries<VEC, BT>(ci, nnz, s, b, out, heads[i], starts[i], run.begin[i], run.end[i], threadIdx.x, kThreads);
+        }
+        for (int i = run.fetch(lane); i < n; i = run.fetch(lane))
+            if ((unsigned)(run.end[i] - run.begin[i]) <= kLong)
+                bias_entries<VEC, BT>(ci, nnz, s, b, out, heads[i], starts[i], run.begin[i], run.end[i], lane, 32);
+        __syncthreads();  // the next run's rows overwrite this one's
+    }
+}
+
+// Piece y of gridDim.y of row x's quads.
+__device__ __forceinline__ void piece_range(unsigned p0, unsigned p1, int piece, int pieces, unsigned& b0, unsigned& b1) {
+    const unsigned f = p0 & ~3u, quads = (p1 - f + 3) / 4;
+    b0 = max(p0, f + 4 * (unsigned)((unsigned long long)quads * piece / pieces));
+    b1 = min(p1, f + 4 * (unsigned)((unsigned long long)quads * (piece + 1) / pieces));
+}
+
+// Few long rows: CTA (x, y) takes piece y of row x.
+template <bool VEC, bool BT>
+__global__ void __launch_bounds__(kThreads) rel_bias_pieces_kernel(int nnz, const int* __restrict__ ro,
+                                                                   const int* __restrict__ ci, const float* s,
+                                                                   const RelArgs b, float* out) {
+    const int r = blockIdx.x, block = r / b.seg_rows;
+    int p0, p1;
+    row_range(ro, r, nnz, p0, p1);
+    if (p0 == p1) return;
+    unsigned b0, b1;
+    piece_range(p0, p1, blockIdx.y, gridDim.y, b0, b1);
+    const int start = rel_start(b, block, r - block * b.seg_rows, __ldg(ci + p0));
+    bias_entries<VEC, BT>(ci, nnz, s, b, out, block % b.heads, start, b0, b1, threadIdx.x, kThreads);
+}
+
+// CTA (h, j) takes part j of J of head h's rows (or of their pieces, where there
+// are few long rows).  Every thread sums its entries into its own column of a
+// histogram in shared memory ([bucket][thread]: no bank conflicts, no atomics),
+// and the columns are added in a fixed order: which thread takes which entry is
+// fixed too.  A thread holds the sum of its latest bucket in a register and
 // writes it back when the bucket changes: far keys share a bucket, so most of a
 // row is a few runs.  Bound by memory: 8 (or 6) bytes a nonzero.
 template <bool BF, bool VEC>
@@ -111,7 +146,8 @@ __global__ void __launch_bounds__(kThreads) rel_bias_grad_kernel(int M, int nnz,
                                                                  const RelArgs b, int blocks, int pieces, int J,
                                                                  float* __restrict__ part) {
     extern __shared__ float hist[];
-    __shared__ int waits[kWarps];
+    __shared__ RowRun run;
+    __shared__ int starts[kRun];
     const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = T >> 5;
     for (int k = 0; k < b.buckets; ++k) hist[k * T + t] = 0.f;
     const int head = blockIdx.x / J, j = blockIdx.x % J;
@@ -119,48 +155,66 @@ __global__ void __launch_bounds__(kThreads) rel_bias_grad_kernel(int M, int nnz,
     const long long items = rows * pieces, i0 = items * j / J, i1 = items * (j + 1) / J;
     int bucket = 0;
     float sum = 0.f;
-    auto item = [&](long long i, unsigned at, unsigned step, bool long_ones) {
-        const long long row = i / pieces;
-        const int in_block = (int)(row % b.seg_rows), block = head + (int)(row / b.seg_rows) * b.heads;
-        const long long r = (long long)block * b.seg_rows + in_block;
-        if (r >= M) return false;
-        int p0, p1;
-        row_range(ro, (int)r, nnz, p0, p1);
-        unsigned b0, b1;
-        piece_range(p0, p1, (int)(i - row * pieces), pieces, b0, b1);
-        if (b0 >= b1) return false;
-        if (!long_ones && b1 - b0 > kLong) return true;
-        const int start = rel_start(b, block, in_block, __ldg(ci + p0));
-#pragma unroll 2
-        for (unsigned q = (b0 & ~3u) + 4 * at; q < b1; q += 4 * step) {
-            int c[4];
-            float x[4];
-            load_columns<VEC>(ci, q, nnz, c);
-            load_quad<BF, VEC>(ds, q, nnz, x);
+    auto entries = [&](int start, unsigned p0, unsigned p1, unsigned at, unsigned threads) {
+        const unsigned step = 4 * threads;
+#pragma unroll 1
+        for (unsigned q0 = (p0 & ~3u) + 4 * at; q0 < p1; q0 += kQuads * step) {
+            int c[kQuads][4];
+            float x[kQuads][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int k = rel_bucket(b, rel_entry(c[u], start, b.reach));
-                const bool in = q + u >= b0 && q + u < b1;
-                if (in && k != bucket) {
-                    hist[bucket * T + t] += sum;
-                    bucket = k;
-                    sum = 0.f;
+            for (int i = 0; i < kQuads; ++i) {
+                const unsigned q = q0 + i * step;
+                if (q < p1) {
+                    load_columns<VEC>(ci, q, nnz, c[i]);
+                    load_quad<BF, VEC>(ds, q, nnz, x[i]);
                 }
-                if (in) sum += x[u];
+            }
+#pragma unroll
+            for (int i = 0; i < kQuads; ++i) {
+                const unsigned q = q0 + i * step;
+                if (q >= p1) break;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int k = rel_bucket(b, rel_entry(c[i][u], start, b.reach));
+                    if (q + u < p0 || q + u >= p1) continue;
+                    if (k != bucket) {
+                        hist[bucket * T + t] += sum;
+                        bucket = k;
+                        sum = 0.f;
+                    }
+                    sum += x[i][u];
+                }
             }
         }
-        return false;
     };
-    for (long long f = i0; f < i1; f += warps) {
-        bool is_long = false;
-        if (f + warp < i1) is_long = item(f + warp, lane, 32, false);
-        if (lane == 0) waits[warp] = is_long;
-        if (__syncthreads_or(is_long)) {
+    for (long long f = i0; f < i1; f += kRun) {
+        const int n = (int)min((long long)kRun, i1 - f);
+        const bool any_long = run.load(
+            ro, nnz, n, kLong,
+            [&](int i) {  // item -> row of the head's blocks (the last block may be shorter)
+                const long long row = (f + i) / pieces;
+                const long long r = (head + row / b.seg_rows * b.heads) * b.seg_rows + row % b.seg_rows;
+                return r < M ? (int)r : -1;
+            },
+            [&](int i, int r) {
+                const int block = r / b.seg_rows, p0 = run.begin[i], p1 = run.end[i];
+                if (p0 == p1) return;
+                starts[i] = rel_start(b, block, r - block * b.seg_rows, __ldg(ci + p0));
+                if (pieces > 1) {
+                    unsigned b0, b1;
+                    piece_range(p0, p1, (int)((f + i) % pieces), pieces, b0, b1);
+                    run.begin[i] = b0;
+                    run.end[i] = max(b0, b1);
+                }
+            });
+        if (any_long) {
 #pragma unroll 1
-            for (int w = 0; w < warps; ++w)
-                if (waits[w]) item(f + w, t, T, true);
-            __syncthreads();
+            for (int i = 0; i < n; ++i)
+                if ((unsigned)(run.end[i] - run.begin[i]) > kLong) entries(starts[i], run.begin[i], run.end[i], t, T);
         }
+        for (int i = warp; i < n; i += warps)
+            if ((unsigned)(run.end[i] - run.begin[i]) <= kLong) entries(starts[i], run.begin[i], run.end[i], lane, 32);
+        __syncthreads();  // the next run's rows overwrite this one's
     }
     hist[bucket * T + t] += sum;
     __syncthreads();
@@ -216,14 +270,28 @@ int launch_rel_bucket_build(int num_buckets, int max_distance, bool causal, int*
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
+namespace {
+template <bool VEC, bool BT>
+void launch_bias(int M, int nnz, const int* ro, const int* ci, const float* scores, const RelArgs& bias, float* out,
+                 cudaStream_t stream) {
+    const int pieces = row_pieces(M, nnz);
+    if (pieces > 1) {
+        rel_bias_pieces_kernel<VEC, BT><<<dim3(M, pieces), kThreads, 0, stream>>>(nnz, ro, ci, scores, bias, out);
+        return;
+    }
+    const int slots = sm_count_current_device() * 4;
+    rel_bias_kernel<VEC, BT><<<M < slots ? M : slots, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, out);
+}
+}  // namespace
+
 int launch_rel_bias(int M, int nnz, const int* ro, const int* ci, const float* scores, const RelArgs& bias, float* out,
                     cudaStream_t stream) {
-    const int pieces = row_pieces(M, nnz);
-    const unsigned grid = (unsigned)(((long long)M * pieces + kWarps - 1) / kWarps);
-    if (quad_aligned(ci, false) && quad_aligned(scores, false) && quad_aligned(out, false))
-        rel_bias_kernel<true><<<grid, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, pieces, out);
+    const bool vec = quad_aligned(ci, false) && quad_aligned(scores, false) && quad_aligned(out, false);
+    auto call = [&](auto launch) { launch(M, nnz, ro, ci, scores, bias, out, stream); };
+    if (bias.table_bf16)
+        vec ? call(launch_bias<true, true>) : call(launch_bias<false, true>);
     else
-        rel_bias_kernel<false><<<grid, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, pieces, out);
+        vec ? call(launch_bias<true, false>) : call(launch_bias<false, false>);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 

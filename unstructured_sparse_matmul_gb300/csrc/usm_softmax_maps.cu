@@ -10,11 +10,15 @@
 // its maximum and then its sums are reduced over the lanes, and the results are
 // written from the registers.  Entries past those are summed as they are read,
 // with a running maximum, and read a second time (from L2) for the output.
-// A warp takes a row; rows over kLong entries wait until the warps of the CTA
-// are done and are then taken by the whole CTA, so a long row among short ones
-// costs an eighth of its time.  Where rows are long throughout, or few, a CTA
-// or a cluster of up to 8 takes each row (launch_map), the CTAs joining their
-// maxima and sums through distributed shared memory.
+// A CTA takes a run of rows: the long ones first, with all its warps, then its
+// warps fetch the others one by one, so that neither a long row nor a long run
+// of luck keeps seven warps waiting.  (A warp and a row each, with a barrier at
+// the end for the long ones: half of all warp time at that barrier, 58 us at
+// 8x4096 rows of 410.)  Where long rows are too few to fill the GPU, a cluster
+// of up to 8 CTAs takes each (launch_rows), joined through distributed shared
+// memory.  Arithmetic is in pairs (f32x2) where it can be: with eight to twelve
+// bytes an entry, a kernel of more than about 16 instructions an entry and lane
+// would be bound by issue slots instead.
 #include <cmath>
 #include <type_traits>
 
@@ -22,6 +26,7 @@
 #include "usm_internal.h"
 #include "usm_quads.cuh"
 #include "usm_rel.cuh"
+#include "usm_rows.cuh"
 
 namespace usm {
 namespace {
@@ -41,13 +46,35 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// What exponents are measured from: the maximum, or 0 where it is -inf (every
-// entry masked), so that exp(-inf - 0) = 0 and the row's map is zero.
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 // 1/z, or 0 for a row without weight; NaN stays NaN.
 __device__ __forceinline__ float inverse(float z) { return z == 0.f ? 0.f : 1.f / z; }
 // w·d, or 0 under a weight of 0 (a masked entry) whatever d is there.
 __device__ __forceinline__ float weighted(float w, float d) { return w == 0.f ? 0.f : w * d; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// exp(s - m) as 2^(s·log2 e - shift), shift = m·log2 e: one fused product and the
+// hardware's exponential.  The rounding of the shift is the same factor in every
+// weight of the row and in their sum.  Scores so large that s·log2 e overflows
+// are first brought near zero (off = m, shift = 0); a maximum of -inf (every
+// entry masked) has shift 0, so that all weights are 0.
+struct Base {
+    float off, shift;
+    __device__ __forceinline__ explicit Base(float m) {
+        const bool huge = fabsf(m) > 1e37f && m != -INFINITY;
+        off = huge ? m : 0.f;
+        shift = huge || m == -INFINITY ? 0.f : m * kLog2e;
+    }
+    __device__ __forceinline__ bool huge() const { return off != 0.f; }
+};
+__device__ __forceinline__ float exp2_flush(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float weight_of(float s, const Base& b) {
+    return exp2_flush(fmaf(s - b.off, kLog2e, -b.shift));
+}
 
 // Sums of one map over (part of) a row: the maximum m, z = Σ exp(s - m) and
 // c = Σ exp(s - m)·d.
@@ -55,23 +82,25 @@ struct Stat {
     float m, z, c;
 };
 
-// Shared memory of a CTA that takes a row: one slot a warp, and the CTA's.
+// Shared memory of a CTA: one slot a warp, and what its cluster reads.
 struct BlockStats {
     float top[2][kWarps];
     float sum[2][2][kWarps];
-    float whole[2][3];
+    float whole_top[2];
+    float whole[2][2];
 };
 
 // One row [p0, p1).  BLOCK: by the CTA (or its cluster's), else by the warp.
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC, bool BLOCK>
-__device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, unsigned p1, BlockStats& sh, int ctas,
-                                        int rank) {
+__device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsigned p0, unsigned p1, BlockStats& sh,
+                                        int ctas, int rank) {
     constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned nnz = a.nnz;
     // Thread t of T takes quads t, t + T, ... of the row.
     const unsigned T = BLOCK ? kThreads * ctas : 32, t = BLOCK ? rank * kThreads + threadIdx.x : lane;
     const unsigned q0 = (p0 & ~3u) + 4 * t, step = 4 * T;
+    const unsigned qw = (p0 & ~3u) + (BLOCK ? 4 * (t & ~31u) : 0);  // the warp's first quad
     const float* s[2] = {a.s1, a.s2};
 
     // Scores of quad q; entries of neighbouring rows become -inf.  Only the
@@ -117,27 +146,28 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             const float top = fmaxf(fmaxf(fmaxf(y[k][0], y[k][1]), fmaxf(y[k][2], y[k][3])), run[k].m);
-            const float base = base_of(top), f = exp_flush(run[k].m - base);
+            const float f = top == -INFINITY ? 0.f : __expf(run[k].m - top);
             run[k].z *= f;
             run[k].c *= f;
             run[k].m = top;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float e = exp_flush(y[k][u] - base);
+                const float e = __expf(y[k][u] - (top == -INFINITY ? 0.f : top));
                 run[k].z += e;
                 if constexpr (GRAD) run[k].c += weighted(e, dy[u]);
             }
         }
     }
 
-    // Maximum over the warp or CTA.
+    // Maximum over the warp, the CTA, the cluster.
     float m[MAPS];
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
         float top = run[k].m;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
-            top = fmaxf(top, fmaxf(fmaxf(x[i][k][0], x[i][k][1]), fmaxf(x[i][k][2], x[i][k][3])));
+            if (qw + i * step < p1)
+                top = fmaxf(top, fmaxf(fmaxf(x[i][k][0], x[i][k][1]), fmaxf(x[i][k][2], x[i][k][3])));
         m[k] = warp_max(top);
         if (BLOCK && lane == 0) sh.top[k][warp] = m[k];
     }
@@ -147,33 +177,58 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
         for (int k = 0; k < MAPS; ++k)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
+        if (ctas > 1) {
+            if (threadIdx.x < MAPS) sh.whole_top[threadIdx.x] = threadIdx.x ? m[MAPS - 1] : m[0];
+            cluster_sync();
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k)
+                for (int i = 0; i < ctas; ++i) m[k] = fmaxf(m[k], load_cluster(smem_addr(&sh.whole_top[k]), i));
+        }
     }
     // Weights (in the scores' registers) and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
     auto dot = [&](int k, bool guarded) {
-        float sum = 0.f;
+        float2 sum = make_float2(0.f, 0.f);
         if constexpr (GRAD) {
 #pragma unroll
             for (int i = 0; i < kQuads; ++i)
+                if (qw + i * step < p1) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    sum = guarded && x[i][k][u] == 0.f ? sum : fmaf(x[i][k][u], d[i][u], sum);
+                    for (int u = 0; u < 4; u += 2) {
+                        float2 w = make_float2(x[i][k][u], x[i][k][u + 1]), v = make_float2(d[i][u], d[i][u + 1]);
+                        if (guarded) {
+                            if (w.x == 0.f) v.x = 0.f;
+                            if (w.y == 0.f) v.y = 0.f;
+                        }
+                        sum = __ffma2_rn(w, v, sum);
+                    }
+                }
         }
-        return sum;
+        return sum.x + sum.y;
     };
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        const float base = base_of(m[k]), f = exp_flush(run[k].m - base);
+        const Base base(m[k]);
+        const float f = weight_of(run[k].m, base);
         z[k] = run[k].z * f;
         run[k].c *= f;
+        const float2 scale = make_float2(kLog2e, kLog2e), shift = make_float2(-base.shift, -base.shift);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)
+            if (qw + i * step < p1) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x[i][k][u] = exp_flush(x[i][k][u] - base);
-                z[k] += x[i][k][u];
+                for (int u = 0; u < 4; u += 2) {
+                    float2 y = make_float2(x[i][k][u], x[i][k][u + 1]);
+                    if (base.huge()) y = make_float2(y.x - base.off, y.y - base.off);
+                    y = __ffma2_rn(y, scale, shift);
+                    y = make_float2(exp2_flush(y.x), exp2_flush(y.y));
+                    x[i][k][u] = y.x;
+                    x[i][k][u + 1] = y.y;
+                    sum = __fadd2_rn(sum, y);
+                }
             }
-        z[k] = warp_sum(z[k]);
+        z[k] = warp_sum(z[k] + (sum.x + sum.y));
         c[k] = 0.f;
         if constexpr (GRAD) c[k] = warp_sum(run[k].c + dot(k, BLOCK));
         if (BLOCK && lane == 0) {
@@ -203,43 +258,33 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
                 if constexpr (GRAD) c[k] += sh.sum[k][1][w];
             }
         }
-    }
-    float own[MAPS];  // what this CTA's weights are multiplied by to be the row's
+        if (ctas > 1) {
+            if (threadIdx.x == 0) {
 #pragma unroll
-    for (int k = 0; k < MAPS; ++k) own[k] = 1.f;
-    if (BLOCK && ctas > 1) {
-        if (threadIdx.x == 0) {
+                for (int k = 0; k < MAPS; ++k) {
+                    sh.whole[k][0] = z[k];
+                    sh.whole[k][1] = c[k];
+                }
+            }
+            cluster_sync();
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
-                sh.whole[k][0] = m[k];
-                sh.whole[k][1] = z[k];
-                sh.whole[k][2] = c[k];
+                z[k] = c[k] = 0.f;
+                for (int i = 0; i < ctas; ++i) {
+                    z[k] += load_cluster(smem_addr(&sh.whole[k][0]), i);
+                    if constexpr (GRAD) c[k] += load_cluster(smem_addr(&sh.whole[k][1]), i);
+                }
             }
+            cluster_sync();  // no CTA leaves what another may still read
         }
-        cluster_sync();
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            float top = -INFINITY;
-            for (int i = 0; i < ctas; ++i) top = fmaxf(top, load_cluster(smem_addr(&sh.whole[k][0]), i));
-            const float base = base_of(top);
-            z[k] = c[k] = 0.f;
-            for (int i = 0; i < ctas; ++i) {
-                const float f = exp_flush(load_cluster(smem_addr(&sh.whole[k][0]), i) - base);
-                z[k] += f * load_cluster(smem_addr(&sh.whole[k][1]), i);
-                if constexpr (GRAD) c[k] += weighted(f, load_cluster(smem_addr(&sh.whole[k][2]), i));
-            }
-            own[k] = exp_flush(m[k] - base);
-        }
-        cluster_sync();  // no CTA goes on to overwrite, or leave, what another reads
     }
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
         inv[k] = inverse(z[k]);
         if constexpr (GRAD) c[k] *= inv[k];
-        inv[k] *= own[k];
     }
     if (GRAD && TWO && a.row_c2 && (BLOCK ? rank == 0 && threadIdx.x == 0 : lane == 0)) a.row_c2[r] = c[MAPS - 1];
-    if constexpr (TWO) inv[1] *= -__ldg(a.lambda + r / a.seg_rows % a.heads);
+    if constexpr (TWO) inv[1] *= -lam;
 
     // The results of one quad from its weights (and dout).  Gradients are
     // w·(inv·d - inv·c).
@@ -250,15 +295,26 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
             for (int k = 0; k < MAPS; ++k) {
                 const float ic = -inv[k] * c[k];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float g = fmaf(inv[k], dy[u], ic);
-                    y[u] = guarded ? weighted(w[k][u], g) : w[k][u] * g;
+                for (int u = 0; u < 4; u += 2) {
+                    const float2 g = __ffma2_rn(make_float2(inv[k], inv[k]), make_float2(dy[u], dy[u + 1]), make_float2(ic, ic));
+                    const float2 v = __fmul2_rn(make_float2(w[k][u], w[k][u + 1]), g);
+                    y[u] = v.x;
+                    y[u + 1] = v.y;
+                    if (guarded) {
+                        if (w[k][u] == 0.f) y[u] = 0.f;
+                        if (w[k][u + 1] == 0.f) y[u + 1] = 0.f;
+                    }
                 }
                 store_quad<OUT, VEC>(k == 0 ? a.out1 : a.out2, q, p0, p1, y);
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = fmaf(w[0][u], inv[0], w[MAPS - 1][u] * inv[MAPS - 1]);
+            for (int u = 0; u < 4; u += 2) {
+                float2 v = __fmul2_rn(make_float2(w[MAPS - 1][u], w[MAPS - 1][u + 1]), make_float2(inv[MAPS - 1], inv[MAPS - 1]));
+                v = __ffma2_rn(make_float2(w[0][u], w[0][u + 1]), make_float2(inv[0], inv[0]), v);
+                y[u] = v.x;
+                y[u + 1] = v.y;
+            }
             store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
         }
     };
@@ -274,45 +330,51 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, unsigned p0, un
         if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-            const float base = base_of(m[k]);
+            const Base base(m[k]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[k][u] = exp_flush(y[k][u] - base);
+            for (int u = 0; u < 4; ++u) y[k][u] = weight_of(y[k][u], base);
         }
         finish(q, y, dy);
     }
 }
 
-// A warp per row; long rows by the CTA.
+// Rows [M·b / B, M·(b+1) / B) of CTA b of B, 64 at a time: rows over `long_at`
+// entries by the whole CTA, then each warp fetches row after row.
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads, TWO && GRAD ? 3 : 4) warp_rows_kernel(const MapArgs a) {
+__global__ void __launch_bounds__(kThreads, TWO && GRAD ? 3 : 4) row_runs_kernel(const MapArgs a, unsigned long_at) {
     __shared__ BlockStats sh;
-    __shared__ int waits[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long first = (long long)blockIdx.x * kWarps;
-    int p0 = 0, p1 = 0;
-    const int r = (int)min(first + warp, (long long)a.M - 1);
-    const bool live = first + warp < a.M;
-    if (live) row_range(a.row_offsets, r, a.nnz, p0, p1);
-    const bool is_long = (unsigned)(p1 - p0) > kLong;
-    if (lane == 0) waits[warp] = is_long;
-    if (live && !is_long) {
-        if (p0 < p1)
-            map_row<TWO, GRAD, DIN, OUT, VEC, false>(a, r, p0, p1, sh, 1, 0);
-        else if (GRAD && TWO && a.row_c2 && lane == 0)
-            a.row_c2[r] = 0.f;
-    }
-    if (!__syncthreads_or(is_long)) return;
+    __shared__ RowRun run;
+    __shared__ float lams[kRun];
+    const int lane = threadIdx.x & 31;
+    const long long r0 = (long long)a.M * blockIdx.x / gridDim.x, r1 = (long long)a.M * (blockIdx.x + 1) / gridDim.x;
+    for (long long r = r0; r < r1; r += kRun) {
+        const int n = (int)min((long long)kRun, r1 - r);
+        const bool any_long =
+            run.load(a.row_offsets, a.nnz, n, long_at, [&](int i) { return (int)r + i; },
+                     [&](int i, int row) {
+                         if (TWO) lams[i] = __ldg(a.lambda + row / a.seg_rows % a.heads);
+                     });
+        if (any_long) {
 #pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-        if (!waits[w]) continue;
-        row_range(a.row_offsets, (int)first + w, a.nnz, p0, p1);
-        map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, (int)first + w, p0, p1, sh, 1, 0);
+            for (int i = 0; i < n; ++i)
+                if ((unsigned)(run.end[i] - run.begin[i]) > long_at)
+                    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, (int)r + i, TWO ? lams[i] : 0.f, run.begin[i], run.end[i], sh, 1, 0);
+        }
+        for (int i = run.fetch(lane); i < n; i = run.fetch(lane)) {
+            const unsigned p0 = run.begin[i], p1 = run.end[i];
+            if (p0 == p1) {
+                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r + i] = 0.f;
+            } else if (p1 - p0 <= long_at) {
+                map_row<TWO, GRAD, DIN, OUT, VEC, false>(a, (int)r + i, TWO ? lams[i] : 0.f, p0, p1, sh, 1, 0);
+            }
+        }
+        __syncthreads();  // the next run's rows overwrite this one's
     }
 }
 
-// A CTA, or a cluster, per row.
+// A cluster per row.
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads) block_rows_kernel(const MapArgs a) {
+__global__ void __launch_bounds__(kThreads) cluster_rows_kernel(const MapArgs a) {
     __shared__ BlockStats sh;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
@@ -322,7 +384,8 @@ __global__ void __launch_bounds__(kThreads) block_rows_kernel(const MapArgs a) {
         if (GRAD && TWO && a.row_c2 && rank == 0 && threadIdx.x == 0) a.row_c2[r] = 0.f;
         return;
     }
-    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, r, p0, p1, sh, ctas, rank);
+    const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
+    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, r, lam, p0, p1, sh, ctas, rank);
 }
 
 // dλ[h] = -Σ c2 over head h's rows: a CTA per head, a fixed order.
@@ -350,11 +413,11 @@ template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
 int launch_rows(const MapArgs& a, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     const int mean = a.nnz / a.M;
-    // A CTA a row where most rows are long, or where rows are too few to fill
-    // the SMs with a warp each; a cluster where they are too few for CTAs.
-    if (mean > (int)kLong || (mean > 128 * kQuads && a.M < kWarps * sms)) {
-        int ctas = 1;
-        while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kThreads * 4 * kQuads / 2) ctas *= 2;
+    // Clusters where rows are long (their CTAs hold over half a CTA's registers'
+    // worth each) and too few to give every SM one.
+    int ctas = 1;
+    while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kThreads * 4 * kQuads / 2) ctas *= 2;
+    if (ctas > 1) {
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = ctas;
@@ -365,10 +428,15 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, block_rows_kernel<TWO, GRAD, DIN, OUT, VEC>, a) == cudaSuccess ? USM_OK
-                                                                                                      : USM_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT, VEC>, a) == cudaSuccess ? USM_OK
+                                                                                                        : USM_ERR_CUDA;
     }
-    warp_rows_kernel<TWO, GRAD, DIN, OUT, VEC><<<(unsigned)(((long long)a.M + kWarps - 1) / kWarps), kThreads, 0, stream>>>(a);
+    // A CTA each while there are fewer rows than CTA slots (a CTA then takes rows
+    // that a warp would have to walk twice), else one wave of CTAs.
+    const int slots = sms * (TWO && GRAD ? 3 : 4);
+    const bool few = a.M <= slots;
+    row_runs_kernel<TWO, GRAD, DIN, OUT, VEC>
+        <<<few ? a.M : slots, kThreads, 0, stream>>>(a, few ? 32 * 4 * kQuads : kLong);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
