@@ -5,35 +5,27 @@
 // Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
 // stored entries.
 //
-// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  A row is
-// read once into registers (four quads a lane: 512 entries a warp, 4096 a CTA),
-// its maximum and then its sums are reduced over the lanes, and the results are
-// written from the registers.  Entries past those are summed as they are read,
-// with a running maximum, and read a second time (from L2) for the output.
-// A CTA takes a run of rows: the long ones first, with all its warps, then its
-// warps fetch the others one by one, so that neither a long row nor a long run
-// of luck keeps seven warps waiting.  (A warp and a row each, with a barrier at
-// the end for the long ones: half of all warp time at that barrier, 58 us at
-// 8x4096 rows of 410.)  Where long rows are too few to fill the GPU, a cluster
-// of up to 8 CTAs takes each (launch_rows), joined through distributed shared
-// memory.  Arithmetic is in pairs (f32x2) where it can be: with eight to twelve
-// bytes an entry, a kernel of more than about 16 instructions an entry and lane
-// would be bound by issue slots instead.
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
+// takes the rows that begin in an equal share of the entries and streams them
+// through a ring of its own in shared memory (usm_stream.cuh), so copies are in
+// flight all the time whatever the rows' arithmetic and lengths do; a row is
+// walked three times there (maximum; weights, their sums, written back in place;
+// results), four entries a lane, in pairs of fp32 (f32x2).  Rows over 1536
+// entries are first taken by the whole CTA; where rows are long and few, a
+// cluster of up to 8 CTAs takes each (launch_rows).  (Rows read into registers by
+// a warp each measured 49 to 58 us for the differential map of 8x4096 rows of 410
+// entries: each row waited for its own loads, and lanes past its ends did the
+// arithmetic of 512.)
 #include <cmath>
-#include <type_traits>
 
 #include "usm_cluster.cuh"
 #include "usm_internal.h"
-#include "usm_quads.cuh"
-#include "usm_rel.cuh"
-#include "usm_rows.cuh"
+#include "usm_stream.cuh"
 
 namespace usm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kQuads = 4;             // quads a lane keeps in registers
-constexpr unsigned kLong = 2048;      // entries above which a CTA takes the row
+constexpr int kSteps = 16;  // entries of a long row a thread keeps in registers
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -82,79 +74,70 @@ struct Stat {
     float m, z, c;
 };
 
-// Shared memory of a CTA: one slot a warp, and what its cluster reads.
+// Shared memory of a CTA that takes a row: one slot a warp, and what its cluster
+// reads.
+template <int WARPS>
 struct BlockStats {
-    float top[2][kWarps];
-    float sum[2][2][kWarps];
+    float top[2][WARPS];
+    float sum[2][2][WARPS];
     float whole_top[2];
     float whole[2][2];
 };
 
-// One row [p0, p1).  BLOCK: by the CTA (or its cluster's), else by the warp.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC, bool BLOCK>
-__device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsigned p0, unsigned p1, BlockStats& sh,
-                                        int ctas, int rank) {
+// A long row [p0, p1) by the CTA's WARPS warps, or its cluster's: 16 entries a
+// thread in registers, the rest read twice.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, int WARPS>
+__device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, int p0, int p1, BlockStats<WARPS>& sh, int ctas,
+                                        int rank) {
     constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned nnz = a.nnz;
-    // Thread t of T takes quads t, t + T, ... of the row.
-    const unsigned T = BLOCK ? kThreads * ctas : 32, t = BLOCK ? rank * kThreads + threadIdx.x : lane;
-    const unsigned q0 = (p0 & ~3u) + 4 * t, step = 4 * T;
-    const unsigned qw = (p0 & ~3u) + (BLOCK ? 4 * (t & ~31u) : 0);  // the warp's first quad
-    const float* s[2] = {a.s1, a.s2};
+    // Thread t of T takes entries t, t + T, ... of the row.
+    const int T = WARPS * 32 * ctas, t = rank * WARPS * 32 + threadIdx.x;
+    const int n = p1 - p0, nw = n - (t - lane);  // entries of the row, and from the warp's first one on
+    const float* s[2] = {a.s1 + p0, TWO ? a.s2 + p0 : nullptr};
+    const void* dout = GRAD ? static_cast<const char*>(a.dout) + (long long)p0 * (DIN ? 2 : 4) : nullptr;
+    void* out[2] = {static_cast<char*>(a.out1) + (long long)p0 * (OUT ? 2 : 4),
+                    GRAD && TWO ? static_cast<char*>(a.out2) + (long long)p0 * (OUT ? 2 : 4) : nullptr};
 
-    // Scores of quad q; entries of neighbouring rows become -inf.  Only the
-    // row's first quad (thread 0's) can hold entries before it.
-    auto load_scores = [&](unsigned q, bool first, float (&x)[MAPS][4]) {
+    // Steps come in pairs; a pair without an entry in the warp is skipped.
+    float2 x[MAPS][kSteps / 2], d[GRAD ? kSteps / 2 : 1];
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) load_quad<false, VEC>(s[k], q, nnz, x[k]);
-        const int left = (int)(p1 - q);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool out = u >= left || (first && q + u < p0);
+    for (int i = 0; i < kSteps / 2; ++i) {
+        const int e = t + 2 * i * T;
+        if (2 * i * T < nw) {
 #pragma unroll
             for (int k = 0; k < MAPS; ++k)
-                if (out) x[k][u] = -INFINITY;
-        }
-    };
-
-    float x[kQuads][MAPS][4], d[GRAD ? kQuads : 1][4];
-#pragma unroll
-    for (int i = 0; i < kQuads; ++i) {
-        const unsigned q = q0 + i * step;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) x[i][k][u] = -INFINITY;
-            if constexpr (GRAD) d[i][u] = 0.f;
-        }
-        if (q < p1) {
-            load_scores(q, i == 0, x[i]);
-            if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, d[i]);
+                x[k][i] = make_float2(e < n ? s[k][e] : -INFINITY, e + T < n ? s[k][e + T] : -INFINITY);
+            if constexpr (GRAD)
+                d[i] = make_float2(e < n ? load_global<DIN>(dout, e) : 0.f, e + T < n ? load_global<DIN>(dout, e + T) : 0.f);
         }
     }
-    // Quads past the registers: a running maximum and sums.
-    const unsigned tail = q0 + kQuads * step;
+    // Entries past the registers, four at a time: a running maximum and sums.
+    const int tail = t + kSteps * T;
     Stat run[MAPS];
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
 #pragma unroll 1
-    for (unsigned q = tail; q < p1; q += step) {
-        float y[MAPS][4], dy[4];
-        load_scores(q, false, y);
-        if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
+    for (int e = tail; e < n; e += 4 * T) {
+        float dy[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if constexpr (GRAD) dy[u] = e + u * T < n ? load_global<DIN>(dout, e + u * T) : 0.f;
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-            const float top = fmaxf(fmaxf(fmaxf(y[k][0], y[k][1]), fmaxf(y[k][2], y[k][3])), run[k].m);
-            const float f = top == -INFINITY ? 0.f : __expf(run[k].m - top);
+            float y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = e + u * T < n ? s[k][e + u * T] : -INFINITY;
+            const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), run[k].m);
+            const float base = top == -INFINITY ? 0.f : top, f = __expf(run[k].m - base);
             run[k].z *= f;
             run[k].c *= f;
             run[k].m = top;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float e = __expf(y[k][u] - (top == -INFINITY ? 0.f : top));
-                run[k].z += e;
-                if constexpr (GRAD) run[k].c += weighted(e, dy[u]);
+                const float w = __expf(y[u] - base);
+                run[k].z += w;
+                if constexpr (GRAD) run[k].c += weighted(w, dy[u]);
             }
         }
     }
@@ -165,18 +148,17 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsi
     for (int k = 0; k < MAPS; ++k) {
         float top = run[k].m;
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i)
-            if (qw + i * step < p1)
-                top = fmaxf(top, fmaxf(fmaxf(x[i][k][0], x[i][k][1]), fmaxf(x[i][k][2], x[i][k][3])));
+        for (int i = 0; i < kSteps / 2; ++i)
+            if (2 * i * T < nw) top = fmaxf(top, fmaxf(x[k][i].x, x[k][i].y));
         m[k] = warp_max(top);
-        if (BLOCK && lane == 0) sh.top[k][warp] = m[k];
+        if (lane == 0) sh.top[k][warp] = m[k];
     }
-    if constexpr (BLOCK) {
+    {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < MAPS; ++k)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
+            for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
         if (ctas > 1) {
             if (threadIdx.x < MAPS) sh.whole_top[threadIdx.x] = threadIdx.x ? m[MAPS - 1] : m[0];
             cluster_sync();
@@ -187,21 +169,16 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsi
     }
     // Weights (in the scores' registers) and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
-    auto dot = [&](int k, bool guarded) {
+    auto dot = [&](int k) {
         float2 sum = make_float2(0.f, 0.f);
         if constexpr (GRAD) {
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i)
-                if (qw + i * step < p1) {
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        float2 w = make_float2(x[i][k][u], x[i][k][u + 1]), v = make_float2(d[i][u], d[i][u + 1]);
-                        if (guarded) {
-                            if (w.x == 0.f) v.x = 0.f;
-                            if (w.y == 0.f) v.y = 0.f;
-                        }
-                        sum = __ffma2_rn(w, v, sum);
-                    }
+            for (int i = 0; i < kSteps / 2; ++i)
+                if (2 * i * T < nw) {
+                    float2 v = d[i];
+                    if (x[k][i].x == 0.f) v.x = 0.f;
+                    if (x[k][i].y == 0.f) v.y = 0.f;
+                    sum = __ffma2_rn(x[k][i], v, sum);
                 }
         }
         return sum.x + sum.y;
@@ -209,51 +186,38 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsi
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
         const Base base(m[k]);
+        if (base.huge()) {
+#pragma unroll
+            for (int i = 0; i < kSteps / 2; ++i)
+                if (2 * i * T < nw) x[k][i] = make_float2(x[k][i].x - base.off, x[k][i].y - base.off);
+        }
         const float f = weight_of(run[k].m, base);
         z[k] = run[k].z * f;
         run[k].c *= f;
         const float2 scale = make_float2(kLog2e, kLog2e), shift = make_float2(-base.shift, -base.shift);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i)
-            if (qw + i * step < p1) {
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {
-                    float2 y = make_float2(x[i][k][u], x[i][k][u + 1]);
-                    if (base.huge()) y = make_float2(y.x - base.off, y.y - base.off);
-                    y = __ffma2_rn(y, scale, shift);
-                    y = make_float2(exp2_flush(y.x), exp2_flush(y.y));
-                    x[i][k][u] = y.x;
-                    x[i][k][u + 1] = y.y;
-                    sum = __fadd2_rn(sum, y);
-                }
+        for (int i = 0; i < kSteps / 2; ++i)
+            if (2 * i * T < nw) {
+                const float2 y = __ffma2_rn(x[k][i], scale, shift);
+                x[k][i] = make_float2(exp2_flush(y.x), exp2_flush(y.y));
+                sum = __fadd2_rn(sum, x[k][i]);
             }
         z[k] = warp_sum(z[k] + (sum.x + sum.y));
         c[k] = 0.f;
-        if constexpr (GRAD) c[k] = warp_sum(run[k].c + dot(k, BLOCK));
-        if (BLOCK && lane == 0) {
+        if constexpr (GRAD) c[k] = warp_sum(run[k].c + dot(k));
+        if (lane == 0) {
             sh.sum[k][0][warp] = z[k];
             sh.sum[k][1][warp] = c[k];
         }
     }
-    // A dout that is not finite makes c so too, even under weights of 0: such a
-    // row (and every row of a CTA) guards each product.
-    bool guarded = BLOCK;
-    if constexpr (GRAD && !BLOCK) {
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k) guarded = guarded || !(fabsf(c[k]) < INFINITY);
-        if (guarded) {
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) c[k] = warp_sum(run[k].c + dot(k, true));
-        }
-    }
-    if constexpr (BLOCK) {
+    {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             z[k] = c[k] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 z[k] += sh.sum[k][0][w];
                 if constexpr (GRAD) c[k] += sh.sum[k][1][w];
             }
@@ -283,99 +247,287 @@ __device__ __forceinline__ void map_row(const MapArgs& a, int r, float lam, unsi
         inv[k] = inverse(z[k]);
         if constexpr (GRAD) c[k] *= inv[k];
     }
-    if (GRAD && TWO && a.row_c2 && (BLOCK ? rank == 0 && threadIdx.x == 0 : lane == 0)) a.row_c2[r] = c[MAPS - 1];
+    if (GRAD && TWO && a.row_c2 && rank == 0 && threadIdx.x == 0) a.row_c2[r] = c[MAPS - 1];
     if constexpr (TWO) inv[1] *= -lam;
 
-    // The results of one quad from its weights (and dout).  Gradients are
+    // The results of two entries from their weights (and dout).  Gradients are
     // w·(inv·d - inv·c).
-    auto finish = [&](unsigned q, const float (&w)[MAPS][4], const float (&dy)[4]) {
-        float y[4];
+    auto finish = [&](int e, const float2 (&w)[MAPS], float2 dy) {
         if constexpr (GRAD) {
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
                 const float ic = -inv[k] * c[k];
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {
-                    const float2 g = __ffma2_rn(make_float2(inv[k], inv[k]), make_float2(dy[u], dy[u + 1]), make_float2(ic, ic));
-                    const float2 v = __fmul2_rn(make_float2(w[k][u], w[k][u + 1]), g);
-                    y[u] = v.x;
-                    y[u + 1] = v.y;
-                    if (guarded) {
-                        if (w[k][u] == 0.f) y[u] = 0.f;
-                        if (w[k][u + 1] == 0.f) y[u + 1] = 0.f;
-                    }
-                }
-                store_quad<OUT, VEC>(k == 0 ? a.out1 : a.out2, q, p0, p1, y);
+                float2 y = __fmul2_rn(w[k], __ffma2_rn(make_float2(inv[k], inv[k]), dy, make_float2(ic, ic)));
+                if (w[k].x == 0.f) y.x = 0.f;
+                if (w[k].y == 0.f) y.y = 0.f;
+                if (e < n) store_entry<OUT>(out[k], e, y.x);
+                if (e + T < n) store_entry<OUT>(out[k], e + T, y.y);
             }
         } else {
-#pragma unroll
-            for (int u = 0; u < 4; u += 2) {
-                float2 v = __fmul2_rn(make_float2(w[MAPS - 1][u], w[MAPS - 1][u + 1]), make_float2(inv[MAPS - 1], inv[MAPS - 1]));
-                v = __ffma2_rn(make_float2(w[0][u], w[0][u + 1]), make_float2(inv[0], inv[0]), v);
-                y[u] = v.x;
-                y[u + 1] = v.y;
-            }
-            store_quad<OUT, VEC>(a.out1, q, p0, p1, y);
+            float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
+            y = __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y);
+            if (e < n) store_entry<OUT>(out[0], e, y.x);
+            if (e + T < n) store_entry<OUT>(out[0], e + T, y.y);
         }
     };
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) {
-        const unsigned q = q0 + i * step;
-        if (q < p1) finish(q, x[i], d[GRAD ? i : 0]);
-    }
-#pragma unroll 1
-    for (unsigned q = tail; q < p1; q += step) {
-        float y[MAPS][4], dy[4];
-        load_scores(q, false, y);
-        if constexpr (GRAD) load_quad<DIN, VEC>(a.dout, q, nnz, dy);
+    for (int i = 0; i < kSteps / 2; ++i)
+        if (2 * i * T < nw) {
+            float2 w[MAPS];
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) w[k] = x[k][i];
+            finish(t + 2 * i * T, w, d[GRAD ? i : 0]);
+        }
+#pragma unroll 2
+    for (int e = tail; e < n; e += 2 * T) {
+        float2 w[MAPS], dy = make_float2(0.f, 0.f);
+        if constexpr (GRAD) {
+            dy.x = load_global<DIN>(dout, e);
+            if (e + T < n) dy.y = load_global<DIN>(dout, e + T);
+        }
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             const Base base(m[k]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[k][u] = weight_of(y[k][u], base);
+            w[k] = make_float2(weight_of(s[k][e], base), weight_of(e + T < n ? s[k][e + T] : -INFINITY, base));
         }
-        finish(q, y, dy);
+        finish(e, w, dy);
     }
 }
 
-// Rows [M·b / B, M·(b+1) / B) of CTA b of B, 64 at a time: rows over `long_at`
-// entries by the whole CTA, then each warp fetches row after row.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads, TWO && GRAD ? 3 : 4) row_runs_kernel(const MapArgs a, unsigned long_at) {
-    __shared__ BlockStats sh;
-    __shared__ RowRun run;
-    __shared__ float lams[kRun];
+
+// Out of line in the kernel below: long rows are rare there.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, int WARPS>
+__device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0, int p1, BlockStats<WARPS>& sh) {
+    block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, 1, 0);
+}
+
+// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
+__device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
+    constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31;
-    const long long r0 = (long long)a.M * blockIdx.x / gridDim.x, r1 = (long long)a.M * (blockIdx.x + 1) / gridDim.x;
-    for (long long r = r0; r < r1; r += kRun) {
-        const int n = (int)min((long long)kRun, r1 - r);
-        const bool any_long =
-            run.load(a.row_offsets, a.nnz, n, long_at, [&](int i) { return (int)r + i; },
-                     [&](int i, int row) {
-                         if (TWO) lams[i] = __ldg(a.lambda + row / a.seg_rows % a.heads);
-                     });
-        if (any_long) {
-#pragma unroll 1
-            for (int i = 0; i < n; ++i)
-                if ((unsigned)(run.end[i] - run.begin[i]) > long_at)
-                    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, (int)r + i, TWO ? lams[i] : 0.f, run.begin[i], run.end[i], sh, 1, 0);
+    const RowQuads rq(p0, p1, lane);
+    const unsigned first = rq.qs + 4 * lane;
+
+    // Maximum.
+    float m[MAPS], xe[MAPS];
+    const float de = GRAD && rq.has_edge ? lds_entry<DIN>(st.at(MAPS, rq.edge)) : 0.f;
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) m[k] = xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
+#pragma unroll 2
+    for (unsigned q = first; q < rq.qe; q += 128) {
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            float2 lo, hi;
+            lds_quad<false>(st.at(k, q), lo, hi);
+            m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
         }
-        for (int i = run.fetch(lane); i < n; i = run.fetch(lane)) {
-            const unsigned p0 = run.begin[i], p1 = run.end[i];
-            if (p0 == p1) {
-                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r + i] = 0.f;
-            } else if (p1 - p0 <= long_at) {
-                map_row<TWO, GRAD, DIN, OUT, VEC, false>(a, (int)r + i, TWO ? lams[i] : 0.f, p0, p1, sh, 1, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) m[k] = warp_max(m[k]);
+
+    // Weights, in place, and their sums.
+    float z[MAPS], c[MAPS], inv[MAPS];
+    float2 zs[MAPS], cs[MAPS], shift[MAPS];
+    float off[MAPS];
+    bool huge = false;
+    const float2 scale = make_float2(kLog2e, kLog2e);
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        const Base base(m[k]);
+        huge = huge || base.huge();
+        off[k] = base.off;
+        shift[k] = make_float2(-base.shift, -base.shift);
+        xe[k] = weight_of(xe[k], base);
+        zs[k] = make_float2(xe[k], 0.f);
+        cs[k] = make_float2(GRAD ? __fmul_rn(xe[k], de) : 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (unsigned q = first; q < rq.qe; q += 128) {
+        float2 d0, d1;
+        if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            float2 lo, hi;
+            lds_quad<false>(st.at(k, q), lo, hi);
+            if (huge) {
+                lo = make_float2(lo.x - off[k], lo.y - off[k]);
+                hi = make_float2(hi.x - off[k], hi.y - off[k]);
+            }
+            lo = __ffma2_rn(lo, scale, shift[k]);
+            hi = __ffma2_rn(hi, scale, shift[k]);
+            lo = make_float2(exp2_flush(lo.x), exp2_flush(lo.y));
+            hi = make_float2(exp2_flush(hi.x), exp2_flush(hi.y));
+            zs[k] = __fadd2_rn(zs[k], __fadd2_rn(lo, hi));
+            if constexpr (GRAD) cs[k] = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, cs[k]));
+            sts_quad(st.at(k, q), lo, hi);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        z[k] = warp_sum(zs[k].x + zs[k].y);
+        c[k] = GRAD ? warp_sum(cs[k].x + cs[k].y) : 0.f;
+    }
+    // A dout that is not finite makes c so too, even under weights of 0: such a
+    // row leaves those products out.
+    bool guarded = false;
+    if constexpr (GRAD) {
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) guarded = guarded || !(fabsf(c[k]) < INFINITY);
+        if (guarded) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                float2 sum = make_float2(xe[k] != 0.f ? __fmul_rn(xe[k], de) : 0.f, 0.f);
+#pragma unroll 1
+                for (unsigned q = first; q < rq.qe; q += 128) {
+                    float2 d0, d1, lo, hi;
+                    lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+                    lds_quad<false>(st.at(k, q), lo, hi);
+                    d0 = make_float2(lo.x == 0.f ? 0.f : d0.x, lo.y == 0.f ? 0.f : d0.y);
+                    d1 = make_float2(hi.x == 0.f ? 0.f : d1.x, hi.y == 0.f ? 0.f : d1.y);
+                    sum = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, sum));
+                }
+                c[k] = warp_sum(sum.x + sum.y);
             }
         }
-        __syncthreads();  // the next run's rows overwrite this one's
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        inv[k] = inverse(z[k]);
+        if constexpr (GRAD) c[k] *= inv[k];
+    }
+    if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = c[MAPS - 1];
+    if constexpr (TWO) inv[1] *= -lam;
+
+    // Results.  Gradients are w·(inv·d - inv·c).
+    auto grad = [&](int k, float2 w, float2 d) {
+        const float ic = -inv[k] * c[k];
+        float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
+        if (guarded) {
+            if (w.x == 0.f) y.x = 0.f;
+            if (w.y == 0.f) y.y = 0.f;
+        }
+        return y;
+    };
+    auto map = [&](const float2 (&w)[MAPS]) {
+        const float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
+        return __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y);
+    };
+    if (rq.has_edge) {
+        if constexpr (GRAD) {
+            store_entry<OUT>(a.out1, rq.edge, grad(0, make_float2(xe[0], 0.f), make_float2(de, 0.f)).x);
+            if constexpr (TWO) store_entry<OUT>(a.out2, rq.edge, grad(1, make_float2(xe[1], 0.f), make_float2(de, 0.f)).x);
+        } else {
+            float2 w[MAPS];
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) w[k] = make_float2(xe[k], 0.f);
+            store_entry<OUT>(a.out1, rq.edge, map(w).x);
+        }
+    }
+#pragma unroll 2
+    for (unsigned q = first; q < rq.qe; q += 128) {
+        float2 lo[MAPS], hi[MAPS];
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
+        if constexpr (GRAD) {
+            float2 d0, d1;
+            lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+            store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
+            if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
+        } else {
+            store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
+        }
+    }
+}
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+
+template <bool TWO, bool GRAD, bool DIN>
+using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0>;
+
+// Warp g of G takes the rows that begin in share g of the entries.  vec: the
+// outputs start on whole quads.
+template <bool TWO, bool GRAD, bool DIN, bool OUT>
+__global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
+    using S = MapStream<TWO, GRAD, DIN>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ BlockStats<kWarps> sh;
+    __shared__ int bounds[kWarps + 1];
+    __shared__ unsigned is_long[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x * kWarps + warp;
+    int r0, r1;
+    first_rows_from(a.row_offsets, a.M, share_begin(a.nnz, min(g, G), G), share_begin(a.nnz, min(g + 1, G), G), lane, r0, r1);
+    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
+    if (g + 1 >= G) r1 = a.M;
+    S st;
+    st.src[0] = reinterpret_cast<const unsigned char*>(a.s1);
+    st.src[1] = static_cast<const unsigned char*>(TWO ? (const void*)a.s2 : a.dout);
+    st.src[2] = static_cast<const unsigned char*>(a.dout);
+    st.base = smem_addr(smem) + warp * S::kBytes;
+    st.nnz = a.nnz;
+    st.lane = lane;
+    st.aligned = aligned;
+    st.issued = 0;
+    st.limit = 0;
+    RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
+    int p0, p1;
+    if (r0 < r1) {
+        walk.range(r1 - 1, p0, p1);
+        st.limit = (int)(((long long)p1 + kChunk - 1) / kChunk);
+        walk.range(r0, p0, p1);
+        st.seek(p0);
+    }
+    if (lane == 0) {
+        bounds[warp] = r0;
+        if (warp == kWarps - 1) bounds[kWarps] = r1;
+    }
+    __syncthreads();
+    // Long rows by the CTA, while the rings fill.
+    for (int r = bounds[0]; r < bounds[kWarps]; r += kThreads) {
+        bool mine = false;
+        if (threadIdx.x < bounds[kWarps] - r) {
+            row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
+            mine = p1 - p0 > kRingRow;
+        }
+        const unsigned mask = __ballot_sync(kFullMask, mine);
+        if (lane == 0) is_long[warp] = mask;
+        if (!__syncthreads_or(mine)) continue;
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll 1
+            for (unsigned left = is_long[w]; left; left &= left - 1) {
+                const int row = r + w * 32 + __ffs(left) - 1;
+                row_range(a.row_offsets, row, a.nnz, p0, p1);
+                long_row<TWO, GRAD, DIN, OUT, kWarps>(a, row, TWO ? __ldg(a.lambda + row / a.seg_rows % a.heads) : 0.f, p0,
+                                                      p1, sh);
+            }
+        __syncthreads();  // is_long is read
+    }
+    float lam = 0.f;
+    long long block_end = 0;  // lam is the head's of the rows before this one
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+        walk.range(r, p0, p1);
+        if (p0 == p1) {
+            if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
+            continue;
+        }
+        if (p1 - p0 > kRingRow) continue;
+        if (TWO && r >= block_end) {
+            const int block = r / a.seg_rows;
+            block_end = (block + 1LL) * a.seg_rows;
+            lam = __ldg(a.lambda + block % a.heads);
+        }
+        st.need(p0, p1);
+        ring_row<TWO, GRAD, DIN, OUT>(a, st, r, lam, p0, p1, vec);
     }
 }
 
 // A cluster per row.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads) cluster_rows_kernel(const MapArgs a) {
-    __shared__ BlockStats sh;
+constexpr int kClusterWarps = 8;
+template <bool TWO, bool GRAD, bool DIN, bool OUT>
+__global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const MapArgs a) {
+    __shared__ BlockStats<kClusterWarps> sh;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
     int p0, p1;
@@ -385,7 +537,7 @@ __global__ void __launch_bounds__(kThreads) cluster_rows_kernel(const MapArgs a)
         return;
     }
     const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
-    map_row<TWO, GRAD, DIN, OUT, VEC, true>(a, r, lam, p0, p1, sh, ctas, rank);
+    block_row<TWO, GRAD, DIN, OUT, kClusterWarps>(a, r, lam, p0, p1, sh, ctas, rank);
 }
 
 // dλ[h] = -Σ c2 over head h's rows: a CTA per head, a fixed order.
@@ -409,50 +561,48 @@ __global__ void __launch_bounds__(1024) lambda_grad_kernel(int M, int blocks, in
     }
 }
 
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool VEC>
+template <bool TWO, bool GRAD, bool DIN, bool OUT>
 int launch_rows(const MapArgs& a, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     const int mean = a.nnz / a.M;
-    // Clusters where rows are long (their CTAs hold over half a CTA's registers'
-    // worth each) and too few to give every SM one.
-    int ctas = 1;
-    while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kThreads * 4 * kQuads / 2) ctas *= 2;
-    if (ctas > 1) {
+    // A CTA of 8 warps a row where rows are long and too few to fill the GPU with
+    // a warp each; a cluster while its CTAs are too few too and keep at least
+    // half their registers' worth each.
+    if (mean > kRingRow && a.M <= 4 * sms) {
+        int ctas = 1;
+        while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kClusterWarps * 32 * kSteps / 2) ctas *= 2;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = ctas;
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((long long)a.M * ctas));
-        cfg.blockDim = dim3(kThreads);
+        cfg.gridDim = dim3((unsigned)(a.M * ctas));
+        cfg.blockDim = dim3(kClusterWarps * 32);
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT, VEC>, a) == cudaSuccess ? USM_OK
-                                                                                                        : USM_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
+                                                                                                   : USM_ERR_CUDA;
     }
-    // A CTA each while there are fewer rows than CTA slots (a CTA then takes rows
-    // that a warp would have to walk twice), else one wave of CTAs.
-    const int slots = sms * (TWO && GRAD ? 3 : 4);
-    const bool few = a.M <= slots;
-    row_runs_kernel<TWO, GRAD, DIN, OUT, VEC>
-        <<<few ? a.M : slots, kThreads, 0, stream>>>(a, few ? 32 * 4 * kQuads : kLong);
+    // Warps: as many as the rings leave room for, with at least 256 entries each.
+    using S = MapStream<TWO, GRAD, DIN>;
+    constexpr int smem = kWarps * S::kBytes, per_sm = 220 * 1024 / (smem + 1280);
+    const int most = sms * per_sm * kWarps, G = a.nnz / 256 < most ? (a.nnz / 256 > 0 ? a.nnz / 256 : 1) : most;
+    const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
+    const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
+    const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return USM_ERR_CUDA;
+    kernel<<<(G + kWarps - 1) / kWarps, kThreads, smem, stream>>>(a, G, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
 template <bool TWO, bool GRAD>
 int launch_map(const MapArgs& a, cudaStream_t stream) {
-    const bool vec = quad_aligned(a.s1, false) && (!TWO || quad_aligned(a.s2, false)) &&
-                     (!GRAD || quad_aligned(a.dout, a.dout_bf16)) && quad_aligned(a.out1, a.out_bf16) &&
-                     (!(GRAD && TWO) || quad_aligned(a.out2, a.out_bf16));
-    auto pick = [&](auto din, auto out) {
-        constexpr bool D = decltype(din)::value, O = decltype(out)::value;
-        return vec ? launch_rows<TWO, GRAD, D, O, true>(a, stream) : launch_rows<TWO, GRAD, D, O, false>(a, stream);
-    };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    if (GRAD && a.dout_bf16) return a.out_bf16 ? pick(std::bool_constant<GRAD>{}, Yes{}) : pick(std::bool_constant<GRAD>{}, No{});
-    return a.out_bf16 ? pick(No{}, Yes{}) : pick(No{}, No{});
+    if constexpr (GRAD) {
+        if (a.dout_bf16)
+            return a.out_bf16 ? launch_rows<TWO, true, true, true>(a, stream) : launch_rows<TWO, true, true, false>(a, stream);
+    }
+    return a.out_bf16 ? launch_rows<TWO, GRAD, false, true>(a, stream) : launch_rows<TWO, GRAD, false, false>(a, stream);
 }
 
 }  // namespace
