@@ -38,8 +38,12 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// 1/z, or 0 for a row without weight; NaN stays NaN.
-__device__ __forceinline__ float inverse(float z) { return z == 0.f ? 0.f : 1.f / z; }
+// 1/z (within one step of 2^-23), or 0 for a row without weight; NaN stays NaN.
+__device__ __forceinline__ float inverse(float z) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(z));
+    return z == 0.f ? 0.f : y;
+}
 // w·d, or 0 under a weight of 0 (a masked entry) whatever d is there.
 __device__ __forceinline__ float weighted(float w, float d) { return w == 0.f ? 0.f : w * d; }
 
@@ -326,19 +330,32 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) m[k] = warp_max(m[k]);
 
-    // Weights, in place, and their sums.
+    // A maximum of -inf (every entry masked) leaves the scores as they are, and
+    // scores so large that s·log2 e overflows are brought near zero first.
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k)
+        if (!(fabsf(m[k]) <= 1e37f)) {
+            if (m[k] != -INFINITY) {
+                xe[k] -= m[k];
+#pragma unroll 1
+                for (unsigned q = first; q < rq.qe; q += 128) {
+                    float2 lo, hi;
+                    lds_quad<false>(st.at(k, q), lo, hi);
+                    sts_quad(st.at(k, q), make_float2(lo.x - m[k], lo.y - m[k]), make_float2(hi.x - m[k], hi.y - m[k]));
+                }
+            }
+            m[k] = 0.f;
+        }
+
+    // Weights exp(s - m) = 2^(s·log2 e - m·log2 e), in place, and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
     float2 zs[MAPS], cs[MAPS], shift[MAPS];
-    float off[MAPS];
-    bool huge = false;
     const float2 scale = make_float2(kLog2e, kLog2e);
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        const Base base(m[k]);
-        huge = huge || base.huge();
-        off[k] = base.off;
-        shift[k] = make_float2(-base.shift, -base.shift);
-        xe[k] = weight_of(xe[k], base);
+        const float sh = -m[k] * kLog2e;
+        shift[k] = make_float2(sh, sh);
+        xe[k] = exp2_flush(fmaf(xe[k], kLog2e, sh));
         zs[k] = make_float2(xe[k], 0.f);
         cs[k] = make_float2(GRAD ? __fmul_rn(xe[k], de) : 0.f, 0.f);
     }
@@ -350,10 +367,6 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
         for (int k = 0; k < MAPS; ++k) {
             float2 lo, hi;
             lds_quad<false>(st.at(k, q), lo, hi);
-            if (huge) {
-                lo = make_float2(lo.x - off[k], lo.y - off[k]);
-                hi = make_float2(hi.x - off[k], hi.y - off[k]);
-            }
             lo = __ffma2_rn(lo, scale, shift[k]);
             hi = __ffma2_rn(hi, scale, shift[k]);
             lo = make_float2(exp2_flush(lo.x), exp2_flush(lo.y));
@@ -467,6 +480,7 @@ __global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, 
     st.nnz = a.nnz;
     st.lane = lane;
     st.aligned = aligned;
+    st.whole = aligned ? a.nnz / kChunk : 0;
     st.issued = 0;
     st.limit = 0;
     RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};

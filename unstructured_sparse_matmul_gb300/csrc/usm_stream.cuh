@@ -25,6 +25,7 @@ struct Stream {
     uint32_t base;  // shared address of the warp's rings
     int nnz, lane;
     bool aligned;   // every array starts on 16 bytes
+    int whole;      // chunks before this one are whole (none, if not aligned)
     int issued;     // chunks before this one are copied or in flight
     int limit;      // chunks from this one on are not needed
 
@@ -33,31 +34,35 @@ struct Stream {
         return array == 0 ? base + i * E0 : array == 1 ? base + kRing * E0 + i * E1 : base + kRing * (E0 + E1) + i * E2;
     }
 
-    template <int E>
+    // Chunk `chunk` of one array: whole, or (EDGE) where the array may end inside
+    // it or starts off 16 bytes.
+    template <int E, bool EDGE>
     __device__ __forceinline__ void copy(int array, int chunk) const {
         if constexpr (E > 0) {
             constexpr int PER = 16 / E;  // entries a copy
-            const unsigned char* from = src[array];
+            const uint32_t p0 = (uint32_t)chunk * kChunk + lane * PER, to = at(array, p0);
+            const unsigned char* from = src[array] + (unsigned long long)p0 * E;
 #pragma unroll
             for (int i = 0; i < kChunk / PER / 32; ++i) {
-                const long long p = (long long)chunk * kChunk + (i * 32 + lane) * PER;
-                const uint32_t to = at(array, (uint32_t)p);
-                const int bytes = (int)min(max(((long long)nnz - p) * E, 0LL), 16LL);  // past the end: zeros, unread
-                if (aligned) {
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from + p * E),
-                                 "r"(bytes)
+                if constexpr (!EDGE) {
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
                                  : "memory");
                 } else {
-#pragma unroll
-                    for (int u = 0; u < PER; ++u) {
-                        if (u * E < bytes) {
+                    const long long left = ((long long)nnz - p0 - i * 32 * PER) * E;
+                    const int bytes = (int)min(max(left, 0LL), 16LL);  // past the end: zeros, unread
+                    if (aligned) {
+                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512),
+                                     "l"(from + i * 512), "r"(bytes)
+                                     : "memory");
+                    } else {
+                        for (int u = 0; u < bytes; u += E) {
                             if constexpr (E == 4)
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + u * 4),
-                                             "r"(reinterpret_cast<const uint32_t*>(from)[p + u])
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 + u),
+                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 + u))
                                              : "memory");
                             else
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + u * 2),
-                                             "h"(reinterpret_cast<const uint16_t*>(from)[p + u])
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 + u),
+                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 + u))
                                              : "memory");
                         }
                     }
@@ -65,12 +70,21 @@ struct Stream {
             }
         }
     }
+    __device__ __noinline__ void copy_edge(int chunk) const {
+        copy<E0, true>(0, chunk);
+        copy<E1, true>(1, chunk);
+        copy<E2, true>(2, chunk);
+    }
     // The next chunk (an empty group past the limit).
     __device__ __forceinline__ void issue() {
         if (issued < limit) {
-            copy<E0>(0, issued);
-            copy<E1>(1, issued);
-            copy<E2>(2, issued);
+            if (issued < whole) {
+                copy<E0, false>(0, issued);
+                copy<E1, false>(1, issued);
+                copy<E2, false>(2, issued);
+            } else {
+                copy_edge(issued);
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         ++issued;
