@@ -33,6 +33,7 @@
 #include "usm_cluster.cuh"
 #include "usm_internal.h"
 #include "usm_rel.cuh"
+#include "usm_stream.cuh"
 
 namespace usm {
 namespace {
@@ -783,9 +784,7 @@ struct Launch {
             float* parts = static_cast<float*>(workspace);
             int* cut_rows = reinterpret_cast<int*>(parts + (size_t)G * 2 * Row::kMaps * (a.N + 2));
             const auto kernel = attention_shares_kernel<Row>;
-            if (R::kSmem > 40 * 1024 &&
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem) != cudaSuccess)
-                return USM_ERR_CUDA;
+            if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
             kernel<<<(G + R::kWarps - 1) / R::kWarps, R::kWarps * 32, R::kSmem, stream>>>(a, parts, cut_rows, G);
             const dim3 grid((unsigned)(G + ((long long)a.M + 255) / 256), (a.N + 31) / 32);
             attention_join_kernel<Row::kMaps><<<grid, 256, 0, stream>>>(a, parts, cut_rows, G);
@@ -797,9 +796,7 @@ struct Launch {
         int ctas = 1;
         while (ctas < 8 && (long long)a.M * ctas < 4LL * sms && (long long)ctas * R::kWarps < windows) ctas *= 2;
         const auto kernel = attention_cluster_kernel<Row>;
-        if (R::kSmem > 40 * 1024 &&
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem) != cudaSuccess)
-            return USM_ERR_CUDA;
+        if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = ctas;

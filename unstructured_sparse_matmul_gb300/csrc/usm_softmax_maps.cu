@@ -5,10 +5,10 @@
 // Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
 // stored entries.
 //
-// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
-// takes the rows that begin in an equal share of the entries and streams them
-// through a ring of its own in shared memory (usm_stream.cuh), so copies are in
-// flight all the time whatever the rows' arithmetic and lengths do; a row is
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every two
+// warps take the rows that begin in an equal share of the entries and stream them
+// through a ring in shared memory (usm_stream.cuh), so copies are in flight all
+// the time whatever the rows' arithmetic and lengths do; a row is
 // walked three times there (maximum; weights, their sums, written back in place;
 // results), four entries a lane, in pairs of fp32 (f32x2).  Rows over 1536
 // entries are first taken by the whole CTA; where rows are long and few, a
@@ -453,21 +453,33 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
     }
 }
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+#ifndef USM_GW
+#define USM_GW 2
+#endif
+constexpr int kWarps = 4, kThreads = kWarps * 32, kGroup = USM_GW, kGroups = kWarps / kGroup;
 
 template <bool TWO, bool GRAD, bool DIN>
-using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0>;
+using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0, kGroup>;
 
-// Warp g of G takes the rows that begin in share g of the entries.  vec: the
+// CTAs an SM that the rings leave room for, at most 6 (80 registers a thread).
+template <class S>
+constexpr int ctas_per_sm() {
+    constexpr int n = 224 * 1024 / (kGroups * S::kBytes + 1280);
+    return n > 6 ? 6 : n;
+}
+
+// Group g of G takes the rows that begin in share g of the entries.  vec: the
 // outputs start on whole quads.
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
-__global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN>>())
+    stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
     using S = MapStream<TWO, GRAD, DIN>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ BlockStats<kWarps> sh;
-    __shared__ int bounds[kWarps + 1];
+    __shared__ int bounds[kGroups + 1];
     __shared__ unsigned is_long[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x * kWarps + warp;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / kGroup, member = warp % kGroup, g = blockIdx.x * kGroups + group;
     int r0, r1;
     first_rows_from(a.row_offsets, a.M, share_begin(a.nnz, min(g, G), G), share_begin(a.nnz, min(g + 1, G), G), lane, r0, r1);
     if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
@@ -476,9 +488,10 @@ __global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, 
     st.src[0] = reinterpret_cast<const unsigned char*>(a.s1);
     st.src[1] = static_cast<const unsigned char*>(TWO ? (const void*)a.s2 : a.dout);
     st.src[2] = static_cast<const unsigned char*>(a.dout);
-    st.base = smem_addr(smem) + warp * S::kBytes;
+    st.base = smem_addr(smem) + group * S::kBytes;
     st.nnz = a.nnz;
-    st.lane = lane;
+    st.lane = member * 32 + lane;
+    st.barrier = 1 + group;
     st.aligned = aligned;
     st.whole = aligned ? a.nnz / kChunk : 0;
     st.issued = 0;
@@ -486,20 +499,20 @@ __global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, 
     RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
     int p0, p1;
     if (r0 < r1) {
-        walk.range(r1 - 1, p0, p1);
-        st.limit = (int)(((long long)p1 + kChunk - 1) / kChunk);
-        walk.range(r0, p0, p1);
-        st.seek(p0);
+        walk.hold(r1, 0);
+        st.limit = (int)(((long long)walk.offset(r1) + kChunk - 1) / kChunk);
+        walk.hold(r0, kGroup);
+        st.seek(walk.offset(r0));
     }
     if (lane == 0) {
-        bounds[warp] = r0;
-        if (warp == kWarps - 1) bounds[kWarps] = r1;
+        bounds[group] = r0;
+        if (group == kGroups - 1) bounds[kGroups] = r1;
     }
     __syncthreads();
     // Long rows by the CTA, while the rings fill.
-    for (int r = bounds[0]; r < bounds[kWarps]; r += kThreads) {
+    for (int r = bounds[0]; r < bounds[kGroups]; r += kThreads) {
         bool mine = false;
-        if (threadIdx.x < bounds[kWarps] - r) {
+        if (threadIdx.x < bounds[kGroups] - r) {
             row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
             mine = p1 - p0 > kRingRow;
         }
@@ -520,21 +533,43 @@ __global__ void __launch_bounds__(kThreads) stream_rows_kernel(const MapArgs a, 
     float lam = 0.f;
     long long block_end = 0;  // lam is the head's of the rows before this one
 #pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-        walk.range(r, p0, p1);
-        if (p0 == p1) {
-            if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
+    for (int r = r0; r < r1;) {
+        walk.hold(r, kGroup);
+        const int begin = walk.offset(r);
+        // As many of the next rows as there are warps and fit the ring together.
+        int n = 0, end = begin;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int next = walk.offset(min(r + i + 1, a.M));
+            if (n == i && r + i < r1 && next - begin <= kRingRow) {
+                if (i == member) {
+                    p0 = end;
+                    p1 = max(next, end);
+                }
+                ++n;
+                end = max(next, end);
+            }
+        }
+        if (n == 0) {  // a long row
+            ++r;
             continue;
         }
-        if (p1 - p0 > kRingRow) continue;
-        if (TWO && r >= block_end) {
-            const int block = r / a.seg_rows;
-            block_end = (block + 1LL) * a.seg_rows;
-            lam = __ldg(a.lambda + block % a.heads);
+        if (begin < end) st.need(begin, end);
+        if (member < n) {
+            const int row = r + member;
+            if (TWO && row >= block_end) {
+                const int block = row / a.seg_rows;
+                block_end = (block + 1LL) * a.seg_rows;
+                lam = __ldg(a.lambda + block % a.heads);
+            }
+            if (p0 < p1)
+                ring_row<TWO, GRAD, DIN, OUT>(a, st, row, lam, p0, p1, vec);
+            else if (GRAD && TWO && a.row_c2 && lane == 0)
+                a.row_c2[row] = 0.f;
         }
-        st.need(p0, p1);
-        ring_row<TWO, GRAD, DIN, OUT>(a, st, r, lam, p0, p1, vec);
+        r += n;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
 }
 
 // A cluster per row.
@@ -598,15 +633,15 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
                                                                                                    : USM_ERR_CUDA;
     }
-    // Warps: as many as the rings leave room for, with at least 256 entries each.
+    // Groups: as many as there is room for their rings, with at least 256 entries each.
     using S = MapStream<TWO, GRAD, DIN>;
-    constexpr int smem = kWarps * S::kBytes, per_sm = 220 * 1024 / (smem + 1280);
-    const int most = sms * per_sm * kWarps, G = a.nnz / 256 < most ? (a.nnz / 256 > 0 ? a.nnz / 256 : 1) : most;
+    constexpr int smem = kGroups * S::kBytes;
+    const int most = sms * ctas_per_sm<S>() * kGroups, G = a.nnz / 256 < most ? (a.nnz / 256 > 0 ? a.nnz / 256 : 1) : most;
     const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
     const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
     const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return USM_ERR_CUDA;
-    kernel<<<(G + kWarps - 1) / kWarps, kThreads, smem, stream>>>(a, G, aligned, vec);
+    if (!allow_shared(kernel, smem)) return USM_ERR_CUDA;
+    kernel<<<(G + kGroups - 1) / kGroups, kThreads, smem, stream>>>(a, G, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 

@@ -1,11 +1,12 @@
-// CSR value arrays streamed through shared memory, a warp at a time.
+// CSR value arrays streamed through shared memory by a group of warps.
 //
-// A warp works on consecutive rows, whose entries are consecutive too, so what
-// it reads of every array is one run.  It has a ring of kRing entries in shared
-// memory for each array (entry p lies at p mod kRing) that asynchronous copies
-// fill kChunk entries at a time, up to a ring ahead of the row it works on: the
-// copies never wait for a row's arithmetic, nor for where rows begin and end.
-// No barriers but the warp's own.
+// A group works on consecutive rows, a row a warp, whose entries are consecutive
+// too: what it reads of every array is one run.  It has a ring of kRing entries
+// in shared memory for each array (entry p lies at p mod kRing) that asynchronous
+// copies fill kChunk entries at a time, up to a ring ahead of the rows it works
+// on: the copies do not wait for the rows' arithmetic, nor for where rows begin
+// and end.  Two warps to a ring: with one, an SM's shared memory holds the rings
+// of 12 warps, too few to cover the latency of a row's own arithmetic.
 #pragma once
 
 #include "usm_device.cuh"
@@ -14,16 +15,19 @@
 namespace usm {
 
 constexpr int kChunk = 512, kRing = 4 * kChunk;
-// Rows up to this long fit the ring wherever they start.
+// A run up to this long fits the ring wherever it starts.
 constexpr int kRingRow = 3 * kChunk;
 
-// Streams up to three arrays of E0, E1, E2 bytes an element (0: none).
-template <int E0, int E1, int E2>
+// Streams up to three arrays of E0, E1, E2 bytes an element (0: none), for GW
+// warps; every warp of the group makes the same calls.
+template <int E0, int E1, int E2, int GW>
 struct Stream {
-    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a warp
+    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a group
     const unsigned char* src[3];
-    uint32_t base;  // shared address of the warp's rings
-    int nnz, lane;
+    uint32_t base;  // shared address of the group's rings
+    int nnz;
+    int lane;       // of the group's 32·GW
+    int barrier;    // the group's named barrier, 1 or 2
     bool aligned;   // every array starts on 16 bytes
     int whole;      // chunks before this one are whole (none, if not aligned)
     int issued;     // chunks before this one are copied or in flight
@@ -43,26 +47,26 @@ struct Stream {
             const uint32_t p0 = (uint32_t)chunk * kChunk + lane * PER, to = at(array, p0);
             const unsigned char* from = src[array] + (unsigned long long)p0 * E;
 #pragma unroll
-            for (int i = 0; i < kChunk / PER / 32; ++i) {
+            for (int i = 0; i < kChunk / PER / (32 * GW); ++i) {
                 if constexpr (!EDGE) {
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512 * GW), "l"(from + i * 512 * GW)
                                  : "memory");
                 } else {
-                    const long long left = ((long long)nnz - p0 - i * 32 * PER) * E;
+                    const long long left = ((long long)nnz - p0 - i * 32 * GW * PER) * E;
                     const int bytes = (int)min(max(left, 0LL), 16LL);  // past the end: zeros, unread
                     if (aligned) {
-                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512),
-                                     "l"(from + i * 512), "r"(bytes)
+                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512 * GW),
+                                     "l"(from + i * 512 * GW), "r"(bytes)
                                      : "memory");
                     } else {
                         for (int u = 0; u < bytes; u += E) {
                             if constexpr (E == 4)
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 + u),
-                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 + u))
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 * GW + u),
+                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 * GW + u))
                                              : "memory");
                             else
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 + u),
-                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 + u))
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 * GW + u),
+                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 * GW + u))
                                              : "memory");
                         }
                     }
@@ -75,7 +79,15 @@ struct Stream {
         copy<E1, true>(1, chunk);
         copy<E2, true>(2, chunk);
     }
-    // The next chunk (an empty group past the limit).
+    __device__ __forceinline__ void sync() const {
+        if constexpr (GW == 1)
+            __syncwarp();
+        else if (barrier == 1)  // constants: a barrier in a register would reserve all 16
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * GW) : "memory");
+        else
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * GW) : "memory");
+    }
+    // The next chunk (an empty set of copies past the limit).
     __device__ __forceinline__ void issue() {
         if (issued < limit) {
             if (issued < whole) {
@@ -92,18 +104,18 @@ struct Stream {
     // Starts at entry p, with a full ring ahead of it.
     __device__ __forceinline__ void seek(int p) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
+        sync();
         issued = p / kChunk;
 #pragma unroll 1
         for (int i = 0; i < kRing / kChunk; ++i) issue();
     }
-    // Makes row [p0, p1) (at most kRingRow entries, one at least) readable by
-    // every lane; rows come in order, and the ring before p0 is given up.
+    // Makes entries [p0, p1) (at most kRingRow, one at least) readable by every
+    // lane; runs come in order, and the ring before p0 is given up.
     __device__ __forceinline__ void need(int p0, int p1) {
         const int c0 = p0 / kChunk;
         if (c0 >= issued || c0 + kRing / kChunk < issued) seek(p0);  // rows were left out
         if (c0 + kRing / kChunk > issued) {
-            __syncwarp();  // every lane is done with what is overwritten
+            sync();  // every warp is done with what is overwritten
             do issue();
             while (c0 + kRing / kChunk > issued);
         }
@@ -116,7 +128,7 @@ struct Stream {
             asm volatile("cp.async.wait_group 2;" ::: "memory");
         else
             asm volatile("cp.async.wait_group 3;" ::: "memory");
-        __syncwarp();
+        sync();
     }
 };
 
@@ -226,22 +238,31 @@ __device__ __forceinline__ void first_rows_from(const int* __restrict__ ro, int 
     r1 = lo[1];
 }
 
-// Lanes hold 32 consecutive row offsets; rows are read off them one by one.
+// Lanes hold 32 consecutive row offsets, read off them one by one.
 struct RowWalk {
     const int* ro;
     int M, nnz, lane, at, held;  // held: offset of row at + lane
-    __device__ __forceinline__ void range(int r, int& p0, int& p1) {
-        if (r - at >= 31 || r < at) {
+    // Offsets of rows r .. r + n (n < 32) can be read.
+    __device__ __forceinline__ void hold(int r, int n) {
+        if (r < at || r - at > 31 - n) {
             at = r;
-            held = __ldg(ro + min((long long)r + lane, (long long)M));
+            held = min(max(__ldg(ro + min((long long)r + lane, (long long)M)), 0), nnz);
         }
-        p0 = min(max(__shfl_sync(kFullMask, held, r - at), 0), nnz);
-        p1 = min(max(__shfl_sync(kFullMask, held, r - at + 1), p0), nnz);
     }
+    __device__ __forceinline__ int offset(int r) const { return __shfl_sync(kFullMask, held, r - at); }
 };
 
 // Share g of G of nnz entries.
 __device__ __forceinline__ int share_begin(int nnz, int g, int G) { return (int)((long long)nnz * g / G); }
+
+// Lets a kernel have `smem` bytes a CTA, and the SM all the shared memory there is
+// (the driver's own split left room for 4 CTAs of 33 KB where 6 fit).
+template <class Kernel>
+inline bool allow_shared(Kernel kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+               cudaSuccess;
+}
 
 inline bool aligned_for_stream(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
