@@ -5,17 +5,14 @@
 // Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
 // stored entries.
 //
-// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every two
-// warps take the rows that begin in an equal share of the entries and stream them
-// through a ring in shared memory (usm_stream.cuh), so copies are in flight all
-// the time whatever the rows' arithmetic and lengths do; a row is
-// walked three times there (maximum; weights, their sums, written back in place;
-// results), four entries a lane, in pairs of fp32 (f32x2).  Rows over 1536
-// entries are first taken by the whole CTA; where rows are long and few, a
-// cluster of up to 8 CTAs takes each (launch_rows).  (Rows read into registers by
-// a warp each measured 49 to 58 us for the differential map of 8x4096 rows of 410
-// entries: each row waited for its own loads, and lanes past its ends did the
-// arithmetic of 512.)
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
+// streams its rows through a ring of its own in shared memory (usm_stream.cuh), so
+// copies are in flight all the time whatever the rows' arithmetic and lengths do.
+// A row of up to 512 entries goes from the ring to registers once (four entries a
+// lane at a time, in pairs of fp32); one of up to 1536 is walked three times in
+// the ring (maximum; weights, their sums, written back in place; results).  Longer
+// rows are first taken by the whole CTA; where rows are long and few, a cluster of
+// up to 8 CTAs takes each (launch_rows).
 #include <cmath>
 
 #include "usm_cluster.cuh"
@@ -25,7 +22,8 @@
 namespace usm {
 namespace {
 
-constexpr int kSteps = 16;  // entries of a long row a thread keeps in registers
+constexpr int kSteps = 16;    // entries of a long row a thread keeps in registers
+constexpr int kRowSteps = 4;  // quads of a short row a lane does
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -306,25 +304,46 @@ __device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0
 }
 
 // A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
+// In registers (FITS: at most 128 whole quads), or walked in the ring.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool FITS, class S>
 __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
     constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31;
     const RowQuads rq(p0, p1, lane);
     const unsigned first = rq.qs + 4 * lane;
+    constexpr int STEPS = FITS ? kRowSteps : 1;
+    float2 x[MAPS][STEPS][2], d[GRAD ? STEPS : 1][2];  // FITS: the lane's quads
 
     // Maximum.
     float m[MAPS], xe[MAPS];
     const float de = GRAD && rq.has_edge ? lds_entry<DIN>(st.at(MAPS, rq.edge)) : 0.f;
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) m[k] = xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
-#pragma unroll 2
-    for (unsigned q = first; q < rq.qe; q += 128) {
+    if constexpr (FITS) {
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            float2 lo, hi;
-            lds_quad<false>(st.at(k, q), lo, hi);
-            m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
+        for (int i = 0; i < STEPS; ++i) {
+            const unsigned q = first + 128 * i;
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) x[k][i][0] = x[k][i][1] = make_float2(-INFINITY, -INFINITY);
+            if constexpr (GRAD) d[i][0] = d[i][1] = make_float2(0.f, 0.f);
+            if (q < rq.qe) {
+#pragma unroll
+                for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), x[k][i][0], x[k][i][1]);
+                if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d[i][0], d[i][1]);
+            }
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k)
+                m[k] = fmaxf(m[k], fmaxf(fmaxf(x[k][i][0].x, x[k][i][0].y), fmaxf(x[k][i][1].x, x[k][i][1].y)));
+        }
+    } else {
+#pragma unroll 2
+        for (unsigned q = first; q < rq.qe; q += 128) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                float2 lo, hi;
+                lds_quad<false>(st.at(k, q), lo, hi);
+                m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
+            }
         }
     }
 #pragma unroll
@@ -337,8 +356,14 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
         if (!(fabsf(m[k]) <= 1e37f)) {
             if (m[k] != -INFINITY) {
                 xe[k] -= m[k];
+                if constexpr (FITS) {
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) x[k][i][h] = make_float2(x[k][i][h].x - m[k], x[k][i][h].y - m[k]);
+                }
 #pragma unroll 1
-                for (unsigned q = first; q < rq.qe; q += 128) {
+                for (unsigned q = first; !FITS && q < rq.qe; q += 128) {
                     float2 lo, hi;
                     lds_quad<false>(st.at(k, q), lo, hi);
                     sts_quad(st.at(k, q), make_float2(lo.x - m[k], lo.y - m[k]), make_float2(hi.x - m[k], hi.y - m[k]));
@@ -359,21 +384,35 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
         zs[k] = make_float2(xe[k], 0.f);
         cs[k] = make_float2(GRAD ? __fmul_rn(xe[k], de) : 0.f, 0.f);
     }
-#pragma unroll 2
-    for (unsigned q = first; q < rq.qe; q += 128) {
-        float2 d0, d1;
-        if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+    // One quad's weights from its scores.
+    auto weights = [&](int k, float2& lo, float2& hi, float2 d0, float2 d1) {
+        lo = __ffma2_rn(lo, scale, shift[k]);
+        hi = __ffma2_rn(hi, scale, shift[k]);
+        lo = make_float2(exp2_flush(lo.x), exp2_flush(lo.y));
+        hi = make_float2(exp2_flush(hi.x), exp2_flush(hi.y));
+        zs[k] = __fadd2_rn(zs[k], __fadd2_rn(lo, hi));
+        if constexpr (GRAD) cs[k] = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, cs[k]));
+    };
+    if constexpr (FITS) {
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            float2 lo, hi;
-            lds_quad<false>(st.at(k, q), lo, hi);
-            lo = __ffma2_rn(lo, scale, shift[k]);
-            hi = __ffma2_rn(hi, scale, shift[k]);
-            lo = make_float2(exp2_flush(lo.x), exp2_flush(lo.y));
-            hi = make_float2(exp2_flush(hi.x), exp2_flush(hi.y));
-            zs[k] = __fadd2_rn(zs[k], __fadd2_rn(lo, hi));
-            if constexpr (GRAD) cs[k] = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, cs[k]));
-            sts_quad(st.at(k, q), lo, hi);
+        for (int i = 0; i < STEPS; ++i)
+            if (rq.qs + 128 * i < rq.qe) {
+#pragma unroll
+                for (int k = 0; k < MAPS; ++k)
+                    weights(k, x[k][i][0], x[k][i][1], d[GRAD ? i : 0][0], d[GRAD ? i : 0][1]);
+            }
+    } else {
+#pragma unroll 2
+        for (unsigned q = first; q < rq.qe; q += 128) {
+            float2 d0, d1;
+            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                float2 lo, hi;
+                lds_quad<false>(st.at(k, q), lo, hi);
+                weights(k, lo, hi, d0, d1);
+                sts_quad(st.at(k, q), lo, hi);
+            }
         }
     }
 #pragma unroll
@@ -391,14 +430,23 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
                 float2 sum = make_float2(xe[k] != 0.f ? __fmul_rn(xe[k], de) : 0.f, 0.f);
-#pragma unroll 1
-                for (unsigned q = first; q < rq.qe; q += 128) {
-                    float2 d0, d1, lo, hi;
-                    lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-                    lds_quad<false>(st.at(k, q), lo, hi);
+                auto add = [&](float2 lo, float2 hi, float2 d0, float2 d1) {
                     d0 = make_float2(lo.x == 0.f ? 0.f : d0.x, lo.y == 0.f ? 0.f : d0.y);
                     d1 = make_float2(hi.x == 0.f ? 0.f : d1.x, hi.y == 0.f ? 0.f : d1.y);
                     sum = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, sum));
+                };
+                if constexpr (FITS) {
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i)
+                        if (rq.qs + 128 * i < rq.qe) add(x[k][i][0], x[k][i][1], d[i][0], d[i][1]);
+                } else {
+#pragma unroll 1
+                    for (unsigned q = first; q < rq.qe; q += 128) {
+                        float2 d0, d1, lo, hi;
+                        lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+                        lds_quad<false>(st.at(k, q), lo, hi);
+                        add(lo, hi, d0, d1);
+                    }
                 }
                 c[k] = warp_sum(sum.x + sum.y);
             }
@@ -437,139 +485,124 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
             store_entry<OUT>(a.out1, rq.edge, map(w).x);
         }
     }
-#pragma unroll 2
-    for (unsigned q = first; q < rq.qe; q += 128) {
-        float2 lo[MAPS], hi[MAPS];
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
+    auto results = [&](unsigned q, const float2 (&lo)[MAPS], const float2 (&hi)[MAPS], float2 d0, float2 d1) {
         if constexpr (GRAD) {
-            float2 d0, d1;
-            lds_quad<DIN>(st.at(MAPS, q), d0, d1);
             store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
             if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
         } else {
             store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
         }
+    };
+    if constexpr (FITS) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const unsigned q = first + 128 * i;
+            if (q < rq.qe) {
+                float2 lo[MAPS], hi[MAPS];
+#pragma unroll
+                for (int k = 0; k < MAPS; ++k) {
+                    lo[k] = x[k][i][0];
+                    hi[k] = x[k][i][1];
+                }
+                results(q, lo, hi, d[GRAD ? i : 0][0], d[GRAD ? i : 0][1]);
+            }
+        }
+    } else {
+#pragma unroll 2
+        for (unsigned q = first; q < rq.qe; q += 128) {
+            float2 lo[MAPS], hi[MAPS], d0, d1;
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
+            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+            results(q, lo, hi, d0, d1);
+        }
     }
 }
 
-#ifndef USM_GW
-#define USM_GW 2
-#endif
-constexpr int kWarps = 4, kThreads = kWarps * 32, kGroup = USM_GW, kGroups = kWarps / kGroup;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 
 template <bool TWO, bool GRAD, bool DIN>
-using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0, kGroup>;
+using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0>;
 
-// CTAs an SM that the rings leave room for, at most 6 (80 registers a thread).
+// CTAs an SM that the rings leave room for.
 template <class S>
 constexpr int ctas_per_sm() {
-    constexpr int n = 224 * 1024 / (kGroups * S::kBytes + 1280);
-    return n > 6 ? 6 : n;
+    return 226 * 1024 / (kWarps * S::kBytes + 4096);
 }
 
-// Group g of G takes the rows that begin in share g of the entries.  vec: the
-// outputs start on whole quads.
+// The rows of a walk in the ring, out of line: most rows are shorter.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
+__device__ __noinline__ void wide_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
+    ring_row<TWO, GRAD, DIN, OUT, false>(a, st, r, lam, p0, p1, vec);
+}
+
+// CTA b of B takes rows [M·b / B, M·(b+1) / B), kBatch at a time; a batch's rows
+// are dealt to the warps by equal parts of its entries.  vec: the outputs start
+// on whole quads.
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN>>())
-    stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
+    stream_rows_kernel(const MapArgs a, bool aligned, bool vec) {
     using S = MapStream<TWO, GRAD, DIN>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ BlockStats<kWarps> sh;
-    __shared__ int bounds[kGroups + 1];
-    __shared__ unsigned is_long[kWarps];
+    __shared__ RowBatch batch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group = warp / kGroup, member = warp % kGroup, g = blockIdx.x * kGroups + group;
-    int r0, r1;
-    first_rows_from(a.row_offsets, a.M, share_begin(a.nnz, min(g, G), G), share_begin(a.nnz, min(g + 1, G), G), lane, r0, r1);
-    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
-    if (g + 1 >= G) r1 = a.M;
+    const long long first = (long long)a.M * blockIdx.x / gridDim.x, last = (long long)a.M * (blockIdx.x + 1) / gridDim.x;
     S st;
     st.src[0] = reinterpret_cast<const unsigned char*>(a.s1);
     st.src[1] = static_cast<const unsigned char*>(TWO ? (const void*)a.s2 : a.dout);
     st.src[2] = static_cast<const unsigned char*>(a.dout);
-    st.base = smem_addr(smem) + group * S::kBytes;
+    st.base = smem_addr(smem) + warp * S::kBytes;
     st.nnz = a.nnz;
-    st.lane = member * 32 + lane;
-    st.barrier = 1 + group;
+    st.lane = lane;
     st.aligned = aligned;
     st.whole = aligned ? a.nnz / kChunk : 0;
-    st.issued = 0;
-    st.limit = 0;
-    RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
-    int p0, p1;
-    if (r0 < r1) {
-        walk.hold(r1, 0);
-        st.limit = (int)(((long long)walk.offset(r1) + kChunk - 1) / kChunk);
-        walk.hold(r0, kGroup);
-        st.seek(walk.offset(r0));
-    }
-    if (lane == 0) {
-        bounds[group] = r0;
-        if (group == kGroups - 1) bounds[kGroups] = r1;
-    }
-    __syncthreads();
-    // Long rows by the CTA, while the rings fill.
-    for (int r = bounds[0]; r < bounds[kGroups]; r += kThreads) {
-        bool mine = false;
-        if (threadIdx.x < bounds[kGroups] - r) {
-            row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
-            mine = p1 - p0 > kRingRow;
+    for (long long b = first; b < last; b += kBatch) {
+        const int n = (int)min((long long)kBatch, last - b);
+        const bool any_long = batch.load(a.row_offsets, a.nnz, (int)b, n, kRingRow);
+        const int i0 = warp == 0 ? 0 : batch.first_from(n, batch.part(n, warp, kWarps), lane);
+        const int i1 = warp == kWarps - 1 ? n : batch.first_from(n, batch.part(n, warp + 1, kWarps), lane);
+        int p0, p1;
+        if (i0 < i1) {
+            st.limit = (int)(((long long)batch.offset[i1] + kChunk - 1) / kChunk);
+            st.seek(batch.offset[i0]);
         }
-        const unsigned mask = __ballot_sync(kFullMask, mine);
-        if (lane == 0) is_long[warp] = mask;
-        if (!__syncthreads_or(mine)) continue;
+        if (any_long) {  // by the CTA, while the rings fill
 #pragma unroll 1
-        for (int w = 0; w < kWarps; ++w)
-#pragma unroll 1
-            for (unsigned left = is_long[w]; left; left &= left - 1) {
-                const int row = r + w * 32 + __ffs(left) - 1;
-                row_range(a.row_offsets, row, a.nnz, p0, p1);
-                long_row<TWO, GRAD, DIN, OUT, kWarps>(a, row, TWO ? __ldg(a.lambda + row / a.seg_rows % a.heads) : 0.f, p0,
-                                                      p1, sh);
-            }
-        __syncthreads();  // is_long is read
-    }
-    float lam = 0.f;
-    long long block_end = 0;  // lam is the head's of the rows before this one
-#pragma unroll 1
-    for (int r = r0; r < r1;) {
-        walk.hold(r, kGroup);
-        const int begin = walk.offset(r);
-        // As many of the next rows as there are warps and fit the ring together.
-        int n = 0, end = begin;
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            const int next = walk.offset(min(r + i + 1, a.M));
-            if (n == i && r + i < r1 && next - begin <= kRingRow) {
-                if (i == member) {
-                    p0 = end;
-                    p1 = max(next, end);
+            for (int i = 0; i < n; ++i) {
+                batch.range(i, p0, p1);
+                if (p1 - p0 > kRingRow) {
+                    const int r = (int)b + i;
+                    long_row<TWO, GRAD, DIN, OUT, kWarps>(a, r, TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f, p0, p1,
+                                                          sh);
                 }
-                ++n;
-                end = max(next, end);
             }
         }
-        if (n == 0) {  // a long row
-            ++r;
-            continue;
-        }
-        if (begin < end) st.need(begin, end);
-        if (member < n) {
-            const int row = r + member;
-            if (TWO && row >= block_end) {
-                const int block = row / a.seg_rows;
+        float lam = 0.f;
+        long long block_end = 0;  // lam is the head's of the rows before this one
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            const int r = (int)b + i;
+            batch.range(i, p0, p1);
+            if (p0 == p1) {
+                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
+                continue;
+            }
+            if (p1 - p0 > kRingRow) continue;
+            if (TWO && r >= block_end) {
+                const int block = r / a.seg_rows;
                 block_end = (block + 1LL) * a.seg_rows;
                 lam = __ldg(a.lambda + block % a.heads);
             }
-            if (p0 < p1)
-                ring_row<TWO, GRAD, DIN, OUT>(a, st, row, lam, p0, p1, vec);
-            else if (GRAD && TWO && a.row_c2 && lane == 0)
-                a.row_c2[row] = 0.f;
+            st.need(p0, p1);
+            if (p1 - p0 <= 128 * kRowSteps)
+                ring_row<TWO, GRAD, DIN, OUT, true>(a, st, r, lam, p0, p1, vec);
+            else
+                wide_row<TWO, GRAD, DIN, OUT>(a, st, r, lam, p0, p1, vec);
         }
-        r += n;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
+        __syncthreads();  // the next batch's offsets overwrite this one's
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
 }
 
 // A cluster per row.
@@ -633,15 +666,18 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
                                                                                                    : USM_ERR_CUDA;
     }
-    // Groups: as many as there is room for their rings, with at least 256 entries each.
+    // As many CTAs as there is room for their rings, of at least 8 rows or 2048
+    // entries each.
     using S = MapStream<TWO, GRAD, DIN>;
-    constexpr int smem = kGroups * S::kBytes;
-    const int most = sms * ctas_per_sm<S>() * kGroups, G = a.nnz / 256 < most ? (a.nnz / 256 > 0 ? a.nnz / 256 : 1) : most;
+    constexpr int smem = kWarps * S::kBytes;
+    const long long most = (long long)sms * ctas_per_sm<S>(), some = a.nnz / 2048 > a.M / 8 ? a.nnz / 2048 : a.M / 8;
+    long long ctas = some < 1 ? 1 : some < most ? some : most;
+    if (ctas > a.M) ctas = a.M;
     const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
     const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
     const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
     if (!allow_shared(kernel, smem)) return USM_ERR_CUDA;
-    kernel<<<(G + kGroups - 1) / kGroups, kThreads, smem, stream>>>(a, G, aligned, vec);
+    kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(a, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
