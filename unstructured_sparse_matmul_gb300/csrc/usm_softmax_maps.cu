@@ -8,11 +8,12 @@
 // Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
 // streams its rows through a ring of its own in shared memory (usm_stream.cuh), so
 // copies are in flight all the time whatever the rows' arithmetic and lengths do.
-// A row of up to 512 entries goes from the ring to registers once (four entries a
-// lane at a time, in pairs of fp32); one of up to 1536 is walked three times in
-// the ring (maximum; weights, their sums, written back in place; results).  Longer
-// rows are first taken by the whole CTA; where rows are long and few, a cluster of
-// up to 8 CTAs takes each (launch_rows).
+// A row of up to 640 entries goes from the ring to registers once (four entries a
+// lane at a time, in pairs of fp32); one of up to 896 is walked three times in the
+// ring (maximum; weights, their sums, written back in place; results); a longer
+// one passes through the ring twice, over 4096 entries with a part of it for each
+// of the CTA's warps.  Where rows are long and few, a cluster of up to 8 CTAs takes
+// each (launch_rows).
 #include <cmath>
 
 #include "usm_cluster.cuh"
@@ -23,7 +24,8 @@ namespace usm {
 namespace {
 
 constexpr int kSteps = 16;    // entries of a long row a thread keeps in registers
-constexpr int kRowSteps = 4;  // quads of a short row a lane does
+constexpr int kRowSteps = 5;  // quads of a short row a lane does
+constexpr int kLong = 4096;   // entries above which the CTA takes a row
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -297,10 +299,146 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
 }
 
 
-// Out of line in the kernel below: long rows are rare there.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, int WARPS>
-__device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0, int p1, BlockStats<WARPS>& sh) {
-    block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, 1, 0);
+// Entries [p0, p1) of a row, or of this warp's part of one (CTA: every warp has a
+// part, empty ones too), streamed twice: for the maximum and sums, which the lanes
+// keep relative to maxima of their own, and for the results.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool CTA, int WARPS, class S>
+__device__ __noinline__ void stream_row(const MapArgs& a, S& st, int r, float lam, int p0, int p1, bool vec,
+                                        BlockStats<WARPS>& sh) {
+    constexpr int MAPS = TWO ? 2 : 1, kPiece = 512;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int limit = st.limit;
+    st.limit = max(limit, (int)(((long long)p1 + kChunk - 1) / kChunk));
+    // Pieces end on whole quads, so only the first and the last have edges.
+    auto pieces = [&](auto entry, auto quad) {
+        for (long long b0 = p0; b0 < p1; b0 = (b0 & ~3LL) + kPiece) {
+            const int b1 = (int)min((long long)p1, (b0 & ~3LL) + kPiece);
+            st.need((int)b0, b1);
+            const RowQuads rq((unsigned)b0, (unsigned)b1, lane);
+            if (rq.has_edge) entry(rq.edge);
+#pragma unroll 1
+            for (unsigned q = rq.qs + 4 * lane; q < rq.qe; q += 128) quad(q);
+        }
+    };
+    Stat run[MAPS];
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
+    auto take = [&](int k, float top, auto add) {
+        top = fmaxf(top, run[k].m);
+        const float base = top == -INFINITY ? 0.f : top, f = __expf(run[k].m - base);
+        run[k].z *= f;
+        run[k].c *= f;
+        run[k].m = top;
+        add(base);
+    };
+    pieces(
+        [&](unsigned e) {
+            const float d = GRAD ? lds_entry<DIN>(st.at(MAPS, e)) : 0.f;
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                const float x = lds_f32(st.at(k, e));
+                take(k, x, [&](float base) {
+                    const float w = __expf(x - base);
+                    run[k].z += w;
+                    if constexpr (GRAD) run[k].c += weighted(w, d);
+                });
+            }
+        },
+        [&](unsigned q) {
+            float2 d0, d1;
+            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                float2 lo, hi;
+                lds_quad<false>(st.at(k, q), lo, hi);
+                take(k, fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)), [&](float base) {
+                    const float w0 = __expf(lo.x - base), w1 = __expf(lo.y - base), w2 = __expf(hi.x - base),
+                                w3 = __expf(hi.y - base);
+                    run[k].z += (w0 + w1) + (w2 + w3);
+                    if constexpr (GRAD)
+                        run[k].c += (weighted(w0, d0.x) + weighted(w1, d0.y)) + (weighted(w2, d1.x) + weighted(w3, d1.y));
+                });
+            }
+        });
+    float m[MAPS], z[MAPS], c[MAPS], inv[MAPS];
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        m[k] = warp_max(run[k].m);
+        if (CTA && lane == 0) sh.top[k][warp] = m[k];
+    }
+    if constexpr (CTA) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k)
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        const float f = run[k].m == -INFINITY ? 0.f : __expf(run[k].m - m[k]);
+        z[k] = warp_sum(run[k].z * f);
+        c[k] = GRAD ? warp_sum(weighted(f, run[k].c)) : 0.f;
+        if (CTA && lane == 0) {
+            sh.sum[k][0][warp] = z[k];
+            sh.sum[k][1][warp] = c[k];
+        }
+    }
+    if constexpr (CTA) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            z[k] = c[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                z[k] += sh.sum[k][0][w];
+                c[k] += sh.sum[k][1][w];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        inv[k] = inverse(z[k]);
+        c[k] *= inv[k];
+    }
+    if (GRAD && TWO && a.row_c2 && lane == 0 && (!CTA || warp == 0)) a.row_c2[r] = c[MAPS - 1];
+    if constexpr (TWO) inv[1] *= -lam;
+    auto grad = [&](int k, float x, float d) {
+        const float w = weight_of(x, Base(m[k]));
+        return weighted(w, fmaf(inv[k], d, -inv[k] * c[k]));
+    };
+    auto map = [&](float x1, float x2) {
+        const float w1 = weight_of(x1, Base(m[0])) * inv[0];
+        return TWO ? fmaf(weight_of(x2, Base(m[MAPS - 1])), inv[MAPS - 1], w1) : w1;
+    };
+    if (p0 < p1) st.seek(p0);
+    pieces(
+        [&](unsigned e) {
+            if constexpr (GRAD) {
+                const float d = lds_entry<DIN>(st.at(MAPS, e));
+                store_entry<OUT>(a.out1, e, grad(0, lds_f32(st.at(0, e)), d));
+                if constexpr (TWO) store_entry<OUT>(a.out2, e, grad(1, lds_f32(st.at(1, e)), d));
+            } else {
+                store_entry<OUT>(a.out1, e, map(lds_f32(st.at(0, e)), lds_f32(st.at(MAPS - 1, e))));
+            }
+        },
+        [&](unsigned q) {
+            float2 lo[MAPS], hi[MAPS];
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
+            if constexpr (GRAD) {
+                float2 d0, d1;
+                lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+#pragma unroll
+                for (int k = 0; k < MAPS; ++k)
+                    store_quad<OUT>(k == 0 ? a.out1 : a.out2, q, make_float2(grad(k, lo[k].x, d0.x), grad(k, lo[k].y, d0.y)),
+                                    make_float2(grad(k, hi[k].x, d1.x), grad(k, hi[k].y, d1.y)), vec);
+            } else {
+                constexpr int L = MAPS - 1;
+                store_quad<OUT>(a.out1, q, make_float2(map(lo[0].x, lo[L].x), map(lo[0].y, lo[L].y)),
+                                make_float2(map(hi[0].x, hi[L].x), map(hi[0].y, hi[L].y)), vec);
+            }
+        });
+    st.limit = limit;
 }
 
 // A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring.
@@ -404,7 +542,7 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
     } else {
 #pragma unroll 2
         for (unsigned q = first; q < rq.qe; q += 128) {
-            float2 d0, d1;
+            float2 d0 = make_float2(0.f, 0.f), d1 = d0;
             if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
@@ -510,7 +648,7 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
     } else {
 #pragma unroll 2
         for (unsigned q = first; q < rq.qe; q += 128) {
-            float2 lo[MAPS], hi[MAPS], d0, d1;
+            float2 lo[MAPS], hi[MAPS], d0 = make_float2(0.f, 0.f), d1 = d0;
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
             if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
@@ -527,7 +665,8 @@ using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? 
 // CTAs an SM that the rings leave room for.
 template <class S>
 constexpr int ctas_per_sm() {
-    return 226 * 1024 / (kWarps * S::kBytes + 4096);
+    constexpr int n = 226 * 1024 / (kWarps * S::kBytes + 4096);
+    return n > 6 ? 6 : n;  // 80 registers a thread
 }
 
 // The rows of a walk in the ring, out of line: most rows are shorter.
@@ -559,24 +698,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
     st.whole = aligned ? a.nnz / kChunk : 0;
     for (long long b = first; b < last; b += kBatch) {
         const int n = (int)min((long long)kBatch, last - b);
-        const bool any_long = batch.load(a.row_offsets, a.nnz, (int)b, n, kRingRow);
+        const bool any_long = batch.load(a.row_offsets, a.nnz, (int)b, n, kLong);
         const int i0 = warp == 0 ? 0 : batch.first_from(n, batch.part(n, warp, kWarps), lane);
         const int i1 = warp == kWarps - 1 ? n : batch.first_from(n, batch.part(n, warp + 1, kWarps), lane);
         int p0, p1;
-        if (i0 < i1) {
-            st.limit = (int)(((long long)batch.offset[i1] + kChunk - 1) / kChunk);
-            st.seek(batch.offset[i0]);
-        }
-        if (any_long) {  // by the CTA, while the rings fill
+        st.issued = st.limit = 0;
+        if (any_long) {
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 batch.range(i, p0, p1);
-                if (p1 - p0 > kRingRow) {
-                    const int r = (int)b + i;
-                    long_row<TWO, GRAD, DIN, OUT, kWarps>(a, r, TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f, p0, p1,
-                                                          sh);
+                if (p1 - p0 <= kLong) continue;
+                const int r = (int)b + i;
+                const long long len = p1 - p0;
+                const int b0 = p0 + (int)(len * warp / kWarps), b1 = p0 + (int)(len * (warp + 1) / kWarps);
+                if (b0 < b1) {
+                    st.limit = (int)(((long long)b1 + kChunk - 1) / kChunk);
+                    st.seek(b0);
                 }
+                stream_row<TWO, GRAD, DIN, OUT, true>(a, st, r, TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f, b0,
+                                                      b1, vec, sh);
             }
+        }
+        if (i0 < i1) {
+            st.limit = (int)(((long long)batch.offset[i1] + kChunk - 1) / kChunk);
+            st.seek(batch.offset[i0]);
         }
         float lam = 0.f;
         long long block_end = 0;  // lam is the head's of the rows before this one
@@ -588,11 +733,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
                 if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
                 continue;
             }
-            if (p1 - p0 > kRingRow) continue;
+            if (p1 - p0 > kLong) continue;
             if (TWO && r >= block_end) {
                 const int block = r / a.seg_rows;
                 block_end = (block + 1LL) * a.seg_rows;
                 lam = __ldg(a.lambda + block % a.heads);
+            }
+            if (p1 - p0 > kRingRow) {
+                stream_row<TWO, GRAD, DIN, OUT, false>(a, st, r, lam, p0, p1, vec, sh);
+                continue;
             }
             st.need(p0, p1);
             if (p1 - p0 <= 128 * kRowSteps)
@@ -600,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
             else
                 wide_row<TWO, GRAD, DIN, OUT>(a, st, r, lam, p0, p1, vec);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the next batch's offsets overwrite this one's
     }
 }
@@ -650,7 +799,7 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
     // A CTA of 8 warps a row where rows are long and too few to fill the GPU with
     // a warp each; a cluster while its CTAs are too few too and keep at least
     // half their registers' worth each.
-    if (mean > kRingRow && a.M <= 4 * sms) {
+    if (mean > 1536 && a.M <= 4 * sms) {
         int ctas = 1;
         while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kClusterWarps * 32 * kSteps / 2) ctas *= 2;
         cudaLaunchAttribute attr;

@@ -13,9 +13,9 @@
 
 namespace usm {
 
-constexpr int kChunk = 512, kRing = 4 * kChunk;
+constexpr int kChunk = 128, kRing = 8 * kChunk;
 // A run up to this long fits the ring wherever it starts.
-constexpr int kRingRow = 3 * kChunk;
+constexpr int kRingRow = 7 * kChunk;
 
 // Streams up to three arrays of E0, E1, E2 bytes an element (0: none).
 template <int E0, int E1, int E2>
@@ -43,7 +43,8 @@ struct Stream {
             const uint32_t p0 = (uint32_t)chunk * kChunk + lane * PER, to = at(array, p0);
             const unsigned char* from = src[array] + (unsigned long long)p0 * E;
 #pragma unroll
-            for (int i = 0; i < kChunk / PER / 32; ++i) {
+            for (int i = 0; i < (kChunk / PER + 31) / 32; ++i) {
+                if (kChunk / PER < 32 && lane >= kChunk / PER) break;
                 if constexpr (!EDGE) {
                     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
                                  : "memory");
@@ -107,15 +108,16 @@ struct Stream {
             do issue();
             while (c0 + kRing / kChunk > issued);
         }
-        const int left = issued - 1 - (p1 - 1) / kChunk;
-        if (left == 0)
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else if (left == 1)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else if (left == 2)
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 3;" ::: "memory");
+        switch (issued - 1 - (p1 - 1) / kChunk) {  // chunks that may stay in flight
+            case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+            case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+            case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+            case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+            case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+            case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+            case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+            default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+        }
         __syncwarp();
     }
 };
