@@ -33,7 +33,6 @@
 #include "usm_cluster.cuh"
 #include "usm_internal.h"
 #include "usm_rel.cuh"
-#include "usm_stream.cuh"
 
 namespace usm {
 namespace {

@@ -118,6 +118,15 @@ inline int effective_seg(int M, int seg_rows) { return (seg_rows <= 0 || seg_row
 
 int launch_wait_timeout_selftest(long long limit_ns, int* status, cudaStream_t stream);
 
+// Lets a kernel have `smem` bytes a CTA, and the SM all the shared memory there is
+// (the driver's own split may leave room for fewer CTAs than fit).
+template <class Kernel>
+inline bool allow_shared(Kernel kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+               cudaSuccess;
+}
+
 // Launch shape forced by usm_set_schedule_override (0: the library's choice).
 struct ScheduleOverride {
     int rows_per_warp, tiles_per_block, k_splits;

@@ -27,14 +27,16 @@ __device__ __forceinline__ int rel_bucket(const RelArgs& b, int entry) {
     return min(max(__ldg(b.map + entry), 0), b.buckets - 1);
 }
 
+// Entry `bucket` of a head's row of the table.
 template <bool BF>
-__device__ __forceinline__ float rel_table(const RelArgs& b, int head, int bucket) {
-    const long long i = (long long)head * b.buckets + bucket;
-    if constexpr (BF) return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(b.table) + i) << 16);
-    return __ldg(static_cast<const float*>(b.table) + i);
+__device__ __forceinline__ float rel_table_entry(const void* row, int bucket) {
+    if constexpr (BF)
+        return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(row) + bucket) << 16);
+    return __ldg(static_cast<const float*>(row) + bucket);
 }
 __device__ __forceinline__ float rel_table(const RelArgs& b, int head, int bucket) {
-    return b.table_bf16 ? rel_table<true>(b, head, bucket) : rel_table<false>(b, head, bucket);
+    const char* row = static_cast<const char*>(b.table) + (long long)head * b.buckets * (b.table_bf16 ? 2 : 4);
+    return b.table_bf16 ? rel_table_entry<true>(row, bucket) : rel_table_entry<false>(row, bucket);
 }
 
 // Entries [s, e) of row r, clamped into [0, nnz) whatever row_offsets holds.

@@ -4,9 +4,7 @@
 // bucket(p) = map[reach + clamp(d, ±reach)], d the key's position less the
 // query's.
 #include "usm_internal.h"
-#include "usm_quads.cuh"
 #include "usm_rel.cuh"
-#include "usm_rows.cuh"
 
 namespace usm {
 namespace {
@@ -26,14 +24,40 @@ __global__ void rel_bucket_kernel(int num_buckets, int reach, int causal, int* _
     map[i] = k + (!causal && d > 0 ? b : 0);
 }
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kQuads = 4;         // quads a lane has in flight
-constexpr unsigned kLong = 2048;  // entries above which a CTA takes a row
+constexpr int kThreads = 256;
+constexpr int kSteps = 4;             // quads of entries a lane has in flight
+constexpr int kTile = kSteps * 128;   // entries of a warp's tile
 
-// Columns of quad q (those past the array's end read as 0).
-template <bool VEC>
-__device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigned q, unsigned nnz, int (&c)[4]) {
-    if (VEC && q + 4 <= nnz) {
+// Four entries from q on (one by one where the array does not start on a quad or
+// ends inside it).  Plain loads: the same kernel may write the array in place.
+template <bool BF>
+__device__ __forceinline__ float load_value(const void* p, unsigned i) {
+    if constexpr (BF) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+    return static_cast<const float*>(p)[i];
+}
+template <bool BF>
+__device__ __forceinline__ void load_values(const void* p, unsigned q, unsigned nnz, bool vec, float (&x)[4]) {
+    if (vec && q + 4 <= nnz) {
+        if constexpr (BF) {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + q);
+            x[0] = __uint_as_float(w.x << 16);
+            x[1] = __uint_as_float(w.x & 0xffff0000u);
+            x[2] = __uint_as_float(w.y << 16);
+            x[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+            const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + q);
+            x[0] = w.x;
+            x[1] = w.y;
+            x[2] = w.z;
+            x[3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = q + u < nnz ? load_value<BF>(p, q + u) : 0.f;
+    }
+}
+__device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigned q, unsigned nnz, bool vec, int (&c)[4]) {
+    if (vec && q + 4 <= nnz) {
         const int4 w = __ldg(reinterpret_cast<const int4*>(ci + q));
         c[0] = w.x;
         c[1] = w.y;
@@ -45,178 +69,217 @@ __device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigne
     }
 }
 
-// Adds the bias to entries [p0, p1) of one row (head and start: the row's), by
-// threads t = 0..T-1.
-template <bool VEC, bool BT>
-__device__ __forceinline__ void bias_entries(const int* __restrict__ ci, unsigned nnz, const float* s, const RelArgs& b,
-                                             float* out, int head, int start, unsigned p0, unsigned p1, unsigned t,
-                                             unsigned T) {
-    const unsigned step = 4 * T;
-#pragma unroll 1
-    for (unsigned q0 = (p0 & ~3u) + 4 * t; q0 < p1; q0 += kQuads * step) {
-        int c[kQuads][4];
-        float x[kQuads][4];
+// The rows of a run of entries: lane i holds row `first + i`'s offset and what a
+// functor makes of the row (31 rows; lane 31 only ends the last).
+struct RowsHeld {
+    const int* ro;
+    int r1;  // rows before this one
+    int nnz, lane;
+    int first, offset;
+
+    __device__ __forceinline__ int load(int r) const {
+        return min(max(__ldg(ro + min((long long)r + lane, (long long)r1)), 0), nnz);
+    }
+    // Holds the row that entry p lies in, found among rows [r, r1) by 128 candidates
+    // a round.
+    __device__ __forceinline__ void find(unsigned p, int r) {
+        long long lo = r, n = (long long)r1 - r;
+        while (n > 31) {
+            const long long step = (n + 127) / 128;
+            int at[4], below = 0;
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-            const unsigned q = q0 + i * step;
-            if (q < p1) {
-                load_columns<VEC>(ci, q, nnz, c[i]);
-                load_quad<false, VEC>(s, q, nnz, x[i]);
+            for (int k = 0; k < 4; ++k) {
+                const long long i = (lane + 32 * k) * step;
+                at[k] = i < n ? __ldg(ro + lo + i) : 0x7fffffff;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) below += __popc(__ballot_sync(kFullMask, at[k] <= (long long)p));
+            const long long skip = max(below - 1, 0) * step;
+            lo += skip;
+            n = min(step, n - skip);
         }
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-            const unsigned q = q0 + i * step;
-            if (q < p1) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    x[i][u] += rel_table<BT>(b, head, rel_bucket(b, rel_entry(c[i][u], start, b.reach)));
-                store_quad<false, VEC>(out, q, p0, p1, x[i]);
+        first = (int)lo;
+        offset = load(first);
+    }
+    // Calls f(lane that holds the row, begin, end) for each row's part of entries
+    // [p, end), which come after what was asked for before.  fresh: other rows are
+    // held than made(row, whether it has entries) was last called for.
+    template <class Made, class F>
+    __device__ __forceinline__ void segments(unsigned p, unsigned end, bool& fresh, Made made, F f) {
+        while (true) {
+            const unsigned next = __shfl_down_sync(kFullMask, offset, 1);
+            const bool row = lane < min(31, r1 - first);
+            if (fresh) made(first + lane, row && next > (unsigned)offset);
+            fresh = false;
+            unsigned left = __ballot_sync(kFullMask, row && next > max((unsigned)offset, p) && (unsigned)offset < end);
+            for (; left; left &= left - 1) {
+                const int i = __ffs(left) - 1;
+                f(i, max((unsigned)__shfl_sync(kFullMask, offset, i), p), min(__shfl_sync(kFullMask, next, i), end));
             }
+            const unsigned held = __shfl_sync(kFullMask, offset, 31);
+            if (held >= end || r1 - first <= 31) return;
+            p = max(p, held);
+            first += 31;
+            offset = load(first);
+            fresh = true;
+            if ((unsigned)__shfl_sync(kFullMask, offset, 31) <= p && r1 - first > 31) find(p, first);  // rows without entries
         }
     }
-}
+};
 
-// Bound by memory: 8 bytes a nonzero in, 4 out.  Quads of entries with 16-byte
-// accesses, four in flight a lane; the map and the head's row of the table are a
-// few hundred bytes that stay in L1.  CTA b of B takes rows [M·b / B, M·(b+1) / B),
-// 64 at a time: long ones by the whole CTA, then each warp fetches row after row.
-template <bool VEC, bool BT>
+// Where column col's distance lies in the map: before or at its start (entry 0:
+// every key further back), at its end or after (the last entry), or between.
+struct Distance {
+    bool back, between;
+    unsigned entry;
+    __device__ __forceinline__ Distance(int col, int start, unsigned last) {
+        entry = (unsigned)col - (unsigned)start;
+        back = col <= start;
+        between = !back && entry < last;
+    }
+};
+
+// Bound by memory: 8 bytes a nonzero in, 4 out.  A warp takes a tile of entries,
+// whatever rows they are in: its loads go out first, and the search for the
+// tile's rows runs while they are in flight.  Each row's part of the tile then
+// gets its bias: most keys are further away than the map reaches, and those have
+// one of two values that the row's lane holds; only the others look up the map
+// and the table.
+template <bool BT>
 __global__ void __launch_bounds__(kThreads) rel_bias_kernel(int M, int nnz, const int* __restrict__ ro,
                                                             const int* __restrict__ ci, const float* s, const RelArgs b,
-                                                            float* out) {
-    __shared__ RowRun run;
-    __shared__ int heads[kRun], starts[kRun];
+                                                            float* out, bool vec) {
     const int lane = threadIdx.x & 31;
-    const long long r0 = (long long)M * blockIdx.x / gridDim.x, r1 = (long long)M * (blockIdx.x + 1) / gridDim.x;
-    for (long long r = r0; r < r1; r += kRun) {
-        const int n = (int)min((long long)kRun, r1 - r);
-        const bool any_long = run.load(ro, nnz, n, kLong, [&](int i) { return (int)r + i; },
-                                       [&](int i, int row) {
-                                           const int block = row / b.seg_rows;
-                                           heads[i] = block % b.heads;
-                                           if (run.begin[i] < run.end[i])
-                                               starts[i] = rel_start(b, block, row - block * b.seg_rows, __ldg(ci + run.begin[i]));
-                                       });
-        if (any_long) {
-#pragma unroll 1
-            for (int i = 0; i < n; ++i)
-                if ((unsigned)(run.end[i] - run.begin[i]) > kLong)
-                    bias_entries<VEC, BT>(ci, nnz, s, b, out, heads[i], starts[i], run.begin[i], run.end[i], threadIdx.x, kThreads);
-        }
-        for (int i = run.fetch(lane); i < n; i = run.fetch(lane))
-            if ((unsigned)(run.end[i] - run.begin[i]) <= kLong)
-                bias_entries<VEC, BT>(ci, nnz, s, b, out, heads[i], starts[i], run.begin[i], run.end[i], lane, 32);
-        __syncthreads();  // the next run's rows overwrite this one's
+    const unsigned tile = (blockIdx.x * (unsigned)(kThreads / 32) + (threadIdx.x >> 5)) * (unsigned)kTile;
+    if (tile >= (unsigned)nnz) return;
+    int c[kSteps][4];
+    float x[kSteps][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        load_columns(ci, tile + 128 * i + 4 * lane, nnz, vec, c[i]);
+        load_values<false>(s, tile + 128 * i + 4 * lane, nnz, vec, x[i]);
     }
-}
-
-// Piece y of gridDim.y of row x's quads.
-__device__ __forceinline__ void piece_range(unsigned p0, unsigned p1, int piece, int pieces, unsigned& b0, unsigned& b1) {
-    const unsigned f = p0 & ~3u, quads = (p1 - f + 3) / 4;
-    b0 = max(p0, f + 4 * (unsigned)((unsigned long long)quads * piece / pieces));
-    b1 = min(p1, f + 4 * (unsigned)((unsigned long long)quads * (piece + 1) / pieces));
-}
-
-// Few long rows: CTA (x, y) takes piece y of row x.
-template <bool VEC, bool BT>
-__global__ void __launch_bounds__(kThreads) rel_bias_pieces_kernel(int nnz, const int* __restrict__ ro,
-                                                                   const int* __restrict__ ci, const float* s,
-                                                                   const RelArgs b, float* out) {
-    const int r = blockIdx.x, block = r / b.seg_rows;
-    int p0, p1;
-    row_range(ro, r, nnz, p0, p1);
-    if (p0 == p1) return;
-    unsigned b0, b1;
-    piece_range(p0, p1, blockIdx.y, gridDim.y, b0, b1);
-    const int start = rel_start(b, block, r - block * b.seg_rows, __ldg(ci + p0));
-    bias_entries<VEC, BT>(ci, nnz, s, b, out, block % b.heads, start, b0, b1, threadIdx.x, kThreads);
-}
-
-// CTA (h, j) takes part j of J of head h's rows (or of their pieces, where there
-// are few long rows).  Every thread sums its entries into its own column of a
-// histogram in shared memory ([bucket][thread]: no bank conflicts, no atomics),
-// and the columns are added in a fixed order: which thread takes which entry is
-// fixed too.  A thread holds the sum of its latest bucket in a register and
-// writes it back when the bucket changes: far keys share a bucket, so most of a
-// row is a few runs.  Bound by memory: 8 (or 6) bytes a nonzero.
-template <bool BF, bool VEC>
-__global__ void __launch_bounds__(kThreads) rel_bias_grad_kernel(int M, int nnz, const int* __restrict__ ro,
-                                                                 const int* __restrict__ ci, const void* __restrict__ ds,
-                                                                 const RelArgs b, int blocks, int pieces, int J,
-                                                                 float* __restrict__ part) {
-    extern __shared__ float hist[];
-    __shared__ RowRun run;
-    __shared__ int starts[kRun];
-    const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = T >> 5;
-    for (int k = 0; k < b.buckets; ++k) hist[k * T + t] = 0.f;
-    const int head = blockIdx.x / J, j = blockIdx.x % J;
-    const long long rows = head < blocks ? (long long)((blocks - 1 - head) / b.heads + 1) * b.seg_rows : 0;
-    const long long items = rows * pieces, i0 = items * j / J, i1 = items * (j + 1) / J;
-    int bucket = 0;
-    float sum = 0.f;
-    auto entries = [&](int start, unsigned p0, unsigned p1, unsigned at, unsigned threads) {
-        const unsigned step = 4 * threads;
-#pragma unroll 1
-        for (unsigned q0 = (p0 & ~3u) + 4 * at; q0 < p1; q0 += kQuads * step) {
-            int c[kQuads][4];
-            float x[kQuads][4];
+    const unsigned all0 = min(max(__ldg(ro), 0), nnz), all1 = min(max(__ldg(ro + M), 0), nnz);
+    const unsigned p0 = max(tile, all0), p1 = min(tile + kTile, all1);
+    if (p0 >= p1) return;
+    RowsHeld rows{ro, M, nnz, lane, 0, 0};
+    rows.find(p0, 0);
+    const unsigned last = 2u * (unsigned)b.reach;
+    const int bucket0 = rel_bucket(b, 0), bucket1 = rel_bucket(b, (int)last);
+    int start = 0, head = 0;
+    float back = 0.f, ahead = 0.f;
+    bool fresh = true;
+    rows.segments(
+        p0, p1, fresh,
+        [&](int r, bool some) {
+            if (!some) return;
+            const int block = r / b.seg_rows;
+            head = block % b.heads;
+            start = rel_start(b, block, r - block * b.seg_rows, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
+            const char* table = static_cast<const char*>(b.table) + (long long)head * b.buckets * (BT ? 2 : 4);
+            back = rel_table_entry<BT>(table, bucket0);
+            ahead = rel_table_entry<BT>(table, bucket1);
+        },
+        [&](int i, unsigned s0, unsigned s1) {
+            const int from = __shfl_sync(kFullMask, start, i);
+            const float far0 = __shfl_sync(kFullMask, back, i), far1 = __shfl_sync(kFullMask, ahead, i);
+            const char* table = static_cast<const char*>(b.table) +
+                                (long long)__shfl_sync(kFullMask, head, i) * b.buckets * (BT ? 2 : 4);
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                const unsigned q = q0 + i * step;
-                if (q < p1) {
-                    load_columns<VEC>(ci, q, nnz, c[i]);
-                    load_quad<BF, VEC>(ds, q, nnz, x[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                const unsigned q = q0 + i * step;
-                if (q >= p1) break;
+            for (int k = 0; k < kSteps; ++k) {
+                const unsigned g = tile + 128 * k, q = g + 4 * lane;
+                if (g + 128 <= s0 || g >= s1) continue;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int k = rel_bucket(b, rel_entry(c[i][u], start, b.reach));
-                    if (q + u < p0 || q + u >= p1) continue;
-                    if (k != bucket) {
-                        hist[bucket * T + t] += sum;
-                        bucket = k;
-                        sum = 0.f;
-                    }
-                    sum += x[i][u];
+                    const Distance d(c[k][u], from, last);
+                    float v = d.back ? far0 : far1;
+                    if (d.between) v = rel_table_entry<BT>(table, rel_bucket(b, (int)d.entry));
+                    if (q + u - s0 < s1 - s0) x[k][u] += v;
                 }
             }
+        });
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const unsigned q = tile + 128 * i + 4 * lane;
+        if (vec && q >= p0 && q + 4 <= p1) {
+            *reinterpret_cast<float4*>(out + q) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (q + u >= p0 && q + u < p1) out[q + u] = x[i][u];
         }
-    };
-    for (long long f = i0; f < i1; f += kRun) {
-        const int n = (int)min((long long)kRun, i1 - f);
-        const bool any_long = run.load(
-            ro, nnz, n, kLong,
-            [&](int i) {  // item -> row of the head's blocks (the last block may be shorter)
-                const long long row = (f + i) / pieces;
-                const long long r = (head + row / b.seg_rows * b.heads) * b.seg_rows + row % b.seg_rows;
-                return r < M ? (int)r : -1;
-            },
-            [&](int i, int r) {
-                const int block = r / b.seg_rows, p0 = run.begin[i], p1 = run.end[i];
-                if (p0 == p1) return;
-                starts[i] = rel_start(b, block, r - block * b.seg_rows, __ldg(ci + p0));
-                if (pieces > 1) {
-                    unsigned b0, b1;
-                    piece_range(p0, p1, (int)((f + i) % pieces), pieces, b0, b1);
-                    run.begin[i] = b0;
-                    run.end[i] = max(b0, b1);
-                }
-            });
-        if (any_long) {
-#pragma unroll 1
-            for (int i = 0; i < n; ++i)
-                if ((unsigned)(run.end[i] - run.begin[i]) > kLong) entries(starts[i], run.begin[i], run.end[i], t, T);
-        }
-        for (int i = warp; i < n; i += warps)
-            if ((unsigned)(run.end[i] - run.begin[i]) <= kLong) entries(starts[i], run.begin[i], run.end[i], lane, 32);
-        __syncthreads();  // the next run's rows overwrite this one's
     }
-    hist[bucket * T + t] += sum;
+}
+
+// Head h's entries lie in runs, one a query block; each is cut into Y parts at
+// quads, and warp w of the W that CTAs (h, 0) .. (h, J - 1) have takes its equal
+// share of the parts.  Every thread sums its entries into its own column of a
+// histogram in shared memory ([bucket][thread]: no bank conflicts, no atomics),
+// those further away than the map reaches into two registers, and the columns are
+// added in a fixed order: which thread takes which entry is fixed too.  Bound by
+// memory: 8 (or 6) bytes a nonzero.
+template <bool BF>
+__global__ void __launch_bounds__(kThreads, 3) rel_bias_grad_kernel(int M, int nnz, const int* __restrict__ ro,
+                                                                 const int* __restrict__ ci, const void* __restrict__ ds,
+                                                                 const RelArgs b, int blocks, int Y, int J,
+                                                                 float* __restrict__ part, bool vec) {
+    extern __shared__ float hist[];
+    const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = T >> 5;
+    for (int k = 0; k < b.buckets; ++k) hist[k * T + t] = 0.f;
+    const int head = blockIdx.x / J;
+    const long long W = (long long)J * warps, w = (long long)(blockIdx.x % J) * warps + warp;
+    const long long parts = head < blocks ? ((blocks - 1 - head) / b.heads + 1LL) * Y : 0;
+    const unsigned last = 2u * (unsigned)b.reach;
+    float back = 0.f, ahead = 0.f;
+#pragma unroll 1
+    for (long long i = parts * w / W; i < parts * (w + 1) / W; ++i) {
+        const int block = (int)(head + i / Y * b.heads), y = (int)(i % Y), r0 = block * b.seg_rows;
+        const int r1 = (int)min((long long)M, (long long)r0 + b.seg_rows);
+        const unsigned e0 = min(max(__ldg(ro + r0), 0), nnz), e1 = min(max(__ldg(ro + r1), 0), nnz);
+        if (e0 >= e1) continue;
+        const unsigned f = e0 & ~3u, quads = (e1 - f + 3) / 4;
+        const unsigned p0 = max(e0, f + 4 * (unsigned)((unsigned long long)quads * y / Y));
+        const unsigned p1 = min(e1, f + 4 * (unsigned)((unsigned long long)quads * (y + 1) / Y));
+        if (p0 >= p1) continue;
+        RowsHeld rows{ro, r1, nnz, lane, 0, 0};
+        int start = 0;
+        bool found = false, fresh = true;
+#pragma unroll 1
+        for (unsigned tile = p0 & ~3u; tile < p1; tile += kTile) {
+            int c[kSteps][4];
+            float x[kSteps][4];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                load_columns(ci, tile + 128 * k + 4 * lane, p1, vec, c[k]);
+                load_values<BF>(ds, tile + 128 * k + 4 * lane, p1, vec, x[k]);
+            }
+            if (!found) rows.find(p0, r0);
+            found = true;
+            rows.segments(
+                max(tile, p0), min(tile + kTile, p1), fresh,
+                [&](int r, bool some) {
+                    if (some) start = rel_start(b, block, r - r0, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
+                },
+                [&](int i, unsigned s0, unsigned s1) {
+                    const int from = __shfl_sync(kFullMask, start, i);
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const unsigned g = tile + 128 * k, q = g + 4 * lane;
+                        if (g + 128 <= s0 || g >= s1) continue;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const Distance d(c[k][u], from, last);
+                            const float v = q + u - s0 < s1 - s0 ? x[k][u] : 0.f;
+                            back += d.back ? v : 0.f;
+                            ahead += d.back || d.between ? 0.f : v;
+                            if (d.between && v != 0.f) hist[rel_bucket(b, (int)d.entry) * T + t] += v;
+                        }
+                    }
+                });
+        }
+    }
+    hist[rel_bucket(b, 0) * T + t] += back;
+    hist[rel_bucket(b, (int)last) * T + t] += ahead;
     __syncthreads();
     for (int k = warp; k < b.buckets; k += warps) {
         float x = 0.f;
@@ -241,25 +304,26 @@ __global__ void rel_bias_grad_sum_kernel(int heads, int buckets, int J, const fl
     if (lane == 0) dtable[i] = x;
 }
 
-// Pieces a row is cut into: more where the mean row would keep a CTA busy and
-// the rows are too few to fill the GPU.
-int row_pieces(int M, int nnz) {
-    int pieces = 1;
-    while (pieces < 64 && (long long)M * pieces < 2048 && nnz / M / pieces > 1024) pieces *= 2;
-    return pieces;
-}
-
 // Threads of a gradient CTA (its histogram is threads × buckets floats, 64 KB
-// at most) and parts each head's items are cut into.
+// at most).
 int grad_threads(int buckets) { return buckets <= 64 ? 256 : buckets <= 128 ? 128 : buckets <= 256 ? 64 : 32; }
 
-int grad_parts(int M, int nnz, int seg_rows, int heads, int buckets) {
-    const long long blocks = query_blocks(M, seg_rows);
-    const long long items = (blocks + heads - 1) / heads * seg_rows * row_pieces(M, nnz);  // of the first head, the longest
+// The gradient's split: CTAs a head, three an SM (of 152) in all or fewer where
+// their warps would have less than a tile of entries each, and parts a query
+// block, as many as give every warp one.
+struct GradSplit {
+    int Y, J;
+};
+GradSplit grad_split(int M, int nnz, int seg_rows, int heads, int buckets) {
     const int warps = grad_threads(buckets) / 32;
-    long long J = (912 + heads - 1) / heads;
-    if (J > (items + warps - 1) / warps) J = (items + warps - 1) / warps;
-    return (int)(J < 1 ? 1 : J);
+    const long long blocks = M > 0 ? (query_blocks(M, seg_rows) + heads - 1) / heads : 1;  // of the first head, the most
+    const long long most = (456 + heads - 1) / heads * (long long)warps, some = nnz / (heads * (long long)kTile) + 1;
+    const long long parts = most < some ? most : some;
+    GradSplit split;
+    split.Y = (int)((parts + blocks - 1) / blocks);
+    const long long all = blocks * split.Y, W = all < most ? all : most;
+    split.J = (int)((W + warps - 1) / warps);
+    return split;
 }
 
 }  // namespace
@@ -271,46 +335,42 @@ int launch_rel_bucket_build(int num_buckets, int max_distance, bool causal, int*
 }
 
 namespace {
-template <bool VEC, bool BT>
+bool quad_aligned(const void* p, bool bf16 = false) { return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 7u : 15u)) == 0; }
+
+template <bool BT>
 void launch_bias(int M, int nnz, const int* ro, const int* ci, const float* scores, const RelArgs& bias, float* out,
                  cudaStream_t stream) {
-    const int pieces = row_pieces(M, nnz);
-    if (pieces > 1) {
-        rel_bias_pieces_kernel<VEC, BT><<<dim3(M, pieces), kThreads, 0, stream>>>(nnz, ro, ci, scores, bias, out);
-        return;
-    }
-    const int slots = sm_count_current_device() * 4;
-    rel_bias_kernel<VEC, BT><<<M < slots ? M : slots, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, out);
+    const bool vec = quad_aligned(ci) && quad_aligned(scores) && quad_aligned(out);
+    const unsigned per_cta = kThreads / 32 * kTile;
+    rel_bias_kernel<BT><<<((unsigned)nnz + per_cta - 1) / per_cta, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, out, vec);
 }
 }  // namespace
 
 int launch_rel_bias(int M, int nnz, const int* ro, const int* ci, const float* scores, const RelArgs& bias, float* out,
                     cudaStream_t stream) {
-    const bool vec = quad_aligned(ci, false) && quad_aligned(scores, false) && quad_aligned(out, false);
-    auto call = [&](auto launch) { launch(M, nnz, ro, ci, scores, bias, out, stream); };
     if (bias.table_bf16)
-        vec ? call(launch_bias<true, true>) : call(launch_bias<false, true>);
+        launch_bias<true>(M, nnz, ro, ci, scores, bias, out, stream);
     else
-        vec ? call(launch_bias<true, false>) : call(launch_bias<false, false>);
+        launch_bias<false>(M, nnz, ro, ci, scores, bias, out, stream);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
 size_t rel_bias_grad_workspace_bytes(int M, int nnz, int seg_rows, int num_heads, int num_buckets) {
-    return (size_t)num_heads * grad_parts(M, nnz, seg_rows, num_heads, num_buckets) * num_buckets * 4;
+    return (size_t)num_heads * grad_split(M, nnz, seg_rows, num_heads, num_buckets).J * num_buckets * 4;
 }
 
 namespace {
-template <bool BF, bool VEC>
+template <bool BF>
 int launch_grad(int M, int nnz, const int* ro, const int* ci, const void* ds, const RelArgs& bias, float* dtable,
                 void* workspace, cudaStream_t stream) {
-    const int J = grad_parts(M, nnz, bias.seg_rows, bias.heads, bias.buckets), T = grad_threads(bias.buckets);
+    const auto [Y, J] = grad_split(M, nnz, bias.seg_rows, bias.heads, bias.buckets);
+    const int T = grad_threads(bias.buckets);
     const int smem = bias.buckets * T * 4;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(rel_bias_grad_kernel<BF, VEC>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return USM_ERR_CUDA;
+    if (!allow_shared(rel_bias_grad_kernel<BF>, smem)) return USM_ERR_CUDA;
     float* part = static_cast<float*>(workspace);
-    rel_bias_grad_kernel<BF, VEC><<<bias.heads * J, T, smem, stream>>>(
-        M, nnz, ro, ci, ds, bias, query_blocks(M, bias.seg_rows), row_pieces(M, nnz), J, part);
+    rel_bias_grad_kernel<BF><<<bias.heads * J, T, smem, stream>>>(
+        M, nnz, ro, ci, ds, bias, query_blocks(M, bias.seg_rows), Y, J, part,
+        quad_aligned(ci) && quad_aligned(ds, BF));
     const long long warps = (long long)bias.heads * bias.buckets;
     rel_bias_grad_sum_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(bias.heads, bias.buckets, J, part, dtable);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
@@ -319,10 +379,8 @@ int launch_grad(int M, int nnz, const int* ro, const int* ci, const void* ds, co
 
 int launch_rel_bias_grad(int M, int nnz, const int* ro, const int* ci, const void* dscores, bool bf16,
                          const RelArgs& bias, float* dtable, void* workspace, cudaStream_t stream) {
-    const bool vec = quad_aligned(ci, false) && quad_aligned(dscores, bf16);
-    auto call = [&](auto launch) { return launch(M, nnz, ro, ci, dscores, bias, dtable, workspace, stream); };
-    if (bf16) return vec ? call(launch_grad<true, true>) : call(launch_grad<true, false>);
-    return vec ? call(launch_grad<false, true>) : call(launch_grad<false, false>);
+    const auto launch = bf16 ? launch_grad<true> : launch_grad<false>;
+    return launch(M, nnz, ro, ci, dscores, bias, dtable, workspace, stream);
 }
 
 }  // namespace usm

@@ -5,15 +5,22 @@
 // Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
 // stored entries.
 //
-// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
-// streams its rows through a ring of its own in shared memory (usm_stream.cuh), so
-// copies are in flight all the time whatever the rows' arithmetic and lengths do.
-// A row of up to 640 entries goes from the ring to registers once (four entries a
-// lane at a time, in pairs of fp32); one of up to 896 is walked three times in the
-// ring (maximum; weights, their sums, written back in place; results); a longer
-// one passes through the ring twice, over 4096 entries with a part of it for each
-// of the CTA's warps.  Where rows are long and few, a cluster of up to 8 CTAs takes
-// each (launch_rows).
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  A warp or
+// two take the rows that begin in an equal share of the entries and stream them
+// through a ring in shared memory (usm_stream.cuh), so copies are in flight all
+// the time whatever the rows' arithmetic and lengths do.  An SM's shared memory
+// holds the rings of 12 to 16 warps, few to cover the latency of a row's
+// arithmetic, which is what is left to wait for:
+//   - A row is walked twice in the ring (weights and their sums; results), four
+//     entries a lane, in pairs of fp32 (f32x2).  Loops are short: rows read into
+//     registers, unrolled, measured 47 to 58 us where these take 42 (the
+//     differential map of 8x4096 rows of 410 entries).
+//   - The maximum is not looked for (45 us with it): exponents are measured from
+//     the largest of a row's first entries, which gives the same quotients unless
+//     a sum passes 2^100; a row whose sum does is done again from its maximum, as
+//     are rows with masks at their start or values that are not finite.
+//   - Rows over 1536 entries are first taken by the whole CTA; where rows are long
+//     and few, a cluster of up to 8 CTAs takes each (launch_rows).
 #include <cmath>
 
 #include "usm_cluster.cuh"
@@ -23,9 +30,7 @@
 namespace usm {
 namespace {
 
-constexpr int kSteps = 16;    // entries of a long row a thread keeps in registers
-constexpr int kRowSteps = 5;  // quads of a short row a lane does
-constexpr int kLong = 4096;   // entries above which the CTA takes a row
+constexpr int kSteps = 16;  // entries of a long row a thread keeps in registers
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -298,219 +303,58 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
     }
 }
 
-
-// Entries [p0, p1) of a row, or of this warp's part of one (CTA: every warp has a
-// part, empty ones too), streamed twice: for the maximum and sums, which the lanes
-// keep relative to maxima of their own, and for the results.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool CTA, int WARPS, class S>
-__device__ __noinline__ void stream_row(const MapArgs& a, S& st, int r, float lam, int p0, int p1, bool vec,
-                                        BlockStats<WARPS>& sh) {
-    constexpr int MAPS = TWO ? 2 : 1, kPiece = 512;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int limit = st.limit;
-    st.limit = max(limit, (int)(((long long)p1 + kChunk - 1) / kChunk));
-    // Pieces end on whole quads, so only the first and the last have edges.
-    auto pieces = [&](auto entry, auto quad) {
-        for (long long b0 = p0; b0 < p1; b0 = (b0 & ~3LL) + kPiece) {
-            const int b1 = (int)min((long long)p1, (b0 & ~3LL) + kPiece);
-            st.need((int)b0, b1);
-            const RowQuads rq((unsigned)b0, (unsigned)b1, lane);
-            if (rq.has_edge) entry(rq.edge);
-#pragma unroll 1
-            for (unsigned q = rq.qs + 4 * lane; q < rq.qe; q += 128) quad(q);
-        }
-    };
-    Stat run[MAPS];
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
-    auto take = [&](int k, float top, auto add) {
-        top = fmaxf(top, run[k].m);
-        const float base = top == -INFINITY ? 0.f : top, f = __expf(run[k].m - base);
-        run[k].z *= f;
-        run[k].c *= f;
-        run[k].m = top;
-        add(base);
-    };
-    pieces(
-        [&](unsigned e) {
-            const float d = GRAD ? lds_entry<DIN>(st.at(MAPS, e)) : 0.f;
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                const float x = lds_f32(st.at(k, e));
-                take(k, x, [&](float base) {
-                    const float w = __expf(x - base);
-                    run[k].z += w;
-                    if constexpr (GRAD) run[k].c += weighted(w, d);
-                });
-            }
-        },
-        [&](unsigned q) {
-            float2 d0, d1;
-            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                float2 lo, hi;
-                lds_quad<false>(st.at(k, q), lo, hi);
-                take(k, fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)), [&](float base) {
-                    const float w0 = __expf(lo.x - base), w1 = __expf(lo.y - base), w2 = __expf(hi.x - base),
-                                w3 = __expf(hi.y - base);
-                    run[k].z += (w0 + w1) + (w2 + w3);
-                    if constexpr (GRAD)
-                        run[k].c += (weighted(w0, d0.x) + weighted(w1, d0.y)) + (weighted(w2, d1.x) + weighted(w3, d1.y));
-                });
-            }
-        });
-    float m[MAPS], z[MAPS], c[MAPS], inv[MAPS];
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k) {
-        m[k] = warp_max(run[k].m);
-        if (CTA && lane == 0) sh.top[k][warp] = m[k];
-    }
-    if constexpr (CTA) {
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k)
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
-    }
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k) {
-        const float f = run[k].m == -INFINITY ? 0.f : __expf(run[k].m - m[k]);
-        z[k] = warp_sum(run[k].z * f);
-        c[k] = GRAD ? warp_sum(weighted(f, run[k].c)) : 0.f;
-        if (CTA && lane == 0) {
-            sh.sum[k][0][warp] = z[k];
-            sh.sum[k][1][warp] = c[k];
-        }
-    }
-    if constexpr (CTA) {
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            z[k] = c[k] = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                z[k] += sh.sum[k][0][w];
-                c[k] += sh.sum[k][1][w];
-            }
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k) {
-        inv[k] = inverse(z[k]);
-        c[k] *= inv[k];
-    }
-    if (GRAD && TWO && a.row_c2 && lane == 0 && (!CTA || warp == 0)) a.row_c2[r] = c[MAPS - 1];
-    if constexpr (TWO) inv[1] *= -lam;
-    auto grad = [&](int k, float x, float d) {
-        const float w = weight_of(x, Base(m[k]));
-        return weighted(w, fmaf(inv[k], d, -inv[k] * c[k]));
-    };
-    auto map = [&](float x1, float x2) {
-        const float w1 = weight_of(x1, Base(m[0])) * inv[0];
-        return TWO ? fmaf(weight_of(x2, Base(m[MAPS - 1])), inv[MAPS - 1], w1) : w1;
-    };
-    if (p0 < p1) st.seek(p0);
-    pieces(
-        [&](unsigned e) {
-            if constexpr (GRAD) {
-                const float d = lds_entry<DIN>(st.at(MAPS, e));
-                store_entry<OUT>(a.out1, e, grad(0, lds_f32(st.at(0, e)), d));
-                if constexpr (TWO) store_entry<OUT>(a.out2, e, grad(1, lds_f32(st.at(1, e)), d));
-            } else {
-                store_entry<OUT>(a.out1, e, map(lds_f32(st.at(0, e)), lds_f32(st.at(MAPS - 1, e))));
-            }
-        },
-        [&](unsigned q) {
-            float2 lo[MAPS], hi[MAPS];
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
-            if constexpr (GRAD) {
-                float2 d0, d1;
-                lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k)
-                    store_quad<OUT>(k == 0 ? a.out1 : a.out2, q, make_float2(grad(k, lo[k].x, d0.x), grad(k, lo[k].y, d0.y)),
-                                    make_float2(grad(k, hi[k].x, d1.x), grad(k, hi[k].y, d1.y)), vec);
-            } else {
-                constexpr int L = MAPS - 1;
-                store_quad<OUT>(a.out1, q, make_float2(map(lo[0].x, lo[L].x), map(lo[0].y, lo[L].y)),
-                                make_float2(map(hi[0].x, hi[L].x), map(hi[0].y, hi[L].y)), vec);
-            }
-        });
-    st.limit = limit;
+// Out of line in the kernel below: long rows are rare there.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, int WARPS>
+__device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0, int p1, BlockStats<WARPS>& sh) {
+    block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, 1, 0);
 }
 
-// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring.
-// In registers (FITS: at most 128 whole quads), or walked in the ring.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, bool FITS, class S>
-__device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
+// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring, walked
+// twice: for weights and their sums, and for results.  MAX: exponents are measured
+// from the row's maximum; else from the largest of its first entries, and false if
+// that does not do (nothing is changed then).
+template <bool TWO, bool GRAD, bool DIN, bool OUT, bool MAX, class S>
+__device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
     constexpr int MAPS = TWO ? 2 : 1;
     const int lane = threadIdx.x & 31;
     const RowQuads rq(p0, p1, lane);
     const unsigned first = rq.qs + 4 * lane;
-    constexpr int STEPS = FITS ? kRowSteps : 1;
-    float2 x[MAPS][STEPS][2], d[GRAD ? STEPS : 1][2];  // FITS: the lane's quads
 
-    // Maximum.
     float m[MAPS], xe[MAPS];
     const float de = GRAD && rq.has_edge ? lds_entry<DIN>(st.at(MAPS, rq.edge)) : 0.f;
 #pragma unroll
-    for (int k = 0; k < MAPS; ++k) m[k] = xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
-    if constexpr (FITS) {
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const unsigned q = first + 128 * i;
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) x[k][i][0] = x[k][i][1] = make_float2(-INFINITY, -INFINITY);
-            if constexpr (GRAD) d[i][0] = d[i][1] = make_float2(0.f, 0.f);
-            if (q < rq.qe) {
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), x[k][i][0], x[k][i][1]);
-                if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d[i][0], d[i][1]);
-            }
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k)
-                m[k] = fmaxf(m[k], fmaxf(fmaxf(x[k][i][0].x, x[k][i][0].y), fmaxf(x[k][i][1].x, x[k][i][1].y)));
-        }
-    } else {
-#pragma unroll 2
+    for (int k = 0; k < MAPS; ++k) {
+        xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
+        m[k] = xe[k];
+#pragma unroll 1
         for (unsigned q = first; q < rq.qe; q += 128) {
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                float2 lo, hi;
-                lds_quad<false>(st.at(k, q), lo, hi);
-                m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
+            float2 lo, hi;
+            lds_quad<false>(st.at(k, q), lo, hi);
+            m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
+            if (!MAX) break;
+        }
+        if (MAX) {
+            m[k] = warp_max(m[k]);
+            // A maximum of -inf (every entry masked) leaves the scores as they are, and
+            // scores so large that s·log2 e overflows are brought near zero first.
+            if (!(fabsf(m[k]) <= 1e37f)) {
+                if (m[k] != -INFINITY) {
+                    xe[k] -= m[k];
+#pragma unroll 1
+                    for (unsigned q = first; q < rq.qe; q += 128) {
+                        float2 lo, hi;
+                        lds_quad<false>(st.at(k, q), lo, hi);
+                        sts_quad(st.at(k, q), make_float2(lo.x - m[k], lo.y - m[k]), make_float2(hi.x - m[k], hi.y - m[k]));
+                    }
+                }
+                m[k] = 0.f;
             }
+        } else {
+            m[k] = fmaxf(__shfl_sync(kFullMask, m[k], 0), __shfl_sync(kFullMask, m[k], 4));
         }
     }
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k) m[k] = warp_max(m[k]);
 
-    // A maximum of -inf (every entry masked) leaves the scores as they are, and
-    // scores so large that s·log2 e overflows are brought near zero first.
-#pragma unroll
-    for (int k = 0; k < MAPS; ++k)
-        if (!(fabsf(m[k]) <= 1e37f)) {
-            if (m[k] != -INFINITY) {
-                xe[k] -= m[k];
-                if constexpr (FITS) {
-#pragma unroll
-                    for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) x[k][i][h] = make_float2(x[k][i][h].x - m[k], x[k][i][h].y - m[k]);
-                }
-#pragma unroll 1
-                for (unsigned q = first; !FITS && q < rq.qe; q += 128) {
-                    float2 lo, hi;
-                    lds_quad<false>(st.at(k, q), lo, hi);
-                    sts_quad(st.at(k, q), make_float2(lo.x - m[k], lo.y - m[k]), make_float2(hi.x - m[k], hi.y - m[k]));
-                }
-            }
-            m[k] = 0.f;
-        }
-
-    // Weights exp(s - m) = 2^(s·log2 e - m·log2 e), in place, and their sums.
+    // Weights exp(s - m) = 2^(s·log2 e - m·log2 e), and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
     float2 zs[MAPS], cs[MAPS], shift[MAPS];
     const float2 scale = make_float2(kLog2e, kLog2e);
@@ -522,74 +366,63 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
         zs[k] = make_float2(xe[k], 0.f);
         cs[k] = make_float2(GRAD ? __fmul_rn(xe[k], de) : 0.f, 0.f);
     }
-    // One quad's weights from its scores.
-    auto weights = [&](int k, float2& lo, float2& hi, float2 d0, float2 d1) {
+    // (Formed again for the results: cheaper than writing them back.)
+    auto weights = [&](int k, unsigned q, float2& lo, float2& hi) {
+        lds_quad<false>(st.at(k, q), lo, hi);
         lo = __ffma2_rn(lo, scale, shift[k]);
         hi = __ffma2_rn(hi, scale, shift[k]);
         lo = make_float2(exp2_flush(lo.x), exp2_flush(lo.y));
         hi = make_float2(exp2_flush(hi.x), exp2_flush(hi.y));
-        zs[k] = __fadd2_rn(zs[k], __fadd2_rn(lo, hi));
-        if constexpr (GRAD) cs[k] = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, cs[k]));
     };
-    if constexpr (FITS) {
+#pragma unroll 1
+    for (unsigned q = first; q < rq.qe; q += 128) {
+        float2 d0, d1;
+        if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            if (rq.qs + 128 * i < rq.qe) {
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k)
-                    weights(k, x[k][i][0], x[k][i][1], d[GRAD ? i : 0][0], d[GRAD ? i : 0][1]);
-            }
-    } else {
-#pragma unroll 2
-        for (unsigned q = first; q < rq.qe; q += 128) {
-            float2 d0 = make_float2(0.f, 0.f), d1 = d0;
-            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                float2 lo, hi;
-                lds_quad<false>(st.at(k, q), lo, hi);
-                weights(k, lo, hi, d0, d1);
-                sts_quad(st.at(k, q), lo, hi);
-            }
+        for (int k = 0; k < MAPS; ++k) {
+            float2 lo, hi;
+            weights(k, q, lo, hi);
+            zs[k] = __fadd2_rn(zs[k], __fadd2_rn(lo, hi));
+            if constexpr (GRAD) cs[k] = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, cs[k]));
         }
     }
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        z[k] = warp_sum(zs[k].x + zs[k].y);
-        c[k] = GRAD ? warp_sum(cs[k].x + cs[k].y) : 0.f;
+        z[k] = zs[k].x + zs[k].y;
+        c[k] = cs[k].x + cs[k].y;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            z[k] += __shfl_xor_sync(kFullMask, z[k], o);
+            if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], o);
+        }
     // A dout that is not finite makes c so too, even under weights of 0: such a
     // row leaves those products out.
-    bool guarded = false;
-    if constexpr (GRAD) {
+    bool fine = true, guarded = false;
+    auto at_weight = [&](float2 w, float2 v) { return make_float2(w.x == 0.f ? 0.f : v.x, w.y == 0.f ? 0.f : v.y); };
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) guarded = guarded || !(fabsf(c[k]) < INFINITY);
-        if (guarded) {
+    for (int k = 0; k < MAPS; ++k) {
+        fine = fine && z[k] < 0x1p100f;
+        if constexpr (GRAD) guarded = guarded || !(fabsf(c[k]) < 0x1p100f);
+    }
+    if (GRAD && guarded) {
 #pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                float2 sum = make_float2(xe[k] != 0.f ? __fmul_rn(xe[k], de) : 0.f, 0.f);
-                auto add = [&](float2 lo, float2 hi, float2 d0, float2 d1) {
-                    d0 = make_float2(lo.x == 0.f ? 0.f : d0.x, lo.y == 0.f ? 0.f : d0.y);
-                    d1 = make_float2(hi.x == 0.f ? 0.f : d1.x, hi.y == 0.f ? 0.f : d1.y);
-                    sum = __ffma2_rn(hi, d1, __ffma2_rn(lo, d0, sum));
-                };
-                if constexpr (FITS) {
-#pragma unroll
-                    for (int i = 0; i < STEPS; ++i)
-                        if (rq.qs + 128 * i < rq.qe) add(x[k][i][0], x[k][i][1], d[i][0], d[i][1]);
-                } else {
+        for (int k = 0; k < MAPS; ++k) {
+            float2 sum = make_float2(xe[k] != 0.f ? __fmul_rn(xe[k], de) : 0.f, 0.f);
 #pragma unroll 1
-                    for (unsigned q = first; q < rq.qe; q += 128) {
-                        float2 d0, d1, lo, hi;
-                        lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-                        lds_quad<false>(st.at(k, q), lo, hi);
-                        add(lo, hi, d0, d1);
-                    }
-                }
-                c[k] = warp_sum(sum.x + sum.y);
+            for (unsigned q = first; q < rq.qe; q += 128) {
+                float2 d0, d1, lo, hi;
+                lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+                weights(k, q, lo, hi);
+                sum = __ffma2_rn(hi, at_weight(hi, d1), __ffma2_rn(lo, at_weight(lo, d0), sum));
             }
+            c[k] = warp_sum(sum.x + sum.y);
+            fine = fine && fabsf(c[k]) < 0x1p100f;
         }
     }
+    if (!MAX && !fine) return false;
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
         inv[k] = inverse(z[k]);
@@ -601,16 +434,13 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
     // Results.  Gradients are w·(inv·d - inv·c).
     auto grad = [&](int k, float2 w, float2 d) {
         const float ic = -inv[k] * c[k];
-        float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
-        if (guarded) {
-            if (w.x == 0.f) y.x = 0.f;
-            if (w.y == 0.f) y.y = 0.f;
-        }
-        return y;
+        if (guarded) d = at_weight(w, d);
+        const float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
+        return guarded ? at_weight(w, y) : y;
     };
     auto map = [&](const float2 (&w)[MAPS]) {
         const float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
-        return __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y);
+        return TWO ? __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y) : y;
     };
     if (rq.has_edge) {
         if constexpr (GRAD) {
@@ -623,135 +453,154 @@ __device__ __forceinline__ void ring_row(const MapArgs& a, const S& st, int r, f
             store_entry<OUT>(a.out1, rq.edge, map(w).x);
         }
     }
-    auto results = [&](unsigned q, const float2 (&lo)[MAPS], const float2 (&hi)[MAPS], float2 d0, float2 d1) {
+#pragma unroll 1
+    for (unsigned q = first; q < rq.qe; q += 128) {
+        float2 lo[MAPS], hi[MAPS];
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) weights(k, q, lo[k], hi[k]);
         if constexpr (GRAD) {
+            float2 d0, d1;
+            lds_quad<DIN>(st.at(MAPS, q), d0, d1);
             store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
             if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
         } else {
             store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
         }
-    };
-    if constexpr (FITS) {
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const unsigned q = first + 128 * i;
-            if (q < rq.qe) {
-                float2 lo[MAPS], hi[MAPS];
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k) {
-                    lo[k] = x[k][i][0];
-                    hi[k] = x[k][i][1];
-                }
-                results(q, lo, hi, d[GRAD ? i : 0][0], d[GRAD ? i : 0][1]);
-            }
-        }
-    } else {
-#pragma unroll 2
-        for (unsigned q = first; q < rq.qe; q += 128) {
-            float2 lo[MAPS], hi[MAPS], d0 = make_float2(0.f, 0.f), d1 = d0;
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) lds_quad<false>(st.at(k, q), lo[k], hi[k]);
-            if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-            results(q, lo, hi, d0, d1);
-        }
     }
+    return true;
+}
+
+// The same from the row's maximum, out of line: rarely needed.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
+__device__ __noinline__ void max_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
+    ring_row<TWO, GRAD, DIN, OUT, true>(a, st, r, lam, p0, p1, vec);
 }
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 
-template <bool TWO, bool GRAD, bool DIN>
-using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0>;
 
-// CTAs an SM that the rings leave room for.
+// Warps to a ring: two where it holds two maps and dout, of whose rings an SM has
+// room for 8 (the gradient of the differential map of 8x4096 rows, 55 us; a warp
+// to a ring, 63); one for the others, which saves the barrier (two: 45 us for the
+// differential map, 42 with one).
+template <bool TWO, bool GRAD>
+constexpr int ring_group() {
+    return TWO && GRAD ? 2 : 1;
+}
+template <bool TWO, bool GRAD, bool DIN>
+using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0, ring_group<TWO, GRAD>()>;
+
+// CTAs an SM that the rings leave room for, at most 6 (80 registers a thread).
 template <class S>
 constexpr int ctas_per_sm() {
-    constexpr int n = 226 * 1024 / (kWarps * S::kBytes + 4096);
-    return n > 6 ? 6 : n;  // 80 registers a thread
+    constexpr int n = 224 * 1024 / (kWarps / S::kGroup * S::kBytes + 1280);
+    return n > 6 ? 6 : n;
 }
 
-// The rows of a walk in the ring, out of line: most rows are shorter.
-template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
-__device__ __noinline__ void wide_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
-    ring_row<TWO, GRAD, DIN, OUT, false>(a, st, r, lam, p0, p1, vec);
-}
-
-// CTA b of B takes rows [M·b / B, M·(b+1) / B), kBatch at a time; a batch's rows
-// are dealt to the warps by equal parts of its entries.  vec: the outputs start
-// on whole quads.
+// Group g of G takes the rows that begin in share g of the entries.  vec: the
+// outputs start on whole quads.
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN>>())
-    stream_rows_kernel(const MapArgs a, bool aligned, bool vec) {
+    stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
     using S = MapStream<TWO, GRAD, DIN>;
+    constexpr int kGroup = S::kGroup, kGroups = kWarps / kGroup;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ BlockStats<kWarps> sh;
-    __shared__ RowBatch batch;
+    __shared__ int bounds[kGroups + 1];
+    __shared__ unsigned is_long[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long first = (long long)a.M * blockIdx.x / gridDim.x, last = (long long)a.M * (blockIdx.x + 1) / gridDim.x;
+    const int group = warp / kGroup, member = warp % kGroup, g = blockIdx.x * kGroups + group;
+    int r0, r1;
+    first_rows_from(a.row_offsets, a.M, share_begin(a.nnz, min(g, G), G), share_begin(a.nnz, min(g + 1, G), G), lane, r0, r1);
+    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
+    if (g + 1 >= G) r1 = a.M;
     S st;
     st.src[0] = reinterpret_cast<const unsigned char*>(a.s1);
     st.src[1] = static_cast<const unsigned char*>(TWO ? (const void*)a.s2 : a.dout);
     st.src[2] = static_cast<const unsigned char*>(a.dout);
-    st.base = smem_addr(smem) + warp * S::kBytes;
+    st.base = smem_addr(smem) + group * S::kBytes;
     st.nnz = a.nnz;
-    st.lane = lane;
+    st.lane = member * 32 + lane;
+    st.barrier = 1 + group;
     st.aligned = aligned;
     st.whole = aligned ? a.nnz / kChunk : 0;
-    for (long long b = first; b < last; b += kBatch) {
-        const int n = (int)min((long long)kBatch, last - b);
-        const bool any_long = batch.load(a.row_offsets, a.nnz, (int)b, n, kLong);
-        const int i0 = warp == 0 ? 0 : batch.first_from(n, batch.part(n, warp, kWarps), lane);
-        const int i1 = warp == kWarps - 1 ? n : batch.first_from(n, batch.part(n, warp + 1, kWarps), lane);
-        int p0, p1;
-        st.issued = st.limit = 0;
-        if (any_long) {
+    st.issued = 0;
+    st.limit = 0;
+    RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
+    int p0, p1;
+    if (r0 < r1) {
+        walk.hold(r1, 0);
+        st.limit = (int)(((long long)walk.offset(r1) + kChunk - 1) / kChunk);
+        walk.hold(r0, kGroup);
+        st.seek(walk.offset(r0));
+    }
+    if (lane == 0) {
+        bounds[group] = r0;
+        if (group == kGroups - 1) bounds[kGroups] = r1;
+    }
+    __syncthreads();
+    // Long rows by the CTA, while the rings fill.
+    for (int r = bounds[0]; r < bounds[kGroups]; r += kThreads) {
+        bool mine = false;
+        if (threadIdx.x < bounds[kGroups] - r) {
+            row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
+            mine = p1 - p0 > kRingRow;
+        }
+        const unsigned mask = __ballot_sync(kFullMask, mine);
+        if (lane == 0) is_long[warp] = mask;
+        if (!__syncthreads_or(mine)) continue;
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                batch.range(i, p0, p1);
-                if (p1 - p0 <= kLong) continue;
-                const int r = (int)b + i;
-                const long long len = p1 - p0;
-                const int b0 = p0 + (int)(len * warp / kWarps), b1 = p0 + (int)(len * (warp + 1) / kWarps);
-                if (b0 < b1) {
-                    st.limit = (int)(((long long)b1 + kChunk - 1) / kChunk);
-                    st.seek(b0);
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll 1
+            for (unsigned left = is_long[w]; left; left &= left - 1) {
+                const int row = r + w * 32 + __ffs(left) - 1;
+                row_range(a.row_offsets, row, a.nnz, p0, p1);
+                long_row<TWO, GRAD, DIN, OUT, kWarps>(a, row, TWO ? __ldg(a.lambda + row / a.seg_rows % a.heads) : 0.f, p0,
+                                                      p1, sh);
+            }
+        __syncthreads();  // is_long is read
+    }
+    float lam = 0.f;
+    long long block_end = 0;  // lam is the head's of the rows before this one
+#pragma unroll 1
+    for (int r = r0; r < r1;) {
+        walk.hold(r, kGroup);
+        const int begin = walk.offset(r);
+        // As many of the next rows as there are warps and fit the ring together.
+        int n = 0, end = begin;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int next = walk.offset(min(r + i + 1, a.M));
+            if (n == i && r + i < r1 && next - begin <= kRingRow) {
+                if (i == member) {
+                    p0 = end;
+                    p1 = max(next, end);
                 }
-                stream_row<TWO, GRAD, DIN, OUT, true>(a, st, r, TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f, b0,
-                                                      b1, vec, sh);
+                ++n;
+                end = max(next, end);
             }
         }
-        if (i0 < i1) {
-            st.limit = (int)(((long long)batch.offset[i1] + kChunk - 1) / kChunk);
-            st.seek(batch.offset[i0]);
+        if (n == 0) {  // a long row
+            ++r;
+            continue;
         }
-        float lam = 0.f;
-        long long block_end = 0;  // lam is the head's of the rows before this one
-#pragma unroll 1
-        for (int i = i0; i < i1; ++i) {
-            const int r = (int)b + i;
-            batch.range(i, p0, p1);
-            if (p0 == p1) {
-                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[r] = 0.f;
-                continue;
-            }
-            if (p1 - p0 > kLong) continue;
-            if (TWO && r >= block_end) {
-                const int block = r / a.seg_rows;
+        if (begin < end) st.need(begin, end);
+        if (member < n) {
+            const int row = r + member;
+            if (TWO && row >= block_end) {
+                const int block = row / a.seg_rows;
                 block_end = (block + 1LL) * a.seg_rows;
                 lam = __ldg(a.lambda + block % a.heads);
             }
-            if (p1 - p0 > kRingRow) {
-                stream_row<TWO, GRAD, DIN, OUT, false>(a, st, r, lam, p0, p1, vec, sh);
-                continue;
+            if (p0 == p1) {
+                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[row] = 0.f;
+            } else if (!ring_row<TWO, GRAD, DIN, OUT, false>(a, st, row, lam, p0, p1, vec)) {
+                max_row<TWO, GRAD, DIN, OUT>(a, st, row, lam, p0, p1, vec);
             }
-            st.need(p0, p1);
-            if (p1 - p0 <= 128 * kRowSteps)
-                ring_row<TWO, GRAD, DIN, OUT, true>(a, st, r, lam, p0, p1, vec);
-            else
-                wide_row<TWO, GRAD, DIN, OUT>(a, st, r, lam, p0, p1, vec);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();  // the next batch's offsets overwrite this one's
+        r += n;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
 }
 
 // A cluster per row.
@@ -799,7 +648,7 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
     // A CTA of 8 warps a row where rows are long and too few to fill the GPU with
     // a warp each; a cluster while its CTAs are too few too and keep at least
     // half their registers' worth each.
-    if (mean > 1536 && a.M <= 4 * sms) {
+    if (mean > kRingRow && a.M <= 4 * sms) {
         int ctas = 1;
         while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kClusterWarps * 32 * kSteps / 2) ctas *= 2;
         cudaLaunchAttribute attr;
@@ -815,18 +664,15 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
                                                                                                    : USM_ERR_CUDA;
     }
-    // As many CTAs as there is room for their rings, of at least 8 rows or 2048
-    // entries each.
+    // Groups: as many as there is room for their rings, with at least 256 entries each.
     using S = MapStream<TWO, GRAD, DIN>;
-    constexpr int smem = kWarps * S::kBytes;
-    const long long most = (long long)sms * ctas_per_sm<S>(), some = a.nnz / 2048 > a.M / 8 ? a.nnz / 2048 : a.M / 8;
-    long long ctas = some < 1 ? 1 : some < most ? some : most;
-    if (ctas > a.M) ctas = a.M;
+    constexpr int kGroups = kWarps / S::kGroup, smem = kGroups * S::kBytes;
+    const int most = sms * ctas_per_sm<S>() * kGroups, some = a.nnz / 256, G = some < 1 ? 1 : some < most ? some : most;
     const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
     const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
     const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
     if (!allow_shared(kernel, smem)) return USM_ERR_CUDA;
-    kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(a, aligned, vec);
+    kernel<<<(G + kGroups - 1) / kGroups, kThreads, smem, stream>>>(a, G, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 

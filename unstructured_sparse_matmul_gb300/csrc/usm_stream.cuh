@@ -1,11 +1,11 @@
-// CSR value arrays streamed through shared memory, a warp at a time.
+// CSR value arrays streamed through shared memory by a group of warps.
 //
-// A warp works on consecutive rows, whose entries are consecutive too, so what it
-// reads of every array is one run.  It has a ring of kRing entries in shared
-// memory for each array (entry p lies at p mod kRing) that asynchronous copies
-// fill kChunk entries at a time, up to a ring ahead of the row it works on: the
-// copies do not wait for the rows' arithmetic, nor for where rows begin and end.
-// No barriers but the warp's own.
+// A group works on consecutive rows, a row a warp, whose entries are consecutive
+// too: what it reads of every array is one run.  It has a ring of kRing entries
+// in shared memory for each array (entry p lies at p mod kRing) that asynchronous
+// copies fill kChunk entries at a time, up to a ring ahead of the rows it works
+// on: the copies do not wait for the rows' arithmetic, nor for where rows begin
+// and end.
 #pragma once
 
 #include "usm_device.cuh"
@@ -13,17 +13,21 @@
 
 namespace usm {
 
-constexpr int kChunk = 128, kRing = 8 * kChunk;
+constexpr int kChunk = 512, kRing = 4 * kChunk;
 // A run up to this long fits the ring wherever it starts.
-constexpr int kRingRow = 7 * kChunk;
+constexpr int kRingRow = 3 * kChunk;
 
-// Streams up to three arrays of E0, E1, E2 bytes an element (0: none).
-template <int E0, int E1, int E2>
+// Streams up to three arrays of E0, E1, E2 bytes an element (0: none), for GW
+// warps; every warp of the group makes the same calls.
+template <int E0, int E1, int E2, int GW>
 struct Stream {
-    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a warp
+    static constexpr int kGroup = GW;
+    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a group
     const unsigned char* src[3];
-    uint32_t base;  // shared address of the warp's rings
-    int nnz, lane;
+    uint32_t base;  // shared address of the group's rings
+    int nnz;
+    int lane;       // of the group's 32·GW
+    int barrier;    // the group's named barrier, 1 or 2
     bool aligned;   // every array starts on 16 bytes
     int whole;      // chunks before this one are whole (none, if not aligned)
     int issued;     // chunks before this one are copied or in flight
@@ -43,27 +47,26 @@ struct Stream {
             const uint32_t p0 = (uint32_t)chunk * kChunk + lane * PER, to = at(array, p0);
             const unsigned char* from = src[array] + (unsigned long long)p0 * E;
 #pragma unroll
-            for (int i = 0; i < (kChunk / PER + 31) / 32; ++i) {
-                if (kChunk / PER < 32 && lane >= kChunk / PER) break;
+            for (int i = 0; i < kChunk / PER / (32 * GW); ++i) {
                 if constexpr (!EDGE) {
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512 * GW), "l"(from + i * 512 * GW)
                                  : "memory");
                 } else {
-                    const long long left = ((long long)nnz - p0 - i * 32 * PER) * E;
+                    const long long left = ((long long)nnz - p0 - i * 32 * GW * PER) * E;
                     const int bytes = (int)min(max(left, 0LL), 16LL);  // past the end: zeros, unread
                     if (aligned) {
-                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512),
-                                     "l"(from + i * 512), "r"(bytes)
+                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512 * GW),
+                                     "l"(from + i * 512 * GW), "r"(bytes)
                                      : "memory");
                     } else {
                         for (int u = 0; u < bytes; u += E) {
                             if constexpr (E == 4)
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 + u),
-                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 + u))
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 * GW + u),
+                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 * GW + u))
                                              : "memory");
                             else
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 + u),
-                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 + u))
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 * GW + u),
+                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 * GW + u))
                                              : "memory");
                         }
                     }
@@ -75,6 +78,14 @@ struct Stream {
         copy<E0, true>(0, chunk);
         copy<E1, true>(1, chunk);
         copy<E2, true>(2, chunk);
+    }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (GW == 1)
+            __syncwarp();
+        else if (barrier == 1)  // constants: a barrier in a register would reserve all 16
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * GW) : "memory");
+        else
+            asm volatile("bar.sync 2, %0;" ::"n"(32 * GW) : "memory");
     }
     // The next chunk (an empty set of copies past the limit).
     __device__ __forceinline__ void issue() {
@@ -93,7 +104,7 @@ struct Stream {
     // Starts at entry p, with a full ring ahead of it.
     __device__ __forceinline__ void seek(int p) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
+        sync();
         issued = p / kChunk;
 #pragma unroll 1
         for (int i = 0; i < kRing / kChunk; ++i) issue();
@@ -104,21 +115,20 @@ struct Stream {
         const int c0 = p0 / kChunk;
         if (c0 >= issued || c0 + kRing / kChunk < issued) seek(p0);  // rows were left out
         if (c0 + kRing / kChunk > issued) {
-            __syncwarp();  // every lane is done with what is overwritten
+            sync();  // every warp is done with what is overwritten
             do issue();
             while (c0 + kRing / kChunk > issued);
         }
-        switch (issued - 1 - (p1 - 1) / kChunk) {  // chunks that may stay in flight
-            case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-            case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-            case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-            case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-            case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-            case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-            case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-            default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-        }
-        __syncwarp();
+        const int left = issued - 1 - (p1 - 1) / kChunk;
+        if (left == 0)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (left == 1)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else if (left == 2)
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 3;" ::: "memory");
+        sync();
     }
 };
 
@@ -198,46 +208,52 @@ struct RowQuads {
     }
 };
 
-// Offsets of a batch of up to kBatch consecutive rows, in shared memory.
-constexpr int kBatch = 512;
-struct RowBatch {
-    int offset[kBatch + 1];
-
-    // Offsets of rows r .. r + n, by every thread of the CTA (a barrier, which also
-    // says whether a row has over `most` entries).
-    __device__ __forceinline__ bool load(const int* __restrict__ ro, int nnz, int r, int n, int most) {
-        bool over = false;
-        for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-            const int p = min(max(__ldg(ro + r + i), 0), nnz);
-            offset[i] = p;
-            if (i < n) over = over || __ldg(ro + r + i + 1) - p > most;
+// First rows r0 and r1 whose offset is at least t0 and t1 (in [0, M]), by 32
+// candidates a round, both at once.
+__device__ __forceinline__ void first_rows_from(const int* __restrict__ ro, int M, int t0, int t1, int lane, int& r0,
+                                                int& r1) {
+    int lo[2] = {0, 0}, hi[2] = {M, M};  // offsets before lo are below the target, hi's is not (or hi is M)
+    const int target[2] = {t0, t1};
+    while (lo[0] < hi[0] || lo[1] < hi[1]) {
+        int step[2], v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            step[k] = (hi[k] - lo[k] + 31) / 32;
+            v[k] = __ldg(ro + min((long long)lo[k] + (long long)lane * step[k], (long long)M));
         }
-        return __syncthreads_or(over);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool candidate = (long long)lo[k] + (long long)lane * step[k] < hi[k];
+            const unsigned below = __ballot_sync(kFullMask, candidate && v[k] < target[k]);
+            if (below == 0) {
+                hi[k] = lo[k];
+            } else {
+                const int last = lo[k] + (31 - __clz(below)) * step[k];
+                hi[k] = (int)min((long long)hi[k], (long long)last + step[k]);
+                lo[k] = last + 1;
+            }
+        }
     }
-    // Entry at which part w of W of the batch's entries begins.
-    __device__ __forceinline__ int part(int n, int w, int W) const {
-        return offset[0] + (int)((long long)max(offset[n] - offset[0], 0) * w / W);
+    r0 = lo[0];
+    r1 = lo[1];
+}
+
+// Lanes hold 32 consecutive row offsets, read off them one by one.
+struct RowWalk {
+    const int* ro;
+    int M, nnz, lane, at, held;  // held: offset of row at + lane
+    // Offsets of rows r .. r + n (n < 32) can be read.
+    __device__ __forceinline__ void hold(int r, int n) {
+        if (r < at || r - at > 31 - n) {
+            at = r;
+            held = min(max(__ldg(ro + min((long long)r + lane, (long long)M)), 0), nnz);
+        }
     }
-    // First row of the batch that begins at entry p or later (n: none does).
-    __device__ __forceinline__ int first_from(int n, int p, int lane) const {
-        int before = 0;
-        for (int i = 0; i < n; i += 32) before += __popc(__ballot_sync(kFullMask, i + lane < n && offset[i + lane] < p));
-        return before;
-    }
-    __device__ __forceinline__ void range(int i, int& p0, int& p1) const {
-        p0 = offset[i];
-        p1 = max(offset[i + 1], p0);
-    }
+    __device__ __forceinline__ int offset(int r) const { return __shfl_sync(kFullMask, held, r - at); }
 };
 
-// Lets a kernel have `smem` bytes a CTA, and the SM all the shared memory there is
-// (the driver's own split left room for 4 CTAs of 33 KB where 6 fit).
-template <class Kernel>
-inline bool allow_shared(Kernel kernel, int smem) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
-           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
-               cudaSuccess;
-}
+// Share g of G of nnz entries.
+__device__ __forceinline__ int share_begin(int nnz, int g, int G) { return (int)((long long)nnz * g / G); }
 
 inline bool aligned_for_stream(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
