@@ -612,6 +612,7 @@ struct Walk {
 template <class Row>
 __global__ void __launch_bounds__(Row::R::kWarps * 32)
     attention_shares_kernel(const AttnArgs a, float* parts, int* cut_rows, int G) {
+    let_next_start();
     using R = typename Row::R;
     constexpr int MAPS = Row::kMaps, NC = Row::kColumns, W = R::kWarps;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -699,8 +700,9 @@ __global__ void __launch_bounds__(Row::R::kWarps * 32)
 // CTAs past G write zeros to the rows without entries, 256 rows each.
 template <int MAPS>
 __global__ void __launch_bounds__(256)
-    attention_join_kernel(const AttnArgs a, const float* __restrict__ parts, const int* __restrict__ cut_rows, int G) {
+    attention_join_kernel(const AttnArgs a, const float* parts, const int* cut_rows, int G) {
     __shared__ float sums[8][MAPS][3][32];
+    await_previous();
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, g0 = blockIdx.x;
     int p0, p1;
     if (g0 >= G) {
@@ -786,8 +788,8 @@ struct Launch {
             if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
             kernel<<<(G + R::kWarps - 1) / R::kWarps, R::kWarps * 32, R::kSmem, stream>>>(a, parts, cut_rows, G);
             const dim3 grid((unsigned)(G + ((long long)a.M + 255) / 256), (a.N + 31) / 32);
-            attention_join_kernel<Row::kMaps><<<grid, 256, 0, stream>>>(a, parts, cut_rows, G);
-            return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+            return launch_next(attention_join_kernel<Row::kMaps>, grid, 256, stream, a, (const float*)parts,
+                               (const int*)cut_rows, G);
         }
         // CTAs a row: more until the rows fill the SMs or a row's windows (on
         // average) no longer give every warp one.

@@ -127,6 +127,27 @@ inline bool allow_shared(Kernel kernel, int smem) {
                cudaSuccess;
 }
 
+// A second kernel that may be brought to the SMs while the stream's last one still
+// runs (which calls let_next_start()); it reads nothing of that one before its own
+// await_previous(), which returns once all of it is done and visible.
+template <class... P, class... A>
+inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // Launch shape forced by usm_set_schedule_override (0: the library's choice).
 struct ScheduleOverride {
     int rows_per_warp, tiles_per_block, k_splits;

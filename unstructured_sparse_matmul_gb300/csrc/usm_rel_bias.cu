@@ -24,61 +24,95 @@ __global__ void rel_bucket_kernel(int num_buckets, int reach, int causal, int* _
     map[i] = k + (!causal && d > 0 ? b : 0);
 }
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kCtas = 3;  // an SM's CTAs (80 registers a thread hold a tile and the walk)
 constexpr int kSteps = 4;             // quads of entries a lane has in flight
 constexpr int kTile = kSteps * 128;   // entries of a warp's tile
 
-// Four entries from q on (one by one where the array does not start on a quad or
-// ends inside it).  Plain loads: the same kernel may write the array in place.
+// Entries of a tile in a warp's registers: lane l has entries 128·i + 4·l + u.
+// `limit`: entries before it exist (others read as 0).  vec: the array starts on a
+// whole quad.  Plain loads of values: the same kernel may write them in place.
 template <bool BF>
-__device__ __forceinline__ float load_value(const void* p, unsigned i) {
-    if constexpr (BF) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-    return static_cast<const float*>(p)[i];
-}
-template <bool BF>
-__device__ __forceinline__ void load_values(const void* p, unsigned q, unsigned nnz, bool vec, float (&x)[4]) {
-    if (vec && q + 4 <= nnz) {
-        if constexpr (BF) {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + q);
-            x[0] = __uint_as_float(w.x << 16);
-            x[1] = __uint_as_float(w.x & 0xffff0000u);
-            x[2] = __uint_as_float(w.y << 16);
-            x[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-            const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + q);
-            x[0] = w.x;
-            x[1] = w.y;
-            x[2] = w.z;
-            x[3] = w.w;
+__device__ __forceinline__ void load_values(const void* p, unsigned tile, unsigned limit, bool vec, int lane,
+                                            float (&x)[kSteps][4]) {
+    if (vec && tile + kTile <= limit) {
+        const char* q = static_cast<const char*>(p) + (size_t)(tile + 4 * lane) * (BF ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if constexpr (BF) {
+                const uint2 w = *reinterpret_cast<const uint2*>(q + i * 256);
+                x[i][0] = __uint_as_float(w.x << 16);
+                x[i][1] = __uint_as_float(w.x & 0xffff0000u);
+                x[i][2] = __uint_as_float(w.y << 16);
+                x[i][3] = __uint_as_float(w.y & 0xffff0000u);
+            } else {
+                const float4 w = *reinterpret_cast<const float4*>(q + i * 512);
+                x[i][0] = w.x;
+                x[i][1] = w.y;
+                x[i][2] = w.z;
+                x[i][3] = w.w;
+            }
         }
     } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = q + u < nnz ? load_value<BF>(p, q + u) : 0.f;
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const unsigned e = tile + 128 * i + 4 * lane + u;
+                if constexpr (BF)
+                    x[i][u] = e < limit ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[e] << 16) : 0.f;
+                else
+                    x[i][u] = e < limit ? static_cast<const float*>(p)[e] : 0.f;
+            }
     }
 }
-__device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigned q, unsigned nnz, bool vec, int (&c)[4]) {
-    if (vec && q + 4 <= nnz) {
-        const int4 w = __ldg(reinterpret_cast<const int4*>(ci + q));
-        c[0] = w.x;
-        c[1] = w.y;
-        c[2] = w.z;
-        c[3] = w.w;
+__device__ __forceinline__ void load_columns(const int* __restrict__ ci, unsigned tile, unsigned limit, bool vec, int lane,
+                                             int (&c)[kSteps][4]) {
+    if (vec && tile + kTile <= limit) {
+        const int4* q = reinterpret_cast<const int4*>(ci + tile) + lane;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int4 w = __ldg(q + 32 * i);
+            c[i][0] = w.x;
+            c[i][1] = w.y;
+            c[i][2] = w.z;
+            c[i][3] = w.w;
+        }
     } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) c[u] = q + u < nnz ? __ldg(ci + q + u) : 0;
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const unsigned e = tile + 128 * i + 4 * lane + u;
+                c[i][u] = e < limit ? __ldg(ci + e) : 0;
+            }
     }
 }
 
-// The rows of a run of entries: lane i holds row `first + i`'s offset and what a
-// functor makes of the row (31 rows; lane 31 only ends the last).
-struct RowsHeld {
-    const int* ro;
-    int r1;  // rows before this one
-    int nnz, lane;
-    int first, offset;
+// Asks L2 for a tile's lines (a lane each), while the warp works on the one before.
+template <int E>
+__device__ __forceinline__ void prefetch_tile(const int* ci, const void* values, unsigned tile, unsigned limit, int lane) {
+    constexpr int kLine = 128 / E;
+    const unsigned e = lane < 16 ? tile + 32 * lane : tile + kLine * (lane - 16);
+    if (e < limit && e < tile + kTile) {
+        const void* at = lane < 16 ? static_cast<const void*>(ci + e) : static_cast<const char*>(values) + (size_t)e * E;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+}
 
-    __device__ __forceinline__ int load(int r) const {
-        return min(max(__ldg(ro + min((long long)r + lane, (long long)r1)), 0), nnz);
+// Walks the rows with entries in [p, end) of rows [r, r1).  Lane i holds row
+// `first + i`'s offset (31 rows; lane 31 only ends the last), and whatever
+// made(row, whether it counts) keeps of it when other rows come to be held.
+struct RowWalk {
+    const int* ro;
+    int r1, nnz, lane;
+    unsigned end;
+    int first, offset;
+    unsigned left;   // held rows from the current one on
+    int at;          // lane that holds the current row
+    unsigned begin;  // where it begins; past `end` if there is none
+
+    __device__ __forceinline__ void load() {
+        offset = min(max(__ldg(ro + min((long long)first + lane, (long long)r1)), 0), nnz);
     }
     // Holds the row that entry p lies in, found among rows [r, r1) by 128 candidates
     // a round.
@@ -86,49 +120,59 @@ struct RowsHeld {
         long long lo = r, n = (long long)r1 - r;
         while (n > 31) {
             const long long step = (n + 127) / 128;
-            int at[4], below = 0;
+            int tried[4], below = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const long long i = (lane + 32 * k) * step;
-                at[k] = i < n ? __ldg(ro + lo + i) : 0x7fffffff;
+                tried[k] = i < n ? __ldg(ro + lo + i) : 0x7fffffff;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) below += __popc(__ballot_sync(kFullMask, at[k] <= (long long)p));
+            for (int k = 0; k < 4; ++k) below += __popc(__ballot_sync(kFullMask, tried[k] <= (long long)p));
             const long long skip = max(below - 1, 0) * step;
             lo += skip;
             n = min(step, n - skip);
         }
         first = (int)lo;
-        offset = load(first);
+        load();
     }
-    // Calls f(lane that holds the row, begin, end) for each row's part of entries
-    // [p, end), which come after what was asked for before.  fresh: other rows are
-    // held than made(row, whether it has entries) was last called for.
-    template <class Made, class F>
-    __device__ __forceinline__ void segments(unsigned p, unsigned end, bool& fresh, Made made, F f) {
-        while (true) {
-            const unsigned next = __shfl_down_sync(kFullMask, offset, 1);
-            const bool row = lane < min(31, r1 - first);
-            if (fresh) made(first + lane, row && next > (unsigned)offset);
-            fresh = false;
-            unsigned left = __ballot_sync(kFullMask, row && next > max((unsigned)offset, p) && (unsigned)offset < end);
-            for (; left; left &= left - 1) {
-                const int i = __ffs(left) - 1;
-                f(i, max((unsigned)__shfl_sync(kFullMask, offset, i), p), min(__shfl_sync(kFullMask, next, i), end));
+    template <class Made>
+    __device__ __forceinline__ void hold(unsigned p, Made made) {
+        const unsigned next = __shfl_down_sync(kFullMask, offset, 1);
+        const bool some = lane < min(31, r1 - first) && next > (unsigned)offset && next > p;
+        made(first + lane, some);
+        left = __ballot_sync(kFullMask, some);
+    }
+    template <class Made>
+    __device__ __forceinline__ void settle(Made made) {
+        while (left == 0) {
+            const unsigned p = __shfl_sync(kFullMask, offset, 31);
+            if (r1 - first <= 31 || p >= end) {
+                begin = 0xffffffffu;
+                return;
             }
-            const unsigned held = __shfl_sync(kFullMask, offset, 31);
-            if (held >= end || r1 - first <= 31) return;
-            p = max(p, held);
             first += 31;
-            offset = load(first);
-            fresh = true;
+            load();
             if ((unsigned)__shfl_sync(kFullMask, offset, 31) <= p && r1 - first > 31) find(p, first);  // rows without entries
+            hold(p, made);
         }
+        at = __ffs(left) - 1;
+        begin = __shfl_sync(kFullMask, offset, at);
+    }
+    template <class Made>
+    __device__ __forceinline__ void start(unsigned p, int r, Made made) {
+        find(p, r);
+        hold(p, made);
+        settle(made);
+    }
+    template <class Made>
+    __device__ __forceinline__ void next(Made made) {
+        left &= left - 1;
+        settle(made);
     }
 };
 
-// Where column col's distance lies in the map: before or at its start (entry 0:
-// every key further back), at its end or after (the last entry), or between.
+// Where a column's distance lies in the map: at its start or before (entry 0: every
+// key further back), between, or at its end or after (the last entry).
 struct Distance {
     bool back, between;
     unsigned entry;
@@ -139,74 +183,119 @@ struct Distance {
     }
 };
 
-// Bound by memory: 8 bytes a nonzero in, 4 out.  A warp takes a tile of entries,
-// whatever rows they are in: its loads go out first, and the search for the
-// tile's rows runs while they are in flight.  Each row's part of the tile then
-// gets its bias: most keys are further away than the map reaches, and those have
-// one of two values that the row's lane holds; only the others look up the map
-// and the table.
+// Bound by memory: 8 bytes a nonzero in, 4 out.  Warp w of W takes an equal share
+// of the entries, whatever rows they are in, a tile at a time; the search for the
+// first tile's rows runs while its loads are in flight.  Most keys are further
+// away than the map reaches, and those have one of two values; only groups of 128
+// entries that have others look up the map and the table.
 template <bool BT>
-__global__ void __launch_bounds__(kThreads) rel_bias_kernel(int M, int nnz, const int* __restrict__ ro,
+__global__ void __launch_bounds__(kThreads, kCtas) rel_bias_kernel(int M, int nnz, const int* __restrict__ ro,
                                                             const int* __restrict__ ci, const float* s, const RelArgs b,
-                                                            float* out, bool vec) {
-    const int lane = threadIdx.x & 31;
-    const unsigned tile = (blockIdx.x * (unsigned)(kThreads / 32) + (threadIdx.x >> 5)) * (unsigned)kTile;
-    if (tile >= (unsigned)nnz) return;
-    int c[kSteps][4];
-    float x[kSteps][4];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        load_columns(ci, tile + 128 * i + 4 * lane, nnz, vec, c[i]);
-        load_values<false>(s, tile + 128 * i + 4 * lane, nnz, vec, x[i]);
-    }
+                                                            float* out, int W, bool vec) {
+    const int lane = threadIdx.x & 31, w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (w >= W) return;
+    const unsigned quads = ((unsigned)nnz + 3) / 4;
+    const unsigned q0 = 4 * (unsigned)((unsigned long long)quads * w / W);
+    const unsigned q1 = min((unsigned)nnz, 4 * (unsigned)((unsigned long long)quads * (w + 1) / W));
     const unsigned all0 = min(max(__ldg(ro), 0), nnz), all1 = min(max(__ldg(ro + M), 0), nnz);
-    const unsigned p0 = max(tile, all0), p1 = min(tile + kTile, all1);
+    const unsigned p0 = max(q0, all0), p1 = min(q1, all1);
     if (p0 >= p1) return;
-    RowsHeld rows{ro, M, nnz, lane, 0, 0};
-    rows.find(p0, 0);
     const unsigned last = 2u * (unsigned)b.reach;
     const int bucket0 = rel_bucket(b, 0), bucket1 = rel_bucket(b, (int)last);
-    int start = 0, head = 0;
+    auto table_of = [&](int head) { return static_cast<const char*>(b.table) + (long long)head * b.buckets * (BT ? 2 : 4); };
+    RowWalk rows{ro, M, nnz, lane, p1, 0, 0, 0, 0, 0};
+    int row_start = 0, row_head = 0;
+    auto made = [&](int r, bool some) {
+        if (!some) return;
+        const int block = r / b.seg_rows;
+        row_head = block % b.heads;
+        row_start = rel_start(b, block, r - block * b.seg_rows, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
+    };
+    // The current row's, and its head's.
+    int start = 0, head = -1;
+    const char* table = nullptr;
     float back = 0.f, ahead = 0.f;
-    bool fresh = true;
-    rows.segments(
-        p0, p1, fresh,
-        [&](int r, bool some) {
-            if (!some) return;
-            const int block = r / b.seg_rows;
-            head = block % b.heads;
-            start = rel_start(b, block, r - block * b.seg_rows, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
-            const char* table = static_cast<const char*>(b.table) + (long long)head * b.buckets * (BT ? 2 : 4);
+    auto enter = [&]() {
+        const int h = __shfl_sync(kFullMask, row_head, rows.at);
+        start = __shfl_sync(kFullMask, row_start, rows.at);
+        if (h != head) {
+            head = h;
+            table = table_of(h);
             back = rel_table_entry<BT>(table, bucket0);
             ahead = rel_table_entry<BT>(table, bucket1);
-        },
-        [&](int i, unsigned s0, unsigned s1) {
-            const int from = __shfl_sync(kFullMask, start, i);
-            const float far0 = __shfl_sync(kFullMask, back, i), far1 = __shfl_sync(kFullMask, ahead, i);
-            const char* table = static_cast<const char*>(b.table) +
-                                (long long)__shfl_sync(kFullMask, head, i) * b.buckets * (BT ? 2 : 4);
+        }
+        rows.next(made);
+    };
+    bool found = false;
+#pragma unroll 1
+    for (unsigned tile = p0 & ~3u; tile < p1; tile += kTile) {
+        int c[kSteps][4];
+        float x[kSteps][4];
+        load_columns(ci, tile, p1, vec, lane, c);
+        load_values<false>(s, tile, p1, vec, lane, x);
+        prefetch_tile<4>(ci, s, tile + kTile, p1, lane);
+        if (!found) {
+            rows.start(p0, 0, made);
+            if (rows.begin == 0xffffffffu) return;
+            enter();
+            found = true;
+        }
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const unsigned g = tile + 128 * k, q = g + 4 * lane;
-                if (g + 128 <= s0 || g >= s1) continue;
+        for (int k = 0; k < kSteps; ++k) {
+            const unsigned g = tile + 128 * k, q = g + 4 * lane;
+            unsigned lo = g;
+            bool more;
+            do {  // a head's part of the group (nearly always all of it)
+                int from[4] = {start, start, start, start};
+                more = false;
+                while (rows.begin < g + 128) {
+                    if (__shfl_sync(kFullMask, row_head, rows.at) != head) {
+                        more = true;
+                        break;
+                    }
+                    const unsigned begin = rows.begin;
+                    enter();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) from[u] = q + u >= begin ? start : from[u];
+                }
+                const unsigned n = (more ? rows.begin : g + 128) - lo;
+                bool any = false, between[4];
+                unsigned entry[4];
+                float v[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const Distance d(c[k][u], from, last);
-                    float v = d.back ? far0 : far1;
-                    if (d.between) v = rel_table_entry<BT>(table, rel_bucket(b, (int)d.entry));
-                    if (q + u - s0 < s1 - s0) x[k][u] += v;
+                    const Distance d(c[k][u], from[u], last);
+                    v[u] = d.back ? back : ahead;
+                    any = any || d.between;
+                    between[u] = d.between;
+                    entry[u] = d.entry;
                 }
-            }
-        });
+                if (__any_sync(kFullMask, any)) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const unsigned q = tile + 128 * i + 4 * lane;
-        if (vec && q >= p0 && q + 4 <= p1) {
-            *reinterpret_cast<float4*>(out + q) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+                    for (int u = 0; u < 4; ++u) {
+                        const float near = rel_table_entry<BT>(table, rel_bucket(b, between[u] ? (int)entry[u] : 0));
+                        v[u] = between[u] ? near : v[u];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (q + u - lo < n) x[k][u] += v[u];
+                lo += n;
+                if (more) enter();
+            } while (more);
+        }
+        if (vec && p0 <= tile && tile + kTile <= p1) {
+            float4* to = reinterpret_cast<float4*>(out + tile) + lane;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) to[32 * i] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
         } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (q + u >= p0 && q + u < p1) out[q + u] = x[i][u];
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const unsigned e = tile + 128 * i + 4 * lane + u;
+                    if (e >= p0 && e < p1) out[e] = x[i][u];
+                }
         }
     }
 }
@@ -219,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(int M, int nnz, cons
 // added in a fixed order: which thread takes which entry is fixed too.  Bound by
 // memory: 8 (or 6) bytes a nonzero.
 template <bool BF>
-__global__ void __launch_bounds__(kThreads, 3) rel_bias_grad_kernel(int M, int nnz, const int* __restrict__ ro,
+__global__ void __launch_bounds__(kThreads, kCtas) rel_bias_grad_kernel(int M, int nnz, const int* __restrict__ ro,
                                                                  const int* __restrict__ ci, const void* __restrict__ ds,
                                                                  const RelArgs b, int blocks, int Y, int J,
                                                                  float* __restrict__ part, bool vec) {
@@ -241,41 +330,62 @@ __global__ void __launch_bounds__(kThreads, 3) rel_bias_grad_kernel(int M, int n
         const unsigned p0 = max(e0, f + 4 * (unsigned)((unsigned long long)quads * y / Y));
         const unsigned p1 = min(e1, f + 4 * (unsigned)((unsigned long long)quads * (y + 1) / Y));
         if (p0 >= p1) continue;
-        RowsHeld rows{ro, r1, nnz, lane, 0, 0};
-        int start = 0;
-        bool found = false, fresh = true;
+        RowWalk rows{ro, r1, nnz, lane, p1, 0, 0, 0, 0, 0};
+        int row_start = 0, start = 0;
+        auto made = [&](int r, bool some) {
+            if (some) row_start = rel_start(b, block, r - r0, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
+        };
+        auto enter = [&]() {
+            start = __shfl_sync(kFullMask, row_start, rows.at);
+            rows.next(made);
+        };
+        bool found = false;
 #pragma unroll 1
         for (unsigned tile = p0 & ~3u; tile < p1; tile += kTile) {
             int c[kSteps][4];
             float x[kSteps][4];
+            load_columns(ci, tile, p1, vec, lane, c);
+            load_values<BF>(ds, tile, p1, vec, lane, x);
+            prefetch_tile<BF ? 2 : 4>(ci, ds, tile + kTile, p1, lane);
+            if (!found) {
+                rows.start(p0, r0, made);
+                if (rows.begin == 0xffffffffu) break;
+                enter();
+                found = true;
+#pragma unroll
+                for (int u = 0; u < 3; ++u)
+                    if (tile + 4 * lane + u < p0) x[0][u] = 0.f;
+            }
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                load_columns(ci, tile + 128 * k + 4 * lane, p1, vec, c[k]);
-                load_values<BF>(ds, tile + 128 * k + 4 * lane, p1, vec, x[k]);
+                const unsigned g = tile + 128 * k, q = g + 4 * lane;
+                int from[4] = {start, start, start, start};
+                while (rows.begin < g + 128) {
+                    const unsigned begin = rows.begin;
+                    enter();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) from[u] = q + u >= begin ? start : from[u];
+                }
+                bool any = false, between[4];
+                unsigned entry[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const Distance d(c[k][u], from[u], last);
+                    if (d.back) back += x[k][u];
+                    if (!d.back && !d.between) ahead += x[k][u];
+                    any = any || d.between;
+                    between[u] = d.between;
+                    entry[u] = d.entry;
+                }
+                if (__any_sync(kFullMask, any)) {
+                    int at[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) at[u] = rel_bucket(b, between[u] ? (int)entry[u] : 0) * T + t;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (between[u]) hist[at[u]] += x[k][u];
+                }
             }
-            if (!found) rows.find(p0, r0);
-            found = true;
-            rows.segments(
-                max(tile, p0), min(tile + kTile, p1), fresh,
-                [&](int r, bool some) {
-                    if (some) start = rel_start(b, block, r - r0, b.seg_cols > 0 ? __ldg(ci + rows.offset) : 0);
-                },
-                [&](int i, unsigned s0, unsigned s1) {
-                    const int from = __shfl_sync(kFullMask, start, i);
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const unsigned g = tile + 128 * k, q = g + 4 * lane;
-                        if (g + 128 <= s0 || g >= s1) continue;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const Distance d(c[k][u], from, last);
-                            const float v = q + u - s0 < s1 - s0 ? x[k][u] : 0.f;
-                            back += d.back ? v : 0.f;
-                            ahead += d.back || d.between ? 0.f : v;
-                            if (d.between && v != 0.f) hist[rel_bucket(b, (int)d.entry) * T + t] += v;
-                        }
-                    }
-                });
         }
     }
     hist[rel_bucket(b, 0) * T + t] += back;
@@ -341,8 +451,11 @@ template <bool BT>
 void launch_bias(int M, int nnz, const int* ro, const int* ci, const float* scores, const RelArgs& bias, float* out,
                  cudaStream_t stream) {
     const bool vec = quad_aligned(ci) && quad_aligned(scores) && quad_aligned(out);
-    const unsigned per_cta = kThreads / 32 * kTile;
-    rel_bias_kernel<BT><<<((unsigned)nnz + per_cta - 1) / per_cta, kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, out, vec);
+    // A warp has half a tile or more.
+    const int most = sm_count_current_device() * kCtas * (kThreads / 32), some = nnz / (kTile / 2) + 1;
+    const int W = some < most ? some : most;
+    rel_bias_kernel<BT>
+        <<<(W + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, stream>>>(M, nnz, ro, ci, scores, bias, out, W, vec);
 }
 }  // namespace
 

@@ -5,22 +5,25 @@
 // Pk = exp(sk - mk) / zk, mk the row's maximum, zk = Σ exp(sk - mk) over its
 // stored entries.
 //
-// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  A warp or
-// two take the rows that begin in an equal share of the entries and stream them
+// Bound by memory: 8 to 12 bytes a nonzero in, 2 to 8 out, each once.  Every warp
+// takes the rows that begin in an equal share of the entries and streams them
 // through a ring in shared memory (usm_stream.cuh), so copies are in flight all
 // the time whatever the rows' arithmetic and lengths do.  An SM's shared memory
-// holds the rings of 12 to 16 warps, few to cover the latency of a row's
+// holds the rings of 8 to 12 warps, few to cover the latency of a row's
 // arithmetic, which is what is left to wait for:
 //   - A row is walked twice in the ring (weights and their sums; results), four
 //     entries a lane, in pairs of fp32 (f32x2).  Loops are short: rows read into
-//     registers, unrolled, measured 47 to 58 us where these take 42 (the
+//     registers, unrolled, measured 47 to 58 us where these take 40 (the
 //     differential map of 8x4096 rows of 410 entries).
+//   - Two rows of about a length are taken at once, by half a warp each (43 us
+//     with one at a time).
 //   - The maximum is not looked for (45 us with it): exponents are measured from
 //     the largest of a row's first entries, which gives the same quotients unless
 //     a sum passes 2^100; a row whose sum does is done again from its maximum, as
 //     are rows with masks at their start or values that are not finite.
-//   - Rows over 1536 entries are first taken by the whole CTA; where rows are long
-//     and few, a cluster of up to 8 CTAs takes each (launch_rows).
+//   - Rows over 1536 entries are first taken by the whole CTA (8x4096 rows without
+//     any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
+//     each (launch_rows).
 #include <cmath>
 
 #include "usm_cluster.cuh"
@@ -309,14 +312,17 @@ __device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0
     block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, 1, 0);
 }
 
-// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring, walked
-// twice: for weights and their sums, and for results.  MAX: exponents are measured
-// from the row's maximum; else from the largest of its first entries, and false if
-// that does not do (nothing is changed then).
+// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring, by the
+// warp or by half of it (width 32 or 16, the same for all lanes; each half has its
+// own row then, which may be empty: false), walked twice: for weights and their
+// sums, and for results.  MAX: exponents are measured from the row's maximum; else
+// from the largest of its first entries, and false if that does not do (nothing is
+// changed then).
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool MAX, class S>
-__device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
+__device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int width, int r, float lam, int p0, int p1, bool vec) {
     constexpr int MAPS = TWO ? 2 : 1;
-    const int lane = threadIdx.x & 31;
+    const int base = threadIdx.x & 31 & -width, lane = threadIdx.x & (width - 1);
+    const unsigned step = 4 * width;
     const RowQuads rq(p0, p1, lane);
     const unsigned first = rq.qs + 4 * lane;
 
@@ -327,7 +333,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
         xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
         m[k] = xe[k];
 #pragma unroll 1
-        for (unsigned q = first; q < rq.qe; q += 128) {
+        for (unsigned q = first; q < rq.qe; q += step) {
             float2 lo, hi;
             lds_quad<false>(st.at(k, q), lo, hi);
             m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
@@ -341,7 +347,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
                 if (m[k] != -INFINITY) {
                     xe[k] -= m[k];
 #pragma unroll 1
-                    for (unsigned q = first; q < rq.qe; q += 128) {
+                    for (unsigned q = first; q < rq.qe; q += step) {
                         float2 lo, hi;
                         lds_quad<false>(st.at(k, q), lo, hi);
                         sts_quad(st.at(k, q), make_float2(lo.x - m[k], lo.y - m[k]), make_float2(hi.x - m[k], hi.y - m[k]));
@@ -350,7 +356,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
                 m[k] = 0.f;
             }
         } else {
-            m[k] = fmaxf(__shfl_sync(kFullMask, m[k], 0), __shfl_sync(kFullMask, m[k], 4));
+            m[k] = fmaxf(__shfl_sync(kFullMask, m[k], base), __shfl_sync(kFullMask, m[k], base + 4));
         }
     }
 
@@ -375,7 +381,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
         hi = make_float2(exp2_flush(hi.x), exp2_flush(hi.y));
     };
 #pragma unroll 1
-    for (unsigned q = first; q < rq.qe; q += 128) {
+    for (unsigned q = first; q < rq.qe; q += step) {
         float2 d0, d1;
         if constexpr (GRAD) lds_quad<DIN>(st.at(MAPS, q), d0, d1);
 #pragma unroll
@@ -392,12 +398,19 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
         c[k] = cs[k].x + cs[k].y;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             z[k] += __shfl_xor_sync(kFullMask, z[k], o);
             if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], o);
         }
+    if (width == 32) {
+#pragma unroll
+        for (int k = 0; k < MAPS; ++k) {
+            z[k] += __shfl_xor_sync(kFullMask, z[k], 16);
+            if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], 16);
+        }
+    }
     // A dout that is not finite makes c so too, even under weights of 0: such a
     // row leaves those products out.
     bool fine = true, guarded = false;
@@ -407,18 +420,22 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
         fine = fine && z[k] < 0x1p100f;
         if constexpr (GRAD) guarded = guarded || !(fabsf(c[k]) < 0x1p100f);
     }
-    if (GRAD && guarded) {
+    if (GRAD && __any_sync(kFullMask, guarded)) {
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             float2 sum = make_float2(xe[k] != 0.f ? __fmul_rn(xe[k], de) : 0.f, 0.f);
 #pragma unroll 1
-            for (unsigned q = first; q < rq.qe; q += 128) {
+            for (unsigned q = first; q < rq.qe; q += step) {
                 float2 d0, d1, lo, hi;
                 lds_quad<DIN>(st.at(MAPS, q), d0, d1);
                 weights(k, q, lo, hi);
                 sum = __ffma2_rn(hi, at_weight(hi, d1), __ffma2_rn(lo, at_weight(lo, d0), sum));
             }
-            c[k] = warp_sum(sum.x + sum.y);
+            float x = sum.x + sum.y;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
+            if (width == 32) x += __shfl_xor_sync(kFullMask, x, 16);
+            if (guarded) c[k] = x;
             fine = fine && fabsf(c[k]) < 0x1p100f;
         }
     }
@@ -454,7 +471,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
         }
     }
 #pragma unroll 1
-    for (unsigned q = first; q < rq.qe; q += 128) {
+    for (unsigned q = first; q < rq.qe; q += step) {
         float2 lo[MAPS], hi[MAPS];
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) weights(k, q, lo[k], hi[k]);
@@ -473,132 +490,120 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int r, f
 // The same from the row's maximum, out of line: rarely needed.
 template <bool TWO, bool GRAD, bool DIN, bool OUT, class S>
 __device__ __noinline__ void max_row(const MapArgs& a, const S& st, int r, float lam, int p0, int p1, bool vec) {
-    ring_row<TWO, GRAD, DIN, OUT, true>(a, st, r, lam, p0, p1, vec);
+    ring_row<TWO, GRAD, DIN, OUT, true>(a, st, 32, r, lam, p0, p1, vec);
 }
+
+template <bool TWO, bool GRAD, bool DIN>
+using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0>;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-
-
-// Warps to a ring: two where it holds two maps and dout, of whose rings an SM has
-// room for 8 (the gradient of the differential map of 8x4096 rows, 55 us; a warp
-// to a ring, 63); one for the others, which saves the barrier (two: 45 us for the
-// differential map, 42 with one).
-template <bool TWO, bool GRAD>
-constexpr int ring_group() {
-    return TWO && GRAD ? 2 : 1;
-}
-template <bool TWO, bool GRAD, bool DIN>
-using MapStream = Stream<4, TWO ? 4 : (GRAD ? (DIN ? 2 : 4) : 0), TWO && GRAD ? (DIN ? 2 : 4) : 0, ring_group<TWO, GRAD>()>;
 
 // CTAs an SM that the rings leave room for, at most 6 (80 registers a thread).
 template <class S>
 constexpr int ctas_per_sm() {
-    constexpr int n = 224 * 1024 / (kWarps / S::kGroup * S::kBytes + 1280);
+    constexpr int n = 224 * 1024 / (kWarps * S::kBytes + 1536);
     return n > 6 ? 6 : n;
 }
 
-// Group g of G takes the rows that begin in share g of the entries.  vec: the
+// Warp g of G takes the rows that begin in share g of the entries.  vec: the
 // outputs start on whole quads.
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN>>())
     stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
+    if constexpr (TWO && GRAD) let_next_start();
     using S = MapStream<TWO, GRAD, DIN>;
-    constexpr int kGroup = S::kGroup, kGroups = kWarps / kGroup;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ BlockStats<kWarps> sh;
-    __shared__ int bounds[kGroups + 1];
+    __shared__ int bounds[kWarps + 1];
     __shared__ unsigned is_long[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group = warp / kGroup, member = warp % kGroup, g = blockIdx.x * kGroups + group;
-    int r0, r1;
-    first_rows_from(a.row_offsets, a.M, share_begin(a.nnz, min(g, G), G), share_begin(a.nnz, min(g + 1, G), G), lane, r0, r1);
-    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
-    if (g + 1 >= G) r1 = a.M;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x * kWarps + warp;
+    const int t0 = share_begin(a.nnz, min(g, G), G), t1 = share_begin(a.nnz, min(g + 1, G), G);
     S st;
     st.src[0] = reinterpret_cast<const unsigned char*>(a.s1);
     st.src[1] = static_cast<const unsigned char*>(TWO ? (const void*)a.s2 : a.dout);
     st.src[2] = static_cast<const unsigned char*>(a.dout);
-    st.base = smem_addr(smem) + group * S::kBytes;
+    st.base = smem_addr(smem) + warp * S::kBytes;
     st.nnz = a.nnz;
-    st.lane = member * 32 + lane;
-    st.barrier = 1 + group;
+    st.lane = lane;
     st.aligned = aligned;
     st.whole = aligned ? a.nnz / kChunk : 0;
     st.issued = 0;
-    st.limit = 0;
+    st.limit = (int)(((long long)t1 + kChunk - 1) / kChunk);
+    st.seek(t0);  // the copies need not wait for the search
+    int r0, r1;
+    first_rows_from(a.row_offsets, a.M, t0, t1, lane, r0, r1);
+    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
+    if (g + 1 >= G) r1 = a.M;
     RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
     int p0, p1;
+    bool any_long = false;
     if (r0 < r1) {
-        walk.hold(r1, 0);
-        st.limit = (int)(((long long)walk.offset(r1) + kChunk - 1) / kChunk);
-        walk.hold(r0, kGroup);
-        st.seek(walk.offset(r0));
+        const int end = min(max(__ldg(a.row_offsets + r1), 0), a.nnz);
+        walk.hold(r0, 2);
+        st.extend((int)(((long long)end + kChunk - 1) / kChunk));
+        any_long = walk.any_over(r0, r1, kRingRow);
     }
     if (lane == 0) {
-        bounds[group] = r0;
-        if (group == kGroups - 1) bounds[kGroups] = r1;
+        bounds[warp] = r0;
+        if (warp == kWarps - 1) bounds[kWarps] = r1;
     }
-    __syncthreads();
     // Long rows by the CTA, while the rings fill.
-    for (int r = bounds[0]; r < bounds[kGroups]; r += kThreads) {
-        bool mine = false;
-        if (threadIdx.x < bounds[kGroups] - r) {
-            row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
-            mine = p1 - p0 > kRingRow;
-        }
-        const unsigned mask = __ballot_sync(kFullMask, mine);
-        if (lane == 0) is_long[warp] = mask;
-        if (!__syncthreads_or(mine)) continue;
+    if (__syncthreads_or(any_long)) {
 #pragma unroll 1
-        for (int w = 0; w < kWarps; ++w)
-#pragma unroll 1
-            for (unsigned left = is_long[w]; left; left &= left - 1) {
-                const int row = r + w * 32 + __ffs(left) - 1;
-                row_range(a.row_offsets, row, a.nnz, p0, p1);
-                long_row<TWO, GRAD, DIN, OUT, kWarps>(a, row, TWO ? __ldg(a.lambda + row / a.seg_rows % a.heads) : 0.f, p0,
-                                                      p1, sh);
+        for (int r = bounds[0]; r < bounds[kWarps]; r += kThreads) {
+            bool mine = false;
+            if (threadIdx.x < bounds[kWarps] - r) {
+                row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
+                mine = p1 - p0 > kRingRow;
             }
-        __syncthreads();  // is_long is read
+            const unsigned mask = __ballot_sync(kFullMask, mine);
+            if (lane == 0) is_long[warp] = mask;
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll 1
+                for (unsigned left = is_long[w]; left; left &= left - 1) {
+                    const int row = r + w * 32 + __ffs(left) - 1;
+                    row_range(a.row_offsets, row, a.nnz, p0, p1);
+                    long_row<TWO, GRAD, DIN, OUT, kWarps>(a, row, TWO ? __ldg(a.lambda + row / a.seg_rows % a.heads) : 0.f,
+                                                          p0, p1, sh);
+                }
+            __syncthreads();  // is_long is read
+        }
     }
     float lam = 0.f;
     long long block_end = 0;  // lam is the head's of the rows before this one
 #pragma unroll 1
     for (int r = r0; r < r1;) {
-        walk.hold(r, kGroup);
-        const int begin = walk.offset(r);
-        // As many of the next rows as there are warps and fit the ring together.
-        int n = 0, end = begin;
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-            const int next = walk.offset(min(r + i + 1, a.M));
-            if (n == i && r + i < r1 && next - begin <= kRingRow) {
-                if (i == member) {
-                    p0 = end;
-                    p1 = max(next, end);
-                }
-                ++n;
-                end = max(next, end);
-            }
-        }
-        if (n == 0) {  // a long row
-            ++r;
-            continue;
-        }
+        // Two rows of about a length by half a warp each: a row's fixed part (its sums
+        // over lanes, first entries, edges) is half its instructions otherwise, as
+        // much as another 450 entries (differences of up to 128, 256 and 512 entries
+        // measured 41.0, 39.7 and 41.1 us).
+        walk.hold(r, 2);
+        const int begin = walk.offset(r), mid = max(walk.offset(r + 1), begin), far = max(walk.offset(r + 2), mid);
+        const bool pair = r + 1 < r1 && far - begin <= kRingRow && abs((mid - begin) - (far - mid)) < 256;
+        const int end = pair ? far : mid, half = pair ? lane >> 4 : 0, row = r + half;
+        r += pair ? 2 : 1;
+        if (end - begin > kRingRow) continue;  // a long row
         if (begin < end) st.need(begin, end);
-        if (member < n) {
-            const int row = r + member;
-            if (TWO && row >= block_end) {
-                const int block = row / a.seg_rows;
-                block_end = (block + 1LL) * a.seg_rows;
-                lam = __ldg(a.lambda + block % a.heads);
-            }
-            if (p0 == p1) {
-                if (GRAD && TWO && a.row_c2 && lane == 0) a.row_c2[row] = 0.f;
-            } else if (!ring_row<TWO, GRAD, DIN, OUT, false>(a, st, row, lam, p0, p1, vec)) {
-                max_row<TWO, GRAD, DIN, OUT>(a, st, row, lam, p0, p1, vec);
-            }
+        p0 = half ? mid : begin;
+        p1 = half ? far : mid;
+        if (TWO && row >= block_end) {
+            const int block = row / a.seg_rows;
+            block_end = (block + 1LL) * a.seg_rows;
+            lam = __ldg(a.lambda + block % a.heads);
         }
-        r += n;
+        bool done = true;
+        if (begin < end) done = ring_row<TWO, GRAD, DIN, OUT, false>(a, st, pair ? 16 : 32, row, lam, p0, p1, vec);
+        if (p0 == p1) {
+            if (GRAD && TWO && a.row_c2 && (lane & 15) == 0) a.row_c2[row] = 0.f;
+            done = true;
+        }
+        for (unsigned again = __ballot_sync(kFullMask, !done) & (pair ? 0x10001u : 1u); again; again &= again - 1) {
+            const int from = __ffs(again) - 1;
+            max_row<TWO, GRAD, DIN, OUT>(a, st, __shfl_sync(kFullMask, row, from), __shfl_sync(kFullMask, lam, from),
+                                         __shfl_sync(kFullMask, p0, from), __shfl_sync(kFullMask, p1, from), vec);
+        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
 }
@@ -607,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
 constexpr int kClusterWarps = 8;
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const MapArgs a) {
+    if constexpr (TWO && GRAD) let_next_start();
     __shared__ BlockStats<kClusterWarps> sh;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
@@ -622,9 +628,9 @@ __global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const 
 
 // dλ[h] = -Σ c2 over head h's rows: a CTA per head, a fixed order.
 __global__ void __launch_bounds__(1024) lambda_grad_kernel(int M, int blocks, int heads, int seg_rows,
-                                                           const float* __restrict__ row_c2,
-                                                           float* __restrict__ dlambda) {
+                                                           const float* row_c2, float* __restrict__ dlambda) {
     __shared__ float warp_part[32];
+    await_previous();
     const int head = blockIdx.x, t = threadIdx.x, lane = t & 31;
     float x = 0.f;
     for (long long b = head; b < blocks; b += heads) {
@@ -664,15 +670,15 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
                                                                                                    : USM_ERR_CUDA;
     }
-    // Groups: as many as there is room for their rings, with at least 256 entries each.
+    // As many warps as there is room for their rings, of at least 256 entries each.
     using S = MapStream<TWO, GRAD, DIN>;
-    constexpr int kGroups = kWarps / S::kGroup, smem = kGroups * S::kBytes;
-    const int most = sms * ctas_per_sm<S>() * kGroups, some = a.nnz / 256, G = some < 1 ? 1 : some < most ? some : most;
+    constexpr int smem = kWarps * S::kBytes;
+    const int most = sms * ctas_per_sm<S>() * kWarps, some = a.nnz / 256, G = some < 1 ? 1 : some < most ? some : most;
     const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
     const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
     const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
     if (!allow_shared(kernel, smem)) return USM_ERR_CUDA;
-    kernel<<<(G + kGroups - 1) / kGroups, kThreads, smem, stream>>>(a, G, aligned, vec);
+    kernel<<<(G + kWarps - 1) / kWarps, kThreads, smem, stream>>>(a, G, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
@@ -694,9 +700,8 @@ int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream) { return laun
 int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stream) {
     const int r = launch_map<true, true>(a, stream);
     if (r != USM_OK || !dlambda) return r;
-    lambda_grad_kernel<<<a.heads, 1024, 0, stream>>>(a.M, query_blocks(a.M, a.seg_rows), a.heads, a.seg_rows,
-                                                       a.row_c2, dlambda);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return launch_next(lambda_grad_kernel, a.heads, 1024, stream, a.M, query_blocks(a.M, a.seg_rows), a.heads, a.seg_rows,
+                       (const float*)a.row_c2, dlambda);
 }
 
 }  // namespace usm

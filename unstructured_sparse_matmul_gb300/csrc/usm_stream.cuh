@@ -1,11 +1,10 @@
-// CSR value arrays streamed through shared memory by a group of warps.
+// CSR value arrays streamed through shared memory, a warp at a time.
 //
-// A group works on consecutive rows, a row a warp, whose entries are consecutive
-// too: what it reads of every array is one run.  It has a ring of kRing entries
-// in shared memory for each array (entry p lies at p mod kRing) that asynchronous
-// copies fill kChunk entries at a time, up to a ring ahead of the rows it works
-// on: the copies do not wait for the rows' arithmetic, nor for where rows begin
-// and end.
+// A warp works on consecutive rows, whose entries are consecutive too: what it
+// reads of every array is one run.  It has a ring of kRing entries in shared
+// memory for each array (entry p lies at p mod kRing) that asynchronous copies
+// fill kChunk entries at a time, up to a ring ahead of the row it works on: the
+// copies do not wait for the row's arithmetic, nor for where rows begin and end.
 #pragma once
 
 #include "usm_device.cuh"
@@ -17,17 +16,13 @@ constexpr int kChunk = 512, kRing = 4 * kChunk;
 // A run up to this long fits the ring wherever it starts.
 constexpr int kRingRow = 3 * kChunk;
 
-// Streams up to three arrays of E0, E1, E2 bytes an element (0: none), for GW
-// warps; every warp of the group makes the same calls.
-template <int E0, int E1, int E2, int GW>
+// Streams up to three arrays of E0, E1, E2 bytes an element (0: none).
+template <int E0, int E1, int E2>
 struct Stream {
-    static constexpr int kGroup = GW;
-    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a group
+    static constexpr int kBytes = kRing * (E0 + E1 + E2);  // shared memory a warp
     const unsigned char* src[3];
-    uint32_t base;  // shared address of the group's rings
-    int nnz;
-    int lane;       // of the group's 32·GW
-    int barrier;    // the group's named barrier, 1 or 2
+    uint32_t base;  // shared address of the warp's rings
+    int nnz, lane;
     bool aligned;   // every array starts on 16 bytes
     int whole;      // chunks before this one are whole (none, if not aligned)
     int issued;     // chunks before this one are copied or in flight
@@ -47,26 +42,26 @@ struct Stream {
             const uint32_t p0 = (uint32_t)chunk * kChunk + lane * PER, to = at(array, p0);
             const unsigned char* from = src[array] + (unsigned long long)p0 * E;
 #pragma unroll
-            for (int i = 0; i < kChunk / PER / (32 * GW); ++i) {
+            for (int i = 0; i < kChunk / PER / 32; ++i) {
                 if constexpr (!EDGE) {
-                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512 * GW), "l"(from + i * 512 * GW)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
                                  : "memory");
                 } else {
-                    const long long left = ((long long)nnz - p0 - i * 32 * GW * PER) * E;
+                    const long long left = ((long long)nnz - p0 - i * 32 * PER) * E;
                     const int bytes = (int)min(max(left, 0LL), 16LL);  // past the end: zeros, unread
                     if (aligned) {
-                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512 * GW),
-                                     "l"(from + i * 512 * GW), "r"(bytes)
+                        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + i * 512),
+                                     "l"(from + i * 512), "r"(bytes)
                                      : "memory");
                     } else {
                         for (int u = 0; u < bytes; u += E) {
                             if constexpr (E == 4)
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 * GW + u),
-                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 * GW + u))
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i * 512 + u),
+                                             "r"(*reinterpret_cast<const uint32_t*>(from + i * 512 + u))
                                              : "memory");
                             else
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 * GW + u),
-                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 * GW + u))
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * 512 + u),
+                                             "h"(*reinterpret_cast<const uint16_t*>(from + i * 512 + u))
                                              : "memory");
                         }
                     }
@@ -78,14 +73,6 @@ struct Stream {
         copy<E0, true>(0, chunk);
         copy<E1, true>(1, chunk);
         copy<E2, true>(2, chunk);
-    }
-    __device__ __forceinline__ void sync() const {
-        if constexpr (GW == 1)
-            __syncwarp();
-        else if (barrier == 1)  // constants: a barrier in a register would reserve all 16
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * GW) : "memory");
-        else
-            asm volatile("bar.sync 2, %0;" ::"n"(32 * GW) : "memory");
     }
     // The next chunk (an empty set of copies past the limit).
     __device__ __forceinline__ void issue() {
@@ -104,10 +91,15 @@ struct Stream {
     // Starts at entry p, with a full ring ahead of it.
     __device__ __forceinline__ void seek(int p) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        sync();
+        __syncwarp();
         issued = p / kChunk;
 #pragma unroll 1
         for (int i = 0; i < kRing / kChunk; ++i) issue();
+    }
+    // Moves the limit up; chunks that the old one kept out are still to be copied.
+    __device__ __forceinline__ void extend(int new_limit) {
+        issued = min(issued, limit);
+        limit = new_limit;
     }
     // Makes entries [p0, p1) (at most kRingRow, one at least) readable by every
     // lane; runs come in order, and the ring before p0 is given up.
@@ -115,7 +107,7 @@ struct Stream {
         const int c0 = p0 / kChunk;
         if (c0 >= issued || c0 + kRing / kChunk < issued) seek(p0);  // rows were left out
         if (c0 + kRing / kChunk > issued) {
-            sync();  // every warp is done with what is overwritten
+            __syncwarp();  // every lane is done with what is overwritten
             do issue();
             while (c0 + kRing / kChunk > issued);
         }
@@ -128,7 +120,7 @@ struct Stream {
             asm volatile("cp.async.wait_group 2;" ::: "memory");
         else
             asm volatile("cp.async.wait_group 3;" ::: "memory");
-        sync();
+        __syncwarp();
     }
 };
 
@@ -250,6 +242,21 @@ struct RowWalk {
         }
     }
     __device__ __forceinline__ int offset(int r) const { return __shfl_sync(kFullMask, held, r - at); }
+    __device__ __forceinline__ void range(int r, int& p0, int& p1) {
+        hold(r, 1);
+        p0 = offset(r);
+        p1 = max(offset(r + 1), p0);
+    }
+    // Whether one of rows r0 .. r1 - 1 has over `most` entries.
+    __device__ __forceinline__ bool any_over(int r0, int r1, int most) {
+        bool over = false;
+        for (int r = r0; r < r1; r += 31) {
+            hold(r, 31);
+            const int next = __shfl_down_sync(kFullMask, held, 1);
+            over = over || (lane < 31 && r + lane < r1 && next - held > most);
+        }
+        return over;
+    }
 };
 
 // Share g of G of nnz entries.
