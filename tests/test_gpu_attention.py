@@ -681,3 +681,54 @@ def test_attention_equal_shares(usm, kind, maps, dtype, D, N, biased):
     need = usm.load().csr_attention_workspace_bytes(p["M"], p["K"], D, N, p["nnz"], int(maps == 2), int(dtype == "bf16"))
     assert need > 0
     run_attention(usm, p, D, N, maps, dtype, biased, pad=True)
+
+
+def gaps(kind):
+    """Runs of thousands of rows without entries: between rows, before the first
+    and behind the last (a padded batch)."""
+    rng = np.random.default_rng([23, sorted(["between", "ends"]).index(kind)])
+    lengths = np.zeros(20000, dtype=np.int64)
+    if kind == "between":
+        lengths[rng.choice(20000, 300, replace=False)] = rng.integers(1, 700, 300)
+        lengths[[5000, 5001, 5002, 5003, 12000]] = [1700, 3, 0, 5000, 2500]
+    else:
+        lengths[9000:9400] = rng.integers(0, 700, 400)
+        lengths[9400] = 3000
+    seg, cols = 1000, 6000
+    ro, ci = W.csr_from_lengths(rng, lengths, cols, np.arange(20000) // seg * cols)
+    return dict(rng=rng, ro=ro, ci=ci, M=20000, K=20 * cols, cols=cols, seg=seg, blocks=20, nnz=ci.size,
+                heads=R.head_of_rows(20000, seg, HEADS), longest=int(lengths.max()))
+
+
+@pytest.mark.parametrize("kind", ["between", "ends"])
+def test_runs_of_empty_rows(usm, kind):
+    p = gaps(kind)
+    rng, ro, ci = p["rng"], dev(p["ro"]), dev(p["ci"])
+    bmap, q_offset, table = bias_inputs(p)
+    kw = dict(seg_rows=p["seg"], seg_cols=p["cols"], q_offset=dev(q_offset))
+    k = R.bucket_of_entries(p["ro"], p["ci"], bmap, p["seg"], p["cols"], q_offset, table.shape[1])
+    r = R.rows_of(p["ro"])
+    s1, s2 = scores_of(p, rng), scores_of(p, rng)
+    assert np.array_equal(host(usm.rel_bias(ro, ci, put(s1), put(table), dev(bmap), **kw)), s1 + table[p["heads"][r], k])
+    ds = rng.integers(-8, 9, p["nnz"]).astype(np.float32)
+    want = np.bincount(p["heads"][r] * table.shape[1] + k, ds, table.size).reshape(table.shape)
+    assert np.array_equal(got(usm.rel_bias_grad(ro, ci, put(ds), *table.shape, dev(bmap), **kw)), want)
+    lam = rng.uniform(0.1, 0.9, HEADS).astype(np.float32)
+    lr = lam.astype(np.float64)[p["heads"]]
+    E = R.softmax_error(p["longest"], SPREAD)
+    size = R.row_softmax(p["ro"], s1) + lr[r] * R.row_softmax(p["ro"], s2)
+    assert_near(got(usm.diff_softmax(ro, put(s1), put(s2), put(lam), seg_rows=p["seg"])), R.diff_map(p["ro"], s1, s2, lr),
+                (E + 2 * U) * size, "map")
+    dout = rng.standard_normal(p["nnz"]).astype(np.float32)
+    g1, g2, dlam = R.diff_grad(p["ro"], s1, s2, lr, dout, HEADS, p["heads"])
+    o1, o2, ol = usm.diff_softmax_grad(ro, put(s1), put(s2), put(lam), put(dout), seg_rows=p["seg"])
+    t1, _ = grad_bound(p, s1, dout, 1.0)
+    t2, c2 = grad_bound(p, s2, dout, lr[r])
+    assert_near(got(o1), g1, t1, "dscores1")
+    assert_near(got(o2), g2, t2, "dscores2")
+    rows = np.bincount(p["heads"], minlength=HEADS)
+    csize = np.bincount(p["heads"], np.abs(R.softmax_grad(p["ro"], s2, dout)[2]), HEADS)
+    assert_near(got(ol), dlam, np.bincount(p["heads"], c2, HEADS) + rows * U * csize, "dlambda")
+    assert_near(got(usm.row_softmax_grad(ro, put(s1), put(dout))), R.softmax_grad(p["ro"], s1, dout)[0], t1, "softmax gradient")
+    for dtype in ("bf16", "f32"):
+        run_attention(usm, p, 64, 64, 2, dtype, False)

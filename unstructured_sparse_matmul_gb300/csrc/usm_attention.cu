@@ -584,14 +584,30 @@ struct Walk {
     const int* ro;
     int nnz, M, r, p, row_end, end;  // at entry p of row r, which ends at row_end; the share ends at `end`
 
+    // The last of rows [lo, M) that starts at or before entry p (32 candidates a
+    // round).
+    __device__ __forceinline__ int row_of(int lo) const {
+        for (int n = M - lo; n > 1;) {
+            const int step = (int)((n + 31LL) / 32), lane = threadIdx.x & 31;
+            const bool in = (long long)lane * step < n;
+            const unsigned before = __ballot_sync(kFullMask, in && __ldg(ro + lo + (in ? lane * step : 0)) <= p);
+            const int skip = before ? (31 - __clz(before)) * step : 0;
+            lo += skip;
+            n = min(step, n - skip);
+        }
+        return lo;
+    }
     // To the first row at or after r that has entries from p on.
     __device__ __forceinline__ void settle() {
-        while (p < end && r < M) {
+        if (p < end && r < M) {
             int b;
             row_range(ro, r, nnz, b, row_end);
             p = max(p, b);
-            if (p < row_end) return;
-            ++r;
+            if (p >= row_end) {  // over the rows without entries
+                r = row_of(r);
+                row_range(ro, r, nnz, b, row_end);
+            }
+            if (p >= b && p < min(row_end, end)) return;
         }
         p = end;
     }
@@ -623,14 +639,7 @@ __global__ void __launch_bounds__(Row::R::kWarps * 32)
     if (g >= G) return;  // no barriers below: warps work alone
     const int begin = share_first(a.nnz, g, G);
     Walk walk{a.row_offsets, a.nnz, a.M, 0, begin, 0, share_first(a.nnz, g + 1, G)};
-    // The last row that starts at or before `begin` (32 candidates a round).
-    for (int lo = 0, hi = a.M; hi - lo > 1;) {
-        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const unsigned before = __ballot_sync(kFullMask, i < hi && __ldg(a.row_offsets + i) <= begin);
-        const int last = before ? 31 - __clz(before) : 0;
-        walk.r = lo = lo + last * step;
-        hi = min(hi, lo + step);
-    }
+    walk.r = walk.row_of(0);
     walk.settle();
 
     R ring;
@@ -788,7 +797,7 @@ struct Launch {
             if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
             kernel<<<(G + R::kWarps - 1) / R::kWarps, R::kWarps * 32, R::kSmem, stream>>>(a, parts, cut_rows, G);
             const dim3 grid((unsigned)(G + ((long long)a.M + 255) / 256), (a.N + 31) / 32);
-            return launch_next(attention_join_kernel<Row::kMaps>, grid, 256, stream, a, (const float*)parts,
+            return launch_next(attention_join_kernel<Row::kMaps>, grid, 256, 1, stream, a, (const float*)parts,
                                (const int*)cut_rows, G);
         }
         // CTAs a row: more until the rows fill the SMs or a row's windows (on

@@ -127,20 +127,24 @@ inline bool allow_shared(Kernel kernel, int smem) {
                cudaSuccess;
 }
 
-// A second kernel that may be brought to the SMs while the stream's last one still
-// runs (which calls let_next_start()); it reads nothing of that one before its own
-// await_previous(), which returns once all of it is done and visible.
+// A second kernel (in clusters of `cluster` CTAs) that may be brought to the SMs
+// while the stream's last one still runs, which calls let_next_start(); it reads
+// nothing of that one before its own await_previous(), which returns once all of
+// it is done and visible.
 template <class... P, class... A>
-inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, int cluster, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 #ifdef __CUDACC__

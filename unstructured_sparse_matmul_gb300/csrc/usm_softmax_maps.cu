@@ -532,8 +532,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
     st.seek(t0);  // the copies need not wait for the search
     int r0, r1;
     first_rows_from(a.row_offsets, a.M, t0, t1, lane, r0, r1);
-    if (g >= G) r0 = a.M;  // rows without entries at the very end belong to the last share
-    if (g + 1 >= G) r1 = a.M;
     RowWalk walk{a.row_offsets, a.M, a.nnz, lane, -64, 0};
     int p0, p1;
     bool any_long = false;
@@ -583,9 +581,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
         const int begin = walk.offset(r), mid = max(walk.offset(r + 1), begin), far = max(walk.offset(r + 2), mid);
         const bool pair = r + 1 < r1 && far - begin <= kRingRow && abs((mid - begin) - (far - mid)) < 256;
         const int end = pair ? far : mid, half = pair ? lane >> 4 : 0, row = r + half;
+        if (begin == end) {
+            r = walk.with_entries(r, r1);
+            continue;
+        }
         r += pair ? 2 : 1;
         if (end - begin > kRingRow) continue;  // a long row
-        if (begin < end) st.need(begin, end);
+        st.need(begin, end);
         p0 = half ? mid : begin;
         p1 = half ? far : mid;
         if (TWO && row >= block_end) {
@@ -593,12 +595,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
             block_end = (block + 1LL) * a.seg_rows;
             lam = __ldg(a.lambda + block % a.heads);
         }
-        bool done = true;
-        if (begin < end) done = ring_row<TWO, GRAD, DIN, OUT, false>(a, st, pair ? 16 : 32, row, lam, p0, p1, vec);
-        if (p0 == p1) {
-            if (GRAD && TWO && a.row_c2 && (lane & 15) == 0) a.row_c2[row] = 0.f;
-            done = true;
-        }
+        bool done = ring_row<TWO, GRAD, DIN, OUT, false>(a, st, pair ? 16 : 32, row, lam, p0, p1, vec);
+        done = done || p0 == p1;
         for (unsigned again = __ballot_sync(kFullMask, !done) & (pair ? 0x10001u : 1u); again; again &= again - 1) {
             const int from = __ffs(again) - 1;
             max_row<TWO, GRAD, DIN, OUT>(a, st, __shfl_sync(kFullMask, row, from), __shfl_sync(kFullMask, lam, from),
@@ -618,33 +616,51 @@ __global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const 
     const int r = blockIdx.x / ctas;
     int p0, p1;
     row_range(a.row_offsets, r, a.nnz, p0, p1);
-    if (p0 == p1) {
-        if (GRAD && TWO && a.row_c2 && rank == 0 && threadIdx.x == 0) a.row_c2[r] = 0.f;
-        return;
-    }
+    if (p0 == p1) return;
     const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
     block_row<TWO, GRAD, DIN, OUT, kClusterWarps>(a, r, lam, p0, p1, sh, ctas, rank);
 }
 
-// dλ[h] = -Σ c2 over head h's rows: a CTA per head, a fixed order.
-__global__ void __launch_bounds__(1024) lambda_grad_kernel(int M, int blocks, int heads, int seg_rows,
-                                                           const float* row_c2, float* __restrict__ dlambda) {
-    __shared__ float warp_part[32];
+// dλ[h] = -Σ c2 over head h's rows (those with entries: the others have no c2): a
+// cluster per head, a fixed order.  CTAs are small, so that they fit beside those
+// of the kernel before (with 1024 threads they start after it: 3 us later).
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) lambda_grad_kernel(const MapArgs a, int blocks, float* __restrict__ dlambda) {
+    __shared__ float warp_part[kSumThreads / 32], whole;
     await_previous();
-    const int head = blockIdx.x, t = threadIdx.x, lane = t & 31;
+    const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
+    const int head = blockIdx.x / ctas, t = threadIdx.x, lane = t & 31;
     float x = 0.f;
-    for (long long b = head; b < blocks; b += heads) {
-        const long long r0 = b * seg_rows;
-        const int n = (int)min((long long)seg_rows, M - r0);
-        for (int i = t; i < n; i += 1024) x += row_c2[r0 + i];
+    // Rows of all of the head's blocks, one after the other.
+    const long long rows = head < blocks ? ((blocks - 1 - head) / a.heads + 1LL) * a.seg_rows : 0;
+    // Four rows a thread in flight.
+    for (long long i0 = rank * kSumThreads + t; i0 < rows; i0 += 4 * kSumThreads * ctas) {
+        float c2[4];
+        bool some[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const unsigned i = (unsigned)min(i0 + u * kSumThreads * ctas, rows - 1);
+            const unsigned block = i / (unsigned)a.seg_rows, row = i - block * a.seg_rows;
+            const long long r = (head + (long long)block * a.heads) * a.seg_rows + row, at = min(r, a.M - 1LL);
+            some[u] = i0 + u * kSumThreads * ctas < rows && r < a.M && __ldg(a.row_offsets + at) < __ldg(a.row_offsets + at + 1);
+            c2[u] = a.row_c2[at];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x += some[u] ? c2[u] : 0.f;
     }
     x = warp_sum(x);
     if (lane == 0) warp_part[t >> 5] = x;
     __syncthreads();
     if (t < 32) {
-        x = warp_sum(warp_part[lane]);
-        if (lane == 0) dlambda[head] = -x;
+        x = warp_sum(lane < kSumThreads / 32 ? warp_part[lane] : 0.f);
+        if (lane == 0) whole = x;
     }
+    if (ctas > 1) cluster_sync();
+    if (rank == 0 && t == 0) {
+        for (int i = 1; i < ctas; ++i) x += load_cluster(smem_addr(&whole), i);
+        dlambda[head] = -x;
+    }
+    if (ctas > 1) cluster_sync();  // no CTA leaves what another may still read
 }
 
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
@@ -700,8 +716,11 @@ int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream) { return laun
 int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stream) {
     const int r = launch_map<true, true>(a, stream);
     if (r != USM_OK || !dlambda) return r;
-    return launch_next(lambda_grad_kernel, a.heads, 1024, stream, a.M, query_blocks(a.M, a.seg_rows), a.heads, a.seg_rows,
-                       (const float*)a.row_c2, dlambda);
+    const int blocks = query_blocks(a.M, a.seg_rows);
+    const long long rows = (blocks + a.heads - 1LL) / a.heads * a.seg_rows;  // of the first head, the most
+    int ctas = 1;
+    while (ctas < 8 && rows > 4LL * kSumThreads * ctas) ctas *= 2;
+    return launch_next(lambda_grad_kernel, a.heads * ctas, kSumThreads, ctas, stream, a, blocks, dlambda);
 }
 
 }  // namespace usm

@@ -242,18 +242,34 @@ struct RowWalk {
         }
     }
     __device__ __forceinline__ int offset(int r) const { return __shfl_sync(kFullMask, held, r - at); }
-    __device__ __forceinline__ void range(int r, int& p0, int& p1) {
-        hold(r, 1);
-        p0 = offset(r);
-        p1 = max(offset(r + 1), p0);
+    // The first row from r on (r < r1) that has entries, or r1.  Runs of rows
+    // without any are passed by a search.
+    __device__ __forceinline__ int with_entries(int r, int r1) {
+        while (true) {
+            hold(r, 1);
+            const int next = __shfl_down_sync(kFullMask, held, 1);
+            const unsigned some = __ballot_sync(kFullMask, lane < 31 && lane >= r - at && next > held);
+            if (some) return min(at + __ffs(some) - 1, r1);
+            const int p = offset(at + 31);
+            if (r1 - at <= 31 || p >= nnz) return r1;
+            r = at + 31;
+            hold(r, 31);
+            if (offset(r + 31) > p) continue;
+            int after, same;
+            first_rows_from(ro, M, p + 1, p + 1, lane, after, same);
+            r = max(after - 1, r + 31);
+            if (r >= r1) return r1;
+        }
     }
     // Whether one of rows r0 .. r1 - 1 has over `most` entries.
     __device__ __forceinline__ bool any_over(int r0, int r1, int most) {
         bool over = false;
-        for (int r = r0; r < r1; r += 31) {
+        for (int r = with_entries(r0, r1); r < r1;) {
             hold(r, 31);
             const int next = __shfl_down_sync(kFullMask, held, 1);
-            over = over || (lane < 31 && r + lane < r1 && next - held > most);
+            over = over || (lane < min(31, r1 - at) && next - held > most);
+            if (r1 - at <= 31) break;
+            r = with_entries(at + 31, r1);
         }
         return over;
     }
