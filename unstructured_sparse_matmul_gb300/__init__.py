@@ -419,10 +419,10 @@ def _entries(n: int) -> int:
     return n
 
 
-def _int32(**values):
-    for name, v in values.items():
-        if not -2**31 <= v < 2**31:
-            raise ValueError(f"{name} = {v} does not fit 32 bits")
+def _int32(values, names):
+    if not -2**31 <= min(values) <= max(values) < 2**31:
+        name, v = next((n, v) for n, v in zip(names, values) if not -2**31 <= v < 2**31)
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 
 def _out(out, like, n, dtype, index, T, name="out"):
@@ -446,7 +446,7 @@ def _workspace(workspace, need: int, like, T):
 
 def _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, index, T, table=None):
     """The usm_rel_bias struct (and nothing that outlives the call)."""
-    _int32(seg_rows=seg_rows, seg_cols=seg_cols, num_heads=num_heads, num_buckets=num_buckets)
+    _int32((seg_rows, seg_cols, num_heads, num_buckets), ("seg_rows", "seg_cols", "num_heads", "num_buckets"))
     _array(bucket_map, "bucket_map", index, T.i32)
     n = bucket_map.numel()
     if n < 3 or n % 2 == 0:
@@ -486,7 +486,7 @@ def rel_bucket_map(num_buckets: int, max_distance: int, causal: bool = False, de
     -max_distance..max_distance, logarithmic past num_buckets/2 (causal) or
     num_buckets/4; see rel_bucket_build."""
     T, lib = _types(), load()
-    _int32(num_buckets=num_buckets, max_distance=max_distance)
+    _int32((num_buckets, max_distance), ("num_buckets", "max_distance"))
     out = T.torch.empty(max(2 * max_distance + 1, 1), dtype=T.i32[0], device="cuda" if device is None else device)
     index = out.get_device()
     _array(out, "bucket_map", index, T.i32)
@@ -556,7 +556,7 @@ def diff_softmax(row_offsets, scores1, scores2, lam, seg_rows: int = 0, out=None
     nnz = _entries(scores1.numel())
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
-    _int32(seg_rows=seg_rows)
+    _int32((seg_rows, 0), ("seg_rows",))
     out = _out(out, scores1, nnz, out_dtype, index, T)
     _run("csr_diff_softmax", lib.csr_diff_softmax, index, T, M, nnz, row_offsets.data_ptr(), scores1.data_ptr(),
          scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, out.data_ptr(), _code(out, T))
@@ -576,7 +576,7 @@ def diff_softmax_grad(row_offsets, scores1, scores2, lam, dout, seg_rows: int = 
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
     _array(dout, "dout", index, T.real, nnz)
-    _int32(seg_rows=seg_rows)
+    _int32((seg_rows, 0), ("seg_rows",))
     if out_dtype is None:
         given = out1 if out1 is not None else out2
         out_dtype = T.f32[0] if given is None else given.dtype
@@ -611,10 +611,13 @@ def _operand(t, name, index, dtypes, rows, cols):
     """A dense operand of the given shape as the library reads it, and its
     leading dimension (a copy only where rows are not 16-byte aligned)."""
     _tensor(t, name, index, dtypes, 2)
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {(rows, cols)}")
-    t = _tma_ready(t)
-    return t, t.stride(0)
+    ld, unit = t.stride()
+    if unit != 1 or ld < cols or (t.data_ptr() | ld * t.element_size()) & 15:
+        t = _tma_ready(t)
+        ld = t.stride(0)
+    return t, ld
 
 
 @_on_stream
@@ -637,7 +640,7 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     Q, ldq = _operand(Q, "Q", index, dt, M, D)
     Km, ldk = _operand(Km, "Km", index, dt, K, D)
     V, ldv = _operand(V, "V", index, dt, K, N)
-    _int32(seg_rows=seg_rows)
+    _int32((seg_rows, 0), ("seg_rows",))
     heads, ldq2, ldk2, b = 1, 0, 0, None
     if lam is None:
         if Q2 is not None or K2 is not None:
@@ -657,8 +660,8 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     elif bucket_map is not None or q_offset is not None:
         raise ValueError("bucket_map and q_offset need a table")
     if out is None:
-        out = _new_dense_out(M, N, Km.device)
-        ldc = out.stride(0)
+        out = _new_dense_out(M, N, V.device) if N % 4 or N == 0 else T.empty((M, N), dtype=T.f32[0], device=V.device)
+        ldc = max(out.stride(0), N)
     else:
         _tensor(out, "out", index, T.f32, 2)
         if tuple(out.shape) != (M, N):
