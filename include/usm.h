@@ -349,7 +349,9 @@ int csr_rel_bias_grad(int M, int K, int nnz, const int *row_offsets, const int *
  * Masked entries: a score of -inf has probability 0 in its map; a row whose
  * scores are all -inf has a zero map, and an empty row writes nothing.  NaN or
  * +inf scores make their row's outputs NaN.
- * Maxima, sums and the difference are fp32; exponentials are CUDA's __expf.
+ * Sums and the difference are fp32.  Exponentials are the GPU's 2^x with x =
+ * (s - m)·log2 e, relative error at most |x|·2^-24 + 2^-22; m may be another of
+ * the row's scores than the largest (x < 31 then; the quotients are the same).
  */
 int csr_diff_softmax(int M, int nnz, const int *row_offsets, const float *scores1, const float *scores2,
                      const float *lambda, int num_heads, int seg_rows, void *out, usm_dtype out_dtype,

@@ -359,14 +359,14 @@ def _on_stream(fn):
 
 class _Types:
     """Element types the operations take (filled in once torch is there)."""
-    torch = i32 = f32 = real = empty = raw_stream = None
+    torch = i32 = f32 = real = empty = current_device = raw_stream = None
 
 
 def _types():
     if _Types.torch is None:
         torch = _torch()
         _Types.i32, _Types.f32, _Types.real = (torch.int32,), (torch.float32,), (torch.float32, torch.bfloat16)
-        _Types.empty = staticmethod(torch.empty)
+        _Types.empty, _Types.current_device = staticmethod(torch.empty), staticmethod(torch.cuda.current_device)
         # The current stream's handle; the public way builds a Stream object for it.
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _Types.raw_stream = staticmethod(raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
@@ -391,10 +391,11 @@ def _tensor(t, name, index, dtypes, dims):
 
 def _array(t, name, index, dtypes, n=None):
     """A contiguous 1-D tensor, of n elements unless None."""
-    _tensor(t, name, index, dtypes, 1)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if n is not None and t.numel() != n:
+    if (t is None or t.dtype not in dtypes or t.dim() != 1 or t.get_device() != index or index < 0
+            or not t.is_contiguous() or (n is not None and t.numel() != n)):
+        _tensor(t, name, index, dtypes, 1)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     return t
 
@@ -406,8 +407,7 @@ def _device_of(t, name) -> int:
 
 
 def _rows(row_offsets, index, T) -> int:
-    _array(row_offsets, "row_offsets", index, T.i32)
-    M = row_offsets.numel() - 1
+    M = _array(row_offsets, "row_offsets", index, T.i32).numel() - 1
     if not 0 <= M < 2**31:
         raise ValueError(f"row_offsets has {M + 1} elements: from 1 to 2**31 are expected")
     return M
@@ -420,7 +420,7 @@ def _entries(n: int) -> int:
 
 
 def _int32(values, names):
-    if not -2**31 <= min(values) <= max(values) < 2**31:
+    if min(values) < -2**31 or max(values) >= 2**31:
         name, v = next((n, v) for n, v in zip(names, values) if not -2**31 <= v < 2**31)
         raise ValueError(f"{name} = {v} does not fit 32 bits")
 
@@ -470,11 +470,10 @@ def _code(t, T) -> int:
 
 def _run(name, fn, index, T, *args):
     """Call the library on device `index`, on its current stream."""
-    cuda = T.torch.cuda
-    if index == cuda.current_device():
+    if index == T.current_device():
         code = fn(*args, T.raw_stream(index))
     else:
-        with cuda.device(index):
+        with T.torch.cuda.device(index):
             code = fn(*args, T.raw_stream(index))
     if code != 0:
         raise USMError(name, code)
@@ -556,7 +555,7 @@ def diff_softmax(row_offsets, scores1, scores2, lam, seg_rows: int = 0, out=None
     nnz = _entries(scores1.numel())
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
-    _int32((seg_rows, 0), ("seg_rows",))
+    _int32((seg_rows, 0), ("seg_rows", ""))
     out = _out(out, scores1, nnz, out_dtype, index, T)
     _run("csr_diff_softmax", lib.csr_diff_softmax, index, T, M, nnz, row_offsets.data_ptr(), scores1.data_ptr(),
          scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, out.data_ptr(), _code(out, T))
@@ -576,7 +575,7 @@ def diff_softmax_grad(row_offsets, scores1, scores2, lam, dout, seg_rows: int = 
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
     _array(dout, "dout", index, T.real, nnz)
-    _int32((seg_rows, 0), ("seg_rows",))
+    _int32((seg_rows, 0), ("seg_rows", ""))
     if out_dtype is None:
         given = out1 if out1 is not None else out2
         out_dtype = T.f32[0] if given is None else given.dtype
@@ -640,7 +639,7 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     Q, ldq = _operand(Q, "Q", index, dt, M, D)
     Km, ldk = _operand(Km, "Km", index, dt, K, D)
     V, ldv = _operand(V, "V", index, dt, K, N)
-    _int32((seg_rows, 0), ("seg_rows",))
+    _int32((seg_rows, 0), ("seg_rows", ""))
     heads, ldq2, ldk2, b = 1, 0, 0, None
     if lam is None:
         if Q2 is not None or K2 is not None:

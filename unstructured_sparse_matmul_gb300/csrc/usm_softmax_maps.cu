@@ -18,9 +18,10 @@
 //   - Two rows of about a length are taken at once, by half a warp each (43 us
 //     with one at a time).
 //   - The maximum is not looked for (45 us with it): exponents are measured from
-//     the largest of a row's first entries, which gives the same quotients unless
-//     a sum passes 2^100; a row whose sum does is done again from its maximum, as
-//     are rows with masks at their start or values that are not finite.
+//     the largest of a row's first entries, which gives the same quotients.  An
+//     exponent x = s·log2 e - m·log2 e is off by half a step, 2^-20 for |x| up to
+//     32 (7e-7 of the weight); a row whose sum passes 2^31 is done again from its
+//     maximum, as are rows with masks at their start or values that are not finite.
 //   - Rows over 1536 entries are first taken by the whole CTA (8x4096 rows without
 //     any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
 //     each (launch_rows).
@@ -417,7 +418,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
     auto at_weight = [&](float2 w, float2 v) { return make_float2(w.x == 0.f ? 0.f : v.x, w.y == 0.f ? 0.f : v.y); };
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        fine = fine && z[k] < 0x1p100f;
+        fine = fine && z[k] < 0x1p31f;
         if constexpr (GRAD) guarded = guarded || !(fabsf(c[k]) < 0x1p100f);
     }
     if (GRAD && __any_sync(kFullMask, guarded)) {
@@ -510,7 +511,7 @@ constexpr int ctas_per_sm() {
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN>>())
     stream_rows_kernel(const MapArgs a, int G, bool aligned, bool vec) {
-    if constexpr (TWO && GRAD) let_next_start();
+    if (TWO && GRAD && a.row_c2) let_next_start();
     using S = MapStream<TWO, GRAD, DIN>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ BlockStats<kWarps> sh;
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
 constexpr int kClusterWarps = 8;
 template <bool TWO, bool GRAD, bool DIN, bool OUT>
 __global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const MapArgs a) {
-    if constexpr (TWO && GRAD) let_next_start();
+    if (TWO && GRAD && a.row_c2) let_next_start();
     __shared__ BlockStats<kClusterWarps> sh;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
@@ -719,7 +720,7 @@ int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stre
     const int blocks = query_blocks(a.M, a.seg_rows);
     const long long rows = (blocks + a.heads - 1LL) / a.heads * a.seg_rows;  // of the first head, the most
     int ctas = 1;
-    while (ctas < 8 && rows > 4LL * kSumThreads * ctas) ctas *= 2;
+    while (ctas < 8 && rows > 4LL * kSumThreads * ctas && (long long)a.heads * ctas < (1 << 24)) ctas *= 2;
     return launch_next(lambda_grad_kernel, a.heads * ctas, kSumThreads, ctas, stream, a, blocks, dlambda);
 }
 
