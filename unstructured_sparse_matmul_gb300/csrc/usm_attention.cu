@@ -704,31 +704,45 @@ __global__ void __launch_bounds__(Row::R::kWarps * 32)
     if (lane == 0) cut_rows[g] = cut;
 }
 
-// CTA (g, c), g < G: columns 32c..32c+31 of the row that goes on after share g,
-// if one does.  Eight threads to a column, each joining every eighth part.  The
-// CTAs past G write zeros to the rows without entries, 256 rows each.
-template <int MAPS>
+// Joins the parts of rows that several shares hold and writes zeros to the rows
+// without entries: columns 32c..32c+31 by CTA (i, c), eight threads to a column,
+// each joining every eighth part.  BY_ROWS, for no more rows than shares: CTA
+// (r, c) looks after row r.  Else CTA (g, c), g < G, after the row that goes on
+// after share g, if one does, and the CTAs past G after 256 rows each.  (256 rows
+// of 1824 shares: 5 us by shares, most of whose CTAs find nothing to do, 4 by
+// rows.)
+template <int MAPS, bool BY_ROWS>
 __global__ void __launch_bounds__(256)
     attention_join_kernel(const AttnArgs a, const float* parts, const int* cut_rows, int G) {
     __shared__ float sums[8][MAPS][3][32];
-    await_previous();
-    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, g0 = blockIdx.x;
-    int p0, p1;
-    if (g0 >= G) {
-        const long long r0 = (g0 - G) * 256LL + grp * 32;
-        bool empty = false;
-        if (blockIdx.y == 0 && r0 + lane < a.M) {
-            row_range(a.row_offsets, (int)r0 + lane, a.nnz, p0, p1);
-            empty = p0 == p1;
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, j = blockIdx.y * 32 + lane;
+    int g0 = blockIdx.x, r = blockIdx.x, p0, p1;
+    if constexpr (BY_ROWS) row_range(a.row_offsets, r, a.nnz, p0, p1);
+    await_previous();  // in every CTA: the kernel must not end before the one it follows
+    if constexpr (BY_ROWS) {
+        if (p0 == p1) {
+            if (grp == 0 && j < a.N) a.C[(long long)r * a.ldc + j] = 0.f;
+            return;
         }
-        for (unsigned rows = __ballot_sync(kFullMask, empty); rows; rows &= rows - 1)
-            for (int j = lane; j < a.N; j += 32) a.C[(r0 + __ffs(rows) - 1) * a.ldc + j] = 0.f;
-        return;
+        g0 = share_of(p0, a.nnz, G);
+    } else {
+        if (g0 >= G) {
+            const long long r0 = (g0 - G) * 256LL + grp * 32;
+            bool empty = false;
+            if (blockIdx.y == 0 && r0 + lane < a.M) {
+                row_range(a.row_offsets, (int)r0 + lane, a.nnz, p0, p1);
+                empty = p0 == p1;
+            }
+            for (unsigned rows = __ballot_sync(kFullMask, empty); rows; rows &= rows - 1)
+                for (int c = lane; c < a.N; c += 32) a.C[(r0 + __ffs(rows) - 1) * a.ldc + c] = 0.f;
+            return;
+        }
+        r = cut_rows[g0];
+        if (r < 0) return;
+        row_range(a.row_offsets, r, a.nnz, p0, p1);
     }
-    const int r = cut_rows[g0], j = blockIdx.y * 32 + lane;
-    if (r < 0) return;
-    row_range(a.row_offsets, r, a.nnz, p0, p1);
     const int g1 = p0 < p1 ? share_of(p1 - 1, a.nnz, G) : g0;
+    if (BY_ROWS && g0 == g1) return;
     const int col = min(j, a.N - 1);
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
@@ -796,9 +810,13 @@ struct Launch {
             const auto kernel = attention_shares_kernel<Row>;
             if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
             kernel<<<(G + R::kWarps - 1) / R::kWarps, R::kWarps * 32, R::kSmem, stream>>>(a, parts, cut_rows, G);
-            const dim3 grid((unsigned)(G + ((long long)a.M + 255) / 256), (a.N + 31) / 32);
-            return launch_next(attention_join_kernel<Row::kMaps>, grid, 256, 1, stream, a, (const float*)parts,
-                               (const int*)cut_rows, G);
+            const unsigned strips = (a.N + 31) / 32;
+            if (a.M <= G)
+                return launch_next(attention_join_kernel<Row::kMaps, true>, dim3(a.M, strips), 256, 1, stream, a,
+                                   (const float*)parts, (const int*)cut_rows, G);
+            return launch_next(attention_join_kernel<Row::kMaps, false>,
+                               dim3((unsigned)(G + ((long long)a.M + 255) / 256), strips), 256, 1, stream, a,
+                               (const float*)parts, (const int*)cut_rows, G);
         }
         // CTAs a row: more until the rows fill the SMs or a row's windows (on
         // average) no longer give every warp one.

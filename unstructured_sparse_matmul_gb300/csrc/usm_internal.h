@@ -130,7 +130,8 @@ inline bool allow_shared(Kernel kernel, int smem) {
 // A second kernel (in clusters of `cluster` CTAs) that may be brought to the SMs
 // while the stream's last one still runs, which calls let_next_start(); it reads
 // nothing of that one before its own await_previous(), which returns once all of
-// it is done and visible.
+// it is done and visible, and which every CTA calls (so that this kernel's end is
+// the other's too).
 template <class... P, class... A>
 inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, int cluster, cudaStream_t stream, A... args) {
     cudaLaunchAttribute attrs[2];
