@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -69,6 +70,9 @@ class RelBias(ctypes.Structure):
     """usm_rel_bias of include/usm.h."""
     _fields_ = [("table", _vp), ("table_dtype", _i), ("num_heads", _i), ("num_buckets", _i), ("bucket_map", _vp),
                 ("max_distance", _i), ("seg_cols", _i), ("q_offset", _vp)]
+
+
+_pack_bias = struct.Struct("@PiiiPiiP").pack  # the same as bytes, in a quarter of the time
 
 
 # csr_validate result codes (usm_csr_check in include/usm.h).
@@ -420,9 +424,9 @@ def _entries(n: int) -> int:
 
 
 def _int32(values, names):
-    if min(values) < -2**31 or max(values) >= 2**31:
-        name, v = next((n, v) for n, v in zip(names, values) if not -2**31 <= v < 2**31)
-        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    for v in values:
+        if not -2**31 <= v < 2**31:
+            raise ValueError(f"{names[values.index(v)]} = {v} does not fit 32 bits")
 
 
 def _out(out, like, n, dtype, index, T, name="out"):
@@ -445,10 +449,9 @@ def _workspace(workspace, need: int, like, T):
 
 
 def _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, index, T, table=None):
-    """The usm_rel_bias struct (and nothing that outlives the call)."""
+    """The usm_rel_bias struct, as bytes that the call takes a pointer to."""
     _int32((seg_rows, seg_cols, num_heads, num_buckets), ("seg_rows", "seg_cols", "num_heads", "num_buckets"))
-    _array(bucket_map, "bucket_map", index, T.i32)
-    n = bucket_map.numel()
+    n = _array(bucket_map, "bucket_map", index, T.i32).numel()
     if n < 3 or n % 2 == 0:
         raise ValueError("bucket_map has 2*max_distance + 1 entries")
     if q_offset is not None:
@@ -456,8 +459,8 @@ def _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, i
         _array(q_offset, "q_offset", index, T.i32, blocks)
     if table is not None and not table.is_contiguous():
         raise ValueError("table must be contiguous")
-    return RelBias(None if table is None else table.data_ptr(), USM_F32 if table is None else _code(table, T), num_heads,
-                   num_buckets, bucket_map.data_ptr(), n // 2, seg_cols, _ptr(q_offset))
+    return _pack_bias(0 if table is None else table.data_ptr(), USM_F32 if table is None else _code(table, T), num_heads,
+                      num_buckets, bucket_map.data_ptr(), n // 2, seg_cols, 0 if q_offset is None else q_offset.data_ptr())
 
 
 def _code(t, T) -> int:
@@ -511,7 +514,7 @@ def rel_bias(row_offsets, col_indices, scores, table, bucket_map, seg_rows: int 
     b = _bias(bucket_map, heads, buckets, seg_rows, seg_cols, q_offset, M, index, T, table)
     out = _out(out, scores, nnz, T.f32[0], index, T)
     _run("csr_rel_bias", lib.csr_rel_bias, index, T, M, _ANY_COLUMN, nnz, row_offsets.data_ptr(),
-         col_indices.data_ptr(), scores.data_ptr(), seg_rows, ctypes.addressof(b), out.data_ptr())
+         col_indices.data_ptr(), scores.data_ptr(), seg_rows, b, out.data_ptr())
     return out
 
 
@@ -539,7 +542,7 @@ def rel_bias_grad(row_offsets, col_indices, dscores, num_heads: int, num_buckets
     need = lib.csr_rel_bias_grad_workspace_bytes(M, nnz, seg_rows, num_heads, num_buckets)
     ws = _workspace(workspace, need, dscores, T)
     _run("csr_rel_bias_grad", lib.csr_rel_bias_grad, index, T, M, _ANY_COLUMN, nnz, row_offsets.data_ptr(),
-         col_indices.data_ptr(), dscores.data_ptr(), _code(dscores, T), seg_rows, ctypes.addressof(b), out.data_ptr(),
+         col_indices.data_ptr(), dscores.data_ptr(), _code(dscores, T), seg_rows, b, out.data_ptr(),
          _ptr(ws), need)
     return out
 
@@ -555,7 +558,7 @@ def diff_softmax(row_offsets, scores1, scores2, lam, seg_rows: int = 0, out=None
     nnz = _entries(scores1.numel())
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
-    _int32((seg_rows, 0), ("seg_rows", ""))
+    _int32((seg_rows,), ("seg_rows",))
     out = _out(out, scores1, nnz, out_dtype, index, T)
     _run("csr_diff_softmax", lib.csr_diff_softmax, index, T, M, nnz, row_offsets.data_ptr(), scores1.data_ptr(),
          scores2.data_ptr(), lam.data_ptr(), lam.numel(), seg_rows, out.data_ptr(), _code(out, T))
@@ -575,7 +578,7 @@ def diff_softmax_grad(row_offsets, scores1, scores2, lam, dout, seg_rows: int = 
     _array(scores2, "scores2", index, T.f32, nnz)
     _array(lam, "lam", index, T.f32)
     _array(dout, "dout", index, T.real, nnz)
-    _int32((seg_rows, 0), ("seg_rows", ""))
+    _int32((seg_rows,), ("seg_rows",))
     if out_dtype is None:
         given = out1 if out1 is not None else out2
         out_dtype = T.f32[0] if given is None else given.dtype
@@ -639,7 +642,7 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     Q, ldq = _operand(Q, "Q", index, dt, M, D)
     Km, ldk = _operand(Km, "Km", index, dt, K, D)
     V, ldv = _operand(V, "V", index, dt, K, N)
-    _int32((seg_rows, 0), ("seg_rows", ""))
+    _int32((seg_rows,), ("seg_rows",))
     heads, ldq2, ldk2, b = 1, 0, 0, None
     if lam is None:
         if Q2 is not None or K2 is not None:
@@ -671,7 +674,7 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     ws = _workspace(workspace, need, Km, T)
     _run("csr_attention", lib.csr_attention, index, T, M, K, D, N, nnz, row_offsets.data_ptr(), col_indices.data_ptr(),
          Q.data_ptr(), ldq, Km.data_ptr(), ldk, _ptr(Q2), ldq2, _ptr(K2), ldk2, V.data_ptr(), ldv, scale, _ptr(lam),
-         heads, seg_rows, None if b is None else ctypes.addressof(b), out.data_ptr(), ldc, code, _ptr(ws), need)
+         heads, seg_rows, b, out.data_ptr(), ldc, code, _ptr(ws), need)
     return out
 
 
