@@ -22,8 +22,8 @@
 //     exponent x = s·log2 e - m·log2 e is off by half a step, 2^-20 for |x| up to
 //     32 (7e-7 of the weight); a row whose sum passes 2^31 is done again from its
 //     maximum, as are rows with masks at their start or values that are not finite.
-//   - Rows over 1536 entries are first taken by the whole CTA (8x4096 rows without
-//     any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
+//   - Rows that do not fit the ring are first taken by the whole CTA (8x4096 rows
+//     without any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
 //     each (launch_rows).
 #include <cmath>
 
@@ -35,6 +35,7 @@ namespace usm {
 namespace {
 
 constexpr int kSteps = 16;  // entries of a long row a thread keeps in registers
+constexpr int kTail = 16;   // and has in flight of the others (82 rows of 16384 entries among 2048: 27 us; 8: 29, 4: 33)
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -125,30 +126,36 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
                 d[i] = make_float2(e < n ? load_global<DIN>(dout, e) : 0.f, e + T < n ? load_global<DIN>(dout, e + T) : 0.f);
         }
     }
-    // Entries past the registers, four at a time: a running maximum and sums.
-    const int tail = t + kSteps * T;
+    // Entries past the registers, kTail at a time: a running maximum and sums.
+    const unsigned tail = t + kSteps * T, un = n;  // unsigned: a tail's end may pass 2^31
     Stat run[MAPS];
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) run[k] = {-INFINITY, 0.f, 0.f};
-#pragma unroll 1
-    for (int e = tail; e < n; e += 4 * T) {
-        float dy[4];
+    auto load_tail = [&](unsigned e, float (&y)[MAPS][kTail], float (&dy)[kTail]) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if constexpr (GRAD) dy[u] = e + u * T < n ? load_global<DIN>(dout, e + u * T) : 0.f;
+        for (int u = 0; u < kTail; ++u) {
+            const bool in = e + u * T < un;
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) y[k][u] = in ? s[k][e + u * T] : -INFINITY;
+            dy[u] = GRAD && in ? load_global<DIN>(dout, e + u * T) : 0.f;
+        }
+    };
+#pragma unroll 1
+    for (unsigned e = tail; e < un; e += kTail * T) {
+        float y[MAPS][kTail], dy[kTail];
+        load_tail(e, y, dy);
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
-            float y[4];
+            float top = run[k].m;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = e + u * T < n ? s[k][e + u * T] : -INFINITY;
-            const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), run[k].m);
+            for (int u = 0; u < kTail; ++u) top = fmaxf(top, y[k][u]);
             const float base = top == -INFINITY ? 0.f : top, f = __expf(run[k].m - base);
             run[k].z *= f;
             run[k].c *= f;
             run[k].m = top;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float w = __expf(y[u] - base);
+            for (int u = 0; u < kTail; ++u) {
+                const float w = __expf(y[k][u] - base);
                 run[k].z += w;
                 if constexpr (GRAD) run[k].c += weighted(w, dy[u]);
             }
@@ -265,7 +272,7 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
 
     // The results of two entries from their weights (and dout).  Gradients are
     // w·(inv·d - inv·c).
-    auto finish = [&](int e, const float2 (&w)[MAPS], float2 dy) {
+    auto finish = [&](unsigned e, const float2 (&w)[MAPS], float2 dy) {
         if constexpr (GRAD) {
 #pragma unroll
             for (int k = 0; k < MAPS; ++k) {
@@ -273,14 +280,14 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
                 float2 y = __fmul2_rn(w[k], __ffma2_rn(make_float2(inv[k], inv[k]), dy, make_float2(ic, ic)));
                 if (w[k].x == 0.f) y.x = 0.f;
                 if (w[k].y == 0.f) y.y = 0.f;
-                if (e < n) store_entry<OUT>(out[k], e, y.x);
-                if (e + T < n) store_entry<OUT>(out[k], e + T, y.y);
+                if (e < un) store_entry<OUT>(out[k], e, y.x);
+                if (e + T < un) store_entry<OUT>(out[k], e + T, y.y);
             }
         } else {
             float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
             y = __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y);
-            if (e < n) store_entry<OUT>(out[0], e, y.x);
-            if (e + T < n) store_entry<OUT>(out[0], e + T, y.y);
+            if (e < un) store_entry<OUT>(out[0], e, y.x);
+            if (e + T < un) store_entry<OUT>(out[0], e + T, y.y);
         }
     };
 #pragma unroll
@@ -291,19 +298,20 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
             for (int k = 0; k < MAPS; ++k) w[k] = x[k][i];
             finish(t + 2 * i * T, w, d[GRAD ? i : 0]);
         }
-#pragma unroll 2
-    for (int e = tail; e < n; e += 2 * T) {
-        float2 w[MAPS], dy = make_float2(0.f, 0.f);
-        if constexpr (GRAD) {
-            dy.x = load_global<DIN>(dout, e);
-            if (e + T < n) dy.y = load_global<DIN>(dout, e + T);
-        }
+#pragma unroll 1
+    for (unsigned e = tail; e < un; e += kTail * T) {
+        float y[MAPS][kTail], dy[kTail];
+        load_tail(e, y, dy);
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            const Base base(m[k]);
-            w[k] = make_float2(weight_of(s[k][e], base), weight_of(e + T < n ? s[k][e + T] : -INFINITY, base));
+        for (int u = 0; u < kTail; u += 2) {
+            float2 w[MAPS];
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                const Base base(m[k]);
+                w[k] = make_float2(weight_of(y[k][u], base), weight_of(y[k][u + 1], base));
+            }
+            finish(e + u * T, w, make_float2(dy[u], dy[u + 1]));
         }
-        finish(e, w, dy);
     }
 }
 
@@ -313,7 +321,7 @@ __device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0
     block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, 1, 0);
 }
 
-// A row [p0, p1) of 1 to kRingRow entries, which lies in the warp's ring, by the
+// A row [p0, p1), which lies in the warp's ring, by the
 // warp or by half of it (width 32 or 16, the same for all lanes; each half has its
 // own row then, which may be empty: false), walked twice: for weights and their
 // sums, and for results.  MAX: exponents are measured from the row's maximum; else
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
         const int end = min(max(__ldg(a.row_offsets + r1), 0), a.nnz);
         walk.hold(r0, 2);
         st.extend((int)(((long long)end + kChunk - 1) / kChunk));
-        any_long = walk.any_over(r0, r1, kRingRow);
+        any_long = walk.any_over(r0, r1);
     }
     if (lane == 0) {
         bounds[warp] = r0;
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
             bool mine = false;
             if (threadIdx.x < bounds[kWarps] - r) {
                 row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
-                mine = p1 - p0 > kRingRow;
+                mine = p0 < p1 && !ring_holds(p0, p1);
             }
             const unsigned mask = __ballot_sync(kFullMask, mine);
             if (lane == 0) is_long[warp] = mask;
@@ -580,14 +588,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
         // measured 41.0, 39.7 and 41.1 us).
         walk.hold(r, 2);
         const int begin = walk.offset(r), mid = max(walk.offset(r + 1), begin), far = max(walk.offset(r + 2), mid);
-        const bool pair = r + 1 < r1 && far - begin <= kRingRow && abs((mid - begin) - (far - mid)) < 256;
+        const bool pair = r + 1 < r1 && ring_holds(begin, far) && abs((mid - begin) - (far - mid)) < 256;
         const int end = pair ? far : mid, half = pair ? lane >> 4 : 0, row = r + half;
         if (begin == end) {
             r = walk.with_entries(r, r1);
             continue;
         }
         r += pair ? 2 : 1;
-        if (end - begin > kRingRow) continue;  // a long row
+        if (!ring_holds(begin, end)) continue;  // a long row
         st.need(begin, end);
         p0 = half ? mid : begin;
         p1 = half ? far : mid;
@@ -671,7 +679,7 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
     // A CTA of 8 warps a row where rows are long and too few to fill the GPU with
     // a warp each; a cluster while its CTAs are too few too and keep at least
     // half their registers' worth each.
-    if (mean > kRingRow && a.M <= 4 * sms) {
+    if (mean > kRing - kChunk && a.M <= 4 * sms) {
         int ctas = 1;
         while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kClusterWarps * 32 * kSteps / 2) ctas *= 2;
         cudaLaunchAttribute attr;

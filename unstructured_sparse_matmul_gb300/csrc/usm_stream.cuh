@@ -13,8 +13,11 @@
 namespace usm {
 
 constexpr int kChunk = 512, kRing = 4 * kChunk;
-// A run up to this long fits the ring wherever it starts.
-constexpr int kRingRow = 3 * kChunk;
+// Whether entries [p0, p1), one at least, fit the ring together: up to 1537 of them
+// do wherever they start, up to 2048 at the start of a chunk.
+__device__ __forceinline__ bool ring_holds(int p0, int p1) {
+    return (unsigned)(p1 - 1) / kChunk - (unsigned)p0 / kChunk < kRing / kChunk;
+}
 
 // Streams up to three arrays of E0, E1, E2 bytes an element (0: none).
 template <int E0, int E1, int E2>
@@ -101,7 +104,7 @@ struct Stream {
         issued = min(issued, limit);
         limit = new_limit;
     }
-    // Makes entries [p0, p1) (at most kRingRow, one at least) readable by every
+    // Makes entries [p0, p1) (one at least, no more than fit) readable by every
     // lane; runs come in order, and the ring before p0 is given up.
     __device__ __forceinline__ void need(int p0, int p1) {
         const int c0 = p0 / kChunk;
@@ -261,13 +264,13 @@ struct RowWalk {
             if (r >= r1) return r1;
         }
     }
-    // Whether one of rows r0 .. r1 - 1 has over `most` entries.
-    __device__ __forceinline__ bool any_over(int r0, int r1, int most) {
+    // Whether one of rows r0 .. r1 - 1 does not fit the ring.
+    __device__ __forceinline__ bool any_over(int r0, int r1) {
         bool over = false;
         for (int r = with_entries(r0, r1); r < r1;) {
             hold(r, 31);
             const int next = __shfl_down_sync(kFullMask, held, 1);
-            over = over || (lane < min(31, r1 - at) && next - held > most);
+            over = over || (lane < min(31, r1 - at) && next > held && !ring_holds(held, next));
             if (r1 - at <= 31) break;
             r = with_entries(at + 31, r1);
         }
