@@ -26,6 +26,7 @@
 //     without any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
 //     each (launch_rows).
 #include <cmath>
+#include <type_traits>
 
 #include "usm_cluster.cuh"
 #include "usm_internal.h"
@@ -458,41 +459,47 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
     if constexpr (TWO) inv[1] *= -lam;
 
     // Results.  Gradients are w·(inv·d - inv·c).
-    auto grad = [&](int k, float2 w, float2 d) {
-        const float ic = -inv[k] * c[k];
-        if (guarded) d = at_weight(w, d);
-        const float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
-        return guarded ? at_weight(w, y) : y;
-    };
     auto map = [&](const float2 (&w)[MAPS]) {
         const float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
         return TWO ? __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y) : y;
     };
-    if (rq.has_edge) {
-        if constexpr (GRAD) {
-            store_entry<OUT>(a.out1, rq.edge, grad(0, make_float2(xe[0], 0.f), make_float2(de, 0.f)).x);
-            if constexpr (TWO) store_entry<OUT>(a.out2, rq.edge, grad(1, make_float2(xe[1], 0.f), make_float2(de, 0.f)).x);
-        } else {
-            float2 w[MAPS];
+    auto results = [&](auto guard) {
+        auto grad = [&](int k, float2 w, float2 d) {
+            const float ic = -inv[k] * c[k];
+            if (guard()) d = at_weight(w, d);
+            const float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
+            return guard() ? at_weight(w, y) : y;
+        };
+        if (rq.has_edge) {
+            if constexpr (GRAD) {
+                store_entry<OUT>(a.out1, rq.edge, grad(0, make_float2(xe[0], 0.f), make_float2(de, 0.f)).x);
+                if constexpr (TWO) store_entry<OUT>(a.out2, rq.edge, grad(1, make_float2(xe[1], 0.f), make_float2(de, 0.f)).x);
+            } else {
+                float2 w[MAPS];
 #pragma unroll
-            for (int k = 0; k < MAPS; ++k) w[k] = make_float2(xe[k], 0.f);
-            store_entry<OUT>(a.out1, rq.edge, map(w).x);
+                for (int k = 0; k < MAPS; ++k) w[k] = make_float2(xe[k], 0.f);
+                store_entry<OUT>(a.out1, rq.edge, map(w).x);
+            }
         }
-    }
 #pragma unroll 1
-    for (unsigned q = first; q < rq.qe; q += step) {
-        float2 lo[MAPS], hi[MAPS];
+        for (unsigned q = first; q < rq.qe; q += step) {
+            float2 lo[MAPS], hi[MAPS];
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) weights(k, q, lo[k], hi[k]);
-        if constexpr (GRAD) {
-            float2 d0, d1;
-            lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-            store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
-            if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
-        } else {
-            store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
+            for (int k = 0; k < MAPS; ++k) weights(k, q, lo[k], hi[k]);
+            if constexpr (GRAD) {
+                float2 d0, d1;
+                lds_quad<DIN>(st.at(MAPS, q), d0, d1);
+                store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
+                if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
+            } else {
+                store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
+            }
         }
-    }
+    };
+    if (GRAD && guarded)
+        results(std::true_type{});
+    else
+        results(std::false_type{});
     return true;
 }
 

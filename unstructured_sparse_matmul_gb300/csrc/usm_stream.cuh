@@ -154,8 +154,9 @@ template <bool BF>
 __device__ __forceinline__ void store_quad(void* p, long long i, float2 lo, float2 hi, bool vec) {
     if constexpr (BF) {
         uint16_t* q = static_cast<uint16_t*>(p) + i;
-        const uint32_t a = f32_to_bf16_rne(lo.x) | ((uint32_t)f32_to_bf16_rne(lo.y) << 16);
-        const uint32_t b = f32_to_bf16_rne(hi.x) | ((uint32_t)f32_to_bf16_rne(hi.y) << 16);
+        uint32_t a, b;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(lo.y), "f"(lo.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(hi.y), "f"(hi.x));
         if (vec) {
             *reinterpret_cast<uint2*>(q) = make_uint2(a, b);
         } else {
