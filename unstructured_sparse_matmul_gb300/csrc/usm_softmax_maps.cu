@@ -10,20 +10,22 @@
 // through a ring in shared memory (usm_stream.cuh), so copies are in flight all
 // the time whatever the rows' arithmetic and lengths do.  An SM's shared memory
 // holds the rings of 8 to 12 warps, few to cover the latency of a row's
-// arithmetic, which is what is left to wait for:
+// arithmetic, which is what is left to wait for (figures: the differential map of
+// 8x4096 rows of 410 entries in a replayed graph):
 //   - A row is walked twice in the ring (weights and their sums; results), four
 //     entries a lane, in pairs of fp32 (f32x2).  Loops are short: rows read into
-//     registers, unrolled, measured 47 to 58 us where these take 40 (the
-//     differential map of 8x4096 rows of 410 entries).
-//   - Two rows of about a length are taken at once, by half a warp each (43 us
-//     with one at a time).
-//   - The maximum is not looked for (45 us with it): exponents are measured from
+//     registers, unrolled, measured 47 to 58 us where these took 45 and, with what
+//     follows, 37.  (Weights written back to the ring instead of formed twice save
+//     0.6 us, but the scores with them, which a second try needs.)
+//   - Two rows of about a length are taken at once, by half a warp each (42.7 to
+//     39.7 us).
+//   - The maximum is not looked for (45 to 42 us): exponents are measured from
 //     the largest of a row's first entries, which gives the same quotients.  An
 //     exponent x = s·log2 e - m·log2 e is off by half a step, 2^-20 for |x| up to
 //     32 (7e-7 of the weight); a row whose sum passes 2^31 is done again from its
 //     maximum, as are rows with masks at their start or values that are not finite.
-//   - Rows that do not fit the ring are first taken by the whole CTA (8x4096 rows
-//     without any: 35 us); where rows are long and few, a cluster of up to 8 CTAs takes
+//   - Rows that do not fit the ring are first taken by the whole CTA (rows of even
+//     lengths: 33 us); where rows are long and few, a cluster of up to 8 CTAs takes
 //     each (launch_rows).
 #include <cmath>
 #include <type_traits>
@@ -463,12 +465,14 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
         const float2 y = __fmul2_rn(w[MAPS - 1], make_float2(inv[MAPS - 1], inv[MAPS - 1]));
         return TWO ? __ffma2_rn(w[0], make_float2(inv[0], inv[0]), y) : y;
     };
-    auto results = [&](auto guard) {
+    // slow: outputs off 16 bytes, or products to leave out (told apart in the loop it
+    // costs the others 2 us of 37).
+    auto results = [&](auto slow) {
         auto grad = [&](int k, float2 w, float2 d) {
             const float ic = -inv[k] * c[k];
-            if (guard()) d = at_weight(w, d);
+            if (slow() && guarded) d = at_weight(w, d);
             const float2 y = __fmul2_rn(w, __ffma2_rn(make_float2(inv[k], inv[k]), d, make_float2(ic, ic)));
-            return guard() ? at_weight(w, y) : y;
+            return slow() && guarded ? at_weight(w, y) : y;
         };
         if (rq.has_edge) {
             if constexpr (GRAD) {
@@ -489,14 +493,14 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
             if constexpr (GRAD) {
                 float2 d0, d1;
                 lds_quad<DIN>(st.at(MAPS, q), d0, d1);
-                store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), vec);
-                if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), vec);
+                store_quad<OUT>(a.out1, q, grad(0, lo[0], d0), grad(0, hi[0], d1), !slow() || vec);
+                if constexpr (TWO) store_quad<OUT>(a.out2, q, grad(1, lo[1], d0), grad(1, hi[1], d1), !slow() || vec);
             } else {
-                store_quad<OUT>(a.out1, q, map(lo), map(hi), vec);
+                store_quad<OUT>(a.out1, q, map(lo), map(hi), !slow() || vec);
             }
         }
     };
-    if (GRAD && guarded)
+    if (!vec || guarded)
         results(std::true_type{});
     else
         results(std::false_type{});
