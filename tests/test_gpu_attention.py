@@ -732,3 +732,81 @@ def test_runs_of_empty_rows(usm, kind):
     assert_near(got(usm.row_softmax_grad(ro, put(s1), put(dout))), R.softmax_grad(p["ro"], s1, dout)[0], t1, "softmax gradient")
     for dtype in ("bf16", "f32"):
         run_attention(usm, p, 64, 64, 2, dtype, False)
+
+
+@pytest.mark.parametrize("low", [-60.0, -1e9, float(np.finfo(np.float32).min), -np.inf])
+def test_rows_that_begin_low(usm, low):
+    """Padding at the left, by a finite value or -inf: the rows' first scores say
+    nothing about their maxima.  Rows without padding lie between, and a row of
+    nothing else."""
+    rng = np.random.default_rng(29)
+    lengths = rng.integers(1, 900, 400)
+    lengths[::9] = 0
+    lengths[17] = 1900
+    ro, ci = W.csr_from_lengths(rng, lengths.astype(np.int64), 4000, None)
+    heads = np.zeros(400, dtype=np.int64)
+    nnz = ci.size
+    s1, s2 = (np.clip(2.5 * rng.standard_normal(nnz), -8, 8).astype(np.float32) for _ in range(2))
+    for r in range(400):
+        if r % 3 == 0:
+            s1[ro[r]:ro[r] + rng.integers(1, 200)] = low  # may run into the next rows
+    s2[ro[30]:ro[31]] = low
+    E = R.softmax_error(1900, SPREAD if low != -60.0 else 68.0)  # lower weights than e^-100 are 0 in both
+    lam = np.array([0.7], dtype=np.float32)
+    lr = np.full(400, np.float64(lam[0]))
+    r = R.rows_of(ro)
+    p1, p2 = R.row_softmax(ro, s1), R.row_softmax(ro, s2)
+    rod, a1, a2, ld = dev(ro), put(s1), put(s2), put(lam)
+    assert_near(got(usm.diff_softmax(rod, a1, a2, ld)), R.diff_map(ro, s1, s2, lr), (E + 2 * U) * (p1 + lr[r] * p2), "map")
+    dout = rng.standard_normal(nnz).astype(np.float32)
+    g1, g2, _ = R.diff_grad(ro, s1, s2, lr, dout, 1, heads)
+    o1, o2, _ = usm.diff_softmax_grad(rod, a1, a2, ld, put(dout))
+    for o, g, p, w, s in ((o1, g1, p1, 1.0, s1), (o2, g2, p2, lr[r], s2),
+                          (usm.row_softmax_grad(rod, a1, put(dout)), g1, p1, 1.0, s1)):
+        masked = s == -np.inf
+        c = R.row_dot(ro, p, np.abs(np.where(masked, 0, dout)), masked)
+        assert_near(got(o), g, w * p * (np.abs(np.where(masked, 0, dout)) + c[r]) * (3 * E + 8 * U), "gradient")
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_results_are_there_for_the_next_kernel(usm, captured):
+    """What follows a call of two kernels on its stream sees both done: a copy of
+    the results, and a call that overwrites the inputs' memory."""
+    import torch
+    rng = np.random.default_rng(31)
+    ro, ci = W.csr_from_lengths(rng, rng.integers(300, 500, 260), 4000, np.arange(260) % 3 * 4000)
+    M, K, nnz = 260, 12000, ci.size
+    rod, cid, lam = dev(ro), dev(ci), put(np.full(HEADS, 0.5))
+    xs = [[torch.randn(n, 64, device="cuda").bfloat16() for n in (M, K, M, K)] + [torch.randn(K, 128, device="cuda").bfloat16()]
+          for _ in range(2)]
+    ss = [[torch.randn(nnz, device="cuda") for _ in range(3)] for _ in range(2)]
+    x, s = [t.clone() for t in xs[0]], [t.clone() for t in ss[0]]
+
+    def step():
+        o = usm.attention(rod, cid, x[0], x[1], x[4], scale=0.125, Q2=x[2], K2=x[3], lam=lam, seg_rows=1)
+        o2 = o * 1
+        g = usm.diff_softmax_grad(rod, s[0], s[1], lam, s[2], seg_rows=1)
+        g2 = [t * 1 for t in g]
+        for a, b in zip(x + s, xs[1] + ss[1]):
+            a.copy_(b)
+        return [o2, *g2]
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out = step()
+        for _ in range(10):
+            for a, b in zip(x + s, xs[0] + ss[0]):
+                a.copy_(b)
+            if captured:
+                graph.replay()
+                have = [t.clone() for t in out]
+            else:
+                have = step()
+            side.synchronize()
+            for a, b in zip(want, have):
+                assert torch.equal(a, b)
