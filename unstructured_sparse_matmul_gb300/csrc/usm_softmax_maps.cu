@@ -20,10 +20,12 @@
 //   - Two rows of about a length are taken at once, by half a warp each (42.7 to
 //     39.7 us).
 //   - The maximum is not looked for (45 to 42 us): exponents are measured from
-//     the largest of a row's first entries, which gives the same quotients.  An
+//     the largest of a few entries (at the row's ends and in its middle), which
+//     gives the same quotients.  An
 //     exponent x = s·log2 e - m·log2 e is off by half a step, 2^-20 for |x| up to
 //     32 (7e-7 of the weight); a row whose sum passes 2^31 is done again from its
-//     maximum, as are rows with masks at their start or values that are not finite.
+//     maximum, as are rows with masks at all those places or values that are not
+//     finite (all rows again: 51 us).
 //   - Rows that do not fit the ring are first taken by the whole CTA (rows of even
 //     lengths: 33 us); where rows are long and few, a cluster of up to 8 CTAs takes
 //     each (launch_rows).
@@ -328,7 +330,7 @@ __device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0
 // warp or by half of it (width 32 or 16, the same for all lanes; each half has its
 // own row then, which may be empty: false), walked twice: for weights and their
 // sums, and for results.  MAX: exponents are measured from the row's maximum; else
-// from the largest of its first entries, and false if that does not do (nothing is
+// from the largest of a few entries, and false if that does not do (nothing is
 // changed then).
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool MAX, class S>
 __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int width, int r, float lam, int p0, int p1, bool vec) {
@@ -337,6 +339,8 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
     const unsigned step = 4 * width;
     const RowQuads rq(p0, p1, lane);
     const unsigned first = rq.qs + 4 * lane;
+    // Lane 4 looks at the row's middle (padding may be on the left).
+    const unsigned probe = lane == 4 && rq.qs < rq.qe ? rq.qs + (((rq.qe - rq.qs) >> 1) & ~3u) : first;
 
     float m[MAPS], xe[MAPS];
     const float de = GRAD && rq.has_edge ? lds_entry<DIN>(st.at(MAPS, rq.edge)) : 0.f;
@@ -345,7 +349,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
         xe[k] = rq.has_edge ? lds_f32(st.at(k, rq.edge)) : -INFINITY;
         m[k] = xe[k];
 #pragma unroll 1
-        for (unsigned q = first; q < rq.qe; q += step) {
+        for (unsigned q = MAX ? first : probe; q < rq.qe; q += step) {
             float2 lo, hi;
             lds_quad<false>(st.at(k, q), lo, hi);
             m[k] = fmaxf(m[k], fmaxf(fmaxf(lo.x, lo.y), fmaxf(hi.x, hi.y)));
