@@ -406,7 +406,9 @@ int csr_row_softmax_grad(int M, int nnz, const int *row_offsets, const float *sc
  *   bias  : usm_rel_bias, or NULL for none; added to both maps' scores.
  *   C     : M×N fp32, ldc ≥ N, overwritten; a row with no entry, or whose
  *           scores are all -inf in both maps, is zero.  Rows of V under an
- *           entry that is -inf in every map are not used, whatever they hold.
+ *           entry that is -inf in every map are not used, whatever they hold;
+ *           an infinity in a row of V that is used makes its column of C
+ *           infinite or NaN (bf16: NaN).
  *   workspace : csr_attention_workspace_bytes(M, K, D, N, nnz, two_maps, dtype)
  *           bytes of device scratch (two_maps: lambda is given), 16-byte
  *           aligned, contents ignored; 0 bytes for small problems.
