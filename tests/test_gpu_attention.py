@@ -810,3 +810,41 @@ def test_results_are_there_for_the_next_kernel(usm, captured):
             side.synchronize()
             for a, b in zip(want, have):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("mean", [1250, 1400, 2000, 4500])
+def test_many_long_rows(usm, mean):
+    """More long rows than the GPU has room for at once: a CTA to a row, which
+    holds it in registers or reads it twice, next to short and empty rows."""
+    rng = np.random.default_rng([37, mean])
+    M = 640
+    lengths = rng.integers(mean // 2, mean * 3 // 2, M)
+    lengths[::50] = 0
+    lengths[1::50] = 3
+    lengths[2::50] = 3 * mean
+    cols = 3 * mean
+    ro, ci = W.csr_from_lengths(rng, lengths.astype(np.int64), cols, None)
+    heads = np.arange(M) % HEADS
+    s1, s2 = (np.clip(2.5 * rng.standard_normal(ci.size), -8, 8).astype(np.float32) for _ in range(2))
+    s1[rng.random(ci.size) < 0.05] = -np.inf
+    s1[ro[7]:ro[8]] = -np.inf
+    lam = rng.uniform(0.1, 0.9, HEADS).astype(np.float32)
+    lr = lam.astype(np.float64)[heads]
+    r = R.rows_of(ro)
+    p = dict(ro=ro, longest=3 * mean)
+    rod, a1, a2, ld = dev(ro), put(s1), put(s2), put(lam)
+    tol = (R.softmax_error(3 * mean, SPREAD) + 2 * U) * (R.row_softmax(ro, s1) + lr[r] * R.row_softmax(ro, s2))
+    assert_near(got(usm.diff_softmax(rod, a1, a2, ld, seg_rows=1)), R.diff_map(ro, s1, s2, lr), tol, "map")
+    dout = rng.standard_normal(ci.size).astype(np.float32)
+    g1, g2, dlam = R.diff_grad(ro, s1, s2, lr, dout, HEADS, heads)
+    o1, o2, ol = usm.diff_softmax_grad(rod, a1, a2, ld, put(dout), seg_rows=1)
+    t1, _ = grad_bound(p, s1, dout, 1.0)
+    t2, c2 = grad_bound(p, s2, dout, lr[r])
+    assert_near(got(o1), g1, t1, "dscores1")
+    assert_near(got(o2), g2, t2, "dscores2")
+    size = np.bincount(heads, np.abs(R.softmax_grad(ro, s2, dout)[2]), HEADS)
+    assert_near(got(ol), dlam, np.bincount(heads, c2, HEADS) + np.bincount(heads, minlength=HEADS) * U * size, "dlambda")
+    assert_near(got(usm.row_softmax_grad(rod, a1, put(dout))), g1, t1, "softmax gradient")
+    x = a1.clone()  # in place
+    usm.row_softmax_grad(rod, x, put(dout), out=x)
+    assert np.array_equal(host(x), host(usm.row_softmax_grad(rod, a1, put(dout))))

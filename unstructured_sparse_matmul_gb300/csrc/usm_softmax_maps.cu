@@ -27,8 +27,8 @@
 //     maximum, as are rows with masks at all those places or values that are not
 //     finite (all rows again: 51 us).
 //   - Rows that do not fit the ring are first taken by the whole CTA (rows of even
-//     lengths: 33 us); where rows are long and few, a cluster of up to 8 CTAs takes
-//     each (launch_rows).
+//     lengths: 33 us); where most rows are long, a CTA takes each, or a cluster of
+//     up to 8 (launch_rows).
 #include <cmath>
 #include <type_traits>
 
@@ -630,19 +630,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // copies of rows left to the CTA
 }
 
-// A cluster per row.
-constexpr int kClusterWarps = 8;
-template <bool TWO, bool GRAD, bool DIN, bool OUT>
-__global__ void __launch_bounds__(kClusterWarps * 32) cluster_rows_kernel(const MapArgs a) {
+// A CTA or a cluster to a row.
+template <bool TWO, bool GRAD, bool DIN, bool OUT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) cluster_rows_kernel(const MapArgs a) {
     if (TWO && GRAD && a.row_c2) let_next_start();
-    __shared__ BlockStats<kClusterWarps> sh;
+    __shared__ BlockStats<WARPS> sh;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int r = blockIdx.x / ctas;
     int p0, p1;
     row_range(a.row_offsets, r, a.nnz, p0, p1);
     if (p0 == p1) return;
     const float lam = TWO ? __ldg(a.lambda + r / a.seg_rows % a.heads) : 0.f;
-    block_row<TWO, GRAD, DIN, OUT, kClusterWarps>(a, r, lam, p0, p1, sh, ctas, rank);
+    block_row<TWO, GRAD, DIN, OUT, WARPS>(a, r, lam, p0, p1, sh, ctas, rank);
 }
 
 // dλ[h] = -Σ c2 over head h's rows (those with entries: the others have no c2): a
@@ -691,24 +690,27 @@ template <bool TWO, bool GRAD, bool DIN, bool OUT>
 int launch_rows(const MapArgs& a, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     const int mean = a.nnz / a.M;
-    // A CTA of 8 warps a row where rows are long and too few to fill the GPU with
-    // a warp each; a cluster while its CTAs are too few too and keep at least
-    // half their registers' worth each.
-    if (mean > kRing - kChunk && a.M <= 4 * sms) {
+    // Rows that rings mostly do not hold: a CTA of 4 warps a row (8192 rows of 2048:
+    // map 53 us, gradient 74, softmax gradient 44; by 8 warps 80, 105 and 72, through
+    // the rings 75, 134 and 69; even at means of about 1500 for the map and 1200 for
+    // gradients).  Of 8 warps where rows are few, and a cluster of CTAs while those
+    // are too few too and keep at least half their registers' worth each.
+    if (mean > (GRAD ? 1280 : 1536)) {
+        const int warps = a.M >= 4 * sms ? 4 : 8;
         int ctas = 1;
-        while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > kClusterWarps * 32 * kSteps / 2) ctas *= 2;
+        while (ctas < 8 && (long long)a.M * ctas < 2LL * sms && mean / ctas > warps * 32 * kSteps / 2) ctas *= 2;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = ctas;
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(a.M * ctas));
-        cfg.blockDim = dim3(kClusterWarps * 32);
+        cfg.gridDim = dim3((unsigned)((long long)a.M * ctas));
+        cfg.blockDim = dim3(warps * 32);
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, cluster_rows_kernel<TWO, GRAD, DIN, OUT>, a) == cudaSuccess ? USM_OK
-                                                                                                   : USM_ERR_CUDA;
+        const auto kernel = warps == 4 ? cluster_rows_kernel<TWO, GRAD, DIN, OUT, 4> : cluster_rows_kernel<TWO, GRAD, DIN, OUT, 8>;
+        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
     }
     // As many warps as there is room for their rings, of at least 256 entries each.
     using S = MapStream<TWO, GRAD, DIN>;
