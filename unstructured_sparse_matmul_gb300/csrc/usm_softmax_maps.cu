@@ -18,7 +18,7 @@
 //     follows, 37.  (Weights written back to the ring instead of formed twice save
 //     0.6 us, but the scores with them, which a second try needs.)
 //   - Two rows of about a length are taken at once, by half a warp each (42.7 to
-//     39.7 us).
+//     39.7 us), or four short ones.
 //   - The maximum is not looked for (45 to 42 us): exponents are measured from
 //     the largest of a few entries (at the row's ends and in its middle), which
 //     gives the same quotients.  An
@@ -327,9 +327,9 @@ __device__ __noinline__ void long_row(const MapArgs& a, int r, float lam, int p0
 }
 
 // A row [p0, p1), which lies in the warp's ring, by the
-// warp or by half of it (width 32 or 16, the same for all lanes; each half has its
-// own row then, which may be empty: false), walked twice: for weights and their
-// sums, and for results.  MAX: exponents are measured from the row's maximum; else
+// warp, half or a quarter of it (width 32, 16 or 8, the same for all lanes; each
+// part has its own row, which may be empty: false), walked twice: for weights and
+// their sums, and for results.  MAX: exponents are measured from the row's maximum; else
 // from the largest of a few entries, and false if that does not do (nothing is
 // changed then).
 template <bool TWO, bool GRAD, bool DIN, bool OUT, bool MAX, class S>
@@ -414,19 +414,13 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
         c[k] = cs[k].x + cs[k].y;
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
+    for (int o = 1; o < 32; o <<= 1)
+        if (o < 8 || o < width)
 #pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            z[k] += __shfl_xor_sync(kFullMask, z[k], o);
-            if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], o);
-        }
-    if (width == 32) {
-#pragma unroll
-        for (int k = 0; k < MAPS; ++k) {
-            z[k] += __shfl_xor_sync(kFullMask, z[k], 16);
-            if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], 16);
-        }
-    }
+            for (int k = 0; k < MAPS; ++k) {
+                z[k] += __shfl_xor_sync(kFullMask, z[k], o);
+                if constexpr (GRAD) c[k] += __shfl_xor_sync(kFullMask, c[k], o);
+            }
     // A dout that is not finite makes c so too, even under weights of 0: such a
     // row leaves those products out.
     bool fine = true, guarded = false;
@@ -449,8 +443,8 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
             }
             float x = sum.x + sum.y;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
-            if (width == 32) x += __shfl_xor_sync(kFullMask, x, 16);
+            for (int o = 1; o < 32; o <<= 1)
+                if (o < 8 || o < width) x += __shfl_xor_sync(kFullMask, x, o);
             if (guarded) c[k] = x;
             fine = fine && fabsf(c[k]) < 0x1p100f;
         }
@@ -601,27 +595,48 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
         // over lanes, first entries, edges) is half its instructions otherwise, as
         // much as another 450 entries (differences of up to 128, 256 and 512 entries
         // measured 41.0, 39.7 and 41.1 us).
-        walk.hold(r, 2);
+        // Four short rows by a quarter each (32768 rows of 64: gradient 29 us, 32 by
+        // halves; 1M rows of 8: map 150 us, 236 by halves).
+        walk.hold(r, 4);
         const int begin = walk.offset(r), mid = max(walk.offset(r + 1), begin), far = max(walk.offset(r + 2), mid);
         const bool pair = r + 1 < r1 && ring_holds(begin, far) && abs((mid - begin) - (far - mid)) < 256;
-        const int end = pair ? far : mid, half = pair ? lane >> 4 : 0, row = r + half;
+        p0 = begin;
+        p1 = mid;
+        int end = mid, width = 32, part = 0;
+        if (pair) {
+            width = 16;
+            part = lane >> 4;
+            end = far;
+            p0 = part ? mid : begin;
+            p1 = part ? far : mid;
+            if (far - begin <= 128 && r + 3 < r1) {
+                const int third = max(walk.offset(r + 3), far), fourth = max(walk.offset(r + 4), third);
+                if (fourth - begin <= 256) {
+                    width = 8;
+                    part = lane >> 3;
+                    end = fourth;
+                    p0 = part == 0 ? begin : part == 1 ? mid : part == 2 ? far : third;
+                    p1 = part == 0 ? mid : part == 1 ? far : part == 2 ? third : fourth;
+                }
+            }
+        }
         if (begin == end) {
             r = walk.with_entries(r, r1);
             continue;
         }
-        r += pair ? 2 : 1;
+        const int row = r + part;
+        r += 32 / width;
         if (!ring_holds(begin, end)) continue;  // a long row
         st.need(begin, end);
-        p0 = half ? mid : begin;
-        p1 = half ? far : mid;
         if (TWO && row >= block_end) {
             const int block = row / a.seg_rows;
             block_end = (block + 1LL) * a.seg_rows;
             lam = __ldg(a.lambda + block % a.heads);
         }
-        bool done = ring_row<TWO, GRAD, DIN, OUT, false>(a, st, pair ? 16 : 32, row, lam, p0, p1, vec);
+        bool done = ring_row<TWO, GRAD, DIN, OUT, false>(a, st, width, row, lam, p0, p1, vec);
         done = done || p0 == p1;
-        for (unsigned again = __ballot_sync(kFullMask, !done) & (pair ? 0x10001u : 1u); again; again &= again - 1) {
+        const unsigned leaders = width == 8 ? 0x01010101u : width == 16 ? 0x10001u : 1u;
+        for (unsigned again = __ballot_sync(kFullMask, !done) & leaders; again; again &= again - 1) {
             const int from = __ffs(again) - 1;
             max_row<TWO, GRAD, DIN, OUT>(a, st, __shfl_sync(kFullMask, row, from), __shfl_sync(kFullMask, lam, from),
                                          __shfl_sync(kFullMask, p0, from), __shfl_sync(kFullMask, p1, from), vec);
