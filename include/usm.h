@@ -349,9 +349,12 @@ int csr_rel_bias_grad(int M, int K, int nnz, const int *row_offsets, const int *
  * Masked entries: a score of -inf has probability 0 in its map; a row whose
  * scores are all -inf has a zero map, and an empty row writes nothing.  NaN or
  * +inf scores make their row's outputs NaN.
+ * Every finite score counts, however far from zero: a row of one value, -1e30
+ * say, has equal probabilities.
  * Sums and the difference are fp32.  Exponentials are the GPU's 2^x with x =
- * (s - m)·log2 e, relative error at most |x|·2^-24 + 2^-22; m may be another of
- * the row's scores than the largest (x < 31 then; the quotients are the same).
+ * (s - m)·log2 e, relative error at most |x|·2^-23 + 2^-22; probabilities below
+ * 2^-124 may be 0.  m need not be one of the row's scores: the largest x is
+ * between -31 and 31, and the quotients are the same.
  */
 int csr_diff_softmax(int M, int nnz, const int *row_offsets, const float *scores1, const float *scores2,
                      const float *lambda, int num_heads, int seg_rows, void *out, usm_dtype out_dtype,

@@ -1,0 +1,96 @@
+"""Sparse-attention operators at the ends of their ranges: values, sums, sizes
+and calls."""
+import numpy as np
+import pytest
+
+import attention_ref as R
+from parity_util import dev
+from test_gpu_attention import HEADS, assert_near, got, put
+
+pytestmark = pytest.mark.gpu
+
+U = R.U
+
+# ---------------------------------------------------------------------------
+# Scores far from zero
+# ---------------------------------------------------------------------------
+# Row lengths for each form of the maps' kernels: rings (four and two rows at
+# once, and one), rows over the ring among short ones (a CTA), mostly long rows
+# (CTAs of four and of eight warps, one row past their registers), and clusters.
+FORMS = {
+    "ring": np.concatenate([np.arange(1, 200), [8] * 64, np.arange(200, 1500, 37), [1536, 0, 7]]),
+    "over": np.concatenate([np.arange(1, 300), [2100, 9000, 3, 17000], np.arange(300)]),
+    "cta4": np.concatenate([np.resize(np.arange(1250, 2200), 640 * 7)[::7], [9000]]),
+    "cta8": np.concatenate([np.arange(1400, 2200, 4), [17000]]),
+    "cluster": np.array([40000, 60001, 50000]),
+}
+FAR = [2e7, -2e7, 3e9, -3e9, 1e10, -1e10, 3e10, -3e10, 1e12, -1e20, 1e20, -1e30, 9e36, -9e36, 1e38, 3e38, -3e38]
+
+
+def far_scores(rng, ro, value):
+    """Rows of the value alone, of values next to it, and of ordinary scores
+    with the value at the left, at the right, at one place or everywhere but at
+    one; every other row also has entries of -inf."""
+    nnz = int(ro[-1])
+    s = np.clip(2.5 * rng.standard_normal(nnz), -8, 8).astype(np.float32)
+    v = np.float32(value)
+    for r in range(ro.size - 1):
+        b, e = int(ro[r]), int(ro[r + 1])
+        n = e - b
+        if n == 0:
+            continue
+        kind = r % 6
+        if kind == 0:
+            s[b:e] = v
+        elif kind == 1:
+            s[b:e] = v * (1 + rng.integers(0, 8, n).astype(np.float32) * np.float32(2.0 ** -23))
+        elif kind == 2:
+            s[b:b + n // 2] = v
+        elif kind == 3:
+            s[b + n // 2:e] = v
+        elif kind == 4:
+            s[b + rng.integers(n)] = v
+        else:
+            keep = b + rng.integers(n)
+            x = s[keep]
+            s[b:e] = v
+            s[keep] = x
+        if r // 6 % 2:
+            s[b:e][rng.random(n) < 0.1] = -np.inf
+    return s
+
+
+@pytest.mark.parametrize("value", FAR)
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_scores_far_from_zero(usm, form, value):
+    """Every finite score counts: maps, gradients and dlambda of rows whose
+    scores lie anywhere in fp32's range."""
+    rng = np.random.default_rng([41, sorted(FORMS).index(form), FAR.index(value)])
+    lengths = FORMS[form].astype(np.int64)
+    ro = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    M, nnz, r = lengths.size, int(ro[-1]), R.rows_of(ro)
+    heads = np.arange(M) % HEADS
+    s1, s2 = far_scores(rng, ro, value), far_scores(rng, ro, -value if form == "ring" else value)
+    dout = rng.standard_normal(nnz).astype(np.float32)
+    lam = rng.uniform(0.1, 0.9, HEADS).astype(np.float32)
+    lr = lam.astype(np.float64)[heads]
+    # Weights count down to e^-90: lower ones may be flushed to zero, and are
+    # below 2^-126 of the sum times at most 4.
+    E, tiny = R.softmax_error(int(lengths.max()), 90.0), 2.0 ** -124
+    p1, p2 = R.row_softmax(ro, s1), R.row_softmax(ro, s2)
+    rod, a1, a2, ld, dd = dev(ro), put(s1), put(s2), put(lam), put(dout)
+    assert_near(got(usm.diff_softmax(rod, a1, a2, ld, seg_rows=1)), p1 - lr[r] * p2,
+                (E + 2 * U) * (p1 + lr[r] * p2) + 2 * tiny, "map")
+    g1, g2, dlam = R.diff_grad(ro, s1, s2, lr, dout, HEADS, heads)
+    o1, o2, ol = usm.diff_softmax_grad(rod, a1, a2, ld, dd, seg_rows=1)
+    o = usm.row_softmax_grad(rod, a1, dd)
+    for x, g, p, w, s, what in ((o1, g1, p1, 1.0, s1, "dscores1"), (o2, g2, p2, lr[r], s2, "dscores2"),
+                                (o, g1, p1, 1.0, s1, "softmax gradient")):
+        masked = s == -np.inf
+        size = np.abs(np.where(masked, 0, dout))
+        c = R.row_dot(ro, p, size, masked)
+        assert_near(got(x), g, w * p * (size + c[r]) * (3 * E + 8 * U) + 20 * tiny, what)
+    c = R.row_dot(ro, p2, np.abs(np.where(s2 == -np.inf, 0, dout)), s2 == -np.inf) * (3 * E + 8 * U)
+    rows = np.bincount(heads, minlength=HEADS)
+    csize = np.bincount(heads, np.abs(R.softmax_grad(ro, s2, dout)[2]), HEADS)
+    assert_near(got(ol), dlam, np.bincount(heads, c, HEADS) + rows * U * csize + 1e-30, "dlambda")

@@ -23,9 +23,10 @@
 //     the largest of a few entries (at the row's ends and in its middle), which
 //     gives the same quotients.  An
 //     exponent x = s·log2 e - m·log2 e is off by half a step, 2^-20 for |x| up to
-//     32 (7e-7 of the weight); a row whose sum passes 2^31 is done again from its
-//     maximum, as are rows with masks at all those places or values that are not
-//     finite (all rows again: 51 us).
+//     32 (7e-7 of the weight); a row whose sum is not in [1/4, 2^31) is done again
+//     from its maximum: rows with masks at all those places, with values that are
+//     not finite, or with scores so far from zero that the rounding of m·log2 e
+//     leaves the exponents' range (all rows again: 51 us).
 //   - Rows that do not fit the ring are first taken by the whole CTA (rows of even
 //     lengths: 33 us); where most rows are long, a CTA takes each, or a cluster of
 //     up to 8 (launch_rows).
@@ -66,17 +67,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // exp(s - m) as 2^(s·log2 e - shift), shift = m·log2 e: one fused product and the
 // hardware's exponential.  The rounding of the shift is the same factor in every
-// weight of the row and in their sum.  Scores so large that s·log2 e overflows
-// are first brought near zero (off = m, shift = 0); a maximum of -inf (every
-// entry masked) has shift 0, so that all weights are 0.
+// weight of the row and in their sum: up to |m| = kNear it is half a step of 2 at
+// most, a factor between 1/2 and 2; from about 1e9 on the factor would be infinite
+// or 0.  Scores with a maximum beyond kNear are therefore first brought near zero
+// (off = m, shift = 0: one more rounding, relative to s - m).  A maximum of -inf
+// (every entry masked) has shift 0, so that all weights are 0.
+constexpr float kNear = 0x1p24f;
 struct Base {
     float off, shift;
     __device__ __forceinline__ explicit Base(float m) {
-        const bool huge = fabsf(m) > 1e37f && m != -INFINITY;
-        off = huge ? m : 0.f;
-        shift = huge || m == -INFINITY ? 0.f : m * kLog2e;
+        const bool far = fabsf(m) > kNear && m != -INFINITY;
+        off = far ? m : 0.f;
+        shift = far || m == -INFINITY ? 0.f : m * kLog2e;
     }
-    __device__ __forceinline__ bool huge() const { return off != 0.f; }
+    __device__ __forceinline__ bool far() const { return off != 0.f; }
 };
 __device__ __forceinline__ float exp2_flush(float x) {
     float y;
@@ -211,7 +215,7 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
         const Base base(m[k]);
-        if (base.huge()) {
+        if (base.far()) {
 #pragma unroll
             for (int i = 0; i < kSteps / 2; ++i)
                 if (2 * i * T < nw) x[k][i] = make_float2(x[k][i].x - base.off, x[k][i].y - base.off);
@@ -358,8 +362,8 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
         if (MAX) {
             m[k] = warp_max(m[k]);
             // A maximum of -inf (every entry masked) leaves the scores as they are, and
-            // scores so large that s·log2 e overflows are brought near zero first.
-            if (!(fabsf(m[k]) <= 1e37f)) {
+            // scores with one beyond kNear are brought near zero first.
+            if (!(fabsf(m[k]) <= kNear)) {
                 if (m[k] != -INFINITY) {
                     xe[k] -= m[k];
 #pragma unroll 1
@@ -427,7 +431,7 @@ __device__ __forceinline__ bool ring_row(const MapArgs& a, const S& st, int widt
     auto at_weight = [&](float2 w, float2 v) { return make_float2(w.x == 0.f ? 0.f : v.x, w.y == 0.f ? 0.f : v.y); };
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
-        fine = fine && z[k] < 0x1p31f;
+        fine = fine && z[k] >= 0.25f && z[k] < 0x1p31f;
         if constexpr (GRAD) guarded = guarded || !(fabsf(c[k]) < 0x1p100f);
     }
     if (GRAD && __any_sync(kFullMask, guarded)) {
