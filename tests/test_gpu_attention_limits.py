@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import attention_ref as R
-from parity_util import dev
+from parity_util import dev, host
 from test_gpu_attention import HEADS, assert_near, got, put
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,49 @@ def test_scores_far_from_zero(usm, form, value):
     rows = np.bincount(heads, minlength=HEADS)
     csize = np.bincount(heads, np.abs(R.softmax_grad(ro, s2, dout)[2]), HEADS)
     assert_near(got(ol), dlam, np.bincount(heads, c, HEADS) + rows * U * csize + 1e-30, "dlambda")
+
+
+# ---------------------------------------------------------------------------
+# Row counts next to 2^31
+# ---------------------------------------------------------------------------
+def test_most_rows(usm):
+    """2^31 - 2 rows (offsets of 8.6 GB), nearly all without entries: a few at
+    the beginning, in the middle and at the very end, long ones among them."""
+    import torch
+    rng = np.random.default_rng(53)
+    M = 2**31 - 2
+    runs = {0: [3, 0, 700, 1, 8, 8, 8, 8], 2**30 - 2: [5, 5000, 0, 40], M - 200: [2100, 0, 9, 17], M - 6: [30, 1, 6000, 0, 2, 11]}
+    rows = np.concatenate([first + np.arange(len(x)) for first, x in runs.items()])
+    lengths = np.concatenate([np.array(x) for x in runs.values()])
+    small = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    nnz = int(small[-1])
+    ro = torch.full((M + 1,), nnz, dtype=torch.int32, device="cuda")
+    ro[0] = 0
+    done = 1
+    for i, row in enumerate(rows):  # offsets of the rows without entries between two of them
+        ro[done:int(row) + 1] = int(small[i])
+        ro[int(row) + 1] = int(small[i + 1])
+        done = int(row) + 2
+    s1, s2 = (np.clip(2.5 * rng.standard_normal(nnz), -8, 8).astype(np.float32) for _ in range(2))
+    dout, lam = rng.standard_normal(nnz).astype(np.float32), np.array([0.7], dtype=np.float32)
+    r, lr = R.rows_of(small), np.full(lengths.size, np.float64(lam[0]))
+    E = R.softmax_error(int(lengths.max()), 16.0)
+    p1, p2 = R.row_softmax(small, s1), R.row_softmax(small, s2)
+    a1, a2, dd, ld = put(s1), put(s2), put(dout), put(lam)
+    assert_near(got(usm.diff_softmax(ro, a1, a2, ld)), p1 - lr[r] * p2, (E + 2 * U) * (p1 + lr[r] * p2), "map")
+    g1, g2, dlam = R.diff_grad(small, s1, s2, lr, dout, 1, np.zeros(lengths.size, dtype=np.int64))
+    o1, o2, ol = usm.diff_softmax_grad(ro, a1, a2, ld, dd)
+    nomask = np.zeros(nnz, dtype=bool)
+    for x, g, p, w in ((o1, g1, p1, 1.0), (o2, g2, p2, lr[r]), (usm.row_softmax_grad(ro, a1, dd), g1, p1, 1.0)):
+        c = R.row_dot(small, p, np.abs(dout), nomask)
+        assert_near(got(x), g, w * p * (np.abs(dout) + c[r]) * (3 * E + 8 * U), "gradient")
+    c = R.row_dot(small, p2, np.abs(dout), nomask)
+    assert_near(got(ol), dlam, c.sum() * (3 * E + 8 * U) + lengths.size * U * c.sum(), "dlambda")
+    # Query positions are row numbers here: keys up to 4 ahead of the last row's.
+    bmap, table = dev(np.arange(9, dtype=np.int32)), rng.standard_normal((1, 9)).astype(np.float32)
+    ci = (np.minimum(rows[r] + rng.integers(-6, 7, nnz), 2**31 - 2).clip(0)).astype(np.int64)
+    k = np.clip(ci - rows[r], -4, 4) + 4
+    cid = dev(ci.astype(np.int32))
+    assert np.array_equal(host(usm.rel_bias(ro, cid, a1, put(table), bmap)), s1 + table[0, k])
+    ds = rng.integers(-8, 9, nnz).astype(np.float32)
+    assert np.array_equal(got(usm.rel_bias_grad(ro, cid, put(ds), 1, 9, bmap))[0], np.bincount(k, ds, 9))

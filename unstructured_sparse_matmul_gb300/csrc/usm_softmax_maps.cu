@@ -569,10 +569,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
     }
     // Long rows by the CTA, while the rings fill.
     if (__syncthreads_or(any_long)) {
+        const int past = bounds[kWarps];
 #pragma unroll 1
-        for (int r = bounds[0]; r < bounds[kWarps]; r += kThreads) {
+        for (int r = bounds[0]; r < past;) {
+            const int rows = min(past - r, kThreads);
             bool mine = false;
-            if (threadIdx.x < bounds[kWarps] - r) {
+            if (threadIdx.x < rows) {
                 row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
                 mine = p0 < p1 && !ring_holds(p0, p1);
             }
@@ -589,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
                                                           p0, p1, sh);
                 }
             __syncthreads();  // is_long is read
+            r += rows;
         }
     }
     float lam = 0.f;
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
         // Four short rows by a quarter each (32768 rows of 64: gradient 29 us, 32 by
         // halves; 1M rows of 8: map 150 us, 236 by halves).
         walk.hold(r, 4);
-        const int begin = walk.offset(r), mid = max(walk.offset(r + 1), begin), far = max(walk.offset(r + 2), mid);
+        const int begin = walk.offset(r), mid = max(walk.offset(r, 1), begin), far = max(walk.offset(r, 2), mid);
         const bool pair = r + 1 < r1 && ring_holds(begin, far) && abs((mid - begin) - (far - mid)) < 256;
         p0 = begin;
         p1 = mid;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
             p0 = part ? mid : begin;
             p1 = part ? far : mid;
             if (far - begin <= 128 && r + 3 < r1) {
-                const int third = max(walk.offset(r + 3), far), fourth = max(walk.offset(r + 4), third);
+                const int third = max(walk.offset(r, 3), far), fourth = max(walk.offset(r, 4), third);
                 if (fourth - begin <= 256) {
                     width = 8;
                     part = lane >> 3;

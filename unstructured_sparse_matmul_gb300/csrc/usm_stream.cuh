@@ -214,7 +214,7 @@ __device__ __forceinline__ void first_rows_from(const int* __restrict__ ro, int 
         int step[2], v[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            step[k] = (hi[k] - lo[k] + 31) / 32;
+            step[k] = (int)(((unsigned)(hi[k] - lo[k]) + 31u) / 32u);
             v[k] = __ldg(ro + min((long long)lo[k] + (long long)lane * step[k], (long long)M));
         }
 #pragma unroll
@@ -234,18 +234,20 @@ __device__ __forceinline__ void first_rows_from(const int* __restrict__ ro, int 
     r1 = lo[1];
 }
 
-// Lanes hold 32 consecutive row offsets, read off them one by one.
+// Lanes hold 32 consecutive row offsets, read off them one by one.  M may be as
+// large as 2^31 - 1: no row number past M is formed.
 struct RowWalk {
     const int* ro;
     int M, nnz, lane, at, held;  // held: offset of row at + lane
     // Offsets of rows r .. r + n (n < 32) can be read.
     __device__ __forceinline__ void hold(int r, int n) {
-        if (r < at || r - at > 31 - n) {
+        if ((unsigned)r - (unsigned)at > (unsigned)(31 - n)) {
             at = r;
             held = min(max(__ldg(ro + min((long long)r + lane, (long long)M)), 0), nnz);
         }
     }
-    __device__ __forceinline__ int offset(int r) const { return __shfl_sync(kFullMask, held, r - at); }
+    // Offset of row r + ahead (the last one's past M).
+    __device__ __forceinline__ int offset(int r, int ahead = 0) const { return __shfl_sync(kFullMask, held, r - at + ahead); }
     // The first row from r on (r < r1) that has entries, or r1.  Runs of rows
     // without any are passed by a search.
     __device__ __forceinline__ int with_entries(int r, int r1) {
@@ -254,11 +256,12 @@ struct RowWalk {
             const int next = __shfl_down_sync(kFullMask, held, 1);
             const unsigned some = __ballot_sync(kFullMask, lane < 31 && lane >= r - at && next > held);
             if (some) return min(at + __ffs(some) - 1, r1);
-            const int p = offset(at + 31);
+            const int p = offset(at, 31);
             if (r1 - at <= 31 || p >= nnz) return r1;
             r = at + 31;
             hold(r, 31);
-            if (offset(r + 31) > p) continue;
+            if (offset(r, 31) > p) continue;
+            if (r1 - r <= 31) return r1;
             int after, same;
             first_rows_from(ro, M, p + 1, p + 1, lane, after, same);
             r = max(after - 1, r + 31);
