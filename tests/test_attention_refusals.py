@@ -155,6 +155,15 @@ def test_attention_refuses(lib):
     assert attention(lib, N=0, C=None) == 0
 
 
+@pytest.mark.parametrize("heads,buckets", [(2**31 - 1, 1), (2**31 - 456, 2), (10**9, 512), (457, 32), (1, 1)])
+def test_workspace_of_many_heads(lib, heads, buckets):
+    """Each head has a part of the sum at least, whatever their number."""
+    parts = heads * buckets * 4
+    need = lib.csr_rel_bias_grad_workspace_bytes(1 << 20, 1 << 20, 1, heads, buckets)
+    assert need >= parts and need % parts == 0
+    assert need // parts <= -(-456 // heads)
+
+
 def test_binding_refuses_without_gpu():
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():

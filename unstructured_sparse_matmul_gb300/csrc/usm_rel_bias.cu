@@ -139,7 +139,7 @@ struct RowWalk {
     __device__ __forceinline__ void hold(unsigned p, Made made) {
         const unsigned next = __shfl_down_sync(kFullMask, offset, 1);
         const bool some = lane < min(31, r1 - first) && next > (unsigned)offset && next > p;
-        made(first + lane, some);
+        made((int)((unsigned)first + lane), some);
         left = __ballot_sync(kFullMask, some);
     }
     template <class Made>
@@ -403,18 +403,19 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     }
 }
 
-// dT[h][k] = Σ_j part[h][j][k]: a warp for each (h, k).
+// dT[h][k] = Σ_j part[h][j][k]: a warp for each (h, k), or for several in large tables.
 __global__ void rel_bias_grad_sum_kernel(int heads, int buckets, int J, const float* __restrict__ part,
                                          float* __restrict__ dtable) {
     const int lane = threadIdx.x & 31;
-    const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (i >= (long long)heads * buckets) return;
-    const long long h = i / buckets, k = i % buckets;
-    float x = 0.f;
-    for (int j = lane; j < J; j += 32) x += part[(h * J + j) * buckets + k];
+    const long long n = (long long)heads * buckets, step = (long long)gridDim.x * blockDim.x >> 5;
+    for (long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < n; i += step) {
+        const long long h = i / buckets, k = i % buckets;
+        float x = 0.f;
+        for (int j = lane; j < J; j += 32) x += part[(h * J + j) * buckets + k];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
-    if (lane == 0) dtable[i] = x;
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
+        if (lane == 0) dtable[i] = x;
+    }
 }
 
 // Threads of a gradient CTA (its histogram is threads × buckets floats, 64 KB
@@ -429,8 +430,9 @@ struct GradSplit {
 };
 GradSplit grad_split(int M, int nnz, int seg_rows, int heads, int buckets) {
     const int warps = grad_threads(buckets) / 32;
-    const long long blocks = M > 0 ? (query_blocks(M, seg_rows) + heads - 1) / heads : 1;  // of the first head, the most
-    const long long most = (456 + heads - 1) / heads * (long long)warps, some = nnz / (heads * (long long)kTile) + 1;
+    // Query blocks of the first head, which has the most.
+    const long long blocks = M > 0 ? ((long long)query_blocks(M, seg_rows) + heads - 1) / heads : 1;
+    const long long most = (455LL + heads) / heads * warps, some = nnz / (heads * (long long)kTile) + 1;
     const long long parts = most < some ? most : some;
     GradSplit split;
     split.Y = (int)((parts + blocks - 1) / blocks);
@@ -487,8 +489,9 @@ int launch_grad(int M, int nnz, const int* ro, const int* ci, const void* ds, co
     rel_bias_grad_kernel<BF><<<bias.heads * J, T, smem, stream>>>(
         M, nnz, ro, ci, ds, bias, query_blocks(M, bias.seg_rows), Y, J, part,
         quad_aligned(ci) && quad_aligned(ds, BF));
-    const long long warps = (long long)bias.heads * bias.buckets;
-    rel_bias_grad_sum_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(bias.heads, bias.buckets, J, part, dtable);
+    const long long ctas = ((long long)bias.heads * bias.buckets + 7) / 8;
+    rel_bias_grad_sum_kernel<<<(unsigned)(ctas < 1 << 20 ? ctas : 1 << 20), 256, 0, stream>>>(bias.heads, bias.buckets, J,
+                                                                                              part, dtable);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 }  // namespace
