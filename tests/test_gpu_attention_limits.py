@@ -140,3 +140,22 @@ def test_most_rows(usm):
     assert np.array_equal(host(usm.rel_bias(ro, cid, a1, put(table), bmap)), s1 + table[0, k])
     ds = rng.integers(-8, 9, nnz).astype(np.float32)
     assert np.array_equal(got(usm.rel_bias_grad(ro, cid, put(ds), 1, 9, bmap))[0], np.bincount(k, ds, 9))
+
+
+def test_runs_of_rows_without_entries_take_no_time(usm):
+    """10^9 rows without entries before a long one: passed by a search (0.1 ms),
+    not walked (seconds)."""
+    import torch
+    M = 10**9
+    ro = torch.full((M + 1,), 3, dtype=torch.int32, device="cuda")
+    ro[0], ro[M] = 0, 5003
+    s, lam = torch.randn(5003, device="cuda"), torch.ones(1, device="cuda")
+    calls = (lambda: usm.diff_softmax(ro, s, s, lam), lambda: usm.row_softmax_grad(ro, s, s))
+    for call in calls:
+        call()
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        call()
+        end.record()
+        end.synchronize()
+        assert begin.elapsed_time(end) < 250

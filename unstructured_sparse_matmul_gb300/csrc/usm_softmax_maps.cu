@@ -570,17 +570,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
     // Long rows by the CTA, while the rings fill.
     if (__syncthreads_or(any_long)) {
         const int past = bounds[kWarps];
+        RowWalk all{a.row_offsets, a.M, a.nnz, lane, -64, 0};
 #pragma unroll 1
         for (int r = bounds[0]; r < past;) {
             const int rows = min(past - r, kThreads);
-            bool mine = false;
+            bool some = false, mine = false;
             if (threadIdx.x < rows) {
                 row_range(a.row_offsets, r + threadIdx.x, a.nnz, p0, p1);
-                mine = p0 < p1 && !ring_holds(p0, p1);
+                some = p0 < p1;
+                mine = some && !ring_holds(p0, p1);
             }
             const unsigned mask = __ballot_sync(kFullMask, mine);
             if (lane == 0) is_long[warp] = mask;
-            __syncthreads();
+            some = __syncthreads_or(some);
 #pragma unroll 1
             for (int w = 0; w < kWarps; ++w)
 #pragma unroll 1
@@ -592,6 +594,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<MapStream<TWO, GRAD, DIN
                 }
             __syncthreads();  // is_long is read
             r += rows;
+            // Runs of rows without entries are passed by a search, the same in every
+            // warp: `all` is where the others' are.
+            if (!some && r < past) r = all.with_entries(r, past);
         }
     }
     float lam = 0.f;
