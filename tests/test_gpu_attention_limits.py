@@ -1,5 +1,7 @@
 """Sparse-attention operators at the ends of their ranges: values, sums, sizes
 and calls."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -94,6 +96,49 @@ def test_scores_far_from_zero(usm, form, value):
     rows = np.bincount(heads, minlength=HEADS)
     csize = np.bincount(heads, np.abs(R.softmax_grad(ro, s2, dout)[2]), HEADS)
     assert_near(got(ol), dlam, np.bincount(heads, c, HEADS) + rows * U * csize + 1e-30, "dlambda")
+
+
+# ---------------------------------------------------------------------------
+# Calls
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("which", ["attention", "attention_shares", "diff_softmax", "poll"])
+def test_a_failed_launch_is_reported_once(usm, which):
+    """What CUDA refuses (work on a stream whose capture was invalidated) fails
+    that call alone: the next call, with nothing wrong, succeeds."""
+    import torch
+    lib, cu = usm.load(), ctypes.CDLL("libcuda.so.1")
+    x = torch.zeros(1 << 16, device="cuda")
+    shares = which == "attention_shares"
+    nnz = 1 << 16 if shares else 4000
+    ro, ci = dev(np.array([0, nnz], dtype=np.int32)), torch.zeros(nnz, dtype=torch.int32, device="cuda")
+    out, ws = torch.zeros(1 << 16, device="cuda"), torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    bmap = torch.empty(257, dtype=torch.int32, device="cuda")
+    lam = torch.ones(1, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s = side.cuda_stream
+    at = lambda t: t.data_ptr()
+    D = 256 if shares else 8
+
+    def call():
+        if which == "poll":
+            return lib.usm_poll_status(s)
+        if which == "diff_softmax":
+            return lib.csr_diff_softmax(1, nnz, at(ro), at(x), at(x), at(lam), 1, 1, at(out), 0, s)
+        return lib.csr_attention(1, 4, D, D, nnz, at(ro), at(ci), at(x), D, at(x), D, None, 0, None, 0, at(x), D, 1.0, None, 1,
+                                 1, None, at(out), D, 0, at(ws), ws.numel(), s)
+
+    assert call() == 0  # nothing is wrong with the call itself
+    side.synchronize()
+    assert cu.cuStreamBeginCapture_v2(ctypes.c_void_p(s), 2) == 0  # relaxed
+    assert cu.cuStreamSynchronize(ctypes.c_void_p(s)) != 0  # not allowed in a capture: it ends as a failure
+    failed = call()
+    graph = ctypes.c_void_p()
+    assert cu.cuStreamEndCapture(ctypes.c_void_p(s), ctypes.byref(graph)) != 0
+    assert failed == -4  # USM_ERR_CUDA
+    assert lib.rel_bucket_build(32, 128, 0, at(bmap), s) == 0
+    assert call() == 0
+    side.synchronize()
 
 
 # ---------------------------------------------------------------------------

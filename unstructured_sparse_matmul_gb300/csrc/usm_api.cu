@@ -524,14 +524,14 @@ int csr_validate(int M, int K, int nnz, const int* row_offsets, const int* col_i
 
 int usm_poll_status(void* stream) {
     cudaStream_t st = as_stream(stream);
-    if (cudaStreamSynchronize(st) != cudaSuccess) return USM_ERR_CUDA;
+    if (cudaStreamSynchronize(st) != cudaSuccess) return cuda_failure();
     int* status = status_word_for_current_device();
     if (!status) return USM_ERR_CUDA;
     int v = 0;
     if (cudaMemcpyAsync(&v, status, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess)
-        return USM_ERR_CUDA;
-    if (cudaMemsetAsync(status, 0, sizeof(int), st) != cudaSuccess) return USM_ERR_CUDA;
-    if (cudaStreamSynchronize(st) != cudaSuccess) return USM_ERR_CUDA;
+        return cuda_failure();
+    if (cudaMemsetAsync(status, 0, sizeof(int), st) != cudaSuccess) return cuda_failure();
+    if (cudaStreamSynchronize(st) != cudaSuccess) return cuda_failure();
     return v;
 }
 

@@ -808,8 +808,9 @@ struct Launch {
             float* parts = static_cast<float*>(workspace);
             int* cut_rows = reinterpret_cast<int*>(parts + (size_t)G * 2 * Row::kMaps * (a.N + 2));
             const auto kernel = attention_shares_kernel<Row>;
-            if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
+            if (!allow_shared(kernel, R::kSmem)) return cuda_failure();
             kernel<<<(G + R::kWarps - 1) / R::kWarps, R::kWarps * 32, R::kSmem, stream>>>(a, parts, cut_rows, G);
+            if (cudaGetLastError() != cudaSuccess) return USM_ERR_CUDA;
             const unsigned strips = (a.N + 31) / 32;
             if (a.M <= G)
                 return launch_next(attention_join_kernel<Row::kMaps, true>, dim3(a.M, strips), 256, 1, stream, a,
@@ -824,7 +825,7 @@ struct Launch {
         int ctas = 1;
         while (ctas < 8 && (long long)a.M * ctas < 4LL * sms && (long long)ctas * R::kWarps < windows) ctas *= 2;
         const auto kernel = attention_cluster_kernel<Row>;
-        if (!allow_shared(kernel, R::kSmem)) return USM_ERR_CUDA;
+        if (!allow_shared(kernel, R::kSmem)) return cuda_failure();
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = ctas;
@@ -836,7 +837,7 @@ struct Launch {
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : cuda_failure();
     }
 };
 

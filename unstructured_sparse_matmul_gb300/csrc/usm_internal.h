@@ -118,6 +118,14 @@ inline int effective_seg(int M, int seg_rows) { return (seg_rows <= 0 || seg_row
 
 int launch_wait_timeout_selftest(long long limit_ns, int* status, cudaStream_t stream);
 
+// The status of a call that CUDA failed.  The runtime remembers the error until it
+// is asked for; it is asked here, so that the next entry point, which asks after
+// its own launches, does not find it.
+inline int cuda_failure() {
+    cudaGetLastError();
+    return USM_ERR_CUDA;
+}
+
 // Lets a kernel have `smem` bytes a CTA, and the SM all the shared memory there is
 // (the driver's own split may leave room for fewer CTAs than fit).
 template <class Kernel>
@@ -146,7 +154,7 @@ inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, int cluster,
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USM_OK : cuda_failure();
 }
 #ifdef __CUDACC__
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }

@@ -484,7 +484,7 @@ int launch_grad(int M, int nnz, const int* ro, const int* ci, const void* ds, co
     const auto [Y, J] = grad_split(M, nnz, bias.seg_rows, bias.heads, bias.buckets);
     const int T = grad_threads(bias.buckets);
     const int smem = bias.buckets * T * 4;
-    if (!allow_shared(rel_bias_grad_kernel<BF>, smem)) return USM_ERR_CUDA;
+    if (!allow_shared(rel_bias_grad_kernel<BF>, smem)) return cuda_failure();
     float* part = static_cast<float*>(workspace);
     rel_bias_grad_kernel<BF><<<bias.heads * J, T, smem, stream>>>(
         M, nnz, ro, ci, ds, bias, query_blocks(M, bias.seg_rows), Y, J, part,

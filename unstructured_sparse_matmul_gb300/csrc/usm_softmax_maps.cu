@@ -737,7 +737,7 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         const auto kernel = warps == 4 ? cluster_rows_kernel<TWO, GRAD, DIN, OUT, 4> : cluster_rows_kernel<TWO, GRAD, DIN, OUT, 8>;
-        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? USM_OK : cuda_failure();
     }
     // As many warps as there is room for their rings, of at least 256 entries each.
     using S = MapStream<TWO, GRAD, DIN>;
@@ -746,7 +746,7 @@ int launch_rows(const MapArgs& a, cudaStream_t stream) {
     const bool aligned = aligned_for_stream(a.s1) && aligned_for_stream(a.s2) && aligned_for_stream(a.dout);
     const bool vec = aligned_for_stream(a.out1) && aligned_for_stream(a.out2);
     const auto kernel = stream_rows_kernel<TWO, GRAD, DIN, OUT>;
-    if (!allow_shared(kernel, smem)) return USM_ERR_CUDA;
+    if (!allow_shared(kernel, smem)) return cuda_failure();
     kernel<<<(G + kWarps - 1) / kWarps, kThreads, smem, stream>>>(a, G, aligned, vec);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }

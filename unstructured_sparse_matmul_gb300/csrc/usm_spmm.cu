@@ -41,7 +41,7 @@ int launch_kernel(SpmmArgs a, int tiles_per_block, const void* B, int ldb, cudaS
     if (dev < 31 && !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
             cudaSuccess)
-            return USM_ERR_CUDA;
+            return cuda_failure();
         __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
     // Row tiles on x (dispatched first, longest rows first under a swizzle),
