@@ -141,6 +141,17 @@ def test_a_failed_launch_is_reported_once(usm, which):
     side.synchronize()
 
 
+def test_bucket_map_is_checked_before_memory_is_taken(usm):
+    import torch
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for reach in (8193, 10**9, 2**31 - 1):
+        with pytest.raises(usm.USMError, match="UNSUPPORTED"):
+            usm.rel_bucket_map(32, reach)
+    assert torch.cuda.max_memory_allocated() == before
+
+
 # ---------------------------------------------------------------------------
 # Row counts next to 2^31
 # ---------------------------------------------------------------------------

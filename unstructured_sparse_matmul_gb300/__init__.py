@@ -72,6 +72,8 @@ class RelBias(ctypes.Structure):
                 ("max_distance", _i), ("seg_cols", _i), ("q_offset", _vp)]
 
 
+REL_BIAS_MAX_DISTANCE = 8192  # USM_REL_BIAS_MAX_DISTANCE of include/usm.h
+
 _pack_bias = struct.Struct("@PiiiPiiP").pack  # the same as bytes, in a quarter of the time
 
 
@@ -489,6 +491,8 @@ def rel_bucket_map(num_buckets: int, max_distance: int, causal: bool = False, de
     num_buckets/4; see rel_bucket_build."""
     T, lib = _types(), load()
     _int32((num_buckets, max_distance), ("num_buckets", "max_distance"))
+    if max_distance > REL_BIAS_MAX_DISTANCE:  # no memory is taken for a map that is refused
+        raise USMError("rel_bucket_build", lib.rel_bucket_build(num_buckets, max_distance, int(bool(causal)), None, None))
     out = T.torch.empty(max(2 * max_distance + 1, 1), dtype=T.i32[0], device="cuda" if device is None else device)
     index = out.get_device()
     _array(out, "bucket_map", index, T.i32)
