@@ -152,6 +152,24 @@ def test_bucket_map_is_checked_before_memory_is_taken(usm):
     assert torch.cuda.max_memory_allocated() == before
 
 
+def test_bucket_map_stream_and_device_agree(usm):
+    import torch
+
+    class Elsewhere:  # a stream of another device
+        device = torch.device("cuda", torch.cuda.device_count())
+
+    with pytest.raises(ValueError, match="stream is on"):
+        usm.rel_bucket_map(32, 128, False, "cuda:0", stream=Elsewhere())
+    with pytest.raises(ValueError, match="stream is on"):
+        usm.rel_bucket_map(32, 128, device=0, stream=Elsewhere())
+    side = torch.cuda.Stream()
+    want = host(usm.rel_bucket_map(32, 128))
+    for device in (None, "cuda", "cuda:0", 0, torch.device("cuda", 0)):
+        t = usm.rel_bucket_map(32, 128, device=device, stream=side)
+        side.synchronize()
+        assert np.array_equal(host(t), want)
+
+
 # ---------------------------------------------------------------------------
 # Row counts next to 2^31
 # ---------------------------------------------------------------------------

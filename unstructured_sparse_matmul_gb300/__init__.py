@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import struct
 import threading
@@ -349,6 +350,9 @@ def _on_stream(fn):
     """Gives an operation its `stream` keyword.  With a stream of the caller's,
     copies, outputs and scratch belong to that stream too (as under
     torch.cuda.stream), so none of them races the current stream's work."""
+    signature = inspect.signature(fn)
+    takes_device = "device" in signature.parameters
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kwargs):
         if stream is None:
@@ -357,6 +361,11 @@ def _on_stream(fn):
         for t in (*args, *kwargs.values()):
             if isinstance(t, torch.Tensor) and t.device != stream.device:
                 raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+        device = signature.bind(*args, **kwargs).arguments.get("device") if takes_device else None
+        if device is not None:
+            device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+            if device.type != "cuda" or device.index not in (None, stream.device.index):
+                raise ValueError(f"stream is on {stream.device}, the result on {device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)
 
