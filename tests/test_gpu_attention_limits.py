@@ -170,6 +170,24 @@ def test_bucket_map_stream_and_device_agree(usm):
         assert np.array_equal(host(t), want)
 
 
+def test_empty_batches(usm):
+    """A batch of no sequences: no rows, no query blocks, no offsets."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ro, none, ci = torch.zeros(1, **i32), torch.empty(0, device="cuda"), torch.empty(0, **i32)
+    bmap, table = dev(np.zeros(5, dtype=np.int32)), put(np.ones((2, 4)))
+    kw = dict(seg_rows=1, seg_cols=8, q_offset=torch.empty(0, **i32))
+    assert usm.rel_bias(ro, ci, none, table, bmap, **kw).numel() == 0
+    assert np.array_equal(got(usm.rel_bias_grad(ro, ci, none, 2, 4, bmap, **kw)), np.zeros((2, 4)))
+    x = torch.empty((0, 8), device="cuda")
+    assert usm.attention(ro, ci, x, x, x, table=table, bucket_map=bmap, **kw).shape == (0, 8)
+    kw["q_offset"] = torch.zeros(1, **i32)  # "one block of M rows"
+    assert usm.rel_bias(ro, ci, none, table, bmap, **kw).numel() == 0
+    kw["q_offset"] = torch.zeros(2, **i32)
+    with pytest.raises(ValueError, match="q_offset"):
+        usm.rel_bias(ro, ci, none, table, bmap, **kw)
+
+
 # ---------------------------------------------------------------------------
 # Row counts next to 2^31
 # ---------------------------------------------------------------------------

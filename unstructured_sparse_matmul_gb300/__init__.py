@@ -467,6 +467,8 @@ def _bias(bucket_map, num_heads, num_buckets, seg_rows, seg_cols, q_offset, M, i
         raise ValueError("bucket_map has 2*max_distance + 1 entries")
     if q_offset is not None:
         blocks = 1 if seg_rows <= 0 or seg_rows > M else -(-M // seg_rows)
+        if M == 0 and q_offset.numel() == 0:
+            blocks = 0  # a batch of no sequences
         _array(q_offset, "q_offset", index, T.i32, blocks)
     if table is not None and not table.is_contiguous():
         raise ValueError("table must be contiguous")
