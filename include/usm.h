@@ -374,7 +374,8 @@ int csr_diff_softmax(int M, int nnz, const int *row_offsets, const float *scores
  *   workspace : csr_diff_softmax_grad_workspace_bytes(M) bytes, 16-byte
  *           aligned, contents ignored.
  * A masked entry (score -inf in map k) gives 0 in dscoresk and adds nothing
- * to ck, whatever dout holds there.  Sums are fp32 in a fixed order.
+ * to ck, whatever dout holds there.  A row's sums are fp32, dlambda's are formed
+ * in two fp32 numbers (about 48 bits) and rounded once, all in a fixed order.
  */
 size_t csr_diff_softmax_grad_workspace_bytes(int M);
 

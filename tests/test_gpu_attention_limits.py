@@ -189,6 +189,29 @@ def test_empty_batches(usm):
 
 
 # ---------------------------------------------------------------------------
+# Long sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("seg", [0, 1])
+def test_dlambda_of_cancelling_rows(usm, seg):
+    """Rows whose contributions cancel leave the others' sum: rows of one entry,
+    dout = 1 but for pairs of 2^30 and -2^30.  Pairs cancel whatever a row's own
+    arithmetic does to them, as it does the same to both; of the others it loses
+    at most 4 U each, and the result is rounded once."""
+    rng = np.random.default_rng(47)
+    M, pairs, heads = 60000, 100, 1 if seg == 0 else 3
+    dout = np.ones(M, dtype=np.float32)
+    head = np.arange(M) % heads
+    for h in range(heads):
+        at = rng.choice(np.flatnonzero(head == h), 2 * pairs, replace=False)
+        dout[at[:pairs]], dout[at[pairs:]] = 2.0 ** 30, -(2.0 ** 30)
+    s = put(np.zeros(M))
+    ro = dev(np.arange(M + 1, dtype=np.int32))
+    dlam = usm.diff_softmax_grad(ro, s, s, put(np.full(heads, 0.5)), put(dout), seg_rows=seg)[2]
+    want = -(np.bincount(head, minlength=heads) - 2.0 * pairs)
+    assert_near(got(dlam), want, 5 * U * np.abs(want), "dlambda")
+
+
+# ---------------------------------------------------------------------------
 # Row counts next to 2^31
 # ---------------------------------------------------------------------------
 def test_most_rows(usm):

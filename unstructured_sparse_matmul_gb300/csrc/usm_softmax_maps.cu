@@ -36,6 +36,7 @@
 #include "usm_cluster.cuh"
 #include "usm_internal.h"
 #include "usm_stream.cuh"
+#include "usm_sums.cuh"
 
 namespace usm {
 namespace {
@@ -672,15 +673,15 @@ __global__ void __launch_bounds__(WARPS * 32) cluster_rows_kernel(const MapArgs 
 }
 
 // dλ[h] = -Σ c2 over head h's rows (those with entries: the others have no c2): a
-// cluster per head, a fixed order.  CTAs are small, so that they fit beside those
+// cluster per head, a fixed order, in two fp32 numbers (rows may cancel).  CTAs are small, so that they fit beside those
 // of the kernel before (with 1024 threads they start after it: 3 us later).
 constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) lambda_grad_kernel(const MapArgs a, int blocks, float* __restrict__ dlambda) {
-    __shared__ float warp_part[kSumThreads / 32], whole;
+    __shared__ LongSum warp_part[kSumThreads / 32], whole;
     await_previous();
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
     const int head = blockIdx.x / ctas, t = threadIdx.x, lane = t & 31;
-    float x = 0.f;
+    LongSum x;
     // Rows of all of the head's blocks, one after the other.
     const long long rows = head < blocks ? ((blocks - 1 - head) / a.heads + 1LL) * a.seg_rows : 0;
     // Four rows a thread in flight.
@@ -696,19 +697,21 @@ __global__ void __launch_bounds__(kSumThreads) lambda_grad_kernel(const MapArgs 
             c2[u] = a.row_c2[at];
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x += some[u] ? c2[u] : 0.f;
+        for (int u = 0; u < 4; ++u) x.add(some[u] ? c2[u] : 0.f);
     }
-    x = warp_sum(x);
+    x = x.over_warp();
     if (lane == 0) warp_part[t >> 5] = x;
     __syncthreads();
     if (t < 32) {
-        x = warp_sum(lane < kSumThreads / 32 ? warp_part[lane] : 0.f);
+        x = lane < kSumThreads / 32 ? warp_part[lane] : LongSum{};
+        x = x.over_warp();
         if (lane == 0) whole = x;
     }
     if (ctas > 1) cluster_sync();
     if (rank == 0 && t == 0) {
-        for (int i = 1; i < ctas; ++i) x += load_cluster(smem_addr(&whole), i);
-        dlambda[head] = -x;
+        for (int i = 1; i < ctas; ++i)
+            x.add(LongSum{load_cluster(smem_addr(&whole.hi), i), load_cluster(smem_addr(&whole.lo), i)});
+        dlambda[head] = -x.value();
     }
     if (ctas > 1) cluster_sync();  // no CTA leaves what another may still read
 }
