@@ -328,8 +328,10 @@ int csr_rel_bias(int M, int K, int nnz, const int *row_offsets, const int *col_i
  *   bias    : as csr_rel_bias; table and table_dtype are not read.
  *   workspace : csr_rel_bias_grad_workspace_bytes(...) bytes of device
  *           scratch, 16-byte aligned, contents ignored.
- * Sums are fp32 in a fixed order (no atomics): the same call gives the same
- * bits.  The scores' own gradient is dscores unchanged.
+ * Sums are in a fixed order (no atomics): the same call gives the same bits.
+ * Positions beyond ±max_distance and the CTAs' parts are summed in two fp32
+ * numbers (about 48 bits); a thread's sums of a bucket's other positions, and
+ * the threads' join, are fp32.  The scores' own gradient is dscores unchanged.
  */
 size_t csr_rel_bias_grad_workspace_bytes(int M, int nnz, int seg_rows, int num_heads, int num_buckets);
 

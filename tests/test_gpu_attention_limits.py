@@ -211,6 +211,25 @@ def test_dlambda_of_cancelling_rows(usm, seg):
     assert_near(got(dlam), want, 5 * U * np.abs(want), "dlambda")
 
 
+@pytest.mark.parametrize("side", ["back", "ahead"])
+def test_bias_gradient_of_long_sums(usm, side):
+    """Many equal entries beyond the map's reach.  A thread adds at most 16 of
+    them in fp32 (15 roundings of relative size U), those sums with compensation
+    (2 U in all, and U^2 an addition); 32 threads of a CTA are joined in 5
+    levels, CTAs in 64 bits, and the result rounded: at most 25 U."""
+    import torch
+    rows, n, buckets = 3000, 4000, 512
+    ro = np.arange(rows + 1, dtype=np.int64) * n
+    ci = torch.arange(n, dtype=torch.int32, device="cuda").repeat(rows)
+    x = torch.full((rows * n,), 0.1, device="cuda")
+    bmap = dev(np.array([3, 4, 5], dtype=np.int32))
+    q_offset = dev(np.array([2**30 if side == "back" else -2**30], dtype=np.int32))
+    out = got(usm.rel_bias_grad(dev(ro.astype(np.int32)), ci, x, 1, buckets, bmap, q_offset=q_offset))
+    want = np.zeros((1, buckets))
+    want[0, 3 if side == "back" else 5] = rows * n * np.float64(np.float32(0.1))
+    assert_near(out, want, 25 * U * want, "dtable")
+
+
 # ---------------------------------------------------------------------------
 # Row counts next to 2^31
 # ---------------------------------------------------------------------------
