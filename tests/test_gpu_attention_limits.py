@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 
 import attention_ref as R
+import workloads as W
 from parity_util import dev, host
-from test_gpu_attention import HEADS, assert_near, got, put
+from test_gpu_attention import HEADS, assert_near, attention_case, got, make, put
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +97,52 @@ def test_scores_far_from_zero(usm, form, value):
     rows = np.bincount(heads, minlength=HEADS)
     csize = np.bincount(heads, np.abs(R.softmax_grad(ro, s2, dout)[2]), HEADS)
     assert_near(got(ol), dlam, np.bincount(heads, c, HEADS) + rows * U * csize + 1e-30, "dlambda")
+
+
+# ---------------------------------------------------------------------------
+# Attention: rows of V that nothing uses
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("maps,N", [(1, 32), (2, 32), (1, 200), (2, 72)])
+@pytest.mark.parametrize("shares", [False, True])
+def test_unused_rows_of_v(usm, shares, maps, N, dtype):
+    """Rows of V under entries that are masked in every map may hold NaN and
+    infinities, in both forms of the kernel."""
+    import torch
+    if shares:
+        rng = np.random.default_rng(43)
+        lengths, cols = rng.integers(600, 900, 200), 4000
+        lengths[::7] = 0
+        ro, ci = W.csr_from_lengths(rng, lengths.astype(np.int64), cols, np.arange(200) % 3 * cols)
+        p = dict(rng=rng, ro=ro, ci=ci, M=200, K=3 * cols, cols=cols, seg=1, blocks=200, nnz=ci.size,
+                 heads=R.head_of_rows(200, 1, HEADS), longest=900)
+    else:
+        p = make("tokens")
+    D = 48
+    Qs, Ks, V, lam, bias, entry = attention_case(p, D, N, maps, dtype, False)
+    # A map of positions to buckets that sends every third key to a bucket of -inf.
+    reach = p["cols"]
+    bmap = (np.arange(2 * reach + 1) % 3).astype(np.int32)
+    table = p["rng"].standard_normal((HEADS, 3)).astype(np.float32)
+    table[:, 1] = -np.inf
+    k = R.bucket_of_entries(p["ro"], p["ci"], bmap, p["seg"], p["cols"], None, 3)
+    masked = table[p["heads"][R.rows_of(p["ro"])], k] == -np.inf
+    unused = np.zeros(p["K"], dtype=bool)
+    unused[p["ci"][masked]] = True
+    unused[p["ci"][~masked]] = False
+    assert unused.sum() > 100
+    need = usm.load().csr_attention_workspace_bytes(p["M"], p["K"], D, N, p["nnz"], int(maps == 2), int(dtype == "bf16"))
+    assert (need > 0) == shares
+    kw = dict(scale=0.2, seg_rows=p["seg"], table=put(table), bucket_map=dev(bmap), seg_cols=p["cols"])
+    if maps == 2:
+        kw.update(Q2=put(Qs[1], dtype), K2=put(Ks[1], dtype), lam=put(lam))
+    v = put(V, dtype)
+    bad = v.clone()
+    at = torch.from_numpy(np.flatnonzero(unused)).cuda()
+    bad[at] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").repeat(at.numel())[:at.numel(), None].to(v.dtype)
+    call = lambda t: usm.attention(dev(p["ro"]), dev(p["ci"]), put(Qs[0], dtype), put(Ks[0], dtype), t, **kw)
+    x, y = call(v), call(bad)
+    assert torch.isfinite(x).all() and torch.equal(x, y)
 
 
 # ---------------------------------------------------------------------------
