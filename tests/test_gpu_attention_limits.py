@@ -139,7 +139,8 @@ def test_unused_rows_of_v(usm, shares, maps, N, dtype):
     v = put(V, dtype)
     bad = v.clone()
     at = torch.from_numpy(np.flatnonzero(unused)).cuda()
-    bad[at] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").repeat(at.numel())[:at.numel(), None].to(v.dtype)
+    junk = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").repeat(at.numel())
+    bad[at] = junk[:at.numel(), None].to(v.dtype)
     call = lambda t: usm.attention(dev(p["ro"]), dev(p["ci"]), put(Qs[0], dtype), put(Ks[0], dtype), t, **kw)
     x, y = call(v), call(bad)
     assert torch.isfinite(x).all() and torch.equal(x, y)

@@ -9,7 +9,7 @@
 // takes the rows that begin in an equal share of the entries and streams them
 // through a ring in shared memory (usm_stream.cuh), so copies are in flight all
 // the time whatever the rows' arithmetic and lengths do.  An SM's shared memory
-// holds the rings of 8 to 12 warps, few to cover the latency of a row's
+// holds the rings of 8 to 16 warps, few to cover the latency of a row's
 // arithmetic, which is what is left to wait for (figures: the differential map of
 // 8x4096 rows of 410 entries in a replayed graph):
 //   - A row is walked twice in the ring (weights and their sums; results), four
@@ -183,19 +183,17 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
         m[k] = warp_max(top);
         if (lane == 0) sh.top[k][warp] = m[k];
     }
-    {
-        __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k)
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
+    if (ctas > 1) {
+        if (threadIdx.x < MAPS) sh.whole_top[threadIdx.x] = threadIdx.x ? m[MAPS - 1] : m[0];
+        cluster_sync();
 #pragma unroll
         for (int k = 0; k < MAPS; ++k)
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) m[k] = fmaxf(m[k], sh.top[k][w]);
-        if (ctas > 1) {
-            if (threadIdx.x < MAPS) sh.whole_top[threadIdx.x] = threadIdx.x ? m[MAPS - 1] : m[0];
-            cluster_sync();
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k)
-                for (int i = 0; i < ctas; ++i) m[k] = fmaxf(m[k], load_cluster(smem_addr(&sh.whole_top[k]), i));
-        }
+            for (int i = 0; i < ctas; ++i) m[k] = fmaxf(m[k], load_cluster(smem_addr(&sh.whole_top[k]), i));
     }
     // Weights (in the scores' registers) and their sums.
     float z[MAPS], c[MAPS], inv[MAPS];
@@ -241,36 +239,34 @@ __device__ __forceinline__ void block_row(const MapArgs& a, int r, float lam, in
             sh.sum[k][1][warp] = c[k];
         }
     }
-    {
-        __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < MAPS; ++k) {
+        z[k] = c[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            z[k] += sh.sum[k][0][w];
+            if constexpr (GRAD) c[k] += sh.sum[k][1][w];
+        }
+    }
+    if (ctas > 1) {
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int k = 0; k < MAPS; ++k) {
+                sh.whole[k][0] = z[k];
+                sh.whole[k][1] = c[k];
+            }
+        }
+        cluster_sync();
 #pragma unroll
         for (int k = 0; k < MAPS; ++k) {
             z[k] = c[k] = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                z[k] += sh.sum[k][0][w];
-                if constexpr (GRAD) c[k] += sh.sum[k][1][w];
+            for (int i = 0; i < ctas; ++i) {
+                z[k] += load_cluster(smem_addr(&sh.whole[k][0]), i);
+                if constexpr (GRAD) c[k] += load_cluster(smem_addr(&sh.whole[k][1]), i);
             }
         }
-        if (ctas > 1) {
-            if (threadIdx.x == 0) {
-#pragma unroll
-                for (int k = 0; k < MAPS; ++k) {
-                    sh.whole[k][0] = z[k];
-                    sh.whole[k][1] = c[k];
-                }
-            }
-            cluster_sync();
-#pragma unroll
-            for (int k = 0; k < MAPS; ++k) {
-                z[k] = c[k] = 0.f;
-                for (int i = 0; i < ctas; ++i) {
-                    z[k] += load_cluster(smem_addr(&sh.whole[k][0]), i);
-                    if constexpr (GRAD) c[k] += load_cluster(smem_addr(&sh.whole[k][1]), i);
-                }
-            }
-            cluster_sync();  // no CTA leaves what another may still read
-        }
+        cluster_sync();  // no CTA leaves what another may still read
     }
 #pragma unroll
     for (int k = 0; k < MAPS; ++k) {
@@ -673,8 +669,9 @@ __global__ void __launch_bounds__(WARPS * 32) cluster_rows_kernel(const MapArgs 
 }
 
 // dλ[h] = -Σ c2 over head h's rows (those with entries: the others have no c2): a
-// cluster per head, a fixed order, in two fp32 numbers (rows may cancel).  CTAs are small, so that they fit beside those
-// of the kernel before (with 1024 threads they start after it: 3 us later).
+// cluster per head, a fixed order, in two fp32 numbers, since rows may cancel.  CTAs
+// are small, so that they fit beside those of the kernel before (with 1024 threads
+// they start after it: 3 us later).
 constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) lambda_grad_kernel(const MapArgs a, int blocks, float* __restrict__ dlambda) {
     __shared__ LongSum warp_part[kSumThreads / 32], whole;
