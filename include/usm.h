@@ -390,7 +390,8 @@ int csr_diff_softmax_grad(int M, int nnz, const int *row_offsets, const float *s
  * csr_row_softmax_grad — the gradient of csr_row_softmax:
  *   dscores[p] = P[p]·(dout[p] - Σ_{q in row} P[q]·dout[q]),
  * P formed again from the fp32 scores.  Types, masked entries and in-place use
- * as csr_diff_softmax_grad.
+ * as csr_diff_softmax_grad: a row whose scores are all -inf has gradient 0 here,
+ * while csr_row_softmax gives NaN for it.
  */
 int csr_row_softmax_grad(int M, int nnz, const int *row_offsets, const float *scores, const void *dout,
                          usm_dtype dout_dtype, void *dscores, usm_dtype out_dtype, void *stream);
