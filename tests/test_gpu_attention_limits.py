@@ -341,3 +341,27 @@ def test_runs_of_rows_without_entries_take_no_time(usm):
         end.record()
         end.synchronize()
         assert begin.elapsed_time(end) < 250
+
+
+def test_sums_that_are_not_finite(usm):
+    """Infinities and NaN come through the sums in two numbers as through plain
+    additions."""
+    inf, nan = np.inf, np.nan
+    # Bucket 0 for keys behind, 1 for the same position, 2 for keys ahead; one row.
+    for value, other, want in ((inf, 1.0, inf), (-inf, 1.0, -inf), (nan, 1.0, nan), (inf, -inf, nan), (3e38, 3e38, inf)):
+        for bucket, cols in enumerate((range(0, 8), (8, 8), range(9, 17))):
+            ci = np.array(list(range(0, 8)) + [8, 8] + list(range(9, 17)), dtype=np.int32)
+            ds = np.ones(ci.size, dtype=np.float32)
+            at = [i for i in range(ci.size) if ci[i] in cols]
+            ds[at[0]], ds[at[-1]] = value, other
+            out = got(usm.rel_bias_grad(dev(np.array([0, ci.size], dtype=np.int32)), dev(ci), put(ds), 1, 3,
+                                        dev(np.arange(3, dtype=np.int32)), q_offset=dev(np.array([8], dtype=np.int32))))
+            expected = np.array([[8.0, 2.0, 8.0]])
+            expected[0, bucket] = want
+            assert np.array_equal(out, expected, equal_nan=True), (value, other, bucket, out)
+    dout = np.ones(3000, dtype=np.float32)
+    dout[300], dout[301], dout[302] = inf, nan, -1.0
+    dout[601] = inf
+    s, ro = put(np.zeros(3000)), dev(np.arange(3001, dtype=np.int32))
+    dlam = got(usm.diff_softmax_grad(ro, s, s, put(np.full(3, 0.5)), put(dout), seg_rows=1)[2])
+    assert dlam[0] == -inf and np.isnan(dlam[1]) and abs(dlam[2] + 998) <= 5 * U * 1000
