@@ -432,6 +432,115 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int *row_offsets, c
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * A paged cache of keys and values, as the two calls below see it.
+ *
+ * Sequence b (of num_seqs) has lengths[b] tokens in its cache, of which the last
+ * n_b are the call's new tokens: its i-th new token stands at position
+ * lengths[b] - n_b + i.  The new tokens of all sequences follow one another in
+ * the calls' arrays: sequence b's are q_offsets[b]..q_offsets[b+1]-1, or, with
+ * q_offsets = NULL, an equal share of them each (their number is then a multiple
+ * of num_seqs).  Position p of sequence b lies in slot p % page_size of page
+ * page_table[b·table_stride + p / page_size]; a slot holds head_dim elements for
+ * each of kv_heads heads, at k + page·k_page_stride + slot·k_slot_stride +
+ * head·k_head_stride (and v alike).  Any order of pages, slots and heads is a
+ * matter of the strides; sequences may share pages.
+ *
+ * Whatever the arrays hold, no address outside the caches is formed: offsets are
+ * clamped into [0, tokens], negative lengths count as 0, positions past the
+ * table's table_pages pages have no slot, and a page outside [0, num_pages) is
+ * clamped where it is read and skipped where it would be written.
+ *
+ * A host struct: the calls read it before they return and keep no pointer to it.
+ */
+typedef struct usm_paged_cache {
+    void *k, *v; /* device, 16-byte aligned */
+    long long k_page_stride, k_slot_stride, k_head_stride; /* elements; multiples of 16 bytes; at least head_dim */
+    long long v_page_stride, v_slot_stride, v_head_stride; /* where there is more than one page, slot or head */
+    const int *page_table; /* device int32, num_seqs rows */
+    const int *lengths;    /* device int32[num_seqs] */
+    const int *q_offsets;  /* device int32[num_seqs + 1], or NULL */
+    usm_dtype dtype;       /* of the cache and of the calls' k, v, q and out */
+    int num_pages, page_size; /* > 0 */
+    int kv_heads, head_dim;   /* > 0; head_dim rows are multiples of 16 bytes */
+    int num_seqs, table_stride, table_pages; /* table_pages: pages listed for a sequence */
+} usm_paged_cache;
+
+/*
+ * usm_tokens — rows of head_dim elements for each new token and head, at data +
+ * token·token_stride + head·head_stride (elements, multiples of 16 bytes; data
+ * 16-byte aligned).  A host struct, as usm_paged_cache.
+ */
+typedef struct usm_tokens {
+    void *data;
+    long long token_stride, head_stride;
+} usm_tokens;
+
+/*
+ * rope_table_build — the table of rotations by position that paged_append reads:
+ * table[p][j] = cos(p·base^(-2j/rot_dim)), table[p][rot_dim/2 + j] = the sine,
+ * for p < positions and j < rot_dim/2.  Angles are formed in 64 bits and their
+ * cosines and sines rounded once, so that far positions lose nothing.
+ *   table : device fp32, positions×rot_dim, written.
+ * Limits: rot_dim even and ≥ 2, base > 0 and finite, positions·rot_dim < 2^31.
+ * positions = 0 is a no-op.
+ */
+int rope_table_build(int positions, int rot_dim, double base, float *table, void *stream);
+
+/*
+ * paged_append — writes the new tokens' keys and values to their slots, the keys
+ * rotated by their positions on the way, and rotates the queries.
+ *
+ *   k, v  : `tokens` rows for kv_heads heads; v is stored unchanged.
+ *   q, q_out, q_heads : the queries and where their rotated form goes; both NULL
+ *           (and q_heads 0) for none.  q_out may be q (same strides).
+ *   rope  : device fp32, rope_positions×rot_dim as rope_table_build makes it (any
+ *           cosines and sines will do), 16-byte aligned; or NULL with rot_dim = 0
+ *           for no rotation.  Of each head's row the first rot_dim elements are
+ *           turned, in pairs (j, j + rot_dim/2), or (2j, 2j + 1) with interleaved = 1:
+ *           (x1·cos - x2·sin, x2·cos + x1·sin), in fp32 with one rounding to
+ *           `dtype`; the others are stored unchanged.
+ * A token at a position without a slot, or whose page is outside [0, num_pages),
+ * is not stored; its query is written all the same.  Positions outside the
+ * table take its nearest row.  Tokens outside every sequence are left alone, in
+ * q_out too.  Where two tokens of a call share a slot either may end up in it.
+ * Limits: 0 ≤ rot_dim ≤ head_dim, even; tokens·(heads) < 2^31.
+ * tokens = 0 or num_seqs = 0 is a no-op.
+ */
+int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, const usm_tokens *v,
+                 const usm_tokens *q, const usm_tokens *q_out, int q_heads, const float *rope, int rope_positions,
+                 int rot_dim, int interleaved, void *stream);
+
+/*
+ * paged_attention — attention of the new tokens over their sequences' caches:
+ *   out[t][h] = Σ_j P[j]·V[j],  P = softmax over the visible j of scale·(q[t][h]·K[j]),
+ * K and V those of head h / (q_heads / kv_heads) of the token's sequence.  With
+ * causal = 1 a token at position p sees positions j ≤ p, with causal = 0 all
+ * j < lengths[b]; with window > 0 only those with j > p - window of them.  The
+ * keys of the new tokens themselves have to be in the cache (paged_append).
+ *
+ *   q, out : `tokens` rows for q_heads heads, a multiple of kv_heads.  out must
+ *            not overlap anything else of the call.
+ *   scale  : finite, ≥ 0.
+ *   workspace : paged_attention_workspace_bytes(...) bytes of device scratch,
+ *            16-byte aligned, contents ignored.
+ * Products, statistics and sums are fp32.  bf16: probabilities are rounded to
+ * bf16 before their product with V (relative 2^-9 each, as the output's own
+ * rounding); head_dim > 128 keeps them in fp32.
+ * A token that sees no key, or whose scores are all -inf, gives a zero row.  Keys
+ * and values that a token does not see never touch its row, whatever they hold
+ * (unwritten slots, later tokens, NaN or infinities); an infinity in a row of V that
+ * it sees makes its column infinite or NaN.  Rows of tokens outside every
+ * sequence are left alone.
+ * Limits: head_dim ≤ 256; tokens·q_heads < 2^31; lengths < 2^30.
+ * Deterministic (no atomics).  tokens = 0 or num_seqs = 0 is a no-op.
+ */
+size_t paged_attention_workspace_bytes(int tokens, int q_heads, int kv_heads, int head_dim, usm_dtype dtype);
+
+int paged_attention(const usm_paged_cache *cache, int tokens, const usm_tokens *q, int q_heads, float scale,
+                    int causal, int window, const usm_tokens *out, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
  * csr_transpose — Aᵀ in CSR, for the sparse layer's input gradient.
  *
  * Source: "Sparse GPU Kernels for Deep Learning", summary card, "Summary"

@@ -67,6 +67,14 @@ SIGNATURES.update({
 })
 
 
+SIGNATURES.update({
+    "rope_table_build": (_i, [_i, _i, ctypes.c_double, _vp, _vp]),
+    "paged_append": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp]),
+    "paged_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "paged_attention": (_i, [_vp, _i, _vp, _i, ctypes.c_float, _i, _i, _vp, _vp, _sz, _vp]),
+})
+
+
 class RelBias(ctypes.Structure):
     """usm_rel_bias of include/usm.h."""
     _fields_ = [("table", _vp), ("table_dtype", _i), ("num_heads", _i), ("num_buckets", _i), ("bucket_map", _vp),
@@ -74,6 +82,22 @@ class RelBias(ctypes.Structure):
 
 
 REL_BIAS_MAX_DISTANCE = 8192  # USM_REL_BIAS_MAX_DISTANCE of include/usm.h
+
+class PagedCache(ctypes.Structure):
+    """usm_paged_cache of include/usm.h."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_page_stride", _ll), ("k_slot_stride", _ll), ("k_head_stride", _ll),
+                ("v_page_stride", _ll), ("v_slot_stride", _ll), ("v_head_stride", _ll), ("page_table", _vp),
+                ("lengths", _vp), ("q_offsets", _vp), ("dtype", _i), ("num_pages", _i), ("page_size", _i),
+                ("kv_heads", _i), ("head_dim", _i), ("num_seqs", _i), ("table_stride", _i), ("table_pages", _i)]
+
+
+class Tokens(ctypes.Structure):
+    """usm_tokens of include/usm.h."""
+    _fields_ = [("data", _vp), ("token_stride", _ll), ("head_stride", _ll)]
+
+
+_pack_paged = struct.Struct("@PPqqqqqqPPPiiiiiiii").pack  # PagedCache and Tokens as bytes
+_pack_tokens = struct.Struct("@Pqq").pack
 
 _pack_bias = struct.Struct("@PiiiPiiP").pack  # the same as bytes, in a quarter of the time
 
@@ -690,6 +714,138 @@ def attention(row_offsets, col_indices, Q, Km, V, scale: float = 1.0, Q2=None, K
     _run("csr_attention", lib.csr_attention, index, T, M, K, D, N, nnz, row_offsets.data_ptr(), col_indices.data_ptr(),
          Q.data_ptr(), ldq, Km.data_ptr(), ldk, _ptr(Q2), ldq2, _ptr(K2), ldk2, V.data_ptr(), ldv, scale, _ptr(lam),
          heads, seg_rows, b, out.data_ptr(), ldc, code, _ptr(ws), need)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Paged cache of keys and values: append with rotation, and attention of the
+# new tokens over it.  Caches are num_pages x page_size x kv_heads x head_dim
+# tensors with any strides; page_table is num_seqs x pages, lengths holds the
+# tokens of each sequence with the new ones included, q_offsets (None: equal
+# shares) where each sequence's new tokens begin.
+# ---------------------------------------------------------------------------
+@_on_stream
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device=None):
+    """fp32 [positions, rot_dim]: cosines, then sines, of p*base^(-2j/rot_dim);
+    see rope_table_build."""
+    T, lib = _types(), load()
+    _int32((positions, rot_dim), ("positions", "rot_dim"))
+    if not 0 <= positions * max(rot_dim, 0) < 2**31 or rot_dim < 2:  # no memory is taken for a table that is refused
+        raise USMError("rope_table_build", lib.rope_table_build(positions, rot_dim, base, None, None))
+    out = T.torch.empty((positions, rot_dim), dtype=T.f32[0], device="cuda" if device is None else device)
+    index = out.get_device()
+    _tensor(out, "rope_table", index, T.f32, 2)
+    _run("rope_table_build", lib.rope_table_build, index, T, positions, rot_dim, base, out.data_ptr())
+    return out
+
+
+def _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T):
+    """The usm_paged_cache struct, as bytes that the call takes a pointer to."""
+    _tensor(k_cache, "k_cache", index, T.real, 4)
+    _tensor(v_cache, "v_cache", index, (k_cache.dtype,), 4)
+    _tensor(page_table, "page_table", index, T.i32, 2)
+    shape = pages, slots, heads, D = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError(f"k_cache is {tuple(shape)}, v_cache {tuple(v_cache.shape)}")
+    kp, ks, kh, k1 = k_cache.stride()
+    vp, vs, vh, v1 = v_cache.stride()
+    seqs, listed = page_table.shape
+    row, one = page_table.stride()
+    if D > 1 and (k1 != 1 or v1 != 1):
+        raise ValueError("caches must have unit stride in their last dimension")
+    if listed > 1 and one != 1:
+        raise ValueError("page_table must have unit column stride")
+    if max(pages, slots, heads, D, seqs, listed, row) >= 2**31:
+        raise ValueError("a dimension of the cache or its page table does not fit 32 bits")
+    _array(lengths, "lengths", index, T.i32, seqs)
+    if q_offsets is not None:
+        _array(q_offsets, "q_offsets", index, T.i32, seqs + 1)
+    return _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), kp, ks, kh, vp, vs, vh, page_table.data_ptr(),
+                       lengths.data_ptr(), 0 if q_offsets is None else q_offsets.data_ptr(), _code(k_cache, T), pages,
+                       slots, heads, D, seqs, row, listed)
+
+
+def _tokens(t, name, index, dtype, shape, copy=True):
+    """Rows of the new tokens (tokens x heads x head_dim) as the library reads
+    them, with the usm_tokens struct as bytes; inputs whose rows are not 16-byte
+    aligned are copied."""
+    _tensor(t, name, index, (dtype,), 3)
+    if t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    a, b, one = t.stride()
+    if copy and (one != 1 or (t.data_ptr() | a * t.element_size() | b * t.element_size()) & 15):
+        t = t.clone(memory_format=_Types.torch.contiguous_format)
+        a, b, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return t, _pack_tokens(t.data_ptr(), a, b)
+
+
+@_on_stream
+def paged_append(k, v, k_cache, v_cache, page_table, lengths, q_offsets=None, rope=None, interleaved: bool = False, q=None,
+                 q_out=None):
+    """Writes the new tokens' keys (rotated by position) and values into their
+    slots of the cache; with q returns the rotated queries (in q_out, which may
+    be q).  k, v: tokens x kv_heads x head_dim, q: tokens x q_heads x head_dim;
+    rope: positions x rot_dim of rope_table, or None; see paged_append."""
+    T, lib = _types(), load()
+    index = _device_of(k_cache, "k_cache")
+    cache = _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T)
+    _tensor(k, "k", index, (k_cache.dtype,), 3)
+    n, (heads, D), dt = _entries(k.shape[0]), k_cache.shape[2:], k_cache.dtype
+    k, kt = _tokens(k, "k", index, dt, (n, heads, D))
+    v, vt = _tokens(v, "v", index, dt, (n, heads, D))
+    qt = ot = None
+    q_heads = rot = positions = 0
+    if q is not None:
+        _tensor(q, "q", index, (dt,), 3)
+        q_heads = q.shape[1]
+        shape = (n, q_heads, D)
+        if q_out is None:
+            q_out = T.empty(shape, dtype=dt, device=q.device)
+        q, qt = _tokens(q, "q", index, dt, shape)
+        _, ot = _tokens(q_out, "q_out", index, dt, shape, copy=False)
+        if q_heads == 0:
+            qt = ot = None
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if rope is not None:
+        _tensor(rope, "rope", index, T.f32, 2)
+        if not rope.is_contiguous():
+            raise ValueError("rope must be contiguous")
+        positions, rot = rope.shape
+    _run("paged_append", lib.paged_append, index, T, cache, n, kt, vt, qt, ot, q_heads, _ptr(rope), positions, rot,
+         int(bool(interleaved)))
+    return q_out
+
+
+@_on_stream
+def paged_attention(q, k_cache, v_cache, page_table, lengths, q_offsets=None, scale: float = 1.0, causal: bool = True,
+                    window: int = 0, out=None, workspace=None):
+    """Attention of the new tokens q (tokens x q_heads x head_dim) over their
+    sequences' pages, of q's type: softmax of scale*(q.K) over the keys up to the
+    token's own position (causal) and, with window > 0, at most window of them;
+    see paged_attention."""
+    T, lib = _types(), load()
+    index = _device_of(k_cache, "k_cache")
+    cache = _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T)
+    dt = k_cache.dtype
+    _tensor(q, "q", index, (dt,), 3)
+    shape = n, q_heads, D = q.shape
+    _entries(n * q_heads)
+    _int32((window,), ("window",))
+    heads = k_cache.shape[2]
+    if D != k_cache.shape[3]:
+        raise ValueError(f"q has {D} columns, the cache {k_cache.shape[3]}")
+    if out is None:
+        out = T.empty(shape, dtype=dt, device=q.device)
+    q, qt = _tokens(q, "q", index, dt, shape)
+    _, ot = _tokens(out, "out", index, dt, shape, copy=False)
+    code = _code(q, T)
+    need = lib.paged_attention_workspace_bytes(n, q_heads, heads, D, code)
+    ws = _workspace(workspace, need, q, T)
+    _run("paged_attention", lib.paged_attention, index, T, cache, n, qt, q_heads, scale, int(bool(causal)), window, ot,
+         _ptr(ws), need)
     return out
 
 

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "usm_device.cuh"
@@ -323,6 +324,56 @@ RelArgs rel_args(const usm_rel_bias* b, int M, int seg_rows) {
     return {b->table,    b->table_dtype == USM_BF16, b->num_heads, b->num_buckets, b->bucket_map, b->max_distance,
             b->seg_cols, b->q_offset,                effective_seg(M, seg_rows)};
 }
+
+constexpr int kPagedMaxHeadDim = 256;
+
+// One cache's array: `extent` x stride, for pages, slots and heads.
+int check_cache_array(const usm_paged_cache& c, const void* p, long long page, long long slot, long long head) {
+    const long long es = (long long)dtype_size(c.dtype);
+    if (!p) return USM_ERR_INVALID_ARG;
+    const struct {
+        int extent;
+        long long stride;
+    } dims[3] = {{c.num_pages, page}, {c.page_size, slot}, {c.kv_heads, head}};
+    for (const auto& d : dims)
+        if (d.extent > 1 && d.stride < c.head_dim) return USM_ERR_INVALID_ARG;
+    for (const auto& d : dims)
+        if (d.extent > 1 && d.stride * es % 16 != 0) return USM_ERR_ALIGNMENT;
+    return aligned16(p) ? USM_OK : USM_ERR_ALIGNMENT;
+}
+
+// A paged cache and the number of its call's tokens; `heads`: rows of a token.
+// Pointers are looked at where there are tokens to work on.
+int check_paged(const usm_paged_cache& c, int tokens, long long heads) {
+    if (tokens < 0 || c.num_seqs < 0 || c.kv_heads <= 0 || c.head_dim <= 0 || c.num_pages <= 0 || c.page_size <= 0 ||
+        c.table_pages < 0 || !dtype_ok(c.dtype))
+        return USM_ERR_INVALID_ARG;
+    if (c.head_dim > kPagedMaxHeadDim || tokens * heads >= 1LL << 31) return USM_ERR_UNSUPPORTED;
+    if (c.head_dim * dtype_size(c.dtype) % 16 != 0) return USM_ERR_ALIGNMENT;
+    if (tokens == 0 || c.num_seqs == 0) return USM_OK;
+    if (!c.lengths || (c.table_pages > 0 && !c.page_table)) return USM_ERR_INVALID_ARG;
+    if (c.num_seqs > 1 && c.table_stride < c.table_pages) return USM_ERR_INVALID_ARG;
+    if (!c.q_offsets && tokens % c.num_seqs != 0) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(c.lengths, 4) || !aligned_to(c.page_table, 4) || !aligned_to(c.q_offsets, 4)) return USM_ERR_ALIGNMENT;
+    const int code = check_cache_array(c, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride);
+    return code != USM_OK ? code : check_cache_array(c, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride);
+}
+
+// Rows of the call's tokens; written ones must not lie over one another.
+int check_tokens(const usm_tokens* t, const usm_paged_cache& c, int tokens, int heads, bool written) {
+    if (!t || !t->data) return USM_ERR_INVALID_ARG;
+    const long long es = (long long)dtype_size(c.dtype), least = written ? c.head_dim : 0;
+    if ((tokens > 1 && t->token_stride < least) || (heads > 1 && t->head_stride < least)) return USM_ERR_INVALID_ARG;
+    if ((tokens > 1 && t->token_stride * es % 16 != 0) || (heads > 1 && t->head_stride * es % 16 != 0))
+        return USM_ERR_ALIGNMENT;
+    return aligned16(t->data) ? USM_OK : USM_ERR_ALIGNMENT;
+}
+
+// Positions that a sequence's row of the page table has slots for.
+int capacity_of(const usm_paged_cache& c) {
+    const long long n = (long long)c.table_pages * c.page_size;
+    return n < kPagedMaxLength ? (int)n : kPagedMaxLength;
+}
 }  // namespace
 
 int rel_bucket_build(int num_buckets, int max_distance, int causal, int* bucket_map, void* stream) {
@@ -485,6 +536,91 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int* row_offsets, c
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return USM_ERR_WORKSPACE;
     if (need > 0 && !aligned16(workspace)) return USM_ERR_ALIGNMENT;
     return launch_attention(a, dtype == USM_BF16, workspace, as_stream(stream));
+}
+
+int rope_table_build(int positions, int rot_dim, double base, float* table, void* stream) {
+    if (positions < 0 || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 0.0) || base > 1.7976931348623157e308)
+        return USM_ERR_INVALID_ARG;
+    if ((long long)positions * rot_dim >= 1LL << 31) return USM_ERR_UNSUPPORTED;
+    if (positions == 0) return USM_OK;
+    if (!table) return USM_ERR_INVALID_ARG;
+    if (!aligned_to(table, 4)) return USM_ERR_ALIGNMENT;
+    return launch_rope_table(positions, rot_dim, base, table, as_stream(stream));
+}
+
+int paged_append(const usm_paged_cache* cache, int tokens, const usm_tokens* k, const usm_tokens* v, const usm_tokens* q,
+                 const usm_tokens* q_out, int q_heads, const float* rope, int rope_positions, int rot_dim,
+                 int interleaved, void* stream) {
+    if (!cache) return USM_ERR_INVALID_ARG;
+    const usm_paged_cache& c = *cache;
+    if ((q != nullptr) != (q_out != nullptr) || q_heads < 0 || (q != nullptr) != (q_heads > 0)) return USM_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim % 2 != 0 || (interleaved != 0 && interleaved != 1)) return USM_ERR_INVALID_ARG;
+    const int code = check_paged(c, tokens, (long long)q_heads + 2LL * c.kv_heads);
+    if (code != USM_OK) return code;
+    if (rot_dim > c.head_dim) return USM_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!rope || rope_positions <= 0)) return USM_ERR_INVALID_ARG;
+    if (rot_dim > 0 && !aligned16(rope)) return USM_ERR_ALIGNMENT;
+    if (tokens == 0 || c.num_seqs == 0) return USM_OK;
+    int status = check_tokens(k, c, tokens, c.kv_heads, false);
+    if (status == USM_OK) status = check_tokens(v, c, tokens, c.kv_heads, false);
+    if (status == USM_OK && q) status = check_tokens(q, c, tokens, q_heads, false);
+    if (status == USM_OK && q) status = check_tokens(q_out, c, tokens, q_heads, true);
+    if (status != USM_OK) return status;
+    AppendArgs a{};
+    a.k = k->data, a.k_token = k->token_stride, a.k_head = k->head_stride;
+    a.v = v->data, a.v_token = v->token_stride, a.v_head = v->head_stride;
+    if (q) {
+        a.q = q->data, a.q_token = q->token_stride, a.q_head = q->head_stride;
+        a.q_out = q_out->data, a.q_out_token = q_out->token_stride, a.q_out_head = q_out->head_stride;
+    }
+    a.k_cache = c.k, a.kc_page = c.k_page_stride, a.kc_slot = c.k_slot_stride, a.kc_head = c.k_head_stride;
+    a.v_cache = c.v, a.vc_page = c.v_page_stride, a.vc_slot = c.v_slot_stride, a.vc_head = c.v_head_stride;
+    a.table = c.page_table, a.lengths = c.lengths, a.q_offsets = c.q_offsets;
+    a.table_stride = c.table_stride, a.num_pages = c.num_pages, a.page_size = c.page_size, a.capacity = capacity_of(c);
+    a.num_seqs = c.num_seqs, a.tokens = tokens, a.per_seq = tokens / c.num_seqs;
+    a.kv_heads = c.kv_heads, a.q_heads = q_heads, a.head_dim = c.head_dim;
+    a.rope = rope, a.rope_positions = rope_positions, a.rot = rot_dim, a.interleaved = interleaved;
+    return launch_paged_append(a, c.dtype == USM_BF16, as_stream(stream));
+}
+
+size_t paged_attention_workspace_bytes(int tokens, int q_heads, int kv_heads, int head_dim, usm_dtype dtype) {
+    if (tokens <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
+        head_dim > kPagedMaxHeadDim || !dtype_ok(dtype) || (long long)tokens * q_heads >= 1LL << 31)
+        return 0;
+    return paged_attention_workspace(tokens, q_heads, kv_heads, head_dim, dtype == USM_BF16);
+}
+
+int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* q, int q_heads, float scale, int causal,
+                    int window, const usm_tokens* out, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!cache) return USM_ERR_INVALID_ARG;
+    const usm_paged_cache& c = *cache;
+    if (q_heads <= 0 || !(scale >= 0.f) || scale > 3.402823466e38f || (causal != 0 && causal != 1) || window < 0)
+        return USM_ERR_INVALID_ARG;
+    const int code = check_paged(c, tokens, q_heads);
+    if (code != USM_OK) return code;
+    if (q_heads % c.kv_heads != 0) return USM_ERR_INVALID_ARG;
+    if (tokens == 0 || c.num_seqs == 0) return USM_OK;
+    int status = check_tokens(q, c, tokens, q_heads, false);
+    if (status == USM_OK) status = check_tokens(out, c, tokens, q_heads, true);
+    if (status != USM_OK) return status;
+    const bool bf16 = c.dtype == USM_BF16;
+    if (!workspace || workspace_bytes < paged_attention_workspace(tokens, q_heads, c.kv_heads, c.head_dim, bf16))
+        return USM_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return USM_ERR_ALIGNMENT;
+    PagedArgs a{};
+    a.q = q->data, a.q_token = q->token_stride, a.q_head = q->head_stride;
+    a.out = out->data, a.out_token = out->token_stride, a.out_head = out->head_stride;
+    a.k = c.k, a.k_page = c.k_page_stride, a.k_slot = c.k_slot_stride, a.k_head = c.k_head_stride;
+    a.v = c.v, a.v_page = c.v_page_stride, a.v_slot = c.v_slot_stride, a.v_head = c.v_head_stride;
+    a.table = c.page_table, a.lengths = c.lengths, a.q_offsets = c.q_offsets;
+    a.table_stride = c.table_stride, a.num_pages = c.num_pages, a.page_size = c.page_size, a.capacity = capacity_of(c);
+    a.num_seqs = c.num_seqs, a.tokens = tokens, a.per_seq = tokens / c.num_seqs;
+    a.kv_heads = c.kv_heads, a.group = q_heads / c.kv_heads, a.head_dim = c.head_dim;
+    // A scale of 0 weighs all keys alike, as does the smallest normal number; it
+    // keeps masked scores at -inf.
+    a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1.17549435e-38f);
+    a.causal = causal, a.window = window;
+    return launch_paged_attention(a, bf16, workspace, as_stream(stream));
 }
 
 size_t csr_transpose_workspace_bytes(int M, int K, int nnz) {

@@ -79,4 +79,43 @@ struct AttnArgs {
     long long ldc;
 };
 
+constexpr int kPagedMaxLength = 1 << 30;  // tokens of a sequence (positions and their differences stay in 32 bits)
+
+// Attention of new tokens over a paged cache, as usm_paged_cache lays it out.
+struct PagedArgs {
+    const void *q, *k, *v;
+    void* out;
+    long long q_token, q_head, out_token, out_head;  // strides, elements
+    long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+    const int* table;
+    const int* lengths;
+    const int* q_offsets;  // may be null: per_seq tokens each
+    int table_stride, num_pages, page_size;
+    int capacity;          // positions that the table has room for
+    int num_seqs, tokens, per_seq;
+    int kv_heads, group, head_dim;
+    float scale_log2;      // scale·log2 e
+    int causal, window;
+    int part_rows;         // rows of a partial result
+    float* parts;          // [2·ctas][part_rows][head_dim], then [2·ctas][part_rows][2]
+    float* part_stats;     // (reference, sum) of each row
+    void* meta;            // PagedMeta[ctas]
+    int* status;
+};
+
+struct AppendArgs {
+    const void *k, *v, *q;  // q: null for none
+    void *k_cache, *v_cache, *q_out;
+    long long k_token, k_head, v_token, v_head, q_token, q_head, q_out_token, q_out_head;
+    long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+    const int* table;
+    const int* lengths;
+    const int* q_offsets;
+    int table_stride, num_pages, page_size, capacity;
+    int num_seqs, tokens, per_seq;
+    int kv_heads, q_heads, head_dim;
+    const float* rope;
+    int rope_positions, rot, interleaved;
+};
+
 }  // namespace usm

@@ -82,6 +82,10 @@ int launch_diff_softmax_grad(const MapArgs& a, float* dlambda, cudaStream_t stre
 int launch_row_softmax_grad(const MapArgs& a, cudaStream_t stream);
 size_t attention_workspace_bytes(const AttnArgs& a, bool bf16);
 int launch_attention(const AttnArgs& a, bool bf16, void* workspace, cudaStream_t stream);
+int launch_rope_table(int positions, int rot, double base, float* table, cudaStream_t stream);
+int launch_paged_append(const AppendArgs& a, bool bf16, cudaStream_t stream);
+size_t paged_attention_workspace(int tokens, int q_heads, int kv_heads, int head_dim, bool bf16);
+int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream);
 int launch_csr_validate(int M, int K, int nnz, const int* row_offsets, const int* col_indices, int* result,
                         cudaStream_t stream);
 

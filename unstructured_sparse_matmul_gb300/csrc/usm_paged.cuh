@@ -1,0 +1,298 @@
+// What the kernels over a paged cache share: sequences and positions, and the
+// division of attention's work among CTAs.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "usm_args.h"
+#include "usm_device.cuh"
+
+namespace usm {
+
+// The new tokens of one sequence.
+struct PagedSeq {
+    int start;  // its first new token in the calls' arrays
+    int n;      // how many
+    int len;    // tokens in its cache, the new ones included (>= 0)
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
+    PagedSeq s;
+    if (a.q_offsets) {
+        s.start = min(max(__ldg(a.q_offsets + b), 0), a.tokens);
+        s.n = min(max(__ldg(a.q_offsets + b + 1), s.start), a.tokens) - s.start;
+    } else {
+        s.start = b * a.per_seq;
+        s.n = a.per_seq;
+    }
+    s.len = min(max(__ldg(a.lengths + b), 0), kPagedMaxLength);
+    return s;
+}
+
+// Rows of attention: new token i of a sequence gives `group` rows for a head of
+// keys, i·group + g, one for each query head that reads it.  A block is kRows of
+// a sequence's rows; an item is a block with one head of keys; a unit is one tile
+// of kKeys keys of an item.
+struct PagedBlock {
+    int lo, hi;  // keys that some row sees lie in [lo, hi)
+    int tile0, tiles;
+};
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ PagedBlock paged_block(const PagedArgs& a, const PagedSeq& s, int block) {
+    const int rows = s.n * a.group;
+    const int first = block * kRows, last = min(rows, first + kRows) - 1;
+    const int p0 = s.len - s.n + first / a.group, p1 = s.len - s.n + last / a.group;
+    const int keys = min(s.len, a.capacity);
+    PagedBlock k;
+    k.hi = a.causal ? min(keys, max(p1 + 1, 0)) : keys;
+    k.lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+    if (k.lo >= k.hi) k.lo = k.hi = 0;
+    k.tile0 = k.lo / kKeys;
+    k.tiles = max((k.hi + kKeys - 1) / kKeys - k.tile0, 1);  // one for a block that sees nothing: it writes zeros
+    return k;
+}
+
+// A CTA's run of tiles of one item.
+struct PagedSegment {
+    int start, n, len;     // the sequence
+    int row0, rows;        // its rows of the block
+    int head;              // head of keys
+    int seq;
+    int lo, hi;            // keys that some row sees
+    int tile0, tiles;      // this segment's tiles
+    int part;              // kPartWhole, or the slot its partial result goes to
+    int ends;              // its last tile is its item's
+    int live;              // 0: no further segment
+    int odd_values;        // set where a partly masked tile holds infinities or NaN in V
+};
+constexpr int kPartWhole = -1, kPartLater = 0, kPartFirst = 1;
+
+// What a CTA tells the joining kernel: an item begun in slot kPartFirst goes on
+// in the next CTAs' slots kPartLater up to the one with `ends`.
+struct PagedMeta {
+    int first_live;         // slot kPartFirst is in use, for this block and head:
+    int start, row0, rows, head;
+    int later_live, ends;   // slot kPartLater is in use, and ends its item
+    int pad;
+};
+
+// The CTAs take equal shares of all units in the order (sequence, block, head,
+// tile).  init() is called by all kThreads threads, next() by one whole warp.
+template <int kRows, int kKeys, int kThreads>
+struct PagedShares {
+    long long left;  // units that remain to this CTA
+    int b, block, blocks, head, tile;
+    PagedSeq s;
+    PagedBlock k;
+
+    __device__ __forceinline__ static int blocks_of(const PagedArgs& a, const PagedSeq& s) {
+        return (int)(((long long)s.n * a.group + kRows - 1) / kRows);
+    }
+    __device__ __forceinline__ static bool many(int blocks) { return blocks > 4; }
+
+    // Units of sequence b (0 past the last), for the calling lane; the whole warp
+    // takes part where a sequence has many blocks.
+    __device__ static long long units_of(const PagedArgs& a, int b) {
+        PagedSeq s{0, 0, 0};
+        if (b < a.num_seqs) s = paged_seq(a, b);
+        const int blocks = blocks_of(a, s);
+        long long t = 0;
+        if (!many(blocks))
+            for (int i = 0; i < blocks; ++i) t += paged_block<kRows, kKeys>(a, s, i).tiles;
+        unsigned rest = __ballot_sync(kFullMask, many(blocks));
+        const int lane = threadIdx.x & 31;
+        while (rest) {
+            const int from = __ffs(rest) - 1;
+            rest &= rest - 1;
+            PagedSeq f;
+            f.start = 0;
+            f.n = __shfl_sync(kFullMask, s.n, from);
+            f.len = __shfl_sync(kFullMask, s.len, from);
+            const int nb = __shfl_sync(kFullMask, blocks, from);
+            long long sum = 0;
+            for (int i = lane; i < nb; i += 32) sum += paged_block<kRows, kKeys>(a, f, i).tiles;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+            if (lane == from) t = sum;
+        }
+        return t * a.kv_heads;
+    }
+
+    __device__ static long long warp_scan(long long x) {  // inclusive
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFullMask, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    }
+
+    // scratch: shared, kThreads / 32 + 2 values.  Afterwards every thread knows
+    // `left`; the first sequence and the units of it that lie before this CTA's
+    // are known to all threads too.
+    __device__ void init(const PagedArgs& a, int cta, int ctas, long long* scratch) {
+        constexpr int kWarps = kThreads / 32;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        long long total = 0, mine = 0, before = 0;
+        // The sum over all sequences; with up to kThreads of them every thread
+        // keeps its own prefix for the search below.
+        for (int at = 0; at < a.num_seqs; at += kThreads) {
+            mine = units_of(a, at + (int)threadIdx.x);
+            const long long scan = warp_scan(mine);
+            if (lane == 31) scratch[warp] = scan;
+            __syncthreads();
+            before = total + scan - mine;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += scratch[w];
+                total += scratch[w];
+            }
+            __syncthreads();
+        }
+        const int active = (int)min((long long)ctas, total);
+        left = 0;
+        b = a.num_seqs;
+        block = blocks = head = tile = 0;
+        if (cta >= active) return;  // the same for the whole CTA
+        const long long u0 = total / active * cta + total % active * cta / active;
+        const long long u1 = total / active * (cta + 1) + total % active * (cta + 1) / active;
+        left = u1 - u0;
+        long long sum = 0;
+        for (int at = 0; at < a.num_seqs; at += kThreads) {
+            if (a.num_seqs > kThreads) {  // the prefixes once more, chunk by chunk
+                mine = units_of(a, at + (int)threadIdx.x);
+                const long long scan = warp_scan(mine);
+                if (lane == 31) scratch[warp] = scan;
+                __syncthreads();
+                before = sum + scan - mine;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) before += scratch[w];
+                    sum += scratch[w];
+                }
+                __syncthreads();
+            }
+            if (u0 >= before && u0 < before + mine) {
+                scratch[kWarps] = at + (int)threadIdx.x;
+                scratch[kWarps + 1] = u0 - before;
+            }
+            if (a.num_seqs <= kThreads || u0 < sum) break;
+        }
+        __syncthreads();
+        b = (int)scratch[kWarps];
+        find(a, scratch[kWarps + 1]);
+    }
+
+    // The block, head and tile `skip` units behind sequence b's first; every warp
+    // searches for itself.
+    __device__ void find(const PagedArgs& a, long long skip) {
+        s = paged_seq(a, b);
+        blocks = blocks_of(a, s);
+        const int lane = threadIdx.x & 31;
+        long long base = 0;
+        for (int at = 0; at < blocks; at += 32) {
+            const long long w =
+                at + lane < blocks ? (long long)paged_block<kRows, kKeys>(a, s, at + lane).tiles * a.kv_heads : 0;
+            const long long scan = base + warp_scan(w);
+            const unsigned here = __ballot_sync(kFullMask, skip < scan);
+            if (here) {
+                const int from = __ffs(here) - 1;
+                block = at + from;
+                skip -= __shfl_sync(kFullMask, scan - w, from);
+                break;
+            }
+            base = __shfl_sync(kFullMask, scan, 31);
+        }
+        k = paged_block<kRows, kKeys>(a, s, block);
+        head = (int)(skip / k.tiles);
+        tile = (int)(skip % k.tiles);
+    }
+
+    // The next segment; whole warp.
+    __device__ PagedSegment next(const PagedArgs& a) {
+        PagedSegment g;
+        g.live = left > 0;
+        g.odd_values = 0;
+        if (!g.live) return g;
+        g.start = s.start;
+        g.n = s.n;
+        g.len = s.len;
+        g.row0 = block * kRows;
+        g.rows = min(kRows, s.n * a.group - g.row0);
+        g.head = head;
+        g.seq = b;
+        g.lo = k.lo;
+        g.hi = k.hi;
+        g.tile0 = k.tile0 + tile;
+        g.tiles = (int)min((long long)(k.tiles - tile), left);
+        g.ends = tile + g.tiles == k.tiles;
+        g.part = tile > 0 ? kPartLater : g.ends ? kPartWhole : kPartFirst;
+        left -= g.tiles;
+        if (left > 0) {
+            tile = 0;
+            if (++head == a.kv_heads) {
+                head = 0;
+                if (++block == blocks) {
+                    block = 0;
+                    const int lane = threadIdx.x & 31;
+                    for (++b; b < a.num_seqs; b += 32) {  // past sequences that bring no token
+                        const int n = b + lane < a.num_seqs ? paged_seq(a, b + lane).n : 0;
+                        const unsigned some = __ballot_sync(kFullMask, n > 0);
+                        if (some) {
+                            b += __ffs(some) - 1;
+                            break;
+                        }
+                    }
+                    if (b >= a.num_seqs) {  // the counts changed under the call
+                        left = 0;
+                        return g;
+                    }
+                    s = paged_seq(a, b);
+                    blocks = blocks_of(a, s);
+                }
+                k = paged_block<kRows, kKeys>(a, s, block);
+            }
+        }
+        return g;
+    }
+};
+
+// Notes a segment with a partial result in the CTA's message to the join.
+__device__ __forceinline__ void paged_note(PagedMeta& m, const PagedSegment& g) {
+    if (g.part == kPartFirst) {
+        m.first_live = 1;
+        m.start = g.start;
+        m.row0 = g.row0;
+        m.rows = g.rows;
+        m.head = g.head;
+    } else if (g.part == kPartLater) {
+        m.later_live = 1;
+        m.ends = g.ends;
+    }
+}
+
+// Keys [lo, hi) that one row of a segment sees; empty for rows past its last.
+__device__ __forceinline__ int2 paged_seen(const PagedArgs& a, const PagedSegment& g, int row) {
+    if (row >= g.rows) return make_int2(0, 0);
+    const int p = g.len - g.n + (g.row0 + row) / a.group;
+    const int keys = min(g.len, a.capacity);
+    const int hi = a.causal ? min(keys, max(p + 1, 0)) : keys;
+    const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Element of the cache where key `key`'s page begins its slot: page and slot.
+__device__ __forceinline__ int2 paged_slot(const PagedArgs& a, int seq, int key) {
+    const int index = key / a.page_size;
+    const int page = __ldg(a.table + (long long)seq * a.table_stride + index);
+    return make_int2(min(max(page, 0), a.num_pages - 1), key - index * a.page_size);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+}  // namespace usm
