@@ -620,6 +620,8 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     // keeps masked scores at -inf.
     a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1.17549435e-38f);
     a.causal = causal, a.window = window;
+    a.status = status_word_for_current_device();
+    if (!a.status) return USM_ERR_CUDA;
     return launch_paged_attention(a, bf16, workspace, as_stream(stream));
 }
 

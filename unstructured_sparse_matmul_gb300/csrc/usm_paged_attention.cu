@@ -291,19 +291,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 // Launch
 // ---------------------------------------------------------------------------
 struct Shape {
+    bool mma;
     int rows;  // of a block
     int ctas;
 };
-template <class T>
-Shape shape_of(int head_dim) {
+Shape shape_of(int head_dim, bool bf16) {
+    if (bf16 && head_dim <= 128) return Shape{true, paged_mma_rows(), sm_count_current_device()};
     const int fit = std::max(1, std::min(4, 220 * 1024 / block_smem(head_dim)));
-    return Shape{kBlockRows, fit * sm_count_current_device()};
+    return Shape{false, kBlockRows, fit * sm_count_current_device()};
 }
 
 int part_rows(int tokens, int q_heads, int kv_heads, int rows) {
     return (int)std::min<long long>(rows, (long long)tokens * (q_heads / kv_heads));
 }
 
+// bf16 heads of up to 128 columns go to the matrix kernel.
 template <class T, int kWide>
 int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_block_kernel<T, kWide>;
@@ -318,19 +320,20 @@ size_t meta_bytes(int ctas) { return ((size_t)ctas * sizeof(PagedMeta) + 15) / 1
 }  // namespace
 
 size_t paged_attention_workspace(int tokens, int q_heads, int kv_heads, int head_dim, bool bf16) {
-    const Shape s = bf16 ? shape_of<__nv_bfloat16>(head_dim) : shape_of<float>(head_dim);
+    const Shape s = shape_of(head_dim, bf16);
     const size_t rows = (size_t)2 * s.ctas * part_rows(tokens, q_heads, kv_heads, s.rows);
     return meta_bytes(s.ctas) + rows * head_dim * 4 + rows * 8;
 }
 
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream) {
-    const Shape s = bf16 ? shape_of<__nv_bfloat16>(a.head_dim) : shape_of<float>(a.head_dim);
+    const Shape s = shape_of(a.head_dim, bf16);
     a.part_rows = (int)std::min<long long>(s.rows, (long long)(a.q_offsets ? a.tokens : a.per_seq) * a.group);
     a.meta = workspace;
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(s.ctas));
     a.part_stats = a.parts + (size_t)2 * s.ctas * a.part_rows * a.head_dim;
     int code;
-    switch ((a.head_dim + 63) / 64) {
+    if (s.mma) code = launch_paged_mma(a, s.ctas, stream);
+    else switch ((a.head_dim + 63) / 64) {
         case 1: code = bf16 ? run_block<__nv_bfloat16, 1>(a, s.ctas, stream) : run_block<float, 1>(a, s.ctas, stream); break;
         case 2: code = bf16 ? run_block<__nv_bfloat16, 2>(a, s.ctas, stream) : run_block<float, 2>(a, s.ctas, stream); break;
         case 3: code = bf16 ? run_block<__nv_bfloat16, 3>(a, s.ctas, stream) : run_block<float, 3>(a, s.ctas, stream); break;
