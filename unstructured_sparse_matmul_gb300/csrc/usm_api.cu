@@ -98,12 +98,32 @@ int sm_count_current_device() {
     return n;
 }
 
-bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
-                          long long cols, long long ld_elems, int box_cols, int box_rows) {
+namespace {
+bool find_encode() {
     std::call_once(g_encode_once, [] {
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_entry("cuTensorMapEncodeTiled", 12000));
     });
-    if (!g_encode) return false;
+    return g_encode != nullptr;
+}
+}  // namespace
+
+bool encode_tensor_map_4d_bf16(CUtensorMap* map, const void* base, const int (&extents)[4], const long long (&strides)[3],
+                               const int (&box)[4]) {
+    if (!find_encode()) return false;
+    cuuint64_t dims[4], bytes[3];
+    cuuint32_t boxes[4];
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)extents[i], boxes[i] = (cuuint32_t)box[i];
+    // A dimension of one is never stepped over, but its stride has to be a valid one.
+    for (int i = 0; i < 3; ++i) bytes[i] = extents[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : (cuuint64_t)extents[0] * 2;
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, bytes, boxes, unit,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
+                          long long cols, long long ld_elems, int box_cols, int box_rows) {
+    if (!find_encode()) return false;
     const int es = bf16 ? 2 : 4;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(ld_elems * es)};

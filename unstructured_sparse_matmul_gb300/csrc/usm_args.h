@@ -96,6 +96,7 @@ struct PagedArgs {
     int kv_heads, group, head_dim;
     float scale_log2;      // scale·log2 e
     int causal, window;
+    int boxes;             // keys and values come by TMA, a box of a page's slots at a time
     int part_rows;         // rows of a partial result
     float* parts;          // [2·ctas][part_rows][head_dim], then [2·ctas][part_rows][2]
     float* part_stats;     // (reference, sum) of each row

@@ -52,6 +52,12 @@ inline bool taller_chunk_pays(int K, int kc, int kc_tall) {
 bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, long long rows,
                           long long cols, long long ld_elems, int box_cols, int box_rows);
 
+// The same for four dimensions of bf16 (the innermost first; strides of the others
+// in elements, any for a dimension of one), rows of 64 columns in the 128-byte
+// swizzle, zeros beyond the extents.
+bool encode_tensor_map_4d_bf16(CUtensorMap* map, const void* base, const int (&extents)[4], const long long (&strides)[3],
+                               const int (&box)[4]);
+
 // softmax: a.values are fp32 scores and each row's values are their softmax
 // probabilities, rounded to B's element type (csr_spmm_row_softmax).
 int launch_spmm(const SpmmArgs& a, const void* B, int ldb, bool bf16, cudaStream_t stream, bool softmax = false);
@@ -88,7 +94,7 @@ size_t paged_attention_workspace(int tokens, int q_heads, int kv_heads, int head
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream);
 // The matrix kernel for bf16 heads of up to 128 columns: rows of its blocks, and its launch.
 int paged_mma_rows();
-int launch_paged_mma(const PagedArgs& a, int ctas, cudaStream_t stream);
+int launch_paged_mma(PagedArgs a, int ctas, cudaStream_t stream);
 int launch_csr_validate(int M, int K, int nnz, const int* row_offsets, const int* col_indices, int* result,
                         cudaStream_t stream);
 

@@ -66,6 +66,7 @@ struct PagedSegment {
     int ends;              // its last tile is its item's
     int live;              // 0: no further segment
     int odd_values;        // set where a partly masked tile holds infinities or NaN in V
+    int hi_least, lo_most; // every row sees the keys in [lo_most, hi_least)
 };
 constexpr int kPartWhole = -1, kPartLater = 0, kPartFirst = 1;
 
@@ -88,7 +89,7 @@ struct PagedShares {
     PagedBlock k;
 
     __device__ __forceinline__ static int blocks_of(const PagedArgs& a, const PagedSeq& s) {
-        return (int)(((long long)s.n * a.group + kRows - 1) / kRows);
+        return (int)(((unsigned)s.n * (unsigned)a.group + kRows - 1) / kRows);  // below 2^31 rows
     }
     __device__ __forceinline__ static bool many(int blocks) { return blocks > 4; }
 
@@ -100,9 +101,11 @@ struct PagedShares {
         const int blocks = blocks_of(a, s);
         long long t = 0;
         if (!many(blocks))
+#pragma unroll 1
             for (int i = 0; i < blocks; ++i) t += paged_block<kRows, kKeys>(a, s, i).tiles;
         unsigned rest = __ballot_sync(kFullMask, many(blocks));
         const int lane = threadIdx.x & 31;
+#pragma unroll 1
         while (rest) {
             const int from = __ffs(rest) - 1;
             rest &= rest - 1;
@@ -112,12 +115,18 @@ struct PagedShares {
             f.len = __shfl_sync(kFullMask, s.len, from);
             const int nb = __shfl_sync(kFullMask, blocks, from);
             long long sum = 0;
+#pragma unroll 1
             for (int i = lane; i < nb; i += 32) sum += paged_block<kRows, kKeys>(a, f, i).tiles;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
             if (lane == from) t = sum;
         }
         return t * a.kv_heads;
+    }
+
+    // 64-bit divisions take hundreds of cycles; few need one.
+    __device__ __forceinline__ static long long divide(long long x, int y) {
+        return x >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
     }
 
     __device__ static long long warp_scan(long long x) {  // inclusive
@@ -130,54 +139,45 @@ struct PagedShares {
         return x;
     }
 
-    // scratch: shared, kThreads / 32 + 2 values.  Afterwards every thread knows
-    // `left`; the first sequence and the units of it that lie before this CTA's
-    // are known to all threads too.
-    __device__ void init(const PagedArgs& a, int cta, int ctas, long long* scratch) {
+    // scratch: shared, kThreads / 32 + 2 values.  Every warp knows the first
+    // segment afterwards.
+    __device__ __forceinline__ void init(const PagedArgs& a, int cta, int ctas, long long* scratch) {
         constexpr int kWarps = kThreads / 32;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        long long total = 0, mine = 0, before = 0;
-        // The sum over all sequences; with up to kThreads of them every thread
-        // keeps its own prefix for the search below.
-        for (int at = 0; at < a.num_seqs; at += kThreads) {
-            mine = units_of(a, at + (int)threadIdx.x);
-            const long long scan = warp_scan(mine);
-            if (lane == 31) scratch[warp] = scan;
-            __syncthreads();
-            before = total + scan - mine;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += scratch[w];
-                total += scratch[w];
-            }
-            __syncthreads();
-        }
-        const int active = (int)min((long long)ctas, total);
+        long long mine = 0, before = 0, u0 = 0;
         left = 0;
         b = a.num_seqs;
         block = blocks = head = tile = 0;
-        if (cta >= active) return;  // the same for the whole CTA
-        const long long u0 = total / active * cta + total % active * cta / active;
-        const long long u1 = total / active * (cta + 1) + total % active * (cta + 1) / active;
-        left = u1 - u0;
-        long long sum = 0;
-        for (int at = 0; at < a.num_seqs; at += kThreads) {
-            if (a.num_seqs > kThreads) {  // the prefixes once more, chunk by chunk
-                mine = units_of(a, at + (int)threadIdx.x);
-                const long long scan = warp_scan(mine);
-                if (lane == 31) scratch[warp] = scan;
-                __syncthreads();
-                before = sum + scan - mine;
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp) before += scratch[w];
-                    sum += scratch[w];
+        // First the sum over all sequences, then the search for this CTA's share;
+        // with up to kThreads sequences every thread still has its own prefix then.
+#pragma unroll 1
+        for (int search = 0; search < 2; ++search) {
+            long long sum = 0;
+#pragma unroll 1
+            for (int at = 0; at < a.num_seqs; at += kThreads) {
+                if (!search || a.num_seqs > kThreads) {
+                    mine = units_of(a, at + (int)threadIdx.x);
+                    const long long scan = warp_scan(mine);
+                    if (lane == 31) scratch[warp] = scan;
+                    __syncthreads();
+                    // A warp's lanes add up the warps' sums, all and those before it.
+                    const long long w = warp_scan(lane < kWarps ? scratch[lane] : 0);
+                    before = sum + scan - mine + (warp ? __shfl_sync(kFullMask, w, warp - 1) : 0);
+                    sum += __shfl_sync(kFullMask, w, 31);
+                    __syncthreads();
                 }
-                __syncthreads();
+                if (search && u0 >= before && u0 < before + mine) {
+                    scratch[kWarps] = at + (int)threadIdx.x;
+                    scratch[kWarps + 1] = u0 - before;
+                }
             }
-            if (u0 >= before && u0 < before + mine) {
-                scratch[kWarps] = at + (int)threadIdx.x;
-                scratch[kWarps + 1] = u0 - before;
-            }
-            if (a.num_seqs <= kThreads || u0 < sum) break;
+            if (search) break;
+            const int active = (int)min((long long)ctas, sum);
+            if (cta >= active) return;  // the same for the whole CTA
+            const long long each = divide(sum, active);
+            const int over = (int)(sum - each * active);  // this many CTAs take one more
+            u0 = each * cta + min(cta, over);
+            left = each + (cta < over ? 1 : 0);
         }
         __syncthreads();
         b = (int)scratch[kWarps];
@@ -191,6 +191,7 @@ struct PagedShares {
         blocks = blocks_of(a, s);
         const int lane = threadIdx.x & 31;
         long long base = 0;
+#pragma unroll 1
         for (int at = 0; at < blocks; at += 32) {
             const long long w =
                 at + lane < blocks ? (long long)paged_block<kRows, kKeys>(a, s, at + lane).tiles * a.kv_heads : 0;
@@ -205,8 +206,8 @@ struct PagedShares {
             base = __shfl_sync(kFullMask, scan, 31);
         }
         k = paged_block<kRows, kKeys>(a, s, block);
-        head = (int)(skip / k.tiles);
-        tile = (int)(skip % k.tiles);
+        head = (int)divide(skip, k.tiles);
+        tile = (int)(skip - (long long)head * k.tiles);
     }
 
     // The next segment; whole warp.
@@ -236,6 +237,7 @@ struct PagedShares {
                 if (++block == blocks) {
                     block = 0;
                     const int lane = threadIdx.x & 31;
+#pragma unroll 1
                     for (++b; b < a.num_seqs; b += 32) {  // past sequences that bring no token
                         const int n = b + lane < a.num_seqs ? paged_seq(a, b + lane).n : 0;
                         const unsigned some = __ballot_sync(kFullMask, n > 0);
@@ -258,6 +260,16 @@ struct PagedShares {
     }
 };
 
+// Keys [lo, hi) that one row of a segment sees; empty for rows past its last.
+__device__ __forceinline__ int2 paged_seen(const PagedArgs& a, const PagedSegment& g, int row) {
+    if (row >= g.rows) return make_int2(0, 0);
+    const int p = g.len - g.n + (g.row0 + row) / a.group;
+    const int keys = min(g.len, a.capacity);
+    const int hi = a.causal ? min(keys, max(p + 1, 0)) : keys;
+    const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
 // Notes a segment with a partial result in the CTA's message to the join.
 __device__ __forceinline__ void paged_note(PagedMeta& m, const PagedSegment& g) {
     if (g.part == kPartFirst) {
@@ -272,17 +284,7 @@ __device__ __forceinline__ void paged_note(PagedMeta& m, const PagedSegment& g) 
     }
 }
 
-// Keys [lo, hi) that one row of a segment sees; empty for rows past its last.
-__device__ __forceinline__ int2 paged_seen(const PagedArgs& a, const PagedSegment& g, int row) {
-    if (row >= g.rows) return make_int2(0, 0);
-    const int p = g.len - g.n + (g.row0 + row) / a.group;
-    const int keys = min(g.len, a.capacity);
-    const int hi = a.causal ? min(keys, max(p + 1, 0)) : keys;
-    const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
-    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
-}
-
-// Element of the cache where key `key`'s page begins its slot: page and slot.
+// Page and slot of a key.
 __device__ __forceinline__ int2 paged_slot(const PagedArgs& a, int seq, int key) {
     const int index = key / a.page_size;
     const int page = __ldg(a.table + (long long)seq * a.table_stride + index);

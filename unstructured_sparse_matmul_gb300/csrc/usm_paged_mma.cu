@@ -51,7 +51,7 @@ struct Sizes {
 };
 
 struct Control {
-    unsigned long long full[10], empty[10];  // stages
+    unsigned long long full[10], empty[10], cleaned[10];  // stages
     unsigned long long q_full, q_empty;
     unsigned long long s_full[2], p_full[2], o_full[2];
     unsigned long long seg_full[kRing], seg_empty[kRing];
@@ -98,18 +98,17 @@ __device__ __forceinline__ uint32_t k_load(uint32_t base, int t) { return base +
 __device__ __forceinline__ uint32_t v_load(uint32_t base, int t, int n) { return base + (t == n - 1 ? 2 * n - 1 : 2 * t + 2); }
 
 // Whether some row of the segment's block does not see all of the tile's keys
-// that lie in [lo, hi).
-struct Edges {
-    int hi_least, lo_most;
-    bool none;
-};
-__device__ __forceinline__ Edges edges_of(const PagedArgs& a, const PagedSegment& g) {
+// that lie in [lo, hi), and whether some keys of the tile lie outside.
+__device__ __forceinline__ void set_edges(const PagedArgs& a, PagedSegment& g) {
     const int2 first = paged_seen(a, g, 0), last = paged_seen(a, g, g.rows - 1);
-    return Edges{first.y, last.x, first.y <= first.x || last.y <= last.x};
+    const bool none = first.y <= first.x || last.y <= last.x;
+    g.hi_least = none ? 0 : first.y;
+    g.lo_most = none ? 0x7fffffff : last.x;
 }
-__device__ __forceinline__ bool partly_seen(const Edges& e, const PagedSegment& g, int key0) {
-    return e.none || min(key0 + kKeys, g.hi) > e.hi_least || max(key0, g.lo) < e.lo_most;
+__device__ __forceinline__ bool partly_seen(const PagedSegment& g, int key0) {
+    return min(key0 + kKeys, g.hi) > g.hi_least || max(key0, g.lo) < g.lo_most;
 }
+__device__ __forceinline__ bool ragged(const PagedSegment& g, int key0) { return key0 < g.lo || key0 + kKeys > g.hi; }
 
 __device__ __forceinline__ bool odd_bf16(uint32_t w) {  // an infinity or NaN in either half
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -121,23 +120,24 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
 }
 
 // ---------------------------------------------------------------------------
-// Copies
+// Copies (four warps).  Pages that divide a tile, or that tiles divide, come by
+// TMA, a box of a page's slots and 64 columns at a time: one warp waits for room
+// and starts the boxes, the others copy the queries and put right what boxes
+// bring beyond the sequence.  Other page sizes (and those under 8) come in 16-byte copies by all four.
+// Those complete on the tile's barrier by themselves too, and the thread that
+// multiplies makes them visible to the tensor cores.
 // ---------------------------------------------------------------------------
 template <int DP>
 struct Copies {
     using Z = Sizes<DP>;
-    static constexpr int kChunks = DP / 8;           // 16-byte chunks of a row
-    static constexpr int kSide = 32 / kChunks;       // rows of a warp's copy
-    static constexpr int kSteps = 128 / (4 * kSide); // copies of a warp for a tile
+    static constexpr int kChunks = DP / 8;      // 16-byte chunks of a row
+    static constexpr int kSide = 32 / kChunks;  // rows of a warp's copy
+    static constexpr int kPanels = DP / 64;
 
     const PagedArgs& a;
     Control* ct;
     uint32_t smem;
     int warp, lane, chunk, side;
-    uint32_t swizzled[2];    // byte offset of the chunk in its panel for rows of either parity of...
-    uint32_t issued = 0, retired = 0, stage_in = 0, stage_out = 0;
-    unsigned is_query = 0, look = 0;  // of the last 32 groups of copies: queries; values to look at
-    unsigned seg_of = 0;              // and two bits each of the ring slot (last 16)
 
     __device__ Copies(const PagedArgs& a, Control* ct, uint32_t smem) : a(a), ct(ct), smem(smem) {
         warp = (threadIdx.x >> 5) & 3;
@@ -145,142 +145,191 @@ struct Copies {
         chunk = lane % kChunks;
         side = lane / kChunks;
     }
-
-    __device__ __forceinline__ int row_of(int step, int side) const { return (step * 4 + warp) * kSide + side; }
-    __device__ __forceinline__ uint32_t place(uint32_t tile, int row) const {
+    __device__ __forceinline__ static uint32_t place(uint32_t tile, int row, int chunk) {
         return tile + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
     }
 
-    __device__ __forceinline__ static void pending(int n) {  // wait until at most n groups are in flight
-        switch (n) {
-            case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-            case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-            case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-            case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-            case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-            case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-            case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-            case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-            case 8: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
-            default: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
+    // Rows row0.. (32 of them) of a tile; row: where the lane's one begins, null for zeros.
+    __device__ __forceinline__ void rows(uint32_t tile, int row0, const char* row) {
+        const bool used = chunk * 8 < (a.head_dim + 15) / 16 * 16;  // a column of the products
+#pragma unroll 4
+        for (int i = side; i < 32; i += kSide) {
+            const unsigned long long from = __shfl_sync(kFullMask, (unsigned long long)row, i);
+            const bool there = from != 0 && chunk * 8 < a.head_dim;
+            if (used)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(tile, row0 + i, chunk)),
+                             "l"(there ? (const char*)from + chunk * 16 : (const char*)a.q), "r"(there ? 16 : 0)
+                             : "memory");
         }
     }
-
-    // The oldest group in flight has landed: tell its reader.
-    __device__ void retire() {
-        pending((int)(issued - retired - 1));
-        const unsigned bit = retired & 31;
-        const bool query = (is_query >> bit) & 1;
-        const uint32_t stage = stage_out % Z::kStages;
-        if ((look >> bit) & 1) look_at(stage, (seg_of >> (2 * (retired & 15))) & 3);
-        fence_proxy_async_smem();
-        arrive_warp(query ? ct->q_full : ct->full[stage]);
-        if (!query) ++stage_out;
-        ++retired;
+    __device__ __forceinline__ void complete_on(const unsigned long long& b) {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&b)) : "memory");
     }
 
-    // Values of a partly masked tile: infinities and NaN would reach rows that do
-    // not see them (0·inf); they are taken out, and added at the end where seen.
-    __device__ void look_at(uint32_t stage, int slot) {
-        if (chunk * 8 >= a.head_dim) return;
-        const uint32_t tile = smem + Z::kStage0 + stage * Z::kTile;
-        for (int step = 0; step < kSteps; ++step) {
-            const uint32_t at = place(tile, row_of(step, side));
-            uint4 w = lds128(at);
-            if (odd_bf16(w.x) || odd_bf16(w.y) || odd_bf16(w.z) || odd_bf16(w.w)) {
-                w = make_uint4(without_odd(w.x), without_odd(w.y), without_odd(w.z), without_odd(w.w));
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-                *(volatile int*)&ct->seg[slot].odd_values = 1;
+    // The segment's queries, by warps first, first + step, ...; rows past the last
+    // group of 32 are left as they are (a row's results depend on nothing else).
+    __device__ void queries(const PagedSegment& g, int first, int step) {
+#pragma unroll 1
+        for (int row0 = 32 * first; row0 < g.rows; row0 += 32 * step) {
+            const int r = row0 + lane;
+            const char* row = nullptr;
+            if (r < g.rows) {
+                const int flat = g.row0 + r, token = flat / a.group;
+                row = (const char*)a.q + 2 * ((g.start + token) * a.q_token + (g.head * a.group + flat - token * a.group) * a.q_head);
             }
+            rows(smem + (row0 >> 7) * Z::kTile, row0 & 127, row);
+        }
+        complete_on(ct->q_full);
+    }
+
+    // Values that must not reach the products: rows outside [lo, hi), which may hold
+    // anything (a weight of 0 does not silence NaN), and, in tiles that not every row
+    // sees, infinities and NaN, which are added at the end where they are seen.
+    // Chunks from, from + step, ... of the tile.
+    __device__ __noinline__ static void clean(uint32_t tile, int lo, int hi, bool partly, int chunks, int from, int end, int step, int* found) {
+#pragma unroll 1
+        for (int i = from; i < end; i += step) {
+            const int row = i / kChunks, chunk = i % kChunks;
+            if (chunk >= chunks) continue;
+            const uint32_t at = place(tile, row, chunk);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row >= lo && row < hi) {
+                if (!partly) continue;
+                w = lds128(at);
+                if (!(odd_bf16(w.x) || odd_bf16(w.y) || odd_bf16(w.z) || odd_bf16(w.w))) continue;
+                w = make_uint4(without_odd(w.x), without_odd(w.y), without_odd(w.z), without_odd(w.w));
+                *(volatile int*)found = 1;
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
         }
     }
-
-    // Waits for a barrier; until it is free, passes on what has landed.
-    __device__ bool acquire(const unsigned long long& b, uint32_t parity) {
-        const uint32_t bar = smem_addr(&b);
-        while (issued != retired) {
-            if (__all_sync(kFullMask, mbar_test_wait(bar, parity))) return true;
-            retire();
-        }
-        return wait(b, parity, ct, a.status);
+    __device__ __forceinline__ void clean(const PagedSegment& g, uint32_t stage, int key0, int from, int end, int step) {
+        clean(smem + Z::kStage0 + stage * Z::kTile, g.lo - key0, g.hi - key0, partly_seen(g, key0), (a.head_dim + 7) / 8, from, end, step,
+              const_cast<int*>(&g.odd_values));
+        fence_proxy_async_smem();
     }
 
-    __device__ __forceinline__ void commit(bool query, bool look_at_it, int slot) {
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const unsigned bit = 1u << (issued & 31);
-        is_query = query ? is_query | bit : is_query & ~bit;
-        look = look_at_it ? look | bit : look & ~bit;
-        const int s = 2 * (issued & 15);
-        seg_of = (seg_of & ~(3u << s)) | ((unsigned)slot << s);
-        ++issued;
+    // Load i of a segment's 2n: K0 K1 V0 K2 V1 ... V(n-1).
+    __device__ __forceinline__ static int tile_of(int i, int n, bool& values) {
+        values = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
+        return i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
     }
 
-    // 128 rows to `tile`; offset: this lane's row's place (elements; lane = step ·
-    // kSide + side), negative for a row of zeros.
-    __device__ __forceinline__ void rows(uint32_t tile, const void* base, long long offset) {
-        const int D = a.head_dim;
-        if (chunk * 8 >= (D + 15) / 16 * 16) chunk = kChunks;  // no column of the products
-#pragma unroll
-        for (int step = 0; step < kSteps; ++step) {
-            const long long from = __shfl_sync(kFullMask, offset, step * kSide + side);
-            if (chunk >= kChunks) continue;
-            const bool real = from >= 0 && chunk * 8 < D;
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(base) + (real ? from + chunk * 8 : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(tile, row_of(step, side))), "l"(src),
-                         "r"(real ? 16 : 0)
-                         : "memory");
-        }
-    }
-
-    __device__ __forceinline__ long long query_row(const PagedSegment& g, int half) const {
-        const int r = 128 * half + row_of(lane / kSide, lane % kSide);
-        if (r >= g.rows) return -1;
-        const int flat = g.row0 + r, token = flat / a.group;
-        return (long long)(g.start + token) * a.q_token + (long long)(g.head * a.group + flat - token * a.group) * a.q_head;
-    }
-
-    __device__ __forceinline__ bool tile(const PagedSegment& g, int key0, bool values, bool look_at_it, int slot) {
-        const int key = key0 + row_of(lane / kSide, lane % kSide);
-        long long offset = -1;
-        if (key >= g.lo && key < g.hi) {
-            const int2 w = paged_slot(a, g.seq, key);
-            offset = values ? w.x * a.v_page + w.y * a.v_slot + g.head * a.v_head
-                            : w.x * a.k_page + w.y * a.k_slot + g.head * a.k_head;
-        }
-        const uint32_t stage = stage_in % Z::kStages;
-        if (!acquire(ct->empty[stage], (stage_in / Z::kStages & 1) ^ 1)) return false;
-        rows(smem + Z::kStage0 + stage * Z::kTile, values ? a.v : a.k, offset);
-        commit(false, look_at_it, slot);
-        ++stage_in;
-        return true;
-    }
-
-    __device__ void run() {
+    // One warp: boxes of keys and values.  Lane = page of the tile · panels + panel.
+    __device__ void boxes(const CUtensorMap* k_map, const CUtensorMap* v_map) {
+        const int slots = min(a.page_size, kKeys);  // of a box
+        const int page = lane / kPanels, panel = lane % kPanels;
+        const uint32_t to = panel * 16384 + page * slots * 128;
+        uint32_t stage = 0, parity = 1;
+        started = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!acquire(ct->seg_full[slot], it / kRing & 1)) return;
-            const PagedSegment g = ct->seg[slot];
+            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
-            if (it > 0 && !acquire(ct->q_empty, (it - 1) & 1)) return;
-            rows(smem, a.q, query_row(g, 0));
-            if (g.rows > 128) rows(smem + Z::kTile, a.q, query_row(g, 1));
-            commit(true, false, slot);
-            const Edges e = edges_of(a, g);
-            const int n = g.tiles, key0 = g.tile0 * kKeys;
-            for (int i = 0; i < 2 * n; ++i) {  // K0 K1 V0 K2 V1 ...
-                const bool values = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
-                const int t = i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
-                const int at = key0 + t * kKeys;
-                if (!tile(g, at, values, values && partly_seen(e, g, at), slot)) return;
+            const int n = g.tiles, key0 = g.tile0 * kKeys, lo = g.lo, hi = g.hi, seq = g.seq, head = g.head;
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i) {
+                bool values;
+                const int key = key0 + tile_of(i, n, values) * kKeys + page * slots;
+                const bool mine = page * slots < kKeys && key < hi && key + slots > lo;
+                int2 at = make_int2(0, 0);
+                if (mine) at = paged_slot(a, seq, key);
+                if (!wait(ct->empty[stage], parity, ct, a.status)) return;
+                const uint32_t bar = smem_addr(&ct->full[stage]);
+                const unsigned boxes = __ballot_sync(kFullMask, mine);
+                if (lane == 0) mbar_arrive_expect_tx(bar, __popc(boxes) * slots * 128);
+                __syncwarp();
+                ++started;
+                if (mine)
+                    tma_load_4d(smem + Z::kStage0 + stage * Z::kTile + to, values ? v_map : k_map, panel * 64, at.y, head, at.x, bar);
+                __syncwarp();
+                if (++stage == Z::kStages) {
+                    stage = 0;
+                    parity ^= 1;
+                }
             }
-            while (issued != retired) retire();
+            arrive_warp(ct->seg_empty[slot]);
+        }
+    }
+
+    uint32_t started;  // loads
+    // Every box has landed before the CTA ends, however it ends.
+    __device__ void landed() {
+        for (uint32_t i = started > Z::kStages ? started - Z::kStages : 0; i < started; ++i)
+            mbar_wait_bounded(smem_addr(&ct->full[i % Z::kStages]), i / Z::kStages & 1, kWaitLimitNs);
+    }
+
+    // The other three warps beside it.
+    __device__ void helpers() {
+        uint32_t load = 0;
+        for (uint32_t it = 0;; ++it) {
+            const int slot = it % kRing;
+            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            const PagedSegment& g = ct->seg[slot];
+            if (!g.live) break;
+            if (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return;
+            queries(g, warp - 1, 3);
+            const int n = g.tiles;
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                const int key0 = (g.tile0 + t) * kKeys;
+                if (!partly_seen(g, key0) && !ragged(g, key0)) continue;
+                const uint32_t i = v_load(load, t, n), stage = i % Z::kStages;
+                if (!wait(ct->full[stage], i / Z::kStages & 1, ct, a.status)) return;
+                clean(g, stage, key0, (int)(threadIdx.x & 127) - 32, 128 * kChunks, 96);
+                arrive_warp(ct->cleaned[stage]);
+            }
+            load += 2 * n;
+            arrive_warp(ct->seg_empty[slot]);
+        }
+    }
+
+    // All four warps: 16-byte copies.
+    __device__ void chunks() {
+        uint32_t stage = 0, parity = 1;
+        for (uint32_t it = 0;; ++it) {
+            const int slot = it % kRing;
+            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            const PagedSegment& g = ct->seg[slot];
+            if (!g.live) break;
+            const int n = g.tiles, key0 = g.tile0 * kKeys;
+            if (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return;
+            queries(g, warp, 4);
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i) {
+                bool values;
+                const int at = key0 + tile_of(i, n, values) * kKeys, key = at + 32 * warp + lane;
+                const char* row = nullptr;
+                if (key >= g.lo && key < g.hi) {
+                    const int2 w = paged_slot(a, g.seq, key);
+                    row = values ? (const char*)a.v + 2 * (w.x * a.v_page + w.y * a.v_slot + g.head * a.v_head)
+                                 : (const char*)a.k + 2 * (w.x * a.k_page + w.y * a.k_slot + g.head * a.k_head);
+                }
+                if (!wait(ct->empty[stage], parity, ct, a.status)) return;
+                rows(smem + Z::kStage0 + stage * Z::kTile, 32 * warp, row);
+                if (values && partly_seen(g, at)) {
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    __syncwarp();  // this warp's rows alone
+                    clean(g, stage, at, 32 * warp * kChunks + lane, 32 * (warp + 1) * kChunks, 32);
+                    mbar_arrive(smem_addr(&ct->full[stage]));
+                } else {
+                    complete_on(ct->full[stage]);
+                }
+                if (++stage == Z::kStages) {
+                    stage = 0;
+                    parity ^= 1;
+                }
+            }
             arrive_warp(ct->seg_empty[slot]);
         }
     }
 };
 
 // ---------------------------------------------------------------------------
-// Matrix products (one warp; its lane 0 issues)
+// Matrix products: one elected thread (the compiler then issues the products from
+// uniform registers as they stand; behind a test of the lane it goes through the
+// warp's threads for each of them)
 // ---------------------------------------------------------------------------
 template <int DP>
 struct Products {
@@ -290,43 +339,53 @@ struct Products {
     uint32_t smem, tmem;
     uint32_t qk_shape, pv_shape;
     int steps;
-    bool lead;
     uint32_t p_uses[2] = {0, 0};
+    uint32_t cleanings = 0;  // parity of each stage's
 
     __device__ Products(const PagedArgs& a, Control* ct, uint32_t smem, uint32_t tmem) : a(a), ct(ct), smem(smem), tmem(tmem) {
         steps = (a.head_dim + 15) / 16;
         qk_shape = bf16_mma_shape(kKeys, false);
         pv_shape = bf16_mma_shape(steps * 16, true);
-        lead = (threadIdx.x & 31) == 0;
     }
-    __device__ __forceinline__ void commit(const unsigned long long& b) {
-        if (lead) tmem_commit(smem_addr(&b));
+    __device__ __forceinline__ bool await(const unsigned long long& b, uint32_t parity) {
+        const uint32_t bar = smem_addr(&b);
+        return mbar_try_wait(bar, parity) || wait_slow(bar, parity, ct, a.status);
     }
+    __device__ __forceinline__ void commit(const unsigned long long& b) { tmem_commit(smem_addr(&b)); }
     __device__ __forceinline__ bool loaded(uint32_t load) {
-        return wait(ct->full[load % Z::kStages], load / Z::kStages & 1, ct, a.status);
+        if (!await(ct->full[load % Z::kStages], load / Z::kStages & 1)) return false;
+        if (!a.boxes) fence_proxy_async_smem();  // the copies were ordinary writes
+        return true;
+    }
+    __device__ __forceinline__ bool values_loaded(const PagedSegment& g, int t, uint32_t load) {
+        if (!loaded(load)) return false;
+        const int key0 = (g.tile0 + t) * kKeys, stage = load % Z::kStages;
+        if (a.boxes && (partly_seen(g, key0) || ragged(g, key0))) {
+            if (!await(ct->cleaned[stage], cleanings >> stage & 1)) return false;
+            cleanings ^= 1u << stage;
+        }
+        return true;
     }
     __device__ __forceinline__ uint32_t stage(uint32_t load) const { return smem + Z::kStage0 + load % Z::kStages * Z::kTile; }
     __device__ __forceinline__ void release(uint32_t load) { commit(ct->empty[load % Z::kStages]); }
 
     __device__ __forceinline__ void scores(int half, int q_half, uint32_t load) {
-        if (lead) {
-            const uint64_t q = swizzled_desc(smem + q_half * Z::kTile, 0), k = swizzled_desc(stage(load), 0);
-            for (int i = 0; i < steps; ++i) {
-                const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-                mma_bf16_ss(tmem + half * kKeys, q + at, k + at, qk_shape, i > 0);
-            }
+        const uint64_t q = swizzled_desc(smem + q_half * Z::kTile, 0), k = swizzled_desc(stage(load), 0);
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+            if (i >= steps) break;
+            const uint32_t at = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + half * kKeys, q + at, k + at, qk_shape, i > 0);
         }
         commit(ct->s_full[half]);
     }
     __device__ __forceinline__ bool weigh(int half, uint32_t load, bool accumulate) {
-        if (!wait(ct->p_full[half], p_uses[half]++ & 1, ct, a.status)) return false;
+        if (!await(ct->p_full[half], p_uses[half]++ & 1)) return false;
         tmem_fence_after_sync();
-        if (lead) {
-            const uint64_t v = swizzled_desc(stage(load), 16384);
+        const uint64_t v = swizzled_desc(stage(load), 16384);
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-                mma_bf16_ts(tmem + 256 + half * DP, tmem + half * kKeys + i * 8, v + (i * 2048 >> 4), pv_shape, accumulate || i > 0);
-        }
+        for (int i = 0; i < kKeys / 16; ++i)
+            mma_bf16_ts(tmem + 256 + half * DP, tmem + half * kKeys + i * 8, v + (i * 2048 >> 4), pv_shape, accumulate || i > 0);
         return true;
     }
 
@@ -334,11 +393,14 @@ struct Products {
         uint32_t base = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
-            if (!ct->seg[slot].live) break;
-            const int n = ct->seg[slot].tiles;
-            const bool shared = ct->seg[slot].rows <= 128;
-            if (!wait(ct->q_full, it & 1, ct, a.status) || !loaded(k_load(base, 0))) return;
+            if (!await(ct->seg_full[slot], it / kRing & 1)) return;
+            const PagedSegment& g = ct->seg[slot];
+            if (!g.live) break;
+            const int n = g.tiles;
+            const bool shared = g.rows <= 128;
+            if (!await(ct->q_full, it & 1)) return;
+            fence_proxy_async_smem();
+            if (!loaded(k_load(base, 0))) return;
             scores(0, 0, k_load(base, 0));
             if (!shared) scores(1, 1, k_load(base, 0));
             release(k_load(base, 0));
@@ -352,7 +414,7 @@ struct Products {
             for (int t = 0; t < n; ++t) {
                 const uint32_t v = v_load(base, t, n), k = k_load(base, t + ahead);
                 const bool more = t + ahead < n;
-                if (!loaded(v) || (more && !loaded(k))) return;
+                if (!values_loaded(g, t, v) || (more && !loaded(k))) return;
                 if (shared) {
                     const int half = t & 1;
                     if (!weigh(half, v, t >= 2)) return;
@@ -360,7 +422,7 @@ struct Products {
                     if (more) scores(half, 0, k);
                     else commit(ct->o_full[half]);
                 } else {
-#pragma unroll 1
+#pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         if (!weigh(half, v, t > 0)) return;
                         if (more) scores(half, half, k);
@@ -372,7 +434,7 @@ struct Products {
                 if (more && t + ahead == n - 1) commit(ct->q_empty);
             }
             base += 2 * n;
-            arrive_warp(ct->seg_empty[slot]);
+            mbar_arrive(smem_addr(&ct->seg_empty[slot]));
         }
     }
 };
@@ -380,7 +442,7 @@ struct Products {
 // ---------------------------------------------------------------------------
 // Softmax and output: one row a thread
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void store16(void* p, const uint32_t* w) {  // 32 bytes, 16-byte aligned
+__device__ __forceinline__ void store16(void* p, const uint32_t* w) {  // 16 bytes
     asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
@@ -438,44 +500,31 @@ struct Softmax {
             l *= f;
             if (!first) rescale(f);
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        const bool far = !(fabsf(mc) <= kNear);
-        uint64_t sum[2] = {0, 0};
-        if (!__any_sync(kFullMask, far)) {
-            const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t(&s)[32] = w[2 * h + (j >> 4)];
-                    const int i = 2 * (j & 15);
-                    float x, y;
-                    unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, mc2), x, y);
-                    x = exp2_fast(x);
-                    y = exp2_fast(y);
-                    sum[j & 1] = add2(sum[j & 1], pack2(x, y));
-                    p[j] = bf16x2(x, y);
-                }
-                tmem_st32(s_col + 32 * h, p);
-            }
-        } else {
+        float mc = m == -INFINITY ? 0.f : m * c;
+        if (__any_sync(kFullMask, !(fabsf(mc) <= kNear))) {
             // Far from zero the difference is formed first: it is exact near m.
             const float base = m == -INFINITY ? 0.f : m;
+            mc = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t(&s)[32] = w[2 * h + (j >> 4)];
-                    const int i = 2 * (j & 15);
-                    const float x = exp2_fast((__uint_as_float(s[i]) - base) * c);
-                    const float y = exp2_fast((__uint_as_float(s[i + 1]) - base) * c);
-                    sum[j & 1] = add2(sum[j & 1], pack2(x, y));
-                    p[j] = bf16x2(x, y);
-                }
-                tmem_st32(s_col + 32 * h, p);
+                for (int j = 0; j < 32; ++j) w[i][j] = __float_as_uint(__uint_as_float(w[i][j]) - base);
+        }
+        uint64_t sum[2] = {0, 0};
+        const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(w[h][2 * j]), __uint_as_float(w[h][2 * j + 1])), c2, mc2), x, y);
+                x = exp2_fast(x);
+                y = exp2_fast(y);
+                sum[j & 1] = add2(sum[j & 1], pack2(x, y));
+                p[j] = bf16x2(x, y);
             }
+            tmem_st16(s_col + 16 * h, p);
         }
         float x0, x1, y0, y1;
         unpack2(sum[0], x0, x1);
@@ -484,121 +533,133 @@ struct Softmax {
         tmem_wait_st();
     }
 
-    __device__ void rescale(float f) {
+    __device__ __forceinline__ void rescale(float f) {
         const int columns = (a.head_dim + 15) / 16 * 16;
-#pragma unroll
-        for (int j = 0; j < DP / 32; ++j) {
-            if (32 * j >= columns) break;
-            uint32_t w[32];
-            tmem_ld32(o_col + 32 * j, w);
+#pragma unroll 1
+        for (int j = 0; j < columns; j += 16) {
+            uint32_t w[16];
+            tmem_ld16(o_col + j, w);
             tmem_wait_ld(w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-            tmem_st32(o_col + 32 * j, w);
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+            tmem_st16(o_col + j, w);
         }
         tmem_wait_st();
     }
 
-    // Adds what was taken out of partly masked tiles (infinities and NaN of rows
-    // of V that this row sees) to columns 32·j.. of its sums.
-    __device__ void add_odd(const PagedSegment& g, bool shared, int j, uint32_t (&w)[32]) {
-        const Edges e = edges_of(a, g);
-        for (int t = shared ? half : 0; t < g.tiles; t += shared ? 2 : 1) {
-            const int key0 = (g.tile0 + t) * kKeys;
-            if (!partly_seen(e, g, key0)) continue;
-            for (int key = max(key0, seen.x); key < min(key0 + kKeys, seen.y); ++key) {
-                const int2 at = paged_slot(a, g.seq, key);
-                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + at.x * a.v_page + at.y * a.v_slot + g.head * a.v_head;
+    // Adds what was taken out of partly masked tiles: infinities and NaN of rows
+    // of V that this row sees.  Whole warp; the half's tiles are first, first + step, ...
+    __device__ __noinline__ static void add_odd(const PagedArgs& a, const PagedSegment& g, uint32_t o_col, int2 seen, int first,
+                                                int step) {
+#pragma unroll 1
+        for (int j = 0; j < a.head_dim; j += 16) {
+            uint32_t w[16];
+            tmem_ld16(o_col + j, w);
+            tmem_wait_ld(w);
+#pragma unroll 1
+            for (int t = first; t < g.tiles; t += step) {
+                const int key0 = (g.tile0 + t) * kKeys;
+                if (!partly_seen(g, key0)) continue;
+#pragma unroll 1
+                for (int key = max(key0, seen.x); key < min(key0 + kKeys, seen.y); ++key) {
+                    const int2 at = paged_slot(a, g.seq, key);
+                    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + at.x * a.v_page + at.y * a.v_slot + g.head * a.v_head + j;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (32 * j + i >= a.head_dim) break;
-                    const float x = __bfloat162float(v[32 * j + i]);
-                    if (!isfinite(x)) w[i] = __float_as_uint(__uint_as_float(w[i]) + x);
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = j + i < a.head_dim ? __bfloat162float(v[i]) : 0.f;
+                        if (!isfinite(x)) w[i] = __float_as_uint(__uint_as_float(w[i]) + x);
+                    }
                 }
             }
+            __syncwarp();
+            tmem_st16(o_col + j, w);
         }
+        tmem_wait_st();
     }
 
-    // Columns 32·j.. of a row of results: to the output, or to the partial results.
-    __device__ __forceinline__ void store(const PagedSegment& g, int row, int j, const uint32_t (&w)[32], float z) {
-        const int left = a.head_dim - 32 * j;  // a multiple of 8
-        if (g.part == kPartWhole) {
-            const int flat = g.row0 + row, token = flat / a.group;
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + (long long)(g.start + token) * a.out_token +
-                                (long long)(g.head * a.group + flat - token * a.group) * a.out_head + 32 * j;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (8 * i >= left) break;
-                uint32_t p[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    p[u] = bf16x2(__uint_as_float(w[8 * i + 2 * u]) * z, __uint_as_float(w[8 * i + 2 * u + 1]) * z);
-                store16(to + 8 * i, p);
-            }
-        } else {
-            float* to = a.parts + ((2LL * blockIdx.x + g.part) * a.part_rows + row) * a.head_dim + 32 * j;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (4 * i >= left) break;
-                store16(to + 4 * i, w + 4 * i);
-            }
-        }
-    }
-
-    // Sums of the two halves over the same rows, 32 columns at a time through the
-    // queries' second tile (free here: the block has one).
-    __device__ bool join_halves(const PagedSegment& g, int row) {
-        const bool mine = __any_sync(kFullMask, row < g.rows);  // a warp with rows
-        const bool odd = *(volatile int*)&ct->seg[slot].odd_values;
+    // A row's sums, 32 columns at a time: those of the two halves joined where they
+    // took the same rows (through the queries' second tile, which is free then),
+    // divided, and written to the output or to the partial results.
+    __device__ __forceinline__ bool write(const PagedSegment& g, int row, bool both) {
+        const bool mine = row < g.rows, whole = g.part == kPartWhole;
+        const bool some = __any_sync(kFullMask, mine);
         const uint32_t box = smem + Z::kTile + 4 * tid;  // [32 columns][128 rows]
-        float z = 0.f, f0 = 1.f, f1 = 1.f;
-        for (int j = 0; j < DP / 32; ++j) {
-            if (32 * j >= a.head_dim) break;
+        const int flat = g.row0 + row, token = flat / a.group;
+        const long long part = (2LL * blockIdx.x + g.part) * a.part_rows + row;
+        char* to = whole ? static_cast<char*>(a.out) + 2 * ((g.start + token) * a.out_token + (g.head * a.group + flat - token * a.group) * a.out_head)
+                         : reinterpret_cast<char*>(a.parts + part * a.head_dim);
+        float f0 = 1.f, f1 = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < a.head_dim; j += 32) {
             uint32_t w[32];
-            if (mine) {
-                tmem_ld32(o_col + 32 * j, w);
+            if (some) {
+                tmem_ld32(o_col + j, w);
                 tmem_wait_ld(w);
-                if (odd && row < g.rows) add_odd(g, true, j, w);
             }
-            const uint32_t use = box_uses++;
-            if (half == 1) {
-                if (use > 0 && !wait(ct->box_free, (use - 1) & 1, ct, a.status)) return false;
-                if (j == 0) ct->stats[tid] = make_float2(m, l);
-                if (mine)
+            if (both) {
+                const uint32_t use = box_uses++;
+                if (half == 1) {
+                    if (use > 0 && !wait(ct->box_free, (use - 1) & 1, ct, a.status)) return false;
+                    if (j == 0) ct->stats[tid] = make_float2(m, l);
+                    if (some)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(box + 512 * i), "r"(w[i]) : "memory");
-                arrive_warp(ct->box_full);
-                continue;
+                        for (int i = 0; i < 32; ++i)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(box + 512 * i), "r"(w[i]) : "memory");
+                    arrive_warp(ct->box_full);
+                    continue;
+                }
+                if (!wait(ct->box_full, use & 1, ct, a.status)) return false;
             }
-            if (!wait(ct->box_full, use & 1, ct, a.status)) return false;
-            if (mine) {
-                if (j == 0) {
+            if (j == 0) {
+                if (both) {
                     const float2 other = ct->stats[tid];
                     const float t = fmaxf(m, other.x);
                     f0 = m == -INFINITY ? 0.f : exp2_fast((m - t) * a.scale_log2);
                     f1 = other.x == -INFINITY ? 0.f : exp2_fast((other.x - t) * a.scale_log2);
                     m = t;
                     l = l * f0 + other.y * f1;
-                    z = l == 0.f ? 0.f : 1.f / l;
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    w[i] = __float_as_uint(__uint_as_float(w[i]) * f0 + __uint_as_float(lds32(box + 512 * i)) * f1);
+                const float z = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                f0 *= z;
+                f1 *= z;
             }
-            arrive_warp(ct->box_free);
-            if (row < g.rows) store(g, row, j, w, z);
+            if (some) {
+                if (both)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        w[i] = __float_as_uint(__uint_as_float(w[i]) * f0 + __uint_as_float(lds32(box + 512 * i)) * f1);
+                else
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f0);
+            }
+            if (both) arrive_warp(ct->box_free);
+            if (!mine) continue;
+            const int left = a.head_dim - j;  // a multiple of 8
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        p[u] = bf16x2(__uint_as_float(w[8 * i + 2 * u]), __uint_as_float(w[8 * i + 2 * u + 1]));
+                    if (8 * i < left) store16(to + 2 * j + 16 * i, p);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (4 * i < left) store16(to + 4 * j + 16 * i, w + 4 * i);
+            }
         }
+        if (!whole && mine && (!both || half == 0))
+            *reinterpret_cast<float2*>(a.part_stats + 2 * part) = make_float2(m, l);
         return true;
     }
 
-    int slot;
-
     __device__ void run() {
         for (uint32_t it = 0;; ++it) {
-            slot = it % kRing;
+            const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
-            const PagedSegment g = ct->seg[slot];
+            const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const bool shared = g.rows <= 128;
             const int row = shared ? tid : half * 128 + tid;
@@ -612,38 +673,22 @@ struct Softmax {
             if (!shared) arrive_warp(ct->q_empty);
             m = -INFINITY;
             l = 0.f;
-            const int first = shared ? half : 0, step = shared ? 2 : 1;
-            for (int t = first; t < g.tiles; t += step) {
+            const int first = shared ? half : 0, step = shared ? 2 : 1, tiles = g.tiles, tile0 = g.tile0;
+#pragma unroll 1
+            for (int t = first; t < tiles; t += step) {
                 if (!wait(ct->s_full[half], s_uses++ & 1, ct, a.status)) return;
                 tmem_fence_after_sync();
-                const int key0 = (g.tile0 + t) * kKeys;
+                const int key0 = (tile0 + t) * kKeys;
                 if (some) weights(key0, key0 < lo || key0 + kKeys > hi, t == first);
                 tmem_fence_before_sync();
                 arrive_warp(ct->p_full[half]);
             }
-            const bool both = shared && g.tiles > 1;
-            if (first < g.tiles) {
+            if (first < tiles) {  // not so for the second half of a single tile
                 if (!wait(ct->o_full[half], o_uses++ & 1, ct, a.status)) return;
                 tmem_fence_after_sync();
+                if (some && *(volatile int*)&ct->seg[slot].odd_values) add_odd(a, g, o_col, seen, first, step);
+                if (!write(g, row, shared && tiles > 1)) return;
             }
-            if (both) {
-                if (!join_halves(g, row)) return;
-            } else if (some && first < g.tiles) {
-                const float z = l == 0.f ? 0.f : 1.f / l;
-                const bool odd = *(volatile int*)&ct->seg[slot].odd_values;
-                for (int j = 0; j < DP / 32; ++j) {
-                    if (32 * j >= a.head_dim) break;
-                    uint32_t w[32];
-                    tmem_ld32(o_col + 32 * j, w);
-                    tmem_wait_ld(w);
-                    if (row < g.rows) {
-                        if (odd) add_odd(g, shared, j, w);
-                        store(g, row, j, w, z);
-                    }
-                }
-            }
-            if (g.part != kPartWhole && row < g.rows && (!shared || half == 0))
-                *reinterpret_cast<float2*>(a.part_stats + 2 * ((2LL * blockIdx.x + g.part) * a.part_rows + row)) = make_float2(m, l);
             tmem_fence_before_sync();
             if (shared) arrive_warp(ct->q_empty);
             arrive_warp(ct->seg_empty[slot]);
@@ -651,8 +696,12 @@ struct Softmax {
     }
 };
 
+struct Maps {
+    CUtensorMap k, v;  // columns, slots, heads, pages
+};
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Maps maps) {
     using Z = Sizes<DP>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Control* ct = reinterpret_cast<Control*>(smem + Z::kControl);
@@ -660,10 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
     let_next_start();
     if (threadIdx.x == 0) {
         for (int i = 0; i < Z::kStages; ++i) {
-            mbar_init(smem_addr(&ct->full[i]), 4);
+            mbar_init(smem_addr(&ct->full[i]), a.boxes ? 1 : 128);
             mbar_init(smem_addr(&ct->empty[i]), 1);
+            mbar_init(smem_addr(&ct->cleaned[i]), 3);
         }
-        mbar_init(smem_addr(&ct->q_full), 4);
+        mbar_init(smem_addr(&ct->q_full), a.boxes ? 96 : 128);
         mbar_init(smem_addr(&ct->q_empty), 1 + 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ct->s_full[i]), 1);
@@ -688,29 +738,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
     tmem_fence_after_sync();
     const uint32_t tmem = *(volatile uint32_t*)&ct->tmem, base = smem_addr(smem);
 
-    // 192 + 192 + 72 + 56 registers: the 4 x 128 that the launch has.
+    // 200 + 200 + 56 + 56 registers: the 4 x 128 that the launch has.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         Softmax<DP>(a, ct, base, tmem).run();
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         Copies<DP> copies(a, ct, base);
-        copies.run();
+        if (!a.boxes) {
+            copies.chunks();
+        } else if (warp == 8) {
+            copies.boxes(&maps.k, &maps.v);
+            copies.landed();
+        } else {
+            copies.helpers();
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 12) {
-            Products<DP>(a, ct, base, tmem).run();
-            // Whatever was issued is done before tensor memory is given back.
-            if (lane == 0) tmem_commit(smem_addr(&ct->drained));
+            if (elect_one()) {
+                Products<DP>(a, ct, base, tmem).run();
+                // Whatever was issued is done before tensor memory is given back.
+                tmem_commit(smem_addr(&ct->drained));
+            }
             __syncwarp();
             mbar_wait_bounded(smem_addr(&ct->drained), 0, kWaitLimitNs);
         } else if (warp == 13) {
             PagedMeta meta = {};
             for (uint32_t it = 0;; ++it) {
                 const int slot = it % kRing;
-                const PagedSegment g = shares.next(a);
-                if (g.live) paged_note(meta, g);
+                PagedSegment g = shares.next(a);
+                if (g.live) {
+                    paged_note(meta, g);
+                    set_edges(a, g);
+                }
                 if (it >= kRing && !wait(ct->seg_empty[slot], (it / kRing - 1) & 1, ct, a.status)) break;
                 if (lane == 0) ct->seg[slot] = g;
                 arrive_warp(ct->seg_full[slot]);
@@ -724,19 +786,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
 }
 
 template <int DP>
-int run(const PagedArgs& a, int ctas, cudaStream_t stream) {
+int run(const PagedArgs& a, const Maps& maps, int ctas, cudaStream_t stream) {
     const auto kernel = paged_mma_kernel<DP>;
     constexpr int smem = Sizes<DP>::kControl + (int)sizeof(Control);
     if (!allow_shared(kernel, smem)) return cuda_failure();
-    kernel<<<ctas, kThreads, smem, stream>>>(a);
+    kernel<<<ctas, kThreads, smem, stream>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+}
+
+bool encode(CUtensorMap* map, const PagedArgs& a, const void* base, long long page, long long slot, long long head) {
+    const int dims[4] = {a.head_dim, a.page_size, a.kv_heads, a.num_pages};
+    const long long strides[3] = {slot, head, page};
+    const int box[4] = {64, std::min(a.page_size, kKeys), 1, 1};
+    return encode_tensor_map_4d_bf16(map, base, dims, strides, box);
 }
 
 }  // namespace
 
 int paged_mma_rows() { return kRows; }
-int launch_paged_mma(const PagedArgs& a, int ctas, cudaStream_t stream) {
-    return a.head_dim <= 64 ? run<64>(a, ctas, stream) : run<128>(a, ctas, stream);
+int launch_paged_mma(PagedArgs a, int ctas, cudaStream_t stream) {
+    Maps maps = {};
+    // Boxes of a page's slots: from 8 slots on (a tile is then 32 boxes at most),
+    // where pages and tiles fit one another.
+    a.boxes = a.page_size >= 8 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0) &&
+              encode(&maps.k, a, a.k, a.k_page, a.k_slot, a.k_head) && encode(&maps.v, a, a.v, a.v_page, a.v_slot, a.v_head);
+    return a.head_dim <= 64 ? run<64>(a, maps, ctas, stream) : run<128>(a, maps, ctas, stream);
 }
 
 }  // namespace usm
