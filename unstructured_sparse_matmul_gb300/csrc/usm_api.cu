@@ -633,7 +633,8 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     a.k = c.k, a.k_page = c.k_page_stride, a.k_slot = c.k_slot_stride, a.k_head = c.k_head_stride;
     a.v = c.v, a.v_page = c.v_page_stride, a.v_slot = c.v_slot_stride, a.v_head = c.v_head_stride;
     a.table = c.page_table, a.lengths = c.lengths, a.q_offsets = c.q_offsets;
-    a.table_stride = c.table_stride, a.num_pages = c.num_pages, a.page_size = c.page_size, a.capacity = capacity_of(c);
+    a.table_stride = c.table_stride, a.table_pages = c.table_pages;
+    a.num_pages = c.num_pages, a.page_size = c.page_size, a.capacity = capacity_of(c);
     a.num_seqs = c.num_seqs, a.tokens = tokens, a.per_seq = tokens / c.num_seqs;
     a.kv_heads = c.kv_heads, a.group = q_heads / c.kv_heads, a.head_dim = c.head_dim;
     // A scale of 0 weighs all keys alike, as does the smallest normal number; it

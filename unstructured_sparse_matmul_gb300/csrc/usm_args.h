@@ -96,6 +96,8 @@ struct PagedArgs {
     int kv_heads, group, head_dim;
     float scale_log2;      // scale·log2 e
     int causal, window;
+    int table_pages;       // entries of a sequence's row of the table
+    int out32;             // rows of the output are 32-byte aligned and that much at least
     int boxes;             // keys and values come by TMA, a box of a page's slots at a time
     int part_rows;         // rows of a partial result
     float* parts;          // [2·ctas][part_rows][head_dim], then [2·ctas][part_rows][2]

@@ -80,11 +80,12 @@ struct PagedMeta {
 };
 
 // The CTAs take equal shares of all units in the order (sequence, block, head,
-// tile).  init() is called by all kThreads threads, next() by one whole warp.
-template <int kRows, int kKeys, int kThreads>
+// tile); an item counts kCost units more than it has tiles, before its first.
+// init() is called by all kThreads threads, next() by one whole warp.
+template <int kRows, int kKeys, int kThreads, int kCost>
 struct PagedShares {
     long long left;  // units that remain to this CTA
-    int b, block, blocks, head, tile;
+    int b, block, blocks, head, unit;  // the next one, of its item
     PagedSeq s;
     PagedBlock k;
 
@@ -102,7 +103,7 @@ struct PagedShares {
         long long t = 0;
         if (!many(blocks))
 #pragma unroll 1
-            for (int i = 0; i < blocks; ++i) t += paged_block<kRows, kKeys>(a, s, i).tiles;
+            for (int i = 0; i < blocks; ++i) t += paged_block<kRows, kKeys>(a, s, i).tiles + kCost;
         unsigned rest = __ballot_sync(kFullMask, many(blocks));
         const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -116,7 +117,7 @@ struct PagedShares {
             const int nb = __shfl_sync(kFullMask, blocks, from);
             long long sum = 0;
 #pragma unroll 1
-            for (int i = lane; i < nb; i += 32) sum += paged_block<kRows, kKeys>(a, f, i).tiles;
+            for (int i = lane; i < nb; i += 32) sum += paged_block<kRows, kKeys>(a, f, i).tiles + kCost;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
             if (lane == from) t = sum;
@@ -147,7 +148,7 @@ struct PagedShares {
         long long mine = 0, before = 0, u0 = 0;
         left = 0;
         b = a.num_seqs;
-        block = blocks = head = tile = 0;
+        block = blocks = head = unit = 0;
         // First the sum over all sequences, then the search for this CTA's share;
         // with up to kThreads sequences every thread still has its own prefix then.
 #pragma unroll 1
@@ -192,9 +193,9 @@ struct PagedShares {
         const int lane = threadIdx.x & 31;
         long long base = 0;
 #pragma unroll 1
-        for (int at = 0; at < blocks; at += 32) {
+        for (int at = 0; at < blocks && blocks > 1; at += 32) {
             const long long w =
-                at + lane < blocks ? (long long)paged_block<kRows, kKeys>(a, s, at + lane).tiles * a.kv_heads : 0;
+                at + lane < blocks ? (long long)(paged_block<kRows, kKeys>(a, s, at + lane).tiles + kCost) * a.kv_heads : 0;
             const long long scan = base + warp_scan(w);
             const unsigned here = __ballot_sync(kFullMask, skip < scan);
             if (here) {
@@ -206,33 +207,37 @@ struct PagedShares {
             base = __shfl_sync(kFullMask, scan, 31);
         }
         k = paged_block<kRows, kKeys>(a, s, block);
-        head = (int)divide(skip, k.tiles);
-        tile = (int)(skip - (long long)head * k.tiles);
+        head = (int)divide(skip, k.tiles + kCost);
+        unit = (int)(skip - (long long)head * (k.tiles + kCost));
     }
 
     // The next segment; whole warp.
     __device__ PagedSegment next(const PagedArgs& a) {
         PagedSegment g;
-        g.live = left > 0;
+        g.live = 0;
         g.odd_values = 0;
-        if (!g.live) return g;
-        g.start = s.start;
-        g.n = s.n;
-        g.len = s.len;
-        g.row0 = block * kRows;
-        g.rows = min(kRows, s.n * a.group - g.row0);
-        g.head = head;
-        g.seq = b;
-        g.lo = k.lo;
-        g.hi = k.hi;
-        g.tile0 = k.tile0 + tile;
-        g.tiles = (int)min((long long)(k.tiles - tile), left);
-        g.ends = tile + g.tiles == k.tiles;
-        g.part = tile > 0 ? kPartLater : g.ends ? kPartWhole : kPartFirst;
-        left -= g.tiles;
-        if (left > 0) {
-            tile = 0;
-            if (++head == a.kv_heads) {
+        while (left > 0) {
+            const int take = (int)min((long long)(k.tiles + kCost - unit), left);
+            const int begin = max(unit - kCost, 0), end = unit + take - kCost;
+            if (end > begin) {  // else a share that ends before the item's first tile
+                g.live = 1;
+                g.start = s.start;
+                g.n = s.n;
+                g.len = s.len;
+                g.row0 = block * kRows;
+                g.rows = min(kRows, s.n * a.group - g.row0);
+                g.head = head;
+                g.seq = b;
+                g.lo = k.lo;
+                g.hi = k.hi;
+                g.tile0 = k.tile0 + begin;
+                g.tiles = end - begin;
+                g.ends = end == k.tiles;
+                g.part = begin > 0 ? kPartLater : g.ends ? kPartWhole : kPartFirst;
+            }
+            left -= take;
+            unit = 0;
+            if (left > 0 && ++head == a.kv_heads) {
                 head = 0;
                 if (++block == blocks) {
                     block = 0;
@@ -255,6 +260,7 @@ struct PagedShares {
                 }
                 k = paged_block<kRows, kKeys>(a, s, block);
             }
+            if (g.live) break;
         }
         return g;
     }

@@ -17,7 +17,7 @@ namespace {
 // scores and 4 rows x up to 16 columns of the sums.
 // ---------------------------------------------------------------------------
 constexpr int kBlockRows = 64, kBlockKeys = 64, kBlockThreads = 256;
-using BlockShares = PagedShares<kBlockRows, kBlockKeys, kBlockThreads>;
+using BlockShares = PagedShares<kBlockRows, kBlockKeys, kBlockThreads, 2>;
 
 template <class T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -340,6 +340,9 @@ int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t
         default: code = bf16 ? run_block<__nv_bfloat16, 4>(a, s.ctas, stream) : run_block<float, 4>(a, s.ctas, stream); break;
     }
     if (code != USM_OK) return code;
+    // The join asks for the same split of an SM's memory as the kernel before it: to
+    // change it the SM has to drain.
+    if (!allow_shared(paged_join_kernel<__nv_bfloat16>, 0) || !allow_shared(paged_join_kernel<float>, 0)) return cuda_failure();
     const dim3 grid(s.ctas, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
     if (bf16) return launch_next(paged_join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, 1, stream, a, s.ctas);
     return launch_next(paged_join_kernel<float>, grid, kJoinWarps * 32, 1, stream, a, s.ctas);

@@ -20,7 +20,7 @@
 // Roles: warps 0-3 and 4-7 softmax and output of the halves, 8-11 copies of
 // queries, keys and values (16 bytes a copy, through the page table, rows outside
 // the sequence filled with zeros), 12 issues the matrix products, 13 hands out
-// the segments.
+// the segments, 14 and 15 help with the copies.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -33,14 +33,17 @@ namespace usm {
 namespace {
 
 constexpr int kRows = 256, kKeys = 128, kThreads = 512;
+// What an item costs a CTA beyond its tiles (its queries, the first products and the
+// output), in tiles: 8000 to 14000 cycles where a tile takes 2000 to 2800.
+constexpr int kSegmentCost = 4;
 constexpr int kRing = 4;       // segments handed out ahead
-constexpr int kConsumers = 13; // warps that read a segment
+constexpr int kConsumers = 13; // warps that read a segment (and two more where they copy queries)
 constexpr float kRaise = 8.f;  // log2 of the largest weight before a row's reference is raised
 // Largest |m·c| for which S·c - m·c is formed by one FMA: the rounding of m·c,
 // a common factor of the row's weights, stays below 2^(4096·2^-24).
 constexpr float kNear = 4096.f;
 
-using Shares = PagedShares<kRows, kKeys, kThreads>;
+using Shares = PagedShares<kRows, kKeys, kThreads, kSegmentCost>;
 
 template <int DP>  // columns of shared memory: 64 or 128
 struct Sizes {
@@ -51,7 +54,7 @@ struct Sizes {
 };
 
 struct Control {
-    unsigned long long full[10], empty[10], cleaned[10];  // stages
+    unsigned long long full[10], empty[10], started[10], cleaned[10];  // stages
     unsigned long long q_full, q_empty;
     unsigned long long s_full[2], p_full[2], o_full[2];
     unsigned long long seg_full[kRing], seg_empty[kRing];
@@ -98,7 +101,7 @@ __device__ __forceinline__ uint32_t k_load(uint32_t base, int t) { return base +
 __device__ __forceinline__ uint32_t v_load(uint32_t base, int t, int n) { return base + (t == n - 1 ? 2 * n - 1 : 2 * t + 2); }
 
 // Whether some row of the segment's block does not see all of the tile's keys
-// that lie in [lo, hi), and whether some keys of the tile lie outside.
+// that lie in [lo, hi).
 __device__ __forceinline__ void set_edges(const PagedArgs& a, PagedSegment& g) {
     const int2 first = paged_seen(a, g, 0), last = paged_seen(a, g, g.rows - 1);
     const bool none = first.y <= first.x || last.y <= last.x;
@@ -108,7 +111,10 @@ __device__ __forceinline__ void set_edges(const PagedArgs& a, PagedSegment& g) {
 __device__ __forceinline__ bool partly_seen(const PagedSegment& g, int key0) {
     return min(key0 + kKeys, g.hi) > g.hi_least || max(key0, g.lo) < g.lo_most;
 }
-__device__ __forceinline__ bool ragged(const PagedSegment& g, int key0) { return key0 < g.lo || key0 + kKeys > g.hi; }
+// Whether a tile's values need cleaning: that, or keys of it lie outside [lo, hi).
+__device__ __forceinline__ bool needs_cleaning(const PagedSegment& g, int key0) {
+    return partly_seen(g, key0) || key0 < g.lo || key0 + kKeys > g.hi;
+}
 
 __device__ __forceinline__ bool odd_bf16(uint32_t w) {  // an infinity or NaN in either half
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -121,9 +127,9 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
 
 // ---------------------------------------------------------------------------
 // Copies (four warps).  Pages that divide a tile, or that tiles divide, come by
-// TMA, a box of a page's slots and 64 columns at a time: one warp waits for room
-// and starts the boxes, the others copy the queries and put right what boxes
-// bring beyond the sequence.  Other page sizes (and those under 8) come in 16-byte copies by all four.
+// TMA, a box of a page's slots and 64 columns at a time: a warp for keys and one
+// for values wait for room and start the boxes, two put right what boxes bring
+// beyond the sequence, and two (14, 15) copy the queries.  Other page sizes (and those under 8) come in 16-byte copies by all four.
 // Those complete on the tile's barrier by themselves too, and the thread that
 // multiplies makes them visible to the tensor cores.
 // ---------------------------------------------------------------------------
@@ -185,22 +191,32 @@ struct Copies {
     // Values that must not reach the products: rows outside [lo, hi), which may hold
     // anything (a weight of 0 does not silence NaN), and, in tiles that not every row
     // sees, infinities and NaN, which are added at the end where they are seen.
-    // Chunks from, from + step, ... of the tile.
+    // Chunks from, from + step, ... of the tile, four at a time.
     __device__ __noinline__ static void clean(uint32_t tile, int lo, int hi, bool partly, int chunks, int from, int end, int step, int* found) {
 #pragma unroll 1
-        for (int i = from; i < end; i += step) {
-            const int row = i / kChunks, chunk = i % kChunks;
-            if (chunk >= chunks) continue;
-            const uint32_t at = place(tile, row, chunk);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row >= lo && row < hi) {
-                if (!partly) continue;
-                w = lds128(at);
-                if (!(odd_bf16(w.x) || odd_bf16(w.y) || odd_bf16(w.z) || odd_bf16(w.w))) continue;
-                w = make_uint4(without_odd(w.x), without_odd(w.y), without_odd(w.z), without_odd(w.w));
-                *(volatile int*)found = 1;
+        for (int i = from; i < end; i += 4 * step) {
+            uint4 w[4];
+            uint32_t at[4];
+            bool in[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int row = (i + u * step) / kChunks, chunk = (i + u * step) % kChunks;
+                in[u] = row >= lo && row < hi;
+                at[u] = i + u * step < end && chunk < chunks && (partly || !in[u]) ? place(tile, row, chunk) : 0;
+                w[u] = make_uint4(0, 0, 0, 0);
+                if (at[u] && in[u]) w[u] = lds128(at[u]);
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!at[u]) continue;
+                if (in[u]) {
+                    if (!(odd_bf16(w[u].x) || odd_bf16(w[u].y) || odd_bf16(w[u].z) || odd_bf16(w[u].w))) continue;
+                    w[u] = make_uint4(without_odd(w[u].x), without_odd(w[u].y), without_odd(w[u].z), without_odd(w[u].w));
+                    *(volatile int*)found = 1;
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at[u]), "r"(w[u].x), "r"(w[u].y), "r"(w[u].z), "r"(w[u].w)
+                             : "memory");
+            }
         }
     }
     __device__ __forceinline__ void clean(const PagedSegment& g, uint32_t stage, int key0, int from, int end, int step) {
@@ -215,74 +231,120 @@ struct Copies {
         return i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
     }
 
-    // One warp: boxes of keys and values.  Lane = page of the tile · panels + panel.
-    __device__ void boxes(const CUtensorMap* k_map, const CUtensorMap* v_map) {
-        const int slots = min(a.page_size, kKeys);  // of a box
-        const int page = lane / kPanels, panel = lane % kPanels;
-        const uint32_t to = panel * 16384 + page * slots * 128;
-        uint32_t stage = 0, parity = 1;
-        started = 0;
+    // One warp for keys, one for values: boxes, all issued by one thread (threads of
+    // a warp side by side take 100 cycles for each).  The pages of 32 entries of the
+    // table are kept a lane each, and the next 32 behind them: a look-up takes
+    // longer than a tile.
+    // False where a wait gave up.
+    __device__ bool boxes(const CUtensorMap* map, bool values) {
+        const int slots = min(a.page_size, kKeys), per_tile = kKeys / slots;  // of a box; pages of a tile
+        const int tiles_of_page = a.page_size / slots;
+        const bool lead = elect_one();
+        uint32_t base = 0;
+        for (uint32_t it = 0;; ++it) {
+            const int slot = it % kRing;
+            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return false;
+            const PagedSegment& g = ct->seg[slot];
+            if (!g.live) break;
+            const int n = g.tiles, tile0 = g.tile0, lo = g.lo, hi = g.hi, head = g.head;
+            const int* table = a.table + (long long)g.seq * a.table_stride;
+            int group = -1, now = 0, next = 0;
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                const int tile = tile0 + t, first = tile * kKeys;
+                const int entry = tiles_of_page == 1 ? tile * per_tile : tile / tiles_of_page;
+                if (entry >> 5 != group) {
+                    const int i = (entry & ~31) + lane;
+                    now = entry >> 5 == group + 1 && group >= 0 ? next : i < a.table_pages ? __ldg(table + i) : 0;
+                    next = i + 32 < a.table_pages ? __ldg(table + i + 32) : 0;
+                    group = entry >> 5;
+                    now = min(max(now, 0), a.num_pages - 1);
+                }
+                // Pages of the tile with keys in [lo, hi): begin..end-1.
+                const int begin = first < lo ? (lo - first) / slots : 0;
+                const int end = first + kKeys > hi ? (hi - first + slots - 1) / slots : per_tile;
+                const int in_page = tiles_of_page == 1 ? 0 : first - entry * a.page_size;
+                const uint32_t load = values ? v_load(base, t, n) : k_load(base, t);
+                const uint32_t stage = load % Z::kStages;
+                if (!wait(ct->empty[stage], (load / Z::kStages & 1) ^ 1, ct, a.status)) return false;
+                const uint32_t bar = smem_addr(&ct->full[stage]), to = smem + Z::kStage0 + stage * Z::kTile;
+                if (lead) mbar_arrive_expect_tx(bar, max(end - begin, 0) * kPanels * slots * 128);
+                loaded |= 1u << stage;
+                phases = (phases & ~(1u << stage)) | ((load / Z::kStages & 1) << stage);
+                for (int j = begin; j < end; j += 8) {
+                    int page[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) page[u] = __shfl_sync(kFullMask, now, (entry + j + u) & 31);
+                    if (lead)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (j + u < end)
+#pragma unroll
+                                for (int panel = 0; panel < kPanels; ++panel)
+                                    tma_load_4d(to + panel * 16384 + (j + u) * slots * 128, map, panel * 64, in_page, head, page[u], bar);
+                }
+                if (lead && values && needs_cleaning(g, first)) mbar_arrive(smem_addr(&ct->started[stage]));
+                __syncwarp();
+            }
+            base += 2 * n;
+            arrive_warp(ct->seg_empty[slot]);
+        }
+        return true;
+    }
+    uint32_t loaded = 0, phases = 0;  // a bit a stage: by this warp, and in which phase last
+    // After a wait that gave up: the boxes have landed before the CTA ends, or had
+    // long enough to.
+    __device__ void landed() {
+        for (int i = 0; i < Z::kStages; ++i)
+            if (loaded >> i & 1) mbar_wait_bounded(smem_addr(&ct->full[i]), phases >> i & 1, kWaitLimitNs);
+    }
+
+    // Two further warps: the queries.
+    __device__ void all_queries() {
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
-            if (!g.live) break;
-            const int n = g.tiles, key0 = g.tile0 * kKeys, lo = g.lo, hi = g.hi, seq = g.seq, head = g.head;
-#pragma unroll 1
-            for (int i = 0; i < 2 * n; ++i) {
-                bool values;
-                const int key = key0 + tile_of(i, n, values) * kKeys + page * slots;
-                const bool mine = page * slots < kKeys && key < hi && key + slots > lo;
-                int2 at = make_int2(0, 0);
-                if (mine) at = paged_slot(a, seq, key);
-                if (!wait(ct->empty[stage], parity, ct, a.status)) return;
-                const uint32_t bar = smem_addr(&ct->full[stage]);
-                const unsigned boxes = __ballot_sync(kFullMask, mine);
-                if (lane == 0) mbar_arrive_expect_tx(bar, __popc(boxes) * slots * 128);
-                __syncwarp();
-                ++started;
-                if (mine)
-                    tma_load_4d(smem + Z::kStage0 + stage * Z::kTile + to, values ? v_map : k_map, panel * 64, at.y, head, at.x, bar);
-                __syncwarp();
-                if (++stage == Z::kStages) {
-                    stage = 0;
-                    parity ^= 1;
-                }
-            }
+            if (!g.live || (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status))) return;
+            queries(g, warp & 1, 2);
             arrive_warp(ct->seg_empty[slot]);
         }
     }
 
-    uint32_t started;  // loads
-    // Every box has landed before the CTA ends, however it ends.
-    __device__ void landed() {
-        for (uint32_t i = started > Z::kStages ? started - Z::kStages : 0; i < started; ++i)
-            mbar_wait_bounded(smem_addr(&ct->full[i % Z::kStages]), i / Z::kStages & 1, kWaitLimitNs);
-    }
-
-    // The other three warps beside it.
-    __device__ void helpers() {
-        uint32_t load = 0;
+    // And two: the cleaning.
+    __device__ void all_cleaning() {
+        uint32_t load = 0, startings = 0;  // startings: parity of each stage's
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
-            if (!g.live) break;
-            if (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return;
-            queries(g, warp - 1, 3);
+            if (!g.live) return;
             const int n = g.tiles;
 #pragma unroll 1
             for (int t = 0; t < n; ++t) {
                 const int key0 = (g.tile0 + t) * kKeys;
-                if (!partly_seen(g, key0) && !ragged(g, key0)) continue;
+                if (!needs_cleaning(g, key0)) continue;
                 const uint32_t i = v_load(load, t, n), stage = i % Z::kStages;
+                // Its phase of `full` can be told from others only once it has begun.
+                if (!wait(ct->started[stage], startings >> stage & 1, ct, a.status)) return;
+                startings ^= 1u << stage;
                 if (!wait(ct->full[stage], i / Z::kStages & 1, ct, a.status)) return;
-                clean(g, stage, key0, (int)(threadIdx.x & 127) - 32, 128 * kChunks, 96);
+                clean(g, stage, key0, (int)(threadIdx.x & 63), 128 * kChunks, 64);
                 arrive_warp(ct->cleaned[stage]);
             }
             load += 2 * n;
             arrive_warp(ct->seg_empty[slot]);
         }
+    }
+
+    // Where this lane's row of load i begins; null outside [lo, hi).
+    __device__ __forceinline__ const char* key_row(const PagedSegment& g, int i) const {
+        bool values;
+        const int key = (g.tile0 + tile_of(i, g.tiles, values)) * kKeys + 32 * warp + lane;
+        if (key < g.lo || key >= g.hi) return nullptr;
+        const int2 w = paged_slot(a, g.seq, key);
+        return values ? (const char*)a.v + 2 * (w.x * a.v_page + w.y * a.v_slot + g.head * a.v_head)
+                      : (const char*)a.k + 2 * (w.x * a.k_page + w.y * a.k_slot + g.head * a.k_head);
     }
 
     // All four warps: 16-byte copies.
@@ -296,16 +358,13 @@ struct Copies {
             const int n = g.tiles, key0 = g.tile0 * kKeys;
             if (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return;
             queries(g, warp, 4);
+            const char* next = key_row(g, 0);
 #pragma unroll 1
             for (int i = 0; i < 2 * n; ++i) {
                 bool values;
-                const int at = key0 + tile_of(i, n, values) * kKeys, key = at + 32 * warp + lane;
-                const char* row = nullptr;
-                if (key >= g.lo && key < g.hi) {
-                    const int2 w = paged_slot(a, g.seq, key);
-                    row = values ? (const char*)a.v + 2 * (w.x * a.v_page + w.y * a.v_slot + g.head * a.v_head)
-                                 : (const char*)a.k + 2 * (w.x * a.k_page + w.y * a.k_slot + g.head * a.k_head);
-                }
+                const int at = key0 + tile_of(i, n, values) * kKeys;
+                const char* row = next;
+                next = i + 1 < 2 * n ? key_row(g, i + 1) : nullptr;  // its look-up runs behind this tile's copies
                 if (!wait(ct->empty[stage], parity, ct, a.status)) return;
                 rows(smem + Z::kStage0 + stage * Z::kTile, 32 * warp, row);
                 if (values && partly_seen(g, at)) {
@@ -360,7 +419,7 @@ struct Products {
     __device__ __forceinline__ bool values_loaded(const PagedSegment& g, int t, uint32_t load) {
         if (!loaded(load)) return false;
         const int key0 = (g.tile0 + t) * kKeys, stage = load % Z::kStages;
-        if (a.boxes && (partly_seen(g, key0) || ragged(g, key0))) {
+        if (a.boxes && needs_cleaning(g, key0)) {
             if (!await(ct->cleaned[stage], cleanings >> stage & 1)) return false;
             cleanings ^= 1u << stage;
         }
@@ -444,6 +503,12 @@ struct Products {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void store16(void* p, const uint32_t* w) {  // 16 bytes
     asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {  // 32 bytes, aligned to them
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 template <int DP>
@@ -635,7 +700,16 @@ struct Softmax {
             if (both) arrive_warp(ct->box_free);
             if (!mine) continue;
             const int left = a.head_dim - j;  // a multiple of 8
-            if (whole) {
+            if (whole && a.out32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        p[u] = bf16x2(__uint_as_float(w[16 * i + 2 * u]), __uint_as_float(w[16 * i + 2 * u + 1]));
+                    if (16 * i < left) store32(to + 2 * j + 32 * i, p);
+                }
+            } else if (whole) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t p[4];
@@ -711,9 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
         for (int i = 0; i < Z::kStages; ++i) {
             mbar_init(smem_addr(&ct->full[i]), a.boxes ? 1 : 128);
             mbar_init(smem_addr(&ct->empty[i]), 1);
-            mbar_init(smem_addr(&ct->cleaned[i]), 3);
+            mbar_init(smem_addr(&ct->started[i]), 1);
+            mbar_init(smem_addr(&ct->cleaned[i]), 2);
         }
-        mbar_init(smem_addr(&ct->q_full), a.boxes ? 96 : 128);
+        mbar_init(smem_addr(&ct->q_full), a.boxes ? 64 : 128);
         mbar_init(smem_addr(&ct->q_empty), 1 + 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ct->s_full[i]), 1);
@@ -722,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), kConsumers);
+            mbar_init(smem_addr(&ct->seg_empty[i]), kConsumers + (a.boxes ? 2 : 0));
         }
         mbar_init(smem_addr(&ct->box_full), 4);
         mbar_init(smem_addr(&ct->box_free), 4);
@@ -747,11 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
         Copies<DP> copies(a, ct, base);
         if (!a.boxes) {
             copies.chunks();
-        } else if (warp == 8) {
-            copies.boxes(&maps.k, &maps.v);
-            copies.landed();
+        } else if (warp < 10) {
+            if (!copies.boxes(warp == 8 ? &maps.k : &maps.v, warp == 9)) copies.landed();
         } else {
-            copies.helpers();
+            copies.all_cleaning();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -779,6 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
                 if (!g.live) break;
             }
             if (lane == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = meta;
+        } else if (a.boxes) {
+            Copies<DP>(a, ct, base).all_queries();
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     }
     __syncthreads();
@@ -810,6 +887,7 @@ int launch_paged_mma(PagedArgs a, int ctas, cudaStream_t stream) {
     // where pages and tiles fit one another.
     a.boxes = a.page_size >= 8 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0) &&
               encode(&maps.k, a, a.k, a.k_page, a.k_slot, a.k_head) && encode(&maps.v, a, a.v, a.v_page, a.v_slot, a.v_head);
+    a.out32 = a.head_dim % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.out) | (2 * a.out_token) | (2 * a.out_head)) & 31) == 0;
     return a.head_dim <= 64 ? run<64>(a, maps, ctas, stream) : run<128>(a, maps, ctas, stream);
 }
 
