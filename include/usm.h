@@ -534,7 +534,8 @@ int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, 
  * Limits: head_dim ≤ 256; tokens·q_heads < 2^31; lengths < 2^30.
  * Deterministic (no atomics).  tokens = 0 or num_seqs = 0 is a no-op.
  */
-size_t paged_attention_workspace_bytes(int tokens, int q_heads, int kv_heads, int head_dim, usm_dtype dtype);
+size_t paged_attention_workspace_bytes(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim,
+                                       usm_dtype dtype);
 
 int paged_attention(const usm_paged_cache *cache, int tokens, const usm_tokens *q, int q_heads, float scale,
                     int causal, int window, const usm_tokens *out, void *workspace, size_t workspace_bytes,

@@ -95,7 +95,7 @@ def test_attention_refuses(lib):
         assert attention(lib, **kw) == INVALID, kw
     assert attention(lib, n=1 << 30, heads=2) == UNSUPPORTED
     assert attention(lib, ws=None) == WORKSPACE
-    need = lib.paged_attention_workspace_bytes(6, 4, 2, 8, 1)
+    need = lib.paged_attention_workspace_bytes(6, 2, 4, 2, 8, 1)
     assert need > 0 and attention(lib, wsb=need - 1) == WORKSPACE
     assert attention(lib, ws=ODD8) == ALIGN
 
@@ -110,11 +110,11 @@ def test_empty_calls_touch_nothing(lib):
 
 def test_workspace_bytes(lib):
     f = lib.paged_attention_workspace_bytes
-    for bad in ((0, 4, 2, 8, 1), (4, 0, 2, 8, 1), (4, 4, 0, 8, 1), (4, 3, 2, 8, 1), (4, 4, 2, 0, 1), (4, 4, 2, 257, 1),
-                (4, 4, 2, 8, 2), (1 << 30, 2, 1, 8, 1)):
+    for bad in ((0, 4, 4, 2, 8, 1), (4, 0, 4, 2, 8, 1), (4, 4, 0, 2, 8, 1), (4, 4, 4, 0, 8, 1), (4, 4, 3, 2, 8, 1),
+                (4, 4, 4, 2, 0, 1), (4, 4, 4, 2, 257, 1), (4, 4, 4, 2, 8, 2), (1 << 30, 4, 2, 1, 8, 1)):
         assert f(*bad) == 0, bad
-    assert 0 < f(1, 4, 4, 64, 1) < f(64, 4, 4, 64, 1) <= f(4096, 32, 4, 64, 1)
-    assert 0 < f(1, 4, 4, 64, 0) < f(64, 4, 4, 64, 0)
+    assert 0 < f(1, 1, 4, 4, 64, 1) < f(64, 1, 4, 4, 64, 1) <= f(4096, 1, 32, 4, 64, 1)
+    assert 0 < f(1, 1, 4, 4, 64, 0) < f(64, 1, 4, 4, 64, 0)
 
 
 def test_rope_table_refuses(lib):

@@ -70,7 +70,7 @@ SIGNATURES.update({
 SIGNATURES.update({
     "rope_table_build": (_i, [_i, _i, ctypes.c_double, _vp, _vp]),
     "paged_append": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp]),
-    "paged_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "paged_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "paged_attention": (_i, [_vp, _i, _vp, _i, ctypes.c_float, _i, _i, _vp, _vp, _sz, _vp]),
 })
 
@@ -842,7 +842,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, q_offsets=None, sc
     q, qt = _tokens(q, "q", index, dt, shape)
     _, ot = _tokens(out, "out", index, dt, shape, copy=False)
     code = _code(q, T)
-    need = lib.paged_attention_workspace_bytes(n, q_heads, heads, D, code)
+    need = lib.paged_attention_workspace_bytes(n, page_table.shape[0], q_heads, heads, D, code)
     ws = _workspace(workspace, need, q, T)
     _run("paged_attention", lib.paged_attention, index, T, cache, n, qt, q_heads, scale, int(bool(causal)), window, ot,
          _ptr(ws), need)

@@ -603,11 +603,11 @@ int paged_append(const usm_paged_cache* cache, int tokens, const usm_tokens* k, 
     return launch_paged_append(a, c.dtype == USM_BF16, as_stream(stream));
 }
 
-size_t paged_attention_workspace_bytes(int tokens, int q_heads, int kv_heads, int head_dim, usm_dtype dtype) {
-    if (tokens <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
+size_t paged_attention_workspace_bytes(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, usm_dtype dtype) {
+    if (tokens <= 0 || num_seqs <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
         head_dim > kPagedMaxHeadDim || !dtype_ok(dtype) || (long long)tokens * q_heads >= 1LL << 31)
         return 0;
-    return paged_attention_workspace(tokens, q_heads, kv_heads, head_dim, dtype == USM_BF16);
+    return paged_attention_workspace(tokens, num_seqs, q_heads, kv_heads, head_dim, dtype == USM_BF16);
 }
 
 int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* q, int q_heads, float scale, int causal,
@@ -624,7 +624,7 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     if (status == USM_OK) status = check_tokens(out, c, tokens, q_heads, true);
     if (status != USM_OK) return status;
     const bool bf16 = c.dtype == USM_BF16;
-    if (!workspace || workspace_bytes < paged_attention_workspace(tokens, q_heads, c.kv_heads, c.head_dim, bf16))
+    if (!workspace || workspace_bytes < paged_attention_workspace(tokens, c.num_seqs, q_heads, c.kv_heads, c.head_dim, bf16))
         return USM_ERR_WORKSPACE;
     if (!aligned16(workspace)) return USM_ERR_ALIGNMENT;
     PagedArgs a{};

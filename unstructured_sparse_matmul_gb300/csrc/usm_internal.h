@@ -90,7 +90,7 @@ size_t attention_workspace_bytes(const AttnArgs& a, bool bf16);
 int launch_attention(const AttnArgs& a, bool bf16, void* workspace, cudaStream_t stream);
 int launch_rope_table(int positions, int rot, double base, float* table, cudaStream_t stream);
 int launch_paged_append(const AppendArgs& a, bool bf16, cudaStream_t stream);
-size_t paged_attention_workspace(int tokens, int q_heads, int kv_heads, int head_dim, bool bf16);
+size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16);
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream);
 // The matrix kernel for bf16 heads of up to 128 columns: rows of its blocks, and its launch.
 int paged_mma_rows();

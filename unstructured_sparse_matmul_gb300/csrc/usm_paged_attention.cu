@@ -6,18 +6,10 @@
 
 #include "usm_internal.h"
 #include "usm_paged.cuh"
+#include "usm_tmem.cuh"
 
 namespace usm {
 namespace {
-
-// ---------------------------------------------------------------------------
-// fp32 products on the FMA units: fp32 caches, and bf16 heads wider than the
-// matrix kernel takes.  kRows rows of queries stay in shared memory; tiles of
-// 64 keys pass through it.  Each of 256 threads holds 4 rows x 4 keys of the
-// scores and 4 rows x up to 16 columns of the sums.
-// ---------------------------------------------------------------------------
-constexpr int kBlockRows = 64, kBlockKeys = 64, kBlockThreads = 256;
-using BlockShares = PagedShares<kBlockRows, kBlockKeys, kBlockThreads, 2>;
 
 template <class T>
 __device__ __forceinline__ float4 load4(const T* p);
@@ -33,38 +25,70 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 }
 __device__ __forceinline__ void store4(float4 x, float* p) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(float4 x, __nv_bfloat16* p) {
-    uint2 w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
-    *reinterpret_cast<uint2*>(p) = w;
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(x.x, x.y), bf16x2(x.z, x.w));
+}
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+__device__ __forceinline__ float4 add_scaled(float4 x, float4 y, float f) {
+    return make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
 }
 
-// Row pitch of the shared arrays: a multiple of 4 that is 4 modulo 32, so that 8
-// consecutive rows start in different groups of banks.
-constexpr int block_pitch(int head_dim) { return (head_dim + 31) / 32 * 32 + 4; }
-constexpr int block_smem(int head_dim) {
-    return (kBlockRows + 2 * kBlockKeys) * block_pitch(head_dim) * 4 + kBlockRows * (kBlockKeys + 4) * 4;
-}
-
-// Reference of a row's exponents and its weight relative to another's: both
-// -inf (nothing seen) gives 0.
+// A row's weight relative to a reference `top`: nothing seen (-inf) gives 0.
 __device__ __forceinline__ float weight_of(float m, float top, float scale_log2) {
     return m == -INFINITY ? 0.f : exp2_fast((m - top) * scale_log2);
 }
 
+// Query row `row` of a segment, and its row of the output.
+template <class T>
+__device__ __forceinline__ const T* query_of(const PagedArgs& a, const PagedSegment& g, int row) {
+    const int flat = g.row0 + row, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
+    return (const T*)a.q + (g.start + token) * a.q_token + head * a.q_head;
+}
+template <class T>
+__device__ __forceinline__ T* output_of(const PagedArgs& a, const PagedSegment& g, int row) {
+    const int flat = g.row0 + row, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
+    return (T*)a.out + (g.start + token) * a.out_token + head * a.out_head;
+}
+
+// ---------------------------------------------------------------------------
+// fp32 caches, many rows, and bf16 heads wider than the matrix kernel takes:
+// products on the FMA units.  64 rows of queries stay in shared memory; tiles of
+// 64 keys pass through it, fp32 ones copied asynchronously one tile ahead.  Each
+// of 256 threads holds 4 rows x 4 keys of the scores and 4 rows x up to 16
+// columns of the sums, all in pairs (two FMAs an instruction); 12 wavefronts of
+// shared memory feed 64 FMAs of a warp.
+// ---------------------------------------------------------------------------
+constexpr int kBlockRows = 64, kBlockKeys = 64, kBlockThreads = 256;
+using BlockShares = PagedShares<kBlockRows, kBlockKeys, kBlockThreads, 3>;
+
+// Row pitch of the shared arrays: a multiple of 4 that is 4 modulo 32, so that 8
+// consecutive rows start in different groups of banks.
+constexpr int block_pitch(int head_dim) { return (head_dim + 31) / 32 * 32 + 4; }
+// Tiles of keys and values in shared memory: two where they fit.
+constexpr int block_stages(int head_dim) { return head_dim <= 128 ? 2 : 1; }
+constexpr int block_smem(int head_dim) {
+    return (kBlockRows + 2 * block_stages(head_dim) * kBlockKeys) * block_pitch(head_dim) * 4 + kBlockRows * (kBlockKeys + 4) * 4;
+}
+
+__device__ __forceinline__ void copy4(float* to, const float* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(float* to, const __nv_bfloat16* from, bool there) {
+    *reinterpret_cast<float4*>(to) = there ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 template <class T, int kWide>  // kWide: groups of 64 columns
-__global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ float4 smem_raw[];
     __shared__ long long scratch[kBlockThreads / 32 + 2];
     __shared__ PagedSegment seg;
     let_next_start();
+    constexpr int kStages = kWide <= 2 ? 2 : 1;
+    constexpr int kP = kBlockKeys + 4;
     const int D = a.head_dim, pitch = block_pitch(D);
     float* q = reinterpret_cast<float*>(smem_raw);
-    float* k = q + kBlockRows * pitch;
-    float* v = k + kBlockKeys * pitch;
-    float* p = v + kBlockKeys * pitch;  // probabilities, [row][key]
-    constexpr int kP = kBlockKeys + 4;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    float* tiles = q + kBlockRows * pitch;  // [stage][keys, then values][64][pitch]
+    float* p = tiles + kStages * 2 * kBlockKeys * pitch;  // probabilities, [row][key]
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
     const int quads = D / 4;
 
     BlockShares shares;
@@ -79,65 +103,78 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const PagedA
         }
         __syncthreads();
         if (!seg.live) break;
-        const PagedSegment g = seg;
-        for (int i = tid; i < kBlockRows * quads; i += kBlockThreads) {
-            const int r = i / quads, c = i - r * quads;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < g.rows) {
-                const int flat = g.row0 + r, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
-                x = load4((const T*)a.q + (g.start + token) * a.q_token + head * a.q_head + 4 * c);
-            }
-            *reinterpret_cast<float4*>(q + r * pitch + 4 * c) = x;
+        const PagedSegment& g = seg;
+        // A warp copies rows; its lanes find their places, one each.
+        for (int r0 = 8 * warp; r0 < 8 * warp + 8; ++r0) {
+            const bool there = r0 < g.rows;
+            const T* row = there ? query_of<T>(a, g, r0) : (const T*)a.q;
+            for (int c = lane; c < quads; c += 32) copy4(q + r0 * pitch + 4 * c, row + 4 * c, there);
         }
+        const auto load = [&](int t) {  // a warp: 8 keys and their values
+            const int key0 = (g.tile0 + t) * kBlockKeys + 8 * warp, key = key0 + (lane & 7);
+            int2 w = make_int2(-1, 0);
+            if (key >= g.lo && key < g.hi) w = paged_slot(a, g.seq, key);
+            float* to = tiles + (t % kStages) * 2 * kBlockKeys * pitch + 8 * warp * pitch;
+#pragma unroll 2
+            for (int r = 0; r < 8; ++r) {
+                const int page = __shfl_sync(kFullMask, w.x, r), slot = __shfl_sync(kFullMask, w.y, r);
+                const bool there = page >= 0;
+                const T* k = (const T*)a.k + (there ? page * a.k_page + slot * a.k_slot + g.head * a.k_head : 0);
+                const T* v = (const T*)a.v + (there ? page * a.v_page + slot * a.v_slot + g.head * a.v_head : 0);
+                for (int c = lane; c < quads; c += 32) {
+                    copy4(to + r * pitch + 4 * c, k + 4 * c, there);
+                    copy4(to + (kBlockKeys + r) * pitch + 4 * c, v + 4 * c, there);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         int2 seen[4];
-        float m[4], l[4], o[4][4 * kWide];
+        float m[4], l[4];
+        uint64_t o[4][2 * kWide];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             seen[i] = paged_seen(a, g, ty * 4 + i);
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4 * kWide; ++j) o[i][j] = 0.f;
+            for (int j = 0; j < 2 * kWide; ++j) o[i][j] = 0;
         }
-        for (int t = 0; t < g.tiles; ++t) {
+        const int n = g.tiles;
+        load(0);
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
             const int key0 = (g.tile0 + t) * kBlockKeys;
-            __syncthreads();  // the last tile's readers are done
-            for (int i = tid; i < kBlockKeys * quads; i += kBlockThreads) {
-                const int r = i / quads, c = i - r * quads, key = key0 + r;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (key >= g.lo && key < g.hi) {
-                    const int2 w = paged_slot(a, g.seq, key);
-                    x = load4((const T*)a.k + w.x * a.k_page + w.y * a.k_slot + g.head * a.k_head + 4 * c);
-                    y = load4((const T*)a.v + w.x * a.v_page + w.y * a.v_slot + g.head * a.v_head + 4 * c);
-                }
-                *reinterpret_cast<float4*>(k + r * pitch + 4 * c) = x;
-                *reinterpret_cast<float4*>(v + r * pitch + 4 * c) = y;
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
-            // Scores of rows 4·ty.. and keys tx, tx + 16, ...
-            float s[4][4] = {};
+            if (kStages == 2 && t + 1 < n) load(t + 1);
+            const float* k = tiles + (t % kStages) * 2 * kBlockKeys * pitch;
+            const float* v = k + kBlockKeys * pitch;
+            // Scores of rows 4·ty.. and keys tx, tx + 16, ..., even and odd columns apart.
+            uint64_t s2[4][4] = {};
+#pragma unroll 2
             for (int d = 0; d < D; d += 4) {
-                float4 qa[4], ka[4];
+                ulonglong2 qa[4], ka[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    qa[i] = *reinterpret_cast<const float4*>(q + (ty * 4 + i) * pitch + d);
-                    ka[i] = *reinterpret_cast<const float4*>(k + (tx + 16 * i) * pitch + d);
+                    qa[i] = *reinterpret_cast<const ulonglong2*>(q + (ty * 4 + i) * pitch + d);
+                    ka[i] = *reinterpret_cast<const ulonglong2*>(k + (tx + 16 * i) * pitch + d);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[i][j] = fmaf(qa[i].w, ka[j].w, fmaf(qa[i].z, ka[j].z, fmaf(qa[i].y, ka[j].y, fmaf(qa[i].x, ka[j].x, s[i][j]))));
+                    for (int j = 0; j < 4; ++j) s2[i][j] = fma2(qa[i].y, ka[j].y, fma2(qa[i].x, ka[j].x, s2[i][j]));
             }
             bool partly = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float top = -INFINITY;
+                float s[4], top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    float x, y;
+                    unpack2(s2[i][j], x, y);
                     const int key = key0 + tx + 16 * j;
-                    if (key < seen[i].x || key >= seen[i].y) s[i][j] = -INFINITY;
-                    top = fmaxf(top, s[i][j]);
+                    s[j] = key >= seen[i].x && key < seen[i].y ? x + y : -INFINITY;
+                    top = fmaxf(top, s[j]);
                 }
 #pragma unroll
                 for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w));
@@ -147,50 +184,50 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const PagedA
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = s[i][j] == -INFINITY ? 0.f : exp2_fast((s[i][j] - top) * a.scale_log2);
+                    const float e = s[j] == -INFINITY ? 0.f : exp2_fast((s[j] - top) * a.scale_log2);
                     p[(ty * 4 + i) * kP + tx + 16 * j] = e;
                     sum += e;
                 }
                 l[i] = l[i] * f + sum;  // this thread's keys
+                const uint64_t f2 = pack2(f, f);
 #pragma unroll
-                for (int j = 0; j < 4 * kWide; ++j) o[i][j] *= f;
+                for (int j = 0; j < 2 * kWide; ++j) o[i][j] = mul2(o[i][j], f2);
                 partly |= seen[i].x > key0 || seen[i].y < key0 + kBlockKeys;
             }
             __syncwarp();  // a warp's rows of p are its own
             // Where a row does not see the whole tile a weight of 0 takes no value.
             const bool guard = __any_sync(kFullMask, partly);
+#pragma unroll 1
             for (int key = 0; key < kBlockKeys; key += 4) {
                 float4 w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + (ty * 4 + i) * kP + key);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
+                    ulonglong2 y[kWide];
 #pragma unroll
                     for (int c = 0; c < kWide; ++c) {
                         const int col = 64 * c + 4 * tx;
-                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (col < D) y = *reinterpret_cast<const float4*>(v + (key + u) * pitch + col);
+                        y[c] = make_ulonglong2(0, 0);
+                        if (col < D) y[c] = *reinterpret_cast<const ulonglong2*>(v + (key + u) * pitch + col);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float e = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
-                            if (guard) {
-                                const int at = key0 + key + u;
-                                const bool use = at >= seen[i].x && at < seen[i].y;
-                                if (use) {
-                                    o[i][4 * c] = fmaf(e, y.x, o[i][4 * c]);
-                                    o[i][4 * c + 1] = fmaf(e, y.y, o[i][4 * c + 1]);
-                                    o[i][4 * c + 2] = fmaf(e, y.z, o[i][4 * c + 2]);
-                                    o[i][4 * c + 3] = fmaf(e, y.w, o[i][4 * c + 3]);
-                                }
-                            } else {
-                                o[i][4 * c] = fmaf(e, y.x, o[i][4 * c]);
-                                o[i][4 * c + 1] = fmaf(e, y.y, o[i][4 * c + 1]);
-                                o[i][4 * c + 2] = fmaf(e, y.z, o[i][4 * c + 2]);
-                                o[i][4 * c + 3] = fmaf(e, y.w, o[i][4 * c + 3]);
-                            }
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
+                        const int at = key0 + key + u;
+                        if (guard && (at < seen[i].x || at >= seen[i].y)) continue;
+                        const uint64_t e2 = pack2(e, e);
+#pragma unroll
+                        for (int c = 0; c < kWide; ++c) {
+                            o[i][2 * c] = fma2(e2, y[c].x, o[i][2 * c]);
+                            o[i][2 * c + 1] = fma2(e2, y[c].y, o[i][2 * c + 1]);
                         }
                     }
                 }
+            }
+            if (kStages == 1 && t + 1 < n) {
+                __syncthreads();
+                load(t + 1);
             }
         }
 #pragma unroll
@@ -199,27 +236,192 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const PagedA
             for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(kFullMask, l[i], w);
             const int r = ty * 4 + i;
             if (r >= g.rows) continue;
-            if (g.part == kPartWhole) {
-                const int flat = g.row0 + r, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
-                const float z = l[i] == 0.f ? 0.f : 1.f / l[i];
-                T* out = (T*)a.out + (g.start + token) * a.out_token + head * a.out_head;
+            const bool whole = g.part == kPartWhole;
+            const float z = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+            const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
+            T* out = output_of<T>(a, g, r);
 #pragma unroll
-                for (int c = 0; c < kWide; ++c) {
-                    const int col = 64 * c + 4 * tx;
-                    if (col < D)
-                        store4(make_float4(o[i][4 * c] * z, o[i][4 * c + 1] * z, o[i][4 * c + 2] * z, o[i][4 * c + 3] * z),
-                               out + col);
+            for (int c = 0; c < kWide; ++c) {
+                const int col = 64 * c + 4 * tx;
+                if (col >= D) continue;
+                float4 x;
+                unpack2(o[i][2 * c], x.x, x.y);
+                unpack2(o[i][2 * c + 1], x.z, x.w);
+                if (whole) store4(scaled(x, z), out + col);
+                else store4(x, a.parts + row * D + col);
+            }
+            if (!whole && tx == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(m[i], l[i]);
+        }
+    }
+    if (tid == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = meta;
+}
+
+// ---------------------------------------------------------------------------
+// fp32 caches, few rows (single tokens): every warp takes batches of keys straight
+// from memory, kLanes lanes a key, four columns each.  A lane's partial products
+// of a batch are summed across lanes all at once, halving the number of values a
+// lane holds with every step, so that a score costs about one shuffle; each lane
+// then has one key's weight, which goes back to all for the sums.  16 warps an SM
+// keep 64 to 128 KB of keys and values on the way.
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 256, kFewKeys = 128;
+
+template <int kLanes, int kR>  // 8, 16, 32 lanes: heads of up to 32, 64, 128 columns; rows
+__global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_constant__ PagedArgs a) {
+    using Shares = PagedShares<kR, kFewKeys, kFewThreads, 2>;
+    constexpr int kWarps = kFewThreads / 32, kSide = 32 / kLanes;
+    constexpr int kLoads = kR <= 4 ? 8 : 4;       // of keys, and of values, of a batch
+    constexpr int kBatch = kLoads * kSide;        // keys
+    constexpr int kSteps = kLoads == 8 ? 3 : 2;   // that halve the values
+    extern __shared__ float4 smem_raw[];          // queries [row][lane]; sums [warp][row][lane]; (reference, sum) [warp][row]
+    __shared__ int2 sees[kR];
+    __shared__ long long scratch[kWarps + 2];
+    __shared__ PagedSegment seg;
+    let_next_start();
+    const int D = a.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int side = lane / kLanes, col = 4 * (lane % kLanes);
+    const bool column = col < D;
+    float4* queries = smem_raw;
+    float4* sums = queries + kR * kLanes;
+    float2* stats = reinterpret_cast<float2*>(sums + kWarps * kR * kLanes);
+    // The load whose score this lane ends up with.
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) mine |= (lane & (kLanes >> (i + 1))) ? (kLoads >> (i + 1)) : 0;
+    const float c = a.scale_log2;
+
+    Shares shares;
+    shares.init(a, blockIdx.x, gridDim.x, scratch);
+    PagedMeta meta = {};
+    while (true) {
+        __syncthreads();
+        if (tid < 32) {
+            const PagedSegment g = shares.next(a);
+            if (g.live) paged_note(meta, g);
+            if (tid == 0) seg = g;
+        }
+        __syncthreads();
+        if (!seg.live) break;
+        const PagedSegment& g = seg;
+        for (int i = tid; i < kR * kLanes; i += kFewThreads) {
+            const int r = i / kLanes, at = i % kLanes;
+            queries[i] = r < g.rows && 4 * at < D ? load4(query_of<float>(a, g, r) + 4 * at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at == 0) sees[r] = paged_seen(a, g, r);
+        }
+        __syncthreads();
+        float4 o[kR];
+        float m[kR], l[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+        const int lo = g.lo, hi = g.hi, seq = g.seq;
+        const float* kb = (const float*)a.k + g.head * a.k_head + col;
+        const float* vb = (const float*)a.v + g.head * a.v_head + col;
+        const int first = g.tile0 * kFewKeys + warp * kBatch, end = min((g.tile0 + g.tiles) * kFewKeys, hi);
+        const auto slot_of = [&](int base) {  // of this lane's key of a batch
+            const int key = base + lane;
+            return lane < kBatch && key >= lo && key < end ? paged_slot(a, seq, key) : make_int2(-1, 0);
+        };
+        int2 next = slot_of(first);
+#pragma unroll 1
+        for (int base = first; base < end; base += kWarps * kBatch) {
+            const int2 w = next;
+            next = slot_of(base + kWarps * kBatch);
+            float4 k[kLoads], v[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int page = __shfl_sync(kFullMask, w.x, j * kSide + side), slot = __shfl_sync(kFullMask, w.y, j * kSide + side);
+                k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (page >= 0 && column) {
+                    k[j] = load4(kb + page * a.k_page + slot * a.k_slot);
+                    v[j] = load4(vb + page * a.v_page + slot * a.v_slot);
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const float4 q = queries[r * kLanes + lane % kLanes];
+                float s[kLoads];
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) s[j] = fmaf(q.w, k[j].w, fmaf(q.z, k[j].z, fmaf(q.y, k[j].y, q.x * k[j].x)));
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int half = kLoads >> (i + 1), mask = kLanes >> (i + 1);
+                    const bool upper = lane & mask;
+#pragma unroll
+                    for (int j = 0; j < half; ++j) {
+                        const float give = upper ? s[j] : s[j + half], keep = upper ? s[j + half] : s[j];
+                        s[j] = keep + __shfl_xor_sync(kFullMask, give, mask);
+                    }
+                }
+#pragma unroll
+                for (int mask = kLanes >> (kSteps + 1); mask > 0; mask >>= 1) s[0] += __shfl_xor_sync(kFullMask, s[0], mask);
+                const int key = base + mine * kSide + side;
+                const int2 seen = sees[r];
+                const bool use = key >= max(lo, seen.x) && key < min(end, seen.y);
+                const float x = use ? s[0] : -INFINITY;
+                if (__any_sync(kFullMask, x > m[r])) {
+                    float top = x;
+#pragma unroll
+                    for (int mask = 16; mask > 0; mask >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, mask));
+                    top = fmaxf(top, m[r]);
+                    const float f = weight_of(m[r], top, c);
+                    m[r] = top;
+                    l[r] *= f;
+                    o[r] = scaled(o[r], f);
+                }
+                const float p = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
+                l[r] += p;
+                // Where some key of the batch is not seen a weight of 0 takes no value.
+                const bool all = __all_sync(kFullMask, use);
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    int from = side * kLanes;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
+                    const float pj = __shfl_sync(kFullMask, p, from);
+                    if (all || pj != 0.f) o[r] = add_scaled(o[r], v[j], pj);
+                }
+            }
+        }
+        // Keys of a warp's sides, then the warps.
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+#pragma unroll
+            for (int mask = kLanes; mask < 32; mask <<= 1) {
+                o[r].x += __shfl_xor_sync(kFullMask, o[r].x, mask);
+                o[r].y += __shfl_xor_sync(kFullMask, o[r].y, mask);
+                o[r].z += __shfl_xor_sync(kFullMask, o[r].z, mask);
+                o[r].w += __shfl_xor_sync(kFullMask, o[r].w, mask);
+            }
+#pragma unroll
+            for (int mask = 16; mask > 0; mask >>= 1) l[r] += __shfl_xor_sync(kFullMask, l[r], mask);
+            l[r] *= (float)kLoads / kLanes;  // each score is in kLanes / kLoads lanes
+            if (side == 0) sums[(warp * kR + r) * kLanes + lane] = o[r];
+            if (lane == 0) stats[warp * kR + r] = make_float2(m[r], l[r]);
+        }
+        __syncthreads();
+        for (int i = tid; i < kR * kLanes; i += kFewThreads) {
+            const int r = i / kLanes, at = i % kLanes;
+            if (r >= g.rows || 4 * at >= D) continue;
+            float top = -INFINITY, sum = 0.f;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * kR + r].x);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 st = stats[w * kR + r];
+                if (st.x == -INFINITY) continue;
+                const float f = weight_of(st.x, top, c);
+                sum = fmaf(st.y, f, sum);
+                x = add_scaled(x, sums[(w * kR + r) * kLanes + at], f);
+            }
+            if (g.part == kPartWhole) {
+                store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<float>(a, g, r) + 4 * at);
             } else {
                 const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
-#pragma unroll
-                for (int c = 0; c < kWide; ++c) {
-                    const int col = 64 * c + 4 * tx;
-                    if (col < D)
-                        store4(make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]),
-                               a.parts + row * D + col);
-                }
-                if (tx == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(m[i], l[i]);
+                store4(x, a.parts + row * D + 4 * at);
+                if (at == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(top, sum);
             }
         }
     }
@@ -228,21 +430,49 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const PagedA
 
 // ---------------------------------------------------------------------------
 // Joins the parts of items that several CTAs took: CTA (c, y) of this kernel
-// takes rows 8·y.. of the item that CTA c began, a warp each.
+// takes some rows of the item that CTA c began.  A group of kLanes lanes holds
+// one row; where the rows leave groups idle, a row's parts are dealt out to
+// several.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 256;
+constexpr int join_rows(int lanes) { return 2 * kJoinThreads / lanes; }  // of a CTA: two a group
 
-template <class T>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedArgs a, int ctas) {
+// A part's (reference, sum) and columns 4·lane.. of its sums.
+struct JoinPart {
+    float2 stat;
+    float4 x[2];
+};
+
+// Adds a part to sums with a reference that is no less.
+__device__ __forceinline__ void add_part(JoinPart& sum, const JoinPart& p, float scale_log2, int quads) {
+    if (p.stat.x == -INFINITY) return;  // no key seen there
+    const float w = weight_of(p.stat.x, sum.stat.x, scale_log2);
+    sum.stat.y = fmaf(p.stat.y, w, sum.stat.y);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (j >= quads) break;
+        sum.x[j].x = fmaf(p.x[j].x, w, sum.x[j].x);
+        sum.x[j].y = fmaf(p.x[j].y, w, sum.x[j].y);
+        sum.x[j].z = fmaf(p.x[j].z, w, sum.x[j].z);
+        sum.x[j].w = fmaf(p.x[j].w, w, sum.x[j].w);
+    }
+}
+
+template <class T, int kLanes>  // 8, 16 or 32: heads of up to 32, 64, 256 columns
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
+    constexpr int kJoinRows = join_rows(kLanes), kGroups = kJoinThreads / kLanes, kQuads = kLanes == 32 ? 2 : 1, kAhead = 4;
+    __shared__ JoinPart shared[kGroups][kLanes];
     await_previous();
     const PagedMeta* meta = static_cast<const PagedMeta*>(a.meta);
-    const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    const PagedMeta first = meta[c];
-    if (!first.first_live || r >= first.rows) return;
+    const int c = blockIdx.x, warp_lane = threadIdx.x & 31;
+    const int4 begin = __ldcg(reinterpret_cast<const int4*>(meta + c));  // first_live, start, row0, rows
+    const int row_base = blockIdx.y * kJoinRows, rows = min(begin.w - row_base, kJoinRows);
+    if (!begin.x || rows <= 0) return;
+    const int head0 = meta[c].head * a.group;
     // The CTAs c + 1 .. c + count hold the rest.
     int count = 0;
     for (int at = c + 1; at < ctas; at += 32) {
-        const int i = at + lane;
+        const int i = at + warp_lane;
         const bool last = i >= ctas || !meta[i].later_live || meta[i].ends;
         const unsigned stop = __ballot_sync(kFullMask, last);
         if (stop) {
@@ -250,62 +480,92 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
             break;
         }
     }
-    if (!meta[c + count].later_live) return;  // not a message of this call: nothing to join
-    const int D = a.head_dim;
-    const auto row_of = [&](int i) { return (i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater) * a.part_rows + r; };
-    const auto stat_of = [&](int i) { return *reinterpret_cast<const float2*>(a.part_stats + 2 * row_of(i)); };
-    float top = -INFINITY;
-    for (int i = lane; i <= count; i += 32) top = fmaxf(top, stat_of(i).x);
+    const int D = a.head_dim, group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    int split = 1;  // groups a row
+    while (2 * split * rows <= kGroups && split <= count) split *= 2;
+    const int side = kGroups / split, share = group / side;  // rows side by side; this group's share of the parts
+    for (int r0 = 0; r0 < rows; r0 += side) {
+        const int r = row_base + r0 + group % side;
+        const bool real = r0 + group % side < rows;
+        JoinPart sum = {make_float2(-INFINITY, 0.f), {}};
+        if (real) {
+            const auto row_of = [&](int i) { return (i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater) * a.part_rows + r; };
+            for (int i0 = share; i0 <= count; i0 += kAhead * split) {
+                JoinPart p[kAhead];
+                float top = sum.stat.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-    float sum = 0.f;
-    float4 x[2] = {};
-    for (int i = 0; i <= count; ++i) {
-        const float2 st = stat_of(i);
-        const float w = weight_of(st.x, top, a.scale_log2);
-        sum = fmaf(st.y, w, sum);
-        const float* part = a.parts + row_of(i) * D;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * split;
+                    p[u].stat = make_float2(-INFINITY, 0.f);
+                    if (i > count) continue;
+                    const long long row = row_of(i);
+                    p[u].stat = __ldcg(reinterpret_cast<const float2*>(a.part_stats + 2 * row));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = 128 * j + 4 * lane;
-            if (col < D && st.x != -INFINITY) {
-                const float4 y = *reinterpret_cast<const float4*>(part + col);
-                x[j].x = fmaf(y.x, w, x[j].x);
-                x[j].y = fmaf(y.y, w, x[j].y);
-                x[j].z = fmaf(y.z, w, x[j].z);
-                x[j].w = fmaf(y.w, w, x[j].w);
+                    for (int j = 0; j < kQuads; ++j)
+                        if (128 * j + 4 * lane < D) p[u].x[j] = __ldcg(reinterpret_cast<const float4*>(a.parts + row * D + 128 * j + 4 * lane));
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) top = fmaxf(top, p[u].stat.x);
+                const float f = weight_of(sum.stat.x, top, a.scale_log2);
+                sum.stat = make_float2(top, sum.stat.y * f);
+#pragma unroll
+                for (int j = 0; j < kQuads; ++j) sum.x[j].x *= f, sum.x[j].y *= f, sum.x[j].z *= f, sum.x[j].w *= f;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) add_part(sum, p[u], a.scale_log2, kQuads);
             }
         }
-    }
-    const int flat = first.row0 + r, token = flat / a.group, head = first.head * a.group + flat - token * a.group;
-    T* out = (T*)a.out + (first.start + token) * a.out_token + head * a.out_head;
-    const float z = sum == 0.f ? 0.f : 1.f / sum;
+        if (split > 1) {  // one row group a CTA then
+            shared[group][lane] = sum;
+            __syncthreads();
+            if (share > 0 || !real) return;
+            float top = sum.stat.x;
+            for (int u = 1; u < split; ++u) top = fmaxf(top, shared[group + u * side][lane].stat.x);
+            const float f = weight_of(sum.stat.x, top, a.scale_log2);
+            sum.stat = make_float2(top, sum.stat.y * f);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = 128 * j + 4 * lane;
-        if (col < D) store4(make_float4(x[j].x * z, x[j].y * z, x[j].z * z, x[j].w * z), out + col);
+            for (int j = 0; j < kQuads; ++j) sum.x[j].x *= f, sum.x[j].y *= f, sum.x[j].z *= f, sum.x[j].w *= f;
+            for (int u = 1; u < split; ++u) add_part(sum, shared[group + u * side][lane], a.scale_log2, kQuads);
+        }
+        if (!real) continue;
+        const int flat = begin.z + r, token = flat / a.group;
+        T* out = (T*)a.out + (begin.y + token) * a.out_token + (head0 + flat - token * a.group) * a.out_head;
+        const float z = sum.stat.y == 0.f ? 0.f : 1.f / sum.stat.y;
+#pragma unroll
+        for (int j = 0; j < kQuads; ++j)
+            if (128 * j + 4 * lane < D)
+                store4(make_float4(sum.x[j].x * z, sum.x[j].y * z, sum.x[j].z * z, sum.x[j].w * z), out + 128 * j + 4 * lane);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
+enum class Form { Mma, Block, Few1, Few4, Few8 };
 struct Shape {
-    bool mma;
+    Form form;
     int rows;  // of a block
     int ctas;
 };
-Shape shape_of(int head_dim, bool bf16) {
-    if (bf16 && head_dim <= 128) return Shape{true, paged_mma_rows(), sm_count_current_device()};
-    const int fit = std::max(1, std::min(4, 220 * 1024 / block_smem(head_dim)));
-    return Shape{false, kBlockRows, fit * sm_count_current_device()};
+// bf16 heads of up to 128 columns go to the matrix kernel.  fp32 heads of that
+// width with up to 8 rows a sequence and head of keys, on average, are read by few
+// rows at a time: from 9 on the keys would be read twice, and the block kernel is
+// as fast.
+Shape shape_of(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16) {
+    const int sms = sm_count_current_device();
+    if (bf16 && head_dim <= 128) return Shape{Form::Mma, paged_mma_rows(), sms};
+    const long long rows = (long long)tokens * (q_heads / kv_heads);
+    if (!bf16 && head_dim <= 128 && rows <= 8LL * num_seqs) {
+        if (rows <= num_seqs) return Shape{Form::Few1, 1, 2 * sms};
+        return rows <= 4LL * num_seqs ? Shape{Form::Few4, 4, 2 * sms} : Shape{Form::Few8, 8, 2 * sms};
+    }
+    const int fit = std::max(1, std::min(2, 220 * 1024 / block_smem(head_dim)));
+    return Shape{Form::Block, kBlockRows, fit * sms};
 }
 
 int part_rows(int tokens, int q_heads, int kv_heads, int rows) {
     return (int)std::min<long long>(rows, (long long)tokens * (q_heads / kv_heads));
 }
 
-// bf16 heads of up to 128 columns go to the matrix kernel.
 template <class T, int kWide>
 int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_block_kernel<T, kWide>;
@@ -315,37 +575,64 @@ int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
 
+template <int kLanes, int kR>
+int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
+    const auto kernel = paged_few_kernel<kLanes, kR>;
+    constexpr int smem = kR * kLanes * 16 + kFewThreads / 32 * kR * (kLanes * 16 + 8);
+    if (!allow_shared(kernel, smem)) return cuda_failure();
+    kernel<<<ctas, kFewThreads, smem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+}
+template <int kR>
+int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
+    if (a.head_dim <= 32) return run_few<8, kR>(a, ctas, stream);
+    return a.head_dim <= 64 ? run_few<16, kR>(a, ctas, stream) : run_few<32, kR>(a, ctas, stream);
+}
+template <class T>
+int run_block(const PagedArgs& a, int ctas, cudaStream_t stream) {
+    if (a.head_dim <= 64) return run_block<T, 1>(a, ctas, stream);
+    if (a.head_dim <= 128) return run_block<T, 2>(a, ctas, stream);
+    return a.head_dim <= 192 ? run_block<T, 3>(a, ctas, stream) : run_block<T, 4>(a, ctas, stream);
+}
+
+template <class T, int kLanes>
+int join(const PagedArgs& a, int ctas, cudaStream_t stream) {
+    const auto kernel = paged_join_kernel<T, kLanes>;
+    // The same split of an SM's memory as the kernel before it has: to change it the
+    // SM would have to drain.
+    if (!allow_shared(kernel, 0)) return cuda_failure();
+    return launch_next(kernel, dim3(ctas, (a.part_rows + join_rows(kLanes) - 1) / join_rows(kLanes)), kJoinThreads, 1, stream, a, ctas);
+}
+
 size_t meta_bytes(int ctas) { return ((size_t)ctas * sizeof(PagedMeta) + 15) / 16 * 16; }
 
 }  // namespace
 
-size_t paged_attention_workspace(int tokens, int q_heads, int kv_heads, int head_dim, bool bf16) {
-    const Shape s = shape_of(head_dim, bf16);
+size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16) {
+    const Shape s = shape_of(tokens, num_seqs, q_heads, kv_heads, head_dim, bf16);
     const size_t rows = (size_t)2 * s.ctas * part_rows(tokens, q_heads, kv_heads, s.rows);
     return meta_bytes(s.ctas) + rows * head_dim * 4 + rows * 8;
 }
 
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream) {
-    const Shape s = shape_of(a.head_dim, bf16);
+    const Shape s = shape_of(a.tokens, a.num_seqs, a.kv_heads * a.group, a.kv_heads, a.head_dim, bf16);
+    // Rows of an item at most.
     a.part_rows = (int)std::min<long long>(s.rows, (long long)(a.q_offsets ? a.tokens : a.per_seq) * a.group);
     a.meta = workspace;
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(s.ctas));
     a.part_stats = a.parts + (size_t)2 * s.ctas * a.part_rows * a.head_dim;
     int code;
-    if (s.mma) code = launch_paged_mma(a, s.ctas, stream);
-    else switch ((a.head_dim + 63) / 64) {
-        case 1: code = bf16 ? run_block<__nv_bfloat16, 1>(a, s.ctas, stream) : run_block<float, 1>(a, s.ctas, stream); break;
-        case 2: code = bf16 ? run_block<__nv_bfloat16, 2>(a, s.ctas, stream) : run_block<float, 2>(a, s.ctas, stream); break;
-        case 3: code = bf16 ? run_block<__nv_bfloat16, 3>(a, s.ctas, stream) : run_block<float, 3>(a, s.ctas, stream); break;
-        default: code = bf16 ? run_block<__nv_bfloat16, 4>(a, s.ctas, stream) : run_block<float, 4>(a, s.ctas, stream); break;
+    switch (s.form) {
+        case Form::Mma: code = launch_paged_mma(a, s.ctas, stream); break;
+        case Form::Few1: code = run_few<1>(a, s.ctas, stream); break;
+        case Form::Few4: code = run_few<4>(a, s.ctas, stream); break;
+        case Form::Few8: code = run_few<8>(a, s.ctas, stream); break;
+        default: code = bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
     }
     if (code != USM_OK) return code;
-    // The join asks for the same split of an SM's memory as the kernel before it: to
-    // change it the SM has to drain.
-    if (!allow_shared(paged_join_kernel<__nv_bfloat16>, 0) || !allow_shared(paged_join_kernel<float>, 0)) return cuda_failure();
-    const dim3 grid(s.ctas, (a.part_rows + kJoinWarps - 1) / kJoinWarps);
-    if (bf16) return launch_next(paged_join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, 1, stream, a, s.ctas);
-    return launch_next(paged_join_kernel<float>, grid, kJoinWarps * 32, 1, stream, a, s.ctas);
+    if (a.head_dim <= 32) return bf16 ? join<__nv_bfloat16, 8>(a, s.ctas, stream) : join<float, 8>(a, s.ctas, stream);
+    if (a.head_dim <= 64) return bf16 ? join<__nv_bfloat16, 16>(a, s.ctas, stream) : join<float, 16>(a, s.ctas, stream);
+    return bf16 ? join<__nv_bfloat16, 32>(a, s.ctas, stream) : join<float, 32>(a, s.ctas, stream);
 }
 
 }  // namespace usm
