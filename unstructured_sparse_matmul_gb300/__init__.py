@@ -739,72 +739,103 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device=None)
     return out
 
 
+# The two calls below are made for every token and layer: each argument's checks
+# are one expression, `stream` is an argument of their own (through _on_stream
+# costs a call 2 us) and sizes that follow from other sizes are remembered.
 def _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T):
     """The usm_paged_cache struct, as bytes that the call takes a pointer to."""
-    _tensor(k_cache, "k_cache", index, T.real, 4)
-    _tensor(v_cache, "v_cache", index, (k_cache.dtype,), 4)
-    _tensor(page_table, "page_table", index, T.i32, 2)
-    shape = pages, slots, heads, D = k_cache.shape
-    if v_cache.shape != shape:
-        raise ValueError(f"k_cache is {tuple(shape)}, v_cache {tuple(v_cache.shape)}")
+    if (v_cache is None or page_table is None or lengths is None or k_cache.dtype not in T.real or index < 0
+            or v_cache.dtype is not k_cache.dtype or k_cache.dim() != 4 or v_cache.shape != k_cache.shape
+            or v_cache.get_device() != index or page_table.dtype is not T.i32[0] or page_table.dim() != 2
+            or page_table.get_device() != index):
+        _tensor(k_cache, "k_cache", index, T.real, 4)
+        _tensor(v_cache, "v_cache", index, (k_cache.dtype,), 4)
+        _tensor(page_table, "page_table", index, T.i32, 2)
+        _tensor(lengths, "lengths", index, T.i32, 1)
+        raise ValueError(f"k_cache is {tuple(k_cache.shape)}, v_cache {tuple(v_cache.shape)}")
+    pages, slots, heads, D = k_cache.shape
     kp, ks, kh, k1 = k_cache.stride()
     vp, vs, vh, v1 = v_cache.stride()
     seqs, listed = page_table.shape
     row, one = page_table.stride()
-    if D > 1 and (k1 != 1 or v1 != 1):
-        raise ValueError("caches must have unit stride in their last dimension")
-    if listed > 1 and one != 1:
-        raise ValueError("page_table must have unit column stride")
-    if max(pages, slots, heads, D, seqs, listed, row) >= 2**31:
-        raise ValueError("a dimension of the cache or its page table does not fit 32 bits")
     _array(lengths, "lengths", index, T.i32, seqs)
     if q_offsets is not None:
         _array(q_offsets, "q_offsets", index, T.i32, seqs + 1)
+    if k1 != 1 or v1 != 1 or one != 1 or pages | slots | heads | D | seqs | listed | row >= 2**31:
+        if D > 1 and (k1 != 1 or v1 != 1):
+            raise ValueError("caches must have unit stride in their last dimension")
+        if listed > 1 and one != 1:
+            raise ValueError("page_table must have unit column stride")
+        if pages | slots | heads | D | seqs | listed | row >= 2**31:
+            raise ValueError("a dimension of the cache or its page table does not fit 32 bits")
     return _pack_paged(k_cache.data_ptr(), v_cache.data_ptr(), kp, ks, kh, vp, vs, vh, page_table.data_ptr(),
-                       lengths.data_ptr(), 0 if q_offsets is None else q_offsets.data_ptr(), _code(k_cache, T), pages,
-                       slots, heads, D, seqs, row, listed)
+                       lengths.data_ptr(), 0 if q_offsets is None else q_offsets.data_ptr(),
+                       USM_F32 if k_cache.dtype is T.f32[0] else USM_BF16, pages, slots, heads, D, seqs, row, listed)
 
 
-def _tokens(t, name, index, dtype, shape, copy=True):
+def _tokens(t, name, index, dtype, shape, written=False):
     """Rows of the new tokens (tokens x heads x head_dim) as the library reads
     them, with the usm_tokens struct as bytes; inputs whose rows are not 16-byte
     aligned are copied."""
-    _tensor(t, name, index, (dtype,), 3)
-    if t.shape != shape:
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _tensor(t, name, index, (dtype,), 3)
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
     a, b, one = t.stride()
-    if copy and (one != 1 or (t.data_ptr() | a * t.element_size() | b * t.element_size()) & 15):
+    at = t.data_ptr()
+    if not written and (one != 1 or (at | a * t.element_size() | b * t.element_size()) & 15):
         t = t.clone(memory_format=_Types.torch.contiguous_format)
         a, b, one = t.stride()
+        at = t.data_ptr()
     if one != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return t, _pack_tokens(t.data_ptr(), a, b)
+    return t, _pack_tokens(at, a, b)
 
 
-@_on_stream
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(index, tokens, seqs, q_heads, kv_heads, head_dim, code):
+    """Bytes of a call's workspace on device `index`."""
+    with _Types.torch.cuda.device(index):
+        return load().paged_attention_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim, code)
+
+
+def _under(stream, fn, *args):
+    """fn(*args) with a stream of the caller's, as _on_stream has it."""
+    torch = _torch()
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args)
+
+
 def paged_append(k, v, k_cache, v_cache, page_table, lengths, q_offsets=None, rope=None, interleaved: bool = False, q=None,
-                 q_out=None):
+                 q_out=None, stream=None):
     """Writes the new tokens' keys (rotated by position) and values into their
     slots of the cache; with q returns the rotated queries (in q_out, which may
     be q).  k, v: tokens x kv_heads x head_dim, q: tokens x q_heads x head_dim;
     rope: positions x rot_dim of rope_table, or None; see paged_append."""
+    if stream is not None:
+        return _under(stream, paged_append, k, v, k_cache, v_cache, page_table, lengths, q_offsets, rope, interleaved, q, q_out)
     T, lib = _types(), load()
     index = _device_of(k_cache, "k_cache")
     cache = _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T)
-    _tensor(k, "k", index, (k_cache.dtype,), 3)
-    n, (heads, D), dt = _entries(k.shape[0]), k_cache.shape[2:], k_cache.dtype
-    k, kt = _tokens(k, "k", index, dt, (n, heads, D))
-    v, vt = _tokens(v, "v", index, dt, (n, heads, D))
+    dt = k_cache.dtype
+    if k is None or k.dim() != 3:
+        _tensor(k, "k", index, (dt,), 3)
+    n = _entries(k.shape[0])
+    shape = (n, *k_cache.shape[2:])
+    k, kt = _tokens(k, "k", index, dt, shape)
+    v, vt = _tokens(v, "v", index, dt, shape)
     qt = ot = None
     q_heads = rot = positions = 0
     if q is not None:
-        _tensor(q, "q", index, (dt,), 3)
+        if q.dim() != 3:
+            _tensor(q, "q", index, (dt,), 3)
         q_heads = q.shape[1]
-        shape = (n, q_heads, D)
+        q, qt = _tokens(q, "q", index, dt, (n, q_heads, shape[2]))
         if q_out is None:
-            q_out = T.empty(shape, dtype=dt, device=q.device)
-        q, qt = _tokens(q, "q", index, dt, shape)
-        _, ot = _tokens(q_out, "q_out", index, dt, shape, copy=False)
+            q_out = T.torch.empty_like(q, memory_format=T.torch.contiguous_format)
+        _, ot = _tokens(q_out, "q_out", index, dt, q.shape, written=True)
         if q_heads == 0:
             qt = ot = None
     elif q_out is not None:
@@ -814,38 +845,39 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, q_offsets=None, ro
         if not rope.is_contiguous():
             raise ValueError("rope must be contiguous")
         positions, rot = rope.shape
-    _run("paged_append", lib.paged_append, index, T, cache, n, kt, vt, qt, ot, q_heads, _ptr(rope), positions, rot,
-         int(bool(interleaved)))
+    _run("paged_append", lib.paged_append, index, T, cache, n, kt, vt, qt, ot, q_heads,
+         None if rope is None else rope.data_ptr(), positions, rot, 1 if interleaved else 0)
     return q_out
 
 
-@_on_stream
 def paged_attention(q, k_cache, v_cache, page_table, lengths, q_offsets=None, scale: float = 1.0, causal: bool = True,
-                    window: int = 0, out=None, workspace=None):
+                    window: int = 0, out=None, workspace=None, stream=None):
     """Attention of the new tokens q (tokens x q_heads x head_dim) over their
     sequences' pages, of q's type: softmax of scale*(q.K) over the keys up to the
     token's own position (causal) and, with window > 0, at most window of them;
     see paged_attention."""
+    if stream is not None:
+        return _under(stream, paged_attention, q, k_cache, v_cache, page_table, lengths, q_offsets, scale, causal, window,
+                      out, workspace)
     T, lib = _types(), load()
     index = _device_of(k_cache, "k_cache")
     cache = _cache(k_cache, v_cache, page_table, lengths, q_offsets, index, T)
     dt = k_cache.dtype
-    _tensor(q, "q", index, (dt,), 3)
+    if q is None or q.dim() != 3:
+        _tensor(q, "q", index, (dt,), 3)
     shape = n, q_heads, D = q.shape
     _entries(n * q_heads)
     _int32((window,), ("window",))
-    heads = k_cache.shape[2]
     if D != k_cache.shape[3]:
         raise ValueError(f"q has {D} columns, the cache {k_cache.shape[3]}")
-    if out is None:
-        out = T.empty(shape, dtype=dt, device=q.device)
     q, qt = _tokens(q, "q", index, dt, shape)
-    _, ot = _tokens(out, "out", index, dt, shape, copy=False)
-    code = _code(q, T)
-    need = lib.paged_attention_workspace_bytes(n, page_table.shape[0], q_heads, heads, D, code)
+    if out is None:
+        out = T.torch.empty_like(q, memory_format=T.torch.contiguous_format)
+    _, ot = _tokens(out, "out", index, dt, shape, written=True)
+    need = _attention_workspace(index, n, page_table.shape[0], q_heads, k_cache.shape[2], D, USM_F32 if dt is T.f32[0] else USM_BF16)
     ws = _workspace(workspace, need, q, T)
-    _run("paged_attention", lib.paged_attention, index, T, cache, n, qt, q_heads, scale, int(bool(causal)), window, ot,
-         _ptr(ws), need)
+    _run("paged_attention", lib.paged_attention, index, T, cache, n, qt, q_heads, scale, 1 if causal else 0, window, ot,
+         None if ws is None else ws.data_ptr(), need)
     return out
 
 

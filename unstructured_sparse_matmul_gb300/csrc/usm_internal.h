@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "usm.h"
 #include "usm_args.h"
 
@@ -147,6 +149,26 @@ inline bool allow_shared(Kernel kernel, int smem) {
            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
                cudaSuccess;
 }
+
+// allow_shared by a call that is made often: once for each device and context (the
+// two settings cost a quarter of a microsecond each).  One object per kernel.
+class SharedOnce {
+  public:
+    template <class Kernel>
+    bool allow(Kernel kernel, int smem) {
+        int dev = 0;
+        const unsigned long long id = current_context_id();
+        if (id == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return allow_shared(kernel, smem);
+        if (context_[dev].load(std::memory_order_relaxed) == id) return true;
+        if (!allow_shared(kernel, smem)) return false;
+        context_[dev].store(id, std::memory_order_relaxed);
+        return true;
+    }
+
+  private:
+    static constexpr int kMaxDevices = 64;
+    std::atomic<unsigned long long> context_[kMaxDevices] = {};
+};
 
 // A second kernel (in clusters of `cluster` CTAs) that may be brought to the SMs
 // while the stream's last one still runs, which calls let_next_start(); it reads

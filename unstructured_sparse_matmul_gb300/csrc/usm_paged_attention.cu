@@ -49,6 +49,32 @@ __device__ __forceinline__ T* output_of(const PagedArgs& a, const PagedSegment& 
     return (T*)a.out + (g.start + token) * a.out_token + head * a.out_head;
 }
 
+// A CTA's walk over its share, in shared memory: its first warp takes the steps.
+template <class Shares>
+struct Walk {
+    alignas(8) char shares[sizeof(Shares)];
+    PagedMeta meta;
+
+    __device__ __forceinline__ void begin(const PagedArgs& a, long long* scratch) {
+        Shares s;
+        s.init(a, blockIdx.x, gridDim.x, scratch);
+        if (threadIdx.x == 0) {
+            memcpy(shares, &s, sizeof s);
+            meta = PagedMeta{};
+        }
+    }
+    __device__ __forceinline__ void next(const PagedArgs& a, PagedSegment& seg) {
+        Shares s;
+        memcpy(&s, shares, sizeof s);
+        const PagedSegment g = s.next(a);
+        if (threadIdx.x == 0) {
+            memcpy(shares, &s, sizeof s);
+            if (g.live) paged_note(meta, g);
+            seg = g;
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // fp32 caches, many rows, and bf16 heads wider than the matrix kernel takes:
 // products on the FMA units.  64 rows of queries stay in shared memory; tiles of
@@ -91,16 +117,11 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
     const int quads = D / 4;
 
-    BlockShares shares;
-    shares.init(a, blockIdx.x, gridDim.x, scratch);
-    PagedMeta meta = {};
+    __shared__ Walk<BlockShares> walk;
+    walk.begin(a, scratch);
     while (true) {
         __syncthreads();
-        if (tid < 32) {
-            const PagedSegment g = shares.next(a);
-            if (g.live) paged_note(meta, g);
-            if (tid == 0) seg = g;
-        }
+        if (tid < 32) walk.next(a, seg);
         __syncthreads();
         if (!seg.live) break;
         const PagedSegment& g = seg;
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
             if (!whole && tx == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(m[i], l[i]);
         }
     }
-    if (tid == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = meta;
+    if (tid == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = walk.meta;
 }
 
 // ---------------------------------------------------------------------------
@@ -290,16 +311,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
     for (int i = 0; i < kSteps; ++i) mine |= (lane & (kLanes >> (i + 1))) ? (kLoads >> (i + 1)) : 0;
     const float c = a.scale_log2;
 
-    Shares shares;
-    shares.init(a, blockIdx.x, gridDim.x, scratch);
-    PagedMeta meta = {};
+    __shared__ Walk<Shares> walk;
+    walk.begin(a, scratch);
     while (true) {
         __syncthreads();
-        if (tid < 32) {
-            const PagedSegment g = shares.next(a);
-            if (g.live) paged_note(meta, g);
-            if (tid == 0) seg = g;
-        }
+        if (tid < 32) walk.next(a, seg);
         __syncthreads();
         if (!seg.live) break;
         const PagedSegment& g = seg;
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
             }
         }
     }
-    if (tid == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = meta;
+    if (tid == 0) static_cast<PagedMeta*>(a.meta)[blockIdx.x] = walk.meta;
 }
 
 // ---------------------------------------------------------------------------
@@ -570,7 +586,8 @@ template <class T, int kWide>
 int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_block_kernel<T, kWide>;
     const int smem = block_smem(a.head_dim);
-    if (!allow_shared(kernel, smem)) return cuda_failure();
+    static SharedOnce once;
+    if (!once.allow(kernel, block_smem(64 * kWide))) return cuda_failure();
     kernel<<<ctas, kBlockThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
@@ -579,7 +596,8 @@ template <int kLanes, int kR>
 int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_few_kernel<kLanes, kR>;
     constexpr int smem = kR * kLanes * 16 + kFewThreads / 32 * kR * (kLanes * 16 + 8);
-    if (!allow_shared(kernel, smem)) return cuda_failure();
+    static SharedOnce once;
+    if (!once.allow(kernel, smem)) return cuda_failure();
     kernel<<<ctas, kFewThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
@@ -600,7 +618,8 @@ int join(const PagedArgs& a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_join_kernel<T, kLanes>;
     // The same split of an SM's memory as the kernel before it has: to change it the
     // SM would have to drain.
-    if (!allow_shared(kernel, 0)) return cuda_failure();
+    static SharedOnce once;
+    if (!once.allow(kernel, 0)) return cuda_failure();
     return launch_next(kernel, dim3(ctas, (a.part_rows + join_rows(kLanes) - 1) / join_rows(kLanes)), kJoinThreads, 1, stream, a, ctas);
 }
 

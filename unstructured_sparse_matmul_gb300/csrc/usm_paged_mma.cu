@@ -866,7 +866,8 @@ template <int DP>
 int run(const PagedArgs& a, const Maps& maps, int ctas, cudaStream_t stream) {
     const auto kernel = paged_mma_kernel<DP>;
     constexpr int smem = Sizes<DP>::kControl + (int)sizeof(Control);
-    if (!allow_shared(kernel, smem)) return cuda_failure();
+    static SharedOnce once;
+    if (!once.allow(kernel, smem)) return cuda_failure();
     kernel<<<ctas, kThreads, smem, stream>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
 }
