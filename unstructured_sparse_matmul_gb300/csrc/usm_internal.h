@@ -191,6 +191,21 @@ inline int launch_next(void (*kernel)(P...), dim3 grid, dim3 block, int cluster,
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USM_OK : cuda_failure();
 }
+// The same with dynamic shared memory and no clusters.
+template <class... P, class... A>
+inline int launch_next_shared(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? USM_OK : cuda_failure();
+}
 #ifdef __CUDACC__
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

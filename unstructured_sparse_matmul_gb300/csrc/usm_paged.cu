@@ -131,9 +131,11 @@ constexpr int kInFlight = 4;  // heads whose chunks are loaded before the first 
 // One row's two chunks at a time, kInFlight rows in flight.
 // blockDim: (units, heads walked side by side, tokens).
 template <class T>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
     using C = Chunk<T>;
     constexpr int E = C::E;
+    await_previous();
+    let_next_start();
     const int u = threadIdx.x, step = blockDim.y;
     const int token = blockIdx.x * blockDim.z + threadIdx.z;
     if (token >= a.tokens) return;
@@ -233,7 +235,9 @@ __device__ __forceinline__ void narrow(float x, float* to) { *to = x; }
 __device__ __forceinline__ void narrow(float x, __nv_bfloat16* to) { *to = __float2bfloat16_rn(x); }
 
 template <class T>
-__global__ void __launch_bounds__(kAppendThreads) append_pairs_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) append_pairs_kernel(const __grid_constant__ AppendArgs a) {
+    await_previous();
+    let_next_start();
     const int token = blockIdx.x;
     const Place at = place_of(a, token);
     if (!at.known) return;
@@ -281,8 +285,7 @@ int append(const AppendArgs& a, cudaStream_t stream) {
     // table's rows are read by 16 bytes.
     const bool whole = a.rot == 0 || (a.interleaved ? a.rot % E == 0 && a.rot % 8 == 0 : a.rot % (2 * E) == 0);
     if (!whole) {
-        append_pairs_kernel<T><<<a.tokens, kAppendThreads, 0, stream>>>(a);
-        return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+        return launch_next_shared(append_pairs_kernel<T>, dim3(a.tokens), kAppendThreads, 0, stream, a);
     }
     const int units = (a.head_dim / E + 1) / 2;  // at most 32
     // Heads side by side: few tokens are spread over more threads.
@@ -293,8 +296,7 @@ int append(const AppendArgs& a, cudaStream_t stream) {
     while (side * units > kAppendThreads) side /= 2;
     const int tokens = std::max(1, std::min(64, kAppendThreads / (side * units)));
     const unsigned grid = (unsigned)(((long long)a.tokens + tokens - 1) / tokens);
-    append_kernel<T><<<dim3(grid, 1), dim3(units, side, tokens), 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return launch_next_shared(append_kernel<T>, dim3(grid), dim3(units, side, tokens), 0, stream, a);
 }
 
 }  // namespace

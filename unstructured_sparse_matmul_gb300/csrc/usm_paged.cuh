@@ -140,6 +140,17 @@ struct PagedShares {
         return x;
     }
 
+    // This CTA's share of `sum` units: its first, and how many (`left`).  False for none.
+    __device__ __forceinline__ bool share_of(long long sum, int cta, int ctas, long long& u0) {
+        const int active = (int)min((long long)ctas, sum);
+        if (cta >= active) return false;
+        const long long each = divide(sum, active);
+        const int over = (int)(sum - each * active);  // this many CTAs take one more
+        u0 = each * cta + min(cta, over);
+        left = each + (cta < over ? 1 : 0);
+        return true;
+    }
+
     // scratch: shared, kThreads / 32 + 2 values.  Every warp knows the first
     // segment afterwards.
     __device__ __forceinline__ void init(const PagedArgs& a, int cta, int ctas, long long* scratch) {
@@ -149,6 +160,14 @@ struct PagedShares {
         left = 0;
         b = a.num_seqs;
         block = blocks = head = unit = 0;
+        if (a.num_seqs <= 32) {  // every warp finds its way by itself
+            mine = units_of(a, lane);
+            const long long scan = warp_scan(mine);
+            if (!share_of(__shfl_sync(kFullMask, scan, 31), cta, ctas, u0)) return;  // the same for the whole CTA
+            b = __ffs(__ballot_sync(kFullMask, u0 < scan)) - 1;
+            find(a, u0 - __shfl_sync(kFullMask, scan - mine, b));
+            return;
+        }
         // First the sum over all sequences, then the search for this CTA's share;
         // with up to kThreads sequences every thread still has its own prefix then.
 #pragma unroll 1
@@ -172,13 +191,7 @@ struct PagedShares {
                     scratch[kWarps + 1] = u0 - before;
                 }
             }
-            if (search) break;
-            const int active = (int)min((long long)ctas, sum);
-            if (cta >= active) return;  // the same for the whole CTA
-            const long long each = divide(sum, active);
-            const int over = (int)(sum - each * active);  // this many CTAs take one more
-            u0 = each * cta + min(cta, over);
-            left = each + (cta < over ? 1 : 0);
+            if (!search && !share_of(sum, cta, ctas, u0)) return;
         }
         __syncthreads();
         b = (int)scratch[kWarps];
@@ -211,56 +224,63 @@ struct PagedShares {
         unit = (int)(skip - (long long)head * (k.tiles + kCost));
     }
 
+    // On to the next item; whole warp.
+    __device__ __forceinline__ void advance(const PagedArgs& a) {
+        unit = 0;
+        if (++head < a.kv_heads) return;
+        head = 0;
+        if (++block == blocks) {
+            block = 0;
+            const int lane = threadIdx.x & 31;
+#pragma unroll 1
+            for (++b; b < a.num_seqs; b += 32) {  // past sequences that bring no token
+                const int n = b + lane < a.num_seqs ? paged_seq(a, b + lane).n : 0;
+                const unsigned some = __ballot_sync(kFullMask, n > 0);
+                if (some) {
+                    b += __ffs(some) - 1;
+                    break;
+                }
+            }
+            if (b >= a.num_seqs) {  // the counts changed under the call
+                left = 0;
+                return;
+            }
+            s = paged_seq(a, b);
+            blocks = blocks_of(a, s);
+        }
+        k = paged_block<kRows, kKeys>(a, s, block);
+    }
+
     // The next segment; whole warp.
-    __device__ PagedSegment next(const PagedArgs& a) {
+    __device__ __forceinline__ PagedSegment next(const PagedArgs& a) {
         PagedSegment g;
         g.live = 0;
         g.odd_values = 0;
         while (left > 0) {
+            if (unit == k.tiles + kCost) {
+                advance(a);
+                if (left == 0) break;
+            }
             const int take = (int)min((long long)(k.tiles + kCost - unit), left);
             const int begin = max(unit - kCost, 0), end = unit + take - kCost;
-            if (end > begin) {  // else a share that ends before the item's first tile
-                g.live = 1;
-                g.start = s.start;
-                g.n = s.n;
-                g.len = s.len;
-                g.row0 = block * kRows;
-                g.rows = min(kRows, s.n * a.group - g.row0);
-                g.head = head;
-                g.seq = b;
-                g.lo = k.lo;
-                g.hi = k.hi;
-                g.tile0 = k.tile0 + begin;
-                g.tiles = end - begin;
-                g.ends = end == k.tiles;
-                g.part = begin > 0 ? kPartLater : g.ends ? kPartWhole : kPartFirst;
-            }
             left -= take;
-            unit = 0;
-            if (left > 0 && ++head == a.kv_heads) {
-                head = 0;
-                if (++block == blocks) {
-                    block = 0;
-                    const int lane = threadIdx.x & 31;
-#pragma unroll 1
-                    for (++b; b < a.num_seqs; b += 32) {  // past sequences that bring no token
-                        const int n = b + lane < a.num_seqs ? paged_seq(a, b + lane).n : 0;
-                        const unsigned some = __ballot_sync(kFullMask, n > 0);
-                        if (some) {
-                            b += __ffs(some) - 1;
-                            break;
-                        }
-                    }
-                    if (b >= a.num_seqs) {  // the counts changed under the call
-                        left = 0;
-                        return g;
-                    }
-                    s = paged_seq(a, b);
-                    blocks = blocks_of(a, s);
-                }
-                k = paged_block<kRows, kKeys>(a, s, block);
-            }
-            if (g.live) break;
+            unit += take;
+            if (end <= begin) continue;  // a share that ends before the item's first tile
+            g.live = 1;
+            g.start = s.start;
+            g.n = s.n;
+            g.len = s.len;
+            g.row0 = block * kRows;
+            g.rows = min(kRows, s.n * a.group - g.row0);
+            g.head = head;
+            g.seq = b;
+            g.lo = k.lo;
+            g.hi = k.hi;
+            g.tile0 = k.tile0 + begin;
+            g.tiles = end - begin;
+            g.ends = end == k.tiles;
+            g.part = begin > 0 ? kPartLater : g.ends ? kPartWhole : kPartFirst;
+            break;
         }
         return g;
     }

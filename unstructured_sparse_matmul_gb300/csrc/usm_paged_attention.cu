@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
     extern __shared__ float4 smem_raw[];
     __shared__ long long scratch[kBlockThreads / 32 + 2];
     __shared__ PagedSegment seg;
+    await_previous();
     let_next_start();
     constexpr int kStages = kWide <= 2 ? 2 : 1;
     constexpr int kP = kBlockKeys + 4;
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
     __shared__ int2 sees[kR];
     __shared__ long long scratch[kWarps + 2];
     __shared__ PagedSegment seg;
+    await_previous();
     let_next_start();
     const int D = a.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int side = lane / kLanes, col = 4 * (lane % kLanes);
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
     constexpr int kJoinRows = join_rows(kLanes), kGroups = kJoinThreads / kLanes, kQuads = kLanes == 32 ? 2 : 1, kAhead = 4;
     __shared__ JoinPart shared[kGroups][kLanes];
     await_previous();
+    let_next_start();
     const PagedMeta* meta = static_cast<const PagedMeta*>(a.meta);
     const int c = blockIdx.x, warp_lane = threadIdx.x & 31;
     const int4 begin = __ldcg(reinterpret_cast<const int4*>(meta + c));  // first_live, start, row0, rows
@@ -588,8 +591,7 @@ int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     const int smem = block_smem(a.head_dim);
     static SharedOnce once;
     if (!once.allow(kernel, block_smem(64 * kWide))) return cuda_failure();
-    kernel<<<ctas, kBlockThreads, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return launch_next_shared(kernel, dim3(ctas), kBlockThreads, smem, stream, a);
 }
 
 template <int kLanes, int kR>
@@ -598,8 +600,7 @@ int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
     constexpr int smem = kR * kLanes * 16 + kFewThreads / 32 * kR * (kLanes * 16 + 8);
     static SharedOnce once;
     if (!once.allow(kernel, smem)) return cuda_failure();
-    kernel<<<ctas, kFewThreads, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return launch_next_shared(kernel, dim3(ctas), kFewThreads, smem, stream, a);
 }
 template <int kR>
 int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {

@@ -65,6 +65,7 @@ struct Control {
     float2 stats[128];  // (reference, sum) of the second half's rows
     uint32_t tmem;
     int abort;
+    int joined;  // warps that are done with their joining of a segment's halves, over all segments
 };
 static_assert(Sizes<128>::kControl + sizeof(Control) <= 227 * 1024, "shared memory");
 
@@ -119,6 +120,11 @@ __device__ __forceinline__ bool needs_cleaning(const PagedSegment& g, int key0) 
 __device__ __forceinline__ bool odd_bf16(uint32_t w) {  // an infinity or NaN in either half
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
+__device__ __forceinline__ uint32_t nan_if_odd(uint32_t sum, uint32_t w) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0), "r"(sum));
+    return r;
+}
 __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
@@ -172,6 +178,26 @@ struct Copies {
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&b)) : "memory");
     }
 
+    // Segment `it`'s queries may come: those before are no longer read, and, where
+    // there is a second tile of them, no halves are being joined through it.
+    __device__ __forceinline__ bool room_for_queries(const PagedSegment& g, uint32_t it) {
+        if (it == 0) return true;
+        if (!wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return false;
+        if (g.rows <= 128) return true;
+        const unsigned long long t0 = global_timer_ns();
+        bool ok = true;
+        while (ok && *(volatile int*)&ct->joined < 8 * (int)it) {
+            if (*(volatile int*)&ct->abort) ok = false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *(volatile int*)&ct->abort = 1;
+                record_status(a.status, USM_ERR_TIMEOUT);
+                ok = false;
+            }
+        }
+        __threadfence_block();
+        return __all_sync(kFullMask, ok);
+    }
+
     // The segment's queries, by warps first, first + step, ...; rows past the last
     // group of 32 are left as they are (a row's results depend on nothing else).
     __device__ void queries(const PagedSegment& g, int first, int step) {
@@ -189,39 +215,52 @@ struct Copies {
     }
 
     // Values that must not reach the products: rows outside [lo, hi), which may hold
-    // anything (a weight of 0 does not silence NaN), and, in tiles that not every row
-    // sees, infinities and NaN, which are added at the end where they are seen.
-    // Chunks from, from + step, ... of the tile, four at a time.
-    __device__ __noinline__ static void clean(uint32_t tile, int lo, int hi, bool partly, int chunks, int from, int end, int step, int* found) {
+    // anything (a weight of 0 does not silence NaN), and infinities and NaN in keys
+    // that not every row sees, which are added at the end where they are seen.
+    // Rows begin..end-1 of a tile, by `threads` threads.
+    __device__ __forceinline__ static void zero(uint32_t tile, int begin, int end, int thread, int threads) {
+        const int chunk = thread % kChunks;
+        for (int row = begin + thread / kChunks; row < end; row += threads / kChunks)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(place(tile, row, chunk)), "r"(0) : "memory");
+    }
+    __device__ __forceinline__ static void silence(uint32_t tile, int begin, int end, int thread, int threads, int* found) {
+        const int chunk = thread % kChunks, step = threads / kChunks;
 #pragma unroll 1
-        for (int i = from; i < end; i += 4 * step) {
+        for (int row = begin + thread / kChunks; row < end; row += 4 * step) {
             uint4 w[4];
-            uint32_t at[4];
-            bool in[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) w[u] = row + u * step < end ? lds128(place(tile, row + u * step, chunk)) : make_uint4(0, 0, 0, 0);
+            uint32_t sum = 0;  // x·0 + sum: NaN once some x is one or infinite
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sum = nan_if_odd(nan_if_odd(nan_if_odd(nan_if_odd(sum, w[u].x), w[u].y), w[u].z), w[u].w);
+            if ((sum & 0x7fff7fffu) == 0) continue;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int row = (i + u * step) / kChunks, chunk = (i + u * step) % kChunks;
-                in[u] = row >= lo && row < hi;
-                at[u] = i + u * step < end && chunk < chunks && (partly || !in[u]) ? place(tile, row, chunk) : 0;
-                w[u] = make_uint4(0, 0, 0, 0);
-                if (at[u] && in[u]) w[u] = lds128(at[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (!at[u]) continue;
-                if (in[u]) {
-                    if (!(odd_bf16(w[u].x) || odd_bf16(w[u].y) || odd_bf16(w[u].z) || odd_bf16(w[u].w))) continue;
-                    w[u] = make_uint4(without_odd(w[u].x), without_odd(w[u].y), without_odd(w[u].z), without_odd(w[u].w));
-                    *(volatile int*)found = 1;
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at[u]), "r"(w[u].x), "r"(w[u].y), "r"(w[u].z), "r"(w[u].w)
+                if (!(odd_bf16(w[u].x) || odd_bf16(w[u].y) || odd_bf16(w[u].z) || odd_bf16(w[u].w))) continue;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(tile, row + u * step, chunk)), "r"(without_odd(w[u].x)),
+                             "r"(without_odd(w[u].y)), "r"(without_odd(w[u].z)), "r"(without_odd(w[u].w))
                              : "memory");
+                *(volatile int*)found = 1;
             }
         }
     }
-    __device__ __forceinline__ void clean(const PagedSegment& g, uint32_t stage, int key0, int from, int end, int step) {
-        clean(smem + Z::kStage0 + stage * Z::kTile, g.lo - key0, g.hi - key0, partly_seen(g, key0), (a.head_dim + 7) / 8, from, end, step,
-              const_cast<int*>(&g.odd_values));
+    // Of the tile's rows first..first+count-1; lo, most, least, hi: the edges, from its first key.
+    __device__ __noinline__ static void clean(uint32_t tile, int lo, int most, int least, int hi, int first, int count, int chunks,
+                                              int thread, int threads, int* found) {
+        if (thread % kChunks >= chunks) return;  // columns that no copy wrote
+        const int end = first + count;
+        lo = min(max(lo, first), end);
+        hi = min(max(hi, lo), end);
+        most = min(max(most, lo), hi);
+        least = max(min(least, hi), most);
+        zero(tile, first, lo, thread, threads);
+        zero(tile, hi, end, thread, threads);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) silence(tile, i ? least : lo, i ? hi : most, thread, threads, found);
+    }
+    __device__ __forceinline__ void clean(const PagedSegment& g, uint32_t stage, int key0, int first, int count, int thread, int threads) {
+        clean(smem + Z::kStage0 + stage * Z::kTile, g.lo - key0, (int)min((long long)g.lo_most - key0, 1LL << 30), g.hi_least - key0, g.hi - key0,
+              first, count, (a.head_dim + 7) / 8, thread, threads, const_cast<int*>(&g.odd_values));
         fence_proxy_async_smem();
     }
 
@@ -305,7 +344,7 @@ struct Copies {
             const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
-            if (!g.live || (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status))) return;
+            if (!g.live || !room_for_queries(g, it)) return;
             queries(g, warp & 1, 2);
             arrive_warp(ct->seg_empty[slot]);
         }
@@ -329,7 +368,7 @@ struct Copies {
                 if (!wait(ct->started[stage], startings >> stage & 1, ct, a.status)) return;
                 startings ^= 1u << stage;
                 if (!wait(ct->full[stage], i / Z::kStages & 1, ct, a.status)) return;
-                clean(g, stage, key0, (int)(threadIdx.x & 63), 128 * kChunks, 64);
+                clean(g, stage, key0, 0, kKeys, threadIdx.x & 63, 64);
                 arrive_warp(ct->cleaned[stage]);
             }
             load += 2 * n;
@@ -356,7 +395,7 @@ struct Copies {
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const int n = g.tiles, key0 = g.tile0 * kKeys;
-            if (it > 0 && !wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return;
+            if (!room_for_queries(g, it)) return;
             queries(g, warp, 4);
             const char* next = key_row(g, 0);
 #pragma unroll 1
@@ -370,7 +409,7 @@ struct Copies {
                 if (values && partly_seen(g, at)) {
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     __syncwarp();  // this warp's rows alone
-                    clean(g, stage, at, 32 * warp * kChunks + lane, 32 * (warp + 1) * kChunks, 32);
+                    clean(g, stage, at, 32 * warp, 32, lane, 32);
                     mbar_arrive(smem_addr(&ct->full[stage]));
                 } else {
                     complete_on(ct->full[stage]);
@@ -521,7 +560,9 @@ struct Softmax {
     uint32_t s_col, o_col;   // this warp's lanes of tensor memory
     uint32_t s_uses = 0, o_uses = 0, box_uses = 0;
     // Of the current segment:
-    float m, l;  // reference (a score) and sum of the weights
+    float m, l;      // reference (a score) and sum of the weights
+    float mc;        // what an exponent subtracts
+    bool far;        // some row of the warp is far from zero
     int2 seen;
 
     __device__ Softmax(const PagedArgs& a, Control* ct, uint32_t smem, uint32_t tmem) : a(a), ct(ct), smem(smem) {
@@ -563,13 +604,13 @@ struct Softmax {
             const float f = raise ? exp2_fast((m - to) * c) : 1.f;
             m = to;
             l *= f;
+            mc = m == -INFINITY ? 0.f : m * c;
+            far = __any_sync(kFullMask, !(fabsf(mc) <= kNear));
+            if (far) mc = 0.f;
             if (!first) rescale(f);
         }
-        float mc = m == -INFINITY ? 0.f : m * c;
-        if (__any_sync(kFullMask, !(fabsf(mc) <= kNear))) {
-            // Far from zero the difference is formed first: it is exact near m.
+        if (far) {  // the difference is formed first: it is exact near m
             const float base = m == -INFINITY ? 0.f : m;
-            mc = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -627,6 +668,8 @@ struct Softmax {
                 if (!partly_seen(g, key0)) continue;
 #pragma unroll 1
                 for (int key = max(key0, seen.x); key < min(key0 + kKeys, seen.y); ++key) {
+                    if (key >= g.lo_most && key < g.hi_least) key = min(key0 + kKeys, g.hi_least);  // seen by all: left in place
+                    if (key >= min(key0 + kKeys, seen.y)) break;
                     const int2 at = paged_slot(a, g.seq, key);
                     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + at.x * a.v_page + at.y * a.v_slot + g.head * a.v_head + j;
 #pragma unroll
@@ -648,7 +691,9 @@ struct Softmax {
     __device__ __forceinline__ bool write(const PagedSegment& g, int row, bool both) {
         const bool mine = row < g.rows, whole = g.part == kPartWhole;
         const bool some = __any_sync(kFullMask, mine);
-        const uint32_t box = smem + Z::kTile + 4 * tid;  // [32 columns][128 rows]
+        // [columns][rows], as many columns at a time as the box has room for.
+        const int lanes = (min(g.rows, 128) + 31) / 32 * 32, wide = max(Z::kTile / 4 / lanes / 32, 1) * 32;
+        const uint32_t box = smem + Z::kTile + 4 * tid;
         const int flat = g.row0 + row, token = flat / a.group;
         const long long part = (2LL * blockIdx.x + g.part) * a.part_rows + row;
         char* to = whole ? static_cast<char*>(a.out) + 2 * ((g.start + token) * a.out_token + (g.head * a.group + flat - token * a.group) * a.out_head)
@@ -661,19 +706,23 @@ struct Softmax {
                 tmem_ld32(o_col + j, w);
                 tmem_wait_ld(w);
             }
+            const uint32_t at = box + (uint32_t)(j % wide) * lanes * 4;
+            const bool last = (j + 32) % wide == 0 || j + 32 >= a.head_dim;
             if (both) {
-                const uint32_t use = box_uses++;
                 if (half == 1) {
-                    if (use > 0 && !wait(ct->box_free, (use - 1) & 1, ct, a.status)) return false;
+                    if (j % wide == 0 && box_uses > 0 && !wait(ct->box_free, (box_uses - 1) & 1, ct, a.status)) return false;
                     if (j == 0) ct->stats[tid] = make_float2(m, l);
                     if (some)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(box + 512 * i), "r"(w[i]) : "memory");
-                    arrive_warp(ct->box_full);
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i * lanes * 4), "r"(w[i]) : "memory");
+                    if (last) {
+                        arrive_warp(ct->box_full);
+                        ++box_uses;
+                    }
                     continue;
                 }
-                if (!wait(ct->box_full, use & 1, ct, a.status)) return false;
+                if (j % wide == 0 && !wait(ct->box_full, box_uses & 1, ct, a.status)) return false;
             }
             if (j == 0) {
                 if (both) {
@@ -692,12 +741,15 @@ struct Softmax {
                 if (both)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(__uint_as_float(w[i]) * f0 + __uint_as_float(lds32(box + 512 * i)) * f1);
+                        w[i] = __float_as_uint(__uint_as_float(w[i]) * f0 + __uint_as_float(lds32(at + i * lanes * 4)) * f1);
                 else
 #pragma unroll
                     for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f0);
             }
-            if (both) arrive_warp(ct->box_free);
+            if (both && last) {
+                arrive_warp(ct->box_free);
+                ++box_uses;
+            }
             if (!mine) continue;
             const int left = a.head_dim - j;  // a multiple of 8
             if (whole && a.out32) {
@@ -744,9 +796,9 @@ struct Softmax {
             if (row < g.rows && seen.x >= seen.y) lo = 0x7fffffff;
             lo = __reduce_max_sync(kFullMask, lo);
             hi = __reduce_min_sync(kFullMask, hi);
-            if (!shared) arrive_warp(ct->q_empty);
             m = -INFINITY;
-            l = 0.f;
+            l = mc = 0.f;
+            far = false;
             const int first = shared ? half : 0, step = shared ? 2 : 1, tiles = g.tiles, tile0 = g.tile0;
 #pragma unroll 1
             for (int t = first; t < tiles; t += step) {
@@ -764,7 +816,11 @@ struct Softmax {
                 if (!write(g, row, shared && tiles > 1)) return;
             }
             tmem_fence_before_sync();
-            if (shared) arrive_warp(ct->q_empty);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) {
+                __threadfence_block();
+                atomicAdd(&ct->joined, 1);
+            }
             arrive_warp(ct->seg_empty[slot]);
         }
     }
@@ -780,7 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
     extern __shared__ __align__(1024) unsigned char smem[];
     Control* ct = reinterpret_cast<Control*>(smem + Z::kControl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    let_next_start();
     if (threadIdx.x == 0) {
         for (int i = 0; i < Z::kStages; ++i) {
             mbar_init(smem_addr(&ct->full[i]), a.boxes ? 1 : 128);
@@ -789,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
             mbar_init(smem_addr(&ct->cleaned[i]), 2);
         }
         mbar_init(smem_addr(&ct->q_full), a.boxes ? 64 : 128);
-        mbar_init(smem_addr(&ct->q_empty), 1 + 8);
+        mbar_init(smem_addr(&ct->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ct->s_full[i]), 1);
             mbar_init(smem_addr(&ct->p_full[i]), 4);
@@ -802,10 +857,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
         mbar_init(smem_addr(&ct->box_full), 4);
         mbar_init(smem_addr(&ct->box_free), 4);
         mbar_init(smem_addr(&ct->drained), 1);
-        ct->abort = 0;
+        ct->abort = ct->joined = 0;
         fence_barrier_init();
     }
     if (warp == 12) tmem_alloc(smem_addr(&ct->tmem), 512);
+    await_previous();  // nothing of the caller's is read or written before
+    let_next_start();
     Shares shares;
     shares.init(a, blockIdx.x, gridDim.x, ct->scratch);
     tmem_fence_before_sync();
@@ -868,8 +925,7 @@ int run(const PagedArgs& a, const Maps& maps, int ctas, cudaStream_t stream) {
     constexpr int smem = Sizes<DP>::kControl + (int)sizeof(Control);
     static SharedOnce once;
     if (!once.allow(kernel, smem)) return cuda_failure();
-    kernel<<<ctas, kThreads, smem, stream>>>(a, maps);
-    return cudaGetLastError() == cudaSuccess ? USM_OK : USM_ERR_CUDA;
+    return launch_next_shared(kernel, dim3(ctas), kThreads, smem, stream, a, maps);
 }
 
 bool encode(CUtensorMap* map, const PagedArgs& a, const void* base, long long page, long long slot, long long head) {
