@@ -10,7 +10,8 @@
 //   O += P·V     P from tensor memory, V from shared memory, fp32 in tensor memory.
 // While one half's softmax runs the tensor cores work for the other.  Where a
 // block has no more than 128 rows (single tokens, drafts) the halves take the
-// same rows over alternate tiles, and their sums are joined at the end.
+// same rows over alternate tiles (on from one segment to the next), and the half
+// that is done first leaves its sums to the other and goes on.
 //
 // The reference m of a row is its maximum, but it is raised only when a tile's
 // maximum passes it by more than 2^8 in the weights: fp32 sums and bf16 weights keep
@@ -62,7 +63,7 @@ struct Control {
     unsigned long long drained;
     long long scratch[kThreads / 32 + 2];
     PagedSegment seg[kRing];
-    float2 stats[128];  // (reference, sum) of the second half's rows
+    float2 stats[128];  // (reference, sum) of the rows that one half leaves to the other
     uint32_t tmem;
     int abort;
     int joined;  // warps that are done with their joining of a segment's halves, over all segments
@@ -437,8 +438,9 @@ struct Products {
     uint32_t smem, tmem;
     uint32_t qk_shape, pv_shape;
     int steps;
-    uint32_t p_uses[2] = {0, 0};
+    uint32_t weighed = 0;    // parity of each half's weights
     uint32_t cleanings = 0;  // parity of each stage's
+    int turn = 0;            // the half that takes the next tile of shared rows
 
     __device__ Products(const PagedArgs& a, Control* ct, uint32_t smem, uint32_t tmem) : a(a), ct(ct), smem(smem), tmem(tmem) {
         steps = (a.head_dim + 15) / 16;
@@ -468,7 +470,7 @@ struct Products {
     __device__ __forceinline__ void release(uint32_t load) { commit(ct->empty[load % Z::kStages]); }
 
     __device__ __forceinline__ void scores(int half, int q_half, uint32_t load) {
-        const uint64_t q = swizzled_desc(smem + q_half * Z::kTile, 0), k = swizzled_desc(stage(load), 0);
+        const uint32_t q = swizzled_desc(smem + q_half * Z::kTile, 0), k = swizzled_desc(stage(load), 0);
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
             if (i >= steps) break;
@@ -478,9 +480,10 @@ struct Products {
         commit(ct->s_full[half]);
     }
     __device__ __forceinline__ bool weigh(int half, uint32_t load, bool accumulate) {
-        if (!await(ct->p_full[half], p_uses[half]++ & 1)) return false;
+        if (!await(ct->p_full[half], weighed >> half & 1)) return false;
+        weighed ^= 1u << half;
         tmem_fence_after_sync();
-        const uint64_t v = swizzled_desc(stage(load), 16384);
+        const uint32_t v = swizzled_desc(stage(load), 16384);
 #pragma unroll
         for (int i = 0; i < kKeys / 16; ++i)
             mma_bf16_ts(tmem + 256 + half * DP, tmem + half * kKeys + i * 8, v + (i * 2048 >> 4), pv_shape, accumulate || i > 0);
@@ -499,12 +502,12 @@ struct Products {
             if (!await(ct->q_full, it & 1)) return;
             fence_proxy_async_smem();
             if (!loaded(k_load(base, 0))) return;
-            scores(0, 0, k_load(base, 0));
+            scores(shared ? turn : 0, 0, k_load(base, 0));
             if (!shared) scores(1, 1, k_load(base, 0));
             release(k_load(base, 0));
             if (shared && n > 1) {
                 if (!loaded(k_load(base, 1))) return;
-                scores(1, 0, k_load(base, 1));
+                scores(turn ^ 1, 0, k_load(base, 1));
                 release(k_load(base, 1));
             }
             const int ahead = shared ? 2 : 1;  // tiles whose scores are formed before the sums of tile t
@@ -514,7 +517,7 @@ struct Products {
                 const bool more = t + ahead < n;
                 if (!values_loaded(g, t, v) || (more && !loaded(k))) return;
                 if (shared) {
-                    const int half = t & 1;
+                    const int half = (t & 1) ^ turn;
                     if (!weigh(half, v, t >= 2)) return;
                     release(v);
                     if (more) scores(half, 0, k);
@@ -532,6 +535,7 @@ struct Products {
                 if (more && t + ahead == n - 1) commit(ct->q_empty);
             }
             base += 2 * n;
+            if (shared) turn ^= n & 1;
             mbar_arrive(smem_addr(&ct->seg_empty[slot]));
         }
     }
@@ -558,12 +562,19 @@ struct Softmax {
     uint32_t smem;
     int half, tid;           // thread of the half
     uint32_t s_col, o_col;   // this warp's lanes of tensor memory
-    uint32_t s_uses = 0, o_uses = 0, box_uses = 0;
+    // Parities of this half's waits for scores and for sums and of the halves'
+    // exchange, whether there was one yet, and the half that takes the next tile of
+    // shared rows.
+    uint32_t state = 0;
+    static constexpr uint32_t kScores = 1, kSums = 2, kBox = 4, kBoxUsed = 8, kTurn = 16, kFailed = 32;
+    __device__ __forceinline__ uint32_t flip(uint32_t bit) {  // its old value
+        state ^= bit;
+        return (state & bit) ? 0 : 1;
+    }
     // Of the current segment:
     float m, l;      // reference (a score) and sum of the weights
     float mc;        // what an exponent subtracts
     bool far;        // some row of the warp is far from zero
-    int2 seen;
 
     __device__ Softmax(const PagedArgs& a, Control* ct, uint32_t smem, uint32_t tmem) : a(a), ct(ct), smem(smem) {
         half = threadIdx.x >> 7;
@@ -573,8 +584,11 @@ struct Softmax {
         o_col = tmem + lanes + 256 + half * DP;
     }
 
-    // One tile's scores into weights.  `first`: O holds nothing yet.
-    __device__ __forceinline__ void weights(int key0, bool masked, bool first) {
+    // Row of the segment's block that this thread has.
+    __device__ __forceinline__ int row_of(const PagedSegment& g) const { return g.rows <= 128 ? tid : half * 128 + tid; }
+
+    // Tile t0's scores into weights.  `first`: O holds nothing yet.
+    __device__ __forceinline__ void weights(const PagedSegment& g, int t0, bool masked, bool first) {
         uint32_t w[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, w[i]);
@@ -582,7 +596,8 @@ struct Softmax {
         for (int i = 0; i < 4; ++i) tmem_wait_ld(w[i]);
         const float c = a.scale_log2;
         if (masked) {
-            const unsigned from = (unsigned)(seen.x - key0), count = (unsigned)(seen.y - seen.x);
+            const int2 seen = paged_seen(a, g, row_of(g));
+            const unsigned from = (unsigned)(seen.x - (g.tile0 + t0) * kKeys), count = (unsigned)(seen.y - seen.x);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -685,15 +700,19 @@ struct Softmax {
         tmem_wait_st();
     }
 
-    // A row's sums, 32 columns at a time: those of the two halves joined where they
-    // took the same rows (through the queries' second tile, which is free then),
-    // divided, and written to the output or to the partial results.
-    __device__ __forceinline__ bool write(const PagedSegment& g, int row, bool both) {
+    // A row's sums, 32 columns at a time: divided, and written to the output or to
+    // the partial results.  Where the halves took the same rows (`both`) the one that
+    // had the last tile (`last`) first adds the other's, which come through the
+    // queries' second tile (free then): [row][columns], as many columns at a time as
+    // there is room for, 16-byte chunks swizzled by the row.
+    // Returns the new state, kFailed where a wait gave up.
+    __device__ __forceinline__ static uint32_t write(const PagedArgs& a, Control* ct, const PagedSegment& g, uint32_t smem, uint32_t o_col, int row,
+                                                  float m, float l, bool both, bool last, uint32_t state) {
+        const int tid = threadIdx.x & 127;
         const bool mine = row < g.rows, whole = g.part == kPartWhole;
         const bool some = __any_sync(kFullMask, mine);
-        // [columns][rows], as many columns at a time as the box has room for.
         const int lanes = (min(g.rows, 128) + 31) / 32 * 32, wide = max(Z::kTile / 4 / lanes / 32, 1) * 32;
-        const uint32_t box = smem + Z::kTile + 4 * tid;
+        const uint32_t box = smem + Z::kTile + tid * wide * 4;
         const int flat = g.row0 + row, token = flat / a.group;
         const long long part = (2LL * blockIdx.x + g.part) * a.part_rows + row;
         char* to = whole ? static_cast<char*>(a.out) + 2 * ((g.start + token) * a.out_token + (g.head * a.group + flat - token * a.group) * a.out_head)
@@ -706,24 +725,24 @@ struct Softmax {
                 tmem_ld32(o_col + j, w);
                 tmem_wait_ld(w);
             }
-            const uint32_t at = box + (uint32_t)(j % wide) * lanes * 4;
-            const bool last = (j + 32) % wide == 0 || j + 32 >= a.head_dim;
-            if (both) {
-                if (half == 1) {
-                    if (j % wide == 0 && box_uses > 0 && !wait(ct->box_free, (box_uses - 1) & 1, ct, a.status)) return false;
-                    if (j == 0) ct->stats[tid] = make_float2(m, l);
-                    if (some)
+            const uint32_t at = box + (uint32_t)(j % wide) * 4;
+            const bool begins = j % wide == 0, ends = (j + 32) % wide == 0 || j + 32 >= a.head_dim;
+            if (both && !last) {
+                if (begins && (state & kBoxUsed) && !wait(ct->box_free, (state & kBox) ? 0 : 1, ct, a.status)) return kFailed;
+                if (j == 0) ct->stats[tid] = make_float2(m, l);
+                if (some)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i * lanes * 4), "r"(w[i]) : "memory");
-                    if (last) {
-                        arrive_warp(ct->box_full);
-                        ++box_uses;
-                    }
-                    continue;
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((i ^ (tid & 7)) << 4)), "r"(w[4 * i]),
+                                     "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                                     : "memory");
+                if (ends) {
+                    arrive_warp(ct->box_full);
+                    state = (state ^ kBox) | kBoxUsed;
                 }
-                if (j % wide == 0 && !wait(ct->box_full, box_uses & 1, ct, a.status)) return false;
+                continue;
             }
+            if (both && begins && !wait(ct->box_full, (state & kBox) ? 1 : 0, ct, a.status)) return kFailed;
             if (j == 0) {
                 if (both) {
                     const float2 other = ct->stats[tid];
@@ -738,17 +757,21 @@ struct Softmax {
                 f1 *= z;
             }
             if (some) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f0);
                 if (both)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(__uint_as_float(w[i]) * f0 + __uint_as_float(lds32(at + i * lanes * 4)) * f1);
-                else
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f0);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 y = lds128(at + ((i ^ (tid & 7)) << 4));
+                        w[4 * i] = __float_as_uint(fmaf(__uint_as_float(y.x), f1, __uint_as_float(w[4 * i])));
+                        w[4 * i + 1] = __float_as_uint(fmaf(__uint_as_float(y.y), f1, __uint_as_float(w[4 * i + 1])));
+                        w[4 * i + 2] = __float_as_uint(fmaf(__uint_as_float(y.z), f1, __uint_as_float(w[4 * i + 2])));
+                        w[4 * i + 3] = __float_as_uint(fmaf(__uint_as_float(y.w), f1, __uint_as_float(w[4 * i + 3])));
+                    }
             }
-            if (both && last) {
+            if (both && ends) {
                 arrive_warp(ct->box_free);
-                ++box_uses;
+                state = (state ^ kBox) | kBoxUsed;
             }
             if (!mine) continue;
             const int left = a.head_dim - j;  // a multiple of 8
@@ -776,9 +799,8 @@ struct Softmax {
                     if (4 * i < left) store16(to + 4 * j + 16 * i, w + 4 * i);
             }
         }
-        if (!whole && mine && (!both || half == 0))
-            *reinterpret_cast<float2*>(a.part_stats + 2 * part) = make_float2(m, l);
-        return true;
+        if (!whole && mine && (!both || last)) *reinterpret_cast<float2*>(a.part_stats + 2 * part) = make_float2(m, l);
+        return state;
     }
 
     __device__ void run() {
@@ -787,34 +809,40 @@ struct Softmax {
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
-            const bool shared = g.rows <= 128;
-            const int row = shared ? tid : half * 128 + tid;
-            const bool some = __any_sync(kFullMask, row < g.rows);
-            seen = paged_seen(a, g, row);
-            // Keys that every row of this warp sees.
-            int lo = row < g.rows ? seen.x : 0, hi = row < g.rows ? seen.y : 0x7fffffff;
-            if (row < g.rows && seen.x >= seen.y) lo = 0x7fffffff;
-            lo = __reduce_max_sync(kFullMask, lo);
-            hi = __reduce_min_sync(kFullMask, hi);
+            const bool some = __any_sync(kFullMask, row_of(g) < g.rows);
+            // Tiles that every row of this warp sees whole: whole.x <= t < whole.y.
+            int2 whole;
+            {
+                const int row = row_of(g);
+                const int2 seen = paged_seen(a, g, row);
+                int lo = row < g.rows ? seen.x : 0, hi = row < g.rows ? seen.y : 0x7fffffff;
+                if (row < g.rows && seen.x >= seen.y) hi = 0;
+                lo = __reduce_max_sync(kFullMask, lo);
+                hi = __reduce_min_sync(kFullMask, hi);
+                whole = make_int2((lo + kKeys - 1) / kKeys - g.tile0, hi / kKeys - g.tile0);
+            }
             m = -INFINITY;
             l = mc = 0.f;
             far = false;
-            const int first = shared ? half : 0, step = shared ? 2 : 1, tiles = g.tiles, tile0 = g.tile0;
+            const int first = g.rows <= 128 ? half ^ (state & kTurn ? 1 : 0) : 0, tiles = g.tiles;
 #pragma unroll 1
-            for (int t = first; t < tiles; t += step) {
-                if (!wait(ct->s_full[half], s_uses++ & 1, ct, a.status)) return;
+            for (int t = first; t < tiles; t += g.rows <= 128 ? 2 : 1) {
+                if (!wait(ct->s_full[half], flip(kScores), ct, a.status)) return;
                 tmem_fence_after_sync();
-                const int key0 = (tile0 + t) * kKeys;
-                if (some) weights(key0, key0 < lo || key0 + kKeys > hi, t == first);
+                if (some) weights(g, t, t < whole.x || t >= whole.y, t == first);
                 tmem_fence_before_sync();
                 arrive_warp(ct->p_full[half]);
             }
-            if (first < tiles) {  // not so for the second half of a single tile
-                if (!wait(ct->o_full[half], o_uses++ & 1, ct, a.status)) return;
+            if (first < tiles) {  // not so for one half of a single tile
+                if (!wait(ct->o_full[half], flip(kSums), ct, a.status)) return;
                 tmem_fence_after_sync();
-                if (some && *(volatile int*)&ct->seg[slot].odd_values) add_odd(a, g, o_col, seen, first, step);
-                if (!write(g, row, shared && tiles > 1)) return;
+                const bool shared = g.rows <= 128;
+                if (some && *(volatile int*)&ct->seg[slot].odd_values)
+                    add_odd(a, g, o_col, paged_seen(a, g, row_of(g)), first, shared ? 2 : 1);
+                state = write(a, ct, g, smem, o_col, row_of(g), m, l, shared && tiles > 1, !shared || ((tiles - 1 - first) & 1) == 0, state);
+                if (state & kFailed) return;
             }
+            if (g.rows <= 128 && (tiles & 1)) state ^= kTurn;
             tmem_fence_before_sync();
             __syncwarp();
             if ((threadIdx.x & 31) == 0) {

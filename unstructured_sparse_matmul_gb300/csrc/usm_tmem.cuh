@@ -58,10 +58,11 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // chunk c of row r at chunk c ^ (r mod 8); eight rows are 1024 bytes, 1024-byte
 // aligned).  `lbo`: bytes between 64-column panels where the rows run along the
 // product's inner dimension; 0 where they run along the outer one.
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo ? lbo >> 4 : 1) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The lower half of its descriptor; the upper half is the same for all.
+__device__ __forceinline__ uint32_t swizzled_desc(uint32_t saddr, uint32_t lbo) {
+    return ((saddr & 0x3FFFFu) >> 4) | (lbo ? lbo >> 4 : 1) << 16;
 }
+constexpr uint32_t kSwizzledDescUpper = (1024 >> 4) | 1u << 14 | 2u << 29;  // 8 rows, version, 128-byte swizzle
 // bf16 x bf16 -> fp32, 128 rows, n columns (a multiple of 16); b_rows_inner: B's
 // rows run along the inner dimension.
 __device__ __forceinline__ uint32_t bf16_mma_shape(int n, bool b_rows_inner) {
@@ -69,19 +70,21 @@ __device__ __forceinline__ uint32_t bf16_mma_shape(int n, bool b_rows_inner) {
 }
 // D (tensor memory) = A·B, + D with `accumulate`; 16 of the inner dimension.  One
 // thread issues it.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool accumulate) {
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kSwizzledDescUpper)
         : "memory");
 }
 // The same with A in tensor memory (two bf16 a column).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool accumulate) {
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kSwizzledDescUpper)
         : "memory");
 }
 
