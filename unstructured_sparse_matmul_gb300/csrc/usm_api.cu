@@ -637,6 +637,11 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     a.num_pages = c.num_pages, a.page_size = c.page_size, a.capacity = capacity_of(c);
     a.num_seqs = c.num_seqs, a.tokens = tokens, a.per_seq = tokens / c.num_seqs;
     a.kv_heads = c.kv_heads, a.group = q_heads / c.kv_heads, a.head_dim = c.head_dim;
+    // ceil(2^shift / group) with 2^(shift - 31) the next power of two: its error, times
+    // any x below 2^31, stays below 2^shift, so the quotients are exact.
+    a.group_shift = 31;
+    while ((1LL << (a.group_shift - 31)) < a.group) ++a.group_shift;
+    a.group_mul = (uint32_t)(((1ULL << a.group_shift) + a.group - 1) / a.group);
     // A scale of 0 weighs all keys alike, as does the smallest normal number; it
     // keeps masked scores at -inf.
     a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1.17549435e-38f);

@@ -94,13 +94,15 @@ struct PagedArgs {
     int capacity;          // positions that the table has room for
     int num_seqs, tokens, per_seq;
     int kv_heads, group, head_dim;
+    uint32_t group_mul;    // x / group = x·group_mul >> group_shift for 0 <= x < 2^31
+    int group_shift;
     float scale_log2;      // scale·log2 e
     int causal, window;
     int table_pages;       // entries of a sequence's row of the table
     int out32;             // rows of the output are 32-byte aligned and that much at least
     int boxes;             // keys and values come by TMA, a box of a page's slots at a time
     int part_rows;         // rows of a partial result
-    float* parts;          // [2·ctas][part_rows][head_dim], then [2·ctas][part_rows][2]
+    float* parts;          // [2·ctas][head_dim / 4][part_rows][4], then [2·ctas][part_rows][2]
     float* part_stats;     // (reference, sum) of each row
     void* meta;            // PagedMeta[ctas]
     int* status;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "usm_args.h"
@@ -30,6 +31,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     return s;
 }
 
+// x / group, for 0 <= x < 2^31.
+__device__ __forceinline__ int by_group(const PagedArgs& a, int x) {
+    return (int)((unsigned long long)x * a.group_mul >> a.group_shift);
+}
+
 // Rows of attention: new token i of a sequence gives `group` rows for a head of
 // keys, i·group + g, one for each query head that reads it.  A block is kRows of
 // a sequence's rows; an item is a block with one head of keys; a unit is one tile
@@ -39,19 +45,26 @@ struct PagedBlock {
     int tile0, tiles;
 };
 
+// (A call, by value: in line, in the half dozen places that need it, it is code
+// that every launch fetches for the first time.)
 template <int kRows, int kKeys>
-__device__ __forceinline__ PagedBlock paged_block(const PagedArgs& a, const PagedSeq& s, int block) {
-    const int rows = s.n * a.group;
+__device__ __noinline__ PagedBlock paged_block_call(uint32_t group_mul, int group_shift, int causal, int window, int keys, int rows,
+                                                    int position, int block) {
     const int first = block * kRows, last = min(rows, first + kRows) - 1;
-    const int p0 = s.len - s.n + first / a.group, p1 = s.len - s.n + last / a.group;
-    const int keys = min(s.len, a.capacity);
+    const int p0 = position + (int)((unsigned long long)first * group_mul >> group_shift);
+    const int p1 = position + (int)((unsigned long long)last * group_mul >> group_shift);
     PagedBlock k;
-    k.hi = a.causal ? min(keys, max(p1 + 1, 0)) : keys;
-    k.lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+    k.hi = causal ? min(keys, max(p1 + 1, 0)) : keys;
+    k.lo = window > 0 ? max(p0 - window + 1, 0) : 0;
     if (k.lo >= k.hi) k.lo = k.hi = 0;
     k.tile0 = k.lo / kKeys;
     k.tiles = max((k.hi + kKeys - 1) / kKeys - k.tile0, 1);  // one for a block that sees nothing: it writes zeros
     return k;
+}
+template <int kRows, int kKeys>
+__device__ __forceinline__ PagedBlock paged_block(const PagedArgs& a, const PagedSeq& s, int block) {
+    return paged_block_call<kRows, kKeys>(a.group_mul, a.group_shift, a.causal, a.window, min(s.len, a.capacity), s.n * a.group,
+                                          s.len - s.n, block);
 }
 
 // A CTA's run of tiles of one item.
@@ -72,11 +85,11 @@ constexpr int kPartWhole = -1, kPartLater = 0, kPartFirst = 1;
 
 // What a CTA tells the joining kernel: an item begun in slot kPartFirst goes on
 // in the next CTAs' slots kPartLater up to the one with `ends`.
-struct PagedMeta {
-    int first_live;         // slot kPartFirst is in use, for this block and head:
-    int start, row0, rows, head;
-    int later_live, ends;   // slot kPartLater is in use, and ends its item
-    int pad;
+struct alignas(16) PagedMeta {  // read in a piece of 16 bytes and one of 8
+    int first_live;        // slot kPartFirst is in use, for this block and head:
+    int start, row0, rows;
+    int later_live, ends;  // slot kPartLater is in use, and ends its item
+    int head, pad;
 };
 
 // The CTAs take equal shares of all units in the order (sequence, block, head,
@@ -96,7 +109,7 @@ struct PagedShares {
 
     // Units of sequence b (0 past the last), for the calling lane; the whole warp
     // takes part where a sequence has many blocks.
-    __device__ static long long units_of(const PagedArgs& a, int b) {
+    __device__ __forceinline__ static long long units_of(const PagedArgs& a, int b) {
         PagedSeq s{0, 0, 0};
         if (b < a.num_seqs) s = paged_seq(a, b);
         const int blocks = blocks_of(a, s);
@@ -151,8 +164,41 @@ struct PagedShares {
         return true;
     }
 
-    // scratch: shared, kThreads / 32 + 2 values.  Every warp knows the first
-    // segment afterwards.
+    // By one warp, for up to kSolo sequences.
+    static constexpr int kSolo = 128;
+    __device__ __forceinline__ void init_solo(const PagedArgs& a, int cta, int ctas) {
+        long long u0 = 0, sum = 0;
+        left = 0;
+        b = a.num_seqs;
+        block = blocks = head = unit = 0;
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (int search = 0; search < 2; ++search) {
+            sum = 0;
+#pragma unroll 1
+            for (int at = 0; at < a.num_seqs; at += 32) {
+                const long long mine = units_of(a, at + lane), scan = sum + warp_scan(mine);
+                const unsigned here = __ballot_sync(kFullMask, u0 < scan);
+                if (search && here) {
+                    const int from = __ffs(here) - 1;
+                    b = at + from;
+                    find(a, u0 - __shfl_sync(kFullMask, scan - mine, from));
+                    return;
+                }
+                sum = __shfl_sync(kFullMask, scan, 31);
+                if (a.num_seqs <= 32 && share_of(sum, cta, ctas, u0)) {  // found in one go
+                    const int from = __ffs(__ballot_sync(kFullMask, u0 < scan)) - 1;
+                    b = from;
+                    find(a, u0 - __shfl_sync(kFullMask, scan - mine, from));
+                    return;
+                }
+            }
+            if (search || !share_of(sum, cta, ctas, u0)) return;
+        }
+    }
+
+    // By all threads, for any number.  scratch: shared, kThreads / 32 + 2 values.
+    // Every warp knows the first segment afterwards.
     __device__ __forceinline__ void init(const PagedArgs& a, int cta, int ctas, long long* scratch) {
         constexpr int kWarps = kThreads / 32;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -160,14 +206,6 @@ struct PagedShares {
         left = 0;
         b = a.num_seqs;
         block = blocks = head = unit = 0;
-        if (a.num_seqs <= 32) {  // every warp finds its way by itself
-            mine = units_of(a, lane);
-            const long long scan = warp_scan(mine);
-            if (!share_of(__shfl_sync(kFullMask, scan, 31), cta, ctas, u0)) return;  // the same for the whole CTA
-            b = __ffs(__ballot_sync(kFullMask, u0 < scan)) - 1;
-            find(a, u0 - __shfl_sync(kFullMask, scan - mine, b));
-            return;
-        }
         // First the sum over all sequences, then the search for this CTA's share;
         // with up to kThreads sequences every thread still has its own prefix then.
 #pragma unroll 1
@@ -200,7 +238,7 @@ struct PagedShares {
 
     // The block, head and tile `skip` units behind sequence b's first; every warp
     // searches for itself.
-    __device__ void find(const PagedArgs& a, long long skip) {
+    __device__ __forceinline__ void find(const PagedArgs& a, long long skip) {
         s = paged_seq(a, b);
         blocks = blocks_of(a, s);
         const int lane = threadIdx.x & 31;
@@ -289,12 +327,14 @@ struct PagedShares {
 // Keys [lo, hi) that one row of a segment sees; empty for rows past its last.
 __device__ __forceinline__ int2 paged_seen(const PagedArgs& a, const PagedSegment& g, int row) {
     if (row >= g.rows) return make_int2(0, 0);
-    const int p = g.len - g.n + (g.row0 + row) / a.group;
+    const int p = g.len - g.n + by_group(a, g.row0 + row);
     const int keys = min(g.len, a.capacity);
     const int hi = a.causal ? min(keys, max(p + 1, 0)) : keys;
     const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
     return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
+
+static_assert(offsetof(PagedMeta, later_live) == 16 && sizeof(PagedMeta) == 32, "read as int4 and int2");
 
 // Notes a segment with a partial result in the CTA's message to the join.
 __device__ __forceinline__ void paged_note(PagedMeta& m, const PagedSegment& g) {

@@ -40,12 +40,12 @@ __device__ __forceinline__ float weight_of(float m, float top, float scale_log2)
 // Query row `row` of a segment, and its row of the output.
 template <class T>
 __device__ __forceinline__ const T* query_of(const PagedArgs& a, const PagedSegment& g, int row) {
-    const int flat = g.row0 + row, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
+    const int flat = g.row0 + row, token = by_group(a, flat), head = g.head * a.group + flat - token * a.group;
     return (const T*)a.q + (g.start + token) * a.q_token + head * a.q_head;
 }
 template <class T>
 __device__ __forceinline__ T* output_of(const PagedArgs& a, const PagedSegment& g, int row) {
-    const int flat = g.row0 + row, token = flat / a.group, head = g.head * a.group + flat - token * a.group;
+    const int flat = g.row0 + row, token = by_group(a, flat), head = g.head * a.group + flat - token * a.group;
     return (T*)a.out + (g.start + token) * a.out_token + head * a.out_head;
 }
 
@@ -57,7 +57,8 @@ struct Walk {
 
     __device__ __forceinline__ void begin(const PagedArgs& a, long long* scratch) {
         Shares s;
-        s.init(a, blockIdx.x, gridDim.x, scratch);
+        if (a.num_seqs > Shares::kSolo) s.init(a, blockIdx.x, gridDim.x, scratch);
+        else if (threadIdx.x < 32) s.init_solo(a, blockIdx.x, gridDim.x);
         if (threadIdx.x == 0) {
             memcpy(shares, &s, sizeof s);
             meta = PagedMeta{};
@@ -74,6 +75,12 @@ struct Walk {
         }
     }
 };
+
+// Where columns 4·quad.. of a row of a partial result lie: a warp that has 32 rows
+// of a column writes them side by side.
+__device__ __forceinline__ float* part_of(const PagedArgs& a, long long slot, int row, int quad) {
+    return a.parts + (slot * a.part_rows * (a.head_dim / 4) + (long long)quad * a.part_rows + row) * 4;
+}
 
 // ---------------------------------------------------------------------------
 // fp32 caches, many rows, and bf16 heads wider than the matrix kernel takes:
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
                 unpack2(o[i][2 * c], x.x, x.y);
                 unpack2(o[i][2 * c + 1], x.z, x.w);
                 if (whole) store4(scaled(x, z), out + col);
-                else store4(x, a.parts + row * D + col);
+                else store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, col / 4));
             }
             if (!whole && tx == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(m[i], l[i]);
         }
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
                 store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<float>(a, g, r) + 4 * at);
             } else {
                 const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
-                store4(x, a.parts + row * D + 4 * at);
+                store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, at));
                 if (at == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(top, sum);
             }
         }
@@ -448,111 +455,107 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 // Joins the parts of items that several CTAs took: CTA (c, y) of this kernel
-// takes some rows of the item that CTA c began.  A group of kLanes lanes holds
-// one row; where the rows leave groups idle, a row's parts are dealt out to
-// several.
+// takes rows 16·y.. of the item that CTA c began.  A thread has four columns of a
+// row; neighbours have up to 8 rows of the same columns (128 bytes of a part), and
+// where that leaves threads idle a row's parts are dealt out to several.
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
-constexpr int join_rows(int lanes) { return 2 * kJoinThreads / lanes; }  // of a CTA: two a group
+constexpr int kJoinThreads = 256, kJoinRows = 16;
 
-// A part's (reference, sum) and columns 4·lane.. of its sums.
-struct JoinPart {
-    float2 stat;
-    float4 x[2];
+struct JoinSum {
+    float2 stat;  // (reference, sum of weights)
+    float4 x;
 };
-
 // Adds a part to sums with a reference that is no less.
-__device__ __forceinline__ void add_part(JoinPart& sum, const JoinPart& p, float scale_log2, int quads) {
-    if (p.stat.x == -INFINITY) return;  // no key seen there
-    const float w = weight_of(p.stat.x, sum.stat.x, scale_log2);
-    sum.stat.y = fmaf(p.stat.y, w, sum.stat.y);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (j >= quads) break;
-        sum.x[j].x = fmaf(p.x[j].x, w, sum.x[j].x);
-        sum.x[j].y = fmaf(p.x[j].y, w, sum.x[j].y);
-        sum.x[j].z = fmaf(p.x[j].z, w, sum.x[j].z);
-        sum.x[j].w = fmaf(p.x[j].w, w, sum.x[j].w);
-    }
+__device__ __forceinline__ void add_part(JoinSum& sum, float2 stat, float4 x, float scale_log2) {
+    if (stat.x == -INFINITY) return;  // no key seen there
+    const float w = weight_of(stat.x, sum.stat.x, scale_log2);
+    sum.stat.y = fmaf(stat.y, w, sum.stat.y);
+    sum.x = add_scaled(sum.x, x, w);
+}
+__device__ __forceinline__ void raise_reference(JoinSum& sum, float top, float scale_log2) {
+    const float f = weight_of(sum.stat.x, top, scale_log2);
+    sum.stat = make_float2(top, sum.stat.y * f);
+    sum.x = scaled(sum.x, f);
 }
 
-template <class T, int kLanes>  // 8, 16 or 32: heads of up to 32, 64, 256 columns
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
-    constexpr int kJoinRows = join_rows(kLanes), kGroups = kJoinThreads / kLanes, kQuads = kLanes == 32 ? 2 : 1, kAhead = 4;
-    __shared__ JoinPart shared[kGroups][kLanes];
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __grid_constant__ PagedArgs a, int ctas) {
+    constexpr int kAhead = 4;
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float2 stats[kJoinThreads];
     await_previous();
     let_next_start();
     const PagedMeta* meta = static_cast<const PagedMeta*>(a.meta);
-    const int c = blockIdx.x, warp_lane = threadIdx.x & 31;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int4 begin = __ldcg(reinterpret_cast<const int4*>(meta + c));  // first_live, start, row0, rows
+    const int head = __ldcg(&meta[c].head);
+    int2 later = make_int2(0, 1);  // later_live, ends
+    if (c + 1 + lane < ctas) later = __ldcg(reinterpret_cast<const int2*>(&meta[c + 1 + lane].later_live));
     const int row_base = blockIdx.y * kJoinRows, rows = min(begin.w - row_base, kJoinRows);
     if (!begin.x || rows <= 0) return;
-    const int head0 = meta[c].head * a.group;
+    const int head0 = head * a.group;
     // The CTAs c + 1 .. c + count hold the rest.
     int count = 0;
+#pragma unroll 1
     for (int at = c + 1; at < ctas; at += 32) {
-        const int i = at + warp_lane;
-        const bool last = i >= ctas || !meta[i].later_live || meta[i].ends;
-        const unsigned stop = __ballot_sync(kFullMask, last);
+        if (at > c + 1) {
+            later = make_int2(0, 1);
+            if (at + lane < ctas) later = __ldcg(reinterpret_cast<const int2*>(&meta[at + lane].later_live));
+        }
+        const unsigned stop = __ballot_sync(kFullMask, !later.x || later.y);
         if (stop) {
             count = min(at + __ffs(stop) - 1, ctas - 1) - c;
             break;
         }
     }
-    const int D = a.head_dim, group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-    int split = 1;  // groups a row
-    while (2 * split * rows <= kGroups && split <= count) split *= 2;
-    const int side = kGroups / split, share = group / side;  // rows side by side; this group's share of the parts
-    for (int r0 = 0; r0 < rows; r0 += side) {
-        const int r = row_base + r0 + group % side;
-        const bool real = r0 + group % side < rows;
-        JoinPart sum = {make_float2(-INFINITY, 0.f), {}};
+    const int quads = a.head_dim / 4;
+    int side = 1;  // rows side by side
+    while (side < 8 && side < rows && 2 * side * quads <= kJoinThreads) side *= 2;
+    const int each = side * quads, split = min(kJoinThreads / each, count + 1);  // threads of a share; shares
+    const int share = threadIdx.x / each, rest = threadIdx.x - share * each, quad = rest / side;
+#pragma unroll 1
+    for (int r0 = rest - quad * side; r0 - rest + quad * side < rows; r0 += side) {
+        const int r = row_base + r0;
+        const bool real = share < split && r0 < rows;
+        JoinSum sum = {make_float2(-INFINITY, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
         if (real) {
-            const auto row_of = [&](int i) { return (i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater) * a.part_rows + r; };
+#pragma unroll 1
             for (int i0 = share; i0 <= count; i0 += kAhead * split) {
-                JoinPart p[kAhead];
+                float2 stat[kAhead];
+                float4 x[kAhead];
                 float top = sum.stat.x;
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = i0 + u * split;
-                    p[u].stat = make_float2(-INFINITY, 0.f);
+                    stat[u] = make_float2(-INFINITY, 0.f);
                     if (i > count) continue;
-                    const long long row = row_of(i);
-                    p[u].stat = __ldcg(reinterpret_cast<const float2*>(a.part_stats + 2 * row));
-#pragma unroll
-                    for (int j = 0; j < kQuads; ++j)
-                        if (128 * j + 4 * lane < D) p[u].x[j] = __ldcg(reinterpret_cast<const float4*>(a.parts + row * D + 128 * j + 4 * lane));
+                    const long long slot = i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater;
+                    stat[u] = __ldcg(reinterpret_cast<const float2*>(a.part_stats + 2 * (slot * a.part_rows + r)));
+                    x[u] = __ldcg(reinterpret_cast<const float4*>(part_of(a, slot, r, quad)));
                 }
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) top = fmaxf(top, p[u].stat.x);
-                const float f = weight_of(sum.stat.x, top, a.scale_log2);
-                sum.stat = make_float2(top, sum.stat.y * f);
+                for (int u = 0; u < kAhead; ++u) top = fmaxf(top, stat[u].x);
+                raise_reference(sum, top, a.scale_log2);
 #pragma unroll
-                for (int j = 0; j < kQuads; ++j) sum.x[j].x *= f, sum.x[j].y *= f, sum.x[j].z *= f, sum.x[j].w *= f;
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) add_part(sum, p[u], a.scale_log2, kQuads);
+                for (int u = 0; u < kAhead; ++u) add_part(sum, stat[u], x[u], a.scale_log2);
             }
         }
-        if (split > 1) {  // one row group a CTA then
-            shared[group][lane] = sum;
+        if (split > 1) {
+            __syncthreads();  // the last rows' sums have been read
+            sums[threadIdx.x] = sum.x;
+            stats[threadIdx.x] = sum.stat;
             __syncthreads();
-            if (share > 0 || !real) return;
-            float top = sum.stat.x;
-            for (int u = 1; u < split; ++u) top = fmaxf(top, shared[group + u * side][lane].stat.x);
-            const float f = weight_of(sum.stat.x, top, a.scale_log2);
-            sum.stat = make_float2(top, sum.stat.y * f);
-#pragma unroll
-            for (int j = 0; j < kQuads; ++j) sum.x[j].x *= f, sum.x[j].y *= f, sum.x[j].z *= f, sum.x[j].w *= f;
-            for (int u = 1; u < split; ++u) add_part(sum, shared[group + u * side][lane], a.scale_log2, kQuads);
+            if (share == 0 && real) {
+                float top = sum.stat.x;
+                for (int u = 1; u < split; ++u) top = fmaxf(top, stats[threadIdx.x + u * each].x);
+                raise_reference(sum, top, a.scale_log2);
+                for (int u = 1; u < split; ++u) add_part(sum, stats[threadIdx.x + u * each], sums[threadIdx.x + u * each], a.scale_log2);
+            }
         }
-        if (!real) continue;
-        const int flat = begin.z + r, token = flat / a.group;
+        if (share > 0 || !real) continue;
+        const int flat = begin.z + r, token = by_group(a, flat);
         T* out = (T*)a.out + (begin.y + token) * a.out_token + (head0 + flat - token * a.group) * a.out_head;
-        const float z = sum.stat.y == 0.f ? 0.f : 1.f / sum.stat.y;
-#pragma unroll
-        for (int j = 0; j < kQuads; ++j)
-            if (128 * j + 4 * lane < D)
-                store4(make_float4(sum.x[j].x * z, sum.x[j].y * z, sum.x[j].z * z, sum.x[j].w * z), out + 128 * j + 4 * lane);
+        store4(scaled(sum.x, sum.stat.y == 0.f ? 0.f : 1.f / sum.stat.y), out + 4 * quad);
     }
 }
 
@@ -614,14 +617,14 @@ int run_block(const PagedArgs& a, int ctas, cudaStream_t stream) {
     return a.head_dim <= 192 ? run_block<T, 3>(a, ctas, stream) : run_block<T, 4>(a, ctas, stream);
 }
 
-template <class T, int kLanes>
+template <class T>
 int join(const PagedArgs& a, int ctas, cudaStream_t stream) {
-    const auto kernel = paged_join_kernel<T, kLanes>;
+    const auto kernel = paged_join_kernel<T>;
     // The same split of an SM's memory as the kernel before it has: to change it the
     // SM would have to drain.
     static SharedOnce once;
     if (!once.allow(kernel, 0)) return cuda_failure();
-    return launch_next(kernel, dim3(ctas, (a.part_rows + join_rows(kLanes) - 1) / join_rows(kLanes)), kJoinThreads, 1, stream, a, ctas);
+    return launch_next(kernel, dim3(ctas, (a.part_rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 1, stream, a, ctas);
 }
 
 size_t meta_bytes(int ctas) { return ((size_t)ctas * sizeof(PagedMeta) + 15) / 16 * 16; }
@@ -650,9 +653,7 @@ int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t
         default: code = bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
     }
     if (code != USM_OK) return code;
-    if (a.head_dim <= 32) return bf16 ? join<__nv_bfloat16, 8>(a, s.ctas, stream) : join<float, 8>(a, s.ctas, stream);
-    if (a.head_dim <= 64) return bf16 ? join<__nv_bfloat16, 16>(a, s.ctas, stream) : join<float, 16>(a, s.ctas, stream);
-    return bf16 ? join<__nv_bfloat16, 32>(a, s.ctas, stream) : join<float, 32>(a, s.ctas, stream);
+    return bf16 ? join<__nv_bfloat16>(a, s.ctas, stream) : join<float>(a, s.ctas, stream);
 }
 
 }  // namespace usm

@@ -66,7 +66,7 @@ struct Control {
     float2 stats[128];  // (reference, sum) of the rows that one half leaves to the other
     uint32_t tmem;
     int abort;
-    int joined;  // warps that are done with their joining of a segment's halves, over all segments
+    int joined;  // warps that have joined a segment's halves, or need not, over all segments
 };
 static_assert(Sizes<128>::kControl + sizeof(Control) <= 227 * 1024, "shared memory");
 
@@ -207,7 +207,7 @@ struct Copies {
             const int r = row0 + lane;
             const char* row = nullptr;
             if (r < g.rows) {
-                const int flat = g.row0 + r, token = flat / a.group;
+                const int flat = g.row0 + r, token = by_group(a, flat);
                 row = (const char*)a.q + 2 * ((g.start + token) * a.q_token + (g.head * a.group + flat - token * a.group) * a.q_head);
             }
             rows(smem + (row0 >> 7) * Z::kTile, row0 & 127, row);
@@ -584,6 +584,15 @@ struct Softmax {
         o_col = tmem + lanes + 256 + half * DP;
     }
 
+    // This warp no longer uses the queries' second tile for this segment.
+    __device__ __forceinline__ void done_joining() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            __threadfence_block();
+            atomicAdd(&ct->joined, 1);
+        }
+    }
+
     // Row of the segment's block that this thread has.
     __device__ __forceinline__ int row_of(const PagedSegment& g) const { return g.rows <= 128 ? tid : half * 128 + tid; }
 
@@ -713,10 +722,10 @@ struct Softmax {
         const bool some = __any_sync(kFullMask, mine);
         const int lanes = (min(g.rows, 128) + 31) / 32 * 32, wide = max(Z::kTile / 4 / lanes / 32, 1) * 32;
         const uint32_t box = smem + Z::kTile + tid * wide * 4;
-        const int flat = g.row0 + row, token = flat / a.group;
+        const int flat = g.row0 + row, token = by_group(a, flat);
         const long long part = (2LL * blockIdx.x + g.part) * a.part_rows + row;
         char* to = whole ? static_cast<char*>(a.out) + 2 * ((g.start + token) * a.out_token + (g.head * a.group + flat - token * a.group) * a.out_head)
-                         : reinterpret_cast<char*>(a.parts + part * a.head_dim);
+                         : reinterpret_cast<char*>(a.parts + (part - row) * a.head_dim + row * 4);
         float f0 = 1.f, f1 = 0.f;
 #pragma unroll 1
         for (int j = 0; j < a.head_dim; j += 32) {
@@ -796,7 +805,7 @@ struct Softmax {
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (4 * i < left) store16(to + 4 * j + 16 * i, w + 4 * i);
+                    if (4 * i < left) store16(to + (long long)(j / 4 + i) * a.part_rows * 16, w + 4 * i);
             }
         }
         if (!whole && mine && (!both || last)) *reinterpret_cast<float2*>(a.part_stats + 2 * part) = make_float2(m, l);
@@ -809,6 +818,7 @@ struct Softmax {
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
+            if (g.rows > 128) done_joining();  // its halves have rows of their own
             const bool some = __any_sync(kFullMask, row_of(g) < g.rows);
             // Tiles that every row of this warp sees whole: whole.x <= t < whole.y.
             int2 whole;
@@ -844,11 +854,7 @@ struct Softmax {
             }
             if (g.rows <= 128 && (tiles & 1)) state ^= kTurn;
             tmem_fence_before_sync();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) {
-                __threadfence_block();
-                atomicAdd(&ct->joined, 1);
-            }
+            if (g.rows <= 128) done_joining();
             arrive_warp(ct->seg_empty[slot]);
         }
     }
@@ -892,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
     await_previous();  // nothing of the caller's is read or written before
     let_next_start();
     Shares shares;
-    shares.init(a, blockIdx.x, gridDim.x, ct->scratch);
+    if (a.num_seqs > Shares::kSolo) shares.init(a, blockIdx.x, gridDim.x, ct->scratch);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
@@ -925,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
             mbar_wait_bounded(smem_addr(&ct->drained), 0, kWaitLimitNs);
         } else if (warp == 13) {
             PagedMeta meta = {};
+            if (a.num_seqs <= Shares::kSolo) shares.init_solo(a, blockIdx.x, gridDim.x);
             for (uint32_t it = 0;; ++it) {
                 const int slot = it % kRing;
                 PagedSegment g = shares.next(a);
