@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Joins the parts of items that several CTAs took: CTA (c, y) of this kernel
 // takes rows 16·y.. of the item that CTA c began.  A thread has four columns of a
-// row; neighbours have up to 8 rows of the same columns (128 bytes of a part), and
+// row; neighbours have up to 16 rows of the same columns (256 bytes of a part), and
 // where that leaves threads idle a row's parts are dealt out to several.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256, kJoinRows = 16;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __gri
     }
     const int quads = a.head_dim / 4;
     int side = 1;  // rows side by side
-    while (side < 8 && side < rows && 2 * side * quads <= kJoinThreads) side *= 2;
+    while (side < kJoinRows && side < rows && 2 * side * quads <= kJoinThreads) side *= 2;
     const int each = side * quads, split = min(kJoinThreads / each, count + 1);  // threads of a share; shares
     const int share = threadIdx.x / each, rest = threadIdx.x - share * each, quad = rest / side;
 #pragma unroll 1
