@@ -91,6 +91,7 @@ __device__ __forceinline__ float* part_of(const PagedArgs& a, long long slot, in
 // shared memory feed 64 FMAs of a warp.
 // ---------------------------------------------------------------------------
 constexpr int kBlockRows = 64, kBlockKeys = 64, kBlockThreads = 256;
+constexpr int kBlockWeights = kBlockKeys + 4;  // pitch of a row of weights
 using BlockShares = PagedShares<kBlockRows, kBlockKeys, kBlockThreads, 3>;
 
 // Row pitch of the shared arrays: a multiple of 4 that is 4 modulo 32, so that 8
@@ -99,7 +100,7 @@ constexpr int block_pitch(int head_dim) { return (head_dim + 31) / 32 * 32 + 4; 
 // Tiles of keys and values in shared memory: two where they fit.
 constexpr int block_stages(int head_dim) { return head_dim <= 128 ? 2 : 1; }
 constexpr int block_smem(int head_dim) {
-    return (kBlockRows + 2 * block_stages(head_dim) * kBlockKeys) * block_pitch(head_dim) * 4 + kBlockRows * (kBlockKeys + 4) * 4;
+    return (kBlockRows + 2 * block_stages(head_dim) * kBlockKeys) * block_pitch(head_dim) * 4 + kBlockRows * kBlockWeights * 4;
 }
 
 __device__ __forceinline__ void copy4(float* to, const float* from, bool there) {
@@ -107,6 +108,39 @@ __device__ __forceinline__ void copy4(float* to, const float* from, bool there) 
 }
 __device__ __forceinline__ void copy4(float* to, const __nv_bfloat16* from, bool there) {
     *reinterpret_cast<float4*>(to) = there ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// o += P·V for 4 rows and columns 64·c + 4·tx.. of a tile.
+template <int kWide, bool kGuard>
+__device__ __forceinline__ void add_values(const float* p, const float* v, int pitch, int D, int tx, int key0, const int2 (&seen)[4],
+                                           uint64_t (&o)[4][2 * kWide]) {
+#pragma unroll 2
+    for (int key = 0; key < kBlockKeys; key += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + i * kBlockWeights + key);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            ulonglong2 y[kWide];
+#pragma unroll
+            for (int c = 0; c < kWide; ++c) {
+                const int col = 64 * c + 4 * tx;
+                y[c] = make_ulonglong2(0, 0);
+                if (col < D) y[c] = *reinterpret_cast<const ulonglong2*>(v + (key + u) * pitch + col);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
+                if (kGuard && (key0 + key + u < seen[i].x || key0 + key + u >= seen[i].y)) continue;
+                const uint64_t e2 = pack2(e, e);
+#pragma unroll
+                for (int c = 0; c < kWide; ++c) {
+                    o[i][2 * c] = fma2(e2, y[c].x, o[i][2 * c]);
+                    o[i][2 * c + 1] = fma2(e2, y[c].y, o[i][2 * c + 1]);
+                }
+            }
+        }
+    }
 }
 
 template <class T, int kWide>  // kWide: groups of 64 columns
@@ -117,7 +151,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
     await_previous();
     let_next_start();
     constexpr int kStages = kWide <= 2 ? 2 : 1;
-    constexpr int kP = kBlockKeys + 4;
+    constexpr int kP = kBlockWeights;
     const int D = a.head_dim, pitch = block_pitch(D);
     float* q = reinterpret_cast<float*>(smem_raw);
     float* tiles = q + kBlockRows * pitch;  // [stage][keys, then values][64][pitch]
@@ -225,35 +259,8 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
             }
             __syncwarp();  // a warp's rows of p are its own
             // Where a row does not see the whole tile a weight of 0 takes no value.
-            const bool guard = __any_sync(kFullMask, partly);
-#pragma unroll 1
-            for (int key = 0; key < kBlockKeys; key += 4) {
-                float4 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + (ty * 4 + i) * kP + key);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    ulonglong2 y[kWide];
-#pragma unroll
-                    for (int c = 0; c < kWide; ++c) {
-                        const int col = 64 * c + 4 * tx;
-                        y[c] = make_ulonglong2(0, 0);
-                        if (col < D) y[c] = *reinterpret_cast<const ulonglong2*>(v + (key + u) * pitch + col);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
-                        const int at = key0 + key + u;
-                        if (guard && (at < seen[i].x || at >= seen[i].y)) continue;
-                        const uint64_t e2 = pack2(e, e);
-#pragma unroll
-                        for (int c = 0; c < kWide; ++c) {
-                            o[i][2 * c] = fma2(e2, y[c].x, o[i][2 * c]);
-                            o[i][2 * c + 1] = fma2(e2, y[c].y, o[i][2 * c + 1]);
-                        }
-                    }
-                }
-            }
+            if (__any_sync(kFullMask, partly)) add_values<kWide, true>(p + ty * 4 * kP, v, pitch, D, tx, key0, seen, o);
+            else add_values<kWide, false>(p + ty * 4 * kP, v, pitch, D, tx, key0, seen, o);
             if (kStages == 1 && t + 1 < n) {
                 __syncthreads();
                 load(t + 1);
