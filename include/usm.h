@@ -522,7 +522,8 @@ int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, 
  *            not overlap anything else of the call.
  *   scale  : finite, ≥ 0.
  *   workspace : paged_attention_workspace_bytes(...) bytes of device scratch,
- *            16-byte aligned, contents ignored.
+ *            16-byte aligned, contents ignored.  The size follows from the arguments
+ *            and the number of SMs of the current device (up to 44 MB).
  * Products, statistics and sums are fp32.  bf16: probabilities are rounded to
  * bf16 before their product with V (relative 2^-9 each, as the output's own
  * rounding); head_dim > 128 keeps them in fp32.

@@ -573,3 +573,146 @@ def test_beside_sparse_attention(usm, dtype):
     listed = got(usm.attention(ints(rows), ints(np.concatenate(cols)), q.reshape(4, 64), flat(k), flat(v), scale=0.125))
     _, bound = p.reference(0.125)
     assert_near(dense.reshape(4, 64), listed, 2 * bound.reshape(4, 64))
+
+
+# ---------------------------------------------------------------------------
+# The ends of the ranges
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("seqs", [31, 32, 33, 127, 128, 129, 256, 257, 511, 512, 513])
+def test_numbers_of_sequences(usm, dtype, seqs):
+    """Around the sizes at which the division of the work changes its form."""
+    rng = np.random.default_rng(seqs)
+    counts = rng.integers(0, 3, seqs)
+    counts[-1], counts[0] = 1, 0
+    lengths = counts + rng.integers(0, 300, seqs) * (rng.random(seqs) < 0.3)
+    Problem("numbers", lengths, counts, heads=4, kv=2, D=32, page=16, dtype=dtype).check(usm)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 12, 16, 64, 100, 128, 256, 384, 1000])
+def test_page_sizes(usm, dtype, page):
+    """Pages that divide a tile of keys, that tiles divide, and neither."""
+    Problem("pages", [700, 129, 5, 384], [1, 129, 5, 3], heads=4, kv=2, D=72, page=page, dtype=dtype).check(usm, window=300)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 9, 17, 64, 127, 128, 129, 200, 255, 256, 257])
+def test_numbers_of_heads(usm, dtype, group):
+    """Query heads of a head of keys: rows of a token in one block of rows or several."""
+    Problem("group", [90, 200], [3, 2], heads=group, kv=1, D=64, page=16, dtype=dtype).check(usm)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_window_longer_than_any_position(usm, dtype):
+    """Windows next to 2^31 with positions below zero, all keys in sight."""
+    for window in (2**30 - 1, 2**30, 2**31 - 1):
+        Problem("huge window", [5, 300], [9, 20], heads=2, kv=1, D=64, dtype=dtype).check(usm, window=window, causal=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_scales(usm, dtype):
+    """A scale that makes the largest score the only one, up to the largest float."""
+    p = Problem("scale", [150], [3], heads=1, kv=1, D=32, dtype=dtype)
+    best = []
+    for t in range(3):
+        j = np.arange(147 + t + 1)
+        x = p.k[p.table[0, j // 16], j % 16, 0].astype(np.float64) @ p.q[t, 0]
+        best.append(p.v[p.table[0, j[x.argmax()] // 16], j[x.argmax()] % 16, 0])
+    for scale in (1e6, 1e30, 3.4e38):
+        x = got(p.run(usm, scale))[:, 0]
+        assert_near(x, np.array(best, dtype=np.float64), R.HALF_STEP[dtype] * np.abs(best) + R.U)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cache_past_32_bits(usm, dtype):
+    """Pages whose offset passes 2^31 elements, and 2^32 bytes."""
+    import torch
+    pages, size, kv, D = 17000, 16, 64, 128
+    assert pages * size * kv * D > 2**31
+    k = torch.empty((pages, size, kv, D), dtype=torch_type(dtype), device="cuda")
+    v = torch.empty_like(k)
+    p = Problem("far", [40, 20], [1, 20], heads=4, kv=2, D=D, page=size, dtype=dtype, extra=0)
+    far = np.array([[16999, 3, 16998], [16390, 16997, 0]])
+    table = np.zeros_like(p.table)
+    for b in range(2):
+        for i in range(-(-p.lengths[b] // size)):
+            table[b, i] = far[b, i]
+            k[far[b, i], :, 62:] = put(p.k[p.table[b, i]], dtype)
+            v[far[b, i], :, 62:] = put(p.v[p.table[b, i]], dtype)
+    _, _, _, _, lens, offsets = p.on_device()
+    new = put(np.zeros((p.T, 2, D)), dtype)
+    scale = D ** -0.5
+    x = usm.paged_attention(put(p.q, dtype), k[:, :, 62:], v[:, :, 62:], ints(table), lens, q_offsets=offsets, scale=scale)
+    ref, bound = p.reference(scale)
+    assert_near(got(x), ref, bound)
+    usm.paged_append(new + 3, new + 4, k[:, :, 62:], v[:, :, 62:], ints(table), lens, q_offsets=offsets)
+    assert torch.all(k[far[0, 2], 39 % size, 62:] == 3) and torch.all(v[far[0, 2], 39 % size, 62:] == 4)
+    assert torch.all(k[far[1, 0], :, 62:] == 3) and torch.all(v[far[1, 1], :4, 62:] == 4)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_broadcast_queries(usm, dtype):
+    """Rows of stride 0: one query for all tokens and heads, one key for all heads."""
+    import torch
+    p = Problem("broadcast", [300, 150], [30, 150], heads=4, kv=2, D=64, dtype=dtype)
+    q, k, v, table, lens, offsets = p.on_device()
+    one = q[:1, :1].expand(p.T, 4, 64)
+    a = usm.paged_attention(one, k, v, table, lens, q_offsets=offsets)
+    assert torch.equal(a, usm.paged_attention(one.contiguous(), k, v, table, lens, q_offsets=offsets))
+    caches = [c.clone() for c in (k, v)]
+    usm.paged_append(one[:, :2], one[:, :2], k, v, table, lens, q_offsets=offsets)
+    usm.paged_append(one[:, :2].contiguous(), one[:, :2].contiguous(), *caches, table, lens, q_offsets=offsets)
+    assert same_values(got(k), got(caches[0])) and same_values(got(v), got(caches[1]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_page_one_slot_one_head(usm, dtype):
+    """Dimensions of one, whatever their strides."""
+    import torch
+    p = Problem("ones", [1], [1], heads=3, kv=1, D=64, page=1, dtype=dtype, spare=0, extra=0)
+    q, k, v, table, lens, _ = p.on_device()
+    odd = lambda c: torch.as_strided(c, c.shape, (1, 3, 5, 1))
+    out = usm.paged_attention(q, odd(k), odd(v), table, lens)
+    assert torch.equal(out, v.reshape(1, 1, 64).expand(1, 3, 64))
+
+
+def test_two_calls_at_once(usm):
+    """Calls on two streams, with other kernels of the library between them."""
+    import torch
+    ps = [Problem("first", [4000, 200, 900], [3, 200, 1], heads=8, kv=2, D=128), Problem("second", [3000] * 8, [1] * 8, heads=8, kv=8)]
+    want = [p.run(usm, scale=0.125) for p in ps]
+    args = [p.on_device() for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (q, k, v, table, lens, offsets) in enumerate(args):
+            outs[i].append(usm.paged_attention(q, k, v, table, lens, q_offsets=offsets, scale=0.125, stream=streams[i]))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+    assert usm.poll_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_junk_in_the_table_and_offsets(usm, dtype):
+    """Arrays that break the contract give wrong numbers at most: wild pages in use,
+    offsets out of order and out of range, lengths below zero and past the table."""
+    import torch
+    p = Problem("junk", [300, 150, 70], [30, 150, 2], heads=4, kv=2, D=64, dtype=dtype)
+    q, k, v, table, lens, offsets = p.on_device()
+    k, v = k.nan_to_num(0.0), v.nan_to_num(0.0)
+    for bad in ([0, 500, -3, 182], [-2**31, 2**31 - 1, 5, 9], [182, 0, 182, 0]):
+        usm.paged_attention(q, k, v, table, lens, q_offsets=ints(bad))
+        usm.paged_append(q[:, :2], q[:, 2:], k, v, table, lens, q_offsets=ints(bad))
+    for bad in ([-2**31, 2**31 - 1, 0], [10**6, -1, 300]):
+        usm.paged_attention(q, k, v, table, ints(bad), q_offsets=offsets)
+        usm.paged_append(q[:, :2], q[:, 2:], k, v, table, ints(bad), q_offsets=offsets)
+    wild = p.rng.integers(-2**31, 2**31 - 1, table.shape)
+    usm.paged_attention(q, k, v, ints(wild), lens, q_offsets=offsets)
+    before = k.clone()
+    usm.paged_append(q[:, :2], q[:, 2:], k, v, ints(wild), lens, q_offsets=offsets)
+    assert torch.equal(k, before) or bool(((wild >= 0) & (wild < k.shape[0])).any())
+    torch.cuda.synchronize()
+    assert usm.poll_status() == 0

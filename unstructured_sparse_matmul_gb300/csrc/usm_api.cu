@@ -644,7 +644,7 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     a.group_mul = (uint32_t)(((1ULL << a.group_shift) + a.group - 1) / a.group);
     // A scale of 0 weighs all keys alike, as does the smallest normal number; it
     // keeps masked scores at -inf.
-    a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1.17549435e-38f);
+    a.scale_log2 = fminf(fmaxf(scale * 1.4426950408889634f, 1.17549435e-38f), 3.402823466e38f);
     a.causal = causal, a.window = window;
     a.status = status_word_for_current_device();
     if (!a.status) return USM_ERR_CUDA;

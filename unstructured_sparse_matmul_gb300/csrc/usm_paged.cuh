@@ -55,7 +55,7 @@ __device__ __noinline__ PagedBlock paged_block_call(uint32_t group_mul, int grou
     const int p1 = position + (int)((unsigned long long)last * group_mul >> group_shift);
     PagedBlock k;
     k.hi = causal ? min(keys, max(p1 + 1, 0)) : keys;
-    k.lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+    k.lo = window > 0 && p0 >= window ? p0 - window + 1 : 0;
     if (k.lo >= k.hi) k.lo = k.hi = 0;
     k.tile0 = k.lo / kKeys;
     k.tiles = max((k.hi + kKeys - 1) / kKeys - k.tile0, 1);  // one for a block that sees nothing: it writes zeros
@@ -330,7 +330,7 @@ __device__ __forceinline__ int2 paged_seen(const PagedArgs& a, const PagedSegmen
     const int p = g.len - g.n + by_group(a, g.row0 + row);
     const int keys = min(g.len, a.capacity);
     const int hi = a.causal ? min(keys, max(p + 1, 0)) : keys;
-    const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+    const int lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
     return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
