@@ -716,3 +716,23 @@ def test_junk_in_the_table_and_offsets(usm, dtype):
     assert torch.equal(k, before) or bool(((wild >= 0) & (wild < k.shape[0])).any())
     torch.cuda.synchronize()
     assert usm.poll_status() == 0
+
+
+@pytest.mark.parametrize("page", [32, 24])
+def test_few_rows_before_many(usm, page):
+    """Blocks of few rows, whose halves leave their sums to one another, followed at
+    once by blocks of many, whose queries take the same place."""
+    import torch
+    p = Problem("few and many", [827, 1700, 1309, 740, 1510], [101, 100, 94, 36, 79], heads=24, kv=3, D=80, page=page)
+    p.check(usm)
+    q, k, v, table, lens, offsets = p.on_device()
+    q, lens = q.repeat(4, 1, 1), lens.repeat(4)
+    counts = np.tile(p.counts, 4)
+    offsets = ints(np.concatenate([[0], np.cumsum(counts)]))
+    run = lambda: usm.paged_attention(q, k, v, table.repeat(4, 1), lens, q_offsets=offsets, scale=p.D ** -0.5)
+    first = run()
+    for part in first.split(p.T):
+        # The same rows in another place of the batch: cut into parts elsewhere.
+        assert_near(got(part), got(first[:p.T]), 3 * p.reference(p.D ** -0.5)[1])
+    for _ in range(20):
+        assert torch.equal(run(), first)

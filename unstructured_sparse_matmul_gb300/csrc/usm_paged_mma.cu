@@ -66,7 +66,7 @@ struct Control {
     float2 stats[128];  // (reference, sum) of the rows that one half leaves to the other
     uint32_t tmem;
     int abort;
-    int joined;  // warps that have joined a segment's halves, or need not, over all segments
+    int joined;  // warps that have joined a segment's halves, over all segments
 };
 static_assert(Sizes<128>::kControl + sizeof(Control) <= 227 * 1024, "shared memory");
 
@@ -180,14 +180,17 @@ struct Copies {
     }
 
     // Segment `it`'s queries may come: those before are no longer read, and, where
-    // there is a second tile of them, no halves are being joined through it.
-    __device__ __forceinline__ bool room_for_queries(const PagedSegment& g, uint32_t it) {
+    // there is a second tile of them, no halves are being joined through it: all
+    // `joins` segments before whose halves are have been.
+    __device__ __forceinline__ bool room_for_queries(const PagedSegment& g, uint32_t it, int& joins) {
+        const int before = joins;
+        if (g.rows <= 128 && g.tiles > 1) ++joins;
         if (it == 0) return true;
         if (!wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return false;
         if (g.rows <= 128) return true;
         const unsigned long long t0 = global_timer_ns();
         bool ok = true;
-        while (ok && *(volatile int*)&ct->joined < 8 * (int)it) {
+        while (ok && *(volatile int*)&ct->joined < 4 * before) {
             if (*(volatile int*)&ct->abort) ok = false;
             if (global_timer_ns() - t0 > kWaitLimitNs) {
                 *(volatile int*)&ct->abort = 1;
@@ -341,11 +344,12 @@ struct Copies {
 
     // Two further warps: the queries.
     __device__ void all_queries() {
+        int joins = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
-            if (!g.live || !room_for_queries(g, it)) return;
+            if (!g.live || !room_for_queries(g, it, joins)) return;
             queries(g, warp & 1, 2);
             arrive_warp(ct->seg_empty[slot]);
         }
@@ -390,13 +394,14 @@ struct Copies {
     // All four warps: 16-byte copies.
     __device__ void chunks() {
         uint32_t stage = 0, parity = 1;
+        int joins = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const int n = g.tiles, key0 = g.tile0 * kKeys;
-            if (!room_for_queries(g, it)) return;
+            if (!room_for_queries(g, it, joins)) return;
             queries(g, warp, 4);
             const char* next = key_row(g, 0);
 #pragma unroll 1
@@ -582,15 +587,6 @@ struct Softmax {
         const uint32_t lanes = (uint32_t)(tid & ~31) << 16;
         s_col = tmem + lanes + half * kKeys;
         o_col = tmem + lanes + 256 + half * DP;
-    }
-
-    // This warp no longer uses the queries' second tile for this segment.
-    __device__ __forceinline__ void done_joining() {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            __threadfence_block();
-            atomicAdd(&ct->joined, 1);
-        }
     }
 
     // Row of the segment's block that this thread has.
@@ -781,6 +777,10 @@ struct Softmax {
             if (both && ends) {
                 arrive_warp(ct->box_free);
                 state = (state ^ kBox) | kBoxUsed;
+                if (j + 32 >= a.head_dim && (threadIdx.x & 31) == 0) {  // this warp has read all of the other half's
+                    __threadfence_block();
+                    atomicAdd(&ct->joined, 1);
+                }
             }
             if (!mine) continue;
             const int left = a.head_dim - j;  // a multiple of 8
@@ -818,7 +818,6 @@ struct Softmax {
             if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
-            if (g.rows > 128) done_joining();  // its halves have rows of their own
             const bool some = __any_sync(kFullMask, row_of(g) < g.rows);
             // Tiles that every row of this warp sees whole: whole.x <= t < whole.y.
             int2 whole;
@@ -854,7 +853,6 @@ struct Softmax {
             }
             if (g.rows <= 128 && (tiles & 1)) state ^= kTurn;
             tmem_fence_before_sync();
-            if (g.rows <= 128) done_joining();
             arrive_warp(ct->seg_empty[slot]);
         }
     }
