@@ -736,3 +736,11 @@ def test_few_rows_before_many(usm, page):
         assert_near(got(part), got(first[:p.T]), 3 * p.reference(p.D ** -0.5)[1])
     for _ in range(20):
         assert torch.equal(run(), first)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 2, 4, 5, 8, 9])
+@pytest.mark.parametrize("width", [32, 64, 128, 136, 200, 256])
+def test_single_tokens_of_all_widths(usm, width, rows, dtype):
+    """Few rows a head of keys, around the sizes at which their kernel changes."""
+    Problem("widths", [700, 3, 0, 130, 2000], [1] * 5, heads=2 * rows, kv=2, D=width, page=16, dtype=dtype).check(usm)

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
 }
 
 // ---------------------------------------------------------------------------
-// fp32 caches, few rows (single tokens): every warp takes batches of keys straight
+// fp32 caches and wide bf16 heads, few rows (single tokens): every warp takes batches of keys straight
 // from memory, kLanes lanes a key, four columns each.  A lane's partial products
 // of a batch are summed across lanes all at once, halving the number of values a
 // lane holds with every step, so that a score costs about one shuffle; each lane
@@ -302,11 +302,13 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256, kFewKeys = 128;
 
-template <int kLanes, int kR>  // 8, 16, 32 lanes: heads of up to 32, 64, 128 columns; rows
+// 8, 16, 32 lanes: heads of up to 32, 64, 128 columns, with kQ = 2 up to 256; kR rows.
+template <class T, int kLanes, int kQ, int kR>
 __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_constant__ PagedArgs a) {
     using Shares = PagedShares<kR, kFewKeys, kFewThreads, 2>;
     constexpr int kWarps = kFewThreads / 32, kSide = 32 / kLanes;
-    constexpr int kLoads = kR <= 4 ? 8 : 4;       // of keys, and of values, of a batch
+    constexpr int kLoads = kR <= 4 && kQ == 1 ? 8 : 4;  // of keys, and of values, of a batch
+    constexpr int kRow = kQ * kLanes;             // quads of columns
     constexpr int kBatch = kLoads * kSide;        // keys
     constexpr int kSteps = kLoads == 8 ? 3 : 2;   // that halve the values
     extern __shared__ float4 smem_raw[];          // queries [row][lane]; sums [warp][row][lane]; (reference, sum) [warp][row]
@@ -317,10 +319,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
     let_next_start();
     const int D = a.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int side = lane / kLanes, col = 4 * (lane % kLanes);
-    const bool column = col < D;
+    bool column[kQ];
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) column[h] = col + 128 * h < D;
     float4* queries = smem_raw;
-    float4* sums = queries + kR * kLanes;
-    float2* stats = reinterpret_cast<float2*>(sums + kWarps * kR * kLanes);
+    float4* sums = queries + kR * kRow;
+    float2* stats = reinterpret_cast<float2*>(sums + kWarps * kR * kRow);
     // The load whose score this lane ends up with.
     int mine = 0;
 #pragma unroll
@@ -335,23 +339,24 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
         __syncthreads();
         if (!seg.live) break;
         const PagedSegment& g = seg;
-        for (int i = tid; i < kR * kLanes; i += kFewThreads) {
-            const int r = i / kLanes, at = i % kLanes;
-            queries[i] = r < g.rows && 4 * at < D ? load4(query_of<float>(a, g, r) + 4 * at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = tid; i < kR * kRow; i += kFewThreads) {
+            const int r = i / kRow, at = i % kRow;
+            queries[i] = r < g.rows && 4 * at < D ? load4(query_of<T>(a, g, r) + 4 * at) : make_float4(0.f, 0.f, 0.f, 0.f);
             if (at == 0) sees[r] = paged_seen(a, g, r);
         }
         __syncthreads();
-        float4 o[kR];
+        float4 o[kR][kQ];
         float m[kR], l[kR];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < kQ; ++h) o[r][h] = make_float4(0.f, 0.f, 0.f, 0.f);
             m[r] = -INFINITY;
             l[r] = 0.f;
         }
         const int lo = g.lo, hi = g.hi, seq = g.seq;
-        const float* kb = (const float*)a.k + g.head * a.k_head + col;
-        const float* vb = (const float*)a.v + g.head * a.v_head + col;
+        const T* kb = (const T*)a.k + g.head * a.k_head + col;
+        const T* vb = (const T*)a.v + g.head * a.v_head + col;
         const int first = g.tile0 * kFewKeys + warp * kBatch, end = min((g.tile0 + g.tiles) * kFewKeys, hi);
         const auto slot_of = [&](int base) {  // of this lane's key of a batch
             const int key = base + lane;
@@ -362,22 +367,31 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
         for (int base = first; base < end; base += kWarps * kBatch) {
             const int2 w = next;
             next = slot_of(base + kWarps * kBatch);
-            float4 k[kLoads], v[kLoads];
+            float4 k[kLoads][kQ], v[kLoads][kQ];
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int page = __shfl_sync(kFullMask, w.x, j * kSide + side), slot = __shfl_sync(kFullMask, w.y, j * kSide + side);
-                k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (page >= 0 && column) {
-                    k[j] = load4(kb + page * a.k_page + slot * a.k_slot);
-                    v[j] = load4(vb + page * a.v_page + slot * a.v_slot);
+#pragma unroll
+                for (int h = 0; h < kQ; ++h) {
+                    k[j][h] = v[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (page >= 0 && column[h]) {
+                        k[j][h] = load4(kb + page * a.k_page + slot * a.k_slot + 128 * h);
+                        v[j][h] = load4(vb + page * a.v_page + slot * a.v_slot + 128 * h);
+                    }
                 }
             }
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-                const float4 q = queries[r * kLanes + lane % kLanes];
                 float s[kLoads];
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j) s[j] = fmaf(q.w, k[j].w, fmaf(q.z, k[j].z, fmaf(q.y, k[j].y, q.x * k[j].x)));
+                for (int h = 0; h < kQ; ++h) {
+                    const float4 q = queries[r * kRow + h * kLanes + lane % kLanes];
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) {
+                        const float x = h == 0 ? q.x * k[j][h].x : fmaf(q.x, k[j][h].x, s[j]);
+                        s[j] = fmaf(q.w, k[j][h].w, fmaf(q.z, k[j][h].z, fmaf(q.y, k[j][h].y, x)));
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     const int half = kLoads >> (i + 1), mask = kLanes >> (i + 1);
@@ -402,7 +416,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
                     const float f = weight_of(m[r], top, c);
                     m[r] = top;
                     l[r] *= f;
-                    o[r] = scaled(o[r], f);
+#pragma unroll
+                    for (int h = 0; h < kQ; ++h) o[r][h] = scaled(o[r][h], f);
                 }
                 const float p = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
                 l[r] += p;
@@ -414,7 +429,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
                     const float pj = __shfl_sync(kFullMask, p, from);
-                    if (all || pj != 0.f) o[r] = add_scaled(o[r], v[j], pj);
+                    if (all || pj != 0.f)
+#pragma unroll
+                        for (int h = 0; h < kQ; ++h) o[r][h] = add_scaled(o[r][h], v[j][h], pj);
                 }
             }
         }
@@ -422,21 +439,23 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
 #pragma unroll
-            for (int mask = kLanes; mask < 32; mask <<= 1) {
-                o[r].x += __shfl_xor_sync(kFullMask, o[r].x, mask);
-                o[r].y += __shfl_xor_sync(kFullMask, o[r].y, mask);
-                o[r].z += __shfl_xor_sync(kFullMask, o[r].z, mask);
-                o[r].w += __shfl_xor_sync(kFullMask, o[r].w, mask);
+            for (int mask = kLanes; mask < 32; mask <<= 1) {  // kQ is 1 where there are sides
+                o[r][0].x += __shfl_xor_sync(kFullMask, o[r][0].x, mask);
+                o[r][0].y += __shfl_xor_sync(kFullMask, o[r][0].y, mask);
+                o[r][0].z += __shfl_xor_sync(kFullMask, o[r][0].z, mask);
+                o[r][0].w += __shfl_xor_sync(kFullMask, o[r][0].w, mask);
             }
 #pragma unroll
             for (int mask = 16; mask > 0; mask >>= 1) l[r] += __shfl_xor_sync(kFullMask, l[r], mask);
             l[r] *= (float)kLoads / kLanes;  // each score is in kLanes / kLoads lanes
-            if (side == 0) sums[(warp * kR + r) * kLanes + lane] = o[r];
+            if (side == 0)
+#pragma unroll
+                for (int h = 0; h < kQ; ++h) sums[(warp * kR + r) * kRow + h * kLanes + lane] = o[r][h];
             if (lane == 0) stats[warp * kR + r] = make_float2(m[r], l[r]);
         }
         __syncthreads();
-        for (int i = tid; i < kR * kLanes; i += kFewThreads) {
-            const int r = i / kLanes, at = i % kLanes;
+        for (int i = tid; i < kR * kRow; i += kFewThreads) {
+            const int r = i / kRow, at = i % kRow;
             if (r >= g.rows || 4 * at >= D) continue;
             float top = -INFINITY, sum = 0.f;
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * kR + r].x);
@@ -446,10 +465,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
                 if (st.x == -INFINITY) continue;
                 const float f = weight_of(st.x, top, c);
                 sum = fmaf(st.y, f, sum);
-                x = add_scaled(x, sums[(w * kR + r) * kLanes + at], f);
+                x = add_scaled(x, sums[(w * kR + r) * kRow + at], f);
             }
             if (g.part == kPartWhole) {
-                store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<float>(a, g, r) + 4 * at);
+                store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<T>(a, g, r) + 4 * at);
             } else {
                 const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
                 store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, at));
@@ -575,18 +594,18 @@ struct Shape {
     int rows;  // of a block
     int ctas;
 };
-// bf16 heads of up to 128 columns go to the matrix kernel.  fp32 heads of that
-// width with up to 8 rows a sequence and head of keys, on average, are read by few
-// rows at a time: from 9 on the keys would be read twice, and the block kernel is
-// as fast.
+// bf16 heads of up to 128 columns go to the matrix kernel.  Others with up to 8 rows
+// a sequence and head of keys, on average, are read by few rows at a time: from
+// 9 on the keys would be read twice, and the block kernel is as fast.  (Wider heads
+// have room for 4 rows: they read the keys of 5 to 8 twice, where the block
+// kernel would fill 8 of its 64 rows.)
 Shape shape_of(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16) {
     const int sms = sm_count_current_device();
     if (bf16 && head_dim <= 128) return Shape{Form::Mma, paged_mma_rows(), sms};
     const long long rows = (long long)tokens * (q_heads / kv_heads);
-    if (!bf16 && head_dim <= 128 && rows <= 8LL * num_seqs) {
-        if (rows <= num_seqs) return Shape{Form::Few1, 1, 2 * sms};
-        return rows <= 4LL * num_seqs ? Shape{Form::Few4, 4, 2 * sms} : Shape{Form::Few8, 8, 2 * sms};
-    }
+    if (rows <= num_seqs) return Shape{Form::Few1, 1, 2 * sms};
+    if (rows <= 8LL * num_seqs)
+        return rows <= 4LL * num_seqs || head_dim > 128 ? Shape{Form::Few4, 4, 2 * sms} : Shape{Form::Few8, 8, 2 * sms};
     const int fit = std::max(1, std::min(2, 220 * 1024 / block_smem(head_dim)));
     return Shape{Form::Block, kBlockRows, fit * sms};
 }
@@ -604,18 +623,22 @@ int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     return launch_next_shared(kernel, dim3(ctas), kBlockThreads, smem, stream, a);
 }
 
-template <int kLanes, int kR>
+template <class T, int kLanes, int kQ, int kR>
 int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
-    const auto kernel = paged_few_kernel<kLanes, kR>;
-    constexpr int smem = kR * kLanes * 16 + kFewThreads / 32 * kR * (kLanes * 16 + 8);
+    const auto kernel = paged_few_kernel<T, kLanes, kQ, kR>;
+    constexpr int smem = kR * kLanes * kQ * 16 + kFewThreads / 32 * kR * (kLanes * kQ * 16 + 8);
     static SharedOnce once;
     if (!once.allow(kernel, smem)) return cuda_failure();
     return launch_next_shared(kernel, dim3(ctas), kFewThreads, smem, stream, a);
 }
 template <int kR>
-int run_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
-    if (a.head_dim <= 32) return run_few<8, kR>(a, ctas, stream);
-    return a.head_dim <= 64 ? run_few<16, kR>(a, ctas, stream) : run_few<32, kR>(a, ctas, stream);
+int run_few(const PagedArgs& a, bool bf16, int ctas, cudaStream_t stream) {
+    if constexpr (kR <= 4) {
+        if (bf16) return run_few<__nv_bfloat16, 32, 2, kR>(a, ctas, stream);
+        if (a.head_dim > 128) return run_few<float, 32, 2, kR>(a, ctas, stream);
+    }
+    if (a.head_dim <= 32) return run_few<float, 8, 1, kR>(a, ctas, stream);
+    return a.head_dim <= 64 ? run_few<float, 16, 1, kR>(a, ctas, stream) : run_few<float, 32, 1, kR>(a, ctas, stream);
 }
 template <class T>
 int run_block(const PagedArgs& a, int ctas, cudaStream_t stream) {
@@ -654,9 +677,9 @@ int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t
     int code;
     switch (s.form) {
         case Form::Mma: code = launch_paged_mma(a, s.ctas, stream); break;
-        case Form::Few1: code = run_few<1>(a, s.ctas, stream); break;
-        case Form::Few4: code = run_few<4>(a, s.ctas, stream); break;
-        case Form::Few8: code = run_few<8>(a, s.ctas, stream); break;
+        case Form::Few1: code = run_few<1>(a, bf16, s.ctas, stream); break;
+        case Form::Few4: code = run_few<4>(a, bf16, s.ctas, stream); break;
+        case Form::Few8: code = run_few<8>(a, bf16, s.ctas, stream); break;
         default: code = bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
     }
     if (code != USM_OK) return code;
