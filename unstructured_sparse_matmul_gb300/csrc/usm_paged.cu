@@ -5,7 +5,8 @@
 // the two halves of eight or four pairs) in registers and walks over heads of
 // its token with it, so the table is read once a token and not once a head, and
 // queries, keys and values go through in one launch.  Bound: HBM, each element
-// read and written once.
+// read and written once: 16384 tokens of 32 + 8 + 8 heads of 128 columns (405 MB) take
+// 65 us, 6.2 TB/s; 32 tokens 2.6 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
