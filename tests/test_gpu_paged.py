@@ -312,6 +312,21 @@ def test_infinities_and_nan_in_values(usm, dtype, where):
     assert_near(np.where(finite, out, 0), np.where(finite, ref, 0), b)
 
 
+@pytest.mark.parametrize("lengths", [[9], [3000], [700] * 40])
+@pytest.mark.parametrize("heads,count", [(1, 1), (4, 1), (8, 1), (2, 45)])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])
+def test_nan_in_a_query(usm, dtype, D, heads, count, lengths):
+    """A token with a NaN gets NaN, however its keys are divided; its neighbours
+    keep their bits."""
+    p = Problem("query", lengths, [min(count, n) for n in lengths], heads=heads, kv=1, D=D, dtype=dtype)
+    before = got(p.run(usm))
+    p.q[-1, 0, 3] = np.nan
+    x = got(p.run(usm))
+    assert np.isnan(x[-1, 0]).all()
+    x[-1, 0] = before[-1, 0]
+    assert np.isfinite(before).all() and np.array_equal(x, before)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_masked_scores(usm, dtype):
     """Keys whose score is -inf weigh nothing; a row of them is zero."""

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int w = 0; w < kWarps; ++w) {
                 const float2 st = stats[w * kR + r];
-                if (st.x == -INFINITY) continue;
+                if (st.x == -INFINITY && st.y == 0.f) continue;
                 const float f = weight_of(st.x, top, c);
                 sum = fmaf(st.y, f, sum);
                 x = add_scaled(x, sums[(w * kR + r) * kRow + at], f);
@@ -497,9 +497,10 @@ struct JoinSum {
     float2 stat;  // (reference, sum of weights)
     float4 x;
 };
-// Adds a part to sums with a reference that is no less.
+// Adds a part to sums with a reference that is no less.  One without a reference
+// saw no key, or only scores of NaN: those are its sum as well, and go on.
 __device__ __forceinline__ void add_part(JoinSum& sum, float2 stat, float4 x, float scale_log2) {
-    if (stat.x == -INFINITY) return;  // no key seen there
+    if (stat.x == -INFINITY && stat.y == 0.f) return;
     const float w = weight_of(stat.x, sum.stat.x, scale_log2);
     sum.stat.y = fmaf(stat.y, w, sum.stat.y);
     sum.x = add_scaled(sum.x, x, w);
