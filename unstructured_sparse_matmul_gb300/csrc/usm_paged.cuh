@@ -193,6 +193,7 @@ struct PagedShares {
                     return;
                 }
             }
+            if (search) left = 0;  // not found: the counts changed under the call
             if (search || !share_of(sum, cta, ctas, u0)) return;
         }
     }
@@ -203,6 +204,7 @@ struct PagedShares {
         constexpr int kWarps = kThreads / 32;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         long long mine = 0, before = 0, u0 = 0;
+        if (threadIdx.x == 0) scratch[kWarps] = -1;  // not found: the counts changed under the call
         left = 0;
         b = a.num_seqs;
         block = blocks = head = unit = 0;
@@ -233,11 +235,13 @@ struct PagedShares {
         }
         __syncthreads();
         b = (int)scratch[kWarps];
-        find(a, scratch[kWarps + 1]);
+        if (b < 0) left = 0;
+        else find(a, scratch[kWarps + 1]);
     }
 
     // The block, head and tile `skip` units behind sequence b's first; every warp
-    // searches for itself.
+    // searches for itself.  (Held to what there is, should lengths change under the
+    // call: the walk ends whatever it reads.)
     __device__ __forceinline__ void find(const PagedArgs& a, long long skip) {
         s = paged_seq(a, b);
         blocks = blocks_of(a, s);
@@ -258,8 +262,8 @@ struct PagedShares {
             base = __shfl_sync(kFullMask, scan, 31);
         }
         k = paged_block<kRows, kKeys>(a, s, block);
-        head = (int)divide(skip, k.tiles + kCost);
-        unit = (int)(skip - (long long)head * (k.tiles + kCost));
+        head = (int)min(divide(skip, k.tiles + kCost), (long long)a.kv_heads - 1);
+        unit = (int)min(skip - (long long)head * (k.tiles + kCost), (long long)k.tiles + kCost);
     }
 
     // On to the next item; whole warp.
