@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "usm_internal.h"
 #include "usm_paged.cuh"
@@ -88,9 +89,11 @@ __device__ __forceinline__ float* part_of(const PagedArgs& a, long long slot, in
 // 64 keys pass through it, fp32 ones copied asynchronously one tile ahead.  Each
 // of 256 threads holds 4 rows x 4 keys of the scores and 4 rows x up to 16
 // columns of the sums, all in pairs (two FMAs an instruction); 12 wavefronts of
-// shared memory feed 64 FMAs of a warp.  1024 tokens over 4096 keys, 8 heads: 33
-// TFLOP/s at 128 columns, 26 at 64.  Bound by latency and moves, with 8 warps an SM;
-// two CTAs an SM with one tile each, or weights stored in pairs, were no faster.
+// shared memory feed 64 FMAs of a warp.  Columns come in groups of 64 and, behind
+// them, one of 32 (heads of 80 columns do the work of 96, not 128: 376 against 401
+// us).  1024 tokens over 4096 keys, 8 heads: 32 TFLOP/s at 128 columns, 25 at 80, 27
+// at 64.  Bound by latency and moves, with 8 warps an SM; two CTAs an SM with one
+// tile each, or weights stored in pairs, were no faster.
 // ---------------------------------------------------------------------------
 constexpr int kBlockRows = 64, kBlockKeys = 64, kBlockThreads = 256;
 constexpr int kBlockWeights = kBlockKeys + 4;  // pitch of a row of weights
@@ -112,10 +115,14 @@ __device__ __forceinline__ void copy4(float* to, const __nv_bfloat16* from, bool
     *reinterpret_cast<float4*>(to) = there ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// o += P·V for 4 rows and columns 64·c + 4·tx.. of a tile.
+__device__ __forceinline__ void store2(float x, float y, float* p) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(float x, float y, __nv_bfloat16* p) { *reinterpret_cast<uint32_t*>(p) = bf16x2(x, y); }
+
+// o += P·V for 4 rows of a tile and this thread's columns: 64·c + 4·tx.. of whole
+// groups of 64 and, where kWide is odd, 2·tx.. of the 32 behind them.
 template <int kWide, bool kGuard>
 __device__ __forceinline__ void add_values(const float* p, const float* v, int pitch, int D, int tx, int key0, const int2 (&seen)[4],
-                                           uint64_t (&o)[4][2 * kWide]) {
+                                           uint64_t (&o)[4][kWide]) {
 #pragma unroll 2
     for (int key = 0; key < kBlockKeys; key += 4) {
         float4 w[4];
@@ -123,12 +130,18 @@ __device__ __forceinline__ void add_values(const float* p, const float* v, int p
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + i * kBlockWeights + key);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            ulonglong2 y[kWide];
+            uint64_t y[kWide];
 #pragma unroll
-            for (int c = 0; c < kWide; ++c) {
+            for (int c = 0; c < kWide / 2; ++c) {
                 const int col = 64 * c + 4 * tx;
-                y[c] = make_ulonglong2(0, 0);
-                if (col < D) y[c] = *reinterpret_cast<const ulonglong2*>(v + (key + u) * pitch + col);
+                ulonglong2 w = make_ulonglong2(0, 0);
+                if (col < D) w = *reinterpret_cast<const ulonglong2*>(v + (key + u) * pitch + col);
+                y[2 * c] = w.x, y[2 * c + 1] = w.y;
+            }
+            if (kWide % 2) {
+                const int col = 32 * (kWide - 1) + 2 * tx;
+                y[kWide - 1] = 0;
+                if (col < D) y[kWide - 1] = *reinterpret_cast<const uint64_t*>(v + (key + u) * pitch + col);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -136,23 +149,20 @@ __device__ __forceinline__ void add_values(const float* p, const float* v, int p
                 if (kGuard && (key0 + key + u < seen[i].x || key0 + key + u >= seen[i].y)) continue;
                 const uint64_t e2 = pack2(e, e);
 #pragma unroll
-                for (int c = 0; c < kWide; ++c) {
-                    o[i][2 * c] = fma2(e2, y[c].x, o[i][2 * c]);
-                    o[i][2 * c + 1] = fma2(e2, y[c].y, o[i][2 * c + 1]);
-                }
+                for (int c = 0; c < kWide; ++c) o[i][c] = fma2(e2, y[c], o[i][c]);
             }
         }
     }
 }
 
-template <class T, int kWide>  // kWide: groups of 64 columns
+template <class T, int kWide>  // kWide: groups of 32 columns
 __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ float4 smem_raw[];
     __shared__ long long scratch[kBlockThreads / 32 + 2];
     __shared__ PagedSegment seg;
     await_previous();
     let_next_start();
-    constexpr int kStages = kWide <= 2 ? 2 : 1;
+    constexpr int kStages = block_stages(32 * kWide);
     constexpr int kP = kBlockWeights;
     const int D = a.head_dim, pitch = block_pitch(D);
     float* q = reinterpret_cast<float*>(smem_raw);
@@ -195,14 +205,14 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
         };
         int2 seen[4];
         float m[4], l[4];
-        uint64_t o[4][2 * kWide];
+        uint64_t o[4][kWide];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             seen[i] = paged_seen(a, g, ty * 4 + i);
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2 * kWide; ++j) o[i][j] = 0;
+            for (int j = 0; j < kWide; ++j) o[i][j] = 0;
         }
         const int n = g.tiles;
         load(0);
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
                 l[i] = l[i] * f + sum;  // this thread's keys
                 const uint64_t f2 = pack2(f, f);
 #pragma unroll
-                for (int j = 0; j < 2 * kWide; ++j) o[i][j] = mul2(o[i][j], f2);
+                for (int j = 0; j < kWide; ++j) o[i][j] = mul2(o[i][j], f2);
                 partly |= seen[i].x > key0 || seen[i].y < key0 + kBlockKeys;
             }
             __syncwarp();  // a warp's rows of p are its own
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
             const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
             T* out = output_of<T>(a, g, r);
 #pragma unroll
-            for (int c = 0; c < kWide; ++c) {
+            for (int c = 0; c < kWide / 2; ++c) {
                 const int col = 64 * c + 4 * tx;
                 if (col >= D) continue;
                 float4 x;
@@ -287,6 +297,12 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
                 unpack2(o[i][2 * c + 1], x.z, x.w);
                 if (whole) store4(scaled(x, z), out + col);
                 else store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, col / 4));
+            }
+            if (const int col = 32 * (kWide - 1) + 2 * tx; kWide % 2 && col < D) {
+                float x, y;
+                unpack2(o[i][kWide - 1], x, y);
+                if (whole) store2(x * z, y * z, out + col);
+                else store2(x, y, part_of(a, 2LL * blockIdx.x + g.part, r, col / 4) + col % 4);
             }
             if (!whole && tx == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(m[i], l[i]);
         }
@@ -626,7 +642,7 @@ int run_block(PagedArgs a, int ctas, cudaStream_t stream) {
     const auto kernel = paged_block_kernel<T, kWide>;
     const int smem = block_smem(a.head_dim);
     static SharedOnce once;
-    if (!once.allow(kernel, block_smem(64 * kWide))) return cuda_failure();
+    if (!once.allow(kernel, block_smem(32 * kWide))) return cuda_failure();
     return launch_next_shared(kernel, dim3(ctas), kBlockThreads, smem, stream, a);
 }
 
@@ -649,9 +665,15 @@ int run_few(const PagedArgs& a, bool bf16, int ctas, cudaStream_t stream) {
 }
 template <class T>
 int run_block(const PagedArgs& a, int ctas, cudaStream_t stream) {
-    if (a.head_dim <= 64) return run_block<T, 1>(a, ctas, stream);
-    if (a.head_dim <= 128) return run_block<T, 2>(a, ctas, stream);
-    return a.head_dim <= 192 ? run_block<T, 3>(a, ctas, stream) : run_block<T, 4>(a, ctas, stream);
+    if constexpr (std::is_same_v<T, float>) {  // bf16 of up to 128 columns: the matrix kernel
+        if (a.head_dim <= 32) return run_block<T, 1>(a, ctas, stream);
+        if (a.head_dim <= 64) return run_block<T, 2>(a, ctas, stream);
+        if (a.head_dim <= 96) return run_block<T, 3>(a, ctas, stream);
+        if (a.head_dim <= 128) return run_block<T, 4>(a, ctas, stream);
+    }
+    if (a.head_dim <= 160) return run_block<T, 5>(a, ctas, stream);
+    if (a.head_dim <= 192) return run_block<T, 6>(a, ctas, stream);
+    return a.head_dim <= 224 ? run_block<T, 7>(a, ctas, stream) : run_block<T, 8>(a, ctas, stream);
 }
 
 template <class T>
