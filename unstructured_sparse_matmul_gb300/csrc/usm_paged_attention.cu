@@ -12,17 +12,21 @@
 namespace usm {
 namespace {
 
-template <class T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
+// Four elements, as they lie in memory and as floats.
+__device__ __forceinline__ float4 quad4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ uint2 quad4(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ void quads8(const __nv_bfloat16* p, uint2* x) {  // two at once
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    x[0] = make_uint2(w.x, w.y), x[1] = make_uint2(w.z, w.w);
 }
-template <>
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+__device__ __forceinline__ float4 floats(float4 x) { return x; }
+__device__ __forceinline__ float4 floats(uint2 w) {
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xffff0000u));
+}
+template <class T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    return floats(quad4(p));
 }
 __device__ __forceinline__ void store4(float4 x, float* p) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(float4 x, __nv_bfloat16* p) {
@@ -311,14 +315,20 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
 }
 
 // ---------------------------------------------------------------------------
-// fp32 caches and wide bf16 heads, few rows (single tokens): every warp takes batches of keys straight
-// from memory, kLanes lanes a key, four columns each.  A lane's partial products
-// of a batch are summed across lanes all at once, halving the number of values a
-// lane holds with every step, so that a score costs about one shuffle; each lane
-// then has one key's weight, which goes back to all for the sums.  16 warps an SM
-// keep 64 to 128 KB of keys and values on the way.  Bound by HBM: 16 tokens over
-// 4096 keys of 64 columns (227 MB) take 51 us, 10 of them start and joining; 4 rows
-// a head of 128 columns read 4.2 TB/s, 8 rows 2.5, one of 256 bf16 columns 3.6.
+// fp32 caches and wide bf16 heads, few rows (single tokens): every warp takes
+// batches of keys straight from memory, kLanes lanes a key, four columns each (wide
+// heads: eight).  A batch's scores come first, then the weights, then the sums: a key
+// is widened once for all rows, and its registers are free again when the values
+// are used.  A lane's partial products of a row are summed across lanes all at once,
+// halving the number of values a lane holds with every step, so that a score costs
+// about one shuffle; each lane then has one key's weight, which goes back to all for
+// the sums.  16 warps an SM keep 64 to 128 KB of keys and values on the way.  Bound
+// by HBM with one row (16 tokens over 4096 fp32 keys of 64 columns, 227 MB: 51 us,
+// 10 of them start and joining; 32 over 4096 bf16 keys of 256 columns: 5.4 TB/s),
+// by instructions with more: 4.5 TB/s with 4 rows of 128 fp32 columns, 2.6 with 8,
+// 3.2 with 4 rows of 256 bf16 columns, 4.3 in fp32.  (Row by row with keys and
+// values held as floats: 4.2, 2.5, 1.7 and 3.6; bf16 quads 128 columns apart, in
+// loads of 8 bytes: 3.9 with one row.)
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256, kFewKeys = 128;
 
@@ -327,10 +337,12 @@ template <class T, int kLanes, int kQ, int kR>
 __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_constant__ PagedArgs a) {
     using Shares = PagedShares<kR, kFewKeys, kFewThreads, 2>;
     constexpr int kWarps = kFewThreads / 32, kSide = 32 / kLanes;
-    constexpr int kLoads = kR <= 4 && kQ == 1 ? 8 : 4;  // of keys, and of values, of a batch
+    // Loads of keys, and of values, of a batch: what fits the registers.
+    constexpr int kRegs = sizeof(T) * kQ;  // of a load
+    constexpr int kLoads = kR == 1 && kRegs <= 4 || kR == 4 && kQ == 1 ? 8 : kR == 4 && kRegs == 8 ? 2 : 4;
     constexpr int kRow = kQ * kLanes;             // quads of columns
     constexpr int kBatch = kLoads * kSide;        // keys
-    constexpr int kSteps = kLoads == 8 ? 3 : 2;   // that halve the values
+    constexpr int kSteps = kLoads == 8 ? 3 : kLoads / 2;  // that halve the values
     extern __shared__ float4 smem_raw[];          // queries [row][lane]; sums [warp][row][lane]; (reference, sum) [warp][row]
     __shared__ int2 sees[kR];
     __shared__ long long scratch[kWarps + 2];
@@ -338,10 +350,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
     await_previous();
     let_next_start();
     const int D = a.head_dim, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int side = lane / kLanes, col = 4 * (lane % kLanes);
-    bool column[kQ];
+    // Quad h of a lane, at = h·kLanes + lane in shared memory, is this quad of a row.
+    static_assert(kQ == 1 || kLanes == 32);
+    const auto quad_of = [](int at) { return sizeof(T) == 2 ? at % 32 * 2 + at / 32 : at; };
+    const int side = lane / kLanes, col = 4 * quad_of(lane % kLanes);
+    bool there[kQ];
 #pragma unroll
-    for (int h = 0; h < kQ; ++h) column[h] = col + 128 * h < D;
+    for (int h = 0; h < kQ; ++h) there[h] = col + 128 * h < D;
     float4* queries = smem_raw;
     float4* sums = queries + kR * kRow;
     float2* stats = reinterpret_cast<float2*>(sums + kWarps * kR * kRow);
@@ -360,8 +375,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
         if (!seg.live) break;
         const PagedSegment& g = seg;
         for (int i = tid; i < kR * kRow; i += kFewThreads) {
-            const int r = i / kRow, at = i % kRow;
-            queries[i] = r < g.rows && 4 * at < D ? load4(query_of<T>(a, g, r) + 4 * at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const int r = i / kRow, at = i % kRow, quad = quad_of(at);
+            queries[i] = r < g.rows && 4 * quad < D ? load4(query_of<T>(a, g, r) + 4 * quad) : make_float4(0.f, 0.f, 0.f, 0.f);
             if (at == 0) sees[r] = paged_seen(a, g, r);
         }
         __syncthreads();
@@ -387,47 +402,60 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
         for (int base = first; base < end; base += kWarps * kBatch) {
             const int2 w = next;
             next = slot_of(base + kWarps * kBatch);
-            float4 k[kLoads][kQ], v[kLoads][kQ];
+            decltype(quad4(kb)) k[kLoads][kQ], v[kLoads][kQ];
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int page = __shfl_sync(kFullMask, w.x, j * kSide + side), slot = __shfl_sync(kFullMask, w.y, j * kSide + side);
+                if constexpr (sizeof(T) == 2) {  // a row's width is a multiple of 16 bytes: both quads are there, or none
+                    k[j][0] = v[j][0] = k[j][1] = v[j][1] = {};
+                    if (page >= 0 && col < D) {
+                        quads8(kb + page * a.k_page + slot * a.k_slot, k[j]);
+                        quads8(vb + page * a.v_page + slot * a.v_slot, v[j]);
+                    }
+                } else {
 #pragma unroll
-                for (int h = 0; h < kQ; ++h) {
-                    k[j][h] = v[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (page >= 0 && column[h]) {
-                        k[j][h] = load4(kb + page * a.k_page + slot * a.k_slot + 128 * h);
-                        v[j][h] = load4(vb + page * a.v_page + slot * a.v_slot + 128 * h);
+                    for (int h = 0; h < kQ; ++h) {
+                        k[j][h] = v[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (page >= 0 && there[h]) {
+                            k[j][h] = quad4(kb + page * a.k_page + slot * a.k_slot + 128 * h);
+                            v[j][h] = quad4(vb + page * a.v_page + slot * a.v_slot + 128 * h);
+                        }
                     }
                 }
             }
+            float s[kR][kLoads];
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                float s[kLoads];
+            for (int h = 0; h < kQ; ++h)
 #pragma unroll
-                for (int h = 0; h < kQ; ++h) {
-                    const float4 q = queries[r * kRow + h * kLanes + lane % kLanes];
+                for (int j = 0; j < kLoads; ++j) {
+                    const float4 y = floats(k[j][h]);
 #pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        const float x = h == 0 ? q.x * k[j][h].x : fmaf(q.x, k[j][h].x, s[j]);
-                        s[j] = fmaf(q.w, k[j][h].w, fmaf(q.z, k[j][h].z, fmaf(q.y, k[j][h].y, x)));
+                    for (int r = 0; r < kR; ++r) {
+                        const float4 q = queries[r * kRow + h * kLanes + lane % kLanes];
+                        const float x = h == 0 ? q.x * y.x : fmaf(q.x, y.x, s[r][j]);
+                        s[r][j] = fmaf(q.w, y.w, fmaf(q.z, y.z, fmaf(q.y, y.y, x)));
                     }
                 }
+            const int key = base + mine * kSide + side;
+            float p[kR];
+            bool all = true;
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     const int half = kLoads >> (i + 1), mask = kLanes >> (i + 1);
                     const bool upper = lane & mask;
 #pragma unroll
                     for (int j = 0; j < half; ++j) {
-                        const float give = upper ? s[j] : s[j + half], keep = upper ? s[j + half] : s[j];
-                        s[j] = keep + __shfl_xor_sync(kFullMask, give, mask);
+                        const float give = upper ? s[r][j] : s[r][j + half], keep = upper ? s[r][j + half] : s[r][j];
+                        s[r][j] = keep + __shfl_xor_sync(kFullMask, give, mask);
                     }
                 }
 #pragma unroll
-                for (int mask = kLanes >> (kSteps + 1); mask > 0; mask >>= 1) s[0] += __shfl_xor_sync(kFullMask, s[0], mask);
-                const int key = base + mine * kSide + side;
+                for (int mask = kLanes >> (kSteps + 1); mask > 0; mask >>= 1) s[r][0] += __shfl_xor_sync(kFullMask, s[r][0], mask);
                 const int2 seen = sees[r];
                 const bool use = key >= max(lo, seen.x) && key < min(end, seen.y);
-                const float x = use ? s[0] : -INFINITY;
+                const float x = use ? s[r][0] : -INFINITY;
                 if (__any_sync(kFullMask, x > m[r])) {
                     float top = x;
 #pragma unroll
@@ -439,19 +467,26 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 #pragma unroll
                     for (int h = 0; h < kQ; ++h) o[r][h] = scaled(o[r][h], f);
                 }
-                const float p = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
-                l[r] += p;
-                // Where some key of the batch is not seen a weight of 0 takes no value.
-                const bool all = __all_sync(kFullMask, use);
+                p[r] = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
+                l[r] += p[r];
+                all &= use;
+            }
+            // Where some key of the batch is not seen a weight of 0 takes no value.
+            all = __all_sync(kFullMask, all);
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j) {
-                    int from = side * kLanes;
+            for (int j = 0; j < kLoads; ++j) {
+                int from = side * kLanes;
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
-                    const float pj = __shfl_sync(kFullMask, p, from);
+                for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
+                float4 y[kQ];
+#pragma unroll
+                for (int h = 0; h < kQ; ++h) y[h] = floats(v[j][h]);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float pj = __shfl_sync(kFullMask, p[r], from);
                     if (all || pj != 0.f)
 #pragma unroll
-                        for (int h = 0; h < kQ; ++h) o[r][h] = add_scaled(o[r][h], v[j][h], pj);
+                        for (int h = 0; h < kQ; ++h) o[r][h] = add_scaled(o[r][h], y[h], pj);
                 }
             }
         }
@@ -475,8 +510,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
         }
         __syncthreads();
         for (int i = tid; i < kR * kRow; i += kFewThreads) {
-            const int r = i / kRow, at = i % kRow;
-            if (r >= g.rows || 4 * at >= D) continue;
+            const int r = i / kRow, at = i % kRow, quad = quad_of(at);
+            if (r >= g.rows || 4 * quad >= D) continue;
             float top = -INFINITY, sum = 0.f;
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * kR + r].x);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -488,10 +523,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
                 x = add_scaled(x, sums[(w * kR + r) * kRow + at], f);
             }
             if (g.part == kPartWhole) {
-                store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<T>(a, g, r) + 4 * at);
+                store4(scaled(x, sum == 0.f ? 0.f : 1.f / sum), output_of<T>(a, g, r) + 4 * quad);
             } else {
                 const long long row = (2LL * blockIdx.x + g.part) * a.part_rows + r;
-                store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, at));
+                store4(x, part_of(a, 2LL * blockIdx.x + g.part, r, quad));
                 if (at == 0) *reinterpret_cast<float2*>(a.part_stats + 2 * row) = make_float2(top, sum);
             }
         }
