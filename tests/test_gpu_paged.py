@@ -312,6 +312,23 @@ def test_infinities_and_nan_in_values(usm, dtype, where):
     assert_near(np.where(finite, out, 0), np.where(finite, ref, 0), b)
 
 
+@pytest.mark.parametrize("length", [40, 1040])
+@pytest.mark.parametrize("heads", [1, 2, 8])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])
+def test_infinity_under_a_weight_of_zero(usm, dtype, D, heads, length):
+    """An infinity that a token sees reaches its row although its weight is 0 in
+    fp32 (0·inf is not finite either); the token before does not see it."""
+    p = Problem("zero weight", [length], [3], heads=heads, kv=1, D=D, dtype=dtype)
+    key = length - 2
+    p.q[..., 0] = 40
+    p.k[..., 0] = np.where(np.isnan(p.k[..., 0]), np.nan, 0)
+    p.k[p.table[0, key // 16], key % 16, 0, 0] = -40  # 2^-2308 against a score of 0, the others within 2^60
+    p.v[p.table[0, key // 16], key % 16, 0, 5] = np.inf
+    seen = np.zeros((3, heads, D), bool)
+    seen[1:, :, 5] = True
+    assert np.array_equal(~np.isfinite(got(p.run(usm, scale=1.0))), seen)
+
+
 @pytest.mark.parametrize("lengths", [[9], [3000], [700] * 40])
 @pytest.mark.parametrize("heads,count", [(1, 1), (4, 1), (8, 1), (2, 45)])
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])

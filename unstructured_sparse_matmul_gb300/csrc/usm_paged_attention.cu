@@ -467,28 +467,32 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 #pragma unroll
                     for (int h = 0; h < kQ; ++h) o[r][h] = scaled(o[r][h], f);
                 }
-                p[r] = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
-                l[r] += p[r];
+                const float weight = x == -INFINITY ? 0.f : exp2_fast((x - m[r]) * c);
+                l[r] += weight;
+                p[r] = use ? weight : -1.f;
                 all &= use;
             }
-            // Where some key of the batch is not seen a weight of 0 takes no value.
-            all = __all_sync(kFullMask, all);
+            // Keys that a row does not see (-1) are left out, not weighed by 0.
+            const auto add_values = [&](auto guard) {
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                int from = side * kLanes;
+                for (int j = 0; j < kLoads; ++j) {
+                    int from = side * kLanes;
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
-                float4 y[kQ];
+                    for (int i = 0; i < kSteps; ++i) from |= (j & (kLoads >> (i + 1))) ? kLanes >> (i + 1) : 0;
+                    float4 y[kQ];
 #pragma unroll
-                for (int h = 0; h < kQ; ++h) y[h] = floats(v[j][h]);
+                    for (int h = 0; h < kQ; ++h) y[h] = floats(v[j][h]);
 #pragma unroll
-                for (int r = 0; r < kR; ++r) {
-                    const float pj = __shfl_sync(kFullMask, p[r], from);
-                    if (all || pj != 0.f)
+                    for (int r = 0; r < kR; ++r) {
+                        const float pj = __shfl_sync(kFullMask, p[r], from);
+                        if (guard && pj < 0.f) continue;
 #pragma unroll
                         for (int h = 0; h < kQ; ++h) o[r][h] = add_scaled(o[r][h], y[h], pj);
+                    }
                 }
-            }
+            };
+            if (__all_sync(kFullMask, all)) add_values(std::false_type());
+            else add_values(std::true_type());
         }
         // Keys of a warp's sides, then the warps.
 #pragma unroll
