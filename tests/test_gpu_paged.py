@@ -312,6 +312,13 @@ def test_infinities_and_nan_in_values(usm, dtype, where):
     assert_near(np.where(finite, out, 0), np.where(finite, ref, 0), b)
 
 
+@pytest.mark.parametrize("D", [24, 64, 128, 136, 200, 256])
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_single_tokens_of_few_rows(usm, dtype, group, D):
+    Problem("few", [700, 33, 1], [1, 1, 1], heads=2 * group, kv=2, D=D, dtype=dtype).check(usm)
+
+
 @pytest.mark.parametrize("length", [40, 1040])
 @pytest.mark.parametrize("heads", [1, 2, 8])
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])
@@ -330,7 +337,7 @@ def test_infinity_under_a_weight_of_zero(usm, dtype, D, heads, length):
 
 
 @pytest.mark.parametrize("lengths", [[9], [3000], [700] * 40])
-@pytest.mark.parametrize("heads,count", [(1, 1), (4, 1), (8, 1), (2, 45)])
+@pytest.mark.parametrize("heads,count", [(1, 1), (2, 1), (4, 1), (8, 1), (2, 45)])
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])
 def test_nan_in_a_query(usm, dtype, D, heads, count, lengths):
     """A token with a NaN gets NaN, however its keys are divided; its neighbours

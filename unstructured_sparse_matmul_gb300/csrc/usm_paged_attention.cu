@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
 // about one shuffle; each lane then has one key's weight, which goes back to all for
 // the sums.  16 warps an SM keep 64 to 128 KB of keys and values on the way.  Bound
 // by HBM with one row (16 tokens over 4096 fp32 keys of 64 columns, 227 MB: 51 us,
-// 10 of them start and joining; 32 over 4096 bf16 keys of 256 columns: 5.4 TB/s),
-// by instructions with more: 4.5 TB/s with 4 rows of 128 fp32 columns, 2.6 with 8,
-// 3.2 with 4 rows of 256 bf16 columns, 4.3 in fp32.  (Row by row with keys and
-// values held as floats: 4.2, 2.5, 1.7 and 3.6; bf16 quads 128 columns apart, in
-// loads of 8 bytes: 3.9 with one row.)
+// 10 of them start and joining; 32 over 4096 bf16 keys of 256 columns: 5.5 TB/s),
+// by instructions with more: 128 fp32 columns 5.0 TB/s with 2 rows, 4.6 with 4, 2.7
+// with 8; 256 columns 5.2 with 2 and 4.6 with 4, in bf16 3.5 with 4.  (Row by row
+// with keys and values held as floats: 4.2, 2.5, 3.6 and 1.7 with 4, 8, 4 and 4; 2
+// rows as 4: 4.5 and 4.4, 192 bf16 columns 2.5 for 4.4; bf16 quads 128 columns
+// apart, in loads of 8 bytes: 3.9 with one row.)
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256, kFewKeys = 128;
 
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
     constexpr int kWarps = kFewThreads / 32, kSide = 32 / kLanes;
     // Loads of keys, and of values, of a batch: what fits the registers.
     constexpr int kRegs = sizeof(T) * kQ;  // of a load
-    constexpr int kLoads = kR == 1 && kRegs <= 4 || kR == 4 && kQ == 1 ? 8 : kR == 4 && kRegs == 8 ? 2 : 4;
+    constexpr int kLoads = kR <= 2 && kRegs <= 4 || kR == 4 && kQ == 1 ? 8 : kR == 4 && kRegs == 8 ? 2 : 4;
     constexpr int kRow = kQ * kLanes;             // quads of columns
     constexpr int kBatch = kLoads * kSide;        // keys
     constexpr int kSteps = kLoads == 8 ? 3 : kLoads / 2;  // that halve the values
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __gri
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-enum class Form { Mma, Block, Few1, Few4, Few8 };
+enum class Form { Mma, Block, Few1, Few2, Few4, Few8 };
 struct Shape {
     Form form;
     int rows;  // of a block
@@ -666,6 +667,7 @@ Shape shape_of(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim
     if (bf16 && head_dim <= 128) return Shape{Form::Mma, paged_mma_rows(), sms};
     const long long rows = (long long)tokens * (q_heads / kv_heads);
     if (rows <= num_seqs) return Shape{Form::Few1, 1, 2 * sms};
+    if (rows <= 2LL * num_seqs) return Shape{Form::Few2, 2, 2 * sms};
     if (rows <= 8LL * num_seqs)
         return rows <= 4LL * num_seqs || head_dim > 128 ? Shape{Form::Few4, 4, 2 * sms} : Shape{Form::Few8, 8, 2 * sms};
     const int fit = std::max(1, std::min(2, 220 * 1024 / block_smem(head_dim)));
@@ -746,6 +748,7 @@ int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t
     switch (s.form) {
         case Form::Mma: code = launch_paged_mma(a, s.ctas, stream); break;
         case Form::Few1: code = run_few<1>(a, bf16, s.ctas, stream); break;
+        case Form::Few2: code = run_few<2>(a, bf16, s.ctas, stream); break;
         case Form::Few4: code = run_few<4>(a, bf16, s.ctas, stream); break;
         case Form::Few8: code = run_few<8>(a, bf16, s.ctas, stream); break;
         default: code = bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
