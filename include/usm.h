@@ -524,9 +524,9 @@ int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, 
  *   workspace : paged_attention_workspace_bytes(...) bytes of device scratch,
  *            16-byte aligned, contents ignored.  The size follows from the arguments
  *            and the number of SMs of the current device (up to 44 MB).
- * Products, statistics and sums are fp32.  bf16: probabilities are rounded to
- * bf16 before their product with V (relative 2^-9 each, as the output's own
- * rounding); head_dim > 128 keeps them in fp32.
+ * Products, statistics and sums are fp32.  bf16: probabilities go into their product
+ * with V as two bf16 parts (relative 2^-16 each; the output's own rounding is
+ * 2^-8); head_dim > 128 keeps them in fp32.
  * A token that sees no key, or whose scores are all -inf, gives a zero row.  Keys
  * and values that a token does not see never touch its row, whatever they hold
  * (unwritten slots, later tokens, NaN or infinities); an infinity in a row of V that

@@ -1,0 +1,41 @@
+"""The paged cache where its calls could go wrong: precision of the weights,
+sizes next to the limits, batches of unequal sequences, infinities under weights
+of zero, calls beside other kernels.  Against the 64-bit definitions in paged_ref."""
+import numpy as np
+import pytest
+
+import paged_ref as R
+from test_gpu_paged import SHAPES, Problem, assert_near, got
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ("f32", "bf16")
+
+
+# ---------------------------------------------------------------------------
+# Precision
+# ---------------------------------------------------------------------------
+PRECISE = {  # name -> Problem's arguments
+    "tokens": dict(lengths=[1000, 129, 2000], counts=[1] * 3, heads=8, kv=2, D=128),
+    "draft": dict(lengths=[260, 1025], counts=[5] * 2, heads=8, kv=2, D=64, page=32),
+    "chunk": dict(lengths=[700, 300], counts=[300, 300], heads=4, kv=2, D=128, page=64),
+    "ragged": dict(lengths=[400, 130, 700], counts=[100, 130, 1], heads=6, kv=2, D=96, page=24),
+    "wide": dict(lengths=[400, 130], counts=[100, 1], heads=4, kv=2, D=192),
+}
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("name", sorted(PRECISE))
+def test_weights_are_not_rounded_to_bf16(usm, name, window):
+    """bf16 caches: beside the output's own rounding (2^-8) a weight is off by 2^-16 at
+    most (its bf16 form leaves up to 2^-8 of it, held to 2^-8 again), and
+    everything else as in fp32."""
+    kw = dict(PRECISE[name])
+    p = Problem(name, kw.pop("lengths"), kw.pop("counts"), dtype="bf16", **kw)
+    scale = p.D ** -0.5
+    x = got(p.run(usm, scale, window=window))
+    args = lambda v: (p.q.astype(np.float64), p.k.astype(np.float64), v, p.table, p.lengths, p.counts, p.starts, scale)
+    v = p.v.astype(np.float64)
+    ref, bound = R.attention(*args(v), window=window, dtype="f32")
+    mass, _ = R.attention(*args(np.abs(v)), window=window, dtype="f32")
+    assert_near(x, ref, bound + 1.01 * 2.0 ** -16 * mass + R.HALF_STEP["bf16"] * np.abs(ref))

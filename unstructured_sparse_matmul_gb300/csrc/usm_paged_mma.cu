@@ -6,20 +6,27 @@
 // 256 rows (tokens x the heads that share keys) in two halves of 128, one row a
 // lane of tensor memory:
 //   S = Q·K^T    both from shared memory, 128 x 128 fp32 in tensor memory;
-//   P = 2^(S·c - m·c), a row a thread, in bf16 over S's own columns;
-//   O += P·V     P from tensor memory, V from shared memory, fp32 in tensor memory.
+//   P = 2^(S·c - m·c), a row a thread, over S's own columns: two bf16 parts, the
+//     rounded weight and what that leaves, which hold a weight to 2^-16 (the rounding
+//     alone, 2^-8, is as large as the output's own);
+//   O += P·V     P from tensor memory, V from shared memory, fp32 in tensor memory,
+//     one part of P after the other.
 // While one half's softmax runs the tensor cores work for the other.  Where a
 // block has no more than 128 rows (single tokens, drafts) the halves take the
 // same rows over alternate tiles (on from one segment to the next), and the half
 // that is done first leaves its sums to the other and goes on.
 //
-// Bounds and figures (measured at the sizes given): single tokens by HBM (64 over
-// 8192 keys, 1.55 GB: 242 us, 6.4 TB/s); chunks by the softmax's latency beside the
-// products (two of 2048 over 16384 keys: 735 us, 1380 TFLOP/s); prompts of a few
-// thousand tokens by start and joining as well (8x4096 of 64 columns: 48 us).
+// Bounds and figures (measured at the sizes given): single tokens by HBM and the
+// softmax's latency (64 over 8192 keys, 1.55 GB: 268 us, 5.8 TB/s); chunks by the
+// softmax's instructions beside the products (two of 2048 over 16384 keys: 995 us, 1015
+// TFLOP/s, half as many again with the second part's); prompts of a few thousand
+// tokens by start and joining as well (8x4096 of 64 columns: 56 us).  With the
+// rounded weight alone these are 242, 735 and 48 us.  Of the difference the forming
+// of the second part is more than its products: tokens take the same time without
+// those, and the weights' storing costs nothing.
 //
 // The reference m of a row is its maximum, but it is raised only when a tile's
-// maximum passes it by more than 2^8 in the weights: fp32 sums and bf16 weights keep
+// maximum passes it by more than 2^8 in the weights: fp32 sums and weights keep
 // their relative precision, and O is rescaled (a pass over tensor memory) once or
 // twice a row instead of in most tiles.
 //
@@ -499,8 +506,11 @@ struct Products {
         tmem_fence_after_sync();
         const uint32_t v = swizzled_desc(stage(load), 16384);
 #pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i)
-            mma_bf16_ts(tmem + 256 + half * DP, tmem + half * kKeys + i * 8, v + (i * 2048 >> 4), pv_shape, accumulate || i > 0);
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+                mma_bf16_ts(tmem + 256 + half * DP, tmem + half * kKeys + part * (kKeys / 2) + i * 8, v + (i * 2048 >> 4), pv_shape,
+                            accumulate || part + i > 0);
         return true;
     }
 
@@ -646,20 +656,24 @@ struct Softmax {
                 for (int j = 0; j < 32; ++j) w[i][j] = __float_as_uint(__uint_as_float(w[i][j]) - base);
         }
         uint64_t sum[2] = {0, 0};
-        const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+        const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc), minus = pack2(-1.f, -1.f);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            uint32_t p[16];
+            uint32_t p[16], rest[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 float x, y;
                 unpack2(fma2(pack2(__uint_as_float(w[h][2 * j]), __uint_as_float(w[h][2 * j + 1])), c2, mc2), x, y);
                 x = exp2_fast(x);
                 y = exp2_fast(y);
-                sum[j & 1] = add2(sum[j & 1], pack2(x, y));
+                const uint64_t xy = pack2(x, y);
+                sum[j & 1] = add2(sum[j & 1], xy);
                 p[j] = bf16x2(x, y);
+                unpack2(fma2(pack2(__uint_as_float(p[j] << 16), __uint_as_float(p[j] & 0xffff0000u)), minus, xy), x, y);
+                rest[j] = bf16x2(x, y);  // of an exact difference
             }
             tmem_st16(s_col + 16 * h, p);
+            tmem_st16(s_col + kKeys / 2 + 16 * h, rest);
         }
         float x0, x1, y0, y1;
         unpack2(sum[0], x0, x1);
