@@ -39,3 +39,37 @@ def test_weights_are_not_rounded_to_bf16(usm, name, window):
     ref, bound = R.attention(*args(v), window=window, dtype="f32")
     mass, _ = R.attention(*args(np.abs(v)), window=window, dtype="f32")
     assert_near(x, ref, bound + 1.01 * 2.0 ** -16 * mass + R.HALF_STEP["bf16"] * np.abs(ref))
+
+
+# ---------------------------------------------------------------------------
+# Calls behind one another
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,D,count", [("f32", 64, 1), ("f32", 64, 40), ("f32", 160, 1), ("bf16", 160, 2), ("bf16", 64, 1), ("bf16", 128, 40)])
+def test_results_of_the_call_before(usm, dtype, D, count):
+    """Calls that follow one another at once, each reading what the last has written
+    (slots, turned queries, lengths), give what they give one by one: kernels start
+    before the last has ended, and read nothing of it before."""
+    import torch
+    p = Problem("behind", [300] * 12, [count] * 12, heads=4, kv=2, D=D, dtype=dtype)
+    q0, kc0, vc0, table, lens0, _ = p.on_device()
+    rope = usm.rope_table(512, D)
+    new = torch.randn(8, 2, q0.shape[0], 2, D, device="cuda").to(q0.dtype)
+
+    def run(after):
+        kc, vc, lens, q, outs = kc0.clone(), vc0.clone(), lens0 - 8, q0.clone(), []
+        after()
+        for k, v in new:
+            lens = lens + 1
+            after()
+            q = usm.paged_append(k, v, kc, vc, table, lens, rope=rope, q=q)
+            after()
+            outs.append(usm.paged_attention(q, kc, vc, table, lens, scale=D ** -0.5))
+            after()
+            q = outs[-1]
+        torch.cuda.synchronize()
+        return torch.stack(outs), kc, vc
+
+    want = run(torch.cuda.synchronize)
+    assert torch.isfinite(want[0]).all()
+    for _ in range(5):
+        assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) for a, b in zip(want, run(lambda: None)))

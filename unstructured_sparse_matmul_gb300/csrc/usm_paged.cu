@@ -44,13 +44,13 @@ __device__ Place place_of(const AppendArgs& a, int token) {
         int lo = 0, hi = a.num_seqs;
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if (__ldg(a.q_offsets + mid) <= token) lo = mid + 1;
+            if (a.q_offsets[mid] <= token) lo = mid + 1;
             else hi = mid;
         }
         b = lo - 1;
         if (b < 0) return w;
-        start = max(__ldg(a.q_offsets + b), 0);
-        const int end = min(__ldg(a.q_offsets + b + 1), a.tokens);
+        start = max(a.q_offsets[b], 0);
+        const int end = min(a.q_offsets[b + 1], a.tokens);
         if (token < start || token >= end) return w;
         n = end - start;
     } else {
@@ -58,12 +58,12 @@ __device__ Place place_of(const AppendArgs& a, int token) {
         start = b * a.per_seq;
         n = a.per_seq;
     }
-    const int len = min(max(__ldg(a.lengths + b), 0), kPagedMaxLength);
+    const int len = min(max(a.lengths[b], 0), kPagedMaxLength);
     w.known = true;
     w.position = len - n + (token - start);
     if (w.position < 0 || w.position >= a.capacity) return w;
     const int index = w.position / a.page_size;
-    const int page = __ldg(a.table + (long long)b * a.table_stride + index);
+    const int page = a.table[(long long)b * a.table_stride + index];
     if ((unsigned)page >= (unsigned)a.num_pages) return w;
     const int slot = w.position - index * a.page_size;
     w.k = page * a.kc_page + slot * a.kc_slot;
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         for (int i = 0; i < E; i += 4) {
             float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (u * E + i < a.rot / 2) {
-                c = __ldg(reinterpret_cast<const float4*>(row + u * E + i));
-                s = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + u * E + i));
+                c = *reinterpret_cast<const float4*>(row + u * E + i);
+                s = *reinterpret_cast<const float4*>(row + a.rot / 2 + u * E + i);
             }
             cos[i] = c.x, cos[i + 1] = c.y, cos[i + 2] = c.z, cos[i + 3] = c.w;
             sin[i] = s.x, sin[i + 1] = s.y, sin[i + 2] = s.z, sin[i + 3] = s.w;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_pairs_kernel(const __gr
             to[j2] = t2;
             continue;
         }
-        const float c = __ldg(row + j), s = __ldg(row + half + j), x1 = widen(t1), x2 = widen(t2);
+        const float c = row[j], s = row[half + j], x1 = widen(t1), x2 = widen(t2);
         narrow(x1 * c - x2 * s, to + j1);
         narrow(x2 * c + x1 * s, to + j2);
     }

@@ -11,6 +11,11 @@
 
 namespace usm {
 
+// What a call reads may be written by the kernel before it, which need not have
+// ended when this one starts (await_previous() waits for its results): such arrays
+// are read by ordinary loads, never through the path for data that nobody writes
+// while a kernel lives.
+
 // The new tokens of one sequence.
 struct PagedSeq {
     int start;  // its first new token in the calls' arrays
@@ -21,13 +26,13 @@ struct PagedSeq {
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     PagedSeq s;
     if (a.q_offsets) {
-        s.start = min(max(__ldg(a.q_offsets + b), 0), a.tokens);
-        s.n = min(max(__ldg(a.q_offsets + b + 1), s.start), a.tokens) - s.start;
+        s.start = min(max(a.q_offsets[b], 0), a.tokens);
+        s.n = min(max(a.q_offsets[b + 1], s.start), a.tokens) - s.start;
     } else {
         s.start = b * a.per_seq;
         s.n = a.per_seq;
     }
-    s.len = min(max(__ldg(a.lengths + b), 0), kPagedMaxLength);
+    s.len = min(max(a.lengths[b], 0), kPagedMaxLength);
     return s;
 }
 
@@ -357,7 +362,7 @@ __device__ __forceinline__ void paged_note(PagedMeta& m, const PagedSegment& g) 
 // Page and slot of a key.
 __device__ __forceinline__ int2 paged_slot(const PagedArgs& a, int seq, int key) {
     const int index = key / a.page_size;
-    const int page = __ldg(a.table + (long long)seq * a.table_stride + index);
+    const int page = a.table[(long long)seq * a.table_stride + index];
     return make_int2(min(max(page, 0), a.num_pages - 1), key - index * a.page_size);
 }
 

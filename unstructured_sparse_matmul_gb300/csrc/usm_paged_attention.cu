@@ -13,10 +13,10 @@ namespace usm {
 namespace {
 
 // Four elements, as they lie in memory and as floats.
-__device__ __forceinline__ float4 quad4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ uint2 quad4(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ float4 quad4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ uint2 quad4(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ void quads8(const __nv_bfloat16* p, uint2* x) {  // two at once
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
     x[0] = make_uint2(w.x, w.y), x[1] = make_uint2(w.z, w.w);
 }
 __device__ __forceinline__ float4 floats(float4 x) { return x; }
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kBlockThreads) paged_block_kernel(const __grid
 // by HBM with one row (16 tokens over 4096 fp32 keys of 64 columns, 227 MB: 51 us,
 // 10 of them start and joining; 32 over 4096 bf16 keys of 256 columns: 5.5 TB/s),
 // by instructions with more: 128 fp32 columns 5.0 TB/s with 2 rows, 4.6 with 4, 2.7
-// with 8; 256 columns 5.2 with 2 and 4.6 with 4, in bf16 3.5 with 4.  (Row by row
+// with 8; 256 columns 5.2 with 2 and 4.3 with 4, in bf16 3.5 with 4.  (Row by row
 // with keys and values held as floats: 4.2, 2.5, 3.6 and 1.7 with 4, 8, 4 and 4; 2
 // rows as 4: 4.5 and 4.4, 192 bf16 columns 2.5 for 4.4; bf16 quads 128 columns
 // apart, in loads of 8 bytes: 3.9 with one row.)

@@ -314,8 +314,8 @@ struct Copies {
                 const int entry = tiles_of_page == 1 ? tile * per_tile : tile / tiles_of_page;
                 if (entry >> 5 != group) {
                     const int i = (entry & ~31) + lane;
-                    now = entry >> 5 == group + 1 && group >= 0 ? next : i < a.table_pages ? __ldg(table + i) : 0;
-                    next = i + 32 < a.table_pages ? __ldg(table + i + 32) : 0;
+                    now = entry >> 5 == group + 1 && group >= 0 ? next : i < a.table_pages ? table[i] : 0;
+                    next = i + 32 < a.table_pages ? table[i + 32] : 0;
                     group = entry >> 5;
                     now = min(max(now, 0), a.num_pages - 1);
                 }
