@@ -73,3 +73,29 @@ def test_results_of_the_call_before(usm, dtype, D, count):
     assert torch.isfinite(want[0]).all()
     for _ in range(5):
         assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) for a, b in zip(want, run(lambda: None)))
+
+
+# ---------------------------------------------------------------------------
+# Next to the limits
+# ---------------------------------------------------------------------------
+def test_append_of_nearly_2_to_31_heads(usm):
+    """tokens·heads next to 2^31: the last step over the heads passes it."""
+    import torch
+    D, heads = 8, 2**31 - 3  # and one of keys, one of values
+    q = torch.empty((1, heads, D), dtype=torch.bfloat16, device="cuda")
+    q.view(-1)[: 1 << 20].normal_()
+    tail = 1 << 12
+    q[:, -tail:].normal_()
+    k, v = torch.randn(2, 1, 1, D, device="cuda").bfloat16()
+    kc, vc = torch.zeros(2, 1, 4, 1, D, device="cuda", dtype=torch.bfloat16)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.full((1,), 3, dtype=torch.int32, device="cuda")
+    rope = usm.rope_table(4, D)
+    parts = [slice(0, 1000), slice(heads - tail, heads)]
+    call = lambda x: usm.paged_append(k, v, kc, vc, table, lens, rope=rope, interleaved=True, q=x, q_out=x)
+    want = [call(q[:, s].clone()) for s in parts]
+    kc.zero_(), vc.zero_()
+    call(q)
+    for s, w in zip(parts, want):
+        assert torch.equal(q[:, s], w)
+    assert torch.equal(vc[0, 2], v[0]) and kc[0, 2].abs().sum() > 0
+    assert not vc[0, [0, 1, 3]].any() and not kc[0, [0, 1, 3]].any()

@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int E = C::E;
     await_previous();
     let_next_start();
-    const int u = threadIdx.x, step = blockDim.y;
+    const int u = threadIdx.x;
+    const unsigned step = blockDim.y;
     const int token = blockIdx.x * blockDim.z + threadIdx.z;
     if (token >= a.tokens) return;
     const Unit w = unit_of<E>(a, u);
@@ -159,25 +160,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
     }
 
-    // Heads in the order q, k, v.
-    const int q_heads = a.q ? a.q_heads : 0, heads = q_heads + (at.k >= 0 ? 2 * a.kv_heads : 0);
-    for (int h0 = blockIdx.y * step + threadIdx.y; h0 < heads; h0 += kInFlight * step * gridDim.y) {
+    // Heads in the order q, k, v; up to 2^31, so that the last steps pass it.
+    const unsigned q_heads = a.q ? a.q_heads : 0, kv_heads = a.kv_heads, heads = q_heads + (at.k >= 0 ? 2 * kv_heads : 0);
+    for (unsigned h0 = threadIdx.y; h0 < heads; h0 += kInFlight * step) {
         uint4 x[kInFlight], y[kInFlight];
         T* to[kInFlight];
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            const int h = h0 + i * step * gridDim.y;
+            const unsigned h = h0 + i * step;
             if (h < heads) {
                 const T* from;
                 if (h < q_heads) {
                     from = (const T*)a.q + token * a.q_token + h * a.q_head;
                     to[i] = (T*)a.q_out + token * a.q_out_token + h * a.q_out_head;
-                } else if (h < q_heads + a.kv_heads) {
+                } else if (h < q_heads + kv_heads) {
                     from = (const T*)a.k + token * a.k_token + (h - q_heads) * a.k_head;
                     to[i] = (T*)a.k_cache + at.k + (h - q_heads) * a.kc_head;
                 } else {
-                    from = (const T*)a.v + token * a.v_token + (h - q_heads - a.kv_heads) * a.v_head;
-                    to[i] = (T*)a.v_cache + at.v + (h - q_heads - a.kv_heads) * a.vc_head;
+                    from = (const T*)a.v + token * a.v_token + (h - q_heads - kv_heads) * a.v_head;
+                    to[i] = (T*)a.v_cache + at.v + (h - q_heads - kv_heads) * a.vc_head;
                 }
                 x[i] = *reinterpret_cast<const uint4*>(from + w.first * E);
                 if (w.second >= 0) y[i] = *reinterpret_cast<const uint4*>(from + w.second * E);
@@ -185,9 +186,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            const int h = h0 + i * step * gridDim.y;
+            const unsigned h = h0 + i * step;
             if (h >= heads) break;
-            if (h < q_heads + a.kv_heads && (w.turn_first || w.turn_second)) {
+            if (h < q_heads + kv_heads && (w.turn_first || w.turn_second)) {
                 float p[E], r[E];
                 C::widen(x[i], p);
                 if (w.second >= 0) C::widen(y[i], r);
