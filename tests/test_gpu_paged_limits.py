@@ -99,3 +99,20 @@ def test_append_of_nearly_2_to_31_heads(usm):
         assert torch.equal(q[:, s], w)
     assert torch.equal(vc[0, 2], v[0]) and kc[0, 2].abs().sum() > 0
     assert not vc[0, [0, 1, 3]].any() and not kc[0, [0, 1, 3]].any()
+
+
+def test_heads_and_positions_past_32_bits_are_refused(usm):
+    """Numbers that the library's 32-bit arguments would cut to small ones."""
+    import torch
+    t = torch.zeros(8, device="cuda", dtype=torch.bfloat16)
+    k, cache = t.view(1, 1, 8), t.clone().view(1, 1, 1, 8)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    add = lambda **kw: usm.paged_append(k, k, cache, cache.clone(), table, lens, **kw)
+    many = k.expand(1, 2**32 + 4, 8)
+    with pytest.raises(ValueError):
+        add(q=many, q_out=many)
+    rope = torch.empty((2**32 + 5, 2), device="cuda")
+    with pytest.raises(ValueError):
+        add(rope=rope)
+    with pytest.raises(ValueError):
+        usm.paged_attention(many, cache, cache, table, lens)

@@ -831,7 +831,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, q_offsets=None, ro
     if q is not None:
         if q.dim() != 3:
             _tensor(q, "q", index, (dt,), 3)
-        q_heads = q.shape[1]
+        q_heads = _entries(q.shape[1])
         q, qt = _tokens(q, "q", index, dt, (n, q_heads, shape[2]))
         if q_out is None:
             q_out = T.torch.empty_like(q, memory_format=T.torch.contiguous_format)
@@ -845,6 +845,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, q_offsets=None, ro
         if not rope.is_contiguous():
             raise ValueError("rope must be contiguous")
         positions, rot = rope.shape
+        _int32((positions, rot), ("positions of rope", "columns of rope"))
     _run("paged_append", lib.paged_append, index, T, cache, n, kt, vt, qt, ot, q_heads,
          None if rope is None else rope.data_ptr(), positions, rot, 1 if interleaved else 0)
     return q_out
