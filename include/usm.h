@@ -450,6 +450,7 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int *row_offsets, c
  * table's table_pages pages have no slot, and a page outside [0, num_pages) is
  * clamped where it is read and skipped where it would be written.
  *
+ * Limit: num_seqs ≤ 2^30.
  * A host struct: the calls read it before they return and keep no pointer to it.
  */
 typedef struct usm_paged_cache {

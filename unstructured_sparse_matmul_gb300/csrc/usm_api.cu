@@ -368,7 +368,7 @@ int check_paged(const usm_paged_cache& c, int tokens, long long heads) {
     if (tokens < 0 || c.num_seqs < 0 || c.kv_heads <= 0 || c.head_dim <= 0 || c.num_pages <= 0 || c.page_size <= 0 ||
         c.table_pages < 0 || !dtype_ok(c.dtype))
         return USM_ERR_INVALID_ARG;
-    if (c.head_dim > kPagedMaxHeadDim || tokens * heads >= 1LL << 31) return USM_ERR_UNSUPPORTED;
+    if (c.head_dim > kPagedMaxHeadDim || c.num_seqs > kPagedMaxSeqs || tokens * heads >= 1LL << 31) return USM_ERR_UNSUPPORTED;
     if (c.head_dim * dtype_size(c.dtype) % 16 != 0) return USM_ERR_ALIGNMENT;
     if (tokens == 0 || c.num_seqs == 0) return USM_OK;
     if (!c.lengths || (c.table_pages > 0 && !c.page_table)) return USM_ERR_INVALID_ARG;
@@ -604,7 +604,7 @@ int paged_append(const usm_paged_cache* cache, int tokens, const usm_tokens* k, 
 }
 
 size_t paged_attention_workspace_bytes(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, usm_dtype dtype) {
-    if (tokens <= 0 || num_seqs <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
+    if (tokens <= 0 || num_seqs <= 0 || num_seqs > kPagedMaxSeqs || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
         head_dim > kPagedMaxHeadDim || !dtype_ok(dtype) || (long long)tokens * q_heads >= 1LL << 31)
         return 0;
     return paged_attention_workspace(tokens, num_seqs, q_heads, kv_heads, head_dim, dtype == USM_BF16);

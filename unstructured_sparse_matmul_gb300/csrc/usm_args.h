@@ -79,6 +79,7 @@ struct AttnArgs {
     long long ldc;
 };
 
+constexpr int kPagedMaxSeqs = 1 << 30;    // sequences of a call (walks over them step past the last, searches add two)
 constexpr int kPagedMaxLength = 1 << 30;  // tokens of a sequence (positions and their differences stay in 32 bits)
 
 // Attention of new tokens over a paged cache, as usm_paged_cache lays it out.
