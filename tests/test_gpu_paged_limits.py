@@ -116,3 +116,24 @@ def test_heads_and_positions_past_32_bits_are_refused(usm):
         add(rope=rope)
     with pytest.raises(ValueError):
         usm.paged_attention(many, cache, cache, table, lens)
+
+
+@pytest.mark.parametrize("page", [4096, 3000])
+def test_items_that_take_seconds(usm, page):
+    """2^30 tokens of a cache (one page listed over and over) before 256 rows of each of
+    24 heads: an item's tiles take longer than a wait's limit, which counts from the
+    last tile.  One key of the page outweighs all others, so that every sum is exact."""
+    import torch
+    kv, group, D = 24, 256, 64
+    k = torch.randn(1, page, kv, D, device="cuda").bfloat16()
+    v = torch.randn(1, page, kv, D, device="cuda").bfloat16()
+    k[..., 0], k[:, 77, :, 0] = -50, 50
+    v[:, 77] = torch.randint(-8, 9, (1, kv, D), device="cuda").bfloat16()
+    q = torch.randn(1, kv * group, D, device="cuda").bfloat16()
+    q[..., 0] = 4
+    pages = 2**30 // page
+    lens = torch.full((1,), pages * page - 1, dtype=torch.int32, device="cuda")
+    out = usm.paged_attention(q, k, v, torch.zeros((1, pages), dtype=torch.int32, device="cuda"), lens)
+    want = v[:, 77].repeat_interleave(group, 1)
+    assert torch.equal(out, want)
+    assert usm.poll_status() == 0

@@ -271,8 +271,8 @@ struct PagedShares {
         unit = (int)min(skip - (long long)head * (k.tiles + kCost), (long long)k.tiles + kCost);
     }
 
-    // On to the next item; whole warp.
-    __device__ __forceinline__ void advance(const PagedArgs& a) {
+    // On to the next item; whole warp.  beat (may be null): changed with every step.
+    __device__ __forceinline__ void advance(const PagedArgs& a, volatile int* beat) {
         unit = 0;
         if (++head < a.kv_heads) return;
         head = 0;
@@ -281,6 +281,7 @@ struct PagedShares {
             const int lane = threadIdx.x & 31;
 #pragma unroll 1
             for (++b; b < a.num_seqs; b += 32) {  // past sequences that bring no token
+                if (beat) *beat = -b;
                 const int n = b + lane < a.num_seqs ? paged_seq(a, b + lane).n : 0;
                 const unsigned some = __ballot_sync(kFullMask, n > 0);
                 if (some) {
@@ -299,13 +300,13 @@ struct PagedShares {
     }
 
     // The next segment; whole warp.
-    __device__ __forceinline__ PagedSegment next(const PagedArgs& a) {
+    __device__ __forceinline__ PagedSegment next(const PagedArgs& a, volatile int* beat = nullptr) {
         PagedSegment g;
         g.live = 0;
         g.odd_values = 0;
         while (left > 0) {
             if (unit == k.tiles + kCost) {
-                advance(a);
+                advance(a, beat);
                 if (left == 0) break;
             }
             const int take = (int)min((long long)(k.tiles + kCost - unit), left);

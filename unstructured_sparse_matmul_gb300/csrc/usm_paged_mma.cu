@@ -80,20 +80,30 @@ struct Control {
     float2 stats[128];  // (reference, sum) of the rows that one half leaves to the other
     uint32_t tmem;
     int abort;
+    int progress;  // changes with every tile that a stage was free for and every step of the search for segments
     int joined;  // warps that have joined a segment's halves, over all segments
 };
 static_assert(Sizes<128>::kControl + sizeof(Control) <= 227 * 1024, "shared memory");
 
-// Waits are bounded: a wait that gives up says so to all others of the CTA.
+// Waits are bounded: a wait that gives up says so to all others of the CTA.  Those for a
+// whole segment (kLong; it may have millions of tiles) count from the last progress.
+template <bool kLong>
 __device__ bool wait_slow(uint32_t bar, uint32_t parity, Control* ct, int* status) {
-    const unsigned long long t0 = global_timer_ns();
+    unsigned long long t0 = global_timer_ns();
     volatile int* abort = &ct->abort;
+    volatile int* progress = &ct->progress;
+    int seen = kLong ? *progress : 0;
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
+            if (kLong && *progress != seen) {
+                seen = *progress;
+                t0 = global_timer_ns();
+                continue;
+            }
             *abort = 1;
             record_status(status, USM_ERR_TIMEOUT);
             return false;
@@ -101,10 +111,11 @@ __device__ bool wait_slow(uint32_t bar, uint32_t parity, Control* ct, int* statu
     }
 }
 // By a whole warp, with one answer.
+template <bool kLong = false>
 __device__ __forceinline__ bool wait(const unsigned long long& b, uint32_t parity, Control* ct, int* status) {
     const uint32_t bar = smem_addr(&b);
     bool ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = wait_slow(bar, parity, ct, status);
+    if (!ok) ok = wait_slow<kLong>(bar, parity, ct, status);
     return __all_sync(kFullMask, ok);
 }
 __device__ __forceinline__ void arrive_warp(const unsigned long long& b) {
@@ -202,7 +213,7 @@ struct Copies {
         const int before = joins;
         if (g.rows <= 128 && g.tiles > 1) ++joins;
         if (it == 0) return true;
-        if (!wait(ct->q_empty, (it - 1) & 1, ct, a.status)) return false;
+        if (!wait<true>(ct->q_empty, (it - 1) & 1, ct, a.status)) return false;
         if (g.rows <= 128) return true;
         const unsigned long long t0 = global_timer_ns();
         bool ok = true;
@@ -302,7 +313,7 @@ struct Copies {
         uint32_t base = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return false;
+            if (!wait<true>(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return false;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const int n = g.tiles, tile0 = g.tile0, lo = g.lo, hi = g.hi, head = g.head;
@@ -327,6 +338,7 @@ struct Copies {
                 const uint32_t stage = load % Z::kStages;
                 if (!wait(ct->empty[stage], (load / Z::kStages & 1) ^ 1, ct, a.status)) return false;
                 const uint32_t bar = smem_addr(&ct->full[stage]), to = smem + Z::kStage0 + stage * Z::kTile;
+                if (lead) *(volatile int*)&ct->progress = (int)load;
                 if (lead) mbar_arrive_expect_tx(bar, max(end - begin, 0) * kPanels * slots * 128);
                 loaded |= 1u << stage;
                 phases = (phases & ~(1u << stage)) | ((load / Z::kStages & 1) << stage);
@@ -363,7 +375,7 @@ struct Copies {
         int joins = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            if (!wait<true>(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live || !room_for_queries(g, it, joins)) return;
             queries(g, warp & 1, 2);
@@ -376,7 +388,7 @@ struct Copies {
         uint32_t load = 0, startings = 0;  // startings: parity of each stage's
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            if (!wait<true>(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) return;
             const int n = g.tiles;
@@ -386,7 +398,7 @@ struct Copies {
                 if (!needs_cleaning(g, key0)) continue;
                 const uint32_t i = v_load(load, t, n), stage = i % Z::kStages;
                 // Its phase of `full` can be told from others only once it has begun.
-                if (!wait(ct->started[stage], startings >> stage & 1, ct, a.status)) return;
+                if (!wait<true>(ct->started[stage], startings >> stage & 1, ct, a.status)) return;
                 startings ^= 1u << stage;
                 if (!wait(ct->full[stage], i / Z::kStages & 1, ct, a.status)) return;
                 clean(g, stage, key0, 0, kKeys, threadIdx.x & 63, 64);
@@ -413,7 +425,7 @@ struct Copies {
         int joins = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            if (!wait<true>(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const int n = g.tiles, key0 = g.tile0 * kKeys;
@@ -427,6 +439,7 @@ struct Copies {
                 const char* row = next;
                 next = i + 1 < 2 * n ? key_row(g, i + 1) : nullptr;  // its look-up runs behind this tile's copies
                 if (!wait(ct->empty[stage], parity, ct, a.status)) return;
+                if (lane == 0) *(volatile int*)&ct->progress = i;
                 rows(smem + Z::kStage0 + stage * Z::kTile, 32 * warp, row);
                 if (values && partly_seen(g, at)) {
                     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -468,9 +481,10 @@ struct Products {
         qk_shape = bf16_mma_shape(kKeys, false);
         pv_shape = bf16_mma_shape(steps * 16, true);
     }
+    template <bool kLong = false>
     __device__ __forceinline__ bool await(const unsigned long long& b, uint32_t parity) {
         const uint32_t bar = smem_addr(&b);
-        return mbar_try_wait(bar, parity) || wait_slow(bar, parity, ct, a.status);
+        return mbar_try_wait(bar, parity) || wait_slow<kLong>(bar, parity, ct, a.status);
     }
     __device__ __forceinline__ void commit(const unsigned long long& b) { tmem_commit(smem_addr(&b)); }
     __device__ __forceinline__ bool loaded(uint32_t load) {
@@ -518,7 +532,7 @@ struct Products {
         uint32_t base = 0;
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!await(ct->seg_full[slot], it / kRing & 1)) return;
+            if (!await<true>(ct->seg_full[slot], it / kRing & 1)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const int n = g.tiles;
@@ -838,7 +852,7 @@ struct Softmax {
     __device__ void run() {
         for (uint32_t it = 0;; ++it) {
             const int slot = it % kRing;
-            if (!wait(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
+            if (!wait<true>(ct->seg_full[slot], it / kRing & 1, ct, a.status)) return;
             const PagedSegment& g = ct->seg[slot];
             if (!g.live) break;
             const bool some = __any_sync(kFullMask, row_of(g) < g.rows);
@@ -912,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
         mbar_init(smem_addr(&ct->box_full), 4);
         mbar_init(smem_addr(&ct->box_free), 4);
         mbar_init(smem_addr(&ct->drained), 1);
-        ct->abort = ct->joined = 0;
+        ct->abort = ct->joined = ct->progress = 0;
         fence_barrier_init();
     }
     if (warp == 12) tmem_alloc(smem_addr(&ct->tmem), 512);
@@ -955,12 +969,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mma_kernel(const __grid_con
             if (a.num_seqs <= Shares::kSolo) shares.init_solo(a, blockIdx.x, gridDim.x);
             for (uint32_t it = 0;; ++it) {
                 const int slot = it % kRing;
-                PagedSegment g = shares.next(a);
+                PagedSegment g = shares.next(a, &ct->progress);
                 if (g.live) {
                     paged_note(meta, g);
                     set_edges(a, g);
                 }
-                if (it >= kRing && !wait(ct->seg_empty[slot], (it / kRing - 1) & 1, ct, a.status)) break;
+                if (it >= kRing && !wait<true>(ct->seg_empty[slot], (it / kRing - 1) & 1, ct, a.status)) break;
                 if (lane == 0) ct->seg[slot] = g;
                 arrive_warp(ct->seg_full[slot]);
                 if (!g.live) break;
