@@ -73,6 +73,7 @@ struct Walk {
         Shares s;
         memcpy(&s, shares, sizeof s);
         const PagedSegment g = s.next(a);
+        __syncwarp();  // every lane has copied the walk's state
         if (threadIdx.x == 0) {
             memcpy(shares, &s, sizeof s);
             if (g.live) paged_note(meta, g);
