@@ -528,10 +528,12 @@ int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, 
  * Products, statistics and sums are fp32.  bf16: probabilities go into their product
  * with V as two bf16 parts (relative 2^-16 each; the output's own rounding is
  * 2^-8); head_dim > 128 keeps them in fp32.
- * A token that sees no key, or whose scores are all -inf, gives a zero row.  Keys
+ * A token that sees no key, or whose scores are all -inf (where the rows of V are
+ * finite), gives a zero row.  Keys
  * and values that a token does not see never touch its row, whatever they hold
  * (unwritten slots, later tokens, NaN or infinities); an infinity in a row of V that
- * it sees makes its column infinite or NaN.  Rows of tokens outside every
+ * it sees makes its column infinite or NaN, whatever its weight (0 and that of a
+ * score of -inf among them).  Rows of tokens outside every
  * sequence are left alone.
  * Limits: head_dim ≤ 256; tokens·q_heads < 2^31; lengths < 2^30.
  * Deterministic (no atomics).  tokens = 0 or num_seqs = 0 is a no-op.

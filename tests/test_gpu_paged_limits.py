@@ -137,3 +137,29 @@ def test_items_that_take_seconds(usm, page):
     want = v[:, 77].repeat_interleave(group, 1)
     assert torch.equal(out, want)
     assert usm.poll_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# Infinities under weights of zero
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("keys", ["some", "all"])
+@pytest.mark.parametrize("length", [40, 1040, 20000])
+@pytest.mark.parametrize("heads", [1, 2, 4, 8, 40])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 160), ("bf16", 64), ("bf16", 160)])
+def test_infinity_under_a_score_of_minus_infinity(usm, dtype, D, heads, length, keys):
+    """A score of -inf weighs nothing, and nothing times an infinity is NaN: the
+    infinity reaches the rows that see it however the keys are divided among lanes,
+    warps and CTAs (whose whole share may be such keys), and no others."""
+    p = Problem("minus infinity", [length], [3], heads=heads, kv=1, D=D, dtype=dtype)
+    p.q[..., 0] = 1
+    j = np.arange(length)
+    hidden = j if keys == "all" else j[: length * 3 // 4]
+    p.k[p.table[0, hidden // 16], hidden % 16, 0, 0] = -np.inf
+    for key in (length // 3, length - 2):  # seen by all three tokens, by the last two
+        p.v[p.table[0, key // 16], key % 16, 0, 5 + (key == length - 2)] = np.inf
+    seen = np.zeros((3, heads, D), bool)
+    seen[:, :, 5], seen[1:, :, 6] = True, True
+    out = got(p.run(usm))
+    assert np.array_equal(~np.isfinite(out), seen)
+    if keys == "all":
+        assert not out[~seen].any()

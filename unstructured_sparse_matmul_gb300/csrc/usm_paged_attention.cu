@@ -523,7 +523,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int w = 0; w < kWarps; ++w) {
                 const float2 st = stats[w * kR + r];
-                if (st.x == -INFINITY && st.y == 0.f) continue;
                 const float f = weight_of(st.x, top, c);
                 sum = fmaf(st.y, f, sum);
                 x = add_scaled(x, sums[(w * kR + r) * kRow + at], f);
@@ -555,9 +554,9 @@ struct JoinSum {
     float4 x;
 };
 // Adds a part to sums with a reference that is no less.  One without a reference
-// saw no key, or only scores of NaN: those are its sum as well, and go on.
+// saw no key (zeros), or only scores of -inf or NaN: an infinity of V under the
+// former's weights of 0, and the latter, are NaN in its sums and go on.
 __device__ __forceinline__ void add_part(JoinSum& sum, float2 stat, float4 x, float scale_log2) {
-    if (stat.x == -INFINITY && stat.y == 0.f) return;
     const float w = weight_of(stat.x, sum.stat.x, scale_log2);
     sum.stat.y = fmaf(stat.y, w, sum.stat.y);
     sum.x = add_scaled(sum.x, x, w);
@@ -618,6 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __gri
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = i0 + u * split;
                     stat[u] = make_float2(-INFINITY, 0.f);
+                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i > count) continue;
                     const long long slot = i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater;
                     stat[u] = __ldcg(reinterpret_cast<const float2*>(a.part_stats + 2 * (slot * a.part_rows + r)));
