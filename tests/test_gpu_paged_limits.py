@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import paged_ref as R
-from test_gpu_paged import SHAPES, Problem, assert_near, got
+from test_gpu_paged import Problem, assert_near, got, torch_type
 
 pytestmark = pytest.mark.gpu
 
@@ -116,6 +116,27 @@ def test_heads_and_positions_past_32_bits_are_refused(usm):
         add(rope=rope)
     with pytest.raises(ValueError):
         usm.paged_attention(many, cache, cache, table, lens)
+
+
+@pytest.mark.parametrize("tokens,heads", [(1, 2**31 - 1), (2**31 - 1, 1), (2**16, 2**15 - 1)])
+@pytest.mark.parametrize("dtype,D", [("f32", 4), ("bf16", 8)])
+def test_attention_of_nearly_2_to_31_rows(usm, dtype, D, tokens, heads):
+    """tokens·heads next to 2^31, all rows the same query: all give its row.  (Not to the
+    last bit: a block of rows that a CTA's share cuts is the sum of two parts, in
+    another order than that of whole ones, within the bound of any order.)"""
+    import torch
+    t = torch_type(dtype)
+    q = torch.randn(1, 1, D, device="cuda").to(t)
+    k, v = torch.randn(2, 1, 100, 1, D, device="cuda").to(t)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.full((1,), 100, dtype=torch.int32, device="cuda")
+    out = torch.full((tokens, heads, D), 7.0, dtype=t, device="cuda")
+    usm.paged_attention(q.expand(tokens, heads, D), k, v, table, lens, causal=False, out=out)
+    ref, bound = R.attention(got(q), got(k), got(v), np.zeros((1, 1), int), [100], [1], [0], 1.0, causal=False, dtype=dtype)
+    for rows in out.view(-1, D).split(1 << 28):
+        for c in range(D):
+            low, high = (float(x) for x in rows[:, c].aminmax())
+            assert abs(low - ref[0, 0, c]) <= bound[0, 0, c] and abs(high - ref[0, 0, c]) <= bound[0, 0, c]
+    assert usm.poll_status() == 0
 
 
 @pytest.mark.parametrize("page", [4096, 3000])

@@ -55,7 +55,7 @@ struct PagedBlock {
 template <int kRows, int kKeys>
 __device__ __noinline__ PagedBlock paged_block_call(uint32_t group_mul, int group_shift, int causal, int window, int keys, int rows,
                                                     int position, int block) {
-    const int first = block * kRows, last = min(rows, first + kRows) - 1;
+    const int first = block * kRows, last = first + min(rows - first, kRows) - 1;
     const int p0 = position + (int)((unsigned long long)first * group_mul >> group_shift);
     const int p1 = position + (int)((unsigned long long)last * group_mul >> group_shift);
     PagedBlock k;
