@@ -184,3 +184,64 @@ def test_infinity_under_a_score_of_minus_infinity(usm, dtype, D, heads, length, 
     assert np.array_equal(~np.isfinite(out), seen)
     if keys == "all":
         assert not out[~seen].any()
+
+
+# ---------------------------------------------------------------------------
+# Batches of unequal sequences
+# ---------------------------------------------------------------------------
+UNEQUAL = {  # new tokens of each sequence
+    "chunk and idle": [70] + [0] * 20,
+    "chunk and single": [90] + [1] * 15,
+    "few and many": [1, 2, 3, 4, 5, 7, 8, 9, 10, 16, 17, 0, 33],
+    "small": [3, 0, 2],
+}
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 8, 9])
+@pytest.mark.parametrize("name", sorted(UNEQUAL))
+@pytest.mark.parametrize("dtype,D", [("f32", 40), ("f32", 128), ("f32", 200), ("bf16", 136), ("bf16", 256), ("bf16", 64)])
+def test_unequal_sequences(usm, dtype, D, name, group):
+    """Sequences of few rows and of many in one call, on either side of the number of
+    rows that parts them, with sequences that bring nothing between them."""
+    counts = UNEQUAL[name]
+    rng = np.random.default_rng(len(counts))
+    lengths = np.array(counts) + rng.integers(0, 400, len(counts))
+    Problem(name, lengths, counts, heads=2 * group, kv=2, D=D, dtype=dtype, before=1, behind=2).check(usm)
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 192)])
+@pytest.mark.parametrize("others", [0, 1])
+def test_others_do_not_change_how_a_chunk_is_read(usm, dtype, D, others):
+    """A chunk among sequences that bring nothing, or a token each (of one key), takes
+    about the time that it takes alone: its rows still share the keys.  (By the
+    average number of rows it would be read two or four rows at a time, in 128
+    walks over the cache instead of four.)"""
+    import torch
+    chunk, length, seqs, kv = 256, 8192, 256 if others else 128, 8
+    t = torch_type(dtype)
+    k, v = torch.randn(2, length // 16, 16, kv, D, device="cuda").to(t)
+    q = torch.randn(chunk + others * (seqs - 1), kv, D, device="cuda").to(t)
+    table = torch.zeros((seqs, length // 16), dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(length // 16, device="cuda")
+    lens = torch.ones(seqs, dtype=torch.int32, device="cuda")
+    lens[0] = length
+    offsets = chunk + others * torch.arange(-1, seqs, device="cuda", dtype=torch.int32)
+    offsets[0] = 0
+
+    def time(n, seqs):
+        run = lambda: usm.paged_attention(q[:n], k, v, table[:seqs], lens[:seqs], q_offsets=offsets[: seqs + 1], scale=D ** -0.5)
+        best = []
+        for _ in range(10):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            begin.record()
+            out = run()
+            end.record()
+            torch.cuda.synchronize()
+            best.append(begin.elapsed_time(end))
+        return min(best), out
+
+    alone, want = time(chunk, 1)
+    among, out = time(q.shape[0], seqs)
+    print(f"{dtype} {D}: {1e3 * alone:.0f} us alone, {1e3 * among:.0f} among others")
+    assert (out[:chunk].float() - want.float()).abs().max() < 0.01
+    assert among < 2 * alone

@@ -2,6 +2,7 @@
 // The declarations and their contracts are in include/usm.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -607,7 +608,11 @@ size_t paged_attention_workspace_bytes(int tokens, int num_seqs, int q_heads, in
     if (tokens <= 0 || num_seqs <= 0 || num_seqs > kPagedMaxSeqs || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
         head_dim > kPagedMaxHeadDim || !dtype_ok(dtype) || (long long)tokens * q_heads >= 1LL << 31)
         return 0;
-    return paged_attention_workspace(tokens, num_seqs, q_heads, kv_heads, head_dim, dtype == USM_BF16);
+    // The caller may or may not bring offsets.
+    size_t bytes = paged_attention_workspace(tokens, num_seqs, q_heads, kv_heads, head_dim, dtype == USM_BF16, false);
+    if (tokens % num_seqs == 0)
+        bytes = std::max(bytes, paged_attention_workspace(tokens, num_seqs, q_heads, kv_heads, head_dim, dtype == USM_BF16, true));
+    return bytes;
 }
 
 int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* q, int q_heads, float scale, int causal,
@@ -624,7 +629,7 @@ int paged_attention(const usm_paged_cache* cache, int tokens, const usm_tokens* 
     if (status == USM_OK) status = check_tokens(out, c, tokens, q_heads, true);
     if (status != USM_OK) return status;
     const bool bf16 = c.dtype == USM_BF16;
-    if (!workspace || workspace_bytes < paged_attention_workspace(tokens, c.num_seqs, q_heads, c.kv_heads, c.head_dim, bf16))
+    if (!workspace || workspace_bytes < paged_attention_workspace(tokens, c.num_seqs, q_heads, c.kv_heads, c.head_dim, bf16, !c.q_offsets))
         return USM_ERR_WORKSPACE;
     if (!aligned16(workspace)) return USM_ERR_ALIGNMENT;
     PagedArgs a{};

@@ -102,6 +102,7 @@ struct PagedArgs {
     int table_pages;       // entries of a sequence's row of the table
     int out32;             // rows of the output are 32-byte aligned and that much at least
     int boxes;             // keys and values come by TMA, a box of a page's slots at a time
+    int least_rows, most_rows;  // rows (tokens·group) of the sequences that the launch takes
     int part_rows;         // rows of a partial result
     float* parts;          // [2·ctas][head_dim / 4][part_rows][4], then [2·ctas][part_rows][2]
     float* part_stats;     // (reference, sum) of each row

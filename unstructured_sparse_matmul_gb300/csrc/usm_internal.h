@@ -92,7 +92,8 @@ size_t attention_workspace_bytes(const AttnArgs& a, bool bf16);
 int launch_attention(const AttnArgs& a, bool bf16, void* workspace, cudaStream_t stream);
 int launch_rope_table(int positions, int rot, double base, float* table, cudaStream_t stream);
 int launch_paged_append(const AppendArgs& a, bool bf16, cudaStream_t stream);
-size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16);
+// equal: every sequence brings as many tokens as any other.
+size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16, bool equal);
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream);
 // The matrix kernel for bf16 heads of up to 128 columns: rows of its blocks, and its launch.
 int paged_mma_rows();

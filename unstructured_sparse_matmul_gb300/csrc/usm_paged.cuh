@@ -32,6 +32,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
         s.start = b * a.per_seq;
         s.n = a.per_seq;
     }
+    const int rows = s.n * a.group;
+    if (rows < a.least_rows || rows > a.most_rows) s.n = 0;  // another launch's
     s.len = min(max(a.lengths[b], 0), kPagedMaxLength);
     return s;
 }

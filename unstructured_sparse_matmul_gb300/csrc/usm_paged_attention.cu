@@ -84,8 +84,11 @@ struct Walk {
 
 // Where columns 4·quad.. of a row of a partial result lie: a warp that has 32 rows
 // of a column writes them side by side.
+__device__ __forceinline__ float* part_of(float* parts, int part_rows, int head_dim, long long slot, int row, int quad) {
+    return parts + (slot * part_rows * (head_dim / 4) + (long long)quad * part_rows + row) * 4;
+}
 __device__ __forceinline__ float* part_of(const PagedArgs& a, long long slot, int row, int quad) {
-    return a.parts + (slot * a.part_rows * (a.head_dim / 4) + (long long)quad * a.part_rows + row) * 4;
+    return part_of(a.parts, a.part_rows, a.head_dim, slot, row, quad);
 }
 
 // ---------------------------------------------------------------------------
@@ -541,7 +544,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_few_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 // Joins the parts of items that several CTAs took: CTA (c, y) of this kernel
-// takes rows 16·y.. of the item that CTA c began.  A thread has four columns of a
+// takes rows 16·y.. of the item that CTA c began (of the first launch's CTAs, then
+// of the second's).  A thread has four columns of a
 // row; neighbours have up to 16 rows of the same columns (256 bytes of a part), and
 // where that leaves threads idle a row's parts are dealt out to several.
 // ---------------------------------------------------------------------------
@@ -567,15 +571,30 @@ __device__ __forceinline__ void raise_reference(JoinSum& sum, float top, float s
     sum.x = scaled(sum.x, f);
 }
 
+// Where a launch leaves its parts, as PagedArgs has it.
+struct Parts {
+    float *parts, *stats;
+    const PagedMeta* meta;
+    int rows, ctas;
+};
+// (An array: two parameters of the struct's type with a choice between them gave wrong
+// members with nvcc 13.0.)
+struct BothParts {
+    Parts launch[2];
+};
+
 template <class T>
-__global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __grid_constant__ PagedArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 5)
+    paged_join_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ BothParts both) {
     constexpr int kAhead = 4;
     __shared__ float4 sums[kJoinThreads];
     __shared__ float2 stats[kJoinThreads];
     await_previous();
     let_next_start();
-    const PagedMeta* meta = static_cast<const PagedMeta*>(a.meta);
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const bool later_launch = blockIdx.x >= both.launch[0].ctas;
+    const Parts& p = both.launch[later_launch];
+    const PagedMeta* meta = p.meta;
+    const int c = blockIdx.x - (later_launch ? both.launch[0].ctas : 0), ctas = p.ctas, lane = threadIdx.x & 31;
     const int4 begin = __ldcg(reinterpret_cast<const int4*>(meta + c));  // first_live, start, row0, rows
     const int head = __ldcg(&meta[c].head);
     int2 later = make_int2(0, 1);  // later_live, ends
@@ -620,8 +639,8 @@ __global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __gri
                     x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i > count) continue;
                     const long long slot = i == 0 ? 2LL * c + kPartFirst : 2LL * (c + i) + kPartLater;
-                    stat[u] = __ldcg(reinterpret_cast<const float2*>(a.part_stats + 2 * (slot * a.part_rows + r)));
-                    x[u] = __ldcg(reinterpret_cast<const float4*>(part_of(a, slot, r, quad)));
+                    stat[u] = __ldcg(reinterpret_cast<const float2*>(p.stats + 2 * (slot * p.rows + r)));
+                    x[u] = __ldcg(reinterpret_cast<const float4*>(part_of(p.parts, p.rows, a.head_dim, slot, r, quad)));
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) top = fmaxf(top, stat[u].x);
@@ -652,31 +671,46 @@ __global__ void __launch_bounds__(kJoinThreads, 5) paged_join_kernel(const __gri
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-enum class Form { Mma, Block, Few1, Few2, Few4, Few8 };
-struct Shape {
+enum class Form { None, Mma, Block, Few1, Few2, Few4, Few8 };
+struct Launch {
     Form form;
     int rows;  // of a block
     int ctas;
+    int least, most;  // rows of the sequences that it takes
 };
-// bf16 heads of up to 128 columns go to the matrix kernel.  Others with up to 8 rows
-// a sequence and head of keys, on average, are read by few rows at a time: from
-// 9 on the keys would be read twice, and the block kernel is as fast.  (Wider heads
-// have room for 4 rows: they read the keys of 5 to 8 twice, where the block
-// kernel would fill 8 of its 64 rows.)
-Shape shape_of(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16) {
-    const int sms = sm_count_current_device();
-    if (bf16 && head_dim <= 128) return Shape{Form::Mma, paged_mma_rows(), sms};
-    const long long rows = (long long)tokens * (q_heads / kv_heads);
-    if (rows <= num_seqs) return Shape{Form::Few1, 1, 2 * sms};
-    if (rows <= 2LL * num_seqs) return Shape{Form::Few2, 2, 2 * sms};
-    if (rows <= 8LL * num_seqs)
-        return rows <= 4LL * num_seqs || head_dim > 128 ? Shape{Form::Few4, 4, 2 * sms} : Shape{Form::Few8, 8, 2 * sms};
-    const int fit = std::max(1, std::min(2, 220 * 1024 / block_smem(head_dim)));
-    return Shape{Form::Block, kBlockRows, fit * sms};
-}
+struct Plan {
+    Launch first, second;
+};
+constexpr int kAll = 0x7fffffff, kFewRows = 8;
 
-int part_rows(int tokens, int q_heads, int kv_heads, int rows) {
-    return (int)std::min<long long>(rows, (long long)tokens * (q_heads / kv_heads));
+// bf16 heads of up to 128 columns go to the matrix kernel.  Of the others, sequences with
+// up to 8 rows a head of keys are read by few rows at a time: from 9 on the keys
+// would be read twice, and the block kernel is as fast.  (Wider heads have room for 4
+// rows: they read the keys of 5 to 8 twice, where the block kernel would fill 8 of
+// its 64 rows.)  With `equal` shares of tokens all sequences are of one kind; else how many
+// tokens each brings is known on the device only, and both kernels are launched, each
+// for its own, which costs 3 us where one finds none.  (By the average alone a
+// chunk's tokens among idle sequences went through the cache a few rows at a time, and
+// single tokens beside a chunk took a block of 64 rows each: a chunk of 1000 beside 16
+// tokens over 4096 fp32 keys of 128 columns, 16/2 heads, 964 us, now 736; one of 256 beside
+// 63, 16/8 heads of 192 bf16 columns, 4690 us, now 963.)
+Plan plan_of(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16, bool equal) {
+    const int sms = sm_count_current_device(), group = q_heads / kv_heads;
+    if (bf16 && head_dim <= 128) return {{Form::Mma, paged_mma_rows(), sms, 0, kAll}, {}};
+    const long long all = (long long)tokens * group;
+    // Rows of a sequence: at most, and on average of those that bring any (one brings a token's at least).
+    const long long most = equal ? all / num_seqs : all, average = std::max<long long>(group, (all + num_seqs - 1) / num_seqs);
+    Launch few = {Form::Few8, 8, 2 * sms, 0, kAll};
+    if (average <= 1) few.form = Form::Few1, few.rows = 1;
+    else if (average <= 2) few.form = Form::Few2, few.rows = 2;
+    else if (average <= 4 || head_dim > 128) few.form = Form::Few4, few.rows = 4;
+    if (most <= kFewRows) return {few, {}};
+    const int fit = std::max(1, std::min(2, 220 * 1024 / block_smem(head_dim)));
+    Launch block = {Form::Block, kBlockRows, fit * sms, 0, kAll};
+    if (equal || group > kFewRows) return {block, {}};
+    block.least = kFewRows + 1;
+    few.most = kFewRows;
+    return {block, few};
 }
 
 template <class T, int kWide>
@@ -719,43 +753,65 @@ int run_block(const PagedArgs& a, int ctas, cudaStream_t stream) {
 }
 
 template <class T>
-int join(const PagedArgs& a, int ctas, cudaStream_t stream) {
+int join(const PagedArgs& a, const BothParts& both, cudaStream_t stream) {
     const auto kernel = paged_join_kernel<T>;
     // The same split of an SM's memory as the kernel before it has: to change it the
     // SM would have to drain.
     static SharedOnce once;
     if (!once.allow(kernel, 0)) return cuda_failure();
-    return launch_next(kernel, dim3(ctas, (a.part_rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 1, stream, a, ctas);
+    const auto& [first, second] = both.launch;
+    const int rows = std::max(first.rows, second.rows);
+    return launch_next(kernel, dim3(first.ctas + second.ctas, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 1, stream, a, both);
 }
 
 size_t meta_bytes(int ctas) { return ((size_t)ctas * sizeof(PagedMeta) + 15) / 16 * 16; }
 
+// Rows of a launch's parts, of sequences with `rows` at most; bytes of its workspace.
+int part_rows(const Launch& s, long long rows) { return (int)std::min<long long>(s.rows, std::min<long long>(s.most, rows)); }
+size_t launch_bytes(const Launch& s, long long rows, int head_dim) {
+    if (s.form == Form::None) return 0;
+    const size_t parts = (size_t)2 * s.ctas * part_rows(s, rows);
+    return meta_bytes(s.ctas) + (parts * (head_dim + 2) * 4 + 15) / 16 * 16;
+}
+
+int launch(const Launch& s, const PagedArgs& a, bool bf16, cudaStream_t stream) {
+    switch (s.form) {
+        case Form::Mma: return launch_paged_mma(a, s.ctas, stream);
+        case Form::Few1: return run_few<1>(a, bf16, s.ctas, stream);
+        case Form::Few2: return run_few<2>(a, bf16, s.ctas, stream);
+        case Form::Few4: return run_few<4>(a, bf16, s.ctas, stream);
+        case Form::Few8: return run_few<8>(a, bf16, s.ctas, stream);
+        default: return bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
+    }
+}
+
 }  // namespace
 
-size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16) {
-    const Shape s = shape_of(tokens, num_seqs, q_heads, kv_heads, head_dim, bf16);
-    const size_t rows = (size_t)2 * s.ctas * part_rows(tokens, q_heads, kv_heads, s.rows);
-    return meta_bytes(s.ctas) + rows * head_dim * 4 + rows * 8;
+size_t paged_attention_workspace(int tokens, int num_seqs, int q_heads, int kv_heads, int head_dim, bool bf16, bool equal) {
+    const Plan p = plan_of(tokens, num_seqs, q_heads, kv_heads, head_dim, bf16, equal);
+    const long long rows = (long long)(equal ? tokens / num_seqs : tokens) * (q_heads / kv_heads);
+    return launch_bytes(p.first, rows, head_dim) + launch_bytes(p.second, rows, head_dim);
 }
 
 int launch_paged_attention(PagedArgs a, bool bf16, void* workspace, cudaStream_t stream) {
-    const Shape s = shape_of(a.tokens, a.num_seqs, a.kv_heads * a.group, a.kv_heads, a.head_dim, bf16);
-    // Rows of an item at most.
-    a.part_rows = (int)std::min<long long>(s.rows, (long long)(a.q_offsets ? a.tokens : a.per_seq) * a.group);
-    a.meta = workspace;
-    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(s.ctas));
-    a.part_stats = a.parts + (size_t)2 * s.ctas * a.part_rows * a.head_dim;
-    int code;
-    switch (s.form) {
-        case Form::Mma: code = launch_paged_mma(a, s.ctas, stream); break;
-        case Form::Few1: code = run_few<1>(a, bf16, s.ctas, stream); break;
-        case Form::Few2: code = run_few<2>(a, bf16, s.ctas, stream); break;
-        case Form::Few4: code = run_few<4>(a, bf16, s.ctas, stream); break;
-        case Form::Few8: code = run_few<8>(a, bf16, s.ctas, stream); break;
-        default: code = bf16 ? run_block<__nv_bfloat16>(a, s.ctas, stream) : run_block<float>(a, s.ctas, stream);
+    const bool equal = !a.q_offsets;
+    const Plan p = plan_of(a.tokens, a.num_seqs, a.kv_heads * a.group, a.kv_heads, a.head_dim, bf16, equal);
+    const long long rows = (long long)(equal ? a.per_seq : a.tokens) * a.group;
+    BothParts both = {};
+    char* at = static_cast<char*>(workspace);
+    for (const Launch* s : {&p.first, &p.second}) {
+        if (s->form == Form::None) continue;
+        a.least_rows = s->least;
+        a.most_rows = s->most;
+        a.part_rows = part_rows(*s, rows);
+        a.meta = at;
+        a.parts = reinterpret_cast<float*>(at + meta_bytes(s->ctas));
+        a.part_stats = a.parts + (size_t)2 * s->ctas * a.part_rows * a.head_dim;
+        both.launch[s == &p.second] = {a.parts, a.part_stats, static_cast<const PagedMeta*>(a.meta), a.part_rows, s->ctas};
+        if (const int code = launch(*s, a, bf16, stream); code != USM_OK) return code;
+        at += launch_bytes(*s, rows, a.head_dim);
     }
-    if (code != USM_OK) return code;
-    return bf16 ? join<__nv_bfloat16>(a, s.ctas, stream) : join<float>(a, s.ctas, stream);
+    return bf16 ? join<__nv_bfloat16>(a, both, stream) : join<float>(a, both, stream);
 }
 
 }  // namespace usm
