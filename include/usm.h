@@ -525,6 +525,8 @@ int paged_append(const usm_paged_cache *cache, int tokens, const usm_tokens *k, 
  *   workspace : paged_attention_workspace_bytes(...) bytes of device scratch,
  *            16-byte aligned, contents ignored.  The size follows from the arguments
  *            and the number of SMs of the current device (up to 41 MB).
+ *            With q_offsets = NULL those of one sequence are enough:
+ *            ..._bytes(tokens / num_seqs, 1, ...).
  * Products, statistics and sums are fp32.  bf16: probabilities go into their product
  * with V as two bf16 parts (relative 2^-16 each; the output's own rounding is
  * 2^-8); head_dim > 128 keeps them in fp32.

@@ -245,3 +245,27 @@ def test_others_do_not_change_how_a_chunk_is_read(usm, dtype, D, others):
     print(f"{dtype} {D}: {1e3 * alone:.0f} us alone, {1e3 * among:.0f} among others")
     assert (out[:chunk].float() - want.float()).abs().max() < 0.01
     assert among < 2 * alone
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 192)])
+@pytest.mark.parametrize("count", [1, 3])
+def test_workspace_of_equal_shares(usm, dtype, D, count):
+    """The workspace of a batch whose sequences bring as many tokens each is that of one
+    sequence: a call takes no more, and is content with it."""
+    import torch
+    p = Problem("equal", [300] * 64, [count] * 64, heads=8, kv=2, D=D, dtype=dtype)
+    one = usm.load().paged_attention_workspace_bytes(count, 1, 8, 2, D, 0 if dtype == "f32" else 1)
+    assert 0 < one <= usm.load().paged_attention_workspace_bytes(64 * count, 64, 8, 2, D, 0 if dtype == "f32" else 1)
+    q, k, v, table, lens, offsets = p.on_device()
+    assert offsets is None
+    run = lambda **kw: usm.paged_attention(q, k, v, table, lens, scale=D ** -0.5, **kw)
+    want = run()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    out = run()
+    taken = torch.cuda.max_memory_allocated() - before
+    assert taken <= one + out.numel() * out.element_size() + 2048, (taken, one)
+    ws = torch.empty(one, dtype=torch.uint8, device="cuda")
+    assert torch.equal(run(workspace=ws), want)
+    p.check(usm)

@@ -875,7 +875,12 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, q_offsets=None, sc
     if out is None:
         out = T.torch.empty_like(q, memory_format=T.torch.contiguous_format)
     _, ot = _tokens(out, "out", index, dt, shape, written=True)
-    need = _attention_workspace(index, n, page_table.shape[0], q_heads, k_cache.shape[2], D, USM_F32 if dt is T.f32[0] else USM_BF16)
+    seqs = page_table.shape[0]
+    if q_offsets is None and seqs > 1 and n % seqs == 0:
+        n_most, seqs = n // seqs, 1  # parts are no longer than one sequence's
+    else:
+        n_most = n
+    need = _attention_workspace(index, n_most, seqs, q_heads, k_cache.shape[2], D, USM_F32 if dt is T.f32[0] else USM_BF16)
     ws = _workspace(workspace, need, q, T)
     _run("paged_attention", lib.paged_attention, index, T, cache, n, qt, q_heads, scale, 1 if causal else 0, window, ot,
          None if ws is None else ws.data_ptr(), need)
