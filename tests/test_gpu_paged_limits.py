@@ -269,3 +269,39 @@ def test_workspace_of_equal_shares(usm, dtype, D, count):
     ws = torch.empty(one, dtype=torch.uint8, device="cuda")
     assert torch.equal(run(workspace=ws), want)
     p.check(usm)
+
+
+def test_calls_beside_other_kernels(usm):
+    """Attention and appends on one stream, the library's sparse products (which use
+    tensor memory too) and sparse attention on another, at once."""
+    import torch
+    import workloads as W
+    p = Problem("beside others", [4000, 200, 900], [3, 200, 1], heads=8, kv=2, D=128)
+    q, k, v, table, lens, offsets = p.on_device()
+    rope = usm.rope_table(4096, 128)
+    new = torch.randn(2, q.shape[0], 2, 128, device="cuda").bfloat16()
+    csr = W.random_csr(3, 1024, 1024, 0.3)
+    ro, ci = (torch.from_numpy(x).cuda() for x in (csr.row_offsets, csr.col_indices))
+    val, B = torch.randn(ci.numel(), device="cuda"), torch.randn(1024, 2048, device="cuda")
+    X, Y = (torch.randn(1024, 256, device="cuda").bfloat16() for _ in range(2))
+
+    def paged():
+        turned = usm.paged_append(new[0], new[1], k, v, table, lens, q_offsets=offsets, rope=rope, q=q)
+        return usm.paged_attention(turned, k, v, table, lens, q_offsets=offsets, scale=0.1)
+
+    def sparse():
+        return [usm.spmm(ro, ci, val, B), usm.spmm(ro, ci, val.bfloat16(), B.bfloat16()), usm.sddmm(ro, ci, X, Y)]
+
+    want, others = paged(), sparse()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got_a, got_b = [], []
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            got_a.append(paged())
+        with torch.cuda.stream(b):
+            got_b.append(sparse())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got_a)
+    assert all(torch.equal(x, y) for g in got_b for x, y in zip(g, others))
+    assert usm.poll_status() == 0
