@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import paged_ref as R
-from test_gpu_paged import Problem, assert_near, got, torch_type
+from test_gpu_paged import Problem, assert_near, got, rounded, torch_type
 
 pytestmark = pytest.mark.gpu
 
@@ -305,3 +305,36 @@ def test_calls_beside_other_kernels(usm):
     assert all(torch.equal(x, want) for x in got_a)
     assert all(torch.equal(x, y) for g in got_b for x, y in zip(g, others))
     assert usm.poll_status() == 0
+
+
+@pytest.mark.parametrize("where", [130, 300])
+def test_weights_of_different_references(usm, where):
+    """Scores that are whole numbers far from zero, and so exact: a tile of keys at S and one
+    key at S + 6 whose tile raises the reference (key 300: in the same half as the
+    first tile; 130: in the other).  Their weights have to keep their ratio; V is chosen
+    so that both nearly cancel.  Bounds: 2^-16 a weight, 130 additions, the power of
+    two, the output's step."""
+    scores = 20 + 47 * np.arange(60)
+    p = Problem("references", [where + 1] * 60, [1] * 60, heads=1, kv=1, D=16, page=128)
+    p.q[:] = 0
+    p.q[..., 0] = p.q[..., 1] = 1
+    for b, s in enumerate(scores):
+        j = np.arange(where + 1)
+        at = p.table[b, j // 128], j % 128, 0
+        p.k[at], p.v[at] = 0, 0
+        high, low = int(s) // 16 * 16, int(s) % 16  # both exact in bf16
+        p.k[(*at, 0)] = np.where(j < 128, high, -500)
+        p.k[(*at, 1)] = np.where(j < 128, low, -500)
+        p.v[(*at, 0)] = 1
+        heavy = p.table[b, where // 128], where % 128, 0
+        p.k[(*heavy, 0)], p.k[(*heavy, 1)] = high, low + 6
+        p.v[(*heavy, 0)] = -0.31640625
+    p.k, p.v = rounded(p.k, "bf16"), rounded(p.v, "bf16")
+    x = got(p.run(usm, scale=1.0))[:, 0, 0]
+    w = np.exp(6.0)
+    ref, mass = (128 - w * 0.31640625) / (128 + w), (128 + w * 0.31640625) / (128 + w)
+    bound = (1.01 * 2.0 ** -16 + 2 * 138 * R.U + 2.0 ** -21) * mass + R.HALF_STEP["bf16"] * abs(ref)
+    exact = p.k[p.table[:, 0], 0, 0, :2].sum(1)
+    assert np.array_equal(exact, scores)
+    off = np.abs(x - ref)
+    assert off.max() <= bound, (off.max(), bound, scores[off.argmax()])

@@ -54,9 +54,11 @@ constexpr int kSegmentCost = 4;
 constexpr int kRing = 4;       // segments handed out ahead
 constexpr int kConsumers = 13; // warps that read a segment (and two more where they copy queries)
 constexpr float kRaise = 8.f;  // log2 of the largest weight before a row's reference is raised
-// Largest |m·c| for which S·c - m·c is formed by one FMA: the rounding of m·c,
-// a common factor of the row's weights, stays below 2^(4096·2^-24).
-constexpr float kNear = 4096.f;
+// Largest |m·c| for which S·c - m·c is formed by one FMA: the rounding of m·c changes
+// the weights that share the reference by one factor, which differs where the
+// reference was raised, in the other half and in other parts; up to here it stays
+// within 2^-17, below a weight's own 2^-16.
+constexpr float kNear = 256.f;
 
 using Shares = PagedShares<kRows, kKeys, kThreads, kSegmentCost>;
 
