@@ -462,9 +462,7 @@ struct Copies {
 };
 
 // ---------------------------------------------------------------------------
-// Matrix products: one elected thread (the compiler then issues the products from
-// uniform registers as they stand; behind a test of the lane it goes through the
-// warp's threads for each of them)
+// Matrix products, issued by one elected thread
 // ---------------------------------------------------------------------------
 template <int DP>
 struct Products {
