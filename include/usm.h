@@ -443,7 +443,7 @@ int csr_attention(int M, int K, int D, int N, int nnz, const int *row_offsets, c
  * page_table[b·table_stride + p / page_size]; a slot holds head_dim elements for
  * each of kv_heads heads, at k + page·k_page_stride + slot·k_slot_stride +
  * head·k_head_stride (and v alike).  Any order of pages, slots and heads is a
- * matter of the strides; sequences may share pages.
+ * matter of the strides (rows must not overlap); sequences may share pages.
  *
  * Whatever the arrays hold, no address outside the caches is formed: offsets are
  * clamped into [0, tokens], negative lengths count as 0, positions past the
@@ -469,7 +469,8 @@ typedef struct usm_paged_cache {
 /*
  * usm_tokens — rows of head_dim elements for each new token and head, at data +
  * token·token_stride + head·head_stride (elements, multiples of 16 bytes; data
- * 16-byte aligned).  A host struct, as usm_paged_cache.
+ * 16-byte aligned).  Rows that a call writes must not overlap.  A host struct, as
+ * usm_paged_cache.
  */
 typedef struct usm_tokens {
     void *data;
@@ -503,7 +504,8 @@ int rope_table_build(int positions, int rot_dim, double base, float *table, void
  * A token at a position without a slot, or whose page is outside [0, num_pages),
  * is not stored; its query is written all the same.  Positions outside the
  * table take its nearest row.  Tokens outside every sequence are left alone, in
- * q_out too.  Where two tokens of a call share a slot either may end up in it.
+ * q_out too.  Where two tokens of a call share a slot, each element of it is one of
+ * theirs, not all of them of the same.
  * Limits: 0 ≤ rot_dim ≤ head_dim, even; tokens·(heads) < 2^31.
  * tokens = 0 or num_seqs = 0 is a no-op.
  */
