@@ -17,13 +17,13 @@
 // that is done first leaves its sums to the other and goes on.
 //
 // Bounds and figures (measured at the sizes given): single tokens by HBM and the
-// softmax's latency (64 over 8192 keys, 1.55 GB: 268 us, 5.8 TB/s); chunks by the
-// softmax's instructions beside the products (two of 2048 over 16384 keys: 995 us, 1015
+// softmax's latency (64 over 8192 keys, 1.55 GB: 263 us, 5.9 TB/s); chunks by the
+// products beside the softmax's latency (two of 2048 over 16384 keys: 1000 us, 1010
 // TFLOP/s, half as many again with the second part's); prompts of a few thousand
 // tokens by start and joining as well (8x4096 of 64 columns: 56 us).  With the
-// rounded weight alone these are 242, 735 and 48 us.  Of the difference the forming
-// of the second part is more than its products: tokens take the same time without
-// those, and the weights' storing costs nothing.
+// rounded weight alone these are 242, 735 and 48 us: tokens pay for the forming of the
+// second part (without its products they take the same time), chunks mostly for its
+// products (without them 800 us); its storing costs nothing.
 //
 // The reference m of a row is its maximum, but it is raised only when a tile's
 // maximum passes it by more than 2^8 in the weights: fp32 sums and weights keep
@@ -47,9 +47,9 @@ namespace {
 
 constexpr int kRows = 256, kKeys = 128, kThreads = 512;
 // What an item costs a CTA beyond its tiles (its queries, the first products and the
-// output), in tiles: 8000 to 14000 cycles where a tile takes 2000 to 2800.  (3 to 8
-// measured: a prompt of 8x4096 takes 47.6 us with 4, 48.3 with 3, 49.5 with 8; local
-// attention 114.6, 113.4, 112.0.)
+// output), in tiles: 8000 to 14000 cycles where a tile takes 2400 to 4200.  (3 to 8
+// measured: a prompt of 8x4096 takes 56.5 us with 4, 56.4 with 3, 59.4 with 8; 64
+// tokens 262, 263, 266; local attention 141.5, 139.8, 137.8.)
 constexpr int kSegmentCost = 4;
 constexpr int kRing = 4;       // segments handed out ahead
 constexpr int kConsumers = 13; // warps that read a segment (and two more where they copy queries)
@@ -166,8 +166,8 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
 // and two copy the queries.  Other page sizes (and those under 8) come in 16-byte
 // copies by the first four; these complete on the tile's barrier by themselves too,
 // and the thread that multiplies makes them visible to the tensor cores.
-// (16-byte copies for all: 64 tokens over 8192 keys took 357 to 414 us, now 242; two
-// chunks over 16384 keys 963, now 735.)
+// (16-byte copies for all: 64 tokens over 8192 keys take 502 us, 263 with boxes; two
+// chunks over 16384 keys 1365, 1000 with boxes.)
 // ---------------------------------------------------------------------------
 template <int DP>
 struct Copies {
