@@ -340,3 +340,38 @@ def test_weights_of_different_references(usm, where):
     assert np.array_equal(exact, scores)
     off = np.abs(x - ref)
     assert off.max() <= bound, (off.max(), bound, scores[off.argmax()])
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 192), ("bf16", 64)])
+def test_captured_with_unequal_sequences(usm, dtype, D):
+    """A call captured once and replayed as its tokens change hands: sequences pass from
+    few rows to many and back, with one workspace that two graphs share."""
+    import torch
+    total, heads, kv, size = 120, 4, 2, 16
+    shares = [[100, 20], [1, 119], [119, 1], [60, 60], [0, 120], [116, 4], [4, 112]]
+    p = Problem("captured", [700, 500], [100, 20], heads=heads, kv=kv, D=D, dtype=dtype, page=size)
+    q, k, v, table, lens, offsets = p.on_device()
+    need = usm.load().paged_attention_workspace_bytes(total, 2, heads, kv, D, 0 if dtype == "f32" else 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    run = lambda **kw: usm.paged_attention(q, k, v, table, lens, q_offsets=offsets, scale=D ** -0.5, workspace=ws, **kw)
+    run()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        graphs.append(g)
+    for i, counts in enumerate(shares):
+        p.counts = np.array(counts)
+        p.starts = np.cumsum(p.counts) - p.counts
+        offsets.copy_(torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32))
+        out = outs[i % 2]
+        out.fill_(77.0)
+        graphs[i % 2].replay()
+        ref, bound = p.reference(D ** -0.5)
+        n = sum(counts)
+        assert_near(got(out)[:n], ref[:n], bound[:n], counts)
+        assert bool((out[n:] == 77.0).all())
+        graphs[1 - i % 2].replay()
+        assert torch.equal(outs[1 - i % 2][:n], out[:n])
+    assert usm.poll_status() == 0
